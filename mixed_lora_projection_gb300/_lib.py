@@ -16,6 +16,21 @@ P = C.c_void_p
 I32P = C.POINTER(C.c_int32)
 IP = C.POINTER(C.c_int)
 
+LL = C.c_longlong
+
+
+class KvCache(C.Structure):
+    """``lora_kv_cache`` of include/lora_layer.h."""
+    _fields_ = [("k", P), ("v", P),
+                ("k_page_stride", LL), ("k_token_stride", LL), ("k_head_stride", LL),
+                ("v_page_stride", LL), ("v_token_stride", LL), ("v_head_stride", LL),
+                ("n_pages", C.c_int), ("page_size", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("block_table", P), ("table_stride", LL), ("pages_per_seq", C.c_int), ("n_seqs", C.c_int),
+                ("kv_lens", P), ("q_offsets", I32P)]
+
+
+CACHE = C.POINTER(KvCache)
+
 SIGNATURES = {
     "lora_linear_create": (C.c_int, [C.POINTER(P), C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
     "lora_linear_forward": (C.c_int, [P, P, C.c_int, I32P, I32P, C.c_int, P, C.POINTER(P), C.POINTER(P),
@@ -43,6 +58,17 @@ SIGNATURES = {
     "lora_linear_k_split": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, IP]),
     "lora_linear_forward_noalloc": (C.c_int, [P, C.c_int, I32P, I32P, C.c_int, C.c_int, C.c_int, C.c_int, P,
                                               C.POINTER(P), C.POINTER(P), C.POINTER(C.c_float), C.c_int, P, P]),
+    "lora_linear_add_rms_norm": (C.c_int, [P, LL, P, LL, P, C.c_float, C.c_float, C.c_int, C.c_int, P, LL, P, LL,
+                                           P, LL, P, C.c_int, P]),
+    "lora_linear_kv_append": (C.c_int, [CACHE, P, LL, LL, P, LL, LL, C.c_int, P, LL, LL, P, LL, LL, P, P, C.c_int,
+                                        C.c_int, P]),
+    "lora_linear_attn_create": (C.c_int, [C.POINTER(P), C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
+                                          C.c_int]),
+    "lora_linear_attn_forward": (C.c_int, [P, CACHE, P, LL, LL, P, LL, LL, C.c_float, C.c_int, C.c_int, P]),
+    "lora_linear_attn_validate": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, CACHE, P, LL, LL,
+                                            P, LL, LL, C.c_float, C.c_int, C.c_int]),
+    "lora_linear_attn_status": (C.c_int, [P, C.c_int]),
+    "lora_linear_attn_destroy": (C.c_int, [P]),
 }
 
 # return codes and options, as in include/lora_linear.h

@@ -19,7 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblora_linear.so")
-SOURCES = ["kernels.cu", "kernels_w4.cu", "api.cpp", "planner.cpp", "noalloc.cu"]
+SOURCES = ["kernels.cu", "kernels_w4.cu", "api.cpp", "planner.cpp", "noalloc.cu",
+           "layer_ops.cu", "attn.cu", "layer_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,7 +39,8 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "lora_linear.h")]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
+        os.path.join(ROOT, "include", h) for h in ("lora_linear.h", "lora_layer.h")]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 

@@ -1,0 +1,367 @@
+// C-ABI of the operators between the projections (include/lora_layer.h): argument checks, the
+// attention handle and its workspace, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <new>
+
+#include "../../include/lora_layer.h"
+#include "layer_internal.h"
+
+using namespace lora;
+
+static_assert(kMaxSeqs == LORA_LAYER_MAX_SEQS, "the kernels' sequence limit is the header's");
+
+namespace {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The bytes that a strided buffer covers: `outer` rows of `extent` bytes, `stride` bytes apart (a
+// row's inner axis may itself be strided; its extent then reaches the last byte of the row).
+struct Span {
+    uintptr_t first = 0, last = 0, stride = 0, extent = 0;
+};
+Span span(const void* p, long long outer, long long so, long long inner, long long si, long long width, int elem) {
+    Span s;
+    if (!p || outer <= 0 || inner <= 0) return s;
+    s.first = reinterpret_cast<uintptr_t>(p);
+    s.stride = (uintptr_t)(so * elem);
+    s.extent = (uintptr_t)(((inner - 1) * si + width) * elem);
+    s.last = s.first + (uintptr_t)(outer - 1) * s.stride + s.extent;
+    return s;
+}
+// Whether two buffers may share a byte. Column slices of one row-strided buffer do not.
+bool meet(const Span& a, const Span& b) {
+    if (!(a.first < b.last && b.first < a.last)) return false;
+    if (a.stride == 0 || a.stride != b.stride) return true;
+    const uintptr_t d = a.first <= b.first ? (b.first - a.first) % a.stride : (a.stride - (a.first - b.first) % a.stride) % a.stride;
+    return !(d >= a.extent && d + b.extent <= a.stride);
+}
+
+constexpr long long kMaxStride = 1ll << 38;   // elements: a tensor map's strides stay under 2^40 bytes
+
+// A stride of `align` elements' multiple, large enough for rows of `least` elements.
+bool stride_ok(long long s, long long least, int align) { return s >= least && s <= kMaxStride && s % align == 0; }
+
+int check_offsets(const int32_t* off, int n, int* rows) {
+    if (!off || off[0] != 0) return LORA_EINVAL;
+    for (int i = 0; i < n; ++i)
+        if (off[i + 1] < off[i]) return LORA_EINVAL;
+    if (off[n] > LORA_MAX_TOKENS) return LORA_EINVAL;
+    *rows = off[n];
+    return LORA_OK;
+}
+
+int check_cache(const lora_kv_cache* c, int* rows) {
+    if (!c || c->n_seqs < 1 || c->n_seqs > LORA_LAYER_MAX_SEQS) return LORA_EINVAL;
+    if (check_offsets(c->q_offsets, c->n_seqs, rows) != LORA_OK) return LORA_EINVAL;
+    if (c->n_kv_heads < 1 || c->n_kv_heads > 4096 || c->head_dim < 8 || c->head_dim > 512 || c->head_dim % 8) return LORA_EINVAL;
+    if (c->page_size < 16 || c->page_size > (1 << 20) || c->page_size % 16) return LORA_EINVAL;
+    if (c->n_pages < 1 || c->pages_per_seq < 1 || (long long)c->pages_per_seq * c->page_size > 0x7fffff00ll) return LORA_EINVAL;
+    if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return LORA_EINVAL;
+    const long long s[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
+                            c->v_page_stride, c->v_token_stride, c->v_head_stride};
+    for (long long v : s)
+        if (!stride_ok(v, 8, 8)) return LORA_EINVAL;
+    if (!c->block_table || !c->kv_lens || !aligned4(c->block_table) || !aligned4(c->kv_lens)) return LORA_EINVAL;
+    if (c->table_stride < c->pages_per_seq || c->table_stride > (1ll << 31)) return LORA_EINVAL;
+    return LORA_OK;
+}
+
+CacheView view(const lora_kv_cache* c) {
+    CacheView v;
+    v.k = c->k;
+    v.v = c->v;
+    v.k_page = c->k_page_stride;
+    v.k_token = c->k_token_stride;
+    v.k_head = c->k_head_stride;
+    v.v_page = c->v_page_stride;
+    v.v_token = c->v_token_stride;
+    v.v_head = c->v_head_stride;
+    v.table = c->block_table;
+    v.kv_lens = c->kv_lens;
+    v.table_stride = c->table_stride;
+    v.n_pages = c->n_pages;
+    v.page_size = c->page_size;
+    v.n_kv = c->n_kv_heads;
+    v.dim = c->head_dim;
+    v.pages_per_seq = c->pages_per_seq;
+    v.n_seqs = c->n_seqs;
+    return v;
+}
+
+Span cache_span(const lora_kv_cache* c, bool v) {
+    // pages, tokens and heads in any order: the far corner of the last element
+    Span s;
+    s.first = reinterpret_cast<uintptr_t>(v ? c->v : c->k);
+    const long long far = (c->n_pages - 1) * (v ? c->v_page_stride : c->k_page_stride) +
+                          (c->page_size - 1) * (v ? c->v_token_stride : c->k_token_stride) +
+                          (c->n_kv_heads - 1) * (v ? c->v_head_stride : c->k_head_stride) + c->head_dim;
+    s.last = s.first + (uintptr_t)far * 2;
+    return s;
+}
+
+// The device's GPU is an sm_103 one (the kernels are compiled for nothing else).
+int check_device(int device) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess) {
+        cudaGetLastError();
+        return LORA_ENODEV;
+    }
+    return major == 10 && minor == 3 ? LORA_OK : LORA_ENODEV;
+}
+
+int check_layout(int n_heads, int n_kv, int dim, int page_size, int max_tokens, int max_seqs) {
+    if (n_kv < 1 || n_heads < n_kv || n_heads > 65536 || n_heads % n_kv || n_heads / n_kv > 128) return LORA_EINVAL;
+    if (dim != 64 && dim != 128 && dim != 256) return LORA_EINVAL;
+    if (page_size < 16 || page_size > (1 << 20) || page_size % 16) return LORA_EINVAL;
+    if (max_tokens < 1 || max_tokens > LORA_MAX_TOKENS || max_seqs < 1 || max_seqs > LORA_LAYER_MAX_SEQS) return LORA_EINVAL;
+    return LORA_OK;
+}
+
+// Makes `device` current for the life of a call.
+struct DeviceGuard {
+    int prev = -1;
+    bool changed = false, ok = true;
+    explicit DeviceGuard(int device) {
+        ok = cudaGetDevice(&prev) == cudaSuccess;
+        if (ok && prev != device) ok = changed = cudaSetDevice(device) == cudaSuccess;
+    }
+    ~DeviceGuard() {
+        if (changed) cudaSetDevice(prev);
+    }
+};
+
+}  // namespace
+
+struct lora_attn {
+    int device = 0, n_heads = 0, n_kv = 0, dim = 0, page_size = 0, max_tokens = 0, max_seqs = 0;
+    int num_sms = 0;
+    int* status = nullptr;
+    unsigned long long wait_limit_ns = 4000000000ull;
+};
+
+extern "C" int lora_linear_add_rms_norm(const void* x, long long x_stride, const void* residual,
+                                        long long residual_stride, const void* weight, float weight_offset, float eps,
+                                        int rows, int width, void* h_out, long long h_stride, void* y,
+                                        long long y_stride, void* q8, long long q8_stride, float* scales, int group,
+                                        void* stream) {
+    if (rows < 0 || width < 8 || width > LORA_LAYER_MAX_WIDTH || width % 8) return LORA_EINVAL;
+    if (!isfinite(eps) || eps < 0.f || !isfinite(weight_offset)) return LORA_EINVAL;
+    if (rows == 0) return LORA_OK;
+    if (!x || !weight || (!y && !q8)) return LORA_EINVAL;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h_out) || !aligned16(y) || !aligned16(q8))
+        return LORA_EINVAL;
+    if (!stride_ok(x_stride, width, 8) || (residual && !stride_ok(residual_stride, width, 8)) ||
+        (h_out && !stride_ok(h_stride, width, 8)) || (y && !stride_ok(y_stride, width, 8)))
+        return LORA_EINVAL;
+    if (q8) {
+        if (width % 8 || !stride_ok(q8_stride, width, 8) || !scales || !aligned4(scales)) return LORA_EINVAL;
+        if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256) return LORA_EINVAL;
+    }
+    const Span sx = span(x, rows, x_stride, 1, 0, width, 2), sr = span(residual, rows, residual_stride, 1, 0, width, 2);
+    const Span sw = span(weight, 1, 0, 1, 0, width, 2);
+    const Span sh = span(h_out, rows, h_stride, 1, 0, width, 2), sy = span(y, rows, y_stride, 1, 0, width, 2);
+    const Span sq = span(q8, rows, q8_stride, 1, 0, width, 1);
+    const Span ss = q8 ? span(scales, rows, group ? (width + group - 1) / group : 1, 1, 0, group ? (width + group - 1) / group : 1, 4)
+                       : Span();
+    const Span outs[4] = {sh, sy, sq, ss};
+    for (int i = 0; i < 4; ++i) {
+        if (meet(outs[i], sw)) return LORA_EINVAL;
+        for (int k = i + 1; k < 4; ++k)
+            if (meet(outs[i], outs[k])) return LORA_EINVAL;
+        // a row is read whole before its outputs are written, so h or y may be an input itself
+        const bool is_x = (i == 0 && h_out == x && h_stride == x_stride) || (i == 1 && y == x && y_stride == x_stride);
+        const bool is_r = residual && ((i == 0 && h_out == residual && h_stride == residual_stride) ||
+                                       (i == 1 && y == residual && y_stride == residual_stride));
+        if ((!is_x && meet(outs[i], sx)) || (!is_r && meet(outs[i], sr))) return LORA_EINVAL;
+    }
+    NormParams p;
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.h = h_out;
+    p.y = y;
+    p.q8 = q8;
+    p.scales = scales;
+    p.x_stride = x_stride;
+    p.r_stride = residual_stride;
+    p.h_stride = h_stride;
+    p.y_stride = y_stride;
+    p.q8_stride = q8_stride;
+    p.weight_offset = weight_offset;
+    p.eps = eps;
+    p.rows = rows;
+    p.width = width;
+    p.group = group;
+    return launch_add_rms_norm(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+extern "C" int lora_linear_kv_append(const lora_kv_cache* cache, const void* q, long long q_stride,
+                                     long long q_head_stride, void* q_out, long long qo_stride,
+                                     long long qo_head_stride, int n_heads, const void* k, long long k_stride,
+                                     long long k_head_stride, const void* v, long long v_stride,
+                                     long long v_head_stride, const float* cos, const float* sin, int rot,
+                                     int n_positions, void* stream) {
+    int rows = 0;
+    if (check_cache(cache, &rows) != LORA_OK) return LORA_EINVAL;
+    const int dim = cache->head_dim, n_kv = cache->n_kv_heads;
+    if (n_heads < 0 || n_heads > 65536 || rot < 0 || rot > dim || rot % 16) return LORA_EINVAL;
+    if (rot && (!cos || !sin || n_positions < 1 || !aligned4(cos) || !aligned4(sin))) return LORA_EINVAL;
+    if (rows == 0) return LORA_OK;
+    if ((q == nullptr) != (q_out == nullptr) || (q && n_heads < 1)) return LORA_EINVAL;
+    if (!k || !v || !aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v)) return LORA_EINVAL;
+    if (q && (!stride_ok(q_stride, dim, 8) || !stride_ok(q_head_stride, dim, 8) || !stride_ok(qo_stride, dim, 8) ||
+              !stride_ok(qo_head_stride, dim, 8)))
+        return LORA_EINVAL;
+    if (!stride_ok(k_stride, dim, 8) || !stride_ok(k_head_stride, dim, 8) || !stride_ok(v_stride, dim, 8) ||
+        !stride_ok(v_head_stride, dim, 8))
+        return LORA_EINVAL;
+    const Span kc = cache_span(cache, false), vc = cache_span(cache, true);
+    const Span sq = span(q, rows, q_stride, n_heads, q_head_stride, dim, 2);
+    const Span so = span(q_out, rows, qo_stride, n_heads, qo_head_stride, dim, 2);
+    const Span sk = span(k, rows, k_stride, n_kv, k_head_stride, dim, 2);
+    const Span sv = span(v, rows, v_stride, n_kv, v_head_stride, dim, 2);
+    if (meet(kc, sq) || meet(kc, sk) || meet(kc, sv) || meet(vc, sq) || meet(vc, sk) || meet(vc, sv) || meet(kc, so) ||
+        meet(vc, so))
+        return LORA_EINVAL;
+    const bool in_place = q && q == q_out && q_stride == qo_stride && q_head_stride == qo_head_stride;
+    // q, k and v may be slices of one buffer, so an output in place is checked against q alone
+    if (q && !in_place && (meet(so, sq) || meet(so, sk) || meet(so, sv))) return LORA_EINVAL;
+    AppendParams p;
+    p.c = view(cache);
+    p.q = q;
+    p.q_out = q_out;
+    p.k = k;
+    p.v = v;
+    p.cos = cos;
+    p.sin = sin;
+    p.q_stride = q_stride;
+    p.q_head = q_head_stride;
+    p.qo_stride = qo_stride;
+    p.qo_head = qo_head_stride;
+    p.k_stride = k_stride;
+    p.k_head = k_head_stride;
+    p.v_stride = v_stride;
+    p.v_head = v_head_stride;
+    p.n_heads = n_heads;
+    p.rot = rot;
+    p.n_positions = n_positions;
+    p.rows = rows;
+    return launch_kv_append(p, cache->q_offsets, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+extern "C" int lora_linear_attn_validate(int n_heads, int n_kv_heads, int head_dim, int page_size, int max_tokens,
+                                         int max_seqs, const lora_kv_cache* cache, const void* q, long long q_stride,
+                                         long long q_head_stride, const void* out, long long out_stride,
+                                         long long out_head_stride, float scale, int window, int sinks) {
+    int rows = 0;
+    if (check_layout(n_heads, n_kv_heads, head_dim, page_size, max_tokens, max_seqs) != LORA_OK) return LORA_EINVAL;
+    if (check_cache(cache, &rows) != LORA_OK) return LORA_EINVAL;
+    if (cache->n_kv_heads != n_kv_heads || cache->head_dim != head_dim || cache->page_size != page_size) return LORA_EINVAL;
+    if (cache->n_seqs > max_seqs || rows > max_tokens) return LORA_EINVAL;
+    if (!isfinite(scale) || !(scale > 0.f) || window < 0 || sinks < 0) return LORA_EINVAL;
+    if (rows == 0) return LORA_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return LORA_EINVAL;
+    if (!stride_ok(q_stride, head_dim, 8) || !stride_ok(q_head_stride, head_dim, 8) || !stride_ok(out_stride, head_dim, 8) ||
+        !stride_ok(out_head_stride, head_dim, 8))
+        return LORA_EINVAL;
+    const Span so = span(out, rows, out_stride, n_heads, out_head_stride, head_dim, 2);
+    if (meet(so, span(q, rows, q_stride, n_heads, q_head_stride, head_dim, 2)) || meet(so, cache_span(cache, false)) ||
+        meet(so, cache_span(cache, true)))
+        return LORA_EINVAL;
+    return LORA_OK;
+}
+
+extern "C" int lora_linear_attn_create(lora_attn** out, int n_heads, int n_kv_heads, int head_dim, int page_size,
+                                       int max_tokens, int max_seqs, int device) {
+    if (!out) return LORA_EINVAL;
+    *out = nullptr;
+    if (check_layout(n_heads, n_kv_heads, head_dim, page_size, max_tokens, max_seqs) != LORA_OK) return LORA_EINVAL;
+    int rc = check_device(device);
+    if (rc != LORA_OK) return rc;
+    lora_attn* h = new (std::nothrow) lora_attn;
+    if (!h) return LORA_ENOMEM;
+    h->device = device;
+    h->n_heads = n_heads;
+    h->n_kv = n_kv_heads;
+    h->dim = head_dim;
+    h->page_size = page_size;
+    h->max_tokens = max_tokens;
+    h->max_seqs = max_seqs;
+    DeviceGuard guard(device);
+    rc = LORA_OK;
+    if (!guard.ok ||
+        cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+        rc = LORA_ENODEV;
+    else if (cudaMalloc(reinterpret_cast<void**>(&h->status), sizeof(int)) != cudaSuccess)
+        rc = LORA_ENOMEM;
+    else if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess)
+        rc = LORA_ECUDA;
+    if (rc != LORA_OK) {
+        cudaGetLastError();
+        lora_linear_attn_destroy(h);
+        return rc;
+    }
+    *out = h;
+    return LORA_OK;
+}
+
+extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache, const void* q, long long q_stride,
+                                        long long q_head_stride, void* out, long long out_stride,
+                                        long long out_head_stride, float scale, int window, int sinks, void* stream) {
+    if (!h) return LORA_EINVAL;
+    if (lora_linear_attn_validate(h->n_heads, h->n_kv, h->dim, h->page_size, h->max_tokens, h->max_seqs, cache, q, q_stride,
+                                  q_head_stride, out, out_stride, out_head_stride, scale, window, sinks) != LORA_OK)
+        return LORA_EINVAL;
+    const int rows = cache->q_offsets[cache->n_seqs];
+    if (rows == 0) return LORA_OK;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LORA_ECUDA;
+    AttnParams p;
+    p.c = view(cache);
+    p.q = q;
+    p.out = out;
+    p.q_stride = q_stride;
+    p.q_head = q_head_stride;
+    p.o_stride = out_stride;
+    p.o_head = out_head_stride;
+    p.n_heads = h->n_heads;
+    p.rows = rows;
+    p.window = window;
+    p.sinks = window ? sinks : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = h->status;
+    p.wait_limit_ns = h->wait_limit_ns;
+    return launch_attention(p, cache->q_offsets, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+extern "C" int lora_linear_attn_status(lora_attn* h, int reset) {
+    if (!h) return LORA_EINVAL;
+    int v = 0;
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return LORA_ECUDA;
+    int rc = LORA_OK;
+    if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+        rc = LORA_ECUDA;
+    else if (reset && cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess)
+        rc = LORA_ECUDA;
+    return rc != LORA_OK ? rc : v ? LORA_ETIMEOUT : LORA_OK;
+}
+
+extern "C" int lora_linear_attn_destroy(lora_attn* h) {
+    if (!h) return LORA_OK;
+    {
+        DeviceGuard guard(h->device);
+        if (guard.ok) {
+            cudaDeviceSynchronize();
+            if (h->status) cudaFree(h->status);
+        }
+    }
+    delete h;
+    return LORA_OK;
+}

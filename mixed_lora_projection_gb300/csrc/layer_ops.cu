@@ -1,0 +1,273 @@
+// The residual's addition with the root-mean-square norm (bf16 or 8-bit output), and the append
+// of new keys and values to the paged cache with the rotary turn. Both move each byte once and
+// are bound by memory (or, on a few rows, by the latency of one pass).
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "layer_internal.h"
+
+namespace lora {
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// max that keeps a NaN of either side, so that a row with one gets NaN scales
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Reduces v over the block (NT threads) or, in the warp form, over the warp; every thread gets it.
+template <bool WARP, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* buf) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? max_nan(v, w) : v + w;
+    }
+    if (WARP) return v;
+    const int n = (int)(blockDim.x >> 5), lane = threadIdx.x & 31;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < n ? buf[lane] : 0.f;      // sums of squares and magnitudes: 0 is neutral to both
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? max_nan(v, w) : v + w;
+    }
+    return v;
+}
+
+constexpr float kE4m3Max = 448.f;
+
+// 8-bit output: scale of a maximum, floored so that its reciprocal is finite and a zero row is exact.
+__device__ __forceinline__ float scale_of(float amax) {
+    const float s = amax * (1.0f / kE4m3Max);
+    return s < 7.888609052210118e-31f ? 7.888609052210118e-31f : s;   // 2^-100; a NaN stays
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const float* f, float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi =
+            __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | hi << 16;
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// One row per block (or per warp: WARP), V 16-byte vectors of it per thread. The row stays in
+// registers between its sum of squares and its outputs, so x and the residual are read once.
+template <int V, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const NormParams p) {
+    __shared__ float buf[2][32];
+    const int nt = WARP ? 32 : (int)blockDim.x;
+    const int tid = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+    const int row = WARP ? (int)(blockIdx.x * 4 + (threadIdx.x >> 5)) : (int)blockIdx.x;
+    if (WARP && row >= p.rows) return;
+    const int nvec = p.width >> 3;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride);
+    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + row * p.r_stride);
+    const uint4* w = static_cast<const uint4*>(p.weight);
+    uint4 xv[V], rv[V], wv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        xv[i] = c < nvec ? x[c] : z;
+        rv[i] = (p.residual && c < nvec) ? r[c] : z;
+        wv[i] = c < nvec ? __ldg(w + c) : z;
+    }
+    float h[V][8], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float b[8];
+        unpack8(xv[i], h[i]);
+        if (p.residual) {
+            unpack8(rv[i], b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[i][k] += b[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = fmaf(h[i][k], h[i][k], ss);
+    }
+    if (p.h) {
+        uint4* ho = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) + row * p.h_stride);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (tid + i * nt < nvec) ho[tid + i * nt] = pack8(h[i]);
+    }
+    ss = row_reduce<WARP, false>(ss, buf[0]);
+    const float inv = rsqrtf(ss / (float)p.width + p.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float b[8];
+        unpack8(wv[i], b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[i][k] = h[i][k] * inv * (b[k] + p.weight_offset);
+    }
+    if (p.y) {
+        uint4* yo = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + row * p.y_stride);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (tid + i * nt < nvec) yo[tid + i * nt] = pack8(h[i]);
+    }
+    if (!p.q8) return;
+    uint2* qo = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q8) + row * p.q8_stride);
+    float amax[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        amax[i] = 0.f;
+        // a thread past the row's end holds zeros (0 * inv), unless inv is not finite
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax[i] = max_nan(amax[i], fabsf(h[i][k]));
+        if (tid + i * nt >= nvec) amax[i] = 0.f;
+    }
+    if (p.group == 0) {
+        float m = amax[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) m = max_nan(m, amax[i]);
+        const float s = scale_of(row_reduce<WARP, true>(m, buf[1]));
+        const float si = 1.f / s;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (tid + i * nt < nvec) qo[tid + i * nt] = to_e4m3(h[i], si);
+        if (tid == 0) p.scales[row] = s;
+        return;
+    }
+    // a group is group / 8 vectors: as many neighbouring lanes, since nt is a multiple of 32
+    const int lanes = p.group >> 3, ng = (p.width + p.group - 1) / p.group;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        float m = amax[i];
+        for (int o = lanes >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = scale_of(m);
+        if (c < nvec) {
+            qo[c] = to_e4m3(h[i], 1.f / s);
+            if ((c & (lanes - 1)) == 0) p.scales[(long long)row * ng + c / lanes] = s;
+        }
+    }
+}
+
+// Turns 8 features of each half: (a, b) -> (a cos - b sin, b cos + a sin).
+__device__ __forceinline__ void turn8(float* a, float* b, const float* cs, const float* sn) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = a[i], y = b[i], c = __ldg(cs + i), s = __ldg(sn + i);
+        a[i] = x * c - y * s;
+        b[i] = y * c + x * s;
+    }
+}
+
+// One block per new row: its sequence, position and place in the cache once, then its heads'
+// 16-byte vectors, those of the two rotary halves in pairs.
+template <int N>
+__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendParams p,
+                                                        const __grid_constant__ SeqOffsets<N> o) {
+    const int t = blockIdx.x;
+    int lo = 0, hi = p.c.n_seqs - 1;                 // the last sequence that begins at or before t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (o.off[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const long long cap = (long long)p.c.pages_per_seq * p.c.page_size;
+    const int len = (int)min((long long)max(p.c.kv_lens[lo], 0), cap);
+    const int pos = len - (o.off[lo + 1] - t);
+    const int rp = min(max(pos, 0), p.n_positions - 1);
+    int page = -1, slot = 0;
+    if (pos >= 0) {
+        page = p.c.table[lo * p.c.table_stride + pos / p.c.page_size];
+        slot = pos % p.c.page_size;
+        if (page >= p.c.n_pages) page = -1;
+    }
+    const int pairs = p.rot >> 4, single = (p.c.dim - p.rot) >> 3;
+    const int per = pairs + single;                  // items of a turned head
+    const int nq = p.q_out ? p.n_heads * per : 0, nk = p.c.n_kv * per, nv = p.c.n_kv * (p.c.dim >> 3);
+    const float* cs = p.cos + (long long)rp * (p.rot >> 1);
+    const float* sn = p.sin + (long long)rp * (p.rot >> 1);
+    typedef __nv_bfloat16 bf;
+    bf* kd = static_cast<bf*>(p.c.k) + page * p.c.k_page + slot * p.c.k_token;
+    bf* vd = static_cast<bf*>(p.c.v) + page * p.c.v_page + slot * p.c.v_token;
+    const int end = page >= 0 ? nq + nk + nv : nq;
+    for (int i = threadIdx.x; i < end; i += blockDim.x) {
+        if (i >= nq + nk) {
+            const int u = i - nq - nk, per_v = p.c.dim >> 3, h = u / per_v, c = u - h * per_v;
+            const bf* s = static_cast<const bf*>(p.v) + t * p.v_stride + h * p.v_head;
+            reinterpret_cast<uint4*>(vd + h * p.c.v_head)[c] = reinterpret_cast<const uint4*>(s)[c];
+            continue;
+        }
+        const bool is_q = i < nq;
+        const int u = is_q ? i : i - nq, h = u / per, c = u - h * per;
+        const bf* s = is_q ? static_cast<const bf*>(p.q) + t * p.q_stride + h * p.q_head
+                           : static_cast<const bf*>(p.k) + t * p.k_stride + h * p.k_head;
+        bf* d = is_q ? static_cast<bf*>(p.q_out) + t * p.qo_stride + h * p.qo_head : kd + h * p.c.k_head;
+        if (c >= pairs) {
+            const int e = p.rot + ((c - pairs) << 3);
+            *reinterpret_cast<uint4*>(d + e) = *reinterpret_cast<const uint4*>(s + e);
+            continue;
+        }
+        const int e = c << 3, f = e + (p.rot >> 1);
+        float a[8], b[8];
+        unpack8(*reinterpret_cast<const uint4*>(s + e), a);
+        unpack8(*reinterpret_cast<const uint4*>(s + f), b);
+        turn8(a, b, cs + e, sn + e);
+        *reinterpret_cast<uint4*>(d + e) = pack8(a);
+        *reinterpret_cast<uint4*>(d + f) = pack8(b);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream) {
+    const int nvec = p.width >> 3;
+    if (nvec <= 128) {
+        const int grid = (p.rows + 3) / 4;
+        if (nvec <= 32) add_rms_norm_kernel<1, true><<<grid, 128, 0, stream>>>(p);
+        else if (nvec <= 64) add_rms_norm_kernel<2, true><<<grid, 128, 0, stream>>>(p);
+        else add_rms_norm_kernel<4, true><<<grid, 128, 0, stream>>>(p);
+    } else {
+        const int v = nvec > 2048 || p.rows > 304 ? 4 : nvec > 1024 ? 2 : 1;
+        const int nt = ((nvec + v - 1) / v + 31) / 32 * 32;
+        if (v == 1) add_rms_norm_kernel<1, false><<<p.rows, nt, 0, stream>>>(p);
+        else if (v == 2) add_rms_norm_kernel<2, false><<<p.rows, nt, 0, stream>>>(p);
+        else add_rms_norm_kernel<4, false><<<p.rows, nt, 0, stream>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+template <int N>
+static cudaError_t append(const AppendParams& p, const int32_t* off, cudaStream_t stream) {
+    SeqOffsets<N> o;
+    for (int i = 0; i <= p.c.n_seqs; ++i) o.off[i] = off[i];
+    kv_append_kernel<N><<<p.rows, 256, 0, stream>>>(p, o);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const AppendParams& p, const int32_t* q_offsets, cudaStream_t stream) {
+    return p.c.n_seqs <= kSmallSeqs ? append<kSmallSeqs>(p, q_offsets, stream) : append<kMaxSeqs>(p, q_offsets, stream);
+}
+
+}  // namespace lora
