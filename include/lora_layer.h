@@ -33,6 +33,7 @@ extern "C" {
 
 #define LORA_LAYER_MAX_WIDTH 32768 /* features of a normalised row */
 #define LORA_LAYER_MAX_SEQS 1024   /* sequences of one call */
+#define LORA_LAYER_MAX_CONTEXT (1 << 27) /* pages_per_seq x page_size: tokens a sequence's table can hold */
 
 /*
  * lora_linear_add_rms_norm -- for every row t of x [rows, width]:

@@ -1,0 +1,584 @@
+// Attention of a few new rows per sequence over the paged cache (at most 64 rows per key/value head:
+// q_len x query heads per key/value head).
+//
+// The work is one pass over K and V, so it is bound by memory. All cache tiles of the call (64
+// tokens of one head), sequence after sequence and head after head, form one line that is cut into
+// equal parts, one per block: uneven lengths and few sequences fill the GPU alike. A block's part
+// may end inside a unit (one head of one sequence); what it has then, unnormalised sums o with their
+// running maximum m and sum l per row, goes to the workspace, and a second small kernel joins a
+// unit's parts c in their order: M = max m_c, o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c.
+//
+// A block is four consumer warps and a TMA producer warp with a ring of K and V tiles. Per tile each
+// consumer computes the scores of 16 tokens (mma.sync m16n8k16: rows are padded to 16 MT), the warps
+// exchange row maxima, write the weights to shared memory as bf16 (the product with V takes bf16
+// operands; their sum is kept of the unrounded fp32 weights) and each adds a quarter of the features
+// of the product with V. With at most 64 rows the matrix work is a fraction of the loads' time, so
+// the warp-level instruction serves; a tcgen05 tile would pad the rows to 128.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn_common.cuh"
+
+namespace lora {
+namespace {
+
+using namespace dev;
+
+constexpr int kTk = kDecodeTile;
+constexpr int kConsumers = 128;
+constexpr int kDecodeThreads = 160;
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
+
+// First flat tile of block c of g: the line of w tiles cut into g equal parts.
+__device__ __forceinline__ unsigned long long part_begin(unsigned long long w, unsigned g, unsigned c) { return w * c / g; }
+// The block that flat tile t belongs to.
+__device__ __forceinline__ unsigned part_of(unsigned long long w, unsigned g, unsigned long long t) {
+    return (unsigned)(((t + 1) * g - 1) / w);
+}
+
+// Shared memory: Q rows, weights, row maxima and sums, prefix, barriers, then the ring (1024-aligned).
+template <int D, int MT>
+struct Layout {
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kQStride = D + 8, kPStride = kTk + 8;   // padded rows: conflict-free ldmatrix
+    static constexpr int kP = kRows * kQStride * 2;
+    static constexpr int kMax = kP + kRows * kPStride * 2;
+    static constexpr int kSum = kMax + 4 * kRows * 4;
+    static constexpr int kBars = kSum + 4 * kRows * 4;           // full[slots], empty[slots] (16 at most each)
+    static constexpr int kAbort = kBars + 32 * 8;
+    static constexpr int kPrefix = kAbort + 16;
+    static constexpr int kSlot = kTk * D * 2;
+};
+
+// Where a block's walk over its part is: a piece of one unit at a time.
+struct Walk {
+    unsigned long long at, end;
+    int i;               // sequence of the list
+};
+
+template <int D, int MT, int N>
+__global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
+    decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ SeqList<N> list) {
+    using S = Layout<D, MT>;
+    constexpr int kRows = S::kRows;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t* full = reinterpret_cast<uint64_t*>(raw + S::kBars);
+    uint64_t* empty = full + 16;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(raw + S::kAbort);
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(raw + S::kPrefix);
+    const uint32_t ring = (smem_addr(raw + S::kPrefix + (list.n + 1) * 4) + 1023u) & ~1023u;
+    const int slots = p.slots;
+
+    if (tid == 0) {
+        for (int s = 0; s < slots; ++s) {
+            mbar_init(smem_addr(&full[s]), 1);
+            mbar_init(smem_addr(&empty[s]), 4);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
+    // tiles of one head before each sequence
+    const AttnParams& a = p.a;
+    for (int i = tid; i < list.n; i += kDecodeThreads) {
+        const int len = cache_len(a.c, list.seq[i]);
+        prefix[i + 1] = (uint32_t)tile_range(len - list.q_len[i], len - 1, a.window, a.sinks, kTk).n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t carry = 0;
+        for (int i0 = 0; i0 < list.n; i0 += 32) {
+            uint32_t v = i0 + lane < list.n ? prefix[i0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (i0 + lane < list.n) prefix[i0 + lane + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+    const int n_kv = a.c.n_kv;
+    const unsigned long long total = (unsigned long long)prefix[list.n] * n_kv;
+    const unsigned grid = (unsigned)min((unsigned long long)gridDim.x, total);
+    if (blockIdx.x == 0)
+        for (int i = tid; i <= list.n; i += kDecodeThreads) p.prefix[i] = prefix[i];
+    griddep_launch_dependents();
+    if (blockIdx.x >= grid) return;      // no tile left (or none at all: the join writes the zeros)
+    Walk w;
+    w.at = part_begin(total, grid, blockIdx.x);
+    w.end = part_begin(total, grid, blockIdx.x + 1);
+    {
+        int lo = 0, hi = list.n - 1;     // the last sequence that begins at or before the first tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((unsigned long long)prefix[mid] * n_kv <= w.at) lo = mid; else hi = mid - 1;
+        }
+        w.i = lo;
+    }
+    const uint64_t limit = a.wait_limit_ns;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ producer
+        const int chunks = D / 64, boxes = (kTk / p.granule) * chunks;
+        const int gi = lane / chunks, ch = lane % chunks;
+        const uint32_t box_bytes = (uint32_t)p.granule * 128;
+        int slot = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && w.at < w.end) {
+            const uint32_t nt = prefix[w.i + 1] - prefix[w.i];
+            if (nt == 0) {
+                ++w.i;
+                continue;
+            }
+            const unsigned long long rel = w.at - (unsigned long long)prefix[w.i] * n_kv;
+            const int head = (int)(rel / nt), t0 = (int)(rel % nt);
+            const int t1 = (int)min((unsigned long long)nt, t0 + (w.end - w.at));
+            const int s = list.seq[w.i], len = cache_len(a.c, s);
+            const TileRange r = tile_range(len - list.q_len[w.i], len - 1, a.window, a.sinks, kTk);
+            const int32_t* table = a.c.table + s * a.c.table_stride;
+            // this lane's granule of tile t: its page (one past the last: zeros) and token in it
+            auto place = [&](int t, int& page, int& tok) {
+                const int j = tile_token(r, t, kTk) + gi * p.granule;
+                page = -1;
+                tok = 0;
+                if (lane < boxes && j < len) {
+                    const int pg = j / a.c.page_size;
+                    page = table[pg];
+                    tok = j - pg * a.c.page_size;
+                    if (page < 0 || page >= a.c.n_pages) page = a.c.n_pages;
+                }
+            };
+            int page, tok;
+            place(t0, page, tok);
+            for (int t = t0; t < t1 && ok; ++t) {
+                int npage = -1, ntok = 0;
+                if (t + 1 < t1) place(t + 1, npage, ntok);       // the next tile's pages, ahead of its turn
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_addr(&full[slot]);
+                    mbar_arrive_expect_tx(bar, bytes, lane == 0);
+                    __syncwarp();
+                    if (page >= 0)
+                        tma_load_kv(ring + (uint32_t)slot * S::kSlot + (uint32_t)ch * (kTk * 128) + (uint32_t)gi * box_bytes,
+                                    kv ? &p.tm_v : &p.tm_k, bar, kv ? p.v_order : p.k_order, ch * 64, head, tok, page);
+                    ++issued;
+                    if (++slot == slots) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                page = npage;
+                tok = ntok;
+            }
+            w.at += t1 - t0;
+            if ((unsigned long long)prefix[w.i + 1] * n_kv <= w.at) ++w.i;
+        }
+        if (!ok)                         // gave up: wait for the copies in flight before the block may end
+            for (int k = max(0, issued - slots); k < issued; ++k)
+                if (lane == 0)
+                    wait_bounded(smem_addr(&full[k % slots]), (uint32_t)((k / slots) & 1), abort_flag, a.status, limit, false);
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int gr = lane >> 2, gc = lane & 3;
+    const uint32_t q_base = smem_addr(raw), p_base = smem_addr(raw + S::kP);
+    float* smax = reinterpret_cast<float*>(raw + S::kMax);
+    float* ssum = reinterpret_cast<float*>(raw + S::kSum);
+    const int g = p.group;
+    int slot = 0;
+    uint32_t phase = 0;
+    // after a wait that ran out the warps run on without data, so that their barriers stay matched;
+    // the status word says that the output is incomplete
+    while (w.at < w.end) {
+        const uint32_t nt = prefix[w.i + 1] - prefix[w.i];
+        if (nt == 0) {
+            ++w.i;
+            continue;
+        }
+        const unsigned long long rel = w.at - (unsigned long long)prefix[w.i] * n_kv;
+        const int head = (int)(rel / nt), t0 = (int)(rel % nt);
+        const int t1 = (int)min((unsigned long long)nt, t0 + (w.end - w.at));
+        const int s = list.seq[w.i], q_len = list.q_len[w.i], len = cache_len(a.c, s);
+        const TileRange r = tile_range(len - q_len, len - 1, a.window, a.sinks, kTk);
+        const int rows = q_len * g;
+        // this unit's queries
+        for (int v = tid; v < kRows * (D / 8); v += kConsumers) {
+            const int row = v / (D / 8), c = v % (D / 8);
+            uint4 val = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+                const int qi = row / g, hq = head * g + row - qi * g;
+                val = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                      (list.row[w.i] + qi) * a.q_stride + hq * a.q_head + c * 8);
+            }
+            *reinterpret_cast<uint4*>(raw + row * S::kQStride * 2 + c * 16) = val;
+        }
+        int pos[MT][2];
+        float m[MT][2], l[MT][2];
+        float o[MT][D / 32][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = mt * 16 + gr + 8 * h;
+                pos[mt][h] = row < rows ? r.first + row / g : -1;
+                m[mt][h] = -INFINITY;
+                l[mt][h] = 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+        }
+        consumer_sync();
+
+        for (int t = t0; t < t1; ++t) {
+            const int j0 = tile_token(r, t, kTk);
+            // ---- scores of this warp's 16 tokens
+            constexpr int SP = MT == 1 ? 2 : 1;      // one row tile: two chains of products
+            float sc[SP][MT][2][4];
+#pragma unroll
+            for (int x = 0; x < SP; ++x)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[x][mt][n][e] = 0.f;
+            wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
+            {
+                const uint32_t kt = ring + (uint32_t)slot * S::kSlot;
+                const int tok = warp * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+                const uint32_t krow = kt + (uint32_t)tok * 128;
+                const uint32_t qrow = q_base + (uint32_t)((lane & 7) + ((lane >> 3) & 1) * 8) * (S::kQStride * 2) + (lane >> 4) * 16;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t b[4];
+                    const int idx = (kk & 3) * 2 + ((lane >> 3) & 1);
+                    ldsm4(krow + (kk >> 2) * (kTk * 128) + ((idx ^ (tok & 7)) << 4), b);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint32_t q4[4];
+                        ldsm4(qrow + mt * 16 * (S::kQStride * 2) + kk * 32, q4);
+                        mma16816(sc[kk % SP][mt][0], q4, b[0], b[1]);
+                        mma16816(sc[kk % SP][mt][1], q4, b[2], b[3]);
+                    }
+                }
+            }
+            const int kslot = slot;
+            if (++slot == slots) {
+                slot = 0;
+                phase ^= 1;
+            }
+            float mx[MT][2];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                mx[mt][0] = mx[mt][1] = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + warp * 16 + n * 8 + gc * 2 + (e & 1), ps = pos[mt][e >> 1];
+                        float x = sc[0][mt][n][e];
+                        if (SP == 2) x += sc[SP - 1][mt][n][e];
+                        x *= a.scale_log2;
+                        const bool seen = j <= ps && (a.window == 0 || j > ps - a.window || j < a.sinks);
+                        x = seen ? x : -INFINITY;
+                        sc[0][mt][n][e] = x;
+                        mx[mt][e >> 1] = fmaxf(mx[mt][e >> 1], x);
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mx[mt][h] = fmaxf(mx[mt][h], __shfl_xor_sync(0xffffffffu, mx[mt][h], 1));
+                    mx[mt][h] = fmaxf(mx[mt][h], __shfl_xor_sync(0xffffffffu, mx[mt][h], 2));
+                    if (gc == 0) smax[warp * kRows + mt * 16 + gr + 8 * h] = mx[mt][h];
+                }
+            }
+            consumer_sync();
+            if (lane == 0) mbar_arrive(smem_addr(&empty[kslot]));
+            // ---- weights
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = mt * 16 + gr + 8 * h;
+                    float mn = m[mt][h];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mn = fmaxf(mn, smax[x * kRows + row]);
+                    const float ms = mn == -INFINITY ? 0.f : mn;
+                    const float alpha = ex2(m[mt][h] - ms);
+                    m[mt][h] = mn;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float w0 = ex2(sc[0][mt][n][2 * h] - ms), w1 = ex2(sc[0][mt][n][2 * h + 1] - ms);
+                        sum += w0 + w1;
+                        *reinterpret_cast<uint32_t*>(raw + S::kP + row * S::kPStride * 2 + (warp * 16 + n * 8 + gc * 2) * 2) =
+                            pack_bf16x2(w0, w1);
+                    }
+                    l[mt][h] = l[mt][h] * alpha + sum;
+                    if (alpha != 1.f) {
+#pragma unroll
+                        for (int n = 0; n < D / 32; ++n) {
+                            o[mt][n][2 * h] *= alpha;
+                            o[mt][n][2 * h + 1] *= alpha;
+                        }
+                    }
+                }
+            wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
+            const uint32_t vt = ring + (uint32_t)slot * S::kSlot;
+            const bool tail = r.len - j0 < kTk;
+            if (tail) {                  // places past the last token may hold anything: their weight is 0, so they must be finite
+                const int valid = r.len - j0;
+                for (int v = valid * (D / 8) + tid; v < kTk * (D / 8); v += kConsumers) {
+                    const int tok = v / (D / 8), c = v % (D / 8);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vt + (c >> 3) * (kTk * 128) + tok * 128 + (c & 7) * 16),
+                                 "r"(0)
+                                 : "memory");
+                }
+                fence_proxy_async_shared();
+            }
+            consumer_sync();
+            // ---- product with V: this warp's quarter of the features
+            {
+                const int tok = (lane & 7) + ((lane >> 3) & 1) * 8;
+                const uint32_t prow = p_base + (uint32_t)tok * (S::kPStride * 2) + (lane >> 4) * 16;
+#pragma unroll
+                for (int kt = 0; kt < kTk / 16; ++kt) {
+                    uint32_t pa[MT][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) ldsm4(prow + mt * 16 * (S::kPStride * 2) + kt * 32, pa[mt]);
+                    const uint32_t vrow = vt + (uint32_t)(kt * 16 + tok) * 128;
+#pragma unroll
+                    for (int np = 0; np < D / 64; ++np) {
+                        uint32_t b[4];
+                        const int dv = warp * (D / 32) + np * 2 + (lane >> 4);
+                        ldsm4t(vrow + (dv >> 3) * (kTk * 128) + (((dv & 7) ^ (tok & 7)) << 4), b);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma16816(o[mt][2 * np], pa[mt], b[0], b[1]);
+                            mma16816(o[mt][2 * np + 1], pa[mt], b[2], b[3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&empty[slot]));
+            if (++slot == slots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+
+        // ---- the piece's end: the warps' sums of weights together
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x = l[mt][h];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                if (gc == 0) ssum[warp * kRows + mt * 16 + gr + 8 * h] = x;
+            }
+        consumer_sync();
+        const bool whole = t0 == 0 && t1 == (int)nt;
+        const long long part = 2ll * blockIdx.x + (t0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = mt * 16 + gr + 8 * h;
+                if (row >= rows) continue;
+                float sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sum += ssum[x * kRows + row];
+                if (whole) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    const int qi = row / g, hq = head * g + row - qi * g;
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (list.row[w.i] + qi) * a.o_stride + hq * a.o_head +
+                                         warp * (D / 4) + gc * 2;
+#pragma unroll
+                    for (int n = 0; n < D / 32; ++n)
+                        *reinterpret_cast<uint32_t*>(out + n * 8) = pack_bf16x2(o[mt][n][2 * h] * inv, o[mt][n][2 * h + 1] * inv);
+                } else {
+                    float* po = p.part_o + (part * kRows + row) * D + warp * (D / 4) + gc * 2;
+#pragma unroll
+                    for (int n = 0; n < D / 32; ++n)
+                        *reinterpret_cast<float2*>(po + n * 8) = make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
+                    if (warp == 0 && gc == 0) p.part_ml[part * kRows + row] = make_float2(m[mt][h], sum);
+                }
+            }
+        w.at += t1 - t0;
+        if ((unsigned long long)prefix[w.i + 1] * n_kv <= w.at) ++w.i;
+    }
+}
+
+// Joins the parts of split units: one block per row of a unit, its four warps take every fourth part.
+// Also writes the zeros of sequences without a visible token.
+template <int D, int MT, int N>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ SeqList<N> list) {
+    constexpr int kRows = 16 * MT, E = D / 32;
+    __shared__ float acc[4][D];
+    __shared__ float2 ml[4];
+    const int most = (int)gridDim.x / p.a.c.n_kv;    // rows of the longest sequence
+    const int i = blockIdx.y, head = blockIdx.x / most, row = blockIdx.x % most, g = p.group;
+    if (row >= list.q_len[i] * g) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_wait();
+    const AttnParams& a = p.a;
+    const uint32_t p0 = p.prefix[i], nt = p.prefix[i + 1] - p0;
+    const unsigned long long total = (unsigned long long)p.prefix[list.n] * a.c.n_kv;
+    const unsigned grid = (unsigned)min((unsigned long long)p.grid, total);
+    const int qi = row / g, hq = head * g + row - qi * g;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (list.row[i] + qi) * a.o_stride + hq * a.o_head;
+    if (nt == 0) {
+        for (int e = threadIdx.x; e < D; e += 128) out[e] = __float2bfloat16_rn(0.f);
+        return;
+    }
+    const unsigned long long first = (unsigned long long)p0 * a.c.n_kv + (unsigned long long)head * nt;
+    const unsigned c0 = part_of(total, grid, first), c1 = part_of(total, grid, first + nt - 1);
+    if (c0 == c1) return;                // one block had the whole unit and wrote it
+    float m = -INFINITY;
+    for (unsigned c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[(2ll * c + (c == c0)) * kRows + row].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float ms = m == -INFINITY ? 0.f : m;
+    float o[E], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (unsigned c = c0 + warp; c <= c1; c += 4) {
+        const long long at = (2ll * c + (c == c0)) * kRows + row;
+        const float2 x = p.part_ml[at];
+        const float w = ex2(x.x - ms);
+        l = fmaf(x.y, w, l);
+        const float* src = p.part_o + at * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src + e);
+            o[e] = fmaf(v.x, w, o[e]);
+            o[e + 1] = fmaf(v.y, w, o[e + 1]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = o[e];
+    if (lane == 0) ml[warp].y = l;
+    __syncthreads();
+    l = ml[0].y + ml[1].y + ml[2].y + ml[3].y;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int e = threadIdx.x; e < D; e += 128)
+        out[e] = __float2bfloat16_rn((acc[0][e] + acc[1][e] + acc[2][e] + acc[3][e]) * inv);
+}
+
+template <int D, int MT, int N>
+cudaError_t launch_n(const DecodeParams& p, const SeqList<kMaxSeqs>& all, cudaStream_t stream) {
+    SeqList<N> list;
+    list.n = all.n;
+    int most = 0;
+    for (int i = 0; i < all.n; ++i) {
+        list.row[i] = all.row[i];
+        list.q_len[i] = all.q_len[i];
+        list.seq[i] = all.seq[i];
+        most = all.q_len[i] > most ? all.q_len[i] : most;
+    }
+    const size_t smem = decode_smem(D, MT, p.slots, all.n);
+    decode_kernel<D, MT, N><<<p.grid, kDecodeThreads, smem, stream>>>(p, list);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.a.c.n_kv * most * p.group), (unsigned)all.n);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, MT, N>, p, list);
+}
+
+template <int D, int MT>
+cudaError_t launch_mt(const DecodeParams& p, const SeqList<kMaxSeqs>& l, cudaStream_t s) {
+    return l.n <= kSmallSeqs ? launch_n<D, MT, kSmallSeqs>(p, l, s) : launch_n<D, MT, kMaxSeqs>(p, l, s);
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeParams& p, const SeqList<kMaxSeqs>& l, int mt, cudaStream_t s) {
+    if (mt == 1) return launch_mt<D, 1>(p, l, s);
+    if (mt == 2) return launch_mt<D, 2>(p, l, s);
+    if (mt == 3) return launch_mt<D, 3>(p, l, s);
+    return launch_mt<D, 4>(p, l, s);
+}
+
+template <int D, int MT>
+cudaError_t opt_in() {
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MT, kSmallSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - 1024);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(decode_kernel<D, MT, kMaxSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - 1024);
+}
+
+template <int D>
+cudaError_t opt_in_d() {
+    cudaError_t e = opt_in<D, 1>();
+    if (e == cudaSuccess) e = opt_in<D, 2>();
+    if (e == cudaSuccess) e = opt_in<D, 3>();
+    if (e == cudaSuccess) e = opt_in<D, 4>();
+    return e;
+}
+
+template <int D>
+size_t fixed_bytes(int mt) {
+    return mt == 1 ? Layout<D, 1>::kPrefix : mt == 2 ? Layout<D, 2>::kPrefix : mt == 3 ? Layout<D, 3>::kPrefix : Layout<D, 4>::kPrefix;
+}
+
+}  // namespace
+
+size_t decode_smem(int dim, int mt, int slots, int seqs) {
+    const size_t fixed = dim == 64 ? fixed_bytes<64>(mt) : dim == 128 ? fixed_bytes<128>(mt) : fixed_bytes<256>(mt);
+    return fixed + (size_t)(seqs + 1) * 4 + 1024 + (size_t)slots * kDecodeTile * dim * 2;
+}
+
+cudaError_t decode_prepare_device() {
+    cudaError_t e = opt_in_d<64>();
+    if (e == cudaSuccess) e = opt_in_d<128>();
+    if (e == cudaSuccess) e = opt_in_d<256>();
+    return e;
+}
+
+cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, int mt, cudaStream_t stream) {
+    if (p.a.c.dim == 64) return launch_d<64>(p, seqs, mt, stream);
+    if (p.a.c.dim == 128) return launch_d<128>(p, seqs, mt, stream);
+    return launch_d<256>(p, seqs, mt, stream);
+}
+
+}  // namespace lora

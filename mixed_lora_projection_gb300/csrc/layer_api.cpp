@@ -5,6 +5,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <new>
 
 #include "../../include/lora_layer.h"
@@ -60,7 +61,7 @@ int check_cache(const lora_kv_cache* c, int* rows) {
     if (check_offsets(c->q_offsets, c->n_seqs, rows) != LORA_OK) return LORA_EINVAL;
     if (c->n_kv_heads < 1 || c->n_kv_heads > 4096 || c->head_dim < 8 || c->head_dim > 512 || c->head_dim % 8) return LORA_EINVAL;
     if (c->page_size < 16 || c->page_size > (1 << 20) || c->page_size % 16) return LORA_EINVAL;
-    if (c->n_pages < 1 || c->pages_per_seq < 1 || (long long)c->pages_per_seq * c->page_size > 0x7fffff00ll) return LORA_EINVAL;
+    if (c->n_pages < 1 || c->pages_per_seq < 1 || (long long)c->pages_per_seq * c->page_size > LORA_LAYER_MAX_CONTEXT) return LORA_EINVAL;
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return LORA_EINVAL;
     const long long s[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
                             c->v_page_stride, c->v_token_stride, c->v_head_stride};
@@ -123,6 +124,32 @@ int check_layout(int n_heads, int n_kv, int dim, int page_size, int max_tokens, 
     return LORA_OK;
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map of a cache: 64 features of one head by `granule` tokens of one page, rows 128-byte
+// swizzled. The axes past the features go by ascending stride, whatever the caller's layout;
+// *order says which of (0 head, 1 token, 2 page) each of them is, two bits per axis.
+bool encode_cache(EncodeTiledFn encode, CUtensorMap* m, int* order, const CacheView& c, bool v, int granule) {
+    struct Axis {
+        int what;
+        uint64_t stride, size;
+        uint32_t box;
+    } ax[3] = {{0, (uint64_t)(v ? c.v_head : c.k_head), (uint64_t)c.n_kv, 1},
+               {1, (uint64_t)(v ? c.v_token : c.k_token), (uint64_t)c.page_size, (uint32_t)granule},
+               {2, (uint64_t)(v ? c.v_page : c.k_page), (uint64_t)c.n_pages, 1}};
+    std::stable_sort(ax, ax + 3, [](const Axis& a, const Axis& b) { return a.stride < b.stride; });
+    cuuint64_t dims[4] = {(cuuint64_t)c.dim, ax[0].size, ax[1].size, ax[2].size};
+    cuuint64_t strides[3] = {ax[0].stride * 2, ax[1].stride * 2, ax[2].stride * 2};
+    cuuint32_t box[4] = {64, ax[0].box, ax[1].box, ax[2].box};
+    cuuint32_t step[4] = {1, 1, 1, 1};
+    *order = ax[0].what | ax[1].what << 2 | ax[2].what << 4;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v ? c.v : c.k, dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Makes `device` current for the life of a call.
 struct DeviceGuard {
     int prev = -1;
@@ -143,7 +170,56 @@ struct lora_attn {
     int num_sms = 0;
     int* status = nullptr;
     unsigned long long wait_limit_ns = 4000000000ull;
+    EncodeTiledFn encode = nullptr;
+    float* part_o = nullptr;            // sums of split units, their maxima and sums of weights
+    float2* part_ml = nullptr;
+    uint32_t* prefix = nullptr;
 };
+
+namespace {
+
+// Everything a handle needs beside itself, on its device (which is current).
+int set_up(lora_attn* h) {
+    if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) return LORA_ENODEV;
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+        return LORA_ECUDA;
+    h->encode = reinterpret_cast<EncodeTiledFn>(fn);
+    if (decode_prepare_device() != cudaSuccess) return LORA_ECUDA;
+    const size_t parts = 2 * (size_t)h->num_sms * kDecodeRows;     // two a block; 16 rows where two blocks share an SM
+    if (cudaMalloc(reinterpret_cast<void**>(&h->status), sizeof(int)) != cudaSuccess ||
+        cudaMalloc(reinterpret_cast<void**>(&h->part_o), parts * h->dim * sizeof(float)) != cudaSuccess ||
+        cudaMalloc(reinterpret_cast<void**>(&h->part_ml), parts * sizeof(float2)) != cudaSuccess ||
+        cudaMalloc(reinterpret_cast<void**>(&h->prefix), (h->max_seqs + 1) * sizeof(uint32_t)) != cudaSuccess)
+        return LORA_ENOMEM;
+    return cudaMemset(h->status, 0, sizeof(int)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+// The decode kernel on the sequences of `list` (at most kDecodeRows rows per key/value head each).
+int run_decode(lora_attn* h, const AttnParams& a, const SeqList<kMaxSeqs>& list, int rows) {
+    DecodeParams p;
+    p.a = a;
+    p.group = h->n_heads / h->n_kv;
+    p.granule = kDecodeTile;                     // a power of two that divides the tile and the page
+    while (h->page_size % p.granule) p.granule /= 2;
+    const int mt = (rows + 15) / 16;
+    // blocks share an SM in pairs where 16 rows leave each a ring worth having
+    const size_t most = mt == 1 ? kSmemTwo : 231424;
+    p.slots = 16;
+    while (p.slots > 2 && decode_smem(h->dim, mt, p.slots, list.n) > most) --p.slots;
+    p.grid = h->num_sms * (mt == 1 ? 2 : 1);
+    p.part_o = h->part_o;
+    p.part_ml = h->part_ml;
+    p.prefix = h->prefix;
+    if (!encode_cache(h->encode, &p.tm_k, &p.k_order, a.c, false, p.granule) ||
+        !encode_cache(h->encode, &p.tm_v, &p.v_order, a.c, true, p.granule))
+        return LORA_EINVAL;
+    return launch_decode(p, list, mt, a.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+}  // namespace
 
 extern "C" int lora_linear_add_rms_norm(const void* x, long long x_stride, const void* residual,
                                         long long residual_stride, const void* weight, float weight_offset, float eps,
@@ -294,14 +370,7 @@ extern "C" int lora_linear_attn_create(lora_attn** out, int n_heads, int n_kv_he
     h->max_tokens = max_tokens;
     h->max_seqs = max_seqs;
     DeviceGuard guard(device);
-    rc = LORA_OK;
-    if (!guard.ok ||
-        cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
-        rc = LORA_ENODEV;
-    else if (cudaMalloc(reinterpret_cast<void**>(&h->status), sizeof(int)) != cudaSuccess)
-        rc = LORA_ENOMEM;
-    else if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess)
-        rc = LORA_ECUDA;
+    rc = guard.ok ? set_up(h) : LORA_ENODEV;
     if (rc != LORA_OK) {
         cudaGetLastError();
         lora_linear_attn_destroy(h);
@@ -337,7 +406,26 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = h->status;
     p.wait_limit_ns = h->wait_limit_ns;
-    return launch_attention(p, cache->q_offsets, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+    p.stream = static_cast<cudaStream_t>(stream);
+    // sequences with few rows and long ones go to different kernels
+    const int g = h->n_heads / h->n_kv;
+    SeqList<kMaxSeqs> few;
+    few.n = 0;
+    int most = 0, prompts = 0;
+    for (int i = 0; i < cache->n_seqs; ++i) {
+        const int n = cache->q_offsets[i + 1] - cache->q_offsets[i];
+        if (n == 0) continue;
+        if ((long long)n * g > kDecodeRows) {
+            ++prompts;
+            continue;
+        }
+        few.seq[few.n] = (uint16_t)i;
+        few.row[few.n] = cache->q_offsets[i];
+        few.q_len[few.n++] = n;
+        most = std::max(most, n * g);
+    }
+    if (prompts) return launch_attention(p, cache->q_offsets, p.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+    return run_decode(h, p, few, most);
 }
 
 extern "C" int lora_linear_attn_status(lora_attn* h, int reset) {
@@ -359,7 +447,10 @@ extern "C" int lora_linear_attn_destroy(lora_attn* h) {
         DeviceGuard guard(h->device);
         if (guard.ok) {
             cudaDeviceSynchronize();
-            if (h->status) cudaFree(h->status);
+            cudaFree(h->status);
+            cudaFree(h->part_o);
+            cudaFree(h->part_ml);
+            cudaFree(h->prefix);
         }
     }
     delete h;

@@ -65,8 +65,39 @@ struct AttnParams {
     float scale_log2;                   // softmax in base 2: scale * log2(e)
     int* status;
     unsigned long long wait_limit_ns;
+    cudaStream_t stream;
 };
 
 cudaError_t launch_attention(const AttnParams& p, const int32_t* q_offsets, cudaStream_t stream);
+
+// The sequences one launch works on: their index in the call, first row and number of rows.
+template <int N>
+struct SeqList {
+    int32_t n;
+    int32_t row[N];
+    int32_t q_len[N];
+    uint16_t seq[N];
+};
+
+constexpr int kDecodeRows = 64;         // most rows per key/value head of a sequence in the decode kernel
+constexpr int kDecodeTile = 64;         // its cache tile, in tokens
+
+struct DecodeParams {
+    CUtensorMap tm_k, tm_v;             // box: 64 features of one head x granule tokens of one page
+    AttnParams a;
+    int k_order, v_order;               // order of the maps' axes (dev::tma_load_kv)
+    int granule;                        // tokens of one load: divides the page size and the tile
+    int group;                          // query heads per key/value head
+    int slots;                          // ring slots of one tile of K or V
+    float* part_o;                      // [2 x grid][16 MT][dim]: unnormalised sums of split units
+    float2* part_ml;                    // [2 x grid][16 MT]: running maximum and sum
+    uint32_t* prefix;                   // [n + 1]: tiles of one head before each sequence
+    int grid;
+};
+size_t decode_smem(int dim, int mt, int slots, int seqs);
+// The most bytes of dynamic shared memory that lets `per_sm` blocks share an SM.
+constexpr int kSmemTwo = 115200;
+cudaError_t decode_prepare_device();
+cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, int mt, cudaStream_t stream);
 
 }  // namespace lora
