@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblora_linear.so")
 SOURCES = ["kernels.cu", "kernels_w4.cu", "api.cpp", "planner.cpp", "noalloc.cu",
-           "layer_ops.cu", "attn.cu", "attn_decode.cu", "layer_api.cpp"]
+           "layer_ops.cu", "attn_decode.cu", "attn_prompt.cu", "layer_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,581 @@
+// Attention of many new rows per sequence over the paged cache, on tcgen05.
+//
+// A unit is one key/value head and a run of its sequence's new rows: the rows of all query heads
+// that share the head are packed into tiles of 128 (row r of a tile is query head r % g of token
+// r / g), so that each tile of K and V is loaded once for all of them. Per cache tile of 128 tokens
+//     S = Q K^T       tcgen05.mma, both operands in shared memory, 128 x 128 fp32 in tensor memory
+//     P = 2^(S - m)   one thread per row: S to registers, P back to tensor memory in bf16
+//     O += P V        tcgen05.mma, P from tensor memory, V in shared memory as its rows lie there
+// with the running maximum m and sum l of a softmax in base 2 per row. O is corrected only when a
+// row's maximum grows by more than 2^8 (the weights stay within bf16's and fp32's range; m, l and O
+// always go by one reference), so a correction is rare after the first tiles.
+//
+// The matrix pipe is the bound (4 D flops a pair of row and token). Heads of 64 and 128 run two
+// tiles of rows per block in turn, so that one tile's products run while the other's weights are
+// computed; a head of 256 has one tile (its O takes half of tensor memory) and two score buffers.
+// Two or one groups of four softmax warps, an MMA warp and a TMA warp; K and V come through one ring.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn_common.cuh"
+
+namespace lora {
+namespace {
+
+using namespace dev;
+
+constexpr int kTk = kPromptTile;
+
+template <int D>
+struct Shape {
+    static constexpr int kQ = D == 256 ? 1 : 2;           // tiles of rows per block
+    static constexpr int kS = D == 256 ? 2 : 1;           // score buffers per tile
+    static constexpr int kPieces = D == 256 ? 2 : 1;      // ring pieces of one tile of K (or of V)
+    static constexpr int kPiece = D == 64 ? 16384 : 32768;
+    static constexpr int kSlots = D == 64 ? 10 : 5;
+    static constexpr int kQBytes = kTk * D * 2;
+    static constexpr int kVTok = kTk / kPieces;           // tokens of one V piece
+    static constexpr int kKChunks = D / 64 / kPieces;     // 64-feature chunks of one K piece
+    static constexpr int kThreads = kQ * 128 + 64;
+    static constexpr int kO = 256;                        // first tensor-memory column of O (S: 128 each, from 0)
+    static constexpr int kRing = kQ * kQBytes;
+    static constexpr int kBars = kRing + kSlots * kPiece;
+    static constexpr int kSmem = kBars + 512 + 1024;
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32],"
+        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], A the bf16 weights as they lie in tensor memory.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                            uint32_t pred) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(pred)
+        : "memory");
+}
+// Shared-memory descriptor of a V tile as the B operand: features along N are contiguous (N-major),
+// 64 of them per 128-byte swizzled row. `chunk` bytes from one 64-feature chunk to the next (leading
+// offset); groups of 8 tokens are 1,024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr, uint32_t chunk) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(chunk >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// One block's work: a unit (or, with splits, one part of its cache tiles).
+struct Unit {
+    int i, seq, head, tok0, q_len, row0, len;
+    TileRange r;
+    int t0, t1;           // its tiles
+};
+template <int D, int N>
+__device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptList<N>& list, int block) {
+    using S = Shape<D>;
+    Unit u;
+    const int unit = block / p.splits, part = block - unit * p.splits;
+    int lo = 0, hi = list.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (list.unit0[mid] <= unit) lo = mid; else hi = mid - 1;
+    }
+    u.i = lo;
+    u.seq = list.seq[lo];
+    u.q_len = list.q_len[lo];
+    u.row0 = list.row[lo];
+    const int step = S::kQ * p.tile_tokens, per = (u.q_len + step - 1) / step, v = unit - list.unit0[lo];
+    u.head = v / per;
+    u.tok0 = (per - 1 - (v - u.head * per)) * step;      // the longest rows first
+    u.len = cache_len(p.a.c, u.seq);
+    const int first = u.len - u.q_len + u.tok0, last = u.len - u.q_len + min(u.q_len, u.tok0 + step) - 1;
+    u.r = tile_range(first, last, p.a.window, p.a.sinks, kTk);
+    u.t0 = (int)((long long)u.r.n * part / p.splits);
+    u.t1 = (int)((long long)u.r.n * (part + 1) / p.splits);
+    return u;
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+    prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
+    using S = Shape<D>;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + S::kBars);
+    uint64_t* full = bars;                                // [kSlots] pieces of K and V
+    uint64_t* empty = full + S::kSlots;
+    uint64_t* s_full = empty + S::kSlots;                 // [kQ * kS] scores
+    uint64_t* p_full = s_full + 2;                        // [kQ * kS] weights (and O corrected)
+    uint64_t* pv_done = p_full + 2;                       // [kQ] product with V
+    uint64_t* q_full = pv_done + 2;
+    uint64_t* drain = q_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kMmaWarp = S::kQ * 4, kTmaWarp = kMmaWarp + 1;
+
+    if (tid == 0) {
+        for (int s = 0; s < S::kSlots; ++s) {
+            mbar_init(smem_addr(&full[s]), 1);
+            mbar_init(smem_addr(&empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&s_full[s]), 1);
+            mbar_init(smem_addr(&p_full[s]), 128);
+            mbar_init(smem_addr(&pv_done[s]), 1);
+        }
+        mbar_init(smem_addr(q_full), S::kQ * 128);
+        mbar_init(smem_addr(drain), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc<1>(smem_addr(tmem_slot), 512);
+    if (warp == kTmaWarp && lane == 0) {
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const AttnParams& a = p.a;
+    const uint64_t limit = a.wait_limit_ns;
+    const Unit u = find_unit<D>(p, list, blockIdx.x);
+    const int n = u.t1 - u.t0;
+    const uint32_t q_smem = smem_addr(base), ring = q_smem + S::kRing;
+    const uint32_t issuer = lane == 0 ? 1u : 0u;
+
+    if (warp == kTmaWarp) {
+        // ------------------------------------------------------------ producer
+        const int gran = p.granule, per_tile = kTk / gran;
+        const uint32_t box_bytes = (uint32_t)gran * 128;
+        const int32_t* table = a.c.table + u.seq * a.c.table_stride;
+        // lane g < per_tile: the page and token of the tile's granule g; page -1: past the sequence
+        auto place = [&](int t, int& page, int& tok) {
+            page = -1;
+            tok = 0;
+            if (t >= n || lane >= per_tile) return;
+            const int j = tile_token(u.r, u.t0 + t, kTk) + lane * gran;
+            if (j >= u.len) return;
+            const int pg = j / a.c.page_size;
+            page = table[pg];
+            tok = j - pg * a.c.page_size;
+            if (page < 0 || page >= a.c.n_pages) page = a.c.n_pages;    // out of the map's range: zeros
+        };
+        int slot = 0, issued = 0;
+        uint32_t phase = 0;
+        // pieces of a tile of K (128 tokens x its share of the features) or of V (its share of the tokens x all)
+        auto load = [&](bool v, int page, int tok) -> bool {
+#pragma unroll
+            for (int x = 0; x < S::kPieces; ++x) {
+                const int chunks = v ? D / 64 : S::kKChunks;
+                const int grans = v ? S::kVTok / gran : per_tile;
+                const int gi = lane / chunks, ch = lane - gi * chunks;
+                const int from = (v ? x * grans : 0) + gi;
+                const int pg = __shfl_sync(0xffffffffu, page, from & 31), tk = __shfl_sync(0xffffffffu, tok, from & 31);
+                const bool mine = gi < grans && pg >= 0;
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
+                if (!wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) return false;
+                const uint32_t bar = smem_addr(&full[slot]);
+                mbar_arrive_expect_tx(bar, bytes, issuer);
+                __syncwarp();
+                if (mine)
+                    tma_load_kv(ring + (uint32_t)slot * S::kPiece + (uint32_t)ch * ((v ? S::kVTok : kTk) * 128) + (uint32_t)gi * box_bytes,
+                                v ? &p.tm_v : &p.tm_k, bar, v ? p.v_order : p.k_order,
+                                ((v ? 0 : x * S::kKChunks) + ch) * 64, u.head, tk, pg);
+                ++issued;
+                if (++slot == S::kSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            return true;
+        };
+        int page, tok, npage, ntok;
+        place(0, page, tok);
+        place(1, npage, ntok);
+        bool ok = n == 0 || load(false, page, tok);
+        for (int t = 0; t < n && ok; ++t) {
+            int fpage, ftok;
+            place(t + 2, fpage, ftok);
+            if (S::kS == 2) {
+                ok = (t + 1 == n || load(false, npage, ntok)) && load(true, page, tok);
+            } else {
+                ok = load(true, page, tok) && (t + 1 == n || load(false, npage, ntok));
+            }
+            page = npage;
+            tok = ntok;
+            npage = fpage;
+            ntok = ftok;
+        }
+        if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
+            for (int k = max(0, issued - S::kSlots); k < issued; ++k)
+                wait_bounded(smem_addr(&full[k % S::kSlots]), (uint32_t)((k / S::kSlots) & 1), abort_flag, a.status, limit, false);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc_s = instr_desc_bf16(128, kTk);
+        const uint32_t idesc_o = instr_desc_bf16(128, D) | 1u << 16;      // B is N-major
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        auto wait_piece = [&](int s, uint32_t ph) { ok = ok && wait_warp(smem_addr(&full[s]), ph, abort_flag, a.status, limit); };
+        auto next = [&](int& s, uint32_t& ph) {
+            if (++s == S::kSlots) {
+                s = 0;
+                ph ^= 1;
+            }
+        };
+        // scores of tile q into buffer b from the K piece(s) at the ring's position
+        auto scores = [&](int q, int b, int s, int x) {
+            const uint32_t kp = ring + (uint32_t)s * S::kPiece, qp = q_smem + (uint32_t)q * S::kQBytes;
+#pragma unroll
+            for (int c = 0; c < S::kKChunks; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16<1>(tmem + (uint32_t)(q * S::kS + b) * 128,
+                                smem_desc<64>(qp + (uint32_t)(x * S::kKChunks + c) * (128 * 128) + k * 32),
+                                smem_desc<64>(kp + (uint32_t)c * (kTk * 128) + k * 32), idesc_s, (x | c | k) != 0, issuer);
+        };
+        auto values = [&](int q, int b, int s, int x, bool add) {
+            const uint32_t vp = ring + (uint32_t)s * S::kPiece;
+#pragma unroll
+            for (int k = 0; k < S::kVTok / 16; ++k)
+                mma_bf16_ts(tmem + S::kO + (uint32_t)q * D, tmem + (uint32_t)(q * S::kS + b) * 128 + (uint32_t)(x * S::kVTok / 16 + k) * 8,
+                            v_desc(vp + (uint32_t)k * 2048, S::kVTok * 128), idesc_o, add || (x | k) != 0, issuer);
+        };
+        if (n > 0) {
+            ok = wait_warp(smem_addr(q_full), 0, abort_flag, a.status, limit);
+            tc_fence_after();
+            if (S::kS == 1) {
+                wait_piece(slot, phase);
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int q = 0; q < S::kQ; ++q) {
+                        scores(q, 0, slot, 0);
+                        mma_commit_local<1>(smem_addr(&s_full[q]), issuer);
+                    }
+                    mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
+                }
+                next(slot, phase);
+                for (int t = 0; t < n && ok; ++t) {
+                    int ks = slot;
+                    uint32_t kph = phase;
+                    next(ks, kph);
+#pragma unroll
+                    for (int q = 0; q < S::kQ; ++q) {
+                        ok = ok && wait_warp(smem_addr(&p_full[q]), t & 1, abort_flag, a.status, limit);
+                        if (q == 0) wait_piece(slot, phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(q, 0, slot, 0, t > 0);
+                        mma_commit_local<1>(smem_addr(&pv_done[q]), issuer);
+                        if (q == S::kQ - 1) mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
+                        if (t + 1 < n) {
+                            if (q == 0) wait_piece(ks, kph);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(q, 0, ks, 0);
+                            mma_commit_local<1>(smem_addr(&s_full[q]), issuer);
+                            if (q == S::kQ - 1) mma_commit_local<1>(smem_addr(&empty[ks]), issuer);
+                        }
+                    }
+                    slot = ks;
+                    phase = kph;
+                    next(slot, phase);
+                }
+            } else {
+                for (int t = -1; t < n && ok; ++t) {
+                    if (t + 1 < n) {
+                        const int b = (t + 1) & 1;
+#pragma unroll
+                        for (int x = 0; x < S::kPieces; ++x) {
+                            wait_piece(slot, phase);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(0, b, slot, x);
+                            mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
+                            next(slot, phase);
+                        }
+                        if (!ok) break;
+                        mma_commit_local<1>(smem_addr(&s_full[b]), issuer);
+                    }
+                    if (t < 0) continue;
+                    ok = ok && wait_warp(smem_addr(&p_full[t & 1]), (t >> 1) & 1, abort_flag, a.status, limit);
+#pragma unroll
+                    for (int x = 0; x < S::kPieces; ++x) {
+                        wait_piece(slot, phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(0, t & 1, slot, x, t > 0);
+                        mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
+                        next(slot, phase);
+                    }
+                    if (ok) mma_commit_local<1>(smem_addr(&pv_done[0]), issuer);
+                }
+            }
+            // every product has ended before tensor memory is given back
+            mma_commit_local<1>(smem_addr(drain), issuer);
+            if (lane == 0) wait_bounded(smem_addr(drain), 0, abort_flag, a.status, limit, false);
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------ softmax: one thread per row
+        const int q = warp >> 2, row = tid & 127, g = p.group;
+        const int qi = row / g, hq = u.head * g + (row - qi * g), tok = u.tok0 + q * p.tile_tokens + qi;
+        const bool valid = qi < p.tile_tokens && tok < u.q_len;
+        const int pos = valid ? u.len - u.q_len + tok : -1;
+        typedef __nv_bfloat16 bf;
+        // this tile's queries into shared memory, 128-byte swizzled rows in chunks of 64 features
+        for (int v = row; v < 128 * (D / 8); v += 128) {
+            const int rr = v / (D / 8), c = v % (D / 8), ri = rr / g, rt = u.tok0 + q * p.tile_tokens + ri;
+            uint4 val = make_uint4(0, 0, 0, 0);
+            if (ri < p.tile_tokens && rt < u.q_len)
+                val = *reinterpret_cast<const uint4*>(static_cast<const bf*>(a.q) + (u.row0 + rt) * a.q_stride +
+                                                      (u.head * g + (rr - ri * g)) * a.q_head + c * 8);
+            *reinterpret_cast<uint4*>(base + q * S::kQBytes + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val;
+        }
+        fence_proxy_async_shared();
+        mbar_arrive(smem_addr(q_full));
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);      // this warp's 32 lanes
+        const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D;
+        const float scl = a.scale_log2;
+        float m = -INFINITY, l = 0.f;
+        // the rows' range of positions in this tile, for the tiles that need no mask
+        const int tile_first = u.r.first + q * p.tile_tokens;
+        bool ok = true;
+        for (int t = 0; t < n && ok; ++t) {
+            const int b = S::kS == 2 ? (t & 1) : 0;
+            const uint32_t par = S::kS == 2 ? (t >> 1) & 1 : t & 1;
+            const int j0 = tile_token(u.r, u.t0 + t, kTk);
+            ok = wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
+            uint32_t v[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, v + c * 32);
+            tmem_ld_wait();
+            const int last_pos = tile_first + p.tile_tokens - 1;
+            if (j0 + kTk - 1 > tile_first || (a.window && j0 <= last_pos - a.window && j0 + kTk > a.sinks)) {
+                // columns up to hi, and from lo or below sk
+                const int hi = pos - j0, lo = a.window ? max(pos - a.window + 1 - j0, 0) : 0, sk = a.window ? a.sinks - j0 : 0;
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (!(c <= hi && (c >= lo || c < sk))) v[c] = 0xff800000u;      // -inf
+            }
+            float mx = __uint_as_float(v[0]);
+#pragma unroll
+            for (int c = 1; c < 128; ++c) mx = fmaxf(mx, __uint_as_float(v[c]));
+            // a new reference: at first, or when the maximum has outgrown the old one by 2^8
+            const bool grow = m == -INFINITY ? mx > -INFINITY : (mx - m) * scl > 8.f;
+            const bool fix = grow && m != -INFINITY;
+            if (__any_sync(0xffffffffu, fix)) {
+                const float alpha = fix ? ex2((m - mx) * scl) : 1.f;
+                ok = wait_warp(smem_addr(&pv_done[q]), (t - 1) & 1, abort_flag, a.status, limit);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(o_addr + c * 32, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+                    tmem_st32(o_addr + c * 32, x);
+                }
+                l *= alpha;
+            }
+            if (grow) m = mx;
+            const float ms = m == -INFINITY ? 0.f : m * scl;
+            uint32_t w[64];
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+                const float x = ex2(fmaf(__uint_as_float(v[c]), scl, -ms)), y = ex2(fmaf(__uint_as_float(v[c + 1]), scl, -ms));
+                sum0 += x;
+                sum1 += y;
+                w[c >> 1] = pack_bf16x2(x, y);
+            }
+            l += sum0 + sum1;
+            tmem_st32(s_addr, w);
+            tmem_st32(s_addr + 32, w + 32);
+            if (q == 0 && u.len - j0 < kTk) {
+                // places past the last token may hold anything: their weight is 0, so they must be finite
+                const int k0 = S::kS == 2 ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t;   // the V pieces' place in the ring's order
+                for (int x = 0; x < S::kPieces; ++x) {
+                    const int s = (k0 + x) % S::kSlots;
+                    ok = ok && wait_warp(smem_addr(&full[s]), (uint32_t)((k0 + x) / S::kSlots) & 1, abort_flag, a.status, limit);
+                    const int from = max(0, u.len - j0 - x * S::kVTok);
+                    for (int e = from * (D / 8) + row; e < S::kVTok * (D / 8); e += 128) {
+                        const int tk = e / (D / 8), c = e % (D / 8);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + (uint32_t)s * S::kPiece +
+                                                                                    (c >> 3) * (S::kVTok * 128) + tk * 128 + (c & 7) * 16),
+                                     "r"(0)
+                                     : "memory");
+                    }
+                }
+                fence_proxy_async_shared();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
+        }
+        // with two score buffers the product before the last may still run: a parity tells one phase from
+        // the next only
+        if (S::kS == 2 && n > 1 && ok) ok = wait_warp(smem_addr(&pv_done[q]), n & 1, abort_flag, a.status, limit);
+        if (n > 0 && ok) ok = wait_warp(smem_addr(&pv_done[q]), (n - 1) & 1, abort_flag, a.status, limit);
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        bf* out = static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + hq * a.o_head;
+        const long long part = ((long long)blockIdx.x * S::kQ + q) * 128 + row;
+        if (p.splits > 1) p.part_ml[part] = make_float2(m * scl, l);
+        if (ok)
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                if (n > 0) {
+                    tmem_ld32(o_addr + c * 32, x);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = 0;
+                }
+                if (!valid) continue;
+                if (p.splits > 1) {
+                    float4* d = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        d[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
+                                           __uint_as_float(x[4 * e + 3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint4 o4;
+                        uint32_t* o = &o4.x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            o[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * inv, __uint_as_float(x[8 * e + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = o4;
+                    }
+                }
+            }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc<1>(tmem, 512);
+    }
+}
+
+// Joins the parts of a unit's cache tiles: one warp per row.
+template <int D, int N>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
+    using S = Shape<D>;
+    constexpr int E = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x / (S::kQ * 32), row = (blockIdx.x % (S::kQ * 32)) * 4 + warp;
+    const Unit u = find_unit<D>(p, list, unit * p.splits);
+    const int q = row >> 7, r = row & 127, g = p.group, qi = r / g, tok = u.tok0 + q * p.tile_tokens + qi;
+    if (qi >= p.tile_tokens || tok >= u.q_len) return;
+    const long long at = ((long long)unit * p.splits * S::kQ + q) * 128 + r, step = S::kQ * 128;
+    float m = -INFINITY;
+    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_ml[at + s * step].x);
+    const float ms = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+        const float2 x = p.part_ml[at + s * step];
+        const float w = ex2(x.x - ms);
+        l = fmaf(x.y, w, l);
+        const float2* src = reinterpret_cast<const float2*>(p.part_o + (at + s * step) * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+            const float2 v = src[e];
+            o[2 * e] = fmaf(v.x, w, o[2 * e]);
+            o[2 * e + 1] = fmaf(v.y, w, o[2 * e + 1]);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
+                         (u.head * g + (r - qi * g)) * p.a.o_head + lane * E;
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) reinterpret_cast<uint32_t*>(out)[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+}
+
+template <int D, int N>
+cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cudaStream_t stream) {
+    PromptList<N> list;
+    list.n = all.n;
+    for (int i = 0; i < all.n; ++i) {
+        list.row[i] = all.row[i];
+        list.q_len[i] = all.q_len[i];
+        list.seq[i] = all.seq[i];
+        list.unit0[i] = all.unit0[i];
+    }
+    prompt_kernel<D, N><<<(unsigned)(p.units * p.splits), Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(p, list);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return e;
+    prompt_join_kernel<D, N><<<(unsigned)(p.units * Shape<D>::kQ * 32), 128, 0, stream>>>(p, list);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const PromptParams& p, const PromptList<kMaxSeqs>& l, cudaStream_t s) {
+    return l.n <= kSmallSeqs ? launch_n<D, kSmallSeqs>(p, l, s) : launch_n<D, kMaxSeqs>(p, l, s);
+}
+
+template <int D>
+cudaError_t opt_in() {
+    cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, kSmallSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(prompt_kernel<D, kMaxSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+}
+
+}  // namespace
+
+int prompt_tiles(int dim) { return dim == 256 ? 1 : 2; }
+
+cudaError_t prompt_prepare_device() {
+    cudaError_t e = opt_in<64>();
+    if (e == cudaSuccess) e = opt_in<128>();
+    if (e == cudaSuccess) e = opt_in<256>();
+    return e;
+}
+
+cudaError_t launch_prompt(const PromptParams& p, const PromptList<kMaxSeqs>& seqs, cudaStream_t stream) {
+    if (p.a.c.dim == 64) return launch_d<64>(p, seqs, stream);
+    if (p.a.c.dim == 128) return launch_d<128>(p, seqs, stream);
+    return launch_d<256>(p, seqs, stream);
+}
+
+}  // namespace lora

@@ -174,6 +174,7 @@ struct lora_attn {
     float* part_o = nullptr;            // sums of split units, their maxima and sums of weights
     float2* part_ml = nullptr;
     uint32_t* prefix = nullptr;
+    int max_parts = 0;                  // tiles of 128 rows that part_o has room for
 };
 
 namespace {
@@ -187,8 +188,11 @@ int set_up(lora_attn* h) {
         q != cudaDriverEntryPointSuccess || !fn)
         return LORA_ECUDA;
     h->encode = reinterpret_cast<EncodeTiledFn>(fn);
-    if (decode_prepare_device() != cudaSuccess) return LORA_ECUDA;
-    const size_t parts = 2 * (size_t)h->num_sms * kDecodeRows;     // two a block; 16 rows where two blocks share an SM
+    if (decode_prepare_device() != cudaSuccess || prompt_prepare_device() != cudaSuccess) return LORA_ECUDA;
+    // decode: two parts a block of at most 64 rows (16 where two blocks share an SM). prompts: calls that
+    // leave SMs without a unit split the units' tiles, into at most four blocks per SM
+    h->max_parts = 4 * h->num_sms * prompt_tiles(h->dim);
+    const size_t parts = std::max(2 * (size_t)h->num_sms * kDecodeRows, (size_t)h->max_parts * kPromptTile);
     if (cudaMalloc(reinterpret_cast<void**>(&h->status), sizeof(int)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_o), parts * h->dim * sizeof(float)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_ml), parts * sizeof(float2)) != cudaSuccess ||
@@ -217,6 +221,40 @@ int run_decode(lora_attn* h, const AttnParams& a, const SeqList<kMaxSeqs>& list,
         !encode_cache(h->encode, &p.tm_v, &p.v_order, a.c, true, p.granule))
         return LORA_EINVAL;
     return launch_decode(p, list, mt, a.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+// The prompt kernel on the sequences of `list`.
+int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
+    PromptParams p;
+    p.a = a;
+    p.group = h->n_heads / h->n_kv;
+    p.tile_tokens = kPromptTile / p.group;
+    p.granule = 64;
+    while (h->page_size % p.granule) p.granule /= 2;
+    const int tiles = prompt_tiles(h->dim), step = tiles * p.tile_tokens;
+    long long units = 0;
+    for (int i = 0; i < list.n; ++i) {
+        list.unit0[i] = (int32_t)units;
+        units += (long long)((list.q_len[i] + step - 1) / step) * h->n_kv;
+        if (units > 0x7fffffff / 8) return LORA_EUNSUPPORTED;
+    }
+    p.units = (int)units;
+    // parts of a unit's cache tiles: as many as shorten the last wave of blocks, 3% each for the join
+    p.splits = 1;
+    double best = (double)((units + h->num_sms - 1) / h->num_sms);
+    for (int s = 2; s <= 16 && units * s * tiles <= h->max_parts; ++s) {
+        const double cost = (double)((units * s + h->num_sms - 1) / h->num_sms) / s + 0.03 * s;
+        if (cost < best) {
+            best = cost;
+            p.splits = s;
+        }
+    }
+    p.part_o = h->part_o;
+    p.part_ml = h->part_ml;
+    if (!encode_cache(h->encode, &p.tm_k, &p.k_order, a.c, false, p.granule) ||
+        !encode_cache(h->encode, &p.tm_v, &p.v_order, a.c, true, p.granule))
+        return LORA_EINVAL;
+    return launch_prompt(p, list, a.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }
 
 }  // namespace
@@ -401,8 +439,8 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
     p.o_head = out_head_stride;
     p.n_heads = h->n_heads;
     p.rows = rows;
-    p.window = window;
-    p.sinks = window ? sinks : 0;
+    p.window = std::min(window, 2 * LORA_LAYER_MAX_CONTEXT);       // longer than any sequence: the same, and no overflow
+    p.sinks = window ? std::min(sinks, LORA_LAYER_MAX_CONTEXT) : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = h->status;
     p.wait_limit_ns = h->wait_limit_ns;
@@ -410,22 +448,23 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
     // sequences with few rows and long ones go to different kernels
     const int g = h->n_heads / h->n_kv;
     SeqList<kMaxSeqs> few;
-    few.n = 0;
-    int most = 0, prompts = 0;
+    PromptList<kMaxSeqs> many;
+    few.n = many.n = 0;
+    int most = 0;
     for (int i = 0; i < cache->n_seqs; ++i) {
         const int n = cache->q_offsets[i + 1] - cache->q_offsets[i];
         if (n == 0) continue;
-        if ((long long)n * g > kDecodeRows) {
-            ++prompts;
-            continue;
-        }
-        few.seq[few.n] = (uint16_t)i;
-        few.row[few.n] = cache->q_offsets[i];
-        few.q_len[few.n++] = n;
-        most = std::max(most, n * g);
+        SeqList<kMaxSeqs>& l = (long long)n * g > kDecodeRows ? many : few;
+        l.seq[l.n] = (uint16_t)i;
+        l.row[l.n] = cache->q_offsets[i];
+        l.q_len[l.n++] = n;
+        if (&l == &few) most = std::max(most, n * g);
     }
-    if (prompts) return launch_attention(p, cache->q_offsets, p.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
-    return run_decode(h, p, few, most);
+    if (many.n) {
+        const int rc = run_prompts(h, p, many);
+        if (rc != LORA_OK) return rc;
+    }
+    return few.n ? run_decode(h, p, few, most) : LORA_OK;
 }
 
 extern "C" int lora_linear_attn_status(lora_attn* h, int reset) {

@@ -68,8 +68,6 @@ struct AttnParams {
     cudaStream_t stream;
 };
 
-cudaError_t launch_attention(const AttnParams& p, const int32_t* q_offsets, cudaStream_t stream);
-
 // The sequences one launch works on: their index in the call, first row and number of rows.
 template <int N>
 struct SeqList {
@@ -99,5 +97,27 @@ size_t decode_smem(int dim, int mt, int slots, int seqs);
 constexpr int kSmemTwo = 115200;
 cudaError_t decode_prepare_device();
 cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, int mt, cudaStream_t stream);
+
+constexpr int kPromptTile = 128;        // the prompt kernel's tile of rows and of cache tokens
+
+// SeqList with the first unit of each sequence: a unit is one key/value head and the rows of
+// prompt_tiles(dim) tiles.
+template <int N>
+struct PromptList : SeqList<N> {
+    int32_t unit0[N];
+};
+
+struct PromptParams {
+    CUtensorMap tm_k, tm_v;             // as DecodeParams
+    AttnParams a;
+    int k_order, v_order, granule, group;
+    int tile_tokens;                    // tokens of one tile of rows: 128 / group
+    int units, splits;                  // blocks: every unit's cache tiles in `splits` parts
+    float* part_o;                      // [units x splits x tiles][128][dim]
+    float2* part_ml;
+};
+int prompt_tiles(int dim);              // tiles of rows of a unit
+cudaError_t prompt_prepare_device();
+cudaError_t launch_prompt(const PromptParams& p, const PromptList<kMaxSeqs>& seqs, cudaStream_t stream);
 
 }  // namespace lora
