@@ -66,6 +66,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
         "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
         : "memory");
 }
+// Waits for the thread's loads from tensor memory; v, one of them, is used after the wait alone.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16],"
+        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem], A the bf16 weights as they lie in tensor memory.
@@ -123,6 +141,41 @@ __device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptLis
     return u;
 }
 
+// Two fp32 values in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    return (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
+// Scores of columns C0 .. C0 + N - 1 that the row does not see become -inf.
+template <int C0, int N>
+__device__ __forceinline__ void mask(uint32_t* v, int hi, int lo, int sk) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+        if (!(C0 + c <= hi && (C0 + c >= lo || C0 + c < sk))) v[c] = 0xff800000u;
+}
+// 32 scores to weights 2^(s scl - ms), rounded to bf16 for the product; sum adds them unrounded.
+__device__ __forceinline__ void weights(const uint32_t* v, uint32_t* w, uint64_t scl2, uint64_t ms2, uint64_t* sum) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const uint64_t e = fma2((uint64_t)v[2 * c + 1] << 32 | v[2 * c], scl2, ms2);
+        const float x = ex2(lo2(e)), y = ex2(hi2(e));
+        sum[c & 3] = add2(sum[c & 3], pack2(x, y));
+        w[c] = pack_bf16x2(x, y);
+    }
+}
+
 template <int D, int N>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
@@ -172,7 +225,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const int n = u.t1 - u.t0;
     const uint32_t q_smem = smem_addr(base), ring = q_smem + S::kRing;
     const uint32_t issuer = lane == 0 ? 1u : 0u;
-
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ producer
         const int gran = p.granule, per_tile = kTk / gran;
@@ -347,7 +399,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (lane == 0) wait_bounded(smem_addr(drain), 0, abort_flag, a.status, limit, false);
             __syncwarp();
         }
-    } else {
+    } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ softmax: one thread per row
         const int q = warp >> 2, row = tid & 127, g = p.group;
         const int qi = row / g, hq = u.head * g + (row - qi * g), tok = u.tok0 + q * p.tile_tokens + qi;
@@ -380,54 +432,76 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
-            uint32_t v[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, v + c * 32);
-            tmem_ld_wait();
             const int last_pos = tile_first + p.tile_tokens - 1;
-            if (j0 + kTk - 1 > tile_first || (a.window && j0 <= last_pos - a.window && j0 + kTk > a.sinks)) {
-                // columns up to hi, and from lo or below sk
-                const int hi = pos - j0, lo = a.window ? max(pos - a.window + 1 - j0, 0) : 0, sk = a.window ? a.sinks - j0 : 0;
+            const bool masked = j0 + kTk - 1 > tile_first || (a.window && j0 <= last_pos - a.window && j0 + kTk > a.sinks);
+            // columns up to hi, and from lo or below sk
+            const int hi = pos - j0, lo = a.window ? max(pos - a.window + 1 - j0, 0) : 0, sk = a.window ? a.sinks - j0 : 0;
+            uint32_t v[64];
+            float mx[8];                 // eight chains
+            {
+                uint32_t y[64];
+                tmem_ld32(s_addr, v);
+                tmem_ld32(s_addr + 32, v + 32);
+                tmem_ld32(s_addr + 64, y);
+                tmem_ld32(s_addr + 96, y + 32);
+                tmem_ld_wait32(v);
+                tmem_ld_wait32(v + 32);
+                tmem_ld_wait32(y);
+                tmem_ld_wait32(y + 32);
+                if (masked) {
+                    mask<0, 64>(v, hi, lo, sk);
+                    mask<64, 64>(y, hi, lo, sk);
+                }
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (!(c <= hi && (c >= lo || c < sk))) v[c] = 0xff800000u;      // -inf
+                for (int c = 0; c < 8; ++c) mx[c] = fmaxf(__uint_as_float(v[c]), __uint_as_float(y[c]));
+#pragma unroll
+                for (int c = 8; c < 64; ++c) mx[c & 7] = fmaxf(mx[c & 7], fmaxf(__uint_as_float(v[c]), __uint_as_float(y[c])));
             }
-            float mx = __uint_as_float(v[0]);
 #pragma unroll
-            for (int c = 1; c < 128; ++c) mx = fmaxf(mx, __uint_as_float(v[c]));
+            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], mx[c + 4]);
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // a new reference: at first, or when the maximum has outgrown the old one by 2^8
-            const bool grow = m == -INFINITY ? mx > -INFINITY : (mx - m) * scl > 8.f;
+            const bool grow = m == -INFINITY ? mx[0] > -INFINITY : (mx[0] - m) * scl > 8.f;
             const bool fix = grow && m != -INFINITY;
             if (__any_sync(0xffffffffu, fix)) {
-                const float alpha = fix ? ex2((m - mx) * scl) : 1.f;
+                const float alpha = fix ? ex2((m - mx[0]) * scl) : 1.f;
                 ok = wait_warp(smem_addr(&pv_done[q]), (t - 1) & 1, abort_flag, a.status, limit);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t x[32];
                     tmem_ld32(o_addr + c * 32, x);
-                    tmem_ld_wait();
+                    tmem_ld_wait32(x);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
                     tmem_st32(o_addr + c * 32, x);
                 }
                 l *= alpha;
             }
-            if (grow) m = mx;
+            if (grow) m = mx[0];
+            // weights, 32 columns at a time; the second half of the scores is read again, which keeps the row
+            // within the registers. Weights overwrite scores that have been read: 32 columns of them fill 16.
             const float ms = m == -INFINITY ? 0.f : m * scl;
-            uint32_t w[64];
-            float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-                const float x = ex2(fmaf(__uint_as_float(v[c]), scl, -ms)), y = ex2(fmaf(__uint_as_float(v[c + 1]), scl, -ms));
-                sum0 += x;
-                sum1 += y;
-                w[c >> 1] = pack_bf16x2(x, y);
-            }
-            l += sum0 + sum1;
-            tmem_st32(s_addr, w);
-            tmem_st32(s_addr + 32, w + 32);
+            const uint64_t scl2 = pack2(scl, scl), ms2 = pack2(-ms, -ms);
+            uint64_t sum[4] = {0, 0, 0, 0};
+            uint32_t y[32], w[16];
+            tmem_ld32(s_addr + 64, y);
+            weights(v, w, scl2, ms2, sum);
+            tmem_st16(s_addr, w);
+            weights(v + 32, w, scl2, ms2, sum);
+            tmem_st16(s_addr + 16, w);
+            tmem_ld_wait32(y);
+            tmem_ld32(s_addr + 96, v);
+            if (masked) mask<64, 32>(y, hi, lo, sk);
+            weights(y, w, scl2, ms2, sum);
+            tmem_st16(s_addr + 32, w);
+            tmem_ld_wait32(v);
+            if (masked) mask<96, 32>(v, hi, lo, sk);
+            weights(v, w, scl2, ms2, sum);
+            tmem_st16(s_addr + 48, w);
+            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += lo2(sum[0]) + hi2(sum[0]);
             if (q == 0 && u.len - j0 < kTk) {
                 // places past the last token may hold anything: their weight is 0, so they must be finite
                 const int k0 = S::kS == 2 ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t;   // the V pieces' place in the ring's order
@@ -464,7 +538,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 uint32_t x[32];
                 if (n > 0) {
                     tmem_ld32(o_addr + c * 32, x);
-                    tmem_ld_wait();
+                    tmem_ld_wait32(x);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0;
