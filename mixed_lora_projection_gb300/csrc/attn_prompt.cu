@@ -37,11 +37,13 @@ struct Shape {
     static constexpr int kQBytes = kTk * D * 2;
     static constexpr int kVTok = kTk / kPieces;           // tokens of one V piece
     static constexpr int kKChunks = D / 64 / kPieces;     // 64-feature chunks of one K piece
-    static constexpr int kThreads = kQ * 128 + 64;
+    static constexpr int kSoftmax = kQ * 256;             // softmax threads: two per row of a tile
+    static constexpr int kThreads = kSoftmax + 64;
     static constexpr int kO = 256;                        // first tensor-memory column of O (S: 128 each, from 0)
     static constexpr int kRing = kQ * kQBytes;
     static constexpr int kBars = kRing + kSlots * kPiece;
-    static constexpr int kSmem = kBars + 512 + 1024;
+    static constexpr int kShare = kBars + 512;            // [kQ][128] floats between the two threads of a row
+    static constexpr int kSmem = kShare + kQ * 512 + 1024;
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
@@ -73,6 +75,13 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t* v) {
                    "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
                    "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
                    "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                  :
                  : "memory");
 }
@@ -158,12 +167,37 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
-// Scores of columns C0 .. C0 + N - 1 that the row does not see become -inf.
-template <int C0, int N>
+// wait_bounded without a call: where it stands a row's scores are in registers, and a call would spill them.
+__device__ __forceinline__ void wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return;
+        if (global_timer_ns() - t0 > limit_ns) {
+            atomicOr(status, 1);
+            *abort_flag = 1;
+            return;
+        }
+    }
+}
+// Scores of columns that the row does not see become -inf: it sees columns up to hi that are lo or more, or below sk.
+template <int N>
 __device__ __forceinline__ void mask(uint32_t* v, int hi, int lo, int sk) {
 #pragma unroll
     for (int c = 0; c < N; ++c)
-        if (!(C0 + c <= hi && (C0 + c >= lo || C0 + c < sk))) v[c] = 0xff800000u;
+        if (!(c <= hi && (c >= lo || c < sk))) v[c] = 0xff800000u;
+}
+// Barrier of the two warps that share 32 rows; true for both if any thread of either wishes it.
+__device__ __forceinline__ bool pair_any(int id, bool wish) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred p, %2, 64, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((int)wish), "r"(id)
+        : "memory");
+    return r != 0;
 }
 // 32 scores to weights 2^(s scl - ms), rounded to bf16 for the product; sum adds them unrounded.
 __device__ __forceinline__ void weights(const uint32_t* v, uint32_t* w, uint64_t scl2, uint64_t ms2, uint64_t* sum) {
@@ -193,7 +227,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kMmaWarp = S::kQ * 4, kTmaWarp = kMmaWarp + 1;
+    constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + 1;
 
     if (tid == 0) {
         for (int s = 0; s < S::kSlots; ++s) {
@@ -202,10 +236,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&s_full[s]), 1);
-            mbar_init(smem_addr(&p_full[s]), 128);
+            mbar_init(smem_addr(&p_full[s]), 256);
             mbar_init(smem_addr(&pv_done[s]), 1);
         }
-        mbar_init(smem_addr(q_full), S::kQ * 128);
+        mbar_init(smem_addr(q_full), S::kSoftmax);
         mbar_init(smem_addr(drain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -400,14 +434,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             __syncwarp();
         }
     } else if (warp < kMmaWarp) {
-        // ------------------------------------------------------------ softmax: one thread per row
-        const int q = warp >> 2, row = tid & 127, g = p.group;
+        // ------------------------------------------------------------ softmax: two threads per row, 64 columns each
+        const int q = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, g = p.group;
         const int qi = row / g, hq = u.head * g + (row - qi * g), tok = u.tok0 + q * p.tile_tokens + qi;
         const bool valid = qi < p.tile_tokens && tok < u.q_len;
         const int pos = valid ? u.len - u.q_len + tok : -1;
+        const int pair = 1 + q * 4 + (warp & 3);                         // named barrier of the two warps of these rows
+        float* share = reinterpret_cast<float*>(base + S::kShare) + q * 128 + row;
         typedef __nv_bfloat16 bf;
         // this tile's queries into shared memory, 128-byte swizzled rows in chunks of 64 features
-        for (int v = row; v < 128 * (D / 8); v += 128) {
+        for (int v = half * 128 + row; v < 128 * (D / 8); v += 256) {
             const int rr = v / (D / 8), c = v % (D / 8), ri = rr / g, rt = u.tok0 + q * p.tile_tokens + ri;
             uint4 val = make_uint4(0, 0, 0, 0);
             if (ri < p.tile_tokens && rt < u.q_len)
@@ -418,88 +454,75 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         fence_proxy_async_shared();
         mbar_arrive(smem_addr(q_full));
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);      // this warp's 32 lanes
-        const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D;
+        const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * (D / 2);
         const float scl = a.scale_log2;
         float m = -INFINITY, l = 0.f;
-        // the rows' range of positions in this tile, for the tiles that need no mask
-        const int tile_first = u.r.first + q * p.tile_tokens;
-        bool ok = true;
-        for (int t = 0; t < n && ok; ++t) {
+        const int tile_first = u.r.first + q * p.tile_tokens, last_pos = tile_first + p.tile_tokens - 1;
+        // After a wait that ran out the warps run on without data, so that their barriers stay matched; the
+        // status word says that the output is incomplete.
+        for (int t = 0; t < n; ++t) {
             const int b = S::kS == 2 ? (t & 1) : 0;
             const uint32_t par = S::kS == 2 ? (t >> 1) & 1 : t & 1;
             const int j0 = tile_token(u.r, u.t0 + t, kTk);
-            ok = wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
-            if (!ok) break;
+            wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
             tc_fence_after();
             const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
-            const int last_pos = tile_first + p.tile_tokens - 1;
-            const bool masked = j0 + kTk - 1 > tile_first || (a.window && j0 <= last_pos - a.window && j0 + kTk > a.sinks);
-            // columns up to hi, and from lo or below sk
-            const int hi = pos - j0, lo = a.window ? max(pos - a.window + 1 - j0, 0) : 0, sk = a.window ? a.sinks - j0 : 0;
             uint32_t v[64];
-            float mx[8];                 // eight chains
-            {
-                uint32_t y[64];
-                tmem_ld32(s_addr, v);
-                tmem_ld32(s_addr + 32, v + 32);
-                tmem_ld32(s_addr + 64, y);
-                tmem_ld32(s_addr + 96, y + 32);
-                tmem_ld_wait32(v);
-                tmem_ld_wait32(v + 32);
-                tmem_ld_wait32(y);
-                tmem_ld_wait32(y + 32);
-                if (masked) {
-                    mask<0, 64>(v, hi, lo, sk);
-                    mask<64, 64>(y, hi, lo, sk);
-                }
-#pragma unroll
-                for (int c = 0; c < 8; ++c) mx[c] = fmaxf(__uint_as_float(v[c]), __uint_as_float(y[c]));
-#pragma unroll
-                for (int c = 8; c < 64; ++c) mx[c & 7] = fmaxf(mx[c & 7], fmaxf(__uint_as_float(v[c]), __uint_as_float(y[c])));
+            tmem_ld32(s_addr + half * 64, v);
+            tmem_ld32(s_addr + half * 64 + 32, v + 32);
+            tmem_ld_wait32(v);
+            tmem_ld_wait32(v + 32);
+            if (j0 + kTk - 1 > tile_first || (a.window && j0 <= last_pos - a.window && j0 + kTk > a.sinks)) {
+                // columns up to hi, and from lo or below sk
+                const int c0 = j0 + half * 64;
+                mask<64>(v, pos - c0, a.window ? pos - a.window + 1 - c0 : 0, a.window ? a.sinks - c0 : 0);
             }
+            float mx[8];                 // eight chains
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(v[c]);
+#pragma unroll
+            for (int c = 8; c < 64; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(v[c]));
 #pragma unroll
             for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], mx[c + 4]);
-            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // a new reference: at first, or when the maximum has outgrown the old one by 2^8
-            const bool grow = m == -INFINITY ? mx[0] > -INFINITY : (mx[0] - m) * scl > 8.f;
-            const bool fix = grow && m != -INFINITY;
-            if (__any_sync(0xffffffffu, fix)) {
-                const float alpha = fix ? ex2((m - mx[0]) * scl) : 1.f;
-                ok = wait_warp(smem_addr(&pv_done[q]), (t - 1) & 1, abort_flag, a.status, limit);
-                if (!ok) break;
-                tc_fence_after();
+            float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // A new reference: at first, or when the maximum has outgrown the old one by 2^8. The barrier also
+            // tells each thread that the other has read its scores, which the weights are about to overwrite.
+            const bool wish = m == -INFINITY ? top > -INFINITY : (top - m) * scl > 8.f;
+            if (pair_any(pair, wish)) {
+                if (half) *share = top;
+                pair_any(pair, false);
+                if (!half) *share = top = fmaxf(top, *share);
+                pair_any(pair, false);
+                if (half) top = *share;
+                const bool grow = m == -INFINITY ? top > -INFINITY : (top - m) * scl > 8.f;
+                const bool fix = grow && m != -INFINITY;
+                if (__any_sync(0xffffffffu, fix)) {
+                    const float alpha = fix ? ex2((m - top) * scl) : 1.f;
+                    wait_here(smem_addr(&pv_done[q]), (t - 1) & 1, abort_flag, a.status, limit);
+                    __syncwarp();
+                    tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t x[32];
-                    tmem_ld32(o_addr + c * 32, x);
-                    tmem_ld_wait32(x);
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t x[16];
+                        tmem_ld16(o_addr + c * 16, x);
+                        tmem_ld_wait16(x);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-                    tmem_st32(o_addr + c * 32, x);
+                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+                        tmem_st16(o_addr + c * 16, x);
+                    }
+                    l *= alpha;
                 }
-                l *= alpha;
+                if (grow) m = top;
             }
-            if (grow) m = mx[0];
-            // weights, 32 columns at a time; the second half of the scores is read again, which keeps the row
-            // within the registers. Weights overwrite scores that have been read: 32 columns of them fill 16.
             const float ms = m == -INFINITY ? 0.f : m * scl;
             const uint64_t scl2 = pack2(scl, scl), ms2 = pack2(-ms, -ms);
             uint64_t sum[4] = {0, 0, 0, 0};
-            uint32_t y[32], w[16];
-            tmem_ld32(s_addr + 64, y);
-            weights(v, w, scl2, ms2, sum);
-            tmem_st16(s_addr, w);
-            weights(v + 32, w, scl2, ms2, sum);
-            tmem_st16(s_addr + 16, w);
-            tmem_ld_wait32(y);
-            tmem_ld32(s_addr + 96, v);
-            if (masked) mask<64, 32>(y, hi, lo, sk);
-            weights(y, w, scl2, ms2, sum);
-            tmem_st16(s_addr + 32, w);
-            tmem_ld_wait32(v);
-            if (masked) mask<96, 32>(v, hi, lo, sk);
-            weights(v, w, scl2, ms2, sum);
-            tmem_st16(s_addr + 48, w);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t w[16];
+                weights(v + x * 32, w, scl2, ms2, sum);
+                tmem_st16(s_addr + half * 32 + x * 16, w);
+            }
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             l += lo2(sum[0]) + hi2(sum[0]);
             if (q == 0 && u.len - j0 < kTk) {
@@ -507,9 +530,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 const int k0 = S::kS == 2 ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t;   // the V pieces' place in the ring's order
                 for (int x = 0; x < S::kPieces; ++x) {
                     const int s = (k0 + x) % S::kSlots;
-                    ok = ok && wait_warp(smem_addr(&full[s]), (uint32_t)((k0 + x) / S::kSlots) & 1, abort_flag, a.status, limit);
+                    wait_warp(smem_addr(&full[s]), (uint32_t)((k0 + x) / S::kSlots) & 1, abort_flag, a.status, limit);
                     const int from = max(0, u.len - j0 - x * S::kVTok);
-                    for (int e = from * (D / 8) + row; e < S::kVTok * (D / 8); e += 128) {
+                    for (int e = from * (D / 8) + half * 128 + row; e < S::kVTok * (D / 8); e += 256) {
                         const int tk = e / (D / 8), c = e % (D / 8);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + (uint32_t)s * S::kPiece +
                                                                                     (c >> 3) * (S::kVTok * 128) + tk * 128 + (c & 7) * 16),
@@ -525,43 +548,48 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         }
         // with two score buffers the product before the last may still run: a parity tells one phase from
         // the next only
-        if (S::kS == 2 && n > 1 && ok) ok = wait_warp(smem_addr(&pv_done[q]), n & 1, abort_flag, a.status, limit);
-        if (n > 0 && ok) ok = wait_warp(smem_addr(&pv_done[q]), (n - 1) & 1, abort_flag, a.status, limit);
+        if (S::kS == 2 && n > 1) wait_warp(smem_addr(&pv_done[q]), n & 1, abort_flag, a.status, limit);
+        if (n > 0) wait_warp(smem_addr(&pv_done[q]), (n - 1) & 1, abort_flag, a.status, limit);
         tc_fence_after();
+        // the row's sum: its two threads' parts
+        if (half) *share = l;
+        pair_any(pair, false);
+        if (!half) *share = l = l + *share;
+        pair_any(pair, false);
+        if (half) l = *share;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        bf* out = static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + hq * a.o_head;
+        bf* out = static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + hq * a.o_head + half * (D / 2);
         const long long part = ((long long)blockIdx.x * S::kQ + q) * 128 + row;
-        if (p.splits > 1) p.part_ml[part] = make_float2(m * scl, l);
-        if (ok)
+        if (p.splits > 1 && half == 0) p.part_ml[part] = make_float2(m * scl, l);
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                if (n > 0) {
-                    tmem_ld32(o_addr + c * 32, x);
-                    tmem_ld_wait32(x);
-                } else {
+        for (int c = 0; c < D / 64; ++c) {
+            uint32_t x[32];
+            if (n > 0) {
+                tmem_ld32(o_addr + c * 32, x);
+                tmem_ld_wait32(x);
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = 0;
-                }
-                if (!valid) continue;
-                if (p.splits > 1) {
-                    float4* d = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+                for (int e = 0; e < 32; ++e) x[e] = 0;
+            }
+            if (!valid) continue;
+            if (p.splits > 1) {
+                float4* d = reinterpret_cast<float4*>(p.part_o + part * D + half * (D / 2) + c * 32);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        d[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
-                                           __uint_as_float(x[4 * e + 3]));
-                } else {
+                for (int e = 0; e < 8; ++e)
+                    d[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
+                                       __uint_as_float(x[4 * e + 3]));
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint4 o4;
-                        uint32_t* o = &o4.x;
+                for (int e = 0; e < 4; ++e) {
+                    uint4 o4;
+                    uint32_t* o = &o4.x;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * inv, __uint_as_float(x[8 * e + 2 * k + 1]) * inv);
-                        *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = o4;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        o[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * inv, __uint_as_float(x[8 * e + 2 * k + 1]) * inv);
+                    *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = o4;
                 }
             }
+        }
         tc_fence_before();
     }
     __syncthreads();
