@@ -38,8 +38,12 @@ struct Shape {
     static constexpr int kVTok = kTk / kPieces;           // tokens of one V piece
     static constexpr int kKChunks = D / 64 / kPieces;     // 64-feature chunks of one K piece
     static constexpr int kSoftmax = kQ * 256;             // softmax threads: two per row of a tile
-    static constexpr int kThreads = kSoftmax + 64;
+    static constexpr bool kApart = D == 64;               // weights beside the scores, not over them
+    static constexpr int kIssuers = D == 64 ? 2 : 1;      // warps that issue products
+    static constexpr int kThreads = kSoftmax + kIssuers * 32 + 32;
     static constexpr int kO = 256;                        // first tensor-memory column of O (S: 128 each, from 0)
+    static constexpr int kP = kApart ? 384 : 0;           // of the weights: 64 columns each, or in their scores' place
+    static constexpr int kPStep = kApart ? 64 : 128;
     static constexpr int kRing = kQ * kQBytes;
     static constexpr int kBars = kRing + kSlots * kPiece;
     static constexpr int kShare = kBars + 512;            // [kQ][128] floats between the two threads of a row
@@ -56,17 +60,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32],"
-        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
-        : "memory");
 }
 // Waits for the thread's loads from tensor memory; v, one of them, is used after the wait alone.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t* v) {
@@ -95,28 +88,34 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem], A the bf16 weights as they lie in tensor memory.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
-                                            uint32_t pred) {
+// Shared-memory operands are given by the low word of their descriptor (the address, and the leading
+// offset); the high word is a constant: stride offset 1,024 bytes (8 rows of a 128-byte swizzle atom),
+// version 1, 128-byte swizzle. The issuing warp shares its scheduler with softmax warps, so a
+// product's operands cost one addition each.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading = 16) { return addr >> 4 | (leading >> 4) << 16; }
+
+// D[tmem] (+)= A[smem] * B[smem]^T, bf16 operands with K contiguous.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t pred) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(pred)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(pred), "n"(kDescHi)
         : "memory");
 }
-// Shared-memory descriptor of a V tile as the B operand: features along N are contiguous (N-major),
-// 64 of them per 128-byte swizzled row. `chunk` bytes from one 64-feature chunk to the next (leading
-// offset); groups of 8 tokens are 1,024 bytes apart (stride offset).
-__device__ __forceinline__ uint64_t v_desc(uint32_t addr, uint32_t chunk) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(chunk >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// D[tmem] (+)= A[tmem] * B[smem], A the bf16 weights as they lie in tensor memory. B is a tile of V as its
+// rows lie in shared memory: features along N are contiguous (N-major), 64 of them per swizzled row; the
+// descriptor's leading offset is the distance of its 64-feature chunks.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t pred) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(pred), "n"(kDescHi)
+        : "memory");
 }
 
 // One block's work: a unit (or, with splits, one part of its cache tiles).
@@ -167,26 +166,39 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
-// wait_bounded without a call: where it stands a row's scores are in registers, and a call would spill them.
-__device__ __forceinline__ void wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return;
+// Waits for several barriers at once: each lane brings one (and its parity). One shared-memory access
+// of the warp then stands for all of them. Bounded like wait_bounded.
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, uint64_t limit_ns) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = global_timer_ns();
+    bool mine = false;
+    while (true) {
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return;
-        if (global_timer_ns() - t0 > limit_ns) {
-            atomicOr(status, 1);
-            *abort_flag = 1;
-            return;
+        for (int i = 0; i < 32; ++i) {
+            mine = mine || mbar_try_wait(bar, parity);
+            if (__all_sync(0xffffffffu, mine)) return true;
+        }
+        const bool late = global_timer_ns() - t0 > limit_ns;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if (late) {
+                atomicOr(status, 1);
+                *abort_flag = 1;
+            }
+            return false;
         }
     }
 }
-// Scores of columns that the row does not see become -inf: it sees columns up to hi that are lo or more, or below sk.
-template <int N>
+// The low n bits (n may be outside 0 .. 64).
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+// Scores of 64 columns that the row does not see become -inf: it sees columns up to hi that are lo or more, or below sk.
 __device__ __forceinline__ void mask(uint32_t* v, int hi, int lo, int sk) {
+    const uint64_t seen = low_bits(hi + 1) & (~low_bits(lo) | low_bits(sk));
+    const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
 #pragma unroll
-    for (int c = 0; c < N; ++c)
-        if (!(c <= hi && (c >= lo || c < sk))) v[c] = 0xff800000u;
+    for (int c = 0; c < 32; ++c) {
+        if (!(s0 & 1u << c)) v[c] = 0xff800000u;
+        if (!(s1 & 1u << c)) v[32 + c] = 0xff800000u;
+    }
 }
 // Barrier of the two warps that share 32 rows; true for both if any thread of either wishes it.
 __device__ __forceinline__ bool pair_any(int id, bool wish) {
@@ -199,15 +211,38 @@ __device__ __forceinline__ bool pair_any(int id, bool wish) {
         : "memory");
     return r != 0;
 }
-// 32 scores to weights 2^(s scl - ms), rounded to bf16 for the product; sum adds them unrounded.
-__device__ __forceinline__ void weights(const uint32_t* v, uint32_t* w, uint64_t scl2, uint64_t ms2, uint64_t* sum) {
+// The largest of 64 scores.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float row_max(const uint32_t* v) {
+    float x[8];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
+    for (int c = 0; c < 8; ++c) x[c] = __uint_as_float(v[c]);
+#pragma unroll
+    for (int c = 8; c < 56; c += 16)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = max3(x[e], __uint_as_float(v[c + e]), __uint_as_float(v[c + 8 + e]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = max3(x[e], x[e + 4], max3(__uint_as_float(v[56 + e]), __uint_as_float(v[60 + e]), -INFINITY));
+    return fmaxf(max3(x[0], x[1], x[2]), x[3]);
+}
+// 64 scores to weights 2^(s scl - ms): v[0 .. 31] get them in pairs, rounded to bf16 for the product with V;
+// returns their sum before that rounding.
+__device__ __forceinline__ float weights(uint32_t* v, float scl, float ms) {
+    const uint64_t scl2 = pack2(scl, scl), ms2 = pack2(-ms, -ms);
+    uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
         const uint64_t e = fma2((uint64_t)v[2 * c + 1] << 32 | v[2 * c], scl2, ms2);
         const float x = ex2(lo2(e)), y = ex2(hi2(e));
         sum[c & 3] = add2(sum[c & 3], pack2(x, y));
-        w[c] = pack_bf16x2(x, y);
+        v[c] = pack_bf16x2(x, y);
     }
+    sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+    return lo2(sum[0]) + hi2(sum[0]);
 }
 
 template <int D, int N>
@@ -221,26 +256,31 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     uint64_t* empty = full + S::kSlots;
     uint64_t* s_full = empty + S::kSlots;                 // [kQ * kS] scores
     uint64_t* p_full = s_full + 2;                        // [kQ * kS] weights (and O corrected)
-    uint64_t* pv_done = p_full + 2;                       // [kQ] product with V
-    uint64_t* q_full = pv_done + 2;
-    uint64_t* drain = q_full + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* pv_done = p_full + 2;                       // [kQ * kS] product with V
+    uint64_t* s_read = pv_done + 2;                       // [kQ] scores are in registers (kApart)
+    uint64_t* q_full = s_read + 2;
+    uint64_t* drain = q_full + 1;                         // [2] an issuer's last product
+    uint64_t* turn = drain + 2;                           // [2] a tile's scores are issued (the first: and used)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + 1;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);              // known to be the same in every lane
+    constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + S::kIssuers;
 
     if (tid == 0) {
         for (int s = 0; s < S::kSlots; ++s) {
             mbar_init(smem_addr(&full[s]), 1);
-            mbar_init(smem_addr(&empty[s]), 1);
+            mbar_init(smem_addr(&empty[s]), S::kIssuers);   // every issuer that reads the piece
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&s_full[s]), 1);
-            mbar_init(smem_addr(&p_full[s]), 256);
+            mbar_init(smem_addr(&p_full[s]), 8);          // one arrival a warp
             mbar_init(smem_addr(&pv_done[s]), 1);
+            mbar_init(smem_addr(&s_read[s]), 8);
+            mbar_init(smem_addr(&drain[s]), 1);
+            mbar_init(smem_addr(&turn[s]), 1);
         }
-        mbar_init(smem_addr(q_full), S::kSoftmax);
-        mbar_init(smem_addr(drain), 1);
+        mbar_init(smem_addr(q_full), S::kSoftmax / 32);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -312,7 +352,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         for (int t = 0; t < n && ok; ++t) {
             int fpage, ftok;
             place(t + 2, fpage, ftok);
-            if (S::kS == 2) {
+            if (S::kS == 2 || S::kApart) {
                 ok = (t + 1 == n || load(false, npage, ntok)) && load(true, page, tok);
             } else {
                 ok = load(true, page, tok) && (t + 1 == n || load(false, npage, ntok));
@@ -325,112 +365,146 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
             for (int k = max(0, issued - S::kSlots); k < issued; ++k)
                 wait_bounded(smem_addr(&full[k % S::kSlots]), (uint32_t)((k / S::kSlots) & 1), abort_flag, a.status, limit, false);
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issuer
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuers
+        // A product of N = 128 or less costs the issuing warp ~90-105 cycles, more than the tensor cores need
+        // for it (64 at N = 128), and a wait or an arrival holds the warp until the products it has issued are
+        // done. So all that a tile needs is waited for at once, and its products then go back to back: those
+        // with V, then the next scores. Two issuers halve that cost but fall into step, so that products and
+        // weights no longer overlap (4,096 rows at the end of 16,384 tokens, heads of 128: 1,350 us with two,
+        // DUMMY with one); heads of 64, where the weights bound the tile, take two.
+        const int me = warp - kMmaWarp;
         const uint32_t idesc_s = instr_desc_bf16(128, kTk);
         const uint32_t idesc_o = instr_desc_bf16(128, D) | 1u << 16;      // B is N-major
-        int slot = 0;
-        uint32_t phase = 0;
         bool ok = true;
-        auto wait_piece = [&](int s, uint32_t ph) { ok = ok && wait_warp(smem_addr(&full[s]), ph, abort_flag, a.status, limit); };
-        auto next = [&](int& s, uint32_t& ph) {
-            if (++s == S::kSlots) {
-                s = 0;
-                ph ^= 1;
-            }
-        };
-        // scores of tile q into buffer b from the K piece(s) at the ring's position
-        auto scores = [&](int q, int b, int s, int x) {
-            const uint32_t kp = ring + (uint32_t)s * S::kPiece, qp = q_smem + (uint32_t)q * S::kQBytes;
+        auto wait_on = [&](uint64_t* bar, uint32_t ph) { ok = ok && wait_warp(smem_addr(bar), ph & 1, abort_flag, a.status, limit); };
+        // piece k of the ring's order
+        auto wait_piece = [&](int k) { wait_on(&full[k % S::kSlots], (uint32_t)(k / S::kSlots)); };
+        auto release = [&](int k) { mma_commit_local<1>(smem_addr(&empty[k % S::kSlots]), issuer); };
+        // scores of tile q into buffer b from K piece k (the x-th of its tile)
+        auto scores = [&](int q, int b, int k, int x) {
+            const uint32_t kp = desc_lo(ring + (uint32_t)(k % S::kSlots) * S::kPiece);
+            const uint32_t qp = desc_lo(q_smem + (uint32_t)q * S::kQBytes + (uint32_t)x * (S::kKChunks * 128 * 128));
 #pragma unroll
             for (int c = 0; c < S::kKChunks; ++c)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16<1>(tmem + (uint32_t)(q * S::kS + b) * 128,
-                                smem_desc<64>(qp + (uint32_t)(x * S::kKChunks + c) * (128 * 128) + k * 32),
-                                smem_desc<64>(kp + (uint32_t)c * (kTk * 128) + k * 32), idesc_s, (x | c | k) != 0, issuer);
+                for (int j = 0; j < 4; ++j)
+                    mma_ss(tmem + (uint32_t)(q * S::kS + b) * 128, qp + ((c * (128 * 128) + j * 32) >> 4),
+                           kp + ((c * (kTk * 128) + j * 32) >> 4), idesc_s, (x | c | j) != 0, issuer);
         };
-        auto values = [&](int q, int b, int s, int x, bool add) {
-            const uint32_t vp = ring + (uint32_t)s * S::kPiece;
+        auto values = [&](int q, int b, int k, int x, bool add) {
+            const uint32_t vp = desc_lo(ring + (uint32_t)(k % S::kSlots) * S::kPiece, S::kVTok * 128);
+            const uint32_t wp = tmem + S::kP + (uint32_t)(q * S::kS + b) * S::kPStep + (uint32_t)x * (S::kVTok / 2);
 #pragma unroll
-            for (int k = 0; k < S::kVTok / 16; ++k)
-                mma_bf16_ts(tmem + S::kO + (uint32_t)q * D, tmem + (uint32_t)(q * S::kS + b) * 128 + (uint32_t)(x * S::kVTok / 16 + k) * 8,
-                            v_desc(vp + (uint32_t)k * 2048, S::kVTok * 128), idesc_o, add || (x | k) != 0, issuer);
+            for (int j = 0; j < S::kVTok / 16; ++j)
+                mma_ts(tmem + S::kO + (uint32_t)q * D, wp + j * 8, vp + (j * 2048 >> 4), idesc_o, add || (x | j) != 0, issuer);
         };
         if (n > 0) {
-            ok = wait_warp(smem_addr(q_full), 0, abort_flag, a.status, limit);
+            wait_on(q_full, 0);
             tc_fence_after();
-            if (S::kS == 1) {
-                wait_piece(slot, phase);
-                tc_fence_after();
+            if (S::kIssuers == 2) {
+                // The ring's order: K(0), then per tile K(t + 1), V(t): the weights lie apart from the scores, so
+                // the next scores need only the last ones read. The tiles of rows begin in turn, so that neither
+                // runs ahead and holds the ring's pieces.
+                auto begin = [&]() {
+                    if (lane == 0) mbar_arrive(smem_addr(&turn[me]));
+                    tc_fence_after();
+                };
+                auto do_scores = [&](int k) {
+                    scores(me, 0, k, 0);
+                    mma_commit_local<1>(smem_addr(&s_full[me]), issuer);
+                    release(k);
+                };
+                wait_piece(0);
+                if (me == 1) wait_on(&turn[0], 0);
                 if (ok) {
-#pragma unroll
-                    for (int q = 0; q < S::kQ; ++q) {
-                        scores(q, 0, slot, 0);
-                        mma_commit_local<1>(smem_addr(&s_full[q]), issuer);
-                    }
-                    mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
+                    begin();
+                    do_scores(0);
                 }
-                next(slot, phase);
                 for (int t = 0; t < n && ok; ++t) {
-                    int ks = slot;
-                    uint32_t kph = phase;
-                    next(ks, kph);
+                    const bool more = t + 1 < n;
+                    if (more) {
+                        wait_on(&turn[1 - me], me == 0 ? t : t + 1);
+                        wait_on(&s_read[me], t);
+                        wait_piece(1 + 2 * t);
+                        if (!ok) break;
+                        begin();
+                        do_scores(1 + 2 * t);
+                    }
+                    const int kv = 1 + 2 * t + (more ? 1 : 0);
+                    wait_on(&p_full[me], t);
+                    wait_piece(kv);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(me, 0, kv, 0, t > 0);
+                    mma_commit_local<1>(smem_addr(&pv_done[me]), issuer);
+                    release(kv);
+                }
+            } else if (S::kQ == 2) {
+                // the ring's order: K(0), then per tile V(t), K(t + 1)
+                for (int t = -1; t < n && ok; ++t) {
+                    const int kv = 1 + 2 * t, ks = 2 + 2 * t;
 #pragma unroll
                     for (int q = 0; q < S::kQ; ++q) {
-                        ok = ok && wait_warp(smem_addr(&p_full[q]), t & 1, abort_flag, a.status, limit);
-                        if (q == 0) wait_piece(slot, phase);
+                        // lane 0 the weights, and for both tiles at once 1 the piece of V, 2 that of K
+                        uint64_t* bar = t >= 0 ? &p_full[q] : &full[0];
+                        uint32_t ph = t >= 0 ? (uint32_t)t : 0;
+                        if (q == 0 && t >= 0 && lane == 1) {
+                            bar = &full[kv % S::kSlots];
+                            ph = (uint32_t)(kv / S::kSlots);
+                        }
+                        if (q == 0 && t + 1 < n && lane == 2) {
+                            bar = &full[ks % S::kSlots];
+                            ph = (uint32_t)(ks / S::kSlots);
+                        }
+                        ok = ok && wait_lanes(smem_addr(bar), ph & 1, abort_flag, a.status, limit);
                         if (!ok) break;
                         tc_fence_after();
-                        values(q, 0, slot, 0, t > 0);
-                        mma_commit_local<1>(smem_addr(&pv_done[q]), issuer);
-                        if (q == S::kQ - 1) mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
+                        if (t >= 0) {
+                            values(q, 0, kv, 0, t > 0);
+                            mma_commit_local<1>(smem_addr(&pv_done[q]), issuer);
+                        }
                         if (t + 1 < n) {
-                            if (q == 0) wait_piece(ks, kph);
-                            if (!ok) break;
-                            tc_fence_after();
                             scores(q, 0, ks, 0);
                             mma_commit_local<1>(smem_addr(&s_full[q]), issuer);
-                            if (q == S::kQ - 1) mma_commit_local<1>(smem_addr(&empty[ks]), issuer);
                         }
                     }
-                    slot = ks;
-                    phase = kph;
-                    next(slot, phase);
+                    if (!ok) break;
+                    if (t >= 0) release(kv);
+                    if (t + 1 < n) release(ks);
                 }
             } else {
                 for (int t = -1; t < n && ok; ++t) {
                     if (t + 1 < n) {
-                        const int b = (t + 1) & 1;
+                        const int b = (t + 1) & 1, k0 = t < 0 ? 0 : S::kPieces * (2 * t + 1);
 #pragma unroll
                         for (int x = 0; x < S::kPieces; ++x) {
-                            wait_piece(slot, phase);
+                            wait_piece(k0 + x);
                             if (!ok) break;
                             tc_fence_after();
-                            scores(0, b, slot, x);
-                            mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
-                            next(slot, phase);
+                            scores(0, b, k0 + x, x);
+                            release(k0 + x);
                         }
                         if (!ok) break;
                         mma_commit_local<1>(smem_addr(&s_full[b]), issuer);
                     }
                     if (t < 0) continue;
-                    ok = ok && wait_warp(smem_addr(&p_full[t & 1]), (t >> 1) & 1, abort_flag, a.status, limit);
+                    wait_on(&p_full[t & 1], t >> 1);
+                    const int k0 = S::kPieces * (2 * t + (t + 1 < n ? 2 : 1));
 #pragma unroll
                     for (int x = 0; x < S::kPieces; ++x) {
-                        wait_piece(slot, phase);
+                        wait_piece(k0 + x);
                         if (!ok) break;
                         tc_fence_after();
-                        values(0, t & 1, slot, x, t > 0);
-                        mma_commit_local<1>(smem_addr(&empty[slot]), issuer);
-                        next(slot, phase);
+                        values(0, t & 1, k0 + x, x, t > 0);
+                        release(k0 + x);
                     }
-                    if (ok) mma_commit_local<1>(smem_addr(&pv_done[0]), issuer);
+                    if (ok) mma_commit_local<1>(smem_addr(&pv_done[t & 1]), issuer);
                 }
             }
             // every product has ended before tensor memory is given back
-            mma_commit_local<1>(smem_addr(drain), issuer);
-            if (lane == 0) wait_bounded(smem_addr(drain), 0, abort_flag, a.status, limit, false);
+            mma_commit_local<1>(smem_addr(&drain[me]), issuer);
+            if (lane == 0) wait_bounded(smem_addr(&drain[me]), 0, abort_flag, a.status, limit, false);
             __syncwarp();
         }
     } else if (warp < kMmaWarp) {
@@ -452,12 +526,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             *reinterpret_cast<uint4*>(base + q * S::kQBytes + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val;
         }
         fence_proxy_async_shared();
-        mbar_arrive(smem_addr(q_full));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(q_full));
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);      // this warp's 32 lanes
         const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * (D / 2);
         const float scl = a.scale_log2;
         float m = -INFINITY, l = 0.f;
-        const int tile_first = u.r.first + q * p.tile_tokens, last_pos = tile_first + p.tile_tokens - 1;
         // After a wait that ran out the warps run on without data, so that their barriers stay matched; the
         // status word says that the output is incomplete.
         for (int t = 0; t < n; ++t) {
@@ -467,27 +541,23 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
             tc_fence_after();
             const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
+            const uint32_t p_addr = lanes + S::kP + (uint32_t)(q * S::kS + b) * S::kPStep + half * 32;
+            const int c0 = j0 + half * 64;
+            const int lo = a.window ? pos - a.window + 1 - c0 : 0, sk = a.window ? a.sinks - c0 : 0;
+            const bool masked = __any_sync(0xffffffffu, pos - c0 < 63 || (lo > 0 && sk < 64));
             uint32_t v[64];
             tmem_ld32(s_addr + half * 64, v);
             tmem_ld32(s_addr + half * 64 + 32, v + 32);
             tmem_ld_wait32(v);
             tmem_ld_wait32(v + 32);
-            if (j0 + kTk - 1 > tile_first || (a.window && j0 <= last_pos - a.window && j0 + kTk > a.sinks)) {
-                // columns up to hi, and from lo or below sk
-                const int c0 = j0 + half * 64;
-                mask<64>(v, pos - c0, a.window ? pos - a.window + 1 - c0 : 0, a.window ? a.sinks - c0 : 0);
-            }
-            float mx[8];                 // eight chains
-#pragma unroll
-            for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(v[c]);
-#pragma unroll
-            for (int c = 8; c < 64; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(v[c]));
-#pragma unroll
-            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], mx[c + 4]);
-            float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // A new reference: at first, or when the maximum has outgrown the old one by 2^8. The barrier also
-            // tells each thread that the other has read its scores, which the weights are about to overwrite.
+            if (masked) mask(v, pos - c0, lo, sk);
+            float top = row_max(v);
+            // The weights by the reference at hand, while the row's other thread does its half; the barrier then
+            // tells whether either maximum has outgrown the reference by 2^8 (or is the first), in which case both
+            // read their scores again and go by a new one. It also orders the weights, which overwrite scores,
+            // after both threads' reads.
             const bool wish = m == -INFINITY ? top > -INFINITY : (top - m) * scl > 8.f;
+            float sum = weights(v, scl, m == -INFINITY ? 0.f : m * scl);
             if (pair_any(pair, wish)) {
                 if (half) *share = top;
                 pair_any(pair, false);
@@ -498,8 +568,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 const bool fix = grow && m != -INFINITY;
                 if (__any_sync(0xffffffffu, fix)) {
                     const float alpha = fix ? ex2((m - top) * scl) : 1.f;
-                    wait_here(smem_addr(&pv_done[q]), (t - 1) & 1, abort_flag, a.status, limit);
-                    __syncwarp();
+                    const int tp = t - 1, bp = S::kS == 2 ? tp & 1 : 0;
+                    wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -513,21 +583,28 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     l *= alpha;
                 }
                 if (grow) m = top;
+                tmem_ld32(s_addr + half * 64, v);
+                tmem_ld32(s_addr + half * 64 + 32, v + 32);
+                tmem_ld_wait32(v);
+                tmem_ld_wait32(v + 32);
+                if (masked) mask(v, pos - c0, lo, sk);
+                sum = weights(v, scl, m == -INFINITY ? 0.f : m * scl);
+                pair_any(pair, false);
             }
-            const float ms = m == -INFINITY ? 0.f : m * scl;
-            const uint64_t scl2 = pack2(scl, scl), ms2 = pack2(-ms, -ms);
-            uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t w[16];
-                weights(v + x * 32, w, scl2, ms2, sum);
-                tmem_st16(s_addr + half * 32 + x * 16, w);
+            if (S::kApart) {
+                tc_fence_before();
+                if (lane == 0) mbar_arrive(smem_addr(&s_read[q]));
+                // the weights' place is free once the product before has ended
+                if (t > 0) wait_warp(smem_addr(&pv_done[q]), (t - 1) & 1, abort_flag, a.status, limit);
+                tc_fence_after();
             }
-            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += lo2(sum[0]) + hi2(sum[0]);
-            if (q == 0 && u.len - j0 < kTk) {
+            l += sum;
+            tmem_st16(p_addr, v);
+            tmem_st16(p_addr + 16, v + 16);
+            if (u.len - j0 < kTk) {
                 // places past the last token may hold anything: their weight is 0, so they must be finite
-                const int k0 = S::kS == 2 ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t;   // the V pieces' place in the ring's order
+                // (each tile of rows writes the same zeros before its own product)
+                const int k0 = S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t;   // the V pieces' place in the ring's order
                 for (int x = 0; x < S::kPieces; ++x) {
                     const int s = (k0 + x) % S::kSlots;
                     wait_warp(smem_addr(&full[s]), (uint32_t)((k0 + x) / S::kSlots) & 1, abort_flag, a.status, limit);
@@ -544,12 +621,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
         }
-        // with two score buffers the product before the last may still run: a parity tells one phase from
-        // the next only
-        if (S::kS == 2 && n > 1) wait_warp(smem_addr(&pv_done[q]), n & 1, abort_flag, a.status, limit);
-        if (n > 0) wait_warp(smem_addr(&pv_done[q]), (n - 1) & 1, abort_flag, a.status, limit);
+        if (n > 0) {
+            const int tp = n - 1, bp = S::kS == 2 ? tp & 1 : 0;
+            wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
+        }
         tc_fence_after();
         // the row's sum: its two threads' parts
         if (half) *share = l;
