@@ -118,34 +118,39 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         : "memory");
 }
 
-// One block's work: a unit (or, with splits, one part of its cache tiles).
+// One block's work: a unit, or one part of its cache tiles.
 struct Unit {
-    int i, seq, head, tok0, q_len, row0, len;
+    int seq, head, tok0, q_len, row0, len;
     TileRange r;
     int t0, t1;           // its tiles
+    int parts;            // of the unit (1: this block writes its output)
+    bool idle;            // a part that is left nothing to do or to write
 };
+// Units go by sequence, then from the last rows (which see most) to the first, then by head. The last
+// ones, from p.whole on, are split in p.splits parts, so that the blocks end together; one with few tiles
+// is left whole all the same.
 template <int D, int N>
-__device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptList<N>& list, int block) {
+__device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptList<N>& list, int unit, int part) {
     using S = Shape<D>;
     Unit u;
-    const int unit = block / p.splits, part = block - unit * p.splits;
     int lo = 0, hi = list.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (list.unit0[mid] <= unit) lo = mid; else hi = mid - 1;
     }
-    u.i = lo;
     u.seq = list.seq[lo];
     u.q_len = list.q_len[lo];
     u.row0 = list.row[lo];
-    const int step = S::kQ * p.tile_tokens, per = (u.q_len + step - 1) / step, v = unit - list.unit0[lo];
-    u.head = v / per;
-    u.tok0 = (per - 1 - (v - u.head * per)) * step;      // the longest rows first
+    const int step = S::kQ * p.tile_tokens, per = (u.q_len + step - 1) / step, v = unit - list.unit0[lo], n_kv = p.a.c.n_kv;
+    u.head = v % n_kv;
+    u.tok0 = (per - 1 - v / n_kv) * step;
     u.len = cache_len(p.a.c, u.seq);
     const int first = u.len - u.q_len + u.tok0, last = u.len - u.q_len + min(u.q_len, u.tok0 + step) - 1;
     u.r = tile_range(first, last, p.a.window, p.a.sinks, kTk);
-    u.t0 = (int)((long long)u.r.n * part / p.splits);
-    u.t1 = (int)((long long)u.r.n * (part + 1) / p.splits);
+    u.parts = unit >= p.whole && u.r.n >= 4 * p.splits ? p.splits : 1;
+    u.idle = part >= u.parts;
+    u.t0 = u.idle ? 0 : (int)((long long)u.r.n * part / u.parts);
+    u.t1 = u.idle ? 0 : (int)((long long)u.r.n * (part + 1) / u.parts);
     return u;
 }
 
@@ -190,15 +195,26 @@ __device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, volati
 }
 // The low n bits (n may be outside 0 .. 64).
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
-// Scores of 64 columns that the row does not see become -inf: it sees columns up to hi that are lo or more, or below sk.
+// Scores of N columns that the row does not see become -inf: it sees columns up to hi that are lo or more, or below sk.
+template <int N>
 __device__ __forceinline__ void mask(uint32_t* v, int hi, int lo, int sk) {
-    const uint64_t seen = low_bits(hi + 1) & (~low_bits(lo) | low_bits(sk));
-    const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-        if (!(s0 & 1u << c)) v[c] = 0xff800000u;
-        if (!(s1 & 1u << c)) v[32 + c] = 0xff800000u;
+    for (int h = 0; h < N; h += 64) {
+        const uint64_t seen = low_bits(hi + 1 - h) & (~low_bits(lo - h) | low_bits(sk - h));
+        const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+            if (!(s0 & 1u << c)) v[h + c] = 0xff800000u;
+            if (!(s1 & 1u << c)) v[h + 32 + c] = 0xff800000u;
+        }
     }
+}
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t* v) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld32(taddr + c, v + c);
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld_wait32(v + c);
 }
 // Barrier of the two warps that share 32 rows; true for both if any thread of either wishes it.
 __device__ __forceinline__ bool pair_any(int id, bool wish) {
@@ -211,31 +227,31 @@ __device__ __forceinline__ bool pair_any(int id, bool wish) {
         : "memory");
     return r != 0;
 }
-// The largest of 64 scores.
+// The largest of three, and of N scores.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+template <int N>
 __device__ __forceinline__ float row_max(const uint32_t* v) {
-    float x[8];
+    float x[8];                                            // eight chains
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = __uint_as_float(v[c]);
+    for (int c = 0; c < 8; ++c) x[c] = fmaxf(__uint_as_float(v[c]), __uint_as_float(v[8 + c]));
 #pragma unroll
-    for (int c = 8; c < 56; c += 16)
+    for (int c = 16; c < N; c += 16)
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = max3(x[e], __uint_as_float(v[c + e]), __uint_as_float(v[c + 8 + e]));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = max3(x[e], x[e + 4], max3(__uint_as_float(v[56 + e]), __uint_as_float(v[60 + e]), -INFINITY));
-    return fmaxf(max3(x[0], x[1], x[2]), x[3]);
+    return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
 }
-// 64 scores to weights 2^(s scl - ms): v[0 .. 31] get them in pairs, rounded to bf16 for the product with V;
+// N scores to weights 2^(s scl - ms): v[0 .. N / 2) get them in pairs, rounded to bf16 for the product with V;
 // returns their sum before that rounding.
+template <int N>
 __device__ __forceinline__ float weights(uint32_t* v, float scl, float ms) {
     const uint64_t scl2 = pack2(scl, scl), ms2 = pack2(-ms, -ms);
     uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < N / 2; ++c) {
         const uint64_t e = fma2((uint64_t)v[2 * c + 1] << 32 | v[2 * c], scl2, ms2);
         const float x = ex2(lo2(e)), y = ex2(hi2(e));
         sum[c & 3] = add2(sum[c & 3], pack2(x, y));
@@ -295,7 +311,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const AttnParams& a = p.a;
     const uint64_t limit = a.wait_limit_ns;
-    const Unit u = find_unit<D>(p, list, blockIdx.x);
+    const int split = (int)blockIdx.x - p.whole;           // which part of the split units, from 0
+    const Unit u = find_unit<D>(p, list, split < 0 ? (int)blockIdx.x : p.whole + split / p.splits, split < 0 ? 0 : split % p.splits);
     const int n = u.t1 - u.t0;
     const uint32_t q_smem = smem_addr(base), ring = q_smem + S::kRing;
     const uint32_t issuer = lane == 0 ? 1u : 0u;
@@ -515,6 +532,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const int pos = valid ? u.len - u.q_len + tok : -1;
         const int pair = 1 + q * 4 + (warp & 3);                         // named barrier of the two warps of these rows
         float* share = reinterpret_cast<float*>(base + S::kShare) + q * 128 + row;
+        constexpr int kCols = kTk / 2, kOut = D / 2;                     // scores and features of this thread
         typedef __nv_bfloat16 bf;
         // this tile's queries into shared memory, 128-byte swizzled rows in chunks of 64 features
         for (int v = half * 128 + row; v < 128 * (D / 8); v += 256) {
@@ -529,7 +547,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(q_full));
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);      // this warp's 32 lanes
-        const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * (D / 2);
+        const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * kOut;
         const float scl = a.scale_log2;
         float m = -INFINITY, l = 0.f;
         // After a wait that ran out the warps run on without data, so that their barriers stay matched; the
@@ -541,23 +559,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
             tc_fence_after();
             const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
-            const uint32_t p_addr = lanes + S::kP + (uint32_t)(q * S::kS + b) * S::kPStep + half * 32;
-            const int c0 = j0 + half * 64;
+            const uint32_t p_addr = lanes + S::kP + (uint32_t)(q * S::kS + b) * S::kPStep + half * (kCols / 2);
+            const int c0 = j0 + half * kCols;
             const int lo = a.window ? pos - a.window + 1 - c0 : 0, sk = a.window ? a.sinks - c0 : 0;
-            const bool masked = __any_sync(0xffffffffu, pos - c0 < 63 || (lo > 0 && sk < 64));
-            uint32_t v[64];
-            tmem_ld32(s_addr + half * 64, v);
-            tmem_ld32(s_addr + half * 64 + 32, v + 32);
-            tmem_ld_wait32(v);
-            tmem_ld_wait32(v + 32);
-            if (masked) mask(v, pos - c0, lo, sk);
-            float top = row_max(v);
+            const bool masked = __any_sync(0xffffffffu, pos - c0 < kCols - 1 || (lo > 0 && sk < kCols));
+            uint32_t v[kCols];
+            load_scores<kCols>(s_addr + half * kCols, v);
+            if (masked) mask<kCols>(v, pos - c0, lo, sk);
+            float top = row_max<kCols>(v);
             // The weights by the reference at hand, while the row's other thread does its half; the barrier then
             // tells whether either maximum has outgrown the reference by 2^8 (or is the first), in which case both
             // read their scores again and go by a new one. It also orders the weights, which overwrite scores,
             // after both threads' reads.
             const bool wish = m == -INFINITY ? top > -INFINITY : (top - m) * scl > 8.f;
-            float sum = weights(v, scl, m == -INFINITY ? 0.f : m * scl);
+            float sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
             if (pair_any(pair, wish)) {
                 if (half) *share = top;
                 pair_any(pair, false);
@@ -572,7 +587,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
+                    for (int c = 0; c < kOut / 16; ++c) {
                         uint32_t x[16];
                         tmem_ld16(o_addr + c * 16, x);
                         tmem_ld_wait16(x);
@@ -583,12 +598,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     l *= alpha;
                 }
                 if (grow) m = top;
-                tmem_ld32(s_addr + half * 64, v);
-                tmem_ld32(s_addr + half * 64 + 32, v + 32);
-                tmem_ld_wait32(v);
-                tmem_ld_wait32(v + 32);
-                if (masked) mask(v, pos - c0, lo, sk);
-                sum = weights(v, scl, m == -INFINITY ? 0.f : m * scl);
+                load_scores<kCols>(s_addr + half * kCols, v);
+                if (masked) mask<kCols>(v, pos - c0, lo, sk);
+                sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
                 pair_any(pair, false);
             }
             if (S::kApart) {
@@ -599,8 +611,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 tc_fence_after();
             }
             l += sum;
-            tmem_st16(p_addr, v);
-            tmem_st16(p_addr + 16, v + 16);
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) tmem_st16(p_addr + c * 16, v + c * 16);
             if (u.len - j0 < kTk) {
                 // places past the last token may hold anything: their weight is 0, so they must be finite
                 // (each tile of rows writes the same zeros before its own product)
@@ -636,11 +648,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         pair_any(pair, false);
         if (half) l = *share;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        bf* out = static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + hq * a.o_head + half * (D / 2);
-        const long long part = ((long long)blockIdx.x * S::kQ + q) * 128 + row;
-        if (p.splits > 1 && half == 0) p.part_ml[part] = make_float2(m * scl, l);
+        bf* out = static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + hq * a.o_head + half * kOut;
+        const long long part = ((long long)split * S::kQ + q) * 128 + row;
+        if (u.parts > 1 && half == 0) p.part_ml[part] = make_float2(m * scl, l);
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
+        for (int c = 0; c < kOut / 32; ++c) {
             uint32_t x[32];
             if (n > 0) {
                 tmem_ld32(o_addr + c * 32, x);
@@ -649,9 +661,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = 0;
             }
-            if (!valid) continue;
-            if (p.splits > 1) {
-                float4* d = reinterpret_cast<float4*>(p.part_o + part * D + half * (D / 2) + c * 32);
+            if (!valid || u.idle) continue;
+            if (u.parts > 1) {
+                float4* d = reinterpret_cast<float4*>(p.part_o + part * D + half * kOut + c * 32);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     d[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
@@ -684,7 +696,8 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     constexpr int E = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.x / (S::kQ * 32), row = (blockIdx.x % (S::kQ * 32)) * 4 + warp;
-    const Unit u = find_unit<D>(p, list, unit * p.splits);
+    const Unit u = find_unit<D>(p, list, p.whole + unit, 0);
+    if (u.parts == 1) return;            // its one block wrote it
     const int q = row >> 7, r = row & 127, g = p.group, qi = r / g, tok = u.tok0 + q * p.tile_tokens + qi;
     if (qi >= p.tile_tokens || tok >= u.q_len) return;
     const long long at = ((long long)unit * p.splits * S::kQ + q) * 128 + r, step = S::kQ * 128;
@@ -723,10 +736,10 @@ cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cud
         list.seq[i] = all.seq[i];
         list.unit0[i] = all.unit0[i];
     }
-    prompt_kernel<D, N><<<(unsigned)(p.units * p.splits), Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(p, list);
+    prompt_kernel<D, N><<<(unsigned)(p.whole + (p.units - p.whole) * p.splits), Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(p, list);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return e;
-    prompt_join_kernel<D, N><<<(unsigned)(p.units * Shape<D>::kQ * 32), 128, 0, stream>>>(p, list);
+    if (e != cudaSuccess || p.whole == p.units) return e;
+    prompt_join_kernel<D, N><<<(unsigned)((p.units - p.whole) * Shape<D>::kQ * 32), 128, 0, stream>>>(p, list);
     return cudaGetLastError();
 }
 

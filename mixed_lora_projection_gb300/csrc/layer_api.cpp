@@ -139,7 +139,7 @@ bool encode_cache(EncodeTiledFn encode, CUtensorMap* m, int* order, const CacheV
     } ax[3] = {{0, (uint64_t)(v ? c.v_head : c.k_head), (uint64_t)c.n_kv, 1},
                {1, (uint64_t)(v ? c.v_token : c.k_token), (uint64_t)c.page_size, (uint32_t)granule},
                {2, (uint64_t)(v ? c.v_page : c.k_page), (uint64_t)c.n_pages, 1}};
-    std::stable_sort(ax, ax + 3, [](const Axis& a, const Axis& b) { return a.stride < b.stride; });
+    std::sort(ax, ax + 3, [](const Axis& a, const Axis& b) { return a.stride != b.stride ? a.stride < b.stride : a.what < b.what; });
     cuuint64_t dims[4] = {(cuuint64_t)c.dim, ax[0].size, ax[1].size, ax[2].size};
     cuuint64_t strides[3] = {ax[0].stride * 2, ax[1].stride * 2, ax[2].stride * 2};
     cuuint32_t box[4] = {64, ax[0].box, ax[1].box, ax[2].box};
@@ -239,16 +239,19 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
         if (units > 0x7fffffff / 8) return LORA_EUNSUPPORTED;
     }
     p.units = (int)units;
-    // parts of a unit's cache tiles: as many as shorten the last wave of blocks, 3% each for the join
+    // the units past the last full wave of blocks run in as many parts as make that wave's end shortest; 4%
+    // of a unit for each part's sums
+    const long long rest = units % h->num_sms;
     p.splits = 1;
-    double best = (double)((units + h->num_sms - 1) / h->num_sms);
-    for (int s = 2; s <= 16 && units * s * tiles <= h->max_parts; ++s) {
-        const double cost = (double)((units * s + h->num_sms - 1) / h->num_sms) / s + 0.03 * s;
+    double best = rest ? 1.0 : 0.0;
+    for (int s = 2; s <= 16 && rest * s * tiles <= h->max_parts; ++s) {
+        const double cost = (double)((rest * s + h->num_sms - 1) / h->num_sms) / s + 0.04 * s;
         if (cost < best) {
             best = cost;
             p.splits = s;
         }
     }
+    p.whole = (int)(p.splits > 1 ? units - rest : units);
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     if (!encode_cache(h->encode, &p.tm_k, &p.k_order, a.c, false, p.granule) ||
@@ -448,7 +451,7 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
     // sequences with few rows and long ones go to different kernels
     const int g = h->n_heads / h->n_kv;
     SeqList<kMaxSeqs> few;
-    PromptList<kMaxSeqs> many;
+    SeqList<kMaxSeqs> many;
     few.n = many.n = 0;
     int most = 0;
     for (int i = 0; i < cache->n_seqs; ++i) {
@@ -461,7 +464,18 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
         if (&l == &few) most = std::max(most, n * g);
     }
     if (many.n) {
-        const int rc = run_prompts(h, p, many);
+        // the sequences with most rows first: the last blocks of a launch had better be short
+        int by[kMaxSeqs];
+        for (int i = 0; i < many.n; ++i) by[i] = i;
+        std::sort(by, by + many.n, [&](int a, int b) { return many.q_len[a] != many.q_len[b] ? many.q_len[a] > many.q_len[b] : a < b; });
+        PromptList<kMaxSeqs> sorted;
+        sorted.n = many.n;
+        for (int i = 0; i < many.n; ++i) {
+            sorted.seq[i] = many.seq[by[i]];
+            sorted.row[i] = many.row[by[i]];
+            sorted.q_len[i] = many.q_len[by[i]];
+        }
+        const int rc = run_prompts(h, p, sorted);
         if (rc != LORA_OK) return rc;
     }
     return few.n ? run_decode(h, p, few, most) : LORA_OK;

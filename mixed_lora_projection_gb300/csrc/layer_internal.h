@@ -112,8 +112,8 @@ struct PromptParams {
     AttnParams a;
     int k_order, v_order, granule, group;
     int tile_tokens;                    // tokens of one tile of rows: 128 / group
-    int units, splits;                  // blocks: every unit's cache tiles in `splits` parts
-    float* part_o;                      // [units x splits x tiles][128][dim]
+    int units, whole, splits;           // the units from `whole` on have their cache tiles in `splits` parts
+    float* part_o;                      // [split units x splits x tiles][128][dim]
     float2* part_ml;
 };
 int prompt_tiles(int dim);              // tiles of rows of a unit
