@@ -279,6 +279,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     uint64_t* turn = drain + 2;                           // [2] a tile's scores are issued (the first: and used)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int split = (int)blockIdx.x - p.whole;           // which part of the split units, from 0
+    const Unit u = find_unit<D>(p, list, split < 0 ? (int)blockIdx.x : p.whole + split / p.splits, split < 0 ? 0 : split % p.splits);
+    if (u.idle) return;
+    const int n = u.t1 - u.t0;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);              // known to be the same in every lane
     constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + S::kIssuers;
@@ -311,9 +315,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const AttnParams& a = p.a;
     const uint64_t limit = a.wait_limit_ns;
-    const int split = (int)blockIdx.x - p.whole;           // which part of the split units, from 0
-    const Unit u = find_unit<D>(p, list, split < 0 ? (int)blockIdx.x : p.whole + split / p.splits, split < 0 ? 0 : split % p.splits);
-    const int n = u.t1 - u.t0;
     const uint32_t q_smem = smem_addr(base), ring = q_smem + S::kRing;
     const uint32_t issuer = lane == 0 ? 1u : 0u;
     if (warp == kTmaWarp) {
@@ -534,14 +535,30 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         float* share = reinterpret_cast<float*>(base + S::kShare) + q * 128 + row;
         constexpr int kCols = kTk / 2, kOut = D / 2;                     // scores and features of this thread
         typedef __nv_bfloat16 bf;
-        // this tile's queries into shared memory, 128-byte swizzled rows in chunks of 64 features
-        for (int v = half * 128 + row; v < 128 * (D / 8); v += 256) {
-            const int rr = v / (D / 8), c = v % (D / 8), ri = rr / g, rt = u.tok0 + q * p.tile_tokens + ri;
-            uint4 val = make_uint4(0, 0, 0, 0);
-            if (ri < p.tile_tokens && rt < u.q_len)
-                val = *reinterpret_cast<const uint4*>(static_cast<const bf*>(a.q) + (u.row0 + rt) * a.q_stride +
-                                                      (u.head * g + (rr - ri * g)) * a.q_head + c * 8);
-            *reinterpret_cast<uint4*>(base + q * S::kQBytes + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val;
+        // this tile's queries into shared memory, 128-byte swizzled rows in chunks of 64 features: each thread
+        // has one 16-byte column of every 2048 / D-th row, and its loads are in flight together
+        {
+            constexpr int kStep = 2048 / D, kLoads = 128 / kStep;
+            const int c = (half * 128 + row) % (D / 8), r0 = (half * 128 + row) / (D / 8);
+            const bf* src = static_cast<const bf*>(a.q) + (long long)(u.row0 + u.tok0 + q * p.tile_tokens) * a.q_stride +
+                            (long long)u.head * g * a.q_head + c * 8;
+            const int last = min(u.q_len - u.tok0 - q * p.tile_tokens, p.tile_tokens);   // tokens of this tile
+            uint8_t* dst = base + q * S::kQBytes + (c >> 3) * (128 * 128);
+#pragma unroll
+            for (int i0 = 0; i0 < kLoads; i0 += 8) {
+                uint4 val[8];
+#pragma unroll
+                for (int i = 0; i < 8 && i0 + i < kLoads; ++i) {
+                    const int rr = r0 + (i0 + i) * kStep, ri = rr / g;
+                    val[i] = make_uint4(0, 0, 0, 0);
+                    if (ri < last) val[i] = *reinterpret_cast<const uint4*>(src + ri * a.q_stride + (rr - ri * g) * a.q_head);
+                }
+#pragma unroll
+                for (int i = 0; i < 8 && i0 + i < kLoads; ++i) {
+                    const int rr = r0 + (i0 + i) * kStep;
+                    *reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val[i];
+                }
+            }
         }
         fence_proxy_async_shared();
         __syncwarp();
@@ -661,7 +678,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = 0;
             }
-            if (!valid || u.idle) continue;
+            if (!valid) continue;
             if (u.parts > 1) {
                 float4* d = reinterpret_cast<float4*>(p.part_o + part * D + half * kOut + c * 32);
 #pragma unroll
