@@ -46,8 +46,9 @@ struct Shape {
     static constexpr int kPStep = kApart ? 64 : 128;
     static constexpr int kRing = kQ * kQBytes;
     static constexpr int kBars = kRing + kSlots * kPiece;
-    static constexpr int kShare = kBars + 512;            // [kQ][128] floats between the two threads of a row
-    static constexpr int kSmem = kShare + kQ * 512 + 1024;
+    static constexpr int kShare = kBars + 320;            // [kQ][128] floats between the two threads of a row
+    static constexpr int kPrefix = kShare + kQ * 512;     // [kPromptBlocks + 1] tiles before each of the last units
+    static constexpr int kSmem = kPrefix + (kPromptBlocks + 1) * 4 + 1024;
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
@@ -118,19 +119,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
         : "memory");
 }
 
-// One block's work: a unit, or one part of its cache tiles.
+// A unit: one key/value head and a run of its sequence's new rows. Units go by sequence, then from the
+// last rows (which see most) to the first, then by head.
 struct Unit {
     int seq, head, tok0, q_len, row0, len;
     TileRange r;
-    int t0, t1;           // its tiles
-    int parts;            // of the unit (1: this block writes its output)
-    bool idle;            // a part that is left nothing to do or to write
 };
-// Units go by sequence, then from the last rows (which see most) to the first, then by head. The last
-// ones, from p.whole on, are split in p.splits parts, so that the blocks end together; one with few tiles
-// is left whole all the same.
 template <int D, int N>
-__device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptList<N>& list, int unit, int part) {
+__device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptList<N>& list, int unit) {
     using S = Shape<D>;
     Unit u;
     int lo = 0, hi = list.n - 1;
@@ -147,12 +143,71 @@ __device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptLis
     u.len = cache_len(p.a.c, u.seq);
     const int first = u.len - u.q_len + u.tok0, last = u.len - u.q_len + min(u.q_len, u.tok0 + step) - 1;
     u.r = tile_range(first, last, p.a.window, p.a.sinks, kTk);
-    u.parts = unit >= p.whole && u.r.n >= 4 * p.splits ? p.splits : 1;
-    u.idle = part >= u.parts;
-    u.t0 = u.idle ? 0 : (int)((long long)u.r.n * part / u.parts);
-    u.t1 = u.idle ? 0 : (int)((long long)u.r.n * (part + 1) / u.parts);
     return u;
 }
+
+// A block's work, which each of its warps walks through for itself. Whole units first, as many for each
+// block, every other round of them backwards (their lengths fall). Of the units that are left, less than
+// one a block, each goes to a block whole, or, where that would leave the blocks waiting for longer than
+// the join takes (kWorth tiles), all their tiles form one line that is cut into equal parts: a part may end
+// inside a unit, whose sums then go to the workspace.
+constexpr int kWorth = 8;
+struct Plan {
+    uint32_t total;       // tiles of the last units, if they are cut (else 0)
+    uint32_t blocks;      // blocks that get a part of them
+};
+__device__ __forceinline__ uint32_t part_begin(const Plan& l, uint32_t c) { return (uint32_t)((uint64_t)l.total * c / l.blocks); }
+__device__ __forceinline__ uint32_t part_of(const Plan& l, uint32_t t) { return (uint32_t)(((uint64_t)(t + 1) * l.blocks - 1) / l.total); }
+// From the last units' running sum of tiles.
+__device__ __forceinline__ Plan plan_rest(const PromptParams& p, const uint32_t* prefix, uint32_t longest) {
+    const uint32_t rest = (uint32_t)(p.units - p.whole), total = prefix[rest];
+    Plan l;
+    const bool cut = rest && (uint64_t)longest * p.blocks > total + (uint64_t)kWorth * p.blocks;
+    l.total = cut ? total : 0;
+    l.blocks = min((uint32_t)p.blocks, max(total, 1u));
+    return l;
+}
+template <int D, int N>
+struct Walk {
+    const PromptParams& p;
+    const PromptList<N>& list;
+    const uint32_t* prefix;
+    Plan plan;
+    int round;
+    uint32_t at, end;
+    __device__ __forceinline__ Walk(const PromptParams& p_, const PromptList<N>& l_, const uint32_t* x, const Plan& plan_)
+        : p(p_), list(l_), prefix(x), plan(plan_), round(0), at(0), end(0) {
+        if (plan.total && blockIdx.x < plan.blocks) {
+            at = part_begin(plan, blockIdx.x);
+            end = part_begin(plan, blockIdx.x + 1);
+        }
+    }
+    // The next piece: a unit, its tiles [t0, t1), and where its sums go (-1: to the output). False at the end.
+    __device__ __forceinline__ bool next(Unit& u, int& t0, int& t1, int& part) {
+        const int g = p.blocks, c = (int)blockIdx.x, rounds = p.whole / g;
+        part = -1;
+        if (round < rounds || (round == rounds && !plan.total && c < p.units - p.whole)) {
+            const int unit = round < rounds ? round * g + (round & 1 ? g - 1 - c : c) : p.whole + c;
+            ++round;
+            u = find_unit<D>(p, list, unit);
+            t0 = 0;
+            t1 = u.r.n;
+            return true;
+        }
+        if (at >= end) return false;
+        int lo = 0, hi = p.units - p.whole - 1;
+        while (lo < hi) {                // the last unit that begins at or before the tile: not one without tiles
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
+        }
+        u = find_unit<D>(p, list, p.whole + lo);
+        t0 = (int)(at - prefix[lo]);
+        t1 = (int)min((uint32_t)u.r.n, t0 + (end - at));
+        if (t0 > 0 || t1 < u.r.n) part = 2 * c + (t0 == 0 ? 1 : 0);
+        at += (uint32_t)(t1 - t0);
+        return true;
+    }
+};
 
 // Two fp32 values in one instruction.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -279,10 +334,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     uint64_t* turn = drain + 2;                           // [2] a tile's scores are issued (the first: and used)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int split = (int)blockIdx.x - p.whole;           // which part of the split units, from 0
-    const Unit u = find_unit<D>(p, list, split < 0 ? (int)blockIdx.x : p.whole + split / p.splits, split < 0 ? 0 : split % p.splits);
-    if (u.idle) return;
-    const int n = u.t1 - u.t0;
+    uint32_t* longest_slot = tmem_slot + 2;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);              // known to be the same in every lane
     constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + S::kIssuers;
@@ -309,25 +361,56 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
     }
+    const AttnParams& a = p.a;
+    const uint64_t limit = a.wait_limit_ns;
+    // the last units' tiles, summed up by the first warp
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(base + S::kPrefix);
+    const int rest = p.units - p.whole;
+    if (tid < rest) prefix[tid + 1] = (uint32_t)find_unit<D>(p, list, p.whole + tid).r.n;
+    if (tid == 0) prefix[0] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const AttnParams& a = p.a;
-    const uint64_t limit = a.wait_limit_ns;
+    uint32_t longest = 0;
+    if (warp == 0) {
+        uint32_t carry = 0;
+        for (int i0 = 0; i0 < rest; i0 += 32) {
+            uint32_t v = i0 + lane < rest ? prefix[i0 + lane + 1] : 0;
+            longest = max(longest, v);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += x;
+            }
+            if (i0 + lane < rest) prefix[i0 + lane + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) *longest_slot = longest;
+        if (blockIdx.x == 0) {           // for the join
+            for (int i = lane; i <= rest; i += 32) p.prefix[i] = prefix[i];
+            if (lane == 0) p.prefix[kPromptBlocks + 1] = longest;
+        }
+    }
+    __syncthreads();
+    const Plan plan = plan_rest(p, prefix, *longest_slot);
+    griddep_launch_dependents();
     const uint32_t q_smem = smem_addr(base), ring = q_smem + S::kRing;
     const uint32_t issuer = lane == 0 ? 1u : 0u;
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ producer
         const int gran = p.granule, per_tile = kTk / gran;
         const uint32_t box_bytes = (uint32_t)gran * 128;
-        const int32_t* table = a.c.table + u.seq * a.c.table_stride;
+        Unit u;
+        int t0, t1, part;
+        const int32_t* table = nullptr;
         // lane g < per_tile: the page and token of the tile's granule g; page -1: past the sequence
         auto place = [&](int t, int& page, int& tok) {
             page = -1;
             tok = 0;
-            if (t >= n || lane >= per_tile) return;
-            const int j = tile_token(u.r, u.t0 + t, kTk) + lane * gran;
+            if (t >= t1 || lane >= per_tile) return;
+            const int j = tile_token(u.r, t, kTk) + lane * gran;
             if (j >= u.len) return;
             const int pg = j / a.c.page_size;
             page = table[pg];
@@ -363,22 +446,28 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             return true;
         };
-        int page, tok, npage, ntok;
-        place(0, page, tok);
-        place(1, npage, ntok);
-        bool ok = n == 0 || load(false, page, tok);
-        for (int t = 0; t < n && ok; ++t) {
-            int fpage, ftok;
-            place(t + 2, fpage, ftok);
-            if (S::kS == 2 || S::kApart) {
-                ok = (t + 1 == n || load(false, npage, ntok)) && load(true, page, tok);
-            } else {
-                ok = load(true, page, tok) && (t + 1 == n || load(false, npage, ntok));
+        bool ok = true;
+        Walk<D, N> work(p, list, prefix, plan);
+        while (ok && work.next(u, t0, t1, part)) {
+            if (t0 == t1) continue;
+            table = a.c.table + u.seq * a.c.table_stride;
+            int page, tok, npage, ntok;
+            place(t0, page, tok);
+            place(t0 + 1, npage, ntok);
+            ok = load(false, page, tok);
+            for (int t = t0; t < t1 && ok; ++t) {
+                int fpage, ftok;
+                place(t + 2, fpage, ftok);
+                if (S::kS == 2 || S::kApart) {
+                    ok = (t + 1 == t1 || load(false, npage, ntok)) && load(true, page, tok);
+                } else {
+                    ok = load(true, page, tok) && (t + 1 == t1 || load(false, npage, ntok));
+                }
+                page = npage;
+                tok = ntok;
+                npage = fpage;
+                ntok = ftok;
             }
-            page = npage;
-            tok = ntok;
-            npage = fpage;
-            ntok = ftok;
         }
         if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
             for (int k = max(0, issued - S::kSlots); k < issued; ++k)
@@ -417,56 +506,52 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             for (int j = 0; j < S::kVTok / 16; ++j)
                 mma_ts(tmem + S::kO + (uint32_t)q * D, wp + j * 8, vp + (j * 2048 >> 4), idesc_o, add || (x | j) != 0, issuer);
         };
-        if (n > 0) {
-            wait_on(q_full, 0);
-            tc_fence_after();
+        // Pieces of the ring, tiles and units so far: the barriers' phases go by them.
+        int k0 = 0, tt = 0, units = 0;
+        Unit u;
+        int t0, t1, part;
+        Walk<D, N> work(p, list, prefix, plan);
+        while (ok && work.next(u, t0, t1, part)) {
+            const int n = t1 - t0;
+            if (n == 0) continue;
             if (S::kIssuers == 2) {
                 // The ring's order: K(0), then per tile K(t + 1), V(t): the weights lie apart from the scores, so
                 // the next scores need only the last ones read. The tiles of rows begin in turn, so that neither
                 // runs ahead and holds the ring's pieces.
-                auto begin = [&]() {
-                    if (lane == 0) mbar_arrive(smem_addr(&turn[me]));
-                    tc_fence_after();
-                };
-                auto do_scores = [&](int k) {
-                    scores(me, 0, k, 0);
-                    mma_commit_local<1>(smem_addr(&s_full[me]), issuer);
-                    release(k);
-                };
-                wait_piece(0);
-                if (me == 1) wait_on(&turn[0], 0);
-                if (ok) {
-                    begin();
-                    do_scores(0);
-                }
-                for (int t = 0; t < n && ok; ++t) {
+                wait_on(q_full, (uint32_t)units);
+                for (int t = -1; t < n && ok; ++t) {
                     const bool more = t + 1 < n;
                     if (more) {
-                        wait_on(&turn[1 - me], me == 0 ? t : t + 1);
-                        wait_on(&s_read[me], t);
-                        wait_piece(1 + 2 * t);
+                        const int next = tt + t + 1, k = k0 + (t < 0 ? 0 : 1 + 2 * t);
+                        if (me == 1 || next > 0) wait_on(&turn[1 - me], (uint32_t)(me == 0 ? next - 1 : next));
+                        if (next > 0) wait_on(&s_read[me], (uint32_t)(next - 1));
+                        wait_piece(k);
                         if (!ok) break;
-                        begin();
-                        do_scores(1 + 2 * t);
+                        if (lane == 0) mbar_arrive(smem_addr(&turn[me]));
+                        tc_fence_after();
+                        scores(me, 0, k, 0);
+                        mma_commit_local<1>(smem_addr(&s_full[me]), issuer);
+                        release(k);
                     }
-                    const int kv = 1 + 2 * t + (more ? 1 : 0);
-                    wait_on(&p_full[me], t);
-                    wait_piece(kv);
+                    if (t < 0) continue;
+                    const int k = k0 + 1 + 2 * t + (more ? 1 : 0);
+                    wait_on(&p_full[me], (uint32_t)(tt + t));
+                    wait_piece(k);
                     if (!ok) break;
                     tc_fence_after();
-                    values(me, 0, kv, 0, t > 0);
+                    values(me, 0, k, 0, t > 0);
                     mma_commit_local<1>(smem_addr(&pv_done[me]), issuer);
-                    release(kv);
+                    release(k);
                 }
             } else if (S::kQ == 2) {
                 // the ring's order: K(0), then per tile V(t), K(t + 1)
                 for (int t = -1; t < n && ok; ++t) {
-                    const int kv = 1 + 2 * t, ks = 2 + 2 * t;
+                    const int kv = k0 + 1 + 2 * t, ks = kv + 1;
 #pragma unroll
                     for (int q = 0; q < S::kQ; ++q) {
-                        // lane 0 the weights, and for both tiles at once 1 the piece of V, 2 that of K
-                        uint64_t* bar = t >= 0 ? &p_full[q] : &full[0];
-                        uint32_t ph = t >= 0 ? (uint32_t)t : 0;
+                        // lane 0 the weights (or the queries), and for both tiles at once 1 the piece of V, 2 that of K
+                        uint64_t* bar = t >= 0 ? &p_full[q] : q_full;
+                        uint32_t ph = t >= 0 ? (uint32_t)(tt + t) : (uint32_t)units;
                         if (q == 0 && t >= 0 && lane == 1) {
                             bar = &full[kv % S::kSlots];
                             ph = (uint32_t)(kv / S::kSlots);
@@ -492,52 +577,75 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     if (t + 1 < n) release(ks);
                 }
             } else {
+                // the ring's order: K(0), then per tile K(t + 1), V(t), two pieces each
+                wait_on(q_full, (uint32_t)units);
                 for (int t = -1; t < n && ok; ++t) {
                     if (t + 1 < n) {
-                        const int b = (t + 1) & 1, k0 = t < 0 ? 0 : S::kPieces * (2 * t + 1);
+                        const int b = (tt + t + 1) & 1, k = k0 + (t < 0 ? 0 : S::kPieces * (2 * t + 1));
 #pragma unroll
                         for (int x = 0; x < S::kPieces; ++x) {
-                            wait_piece(k0 + x);
+                            wait_piece(k + x);
                             if (!ok) break;
                             tc_fence_after();
-                            scores(0, b, k0 + x, x);
-                            release(k0 + x);
+                            scores(0, b, k + x, x);
+                            release(k + x);
                         }
                         if (!ok) break;
                         mma_commit_local<1>(smem_addr(&s_full[b]), issuer);
                     }
                     if (t < 0) continue;
-                    wait_on(&p_full[t & 1], t >> 1);
-                    const int k0 = S::kPieces * (2 * t + (t + 1 < n ? 2 : 1));
+                    const int b = (tt + t) & 1, k = k0 + S::kPieces * (2 * t + (t + 1 < n ? 2 : 1));
+                    wait_on(&p_full[b], (uint32_t)((tt + t) >> 1));
 #pragma unroll
                     for (int x = 0; x < S::kPieces; ++x) {
-                        wait_piece(k0 + x);
+                        wait_piece(k + x);
                         if (!ok) break;
                         tc_fence_after();
-                        values(0, t & 1, k0 + x, x, t > 0);
-                        release(k0 + x);
+                        values(0, b, k + x, x, t > 0);
+                        release(k + x);
                     }
-                    if (ok) mma_commit_local<1>(smem_addr(&pv_done[t & 1]), issuer);
+                    if (ok) mma_commit_local<1>(smem_addr(&pv_done[b]), issuer);
                 }
             }
-            // every product has ended before tensor memory is given back
-            mma_commit_local<1>(smem_addr(&drain[me]), issuer);
-            if (lane == 0) wait_bounded(smem_addr(&drain[me]), 0, abort_flag, a.status, limit, false);
-            __syncwarp();
+            k0 += 2 * S::kPieces * n;
+            tt += n;
+            ++units;
         }
+        // every product has ended before tensor memory is given back
+        mma_commit_local<1>(smem_addr(&drain[me]), issuer);
+        if (lane == 0) wait_bounded(smem_addr(&drain[me]), 0, abort_flag, a.status, limit, false);
+        __syncwarp();
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ softmax: two threads per row, 64 columns each
         const int q = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, g = p.group;
-        const int qi = row / g, hq = u.head * g + (row - qi * g), tok = u.tok0 + q * p.tile_tokens + qi;
-        const bool valid = qi < p.tile_tokens && tok < u.q_len;
-        const int pos = valid ? u.len - u.q_len + tok : -1;
+        const int qi = row / g, hg = row - qi * g;                       // this row's token of the tile, and query head of the group
         const int pair = 1 + q * 4 + (warp & 3);                         // named barrier of the two warps of these rows
         float* share = reinterpret_cast<float*>(base + S::kShare) + q * 128 + row;
         constexpr int kCols = kTk / 2, kOut = D / 2;                     // scores and features of this thread
         typedef __nv_bfloat16 bf;
-        // this tile's queries into shared memory, 128-byte swizzled rows in chunks of 64 features: each thread
-        // has one 16-byte column of every 2048 / D-th row, and its loads are in flight together
-        {
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);      // this warp's 32 lanes
+        const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * kOut;
+        const float scl = a.scale_log2;
+        Unit u{};
+        int t0, t1, part, tok, pos;
+        bool valid;
+        auto out_row = [&]() {
+            return static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + (u.head * g + hg) * a.o_head + half * kOut;
+        };
+        Walk<D, N> work(p, list, prefix, plan);
+        // the next piece that has tiles, with its queries in shared memory: 128-byte swizzled rows in chunks of
+        // 64 features; each thread has one 16-byte column of every 2048 / D-th row, its loads in flight together.
+        // Rows of a unit without tiles are zeros.
+        auto advance = [&]() -> bool {
+            while (true) {
+                if (!work.next(u, t0, t1, part)) return false;
+                tok = u.tok0 + q * p.tile_tokens + qi;
+                valid = qi < p.tile_tokens && tok < u.q_len;
+                pos = valid ? u.len - u.q_len + tok : -1;
+                if (t0 < t1) break;
+                if (valid)
+                    for (int c = 0; c < kOut / 8; ++c) reinterpret_cast<uint4*>(out_row())[c] = make_uint4(0, 0, 0, 0);
+            }
             constexpr int kStep = 2048 / D, kLoads = 128 / kStep;
             const int c = (half * 128 + row) % (D / 8), r0 = (half * 128 + row) / (D / 8);
             const bf* src = static_cast<const bf*>(a.q) + (long long)(u.row0 + u.tok0 + q * p.tile_tokens) * a.q_stride +
@@ -559,20 +667,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     *reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val[i];
                 }
             }
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(q_full));
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);      // this warp's 32 lanes
-        const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * kOut;
-        const float scl = a.scale_log2;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(q_full));
+            return true;
+        };
+        int tt = 0, k0 = 0;              // tiles and ring pieces so far
+        bool more = advance();
+        while (more) {
+        const int n = t1 - t0;
         float m = -INFINITY, l = 0.f;
         // After a wait that ran out the warps run on without data, so that their barriers stay matched; the
         // status word says that the output is incomplete.
         for (int t = 0; t < n; ++t) {
-            const int b = S::kS == 2 ? (t & 1) : 0;
-            const uint32_t par = S::kS == 2 ? (t >> 1) & 1 : t & 1;
-            const int j0 = tile_token(u.r, u.t0 + t, kTk);
+            const int ti = tt + t, b = S::kS == 2 ? ti & 1 : 0;
+            const uint32_t par = (uint32_t)(S::kS == 2 ? ti >> 1 : ti) & 1;
+            const int j0 = tile_token(u.r, t0 + t, kTk);
             wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
             tc_fence_after();
             const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
@@ -600,7 +710,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 const bool fix = grow && m != -INFINITY;
                 if (__any_sync(0xffffffffu, fix)) {
                     const float alpha = fix ? ex2((m - top) * scl) : 1.f;
-                    const int tp = t - 1, bp = S::kS == 2 ? tp & 1 : 0;
+                    const int tp = ti - 1, bp = S::kS == 2 ? tp & 1 : 0;
                     wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
                     tc_fence_after();
 #pragma unroll 1
@@ -624,7 +734,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 tc_fence_before();
                 if (lane == 0) mbar_arrive(smem_addr(&s_read[q]));
                 // the weights' place is free once the product before has ended
-                if (t > 0) wait_warp(smem_addr(&pv_done[q]), (t - 1) & 1, abort_flag, a.status, limit);
+                if (t > 0) wait_warp(smem_addr(&pv_done[q]), (uint32_t)(ti - 1) & 1, abort_flag, a.status, limit);
                 tc_fence_after();
             }
             l += sum;
@@ -633,10 +743,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (u.len - j0 < kTk) {
                 // places past the last token may hold anything: their weight is 0, so they must be finite
                 // (each tile of rows writes the same zeros before its own product)
-                const int k0 = S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t;   // the V pieces' place in the ring's order
+                const int k = k0 + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
                 for (int x = 0; x < S::kPieces; ++x) {
-                    const int s = (k0 + x) % S::kSlots;
-                    wait_warp(smem_addr(&full[s]), (uint32_t)((k0 + x) / S::kSlots) & 1, abort_flag, a.status, limit);
+                    const int s = (k + x) % S::kSlots;
+                    wait_warp(smem_addr(&full[s]), (uint32_t)((k + x) / S::kSlots) & 1, abort_flag, a.status, limit);
                     const int from = max(0, u.len - j0 - x * S::kVTok);
                     for (int e = from * (D / 8) + half * 128 + row; e < S::kVTok * (D / 8); e += 256) {
                         const int tk = e / (D / 8), c = e % (D / 8);
@@ -653,9 +763,18 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
         }
-        if (n > 0) {
-            const int tp = n - 1, bp = S::kS == 2 ? tp & 1 : 0;
-            wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
+        tt += n;
+        k0 += 2 * S::kPieces * n;
+        // The last scores are done, so the queries' place is free: the next ones go there before the output,
+        // and their scores are computed meanwhile. (Their weights, which the first product with V waits for,
+        // come after this thread has read O.)
+        const bool to_out = part < 0, store = valid;
+        bf* const out = out_row();
+        const long long at = ((long long)part * S::kQ + q) * 128 + row;
+        more = advance();
+        {
+            const int tp = tt - 1, bp = S::kS == 2 ? tp & 1 : 0;
+            wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (uint32_t)(S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
         }
         tc_fence_after();
         // the row's sum: its two threads' parts
@@ -665,22 +784,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         pair_any(pair, false);
         if (half) l = *share;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        bf* out = static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + hq * a.o_head + half * kOut;
-        const long long part = ((long long)split * S::kQ + q) * 128 + row;
-        if (u.parts > 1 && half == 0) p.part_ml[part] = make_float2(m * scl, l);
+        if (!to_out && half == 0) p.part_ml[at] = make_float2(m * scl, l);
 #pragma unroll 1
         for (int c = 0; c < kOut / 32; ++c) {
             uint32_t x[32];
-            if (n > 0) {
-                tmem_ld32(o_addr + c * 32, x);
-                tmem_ld_wait32(x);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = 0;
-            }
-            if (!valid) continue;
-            if (u.parts > 1) {
-                float4* d = reinterpret_cast<float4*>(p.part_o + part * D + half * kOut + c * 32);
+            tmem_ld32(o_addr + c * 32, x);
+            tmem_ld_wait32(x);
+            if (!store) continue;
+            if (!to_out) {
+                float4* d = reinterpret_cast<float4*>(p.part_o + at * D + half * kOut + c * 32);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     d[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
@@ -698,6 +810,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
         }
         tc_fence_before();
+        }
     }
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -706,41 +819,72 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
 }
 
-// Joins the parts of a unit's cache tiles: one warp per row.
+// Joins the parts of the cut units: four rows per block. Few parts: one warp per row; many: the warps
+// share out each row's parts and add up through shared memory. Also writes the zeros of cut units without
+// a tile.
 template <int D, int N>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
     using S = Shape<D>;
     constexpr int E = D / 32;
+    __shared__ float acc[4][D];
+    __shared__ float sums[4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = blockIdx.x / (S::kQ * 32), row = (blockIdx.x % (S::kQ * 32)) * 4 + warp;
-    const Unit u = find_unit<D>(p, list, p.whole + unit, 0);
-    if (u.parts == 1) return;            // its one block wrote it
-    const int q = row >> 7, r = row & 127, g = p.group, qi = r / g, tok = u.tok0 + q * p.tile_tokens + qi;
-    if (qi >= p.tile_tokens || tok >= u.q_len) return;
-    const long long at = ((long long)unit * p.splits * S::kQ + q) * 128 + r, step = S::kQ * 128;
-    float m = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_ml[at + s * step].x);
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 x = p.part_ml[at + s * step];
-        const float w = ex2(x.x - ms);
-        l = fmaf(x.y, w, l);
-        const float2* src = reinterpret_cast<const float2*>(p.part_o + (at + s * step) * D + lane * E);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-            const float2 v = src[e];
-            o[2 * e] = fmaf(v.x, w, o[2 * e]);
-            o[2 * e + 1] = fmaf(v.y, w, o[2 * e + 1]);
+    const int unit = blockIdx.x / (S::kQ * 32), row0 = (blockIdx.x % (S::kQ * 32)) * 4;
+    const int g = p.group;
+    const Unit u = find_unit<D>(p, list, p.whole + unit);
+    griddep_wait();
+    const Plan plan = plan_rest(p, p.prefix, p.prefix[kPromptBlocks + 1]);
+    if (plan.total == 0) return;
+    const uint32_t first = p.prefix[unit], n = p.prefix[unit + 1] - first;
+    const uint32_t c0 = n ? part_of(plan, first) : 0, c1 = n ? part_of(plan, first + n - 1) : 0;
+    if (n && c0 == c1) return;           // one block had the whole unit and wrote it
+    const bool shared = c1 - c0 >= 8;
+    for (int i = shared ? 0 : warp; i < (shared ? 4 : warp + 1); ++i) {
+        const int row = row0 + i, q = row >> 7, r = row & 127, qi = r / g, tok = u.tok0 + q * p.tile_tokens + qi;
+        if (qi >= p.tile_tokens || tok >= u.q_len) continue;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
+                             (u.head * g + (r - qi * g)) * p.a.o_head;
+        if (n == 0) {
+            for (int e = lane; e < D; e += 32) out[e] = __float2bfloat16_rn(0.f);
+            continue;
         }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
-                         (u.head * g + (r - qi * g)) * p.a.o_head + lane * E;
+        auto at = [&](uint32_t c) { return ((long long)(2 * c + (c == c0)) * S::kQ + q) * 128 + r; };
+        float m = -INFINITY;
+        for (uint32_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) reinterpret_cast<uint32_t*>(out)[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        const float ms = m == -INFINITY ? 0.f : m;
+        float l = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+        for (uint32_t c = c0 + (shared ? warp : 0); c <= c1; c += shared ? 4 : 1) {
+            const float2 x = p.part_ml[at(c)];
+            const float w = ex2(x.x - ms);
+            l = fmaf(x.y, w, l);
+            const float2* src = reinterpret_cast<const float2*>(p.part_o + at(c) * D + lane * E);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                const float2 v = src[e];
+                o[2 * e] = fmaf(v.x, w, o[2 * e]);
+                o[2 * e + 1] = fmaf(v.y, w, o[2 * e + 1]);
+            }
+        }
+        if (shared) {
+            __syncthreads();             // the row before has been read
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = o[e];
+            if (lane == 0) sums[warp] = l;
+            __syncthreads();
+            if (warp) continue;
+            l = sums[0] + sums[1] + sums[2] + sums[3];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = acc[0][lane * E + e] + acc[1][lane * E + e] + acc[2][lane * E + e] + acc[3][lane * E + e];
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) reinterpret_cast<uint32_t*>(out + lane * E)[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    }
 }
 
 template <int D, int N>
@@ -753,11 +897,19 @@ cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cud
         list.seq[i] = all.seq[i];
         list.unit0[i] = all.unit0[i];
     }
-    prompt_kernel<D, N><<<(unsigned)(p.whole + (p.units - p.whole) * p.splits), Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(p, list);
+    prompt_kernel<D, N><<<(unsigned)p.blocks, Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(p, list);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.whole == p.units) return e;
-    prompt_join_kernel<D, N><<<(unsigned)((p.units - p.whole) * Shape<D>::kQ * 32), 128, 0, stream>>>(p, list);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.units - p.whole) * Shape<D>::kQ * 32));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D, N>, p, list);
 }
 
 template <int D>

@@ -174,7 +174,6 @@ struct lora_attn {
     float* part_o = nullptr;            // sums of split units, their maxima and sums of weights
     float2* part_ml = nullptr;
     uint32_t* prefix = nullptr;
-    int max_parts = 0;                  // tiles of 128 rows that part_o has room for
 };
 
 namespace {
@@ -189,14 +188,12 @@ int set_up(lora_attn* h) {
         return LORA_ECUDA;
     h->encode = reinterpret_cast<EncodeTiledFn>(fn);
     if (decode_prepare_device() != cudaSuccess || prompt_prepare_device() != cudaSuccess) return LORA_ECUDA;
-    // decode: two parts a block of at most 64 rows (16 where two blocks share an SM). prompts: calls that
-    // leave SMs without a unit split the units' tiles, into at most four blocks per SM
-    h->max_parts = 4 * h->num_sms * prompt_tiles(h->dim);
-    const size_t parts = std::max(2 * (size_t)h->num_sms * kDecodeRows, (size_t)h->max_parts * kPromptTile);
+    // two parts a block: of at most 64 rows (16 where two decode blocks share an SM), or of a prompt unit's rows
+    const size_t parts = 2 * (size_t)h->num_sms * std::max(kDecodeRows, kPromptTile * prompt_tiles(h->dim));
     if (cudaMalloc(reinterpret_cast<void**>(&h->status), sizeof(int)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_o), parts * h->dim * sizeof(float)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_ml), parts * sizeof(float2)) != cudaSuccess ||
-        cudaMalloc(reinterpret_cast<void**>(&h->prefix), (h->max_seqs + 1) * sizeof(uint32_t)) != cudaSuccess)
+        cudaMalloc(reinterpret_cast<void**>(&h->prefix), (h->max_seqs + 1 + kPromptBlocks + 2) * sizeof(uint32_t)) != cudaSuccess)
         return LORA_ENOMEM;
     return cudaMemset(h->status, 0, sizeof(int)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }
@@ -231,7 +228,7 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.tile_tokens = kPromptTile / p.group;
     p.granule = 64;
     while (h->page_size % p.granule) p.granule /= 2;
-    const int tiles = prompt_tiles(h->dim), step = tiles * p.tile_tokens;
+    const int step = prompt_tiles(h->dim) * p.tile_tokens;
     long long units = 0;
     for (int i = 0; i < list.n; ++i) {
         list.unit0[i] = (int32_t)units;
@@ -239,19 +236,9 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
         if (units > 0x7fffffff / 8) return LORA_EUNSUPPORTED;
     }
     p.units = (int)units;
-    // the units past the last full wave of blocks run in as many parts as make that wave's end shortest; 4%
-    // of a unit for each part's sums
-    const long long rest = units % h->num_sms;
-    p.splits = 1;
-    double best = rest ? 1.0 : 0.0;
-    for (int s = 2; s <= 16 && rest * s * tiles <= h->max_parts; ++s) {
-        const double cost = (double)((rest * s + h->num_sms - 1) / h->num_sms) / s + 0.04 * s;
-        if (cost < best) {
-            best = cost;
-            p.splits = s;
-        }
-    }
-    p.whole = (int)(p.splits > 1 ? units - rest : units);
+    p.blocks = std::min(h->num_sms, kPromptBlocks);
+    p.whole = (int)(units / p.blocks * p.blocks);
+    p.prefix = h->prefix + h->max_seqs + 1;
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     if (!encode_cache(h->encode, &p.tm_k, &p.k_order, a.c, false, p.granule) ||

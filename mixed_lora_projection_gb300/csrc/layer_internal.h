@@ -98,6 +98,7 @@ constexpr int kSmemTwo = 115200;
 cudaError_t decode_prepare_device();
 cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, int mt, cudaStream_t stream);
 
+constexpr int kPromptBlocks = 152;      // most blocks of a launch, one per SM
 constexpr int kPromptTile = 128;        // the prompt kernel's tile of rows and of cache tokens
 
 // SeqList with the first unit of each sequence: a unit is one key/value head and the rows of
@@ -112,9 +113,10 @@ struct PromptParams {
     AttnParams a;
     int k_order, v_order, granule, group;
     int tile_tokens;                    // tokens of one tile of rows: 128 / group
-    int units, whole, splits;           // the units from `whole` on have their cache tiles in `splits` parts
-    float* part_o;                      // [split units x splits x tiles][128][dim]
+    int units, whole, blocks;           // units [0, whole) run whole, as many on each block
+    float* part_o;                      // [2 x blocks][tiles x 128][dim]: sums of units that parts end in
     float2* part_ml;
+    uint32_t* prefix;                   // [kPromptBlocks + 2]: tiles before each of the other units; the longest
 };
 int prompt_tiles(int dim);              // tiles of rows of a unit
 cudaError_t prompt_prepare_device();
