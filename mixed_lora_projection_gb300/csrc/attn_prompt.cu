@@ -46,9 +46,9 @@ struct Shape {
     static constexpr int kPStep = kApart ? 64 : 128;
     static constexpr int kRing = kQ * kQBytes;
     static constexpr int kBars = kRing + kSlots * kPiece;
-    static constexpr int kShare = kBars + 320;            // [kQ][128] floats between the two threads of a row
-    static constexpr int kPrefix = kShare + kQ * 512;     // [kPromptBlocks + 1] tiles before each of the last units
-    static constexpr int kSmem = kPrefix + (kPromptBlocks + 1) * 4 + 1024;
+    static constexpr int kPieceInfo = kBars + 320;        // [2] the pieces of work at hand
+    static constexpr int kShare = kPieceInfo + 128;       // [kQ][128] floats between the two threads of a row
+    static constexpr int kSmem = kShare + kQ * 512 + 1024;
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
@@ -146,11 +146,10 @@ __device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptLis
     return u;
 }
 
-// A block's work, which each of its warps walks through for itself. Whole units first, as many for each
-// block, every other round of them backwards (their lengths fall). Of the units that are left, less than
-// one a block, each goes to a block whole, or, where that would leave the blocks waiting for longer than
-// the join takes (kWorth tiles), all their tiles form one line that is cut into equal parts: a part may end
-// inside a unit, whose sums then go to the workspace.
+// The units are handed out one by one, those that see most first (a counter in global memory; which block
+// has a unit does not change its output). Of the last ones, fewer than one a block, all tiles form one line
+// that is cut into equal parts, one a block, where that saves more time than the join takes (kWorth tiles
+// a block): a part may end inside a unit, whose sums then go to the workspace.
 constexpr int kWorth = 8;
 struct Plan {
     uint32_t total;       // tiles of the last units, if they are cut (else 0)
@@ -158,56 +157,23 @@ struct Plan {
 };
 __device__ __forceinline__ uint32_t part_begin(const Plan& l, uint32_t c) { return (uint32_t)((uint64_t)l.total * c / l.blocks); }
 __device__ __forceinline__ uint32_t part_of(const Plan& l, uint32_t t) { return (uint32_t)(((uint64_t)(t + 1) * l.blocks - 1) / l.total); }
-// From the last units' running sum of tiles.
-__device__ __forceinline__ Plan plan_rest(const PromptParams& p, const uint32_t* prefix, uint32_t longest) {
-    const uint32_t rest = (uint32_t)(p.units - p.whole), total = prefix[rest];
+// From the last units' running sum of tiles and the longest of them, which stands behind the sums.
+__device__ __forceinline__ Plan plan_rest(const PromptParams& p, const uint32_t* prefix) {
+    const uint32_t rest = (uint32_t)(p.units - p.whole), total = prefix[rest], longest = prefix[rest + 1];
     Plan l;
     const bool cut = rest && (uint64_t)longest * p.blocks > total + (uint64_t)kWorth * p.blocks;
     l.total = cut ? total : 0;
     l.blocks = min((uint32_t)p.blocks, max(total, 1u));
     return l;
 }
-template <int D, int N>
-struct Walk {
-    const PromptParams& p;
-    const PromptList<N>& list;
-    const uint32_t* prefix;
-    Plan plan;
-    int round;
-    uint32_t at, end;
-    __device__ __forceinline__ Walk(const PromptParams& p_, const PromptList<N>& l_, const uint32_t* x, const Plan& plan_)
-        : p(p_), list(l_), prefix(x), plan(plan_), round(0), at(0), end(0) {
-        if (plan.total && blockIdx.x < plan.blocks) {
-            at = part_begin(plan, blockIdx.x);
-            end = part_begin(plan, blockIdx.x + 1);
-        }
-    }
-    // The next piece: a unit, its tiles [t0, t1), and where its sums go (-1: to the output). False at the end.
-    __device__ __forceinline__ bool next(Unit& u, int& t0, int& t1, int& part) {
-        const int g = p.blocks, c = (int)blockIdx.x, rounds = p.whole / g;
-        part = -1;
-        if (round < rounds || (round == rounds && !plan.total && c < p.units - p.whole)) {
-            const int unit = round < rounds ? round * g + (round & 1 ? g - 1 - c : c) : p.whole + c;
-            ++round;
-            u = find_unit<D>(p, list, unit);
-            t0 = 0;
-            t1 = u.r.n;
-            return true;
-        }
-        if (at >= end) return false;
-        int lo = 0, hi = p.units - p.whole - 1;
-        while (lo < hi) {                // the last unit that begins at or before the tile: not one without tiles
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
-        }
-        u = find_unit<D>(p, list, p.whole + lo);
-        t0 = (int)(at - prefix[lo]);
-        t1 = (int)min((uint32_t)u.r.n, t0 + (end - at));
-        if (t0 > 0 || t1 < u.r.n) part = 2 * c + (t0 == 0 ? 1 : 0);
-        at += (uint32_t)(t1 - t0);
-        return true;
-    }
+// A piece of work as the producer hands it to the other warps, through shared memory.
+struct Piece {
+    int head, tok0, q_len, row0, len, s_tiles, lo_tile;     // its unit
+    int t0, n;            // its tiles; n < 0: the end
+    int part;             // where its sums go in the workspace; -1: to the output
+    int pad[6];
 };
+static_assert(sizeof(Piece) == 64, "two pieces fill their place in shared memory");
 
 // Two fp32 values in one instruction.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -331,10 +297,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     uint64_t* s_read = pv_done + 2;                       // [kQ] scores are in registers (kApart)
     uint64_t* q_full = s_read + 2;
     uint64_t* drain = q_full + 1;                         // [2] an issuer's last product
-    uint64_t* turn = drain + 2;                           // [2] a tile's scores are issued (the first: and used)
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
+    uint64_t* turn = drain + 2;                           // [2] a tile's scores are issued
+    uint64_t* told = turn + 2;                            // [2] a piece of work is there
+    uint64_t* done = told + 2;                            // [2] and every warp has finished with it
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    uint32_t* longest_slot = tmem_slot + 2;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);              // known to be the same in every lane
     constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + S::kIssuers;
@@ -351,6 +318,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             mbar_init(smem_addr(&s_read[s]), 8);
             mbar_init(smem_addr(&drain[s]), 1);
             mbar_init(smem_addr(&turn[s]), 1);
+            mbar_init(smem_addr(&told[s]), 1);
+            mbar_init(smem_addr(&done[s]), S::kSoftmax / 32 + S::kIssuers);
         }
         mbar_init(smem_addr(q_full), S::kSoftmax / 32);
         *abort_flag = 0;
@@ -363,38 +332,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
     const AttnParams& a = p.a;
     const uint64_t limit = a.wait_limit_ns;
-    // the last units' tiles, summed up by the first warp
-    uint32_t* prefix = reinterpret_cast<uint32_t*>(base + S::kPrefix);
-    const int rest = p.units - p.whole;
-    if (tid < rest) prefix[tid + 1] = (uint32_t)find_unit<D>(p, list, p.whole + tid).r.n;
-    if (tid == 0) prefix[0] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    uint32_t longest = 0;
-    if (warp == 0) {
-        uint32_t carry = 0;
-        for (int i0 = 0; i0 < rest; i0 += 32) {
-            uint32_t v = i0 + lane < rest ? prefix[i0 + lane + 1] : 0;
-            longest = max(longest, v);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += x;
-            }
-            if (i0 + lane < rest) prefix[i0 + lane + 1] = carry + v;
-            carry += __shfl_sync(0xffffffffu, v, 31);
-        }
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        if (lane == 0) *longest_slot = longest;
-        if (blockIdx.x == 0) {           // for the join
-            for (int i = lane; i <= rest; i += 32) p.prefix[i] = prefix[i];
-            if (lane == 0) p.prefix[kPromptBlocks + 1] = longest;
-        }
-    }
-    __syncthreads();
-    const Plan plan = plan_rest(p, prefix, *longest_slot);
+    Piece* const pieces = reinterpret_cast<Piece*>(base + S::kPieceInfo);
     griddep_launch_dependents();
     const uint32_t q_smem = smem_addr(base), ring = q_smem + S::kRing;
     const uint32_t issuer = lane == 0 ? 1u : 0u;
@@ -402,14 +344,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         // ------------------------------------------------------------ producer
         const int gran = p.granule, per_tile = kTk / gran;
         const uint32_t box_bytes = (uint32_t)gran * 128;
-        Unit u;
-        int t0, t1, part;
+        Unit u{};
+        int t_end = 0;
         const int32_t* table = nullptr;
         // lane g < per_tile: the page and token of the tile's granule g; page -1: past the sequence
         auto place = [&](int t, int& page, int& tok) {
             page = -1;
             tok = 0;
-            if (t >= t1 || lane >= per_tile) return;
+            if (t >= t_end || lane >= per_tile) return;
             const int j = tile_token(u.r, t, kTk) + lane * gran;
             if (j >= u.len) return;
             const int pg = j / a.c.page_size;
@@ -446,10 +388,77 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             return true;
         };
+        // the last units' tiles: each block has its own sums, in global memory
+        const int rest = p.units - p.whole;
+        uint32_t* prefix = p.prefix + (size_t)blockIdx.x * (kPromptBlocks + 2);
+        {
+            uint32_t carry = 0, longest = 0;
+            if (lane == 0) prefix[0] = 0;
+            for (int i0 = 0; i0 < rest; i0 += 32) {
+                uint32_t v = i0 + lane < rest ? (uint32_t)find_unit<D>(p, list, p.whole + i0 + lane).r.n : 0;
+                longest = max(longest, v);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += x;
+                }
+                if (i0 + lane < rest) prefix[i0 + lane + 1] = carry + v;
+                carry += __shfl_sync(0xffffffffu, v, 31);
+            }
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            if (lane == 0) prefix[rest + 1] = longest;
+            __syncwarp();
+        }
+        const Plan plan = plan_rest(p, prefix);
+        const int whole = plan.total ? p.whole : p.units;     // units that are handed out
+        uint32_t at = 0, end = 0;                             // this block's part of the others' tiles
+        if (plan.total && blockIdx.x < plan.blocks) {
+            at = part_begin(plan, blockIdx.x);
+            end = part_begin(plan, blockIdx.x + 1);
+        }
         bool ok = true;
-        Walk<D, N> work(p, list, prefix, plan);
-        while (ok && work.next(u, t0, t1, part)) {
-            if (t0 == t1) continue;
+        int count = 0;                                        // pieces so far
+        int unit = (int)blockIdx.x;                           // the first ones go without the counter
+        while (ok) {
+            unit = __shfl_sync(0xffffffffu, unit, 0);
+            int t0 = 0, t1 = 0, part = -1;
+            const bool last = unit >= whole && at >= end;
+            if (unit < whole) {
+                u = find_unit<D>(p, list, unit);
+                t1 = u.r.n;
+                if (lane == 0) unit = p.blocks + atomicAdd(p.counter, 1);     // the next one, while this one loads
+            } else if (!last) {
+                int lo = 0, hi = rest - 1;
+                while (lo < hi) {        // the last unit that begins at or before the tile: not one without tiles
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
+                }
+                u = find_unit<D>(p, list, p.whole + lo);
+                t0 = (int)(at - prefix[lo]);
+                t1 = (int)min((uint32_t)u.r.n, t0 + (end - at));
+                if (t0 > 0 || t1 < u.r.n) part = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
+                at += (uint32_t)(t1 - t0);
+            }
+            ok = wait_warp(smem_addr(&done[count & 1]), (uint32_t)((count >> 1) & 1) ^ 1, abort_flag, a.status, limit);
+            if (lane == 0) {             // after a wait that ran out: the end, for the warps that still listen
+                Piece& w = pieces[count & 1];
+                w.head = u.head;
+                w.tok0 = u.tok0;
+                w.q_len = u.q_len;
+                w.row0 = u.row0;
+                w.len = u.len;
+                w.s_tiles = u.r.s_tiles;
+                w.lo_tile = u.r.lo_tile;
+                w.t0 = t0;
+                w.n = last || !ok ? -1 : t1 - t0;
+                w.part = part;
+                mbar_arrive(smem_addr(&told[count & 1]));
+            }
+            __syncwarp();
+            ++count;
+            if (last) break;
+            if (!ok || t0 == t1) continue;
+            t_end = t1;
             table = a.c.table + u.seq * a.c.table_stride;
             int page, tok, npage, ntok;
             place(t0, page, tok);
@@ -506,14 +515,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             for (int j = 0; j < S::kVTok / 16; ++j)
                 mma_ts(tmem + S::kO + (uint32_t)q * D, wp + j * 8, vp + (j * 2048 >> 4), idesc_o, add || (x | j) != 0, issuer);
         };
-        // Pieces of the ring, tiles and units so far: the barriers' phases go by them.
-        int k0 = 0, tt = 0, units = 0;
-        Unit u;
-        int t0, t1, part;
-        Walk<D, N> work(p, list, prefix, plan);
-        while (ok && work.next(u, t0, t1, part)) {
-            const int n = t1 - t0;
+        // Tiles and units so far: the barriers' phases and the ring's pieces go by them.
+        int tt = 0, units = 0;
+        for (int count = 0; ok; ++count) {
+            wait_on(&told[count & 1], (uint32_t)(count >> 1));
+            if (!ok) break;
+            const int n = pieces[count & 1].n;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&done[count & 1]));
+            if (n < 0) break;
             if (n == 0) continue;
+            const int k0 = 2 * S::kPieces * tt;
             if (S::kIssuers == 2) {
                 // The ring's order: K(0), then per tile K(t + 1), V(t): the weights lie apart from the scores, so
                 // the next scores need only the last ones read. The tiles of rows begin in turn, so that neither
@@ -607,7 +619,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     if (ok) mma_commit_local<1>(smem_addr(&pv_done[b]), issuer);
                 }
             }
-            k0 += 2 * S::kPieces * n;
             tt += n;
             ++units;
         }
@@ -617,35 +628,54 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         __syncwarp();
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ softmax: two threads per row, 64 columns each
-        const int q = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, g = p.group;
-        const int qi = row / g, hg = row - qi * g;                       // this row's token of the tile, and query head of the group
+        const int q = warp >> 3, half = (warp >> 2) & 1, g = p.group;
         const int pair = 1 + q * 4 + (warp & 3);                         // named barrier of the two warps of these rows
-        float* share = reinterpret_cast<float*>(base + S::kShare) + q * 128 + row;
+        float* share = reinterpret_cast<float*>(base + S::kShare) + (q * 128 + (tid & 127));
         constexpr int kCols = kTk / 2, kOut = D / 2;                     // scores and features of this thread
         typedef __nv_bfloat16 bf;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);      // this warp's 32 lanes
         const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * kOut;
         const float scl = a.scale_log2;
-        Unit u{};
-        int t0, t1, part, tok, pos;
-        bool valid;
-        auto out_row = [&]() {
+        // The piece at hand; what can be had from it again stays there, since a row's scores take most registers.
+        int count = -1, n = 0, pos = -1;
+        // This thread's row of the tile: its query head of the group, its token in the piece's sequence, and
+        // whether there is one. (`row` is hidden from the compiler, which would keep the quotient otherwise.)
+        auto row_of = [&](const Piece& u, int& tok, int& hg) {
+            int row = tid & 127;
+            asm volatile("" : "+r"(row));
+            const int qi = row / g;
+            hg = row - qi * g;
+            tok = u.tok0 + q * p.tile_tokens + qi;
+            return qi < p.tile_tokens && tok < u.q_len;
+        };
+        auto out_row = [&](const Piece& u, int tok, int hg) {
             return static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + (u.head * g + hg) * a.o_head + half * kOut;
         };
-        Walk<D, N> work(p, list, prefix, plan);
+        auto finish = [&](int c) {       // this warp needs piece c no more
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&done[c & 1]));
+        };
         // the next piece that has tiles, with its queries in shared memory: 128-byte swizzled rows in chunks of
         // 64 features; each thread has one 16-byte column of every 2048 / D-th row, its loads in flight together.
         // Rows of a unit without tiles are zeros.
         auto advance = [&]() -> bool {
             while (true) {
-                if (!work.next(u, t0, t1, part)) return false;
-                tok = u.tok0 + q * p.tile_tokens + qi;
-                valid = qi < p.tile_tokens && tok < u.q_len;
+                ++count;
+                const bool there = wait_warp(smem_addr(&told[count & 1]), (uint32_t)(count >> 1) & 1, abort_flag, a.status, limit);
+                if (pair_any(pair, !there)) return false;        // the two warps of a row end together
+                const Piece& u = pieces[count & 1];
+                n = u.n;
+                if (n < 0) return false;
+                int tok, hg;
+                const bool valid = row_of(u, tok, hg);
                 pos = valid ? u.len - u.q_len + tok : -1;
-                if (t0 < t1) break;
+                if (n > 0) break;
                 if (valid)
-                    for (int c = 0; c < kOut / 8; ++c) reinterpret_cast<uint4*>(out_row())[c] = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < kOut / 8; ++c) reinterpret_cast<uint4*>(out_row(u, tok, hg))[c] = make_uint4(0, 0, 0, 0);
+                finish(count);
             }
+            const Piece& u = pieces[count & 1];
+            const int row = tid & 127;
             constexpr int kStep = 2048 / D, kLoads = 128 / kStep;
             const int c = (half * 128 + row) % (D / 8), r0 = (half * 128 + row) / (D / 8);
             const bf* src = static_cast<const bf*>(a.q) + (long long)(u.row0 + u.tok0 + q * p.tile_tokens) * a.q_stride +
@@ -672,17 +702,18 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(smem_addr(q_full));
             return true;
         };
-        int tt = 0, k0 = 0;              // tiles and ring pieces so far
+        int tt = 0;                      // tiles so far
         bool more = advance();
         while (more) {
-        const int n = t1 - t0;
         float m = -INFINITY, l = 0.f;
         // After a wait that ran out the warps run on without data, so that their barriers stay matched; the
         // status word says that the output is incomplete.
         for (int t = 0; t < n; ++t) {
             const int ti = tt + t, b = S::kS == 2 ? ti & 1 : 0;
             const uint32_t par = (uint32_t)(S::kS == 2 ? ti >> 1 : ti) & 1;
-            const int j0 = tile_token(u.r, t0 + t, kTk);
+            const volatile Piece& u = pieces[count & 1];
+            const int at_tile = u.t0 + t, s_tiles = u.s_tiles, j0 = (at_tile < s_tiles ? at_tile : u.lo_tile + at_tile - s_tiles) * kTk;
+            const int tail = u.len - j0;                                 // tokens from the tile's first on
             wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
             tc_fence_after();
             const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
@@ -740,15 +771,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             l += sum;
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c) tmem_st16(p_addr + c * 16, v + c * 16);
-            if (u.len - j0 < kTk) {
+            if (tail < kTk) {
                 // places past the last token may hold anything: their weight is 0, so they must be finite
                 // (each tile of rows writes the same zeros before its own product)
-                const int k = k0 + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
+                const int k = 2 * S::kPieces * tt + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
                 for (int x = 0; x < S::kPieces; ++x) {
                     const int s = (k + x) % S::kSlots;
                     wait_warp(smem_addr(&full[s]), (uint32_t)((k + x) / S::kSlots) & 1, abort_flag, a.status, limit);
-                    const int from = max(0, u.len - j0 - x * S::kVTok);
-                    for (int e = from * (D / 8) + half * 128 + row; e < S::kVTok * (D / 8); e += 256) {
+                    const int from = max(0, tail - x * S::kVTok);
+                    for (int e = from * (D / 8) + half * 128 + (tid & 127); e < S::kVTok * (D / 8); e += 256) {
                         const int tk = e / (D / 8), c = e % (D / 8);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + (uint32_t)s * S::kPiece +
                                                                                     (c >> 3) * (S::kVTok * 128) + tk * 128 + (c & 7) * 16),
@@ -764,13 +795,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
         }
         tt += n;
-        k0 += 2 * S::kPieces * n;
         // The last scores are done, so the queries' place is free: the next ones go there before the output,
         // and their scores are computed meanwhile. (Their weights, which the first product with V waits for,
         // come after this thread has read O.)
-        const bool to_out = part < 0, store = valid;
-        bf* const out = out_row();
-        const long long at = ((long long)part * S::kQ + q) * 128 + row;
+        const int mine = count;
         more = advance();
         {
             const int tp = tt - 1, bp = S::kS == 2 ? tp & 1 : 0;
@@ -784,6 +812,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         pair_any(pair, false);
         if (half) l = *share;
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        const Piece& u = pieces[mine & 1];
+        int tok, hg;
+        const int part = u.part;
+        const bool store = row_of(u, tok, hg), to_out = part < 0;
+        bf* const out = out_row(u, tok, hg);
+        finish(mine);
+        const long long at = ((long long)part * S::kQ + q) * 128 + (tid & 127);
         if (!to_out && half == 0) p.part_ml[at] = make_float2(m * scl, l);
 #pragma unroll 1
         for (int c = 0; c < kOut / 32; ++c) {
@@ -817,6 +852,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc<1>(tmem, 512);
     }
+    // the last block to end leaves the counters as it found them
+    if (tid == 0 && atomicAdd(p.counter + 1, 1) == p.blocks - 1) {
+        p.counter[0] = 0;
+        p.counter[1] = 0;
+        __threadfence();
+    }
 }
 
 // Joins the parts of the cut units: four rows per block. Few parts: one warp per row; many: the warps
@@ -833,7 +874,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     const int g = p.group;
     const Unit u = find_unit<D>(p, list, p.whole + unit);
     griddep_wait();
-    const Plan plan = plan_rest(p, p.prefix, p.prefix[kPromptBlocks + 1]);
+    const Plan plan = plan_rest(p, p.prefix);         // the first block's sums, as every block's
     if (plan.total == 0) return;
     const uint32_t first = p.prefix[unit], n = p.prefix[unit + 1] - first;
     const uint32_t c0 = n ? part_of(plan, first) : 0, c1 = n ? part_of(plan, first + n - 1) : 0;

@@ -168,7 +168,7 @@ struct DeviceGuard {
 struct lora_attn {
     int device = 0, n_heads = 0, n_kv = 0, dim = 0, page_size = 0, max_tokens = 0, max_seqs = 0;
     int num_sms = 0;
-    int* status = nullptr;
+    int* status = nullptr;              // status word; then the prompt kernel's two counters
     unsigned long long wait_limit_ns = 4000000000ull;
     EncodeTiledFn encode = nullptr;
     float* part_o = nullptr;            // sums of split units, their maxima and sums of weights
@@ -190,12 +190,12 @@ int set_up(lora_attn* h) {
     if (decode_prepare_device() != cudaSuccess || prompt_prepare_device() != cudaSuccess) return LORA_ECUDA;
     // two parts a block: of at most 64 rows (16 where two decode blocks share an SM), or of a prompt unit's rows
     const size_t parts = 2 * (size_t)h->num_sms * std::max(kDecodeRows, kPromptTile * prompt_tiles(h->dim));
-    if (cudaMalloc(reinterpret_cast<void**>(&h->status), sizeof(int)) != cudaSuccess ||
+    if (cudaMalloc(reinterpret_cast<void**>(&h->status), 3 * sizeof(int)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_o), parts * h->dim * sizeof(float)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_ml), parts * sizeof(float2)) != cudaSuccess ||
-        cudaMalloc(reinterpret_cast<void**>(&h->prefix), (h->max_seqs + 1 + kPromptBlocks + 2) * sizeof(uint32_t)) != cudaSuccess)
+        cudaMalloc(reinterpret_cast<void**>(&h->prefix), (h->max_seqs + 1 + kPromptBlocks * (kPromptBlocks + 2)) * sizeof(uint32_t)) != cudaSuccess)
         return LORA_ENOMEM;
-    return cudaMemset(h->status, 0, sizeof(int)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+    return cudaMemset(h->status, 0, 3 * sizeof(int)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }
 
 // The decode kernel on the sequences of `list` (at most kDecodeRows rows per key/value head each).
@@ -239,6 +239,7 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.blocks = std::min(h->num_sms, kPromptBlocks);
     p.whole = (int)(units / p.blocks * p.blocks);
     p.prefix = h->prefix + h->max_seqs + 1;
+    p.counter = h->status + 1;
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     if (!encode_cache(h->encode, &p.tm_k, &p.k_order, a.c, false, p.granule) ||

@@ -113,10 +113,11 @@ struct PromptParams {
     AttnParams a;
     int k_order, v_order, granule, group;
     int tile_tokens;                    // tokens of one tile of rows: 128 / group
-    int units, whole, blocks;           // units [0, whole) run whole, as many on each block
+    int units, whole, blocks;           // units from `whole` on, fewer than blocks, may be cut in parts
     float* part_o;                      // [2 x blocks][tiles x 128][dim]: sums of units that parts end in
     float2* part_ml;
-    uint32_t* prefix;                   // [kPromptBlocks + 2]: tiles before each of the other units; the longest
+    uint32_t* prefix;                   // [blocks][kPromptBlocks + 2]: tiles before each of these; the longest
+    int* counter;                       // [2] units handed out past the first of each block; blocks that have ended
 };
 int prompt_tiles(int dim);              // tiles of rows of a unit
 cudaError_t prompt_prepare_device();
