@@ -138,7 +138,7 @@ int lora_linear_attn_create(lora_attn** out, int n_heads, int n_kv_heads, int he
  * The cache holds the new rows' keys and values already (lora_linear_kv_append). Values of
  * tokens at or past kv_lens are never used, whatever they hold; a NaN or infinity in a token's
  * value that one row of a sequence sees may also reach rows of that sequence that do not see it.
- * Sequences of at most 64 rows per key/value head (q_len * n_heads / n_kv_heads) and longer ones
+ * Sequences of at most 16 rows per key/value head (q_len * n_heads / n_kv_heads) and longer ones
  * run in different kernels of the same call; the sums' order depends on the batch, so results of
  * one row in two batches may differ in the last bit. The same call gives the same bits.
  * May be recorded by stream capture.

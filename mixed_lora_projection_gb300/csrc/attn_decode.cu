@@ -1,4 +1,4 @@
-// Attention of a few new rows per sequence over the paged cache (at most 64 rows per key/value head:
+// Attention of a few new rows per sequence over the paged cache (at most 16 rows per key/value head:
 // q_len x query heads per key/value head).
 //
 // The work is one pass over K and V, so it is bound by memory. All cache tiles of the call (64
@@ -9,11 +9,13 @@
 // unit's parts c in their order: M = max m_c, o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c.
 //
 // A block is four consumer warps and a TMA producer warp with a ring of K and V tiles. Per tile each
-// consumer computes the scores of 16 tokens (mma.sync m16n8k16: rows are padded to 16 MT), the warps
+// consumer computes the scores of 16 tokens (mma.sync m16n8k16: rows are padded to 16), the warps
 // exchange row maxima, write the weights to shared memory as bf16 (the product with V takes bf16
 // operands; their sum is kept of the unrounded fp32 weights) and each adds a quarter of the features
-// of the product with V. With at most 64 rows the matrix work is a fraction of the loads' time, so
-// the warp-level instruction serves; a tcgen05 tile would pad the rows to 128.
+// of the product with V. With 16 rows the matrix work is a fraction of the loads' time, so the
+// warp-level instruction serves, at two blocks per SM; more rows go to the prompt kernel, whose
+// tcgen05 tiles of 128 rows the warp-level instruction cannot follow (six sequences with 48 rows
+// per head of 256: 119 us here with three row tiles, where one pass over the cache takes 41).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -57,9 +59,9 @@ __device__ __forceinline__ unsigned part_of(unsigned long long w, unsigned g, un
 }
 
 // Shared memory: Q rows, weights, row maxima and sums, prefix, barriers, then the ring (1024-aligned).
-template <int D, int MT>
+template <int D>
 struct Layout {
-    static constexpr int kRows = 16 * MT;
+    static constexpr int kRows = kDecodeRows;
     static constexpr int kQStride = D + 8, kPStride = kTk + 8;   // padded rows: conflict-free ldmatrix
     static constexpr int kP = kRows * kQStride * 2;
     static constexpr int kMax = kP + kRows * kPStride * 2;
@@ -76,10 +78,10 @@ struct Walk {
     int i;               // sequence of the list
 };
 
-template <int D, int MT, int N>
-__global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
+template <int D, int N>
+__global__ void __launch_bounds__(kDecodeThreads, 2)
     decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ SeqList<N> list) {
-    using S = Layout<D, MT>;
+    using S = Layout<D>;
     constexpr int kRows = S::kRows;
     extern __shared__ __align__(1024) uint8_t raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
         const int s = list.seq[w.i], q_len = list.q_len[w.i], len = cache_len(a.c, s);
         const TileRange r = tile_range(len - q_len, len - 1, a.window, a.sinks, kTk);
         const int rows = q_len * g;
-        // this unit's queries
+        // this unit's queries: through shared memory into the fragments of the score products
         for (int v = tid; v < kRows * (D / 8); v += kConsumers) {
             const int row = v / (D / 8), c = v % (D / 8);
             uint4 val = make_uint4(0, 0, 0, 0);
@@ -244,56 +246,42 @@ __global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
             }
             *reinterpret_cast<uint4*>(raw + row * S::kQStride * 2 + c * 16) = val;
         }
-        int pos[MT][2];
-        float m[MT][2], l[MT][2];
-        float o[MT][D / 32][4];
+        int pos[2];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[D / 32][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int h = 0; h < 2; ++h) pos[h] = gr + 8 * h < rows ? r.first + (gr + 8 * h) / g : -1;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = mt * 16 + gr + 8 * h;
-                pos[mt][h] = row < rows ? r.first + row / g : -1;
-                m[mt][h] = -INFINITY;
-                l[mt][h] = 0.f;
-            }
+        for (int n = 0; n < D / 32; ++n)
 #pragma unroll
-            for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-        }
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
         consumer_sync();
+        uint32_t qf[D / 16][4];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            ldsm4(q_base + (uint32_t)((lane & 7) + ((lane >> 3) & 1) * 8) * (S::kQStride * 2) + (lane >> 4) * 16 + kk * 32, qf[kk]);
 
         for (int t = t0; t < t1; ++t) {
             const int j0 = tile_token(r, t, kTk);
-            // ---- scores of this warp's 16 tokens
-            constexpr int SP = MT == 1 ? 2 : 1;      // one row tile: two chains of products
-            float sc[SP][MT][2][4];
+            // ---- scores of this warp's 16 tokens, in two chains of products
+            float sc[2][2][4];
 #pragma unroll
-            for (int x = 0; x < SP; ++x)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[x][mt][n][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) sc[x][n][e] = 0.f;
             wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
             {
-                const uint32_t kt = ring + (uint32_t)slot * S::kSlot;
                 const int tok = warp * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
-                const uint32_t krow = kt + (uint32_t)tok * 128;
-                const uint32_t qrow = q_base + (uint32_t)((lane & 7) + ((lane >> 3) & 1) * 8) * (S::kQStride * 2) + (lane >> 4) * 16;
+                const uint32_t krow = ring + (uint32_t)slot * S::kSlot + (uint32_t)tok * 128;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     uint32_t b[4];
                     const int idx = (kk & 3) * 2 + ((lane >> 3) & 1);
                     ldsm4(krow + (kk >> 2) * (kTk * 128) + ((idx ^ (tok & 7)) << 4), b);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        uint32_t q4[4];
-                        ldsm4(qrow + mt * 16 * (S::kQStride * 2) + kk * 32, q4);
-                        mma16816(sc[kk % SP][mt][0], q4, b[0], b[1]);
-                        mma16816(sc[kk % SP][mt][1], q4, b[2], b[3]);
-                    }
+                    mma16816(sc[kk & 1][0], qf[kk], b[0], b[1]);
+                    mma16816(sc[kk & 1][1], qf[kk], b[2], b[3]);
                 }
             }
             const int kslot = slot;
@@ -301,65 +289,56 @@ __global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
                 slot = 0;
                 phase ^= 1;
             }
-            float mx[MT][2];
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                mx[mt][0] = mx[mt][1] = -INFINITY;
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + warp * 16 + n * 8 + gc * 2 + (e & 1), ps = pos[mt][e >> 1];
-                        float x = sc[0][mt][n][e];
-                        if (SP == 2) x += sc[SP - 1][mt][n][e];
-                        x *= a.scale_log2;
-                        const bool seen = j <= ps && (a.window == 0 || j > ps - a.window || j < a.sinks);
-                        x = seen ? x : -INFINITY;
-                        sc[0][mt][n][e] = x;
-                        mx[mt][e >> 1] = fmaxf(mx[mt][e >> 1], x);
-                    }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mx[mt][h] = fmaxf(mx[mt][h], __shfl_xor_sync(0xffffffffu, mx[mt][h], 1));
-                    mx[mt][h] = fmaxf(mx[mt][h], __shfl_xor_sync(0xffffffffu, mx[mt][h], 2));
-                    if (gc == 0) smax[warp * kRows + mt * 16 + gr + 8 * h] = mx[mt][h];
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + warp * 16 + n * 8 + gc * 2 + (e & 1), ps = pos[e >> 1];
+                    float x = (sc[0][n][e] + sc[1][n][e]) * a.scale_log2;
+                    const bool seen = j <= ps && (a.window == 0 || j > ps - a.window || j < a.sinks);
+                    x = seen ? x : -INFINITY;
+                    sc[0][n][e] = x;
+                    mx[e >> 1] = fmaxf(mx[e >> 1], x);
                 }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                if (gc == 0) smax[warp * kRows + gr + 8 * h] = mx[h];
             }
             consumer_sync();
             if (lane == 0) mbar_arrive(smem_addr(&empty[kslot]));
             // ---- weights
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int h = 0; h < 2; ++h) {
+                const int row = gr + 8 * h;
+                float mn = m[h];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = mt * 16 + gr + 8 * h;
-                    float mn = m[mt][h];
+                for (int x = 0; x < 4; ++x) mn = fmaxf(mn, smax[x * kRows + row]);
+                const float ms = mn == -INFINITY ? 0.f : mn;
+                const float alpha = ex2(m[h] - ms);
+                m[h] = mn;
+                float sum = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) mn = fmaxf(mn, smax[x * kRows + row]);
-                    const float ms = mn == -INFINITY ? 0.f : mn;
-                    const float alpha = ex2(m[mt][h] - ms);
-                    m[mt][h] = mn;
-                    float sum = 0.f;
+                for (int n = 0; n < 2; ++n) {
+                    const float w0 = ex2(sc[0][n][2 * h] - ms), w1 = ex2(sc[0][n][2 * h + 1] - ms);
+                    sum += w0 + w1;
+                    *reinterpret_cast<uint32_t*>(raw + S::kP + row * S::kPStride * 2 + (warp * 16 + n * 8 + gc * 2) * 2) =
+                        pack_bf16x2(w0, w1);
+                }
+                l[h] = l[h] * alpha + sum;
+                if (alpha != 1.f) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float w0 = ex2(sc[0][mt][n][2 * h] - ms), w1 = ex2(sc[0][mt][n][2 * h + 1] - ms);
-                        sum += w0 + w1;
-                        *reinterpret_cast<uint32_t*>(raw + S::kP + row * S::kPStride * 2 + (warp * 16 + n * 8 + gc * 2) * 2) =
-                            pack_bf16x2(w0, w1);
-                    }
-                    l[mt][h] = l[mt][h] * alpha + sum;
-                    if (alpha != 1.f) {
-#pragma unroll
-                        for (int n = 0; n < D / 32; ++n) {
-                            o[mt][n][2 * h] *= alpha;
-                            o[mt][n][2 * h + 1] *= alpha;
-                        }
+                    for (int n = 0; n < D / 32; ++n) {
+                        o[n][2 * h] *= alpha;
+                        o[n][2 * h + 1] *= alpha;
                     }
                 }
+            }
             wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
             const uint32_t vt = ring + (uint32_t)slot * S::kSlot;
-            const bool tail = r.len - j0 < kTk;
-            if (tail) {                  // places past the last token may hold anything: their weight is 0, so they must be finite
+            if (r.len - j0 < kTk) {      // places past the last token may hold anything: their weight is 0, so they must be finite
                 const int valid = r.len - j0;
                 for (int v = valid * (D / 8) + tid; v < kTk * (D / 8); v += kConsumers) {
                     const int tok = v / (D / 8), c = v % (D / 8);
@@ -376,20 +355,16 @@ __global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
                 const uint32_t prow = p_base + (uint32_t)tok * (S::kPStride * 2) + (lane >> 4) * 16;
 #pragma unroll
                 for (int kt = 0; kt < kTk / 16; ++kt) {
-                    uint32_t pa[MT][4];
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) ldsm4(prow + mt * 16 * (S::kPStride * 2) + kt * 32, pa[mt]);
+                    uint32_t pa[4];
+                    ldsm4(prow + kt * 32, pa);
                     const uint32_t vrow = vt + (uint32_t)(kt * 16 + tok) * 128;
 #pragma unroll
                     for (int np = 0; np < D / 64; ++np) {
                         uint32_t b[4];
                         const int dv = warp * (D / 32) + np * 2 + (lane >> 4);
                         ldsm4t(vrow + (dv >> 3) * (kTk * 128) + (((dv & 7) ^ (tok & 7)) << 4), b);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            mma16816(o[mt][2 * np], pa[mt], b[0], b[1]);
-                            mma16816(o[mt][2 * np + 1], pa[mt], b[2], b[3]);
-                        }
+                        mma16816(o[2 * np], pa, b[0], b[1]);
+                        mma16816(o[2 * np + 1], pa, b[2], b[3]);
                     }
                 }
             }
@@ -403,42 +378,37 @@ __global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
 
         // ---- the piece's end: the warps' sums of weights together
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x = l[mt][h];
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                if (gc == 0) ssum[warp * kRows + mt * 16 + gr + 8 * h] = x;
-            }
+        for (int h = 0; h < 2; ++h) {
+            float x = l[h];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            if (gc == 0) ssum[warp * kRows + gr + 8 * h] = x;
+        }
         consumer_sync();
         const bool whole = t0 == 0 && t1 == (int)nt;
         const long long part = 2ll * blockIdx.x + (t0 == 0 ? 1 : 0);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < 2; ++h) {
+            const int row = gr + 8 * h;
+            if (row >= rows) continue;
+            float sum = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = mt * 16 + gr + 8 * h;
-                if (row >= rows) continue;
-                float sum = 0.f;
+            for (int x = 0; x < 4; ++x) sum += ssum[x * kRows + row];
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int qi = row / g, hq = head * g + row - qi * g;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (list.row[w.i] + qi) * a.o_stride + hq * a.o_head +
+                                     warp * (D / 4) + gc * 2;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sum += ssum[x * kRows + row];
-                if (whole) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    const int qi = row / g, hq = head * g + row - qi * g;
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (list.row[w.i] + qi) * a.o_stride + hq * a.o_head +
-                                         warp * (D / 4) + gc * 2;
+                for (int n = 0; n < D / 32; ++n)
+                    *reinterpret_cast<uint32_t*>(out + n * 8) = pack_bf16x2(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
+            } else {
+                float* po = p.part_o + (part * kRows + row) * D + warp * (D / 4) + gc * 2;
 #pragma unroll
-                    for (int n = 0; n < D / 32; ++n)
-                        *reinterpret_cast<uint32_t*>(out + n * 8) = pack_bf16x2(o[mt][n][2 * h] * inv, o[mt][n][2 * h + 1] * inv);
-                } else {
-                    float* po = p.part_o + (part * kRows + row) * D + warp * (D / 4) + gc * 2;
-#pragma unroll
-                    for (int n = 0; n < D / 32; ++n)
-                        *reinterpret_cast<float2*>(po + n * 8) = make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
-                    if (warp == 0 && gc == 0) p.part_ml[part * kRows + row] = make_float2(m[mt][h], sum);
-                }
+                for (int n = 0; n < D / 32; ++n) *reinterpret_cast<float2*>(po + n * 8) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+                if (warp == 0 && gc == 0) p.part_ml[part * kRows + row] = make_float2(m[h], sum);
             }
+        }
         w.at += t1 - t0;
         if ((unsigned long long)prefix[w.i + 1] * n_kv <= w.at) ++w.i;
     }
@@ -446,9 +416,9 @@ __global__ void __launch_bounds__(kDecodeThreads, MT == 1 ? 2 : 1)
 
 // Joins the parts of split units: one block per row of a unit, its four warps take every fourth part.
 // Also writes the zeros of sequences without a visible token.
-template <int D, int MT, int N>
+template <int D, int N>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ SeqList<N> list) {
-    constexpr int kRows = 16 * MT, E = D / 32;
+    constexpr int kRows = kDecodeRows, E = D / 32;
     __shared__ float acc[4][D];
     __shared__ float2 ml[4];
     const int most = (int)gridDim.x / p.a.c.n_kv;    // rows of the longest sequence
@@ -501,7 +471,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
         out[e] = __float2bfloat16_rn((acc[0][e] + acc[1][e] + acc[2][e] + acc[3][e]) * inv);
 }
 
-template <int D, int MT, int N>
+template <int D, int N>
 cudaError_t launch_n(const DecodeParams& p, const SeqList<kMaxSeqs>& all, cudaStream_t stream) {
     SeqList<N> list;
     list.n = all.n;
@@ -512,8 +482,8 @@ cudaError_t launch_n(const DecodeParams& p, const SeqList<kMaxSeqs>& all, cudaSt
         list.seq[i] = all.seq[i];
         most = all.q_len[i] > most ? all.q_len[i] : most;
     }
-    const size_t smem = decode_smem(D, MT, p.slots, all.n);
-    decode_kernel<D, MT, N><<<p.grid, kDecodeThreads, smem, stream>>>(p, list);
+    const size_t smem = decode_smem(D, p.slots, all.n);
+    decode_kernel<D, N><<<p.grid, kDecodeThreads, smem, stream>>>(p, list);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -525,60 +495,38 @@ cudaError_t launch_n(const DecodeParams& p, const SeqList<kMaxSeqs>& all, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, MT, N>, p, list);
-}
-
-template <int D, int MT>
-cudaError_t launch_mt(const DecodeParams& p, const SeqList<kMaxSeqs>& l, cudaStream_t s) {
-    return l.n <= kSmallSeqs ? launch_n<D, MT, kSmallSeqs>(p, l, s) : launch_n<D, MT, kMaxSeqs>(p, l, s);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, N>, p, list);
 }
 
 template <int D>
-cudaError_t launch_d(const DecodeParams& p, const SeqList<kMaxSeqs>& l, int mt, cudaStream_t s) {
-    if (mt == 1) return launch_mt<D, 1>(p, l, s);
-    if (mt == 2) return launch_mt<D, 2>(p, l, s);
-    if (mt == 3) return launch_mt<D, 3>(p, l, s);
-    return launch_mt<D, 4>(p, l, s);
+cudaError_t launch_d(const DecodeParams& p, const SeqList<kMaxSeqs>& l, cudaStream_t s) {
+    return l.n <= kSmallSeqs ? launch_n<D, kSmallSeqs>(p, l, s) : launch_n<D, kMaxSeqs>(p, l, s);
 }
 
-template <int D, int MT>
+template <int D>
 cudaError_t opt_in() {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MT, kSmallSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - 1024);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(decode_kernel<D, MT, kMaxSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - 1024);
-}
-
-template <int D>
-cudaError_t opt_in_d() {
-    cudaError_t e = opt_in<D, 1>();
-    if (e == cudaSuccess) e = opt_in<D, 2>();
-    if (e == cudaSuccess) e = opt_in<D, 3>();
-    if (e == cudaSuccess) e = opt_in<D, 4>();
-    return e;
-}
-
-template <int D>
-size_t fixed_bytes(int mt) {
-    return mt == 1 ? Layout<D, 1>::kPrefix : mt == 2 ? Layout<D, 2>::kPrefix : mt == 3 ? Layout<D, 3>::kPrefix : Layout<D, 4>::kPrefix;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kSmallSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTwo);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(decode_kernel<D, kMaxSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTwo);
 }
 
 }  // namespace
 
-size_t decode_smem(int dim, int mt, int slots, int seqs) {
-    const size_t fixed = dim == 64 ? fixed_bytes<64>(mt) : dim == 128 ? fixed_bytes<128>(mt) : fixed_bytes<256>(mt);
+size_t decode_smem(int dim, int slots, int seqs) {
+    const size_t fixed = dim == 64 ? Layout<64>::kPrefix : dim == 128 ? Layout<128>::kPrefix : Layout<256>::kPrefix;
     return fixed + (size_t)(seqs + 1) * 4 + 1024 + (size_t)slots * kDecodeTile * dim * 2;
 }
 
 cudaError_t decode_prepare_device() {
-    cudaError_t e = opt_in_d<64>();
-    if (e == cudaSuccess) e = opt_in_d<128>();
-    if (e == cudaSuccess) e = opt_in_d<256>();
+    cudaError_t e = opt_in<64>();
+    if (e == cudaSuccess) e = opt_in<128>();
+    if (e == cudaSuccess) e = opt_in<256>();
     return e;
 }
 
-cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, int mt, cudaStream_t stream) {
-    if (p.a.c.dim == 64) return launch_d<64>(p, seqs, mt, stream);
-    if (p.a.c.dim == 128) return launch_d<128>(p, seqs, mt, stream);
-    return launch_d<256>(p, seqs, mt, stream);
+cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, cudaStream_t stream) {
+    if (p.a.c.dim == 64) return launch_d<64>(p, seqs, stream);
+    if (p.a.c.dim == 128) return launch_d<128>(p, seqs, stream);
+    return launch_d<256>(p, seqs, stream);
 }
 
 }  // namespace lora

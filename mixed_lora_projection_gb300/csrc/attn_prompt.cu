@@ -171,7 +171,8 @@ struct Piece {
     int head, tok0, q_len, row0, len, s_tiles, lo_tile;     // its unit
     int t0, n;            // its tiles; n < 0: the end
     int part;             // where its sums go in the workspace; -1: to the output
-    int pad[6];
+    int two;              // its rows reach into the second tile
+    int pad[5];
 };
 static_assert(sizeof(Piece) == 64, "two pieces fill their place in shared memory");
 
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     uint64_t* p_full = s_full + 2;                        // [kQ * kS] weights (and O corrected)
     uint64_t* pv_done = p_full + 2;                       // [kQ * kS] product with V
     uint64_t* s_read = pv_done + 2;                       // [kQ] scores are in registers (kApart)
-    uint64_t* q_full = s_read + 2;
-    uint64_t* drain = q_full + 1;                         // [2] an issuer's last product
+    uint64_t* q_full = s_read + 2;                        // [kQ] queries
+    uint64_t* drain = q_full + 2;                         // [2] an issuer's last product
     uint64_t* turn = drain + 2;                           // [2] a tile's scores are issued
     uint64_t* told = turn + 2;                            // [2] a piece of work is there
     uint64_t* done = told + 2;                            // [2] and every warp has finished with it
@@ -316,12 +317,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             mbar_init(smem_addr(&p_full[s]), 8);          // one arrival a warp
             mbar_init(smem_addr(&pv_done[s]), 1);
             mbar_init(smem_addr(&s_read[s]), 8);
+            mbar_init(smem_addr(&q_full[s]), 8);
             mbar_init(smem_addr(&drain[s]), 1);
             mbar_init(smem_addr(&turn[s]), 1);
             mbar_init(smem_addr(&told[s]), 1);
             mbar_init(smem_addr(&done[s]), S::kSoftmax / 32 + S::kIssuers);
         }
-        mbar_init(smem_addr(q_full), S::kSoftmax / 32);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 w.t0 = t0;
                 w.n = last || !ok ? -1 : t1 - t0;
                 w.part = part;
+                w.two = S::kIssuers == 2 || u.q_len - u.tok0 > p.tile_tokens;
                 mbar_arrive(smem_addr(&told[count & 1]));
             }
             __syncwarp();
@@ -516,11 +518,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 mma_ts(tmem + S::kO + (uint32_t)q * D, wp + j * 8, vp + (j * 2048 >> 4), idesc_o, add || (x | j) != 0, issuer);
         };
         // Tiles and units so far: the barriers' phases and the ring's pieces go by them.
-        int tt = 0, units = 0;
+        int tt = 0, units = 0, tt2 = 0, units2 = 0;               // the second tile has its own: it may be left out
         for (int count = 0; ok; ++count) {
             wait_on(&told[count & 1], (uint32_t)(count >> 1));
             if (!ok) break;
             const int n = pieces[count & 1].n;
+            const bool two = pieces[count & 1].two;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[count & 1]));
             if (n < 0) break;
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 // The ring's order: K(0), then per tile K(t + 1), V(t): the weights lie apart from the scores, so
                 // the next scores need only the last ones read. The tiles of rows begin in turn, so that neither
                 // runs ahead and holds the ring's pieces.
-                wait_on(q_full, (uint32_t)units);
+                wait_on(&q_full[me], (uint32_t)units);
                 for (int t = -1; t < n && ok; ++t) {
                     const bool more = t + 1 < n;
                     if (more) {
@@ -561,9 +564,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     const int kv = k0 + 1 + 2 * t, ks = kv + 1;
 #pragma unroll
                     for (int q = 0; q < S::kQ; ++q) {
+                        if (q == 1 && !two) continue;
                         // lane 0 the weights (or the queries), and for both tiles at once 1 the piece of V, 2 that of K
-                        uint64_t* bar = t >= 0 ? &p_full[q] : q_full;
-                        uint32_t ph = t >= 0 ? (uint32_t)(tt + t) : (uint32_t)units;
+                        uint64_t* bar = t >= 0 ? &p_full[q] : &q_full[q];
+                        uint32_t ph = (uint32_t)(t >= 0 ? (q ? tt2 : tt) + t : q ? units2 : units);
                         if (q == 0 && t >= 0 && lane == 1) {
                             bar = &full[kv % S::kSlots];
                             ph = (uint32_t)(kv / S::kSlots);
@@ -590,37 +594,43 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 }
             } else {
                 // the ring's order: K(0), then per tile K(t + 1), V(t), two pieces each
-                wait_on(q_full, (uint32_t)units);
                 for (int t = -1; t < n && ok; ++t) {
                     if (t + 1 < n) {
                         const int b = (tt + t + 1) & 1, k = k0 + (t < 0 ? 0 : S::kPieces * (2 * t + 1));
+                        // lanes 0 and 1 a piece of K each, 2 the queries
+                        const int kl = k + (lane & 1);
+                        const bool first = t < 0 && lane == 2;
+                        ok = wait_lanes(smem_addr(first ? q_full : &full[kl % S::kSlots]), (uint32_t)(first ? units : kl / S::kSlots) & 1,
+                                        abort_flag, a.status, limit);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
                         for (int x = 0; x < S::kPieces; ++x) {
-                            wait_piece(k + x);
-                            if (!ok) break;
-                            tc_fence_after();
                             scores(0, b, k + x, x);
                             release(k + x);
                         }
-                        if (!ok) break;
                         mma_commit_local<1>(smem_addr(&s_full[b]), issuer);
                     }
                     if (t < 0) continue;
                     const int b = (tt + t) & 1, k = k0 + S::kPieces * (2 * t + (t + 1 < n ? 2 : 1));
-                    wait_on(&p_full[b], (uint32_t)((tt + t) >> 1));
+                    // lanes 0 and 1 a piece of V each, 2 the weights
+                    const int kl = k + (lane & 1);
+                    ok = wait_lanes(smem_addr(lane == 2 ? &p_full[b] : &full[kl % S::kSlots]),
+                                    (uint32_t)(lane == 2 ? (tt + t) >> 1 : kl / S::kSlots) & 1, abort_flag, a.status, limit);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int x = 0; x < S::kPieces; ++x) {
-                        wait_piece(k + x);
-                        if (!ok) break;
-                        tc_fence_after();
                         values(0, b, k + x, x, t > 0);
                         release(k + x);
                     }
-                    if (ok) mma_commit_local<1>(smem_addr(&pv_done[b]), issuer);
+                    mma_commit_local<1>(smem_addr(&pv_done[b]), issuer);
                 }
             }
             tt += n;
             ++units;
+            tt2 += two ? n : 0;
+            units2 += two ? 1 : 0;
         }
         // every product has ended before tensor memory is given back
         mma_commit_local<1>(smem_addr(&drain[me]), issuer);
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * kOut;
         const float scl = a.scale_log2;
         // The piece at hand; what can be had from it again stays there, since a row's scores take most registers.
-        int count = -1, n = 0, pos = -1;
+        int count = -1, n = 0, pos = -1, all = 0;                        // all: tiles of the pieces before, for the ring's order
         // This thread's row of the tile: its query head of the group, its token in the piece's sequence, and
         // whether there is one. (`row` is hidden from the compiler, which would keep the quotient otherwise.)
         auto row_of = [&](const Piece& u, int& tok, int& hg) {
@@ -655,24 +665,30 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[c & 1]));
         };
-        // the next piece that has tiles, with its queries in shared memory: 128-byte swizzled rows in chunks of
-        // 64 features; each thread has one 16-byte column of every 2048 / D-th row, its loads in flight together.
-        // Rows of a unit without tiles are zeros.
-        auto advance = [&]() -> bool {
-            while (true) {
-                ++count;
-                const bool there = wait_warp(smem_addr(&told[count & 1]), (uint32_t)(count >> 1) & 1, abort_flag, a.status, limit);
-                if (pair_any(pair, !there)) return false;        // the two warps of a row end together
+        // The next piece: kReady with its queries in shared memory (128-byte swizzled rows in chunks of 64
+        // features; each thread has one 16-byte column of every 2048 / D-th row, its loads in flight together),
+        // kNone where it has nothing for this tile of rows (the rows of a unit without tiles are zeros), or kEnd.
+        // One piece at a time: the producer reuses a piece's place when every warp has finished with the one
+        // before the last.
+        enum { kReady, kNone, kEnd };
+        auto advance = [&]() -> int {
+            ++count;
+            const bool there = wait_warp(smem_addr(&told[count & 1]), (uint32_t)(count >> 1) & 1, abort_flag, a.status, limit);
+            if (pair_any(pair, !there)) return kEnd;             // the two warps of a row end together
+            n = pieces[count & 1].n;
+            if (n < 0) return kEnd;
+            {
                 const Piece& u = pieces[count & 1];
-                n = u.n;
-                if (n < 0) return false;
                 int tok, hg;
                 const bool valid = row_of(u, tok, hg);
                 pos = valid ? u.len - u.q_len + tok : -1;
-                if (n > 0) break;
-                if (valid)
-                    for (int c = 0; c < kOut / 8; ++c) reinterpret_cast<uint4*>(out_row(u, tok, hg))[c] = make_uint4(0, 0, 0, 0);
-                finish(count);
+                if (n == 0 || (q == 1 && !u.two)) {
+                    if (valid)
+                        for (int c = 0; c < kOut / 8; ++c) reinterpret_cast<uint4*>(out_row(u, tok, hg))[c] = make_uint4(0, 0, 0, 0);
+                    all += n;
+                    finish(count);
+                    return kNone;
+                }
             }
             const Piece& u = pieces[count & 1];
             const int row = tid & 127;
@@ -699,12 +715,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(q_full));
-            return true;
+            if (lane == 0) mbar_arrive(smem_addr(&q_full[q]));
+            return kReady;
         };
         int tt = 0;                      // tiles so far
-        bool more = advance();
-        while (more) {
+        int state;
+        while ((state = advance()) == kNone) {}
+        while (state == kReady) {
         float m = -INFINITY, l = 0.f;
         // After a wait that ran out the warps run on without data, so that their barriers stay matched; the
         // status word says that the output is incomplete.
@@ -774,7 +791,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (tail < kTk) {
                 // places past the last token may hold anything: their weight is 0, so they must be finite
                 // (each tile of rows writes the same zeros before its own product)
-                const int k = 2 * S::kPieces * tt + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
+                const int k = 2 * S::kPieces * all + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
                 for (int x = 0; x < S::kPieces; ++x) {
                     const int s = (k + x) % S::kSlots;
                     wait_warp(smem_addr(&full[s]), (uint32_t)((k + x) / S::kSlots) & 1, abort_flag, a.status, limit);
@@ -795,11 +812,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
         }
         tt += n;
+        all += n;
         // The last scores are done, so the queries' place is free: the next ones go there before the output,
         // and their scores are computed meanwhile. (Their weights, which the first product with V waits for,
         // come after this thread has read O.)
         const int mine = count;
-        more = advance();
+        state = advance();
         {
             const int tp = tt - 1, bp = S::kS == 2 ? tp & 1 : 0;
             wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (uint32_t)(S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
@@ -845,6 +863,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
         }
         tc_fence_before();
+        while (state == kNone) state = advance();
         }
     }
     __syncthreads();

@@ -188,8 +188,8 @@ int set_up(lora_attn* h) {
         return LORA_ECUDA;
     h->encode = reinterpret_cast<EncodeTiledFn>(fn);
     if (decode_prepare_device() != cudaSuccess || prompt_prepare_device() != cudaSuccess) return LORA_ECUDA;
-    // two parts a block: of at most 64 rows (16 where two decode blocks share an SM), or of a prompt unit's rows
-    const size_t parts = 2 * (size_t)h->num_sms * std::max(kDecodeRows, kPromptTile * prompt_tiles(h->dim));
+    // two parts a block: of 16 rows (two decode blocks share an SM), or of a prompt unit's rows
+    const size_t parts = 2 * (size_t)h->num_sms * std::max(2 * kDecodeRows, kPromptTile * prompt_tiles(h->dim));
     if (cudaMalloc(reinterpret_cast<void**>(&h->status), 3 * sizeof(int)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_o), parts * h->dim * sizeof(float)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_ml), parts * sizeof(float2)) != cudaSuccess ||
@@ -199,25 +199,22 @@ int set_up(lora_attn* h) {
 }
 
 // The decode kernel on the sequences of `list` (at most kDecodeRows rows per key/value head each).
-int run_decode(lora_attn* h, const AttnParams& a, const SeqList<kMaxSeqs>& list, int rows) {
+int run_decode(lora_attn* h, const AttnParams& a, const SeqList<kMaxSeqs>& list) {
     DecodeParams p;
     p.a = a;
     p.group = h->n_heads / h->n_kv;
     p.granule = kDecodeTile;                     // a power of two that divides the tile and the page
     while (h->page_size % p.granule) p.granule /= 2;
-    const int mt = (rows + 15) / 16;
-    // blocks share an SM in pairs where 16 rows leave each a ring worth having
-    const size_t most = mt == 1 ? kSmemTwo : 231424;
     p.slots = 16;
-    while (p.slots > 2 && decode_smem(h->dim, mt, p.slots, list.n) > most) --p.slots;
-    p.grid = h->num_sms * (mt == 1 ? 2 : 1);
+    while (p.slots > 2 && decode_smem(h->dim, p.slots, list.n) > kSmemTwo) --p.slots;
+    p.grid = 2 * h->num_sms;
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     p.prefix = h->prefix;
     if (!encode_cache(h->encode, &p.tm_k, &p.k_order, a.c, false, p.granule) ||
         !encode_cache(h->encode, &p.tm_v, &p.v_order, a.c, true, p.granule))
         return LORA_EINVAL;
-    return launch_decode(p, list, mt, a.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+    return launch_decode(p, list, a.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }
 
 // The prompt kernel on the sequences of `list`.
@@ -441,7 +438,6 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
     SeqList<kMaxSeqs> few;
     SeqList<kMaxSeqs> many;
     few.n = many.n = 0;
-    int most = 0;
     for (int i = 0; i < cache->n_seqs; ++i) {
         const int n = cache->q_offsets[i + 1] - cache->q_offsets[i];
         if (n == 0) continue;
@@ -449,7 +445,6 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
         l.seq[l.n] = (uint16_t)i;
         l.row[l.n] = cache->q_offsets[i];
         l.q_len[l.n++] = n;
-        if (&l == &few) most = std::max(most, n * g);
     }
     if (many.n) {
         // the sequences with most rows first: the last blocks of a launch had better be short
@@ -466,7 +461,7 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
         const int rc = run_prompts(h, p, sorted);
         if (rc != LORA_OK) return rc;
     }
-    return few.n ? run_decode(h, p, few, most) : LORA_OK;
+    return few.n ? run_decode(h, p, few) : LORA_OK;
 }
 
 extern "C" int lora_linear_attn_status(lora_attn* h, int reset) {

@@ -77,7 +77,7 @@ struct SeqList {
     uint16_t seq[N];
 };
 
-constexpr int kDecodeRows = 64;         // most rows per key/value head of a sequence in the decode kernel
+constexpr int kDecodeRows = 16;         // most rows per key/value head of a sequence in the decode kernel
 constexpr int kDecodeTile = 64;         // its cache tile, in tokens
 
 struct DecodeParams {
@@ -87,16 +87,15 @@ struct DecodeParams {
     int granule;                        // tokens of one load: divides the page size and the tile
     int group;                          // query heads per key/value head
     int slots;                          // ring slots of one tile of K or V
-    float* part_o;                      // [2 x grid][16 MT][dim]: unnormalised sums of split units
-    float2* part_ml;                    // [2 x grid][16 MT]: running maximum and sum
+    float* part_o;                      // [2 x grid][16][dim]: unnormalised sums of split units
+    float2* part_ml;                    // [2 x grid][16]: running maximum and sum
     uint32_t* prefix;                   // [n + 1]: tiles of one head before each sequence
     int grid;
 };
-size_t decode_smem(int dim, int mt, int slots, int seqs);
-// The most bytes of dynamic shared memory that lets `per_sm` blocks share an SM.
-constexpr int kSmemTwo = 115200;
+size_t decode_smem(int dim, int slots, int seqs);
+constexpr int kSmemTwo = 115200;        // the most dynamic shared memory that lets two blocks share an SM
 cudaError_t decode_prepare_device();
-cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, int mt, cudaStream_t stream);
+cudaError_t launch_decode(const DecodeParams& p, const SeqList<kMaxSeqs>& seqs, cudaStream_t stream);
 
 constexpr int kPromptBlocks = 152;      // most blocks of a launch, one per SM
 constexpr int kPromptTile = 128;        // the prompt kernel's tile of rows and of cache tokens

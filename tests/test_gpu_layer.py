@@ -254,6 +254,14 @@ def test_prompt(case):
     c.check()
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(64, 64, 64), (48, 48, 128), (32, 32, 256)])
+def test_many_units_with_and_without_tokens(heads, kv_heads, dim):
+    # several units a block; rows before the sequence's start see nothing, last tiles have few rows
+    c = Case([400, 129, 300, 20, 257], [30, 129, 300, 3, 700], heads, kv_heads, dim, 32, seed=dim)
+    c.poison()
+    c.check()
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (63, 4), (128, 0), (129, 128), (300, 150), (10 ** 6, 5)])
 @pytest.mark.parametrize("heads,kv_heads,dim", [(4, 4, 64), (12, 2, 128), (6, 3, 256)])
 def test_prompt_window(window, sinks, heads, kv_heads, dim):
