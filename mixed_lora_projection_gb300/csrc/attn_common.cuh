@@ -59,5 +59,51 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// One row of a split unit, by 128 threads: parts [0, n) with maximum and sum part_ml[at(c)] and
+// unnormalised sums part_o[at(c)][D]. The four warps take every fourth part in one pass (a part's sums are
+// loaded with its maximum, not after it), then add up; the order is the same in every run.
+template <int D, class At>
+__device__ __forceinline__ void join_row(const float* part_o, const float2* part_ml, int n, At at, __nv_bfloat16* out) {
+    constexpr int E = D / 32;
+    __shared__ float acc[4][D];
+    __shared__ float2 ml[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int c = warp; c < n; c += 4) {
+        const long long i = at(c);
+        const float2 x = part_ml[i];
+        float2 v[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) v[e] = *reinterpret_cast<const float2*>(part_o + i * D + lane * E + 2 * e);
+        const float mn = fmaxf(m, x.x), ms = mn == -INFINITY ? 0.f : mn, w = ex2(x.x - ms), old = ex2(m - ms);
+        m = mn;
+        l = l * old + x.y * w;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+            o[2 * e] = o[2 * e] * old + v[e].x * w;
+            o[2 * e + 1] = o[2 * e + 1] * old + v[e].y * w;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = o[e];
+    if (lane == 0) ml[warp] = make_float2(m, l);
+    __syncthreads();
+    m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    const float ms = m == -INFINITY ? 0.f : m;
+    float w[4];
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w[k] = ex2(ml[k].x - ms);
+        l += ml[k].y * w[k];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int e = threadIdx.x; e < D; e += 128)
+        out[e] = __float2bfloat16_rn((acc[0][e] * w[0] + acc[1][e] * w[1] + acc[2][e] * w[2] + acc[3][e] * w[3]) * inv);
+}
+
 }  // namespace dev
 }  // namespace lora

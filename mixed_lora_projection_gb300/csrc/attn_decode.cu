@@ -1,7 +1,7 @@
 // Attention of a few new rows per sequence over the paged cache (at most 16 rows per key/value head:
 // q_len x query heads per key/value head).
 //
-// The work is one pass over K and V, so it is bound by memory. All cache tiles of the call (64
+// The work is one pass over K and V, so it is bound by memory. All cache tiles of the call (64 or 128
 // tokens of one head), sequence after sequence and head after head, form one line that is cut into
 // equal parts, one per block: uneven lengths and few sequences fill the GPU alike. A block's part
 // may end inside a unit (one head of one sequence); what it has then, unnormalised sums o with their
@@ -9,7 +9,7 @@
 // unit's parts c in their order: M = max m_c, o = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c.
 //
 // A block is four consumer warps and a TMA producer warp with a ring of K and V tiles. Per tile each
-// consumer computes the scores of 16 tokens (mma.sync m16n8k16: rows are padded to 16), the warps
+// consumer computes the scores of a quarter of the tokens (mma.sync m16n8k16: rows are padded to 16), the warps
 // exchange row maxima, write the weights to shared memory as bf16 (the product with V takes bf16
 // operands; their sum is kept of the unrounded fp32 weights) and each adds a quarter of the features
 // of the product with V. With 16 rows the matrix work is a fraction of the loads' time, so the
@@ -27,7 +27,11 @@ namespace {
 
 using namespace dev;
 
-constexpr int kTk = kDecodeTile;
+// Tokens of a tile. A tile costs the consumers' chain of waits and products (~1.2 us) whatever it holds,
+// so heads of 64, whose tokens are few bytes, take twice as many (64 sequences of 700 to 7,000 tokens, 16
+// heads of 64: 260 us with 64 tokens, DUMMY with 128).
+template <int D>
+constexpr int kTile = D == 64 ? 128 : 64;
 constexpr int kConsumers = 128;
 constexpr int kDecodeThreads = 160;
 
@@ -61,14 +65,14 @@ __device__ __forceinline__ unsigned part_of(unsigned long long w, unsigned g, un
 // Shared memory: Q rows, weights, row maxima and sums, prefix, barriers, then the ring (1024-aligned).
 template <int D>
 struct Layout {
-    static constexpr int kRows = kDecodeRows;
+    static constexpr int kRows = kDecodeRows, kTk = kTile<D>;
     static constexpr int kQStride = D + 8, kPStride = kTk + 8;   // padded rows: conflict-free ldmatrix
     static constexpr int kP = kRows * kQStride * 2;
     static constexpr int kMax = kP + kRows * kPStride * 2;
     static constexpr int kSum = kMax + 4 * kRows * 4;
     static constexpr int kBars = kSum + 4 * kRows * 4;           // full[slots], empty[slots] (16 at most each)
     static constexpr int kAbort = kBars + 32 * 8;
-    static constexpr int kPrefix = kAbort + 16;
+    static constexpr int kPrefix = kAbort + 16;                  // tiles before each sequence, then the sequences' lengths
     static constexpr int kSlot = kTk * D * 2;
 };
 
@@ -82,14 +86,15 @@ template <int D, int N>
 __global__ void __launch_bounds__(kDecodeThreads, 2)
     decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ SeqList<N> list) {
     using S = Layout<D>;
-    constexpr int kRows = S::kRows;
+    constexpr int kRows = S::kRows, kTk = S::kTk, kOwn = kTk / 4;        // kOwn: tokens of a consumer warp
     extern __shared__ __align__(1024) uint8_t raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t* full = reinterpret_cast<uint64_t*>(raw + S::kBars);
     uint64_t* empty = full + 16;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(raw + S::kAbort);
     uint32_t* prefix = reinterpret_cast<uint32_t*>(raw + S::kPrefix);
-    const uint32_t ring = (smem_addr(raw + S::kPrefix + (list.n + 1) * 4) + 1023u) & ~1023u;
+    int* lens = reinterpret_cast<int*>(prefix + list.n + 1);
+    const uint32_t ring = (smem_addr(raw + S::kPrefix + (2 * list.n + 1) * 4) + 1023u) & ~1023u;
     const int slots = p.slots;
 
     if (tid == 0) {
@@ -105,7 +110,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     // tiles of one head before each sequence
     const AttnParams& a = p.a;
     for (int i = tid; i < list.n; i += kDecodeThreads) {
-        const int len = cache_len(a.c, list.seq[i]);
+        const int len = lens[i] = cache_len(a.c, list.seq[i]);
         prefix[i + 1] = (uint32_t)tile_range(len - list.q_len[i], len - 1, a.window, a.sinks, kTk).n;
     }
     __syncthreads();
@@ -126,11 +131,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     __syncthreads();
     const int n_kv = a.c.n_kv;
     const unsigned long long total = (unsigned long long)prefix[list.n] * n_kv;
-    const unsigned grid = (unsigned)min((unsigned long long)gridDim.x, total);
+    const unsigned grid = (unsigned)min((unsigned long long)gridDim.x, total);     // blocks that get a part
     if (blockIdx.x == 0)
         for (int i = tid; i <= list.n; i += kDecodeThreads) p.prefix[i] = prefix[i];
     griddep_launch_dependents();
-    if (blockIdx.x >= grid) return;      // no tile left (or none at all: the join writes the zeros)
+    // sequences without a visible token: zeros
+    for (int i = blockIdx.x; i < list.n; i += gridDim.x)
+        if (prefix[i + 1] == prefix[i]) {
+            const int per = n_kv * p.group * (D / 8);
+            for (int v = tid; v < list.q_len[i] * per; v += kDecodeThreads) {
+                const int row = list.row[i] + v / per, hq = v % per / (D / 8), c = v % (D / 8);
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * a.o_stride + hq * a.o_head + c * 8) =
+                    make_uint4(0, 0, 0, 0);
+            }
+        }
+    if (blockIdx.x >= grid) return;
     Walk w;
     w.at = part_begin(total, grid, blockIdx.x);
     w.end = part_begin(total, grid, blockIdx.x + 1);
@@ -161,7 +176,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             const unsigned long long rel = w.at - (unsigned long long)prefix[w.i] * n_kv;
             const int head = (int)(rel / nt), t0 = (int)(rel % nt);
             const int t1 = (int)min((unsigned long long)nt, t0 + (w.end - w.at));
-            const int s = list.seq[w.i], len = cache_len(a.c, s);
+            const int s = list.seq[w.i], len = lens[w.i];
             const TileRange r = tile_range(len - list.q_len[w.i], len - 1, a.window, a.sinks, kTk);
             const int32_t* table = a.c.table + s * a.c.table_stride;
             // this lane's granule of tile t: its page (one past the last: zeros) and token in it
@@ -232,7 +247,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         const unsigned long long rel = w.at - (unsigned long long)prefix[w.i] * n_kv;
         const int head = (int)(rel / nt), t0 = (int)(rel % nt);
         const int t1 = (int)min((unsigned long long)nt, t0 + (w.end - w.at));
-        const int s = list.seq[w.i], q_len = list.q_len[w.i], len = cache_len(a.c, s);
+        const int q_len = list.q_len[w.i], len = lens[w.i];
         const TileRange r = tile_range(len - q_len, len - 1, a.window, a.sinks, kTk);
         const int rows = q_len * g;
         // this unit's queries: through shared memory into the fragments of the score products
@@ -263,26 +278,28 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 
         for (int t = t0; t < t1; ++t) {
             const int j0 = tile_token(r, t, kTk);
-            // ---- scores of this warp's 16 tokens, in two chains of products
-            float sc[2][2][4];
+            // ---- scores of this warp's tokens, in two chains of products
+            float sc[2][kOwn / 8][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < kOwn / 8; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[x][n][e] = 0.f;
             wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
             {
-                const int tok = warp * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+                const int tok = warp * kOwn + (lane & 7) + ((lane >> 4) & 1) * 8;
                 const uint32_t krow = ring + (uint32_t)slot * S::kSlot + (uint32_t)tok * 128;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t b[4];
-                    const int idx = (kk & 3) * 2 + ((lane >> 3) & 1);
-                    ldsm4(krow + (kk >> 2) * (kTk * 128) + ((idx ^ (tok & 7)) << 4), b);
-                    mma16816(sc[kk & 1][0], qf[kk], b[0], b[1]);
-                    mma16816(sc[kk & 1][1], qf[kk], b[2], b[3]);
-                }
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int n = 0; n < kOwn / 16; ++n) {
+                        uint32_t b[4];
+                        const int idx = (kk & 3) * 2 + ((lane >> 3) & 1);
+                        ldsm4(krow + (kk >> 2) * (kTk * 128) + n * (16 * 128) + ((idx ^ (tok & 7)) << 4), b);
+                        mma16816(sc[kk & 1][2 * n], qf[kk], b[0], b[1]);
+                        mma16816(sc[kk & 1][2 * n + 1], qf[kk], b[2], b[3]);
+                    }
             }
             const int kslot = slot;
             if (++slot == slots) {
@@ -291,10 +308,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             }
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < kOwn / 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int j = j0 + warp * 16 + n * 8 + gc * 2 + (e & 1), ps = pos[e >> 1];
+                    const int j = j0 + warp * kOwn + n * 8 + gc * 2 + (e & 1), ps = pos[e >> 1];
                     float x = (sc[0][n][e] + sc[1][n][e]) * a.scale_log2;
                     const bool seen = j <= ps && (a.window == 0 || j > ps - a.window || j < a.sinks);
                     x = seen ? x : -INFINITY;
@@ -321,10 +338,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 m[h] = mn;
                 float sum = 0.f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < kOwn / 8; ++n) {
                     const float w0 = ex2(sc[0][n][2 * h] - ms), w1 = ex2(sc[0][n][2 * h + 1] - ms);
                     sum += w0 + w1;
-                    *reinterpret_cast<uint32_t*>(raw + S::kP + row * S::kPStride * 2 + (warp * 16 + n * 8 + gc * 2) * 2) =
+                    *reinterpret_cast<uint32_t*>(raw + S::kP + row * S::kPStride * 2 + (warp * kOwn + n * 8 + gc * 2) * 2) =
                         pack_bf16x2(w0, w1);
                 }
                 l[h] = l[h] * alpha + sum;
@@ -414,61 +431,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
 }
 
-// Joins the parts of split units: one block per row of a unit, its four warps take every fourth part.
-// Also writes the zeros of sequences without a visible token.
+// Joins the parts of split units: one block per row of a unit. (Joined by the block that ends last
+// instead, in the same launch, one chat's step took 12.3 us against 10.3: one block then reads what
+// four warps per row read at once.)
 template <int D, int N>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ SeqList<N> list) {
-    constexpr int kRows = kDecodeRows, E = D / 32;
-    __shared__ float acc[4][D];
-    __shared__ float2 ml[4];
     const int most = (int)gridDim.x / p.a.c.n_kv;    // rows of the longest sequence
     const int i = blockIdx.y, head = blockIdx.x / most, row = blockIdx.x % most, g = p.group;
     if (row >= list.q_len[i] * g) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_wait();
     const AttnParams& a = p.a;
     const uint32_t p0 = p.prefix[i], nt = p.prefix[i + 1] - p0;
+    if (nt == 0) return;                 // the first launch wrote its zeros
     const unsigned long long total = (unsigned long long)p.prefix[list.n] * a.c.n_kv;
     const unsigned grid = (unsigned)min((unsigned long long)p.grid, total);
-    const int qi = row / g, hq = head * g + row - qi * g;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (list.row[i] + qi) * a.o_stride + hq * a.o_head;
-    if (nt == 0) {
-        for (int e = threadIdx.x; e < D; e += 128) out[e] = __float2bfloat16_rn(0.f);
-        return;
-    }
     const unsigned long long first = (unsigned long long)p0 * a.c.n_kv + (unsigned long long)head * nt;
     const unsigned c0 = part_of(total, grid, first), c1 = part_of(total, grid, first + nt - 1);
     if (c0 == c1) return;                // one block had the whole unit and wrote it
-    float m = -INFINITY;
-    for (unsigned c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[(2ll * c + (c == c0)) * kRows + row].x);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const float ms = m == -INFINITY ? 0.f : m;
-    float o[E], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (unsigned c = c0 + warp; c <= c1; c += 4) {
-        const long long at = (2ll * c + (c == c0)) * kRows + row;
-        const float2 x = p.part_ml[at];
-        const float w = ex2(x.x - ms);
-        l = fmaf(x.y, w, l);
-        const float* src = p.part_o + at * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(src + e);
-            o[e] = fmaf(v.x, w, o[e]);
-            o[e + 1] = fmaf(v.y, w, o[e + 1]);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = o[e];
-    if (lane == 0) ml[warp].y = l;
-    __syncthreads();
-    l = ml[0].y + ml[1].y + ml[2].y + ml[3].y;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int e = threadIdx.x; e < D; e += 128)
-        out[e] = __float2bfloat16_rn((acc[0][e] + acc[1][e] + acc[2][e] + acc[3][e]) * inv);
+    const int qi = row / g, hq = head * g + row - qi * g;
+    join_row<D>(p.part_o, p.part_ml, (int)(c1 - c0 + 1), [=](int c) { return (2ll * (c0 + c) + (c == 0)) * kDecodeRows + row; },
+                static_cast<__nv_bfloat16*>(a.out) + (list.row[i] + qi) * a.o_stride + hq * a.o_head);
 }
 
 template <int D, int N>
@@ -513,7 +495,7 @@ cudaError_t opt_in() {
 
 size_t decode_smem(int dim, int slots, int seqs) {
     const size_t fixed = dim == 64 ? Layout<64>::kPrefix : dim == 128 ? Layout<128>::kPrefix : Layout<256>::kPrefix;
-    return fixed + (size_t)(seqs + 1) * 4 + 1024 + (size_t)slots * kDecodeTile * dim * 2;
+    return fixed + (size_t)(2 * seqs + 1) * 4 + 1024 + (size_t)slots * (dim == 64 ? kTile<64> : kTile<128>) * dim * 2;
 }
 
 cudaError_t decode_prepare_device() {

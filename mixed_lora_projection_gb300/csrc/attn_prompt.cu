@@ -157,11 +157,10 @@ struct Plan {
 };
 __device__ __forceinline__ uint32_t part_begin(const Plan& l, uint32_t c) { return (uint32_t)((uint64_t)l.total * c / l.blocks); }
 __device__ __forceinline__ uint32_t part_of(const Plan& l, uint32_t t) { return (uint32_t)(((uint64_t)(t + 1) * l.blocks - 1) / l.total); }
-// From the last units' running sum of tiles and the longest of them, which stands behind the sums.
-__device__ __forceinline__ Plan plan_rest(const PromptParams& p, const uint32_t* prefix) {
-    const uint32_t rest = (uint32_t)(p.units - p.whole), total = prefix[rest], longest = prefix[rest + 1];
+// From the last units' tiles and the longest of them.
+__device__ __forceinline__ Plan plan_rest(const PromptParams& p, uint32_t total, uint32_t longest) {
     Plan l;
-    const bool cut = rest && (uint64_t)longest * p.blocks > total + (uint64_t)kWorth * p.blocks;
+    const bool cut = (uint64_t)longest * p.blocks > total + (uint64_t)kWorth * p.blocks;
     l.total = cut ? total : 0;
     l.blocks = min((uint32_t)p.blocks, max(total, 1u));
     return l;
@@ -389,28 +388,37 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             return true;
         };
-        // the last units' tiles: each block has its own sums, in global memory
+        // the last units' tiles: lane l has the sums before units l, l + 32, ... of them
+        constexpr int kSums = (kPromptBlocks + 31) / 32;
         const int rest = p.units - p.whole;
-        uint32_t* prefix = p.prefix + (size_t)blockIdx.x * (kPromptBlocks + 2);
+        uint32_t before[kSums];
+        Plan plan;
         {
             uint32_t carry = 0, longest = 0;
-            if (lane == 0) prefix[0] = 0;
-            for (int i0 = 0; i0 < rest; i0 += 32) {
-                uint32_t v = i0 + lane < rest ? (uint32_t)find_unit<D>(p, list, p.whole + i0 + lane).r.n : 0;
-                longest = max(longest, v);
+#pragma unroll
+            for (int k = 0; k < kSums; ++k) {
+                const int i = k * 32 + lane;
+                before[k] = 0;
+                if (k * 32 >= rest) continue;
+                const uint32_t n = i < rest ? (uint32_t)find_unit<D>(p, list, p.whole + i).r.n : 0;
+                uint32_t v = n;
+                longest = max(longest, n);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
                     if (lane >= o) v += x;
                 }
-                if (i0 + lane < rest) prefix[i0 + lane + 1] = carry + v;
+                before[k] = carry + v - n;
                 carry += __shfl_sync(0xffffffffu, v, 31);
+                if (blockIdx.x == 0 && i < rest) p.prefix[i] = before[k];     // for the join
             }
             longest = __reduce_max_sync(0xffffffffu, longest);
-            if (lane == 0) prefix[rest + 1] = longest;
-            __syncwarp();
+            if (blockIdx.x == 0 && lane == 0) {
+                p.prefix[rest] = carry;
+                p.prefix[rest + 1] = longest;
+            }
+            plan = plan_rest(p, carry, longest);
         }
-        const Plan plan = plan_rest(p, prefix);
         const int whole = plan.total ? p.whole : p.units;     // units that are handed out
         uint32_t at = 0, end = 0;                             // this block's part of the others' tiles
         if (plan.total && blockIdx.x < plan.blocks) {
@@ -429,13 +437,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 t1 = u.r.n;
                 if (lane == 0) unit = p.blocks + atomicAdd(p.counter, 1);     // the next one, while this one loads
             } else if (!last) {
-                int lo = 0, hi = rest - 1;
-                while (lo < hi) {        // the last unit that begins at or before the tile: not one without tiles
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (prefix[mid] <= at) lo = mid; else hi = mid - 1;
+                // the last unit that begins at or before the tile: not one without tiles
+                int lo = -1;
+                uint32_t from = 0;
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) {
+                    const uint32_t here = __ballot_sync(0xffffffffu, k * 32 + lane < rest && before[k] <= at);
+                    const uint32_t x = __shfl_sync(0xffffffffu, before[k], here ? 31 - __clz(here) : 0);
+                    if (here) {
+                        lo = k * 32 + 31 - __clz(here);
+                        from = x;
+                    }
                 }
                 u = find_unit<D>(p, list, p.whole + lo);
-                t0 = (int)(at - prefix[lo]);
+                t0 = (int)(at - from);
                 t1 = (int)min((uint32_t)u.r.n, t0 + (end - at));
                 if (t0 > 0 || t1 < u.r.n) part = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
                 at += (uint32_t)(t1 - t0);
@@ -879,72 +894,28 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
 }
 
-// Joins the parts of the cut units: four rows per block. Few parts: one warp per row; many: the warps
-// share out each row's parts and add up through shared memory. Also writes the zeros of cut units without
-// a tile.
+// Joins the parts of the cut units: one block per row. Also writes the zeros of cut units without a tile.
 template <int D, int N>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
     using S = Shape<D>;
-    constexpr int E = D / 32;
-    __shared__ float acc[4][D];
-    __shared__ float sums[4];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = blockIdx.x / (S::kQ * 32), row0 = (blockIdx.x % (S::kQ * 32)) * 4;
-    const int g = p.group;
+    const int rest = p.units - p.whole, rows = (int)gridDim.x / rest, unit = blockIdx.x / rows, row = blockIdx.x - unit * rows;
     const Unit u = find_unit<D>(p, list, p.whole + unit);
+    const int g = p.group, q = row >> 7, r = row & 127, qi = r / g, tok = u.tok0 + q * p.tile_tokens + qi;
+    if (qi >= p.tile_tokens || tok >= u.q_len) return;
     griddep_wait();
-    const Plan plan = plan_rest(p, p.prefix);         // the first block's sums, as every block's
+    const Plan plan = plan_rest(p, p.prefix[rest], p.prefix[rest + 1]);
     if (plan.total == 0) return;
     const uint32_t first = p.prefix[unit], n = p.prefix[unit + 1] - first;
-    const uint32_t c0 = n ? part_of(plan, first) : 0, c1 = n ? part_of(plan, first + n - 1) : 0;
-    if (n && c0 == c1) return;           // one block had the whole unit and wrote it
-    const bool shared = c1 - c0 >= 8;
-    for (int i = shared ? 0 : warp; i < (shared ? 4 : warp + 1); ++i) {
-        const int row = row0 + i, q = row >> 7, r = row & 127, qi = r / g, tok = u.tok0 + q * p.tile_tokens + qi;
-        if (qi >= p.tile_tokens || tok >= u.q_len) continue;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
-                             (u.head * g + (r - qi * g)) * p.a.o_head;
-        if (n == 0) {
-            for (int e = lane; e < D; e += 32) out[e] = __float2bfloat16_rn(0.f);
-            continue;
-        }
-        auto at = [&](uint32_t c) { return ((long long)(2 * c + (c == c0)) * S::kQ + q) * 128 + r; };
-        float m = -INFINITY;
-        for (uint32_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        const float ms = m == -INFINITY ? 0.f : m;
-        float l = 0.f, o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-        for (uint32_t c = c0 + (shared ? warp : 0); c <= c1; c += shared ? 4 : 1) {
-            const float2 x = p.part_ml[at(c)];
-            const float w = ex2(x.x - ms);
-            l = fmaf(x.y, w, l);
-            const float2* src = reinterpret_cast<const float2*>(p.part_o + at(c) * D + lane * E);
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-                const float2 v = src[e];
-                o[2 * e] = fmaf(v.x, w, o[2 * e]);
-                o[2 * e + 1] = fmaf(v.y, w, o[2 * e + 1]);
-            }
-        }
-        if (shared) {
-            __syncthreads();             // the row before has been read
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = o[e];
-            if (lane == 0) sums[warp] = l;
-            __syncthreads();
-            if (warp) continue;
-            l = sums[0] + sums[1] + sums[2] + sums[3];
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = acc[0][lane * E + e] + acc[1][lane * E + e] + acc[2][lane * E + e] + acc[3][lane * E + e];
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) reinterpret_cast<uint32_t*>(out + lane * E)[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
+                         (u.head * g + (r - qi * g)) * p.a.o_head;
+    if (n == 0) {
+        for (int e = threadIdx.x; e < D; e += 128) out[e] = __float2bfloat16_rn(0.f);
+        return;
     }
+    const uint32_t c0 = part_of(plan, first), c1 = part_of(plan, first + n - 1);
+    if (c0 == c1) return;                // one block had the whole unit and wrote it
+    join_row<D>(p.part_o, p.part_ml, (int)(c1 - c0 + 1),
+                [=](int c) { return ((2ll * (c0 + c) + (c == 0)) * S::kQ + q) * 128 + r; }, out);
 }
 
 template <int D, int N>
@@ -961,7 +932,11 @@ cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cud
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.whole == p.units) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.units - p.whole) * Shape<D>::kQ * 32));
+    // rows that a unit may have: those of the longest sequence where they fit the first tile, else all
+    int most = 0;
+    for (int i = 0; i < all.n; ++i) most = all.q_len[i] > most ? all.q_len[i] : most;
+    const int rows = most <= p.tile_tokens ? most * p.group : Shape<D>::kQ * 128;
+    cfg.gridDim = dim3((unsigned)((p.units - p.whole) * rows));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -146,7 +146,9 @@ bool encode_cache(EncodeTiledFn encode, CUtensorMap* m, int* order, const CacheV
     cuuint32_t step[4] = {1, 1, 1, 1};
     *order = ax[0].what | ax[1].what << 2 | ax[2].what << 4;
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v ? c.v : c.k, dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  // a head of 64 is 128 bytes of a token: wider fetches would bring in its neighbour
+                  c.dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -173,7 +175,7 @@ struct lora_attn {
     EncodeTiledFn encode = nullptr;
     float* part_o = nullptr;            // sums of split units, their maxima and sums of weights
     float2* part_ml = nullptr;
-    uint32_t* prefix = nullptr;
+    uint32_t* prefix = nullptr;         // sums of tiles: the decode kernel's, then the prompt kernel's
 };
 
 namespace {
@@ -193,7 +195,7 @@ int set_up(lora_attn* h) {
     if (cudaMalloc(reinterpret_cast<void**>(&h->status), 3 * sizeof(int)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_o), parts * h->dim * sizeof(float)) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&h->part_ml), parts * sizeof(float2)) != cudaSuccess ||
-        cudaMalloc(reinterpret_cast<void**>(&h->prefix), (h->max_seqs + 1 + kPromptBlocks * (kPromptBlocks + 2)) * sizeof(uint32_t)) != cudaSuccess)
+        cudaMalloc(reinterpret_cast<void**>(&h->prefix), (h->max_seqs + 1 + kPromptBlocks + 2) * sizeof(uint32_t)) != cudaSuccess)
         return LORA_ENOMEM;
     return cudaMemset(h->status, 0, 3 * sizeof(int)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }
@@ -203,7 +205,7 @@ int run_decode(lora_attn* h, const AttnParams& a, const SeqList<kMaxSeqs>& list)
     DecodeParams p;
     p.a = a;
     p.group = h->n_heads / h->n_kv;
-    p.granule = kDecodeTile;                     // a power of two that divides the tile and the page
+    p.granule = 64;                              // a power of two that divides the tile and the page
     while (h->page_size % p.granule) p.granule /= 2;
     p.slots = 16;
     while (p.slots > 2 && decode_smem(h->dim, p.slots, list.n) > kSmemTwo) --p.slots;

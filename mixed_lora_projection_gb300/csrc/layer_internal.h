@@ -78,7 +78,6 @@ struct SeqList {
 };
 
 constexpr int kDecodeRows = 16;         // most rows per key/value head of a sequence in the decode kernel
-constexpr int kDecodeTile = 64;         // its cache tile, in tokens
 
 struct DecodeParams {
     CUtensorMap tm_k, tm_v;             // box: 64 features of one head x granule tokens of one page
@@ -115,7 +114,7 @@ struct PromptParams {
     int units, whole, blocks;           // units from `whole` on, fewer than blocks, may be cut in parts
     float* part_o;                      // [2 x blocks][tiles x 128][dim]: sums of units that parts end in
     float2* part_ml;
-    uint32_t* prefix;                   // [blocks][kPromptBlocks + 2]: tiles before each of these; the longest
+    uint32_t* prefix;                   // [kPromptBlocks + 2]: tiles before each of these, all of them, the longest's
     int* counter;                       // [2] units handed out past the first of each block; blocks that have ended
 };
 int prompt_tiles(int dim);              // tiles of rows of a unit
