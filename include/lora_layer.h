@@ -97,7 +97,7 @@ typedef struct lora_kv_cache {
  *   q, q_stride, q_head_stride          device bf16 [T, n_heads, head_dim], or NULL with q_out.
  *   q_out, qo_stride, qo_head_stride    device bf16; may be q itself (same strides).
  *   k, v and their strides              device bf16 [T, n_kv_heads, head_dim].
- *   cos, sin           device fp32 [n_positions, rot / 2], rows contiguous; NULL when rot = 0. A
+ *   cos, sin           device fp32 [n_positions, rot / 2], contiguous, 16-byte aligned; NULL when rot = 0. A
  *                      position outside [0, n_positions) uses the last row.
  *   rot                0, or a multiple of 16 up to head_dim.
  *   head_dim           a multiple of 8 up to 512; n_heads >= 0.

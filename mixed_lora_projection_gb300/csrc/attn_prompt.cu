@@ -171,7 +171,8 @@ struct Piece {
     int t0, n;            // its tiles; n < 0: the end
     int part;             // where its sums go in the workspace; -1: to the output
     int two;              // its rows reach into the second tile
-    int pad[5];
+    int k0;               // its first piece in the ring's order
+    int pad[4];
 };
 static_assert(sizeof(Piece) == 64, "two pieces fill their place in shared memory");
 
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 w.t0 = t0;
                 w.n = last || !ok ? -1 : t1 - t0;
                 w.part = part;
+                w.k0 = issued;
                 w.two = S::kIssuers == 2 || u.q_len - u.tok0 > p.tile_tokens;
                 mbar_arrive(smem_addr(&told[count & 1]));
             }
@@ -537,13 +539,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         for (int count = 0; ok; ++count) {
             wait_on(&told[count & 1], (uint32_t)(count >> 1));
             if (!ok) break;
-            const int n = pieces[count & 1].n;
+            const int n = pieces[count & 1].n, k0 = pieces[count & 1].k0;
             const bool two = pieces[count & 1].two;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[count & 1]));
             if (n < 0) break;
             if (n == 0) continue;
-            const int k0 = 2 * S::kPieces * tt;
             if (S::kIssuers == 2) {
                 // The ring's order: K(0), then per tile K(t + 1), V(t): the weights lie apart from the scores, so
                 // the next scores need only the last ones read. The tiles of rows begin in turn, so that neither
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const uint32_t o_addr = lanes + S::kO + (uint32_t)q * D + (uint32_t)half * kOut;
         const float scl = a.scale_log2;
         // The piece at hand; what can be had from it again stays there, since a row's scores take most registers.
-        int count = -1, n = 0, pos = -1, all = 0;                        // all: tiles of the pieces before, for the ring's order
+        int count = -1, n = 0, pos = -1;
         // This thread's row of the tile: its query head of the group, its token in the piece's sequence, and
         // whether there is one. (`row` is hidden from the compiler, which would keep the quotient otherwise.)
         auto row_of = [&](const Piece& u, int& tok, int& hg) {
@@ -700,7 +701,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 if (n == 0 || (q == 1 && !u.two)) {
                     if (valid)
                         for (int c = 0; c < kOut / 8; ++c) reinterpret_cast<uint4*>(out_row(u, tok, hg))[c] = make_uint4(0, 0, 0, 0);
-                    all += n;
                     finish(count);
                     return kNone;
                 }
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (tail < kTk) {
                 // places past the last token may hold anything: their weight is 0, so they must be finite
                 // (each tile of rows writes the same zeros before its own product)
-                const int k = 2 * S::kPieces * all + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
+                const int k = u.k0 + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
                 for (int x = 0; x < S::kPieces; ++x) {
                     const int s = (k + x) % S::kSlots;
                     wait_warp(smem_addr(&full[s]), (uint32_t)((k + x) / S::kSlots) & 1, abort_flag, a.status, limit);
@@ -827,7 +827,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
         }
         tt += n;
-        all += n;
         // The last scores are done, so the queries' place is free: the next ones go there before the output,
         // and their scores are computed meanwhile. (Their weights, which the first product with V waits for,
         // come after this thread has read O.)

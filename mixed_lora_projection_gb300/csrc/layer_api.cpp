@@ -315,7 +315,7 @@ extern "C" int lora_linear_kv_append(const lora_kv_cache* cache, const void* q, 
     if (check_cache(cache, &rows) != LORA_OK) return LORA_EINVAL;
     const int dim = cache->head_dim, n_kv = cache->n_kv_heads;
     if (n_heads < 0 || n_heads > 65536 || rot < 0 || rot > dim || rot % 16) return LORA_EINVAL;
-    if (rot && (!cos || !sin || n_positions < 1 || !aligned4(cos) || !aligned4(sin))) return LORA_EINVAL;
+    if (rot && (!cos || !sin || n_positions < 1 || !aligned16(cos) || !aligned16(sin))) return LORA_EINVAL;
     if (rows == 0) return LORA_OK;
     if ((q == nullptr) != (q_out == nullptr) || (q && n_heads < 1)) return LORA_EINVAL;
     if (!k || !v || !aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v)) return LORA_EINVAL;

@@ -91,14 +91,13 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride);
     const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + row * p.r_stride);
     const uint4* w = static_cast<const uint4*>(p.weight);
-    uint4 xv[V], rv[V], wv[V];
+    uint4 xv[V], rv[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nt;
         const uint4 z = make_uint4(0, 0, 0, 0);
         xv[i] = c < nvec ? x[c] : z;
         rv[i] = (p.residual && c < nvec) ? r[c] : z;
-        wv[i] = c < nvec ? __ldg(w + c) : z;
     }
     float h[V][8], ss = 0.f;
 #pragma unroll
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float b[8];
-        unpack8(wv[i], b);
+        unpack8(tid + i * nt < nvec ? __ldg(w + tid + i * nt) : make_uint4(0, 0, 0, 0), b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h[i][k] = h[i][k] * inv * (b[k] + p.weight_offset);
     }
@@ -150,7 +149,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
 #pragma unroll
         for (int i = 1; i < V; ++i) m = max_nan(m, amax[i]);
         const float s = scale_of(row_reduce<WARP, true>(m, buf[1]));
-        const float si = 1.f / s;
+        const float si = __frcp_rn(s);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (tid + i * nt < nvec) qo[tid + i * nt] = to_e4m3(h[i], si);
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
         return;
     }
     // a group is group / 8 vectors: as many neighbouring lanes, since nt is a multiple of 32
-    const int lanes = p.group >> 3, ng = (p.width + p.group - 1) / p.group;
+    const int lanes = p.group >> 3, shift = 31 - __clz(lanes), ng = (nvec + lanes - 1) >> shift;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nt;
@@ -166,8 +165,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
         for (int o = lanes >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float s = scale_of(m);
         if (c < nvec) {
-            qo[c] = to_e4m3(h[i], 1.f / s);
-            if ((c & (lanes - 1)) == 0) p.scales[(long long)row * ng + c / lanes] = s;
+            qo[c] = to_e4m3(h[i], __frcp_rn(s));
+            if ((c & (lanes - 1)) == 0) p.scales[(long long)row * ng + (c >> shift)] = s;
         }
     }
 }
@@ -175,10 +174,15 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
 // Turns 8 features of each half: (a, b) -> (a cos - b sin, b cos + a sin).
 __device__ __forceinline__ void turn8(float* a, float* b, const float* cs, const float* sn) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = a[i], y = b[i], c = __ldg(cs + i), s = __ldg(sn + i);
-        a[i] = x * c - y * s;
-        b[i] = y * c + x * s;
+    for (int i = 0; i < 8; i += 4) {
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + i)), s4 = __ldg(reinterpret_cast<const float4*>(sn + i));
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float x = a[i + k], y = b[i + k];
+            a[i + k] = x * c[k] - y * s[k];
+            b[i + k] = y * c[k] + x * s[k];
+        }
     }
 }
 
@@ -203,29 +207,32 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
         slot = pos % p.c.page_size;
         if (page >= p.c.n_pages) page = -1;
     }
-    const int pairs = p.rot >> 4, single = (p.c.dim - p.rot) >> 3;
-    const int per = pairs + single;                  // items of a turned head
-    const int nq = p.q_out ? p.n_heads * per : 0, nk = p.c.n_kv * per, nv = p.c.n_kv * (p.c.dim >> 3);
+    // items of 16 bytes: pairs of the two rotary halves (two of them each), the turned heads' other features,
+    // the values; kinds one after another, so that few warps have two of them
+    const int pairs = p.rot >> 4, single = (p.c.dim - p.rot) >> 3, per_v = p.c.dim >> 3;
+    const int nq = p.q_out ? p.n_heads : 0, heads = nq + (page >= 0 ? p.c.n_kv : 0);
+    const int n_pairs = heads * pairs, n_turned = n_pairs + heads * single, end = n_turned + (page >= 0 ? p.c.n_kv * per_v : 0);
     const float* cs = p.cos + (long long)rp * (p.rot >> 1);
     const float* sn = p.sin + (long long)rp * (p.rot >> 1);
     typedef __nv_bfloat16 bf;
     bf* kd = static_cast<bf*>(p.c.k) + page * p.c.k_page + slot * p.c.k_token;
     bf* vd = static_cast<bf*>(p.c.v) + page * p.c.v_page + slot * p.c.v_token;
-    const int end = page >= 0 ? nq + nk + nv : nq;
     for (int i = threadIdx.x; i < end; i += blockDim.x) {
-        if (i >= nq + nk) {
-            const int u = i - nq - nk, per_v = p.c.dim >> 3, h = u / per_v, c = u - h * per_v;
+        if (i >= n_turned) {
+            const int u = i - n_turned, h = u / per_v, c = u - h * per_v;
             const bf* s = static_cast<const bf*>(p.v) + t * p.v_stride + h * p.v_head;
             reinterpret_cast<uint4*>(vd + h * p.c.v_head)[c] = reinterpret_cast<const uint4*>(s)[c];
             continue;
         }
-        const bool is_q = i < nq;
-        const int u = is_q ? i : i - nq, h = u / per, c = u - h * per;
+        const bool pair = i < n_pairs;
+        const int per = pair ? pairs : single, u = pair ? i : i - n_pairs, hh = u / per, c = u - hh * per;
+        const bool is_q = hh < nq;
+        const int h = is_q ? hh : hh - nq;
         const bf* s = is_q ? static_cast<const bf*>(p.q) + t * p.q_stride + h * p.q_head
                            : static_cast<const bf*>(p.k) + t * p.k_stride + h * p.k_head;
         bf* d = is_q ? static_cast<bf*>(p.q_out) + t * p.qo_stride + h * p.qo_head : kd + h * p.c.k_head;
-        if (c >= pairs) {
-            const int e = p.rot + ((c - pairs) << 3);
+        if (!pair) {
+            const int e = p.rot + (c << 3);
             *reinterpret_cast<uint4*>(d + e) = *reinterpret_cast<const uint4*>(s + e);
             continue;
         }
