@@ -176,6 +176,12 @@ struct Piece {
 };
 static_assert(sizeof(Piece) == 64, "two pieces fill their place in shared memory");
 
+// 32 bytes (a whole sector of L2) in one store; p is 32-byte aligned.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 // Two fp32 values in one instruction.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
     return (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
@@ -711,22 +717,30 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             const int c = (half * 128 + row) % (D / 8), r0 = (half * 128 + row) / (D / 8);
             const bf* src = static_cast<const bf*>(a.q) + (long long)(u.row0 + u.tok0 + q * p.tile_tokens) * a.q_stride +
                             (long long)u.head * g * a.q_head + c * 8;
-            const int last = min(u.q_len - u.tok0 - q * p.tile_tokens, p.tile_tokens);   // tokens of this tile
+            const int last = min(u.q_len - u.tok0 - q * p.tile_tokens, p.tile_tokens);   // tokens of this tile (one at least)
             uint8_t* dst = base + q * S::kQBytes + (c >> 3) * (128 * 128);
+            // row r0 + i kStep is token ri, query head rh; rows without a token read the first one's and become zeros
+            int ri = r0 / g, rh = r0 - ri * g;
+            const int di = kStep / g, dh = kStep - di * g;
+            uint4 val[kLoads];
+            uint32_t real = 0;
 #pragma unroll
-            for (int i0 = 0; i0 < kLoads; i0 += 8) {
-                uint4 val[8];
-#pragma unroll
-                for (int i = 0; i < 8 && i0 + i < kLoads; ++i) {
-                    const int rr = r0 + (i0 + i) * kStep, ri = rr / g;
-                    val[i] = make_uint4(0, 0, 0, 0);
-                    if (ri < last) val[i] = *reinterpret_cast<const uint4*>(src + ri * a.q_stride + (rr - ri * g) * a.q_head);
+            for (int i = 0; i < kLoads; ++i) {
+                const bool have = ri < last;
+                real |= (uint32_t)have << i;
+                val[i] = *reinterpret_cast<const uint4*>(src + (have ? ri * a.q_stride + rh * a.q_head : 0));
+                ri += di;
+                rh += dh;
+                if (rh >= g) {
+                    rh -= g;
+                    ++ri;
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < 8 && i0 + i < kLoads; ++i) {
-                    const int rr = r0 + (i0 + i) * kStep;
-                    *reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val[i];
-                }
+            for (int i = 0; i < kLoads; ++i) {
+                const int rr = r0 + i * kStep;
+                if (!(real >> i & 1)) val[i] = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val[i];
             }
             fence_proxy_async_shared();
             __syncwarp();
@@ -760,10 +774,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             // The weights by the reference at hand, while the row's other thread does its half; the barrier then
             // tells whether either maximum has outgrown the reference by 2^8 (or is the first), in which case both
             // read their scores again and go by a new one. It also orders the weights, which overwrite scores,
-            // after both threads' reads.
+            // after both threads' reads. The first tile has no reference and goes the second way at once.
             const bool wish = m == -INFINITY ? top > -INFINITY : (top - m) * scl > 8.f;
-            float sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
-            if (pair_any(pair, wish)) {
+            float sum = 0.f;
+            if (t > 0) sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
+            if (t == 0 || pair_any(pair, wish)) {
                 if (half) *share = top;
                 pair_any(pair, false);
                 if (!half) *share = top = fmaxf(top, *share);
@@ -788,10 +803,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     l *= alpha;
                 }
                 if (grow) m = top;
-                load_scores<kCols>(s_addr + half * kCols, v);
-                if (masked) mask<kCols>(v, pos - c0, lo, sk);
+                if (t > 0) {
+                    load_scores<kCols>(s_addr + half * kCols, v);
+                    if (masked) mask<kCols>(v, pos - c0, lo, sk);
+                }
                 sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
-                pair_any(pair, false);
+                if (t > 0) pair_any(pair, false);
             }
             if (S::kApart) {
                 tc_fence_before();
@@ -859,20 +876,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             tmem_ld_wait32(x);
             if (!store) continue;
             if (!to_out) {
-                float4* d = reinterpret_cast<float4*>(p.part_o + at * D + half * kOut + c * 32);
+                float* d = p.part_o + at * D + half * kOut + c * 32;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    d[e] = make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 2]),
-                                       __uint_as_float(x[4 * e + 3]));
+                for (int e = 0; e < 32; e += 8) store32(d + e, x + e);
             } else {
+                uint32_t o[16];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint4 o4;
-                    uint32_t* o = &o4.x;
+                for (int k = 0; k < 16; ++k)
+                    o[k] = pack_bf16x2(__uint_as_float(x[2 * k]) * inv, __uint_as_float(x[2 * k + 1]) * inv);
+                if (p.out32) {
+                    store32(out + c * 32, o);
+                    store32(out + c * 32 + 16, o + 8);
+                } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[k] = pack_bf16x2(__uint_as_float(x[8 * e + 2 * k]) * inv, __uint_as_float(x[8 * e + 2 * k + 1]) * inv);
-                    *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = o4;
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
         }

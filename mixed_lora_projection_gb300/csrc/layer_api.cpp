@@ -225,6 +225,7 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.a = a;
     p.group = h->n_heads / h->n_kv;
     p.tile_tokens = kPromptTile / p.group;
+    p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.o_stride % 16 == 0 && a.o_head % 16 == 0;
     p.granule = 64;
     while (h->page_size % p.granule) p.granule /= 2;
     const int step = prompt_tiles(h->dim) * p.tile_tokens;

@@ -111,6 +111,7 @@ struct PromptParams {
     AttnParams a;
     int k_order, v_order, granule, group;
     int tile_tokens;                    // tokens of one tile of rows: 128 / group
+    int out32;                          // every row of the output is 32-byte aligned
     int units, whole, blocks;           // units from `whole` on, fewer than blocks, may be cut in parts
     float* part_o;                      // [2 x blocks][tiles x 128][dim]: sums of units that parts end in
     float2* part_ml;
