@@ -40,13 +40,13 @@ struct Shape {
     static constexpr int kSoftmax = kQ * 256;             // softmax threads: two per row of a tile
     static constexpr bool kApart = D == 64;               // weights beside the scores, not over them
     static constexpr int kIssuers = D == 64 ? 2 : 1;      // warps that issue products
-    static constexpr int kThreads = kSoftmax + kIssuers * 32 + 32;
+    static constexpr int kThreads = kSoftmax + kIssuers * 32 + 64;
     static constexpr int kO = 256;                        // first tensor-memory column of O (S: 128 each, from 0)
     static constexpr int kP = kApart ? 384 : 0;           // of the weights: 64 columns each, or in their scores' place
     static constexpr int kPStep = kApart ? 64 : 128;
     static constexpr int kRing = kQ * kQBytes;
     static constexpr int kBars = kRing + kSlots * kPiece;
-    static constexpr int kPieceInfo = kBars + 320;        // [2] the pieces of work at hand
+    static constexpr int kPieceInfo = kBars + 384;        // [2] the pieces of work at hand
     static constexpr int kShare = kPieceInfo + 128;       // [kQ][128] floats between the two threads of a row
     static constexpr int kSmem = kShare + kQ * 512 + 1024;
 };
@@ -182,6 +182,13 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                  "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 // Two fp32 values in one instruction.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
     return (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
@@ -303,7 +310,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     uint64_t* pv_done = p_full + 2;                       // [kQ * kS] product with V
     uint64_t* s_read = pv_done + 2;                       // [kQ] scores are in registers (kApart)
     uint64_t* q_full = s_read + 2;                        // [kQ] queries
-    uint64_t* drain = q_full + 2;                         // [2] an issuer's last product
+    uint64_t* q_free = q_full + 2;                        // [kQ] their last scores are computed
+    uint64_t* drain = q_free + 2;                         // [2] an issuer's last product
     uint64_t* turn = drain + 2;                           // [2] a tile's scores are issued
     uint64_t* told = turn + 2;                            // [2] a piece of work is there
     uint64_t* done = told + 2;                            // [2] and every warp has finished with it
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);              // known to be the same in every lane
-    constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + S::kIssuers;
+    constexpr int kMmaWarp = S::kSoftmax / 32, kTmaWarp = kMmaWarp + S::kIssuers, kQueryWarp = kTmaWarp + 1;
 
     if (tid == 0) {
         for (int s = 0; s < S::kSlots; ++s) {
@@ -323,11 +331,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             mbar_init(smem_addr(&p_full[s]), 8);          // one arrival a warp
             mbar_init(smem_addr(&pv_done[s]), 1);
             mbar_init(smem_addr(&s_read[s]), 8);
-            mbar_init(smem_addr(&q_full[s]), 8);
+            mbar_init(smem_addr(&q_full[s]), 1);
+            mbar_init(smem_addr(&q_free[s]), 1);
             mbar_init(smem_addr(&drain[s]), 1);
             mbar_init(smem_addr(&turn[s]), 1);
             mbar_init(smem_addr(&told[s]), 1);
-            mbar_init(smem_addr(&done[s]), S::kSoftmax / 32 + S::kIssuers);
+            mbar_init(smem_addr(&done[s]), S::kSoftmax / 32 + S::kIssuers + 1);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -506,6 +515,40 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
             for (int k = max(0, issued - S::kSlots); k < issued; ++k)
                 wait_bounded(smem_addr(&full[k % S::kSlots]), (uint32_t)((k / S::kSlots) & 1), abort_flag, a.status, limit, false);
+    } else if (warp == kQueryWarp) {
+        // ------------------------------------------------------------ queries
+        // Each piece's tiles of rows, as soon as the scores of the piece before are computed. (Loaded by the
+        // softmax warps instead, a tile of 128 x 256 took 5 us: beside the ring the first cache level has
+        // little room for loads in flight.)
+        uint32_t used[2] = {0, 0};
+        bool ok = true;
+        for (int count = 0; ok; ++count) {
+            ok = wait_warp(smem_addr(&told[count & 1]), (uint32_t)(count >> 1) & 1, abort_flag, a.status, limit);
+            if (!ok) break;
+            const Piece& w = pieces[count & 1];
+            const int n = w.n, head = w.head * p.group, two = w.two, row = w.row0 + w.tok0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&done[count & 1]));
+            if (n < 0) break;
+            if (n == 0) continue;
+#pragma unroll
+            for (int q = 0; q < S::kQ; ++q) {
+                if (q == 1 && !two) continue;
+                ok = ok && wait_warp(smem_addr(&q_free[q]), (used[q] & 1) ^ 1, abort_flag, a.status, limit);
+                if (!ok) break;
+                const uint32_t bar = smem_addr(&q_full[q]);
+                mbar_arrive_expect_tx(bar, (uint32_t)(p.tile_tokens * p.group) * D * 2, issuer);
+                __syncwarp();
+                const int token = row + q * p.tile_tokens;
+                if (lane < D / 64)
+                    tma_load_3d(q_smem + (uint32_t)(q * S::kQBytes + lane * (128 * 128)), &p.tm_q, bar, lane * 64, p.q_outer ? token : head,
+                                p.q_outer ? head : token);
+                ++used[q];
+            }
+        }
+        if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
+            for (int q = 0; q < S::kQ; ++q)
+                if (used[q]) wait_bounded(smem_addr(&q_full[q]), (used[q] - 1) & 1, abort_flag, a.status, limit, false);
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------------ MMA issuers
         // A product of N = 128 or less costs the issuing warp ~90-105 cycles, more than the tensor cores need
@@ -568,6 +611,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                         tc_fence_after();
                         scores(me, 0, k, 0);
                         mma_commit_local<1>(smem_addr(&s_full[me]), issuer);
+                        if (t + 2 == n) mma_commit_local<1>(smem_addr(&q_free[me]), issuer);
                         release(k);
                     }
                     if (t < 0) continue;
@@ -608,6 +652,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                         if (t + 1 < n) {
                             scores(q, 0, ks, 0);
                             mma_commit_local<1>(smem_addr(&s_full[q]), issuer);
+                            if (t + 2 == n) mma_commit_local<1>(smem_addr(&q_free[q]), issuer);
                         }
                     }
                     if (!ok) break;
@@ -632,6 +677,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                             release(k + x);
                         }
                         mma_commit_local<1>(smem_addr(&s_full[b]), issuer);
+                        if (t + 2 == n) mma_commit_local<1>(smem_addr(&q_free[0]), issuer);
                     }
                     if (t < 0) continue;
                     const int b = (tt + t) & 1, k = k0 + S::kPieces * (2 * t + (t + 1 < n ? 2 : 1));
@@ -675,10 +721,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         auto row_of = [&](const Piece& u, int& tok, int& hg) {
             int row = tid & 127;
             asm volatile("" : "+r"(row));
-            const int qi = row / g;
-            hg = row - qi * g;
+            const int d = p.q_outer ? p.tile_tokens : g, x = row / d, y = row - x * d;
+            const int qi = p.q_outer ? y : x;
+            hg = p.q_outer ? x : y;
             tok = u.tok0 + q * p.tile_tokens + qi;
-            return qi < p.tile_tokens && tok < u.q_len;
+            return row < p.tile_tokens * g && tok < u.q_len;
         };
         auto out_row = [&](const Piece& u, int tok, int hg) {
             return static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + (u.head * g + hg) * a.o_head + half * kOut;
@@ -687,11 +734,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[c & 1]));
         };
-        // The next piece: kReady with its queries in shared memory (128-byte swizzled rows in chunks of 64
-        // features; each thread has one 16-byte column of every 2048 / D-th row, its loads in flight together),
-        // kNone where it has nothing for this tile of rows (the rows of a unit without tiles are zeros), or kEnd.
-        // One piece at a time: the producer reuses a piece's place when every warp has finished with the one
-        // before the last.
+        // The next piece: kReady, kNone where it has nothing for this tile of rows (the rows of a unit without
+        // tiles are zeros), or kEnd. One piece at a time: the producer reuses a piece's place when every warp has
+        // finished with the one before the last.
         enum { kReady, kNone, kEnd };
         auto advance = [&]() -> int {
             ++count;
@@ -703,7 +748,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 const Piece& u = pieces[count & 1];
                 int tok, hg;
                 const bool valid = row_of(u, tok, hg);
-                pos = valid ? u.len - u.q_len + tok : -1;
+                // a row without a token goes with the tile's last one, so that it asks for no mask of its own
+                pos = u.len - u.q_len + min(min(tok, u.q_len - 1), u.tok0 + (q + 1) * p.tile_tokens - 1);
                 if (n == 0 || (q == 1 && !u.two)) {
                     if (valid)
                         for (int c = 0; c < kOut / 8; ++c) reinterpret_cast<uint4*>(out_row(u, tok, hg))[c] = make_uint4(0, 0, 0, 0);
@@ -711,40 +757,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     return kNone;
                 }
             }
-            const Piece& u = pieces[count & 1];
-            const int row = tid & 127;
-            constexpr int kStep = 2048 / D, kLoads = 128 / kStep;
-            const int c = (half * 128 + row) % (D / 8), r0 = (half * 128 + row) / (D / 8);
-            const bf* src = static_cast<const bf*>(a.q) + (long long)(u.row0 + u.tok0 + q * p.tile_tokens) * a.q_stride +
-                            (long long)u.head * g * a.q_head + c * 8;
-            const int last = min(u.q_len - u.tok0 - q * p.tile_tokens, p.tile_tokens);   // tokens of this tile (one at least)
-            uint8_t* dst = base + q * S::kQBytes + (c >> 3) * (128 * 128);
-            // row r0 + i kStep is token ri, query head rh; rows without a token read the first one's and become zeros
-            int ri = r0 / g, rh = r0 - ri * g;
-            const int di = kStep / g, dh = kStep - di * g;
-            uint4 val[kLoads];
-            uint32_t real = 0;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const bool have = ri < last;
-                real |= (uint32_t)have << i;
-                val[i] = *reinterpret_cast<const uint4*>(src + (have ? ri * a.q_stride + rh * a.q_head : 0));
-                ri += di;
-                rh += dh;
-                if (rh >= g) {
-                    rh -= g;
-                    ++ri;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int rr = r0 + i * kStep;
-                if (!(real >> i & 1)) val[i] = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = val[i];
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&q_full[q]));
             return kReady;
         };
         int tt = 0;                      // tiles so far
@@ -844,11 +856,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(smem_addr(&p_full[q * S::kS + b]));
         }
         tt += n;
-        // The last scores are done, so the queries' place is free: the next ones go there before the output,
-        // and their scores are computed meanwhile. (Their weights, which the first product with V waits for,
+        // The next piece's scores are computed meanwhile. (Its first product with V waits for its weights, which
         // come after this thread has read O.)
         const int mine = count;
-        state = advance();
         {
             const int tp = tt - 1, bp = S::kS == 2 ? tp & 1 : 0;
             wait_warp(smem_addr(&pv_done[q * S::kS + bp]), (uint32_t)(S::kS == 2 ? tp >> 1 : tp) & 1, abort_flag, a.status, limit);
@@ -895,7 +905,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
         }
         tc_fence_before();
-        while (state == kNone) state = advance();
+        while ((state = advance()) == kNone) {}
         }
     }
     __syncthreads();
@@ -917,14 +927,15 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     using S = Shape<D>;
     const int rest = p.units - p.whole, rows = (int)gridDim.x / rest, unit = blockIdx.x / rows, row = blockIdx.x - unit * rows;
     const Unit u = find_unit<D>(p, list, p.whole + unit);
-    const int g = p.group, q = row >> 7, r = row & 127, qi = r / g, tok = u.tok0 + q * p.tile_tokens + qi;
-    if (qi >= p.tile_tokens || tok >= u.q_len) return;
+    const int g = p.group, q = row >> 7, r = row & 127, d = p.q_outer ? p.tile_tokens : g, x = r / d, y = r - x * d;
+    const int hg = p.q_outer ? x : y, tok = u.tok0 + q * p.tile_tokens + (p.q_outer ? y : x);
+    if (r >= p.tile_tokens * g || tok >= u.q_len) return;
     griddep_wait();
     const Plan plan = plan_rest(p, p.prefix[rest], p.prefix[rest + 1]);
     if (plan.total == 0) return;
     const uint32_t first = p.prefix[unit], n = p.prefix[unit + 1] - first;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
-                         (u.head * g + (r - qi * g)) * p.a.o_head;
+                         (u.head * g + hg) * p.a.o_head;
     if (n == 0) {
         for (int e = threadIdx.x; e < D; e += 128) out[e] = __float2bfloat16_rn(0.f);
         return;
@@ -952,7 +963,7 @@ cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cud
     // rows that a unit may have: those of the longest sequence where they fit the first tile, else all
     int most = 0;
     for (int i = 0; i < all.n; ++i) most = all.q_len[i] > most ? all.q_len[i] : most;
-    const int rows = most <= p.tile_tokens ? most * p.group : Shape<D>::kQ * 128;
+    const int rows = most > p.tile_tokens ? Shape<D>::kQ * 128 : p.q_outer ? p.tile_tokens * p.group : most * p.group;
     cfg.gridDim = dim3((unsigned)((p.units - p.whole) * rows));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;

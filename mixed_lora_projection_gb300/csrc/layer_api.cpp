@@ -152,6 +152,20 @@ bool encode_cache(EncodeTiledFn encode, CUtensorMap* m, int* order, const CacheV
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map of the queries: 64 features of `group` heads by `tokens` rows, 128-byte swizzled; the axes past
+// the features by ascending stride.
+bool encode_queries(EncodeTiledFn encode, CUtensorMap* m, bool outer, const AttnParams& a, int dim, int group, int tokens) {
+    const cuuint64_t heads = (cuuint64_t)a.n_heads, rows = (cuuint64_t)a.rows;
+    cuuint64_t dims[3] = {(cuuint64_t)dim, outer ? rows : heads, outer ? heads : rows};
+    const cuuint64_t sh = (cuuint64_t)a.q_head * 2, sr = (cuuint64_t)a.q_stride * 2;
+    cuuint64_t strides[2] = {outer ? sr : sh, outer ? sh : sr};
+    cuuint32_t box[3] = {64, (cuuint32_t)(outer ? tokens : group), (cuuint32_t)(outer ? group : tokens)};
+    cuuint32_t step[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Makes `device` current for the life of a call.
 struct DeviceGuard {
     int prev = -1;
@@ -225,6 +239,7 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.a = a;
     p.group = h->n_heads / h->n_kv;
     p.tile_tokens = kPromptTile / p.group;
+    p.q_outer = a.q_head > a.q_stride;
     p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.o_stride % 16 == 0 && a.o_head % 16 == 0;
     p.granule = 64;
     while (h->page_size % p.granule) p.granule /= 2;
@@ -243,7 +258,8 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     if (!encode_cache(h->encode, &p.tm_k, &p.k_order, a.c, false, p.granule) ||
-        !encode_cache(h->encode, &p.tm_v, &p.v_order, a.c, true, p.granule))
+        !encode_cache(h->encode, &p.tm_v, &p.v_order, a.c, true, p.granule) ||
+        !encode_queries(h->encode, &p.tm_q, p.q_outer, a, h->dim, p.group, p.tile_tokens))
         return LORA_EINVAL;
     return launch_prompt(p, list, a.stream) == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }

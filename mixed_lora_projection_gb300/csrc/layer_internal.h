@@ -108,6 +108,9 @@ struct PromptList : SeqList<N> {
 
 struct PromptParams {
     CUtensorMap tm_k, tm_v;             // as DecodeParams
+    CUtensorMap tm_q;                   // box: 64 features x the group's heads x tile_tokens tokens
+    int q_outer;                        // the queries' heads are further apart than their tokens: a tile's rows then go
+                                        // by head (row r is token r % tile_tokens), not by token (row r is head r % group)
     AttnParams a;
     int k_order, v_order, granule, group;
     int tile_tokens;                    // tokens of one tile of rows: 128 / group
