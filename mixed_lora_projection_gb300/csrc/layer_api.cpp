@@ -297,8 +297,7 @@ extern "C" int lora_linear_add_rms_norm(const void* x, long long x_stride, const
             if (meet(outs[i], outs[k])) return LORA_EINVAL;
         // a row is read whole before its outputs are written, so h or y may be an input itself
         const bool is_x = (i == 0 && h_out == x && h_stride == x_stride) || (i == 1 && y == x && y_stride == x_stride);
-        const bool is_r = residual && ((i == 0 && h_out == residual && h_stride == residual_stride) ||
-                                       (i == 1 && y == residual && y_stride == residual_stride));
+        const bool is_r = residual && i == 0 && h_out == residual && h_stride == residual_stride;
         if ((!is_x && meet(outs[i], sx)) || (!is_r && meet(outs[i], sr))) return LORA_EINVAL;
     }
     NormParams p;
