@@ -103,6 +103,7 @@ __device__ __forceinline__ void join_row(const float* part_o, const float2* part
     const float inv = l == 0.f ? 0.f : 1.f / l;
     for (int e = threadIdx.x; e < D; e += 128)
         out[e] = __float2bfloat16_rn((acc[0][e] * w[0] + acc[1][e] * w[1] + acc[2][e] * w[2] + acc[3][e] * w[3]) * inv);
+    __syncthreads();                     // before the next row's sums
 }
 
 }  // namespace dev

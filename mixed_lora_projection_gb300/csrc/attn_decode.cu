@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 
 namespace lora {
@@ -431,45 +433,45 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
 }
 
-// Joins the parts of split units: one block per row of a unit. (Joined by the block that ends last
-// instead, in the same launch, one chat's step took 12.3 us against 10.3: one block then reads what
-// four warps per row read at once.)
+// Joins the parts of split units: a block takes one row of a unit at a time. (Joined by the block that
+// ends last instead, in the same launch, one chat's step took 12.3 us against 10.3: one block then reads
+// what four warps per row read at once.)
 template <int D, int N>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ SeqList<N> list) {
-    const int most = (int)gridDim.x / p.a.c.n_kv;    // rows of the longest sequence
-    const int i = blockIdx.y, head = blockIdx.x / most, row = blockIdx.x % most, g = p.group;
-    if (row >= list.q_len[i] * g) return;
-    griddep_wait();
     const AttnParams& a = p.a;
-    const uint32_t p0 = p.prefix[i], nt = p.prefix[i + 1] - p0;
-    if (nt == 0) return;                 // the first launch wrote its zeros
+    const int g = p.group, most = p.most_rows, per = a.c.n_kv * most;
+    griddep_wait();
     const unsigned long long total = (unsigned long long)p.prefix[list.n] * a.c.n_kv;
     const unsigned grid = (unsigned)min((unsigned long long)p.grid, total);
-    const unsigned long long first = (unsigned long long)p0 * a.c.n_kv + (unsigned long long)head * nt;
-    const unsigned c0 = part_of(total, grid, first), c1 = part_of(total, grid, first + nt - 1);
-    if (c0 == c1) return;                // one block had the whole unit and wrote it
-    const int qi = row / g, hq = head * g + row - qi * g;
-    join_row<D>(p.part_o, p.part_ml, (int)(c1 - c0 + 1), [=](int c) { return (2ll * (c0 + c) + (c == 0)) * kDecodeRows + row; },
-                static_cast<__nv_bfloat16*>(a.out) + (list.row[i] + qi) * a.o_stride + hq * a.o_head);
+    for (int x = blockIdx.x; x < list.n * per; x += gridDim.x) {
+        const int i = x / per, head = (x - i * per) / most, row = x - i * per - head * most;
+        if (row >= list.q_len[i] * g) continue;
+        const uint32_t p0 = p.prefix[i], nt = p.prefix[i + 1] - p0;
+        if (nt == 0) continue;           // the first launch wrote its zeros
+        const unsigned long long first = (unsigned long long)p0 * a.c.n_kv + (unsigned long long)head * nt;
+        const unsigned c0 = part_of(total, grid, first), c1 = part_of(total, grid, first + nt - 1);
+        if (c0 == c1) continue;          // one block had the whole unit and wrote it
+        const int qi = row / g, hq = head * g + row - qi * g;
+        join_row<D>(p.part_o, p.part_ml, (int)(c1 - c0 + 1), [=](int c) { return (2ll * (c0 + c) + (c == 0)) * kDecodeRows + row; },
+                    static_cast<__nv_bfloat16*>(a.out) + (list.row[i] + qi) * a.o_stride + hq * a.o_head);
+    }
 }
 
 template <int D, int N>
 cudaError_t launch_n(const DecodeParams& p, const SeqList<kMaxSeqs>& all, cudaStream_t stream) {
     SeqList<N> list;
     list.n = all.n;
-    int most = 0;
     for (int i = 0; i < all.n; ++i) {
         list.row[i] = all.row[i];
         list.q_len[i] = all.q_len[i];
         list.seq[i] = all.seq[i];
-        most = all.q_len[i] > most ? all.q_len[i] : most;
     }
     const size_t smem = decode_smem(D, p.slots, all.n);
     decode_kernel<D, N><<<p.grid, kDecodeThreads, smem, stream>>>(p, list);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.a.c.n_kv * most * p.group), (unsigned)all.n);
+    cfg.gridDim = dim3((unsigned)std::min<long long>((long long)all.n * p.a.c.n_kv * p.most_rows, 8 * p.grid));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -18,6 +18,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 
 namespace lora {
@@ -921,29 +923,33 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
 }
 
-// Joins the parts of the cut units: one block per row. Also writes the zeros of cut units without a tile.
+// Joins the parts of the cut units, if they were cut: a block takes one row at a time. Also writes the
+// zeros of cut units without a tile.
 template <int D, int N>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
     using S = Shape<D>;
-    const int rest = p.units - p.whole, rows = (int)gridDim.x / rest, unit = blockIdx.x / rows, row = blockIdx.x - unit * rows;
-    const Unit u = find_unit<D>(p, list, p.whole + unit);
-    const int g = p.group, q = row >> 7, r = row & 127, d = p.q_outer ? p.tile_tokens : g, x = r / d, y = r - x * d;
-    const int hg = p.q_outer ? x : y, tok = u.tok0 + q * p.tile_tokens + (p.q_outer ? y : x);
-    if (r >= p.tile_tokens * g || tok >= u.q_len) return;
+    const int rest = p.units - p.whole, g = p.group, d = p.q_outer ? p.tile_tokens : g;
     griddep_wait();
     const Plan plan = plan_rest(p, p.prefix[rest], p.prefix[rest + 1]);
     if (plan.total == 0) return;
-    const uint32_t first = p.prefix[unit], n = p.prefix[unit + 1] - first;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
-                         (u.head * g + hg) * p.a.o_head;
-    if (n == 0) {
-        for (int e = threadIdx.x; e < D; e += 128) out[e] = __float2bfloat16_rn(0.f);
-        return;
+    for (int i = blockIdx.x; i < rest * p.join_rows; i += gridDim.x) {
+        const int unit = i / p.join_rows, row = i - unit * p.join_rows;
+        const int q = row >> 7, r = row & 127, x = r / d, y = r - x * d, hg = p.q_outer ? x : y;
+        const Unit u = find_unit<D>(p, list, p.whole + unit);
+        const int tok = u.tok0 + q * p.tile_tokens + (p.q_outer ? y : x);
+        if (r >= p.tile_tokens * g || tok >= u.q_len) continue;
+        const uint32_t first = p.prefix[unit], n = p.prefix[unit + 1] - first;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + (long long)(u.row0 + tok) * p.a.o_stride +
+                             (u.head * g + hg) * p.a.o_head;
+        if (n == 0) {
+            for (int e = threadIdx.x; e < D; e += 128) out[e] = __float2bfloat16_rn(0.f);
+            continue;
+        }
+        const uint32_t c0 = part_of(plan, first), c1 = part_of(plan, first + n - 1);
+        if (c0 == c1) continue;          // one block had the whole unit and wrote it
+        join_row<D>(p.part_o, p.part_ml, (int)(c1 - c0 + 1),
+                    [=](int c) { return ((2ll * (c0 + c) + (c == 0)) * S::kQ + q) * 128 + r; }, out);
     }
-    const uint32_t c0 = part_of(plan, first), c1 = part_of(plan, first + n - 1);
-    if (c0 == c1) return;                // one block had the whole unit and wrote it
-    join_row<D>(p.part_o, p.part_ml, (int)(c1 - c0 + 1),
-                [=](int c) { return ((2ll * (c0 + c) + (c == 0)) * S::kQ + q) * 128 + r; }, out);
 }
 
 template <int D, int N>
@@ -960,11 +966,7 @@ cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cud
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.whole == p.units) return e;
     cudaLaunchConfig_t cfg = {};
-    // rows that a unit may have: those of the longest sequence where they fit the first tile, else all
-    int most = 0;
-    for (int i = 0; i < all.n; ++i) most = all.q_len[i] > most ? all.q_len[i] : most;
-    const int rows = most > p.tile_tokens ? Shape<D>::kQ * 128 : p.q_outer ? p.tile_tokens * p.group : most * p.group;
-    cfg.gridDim = dim3((unsigned)((p.units - p.whole) * rows));
+    cfg.gridDim = dim3((unsigned)std::min((p.units - p.whole) * p.join_rows, 16 * p.blocks));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

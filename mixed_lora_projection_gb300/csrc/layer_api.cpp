@@ -224,6 +224,8 @@ int run_decode(lora_attn* h, const AttnParams& a, const SeqList<kMaxSeqs>& list)
     p.slots = 16;
     while (p.slots > 2 && decode_smem(h->dim, p.slots, list.n) > kSmemTwo) --p.slots;
     p.grid = 2 * h->num_sms;
+    p.most_rows = 0;
+    for (int i = 0; i < list.n; ++i) p.most_rows = std::max(p.most_rows, (int)list.q_len[i] * p.group);
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     p.prefix = h->prefix;
@@ -239,10 +241,10 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.a = a;
     p.group = h->n_heads / h->n_kv;
     p.tile_tokens = kPromptTile / p.group;
-    p.q_outer = a.q_head > a.q_stride;
     p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.o_stride % 16 == 0 && a.o_head % 16 == 0;
     p.granule = 64;
     while (h->page_size % p.granule) p.granule /= 2;
+    p.q_outer = a.q_head > a.q_stride;
     const int step = prompt_tiles(h->dim) * p.tile_tokens;
     long long units = 0;
     for (int i = 0; i < list.n; ++i) {
@@ -252,6 +254,10 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     }
     p.units = (int)units;
     p.blocks = std::min(h->num_sms, kPromptBlocks);
+    // rows that a unit may have: those of the longest sequence where they fit the first tile, else all
+    int most = 0;
+    for (int i = 0; i < list.n; ++i) most = std::max(most, (int)list.q_len[i]);
+    p.join_rows = most > p.tile_tokens ? prompt_tiles(h->dim) * kPromptTile : p.q_outer ? p.tile_tokens * p.group : most * p.group;
     p.whole = (int)(units / p.blocks * p.blocks);
     p.prefix = h->prefix + h->max_seqs + 1;
     p.counter = h->status + 1;

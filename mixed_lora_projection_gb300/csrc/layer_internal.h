@@ -89,6 +89,7 @@ struct DecodeParams {
     float* part_o;                      // [2 x grid][16][dim]: unnormalised sums of split units
     float2* part_ml;                    // [2 x grid][16]: running maximum and sum
     uint32_t* prefix;                   // [n + 1]: tiles of one head before each sequence
+    int most_rows;                      // of a sequence, per key/value head
     int grid;
 };
 size_t decode_smem(int dim, int slots, int seqs);
@@ -115,6 +116,7 @@ struct PromptParams {
     int k_order, v_order, granule, group;
     int tile_tokens;                    // tokens of one tile of rows: 128 / group
     int out32;                          // every row of the output is 32-byte aligned
+    int join_rows;                      // rows of a unit that may hold a token
     int units, whole, blocks;           // units from `whole` on, fewer than blocks, may be cut in parts
     float* part_o;                      // [2 x blocks][tiles x 128][dim]: sums of units that parts end in
     float2* part_ml;
