@@ -232,18 +232,15 @@ __device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, volati
 }
 // The low n bits (n may be outside 0 .. 64).
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
-// Scores of N columns that the row does not see become -inf: it sees columns up to hi that are lo or more, or below sk.
-template <int N>
-__device__ __forceinline__ void mask(uint32_t* v, int hi, int lo, int sk) {
+// The columns of 64 that a row sees: those up to hi that are lo or more, or below sk.
+__device__ __forceinline__ uint64_t seen_bits(int hi, int lo, int sk) { return low_bits(hi + 1) & (~low_bits(lo) | low_bits(sk)); }
+// Scores of 64 columns that the row does not see become -inf.
+__device__ __forceinline__ void mask(uint32_t* v, uint64_t seen) {
+    const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
 #pragma unroll
-    for (int h = 0; h < N; h += 64) {
-        const uint64_t seen = low_bits(hi + 1 - h) & (~low_bits(lo - h) | low_bits(sk - h));
-        const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            if (!(s0 & 1u << c)) v[h + c] = 0xff800000u;
-            if (!(s1 & 1u << c)) v[h + 32 + c] = 0xff800000u;
-        }
+    for (int c = 0; c < 32; ++c) {
+        if (!(s0 & 1u << c)) v[c] = 0xff800000u;
+        if (!(s1 & 1u << c)) v[32 + c] = 0xff800000u;
     }
 }
 template <int N>
@@ -781,17 +778,24 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             const int c0 = j0 + half * kCols;
             const int lo = a.window ? pos - a.window + 1 - c0 : 0, sk = a.window ? a.sinks - c0 : 0;
             const bool masked = __any_sync(0xffffffffu, pos - c0 < kCols - 1 || (lo > 0 && sk < kCols));
+            // rows of which none sees a column here (past the diagonal, or before the window) have weights of zero
+            const bool blind = masked && t > 0 && !__any_sync(0xffffffffu, seen_bits(pos - c0, lo, sk) != 0);
             uint32_t v[kCols];
-            load_scores<kCols>(s_addr + half * kCols, v);
-            if (masked) mask<kCols>(v, pos - c0, lo, sk);
-            float top = row_max<kCols>(v);
+            float top = -INFINITY, sum = 0.f;
+            if (blind) {
+#pragma unroll
+                for (int c = 0; c < kCols / 2; ++c) v[c] = 0;
+            } else {
+                load_scores<kCols>(s_addr + half * kCols, v);
+                if (masked) mask(v, seen_bits(pos - c0, lo, sk));
+                top = row_max<kCols>(v);
+            }
             // The weights by the reference at hand, while the row's other thread does its half; the barrier then
             // tells whether either maximum has outgrown the reference by 2^8 (or is the first), in which case both
             // read their scores again and go by a new one. It also orders the weights, which overwrite scores,
             // after both threads' reads. The first tile has no reference and goes the second way at once.
             const bool wish = m == -INFINITY ? top > -INFINITY : (top - m) * scl > 8.f;
-            float sum = 0.f;
-            if (t > 0) sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
+            if (t > 0 && !blind) sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
             if (t == 0 || pair_any(pair, wish)) {
                 if (half) *share = top;
                 pair_any(pair, false);
@@ -819,7 +823,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 if (grow) m = top;
                 if (t > 0) {
                     load_scores<kCols>(s_addr + half * kCols, v);
-                    if (masked) mask<kCols>(v, pos - c0, lo, sk);
+                    if (masked) mask(v, seen_bits(pos - c0, lo, sk));
                 }
                 sum = weights<kCols>(v, scl, m == -INFINITY ? 0.f : m * scl);
                 if (t > 0) pair_any(pair, false);
