@@ -78,8 +78,12 @@ __device__ __forceinline__ uint2 to_e4m3(const float* f, float inv) {
     return make_uint2(w[0], w[1]);
 }
 
-// One row per block (or per warp: WARP), V 16-byte vectors of it per thread. The row stays in
-// registers between its sum of squares and its outputs, so x and the residual are read once.
+// h = x + residual, y = h (mean h^2 + eps)^(-1/2) (weight + offset); 8 bits: s = max(max|y| / 448, 2^-100),
+// q = e4m3(y / s). One row per block (or per warp: WARP), V 16-byte vectors of it per thread. The row stays
+// in registers (fp32) between its sum of squares and its outputs, so x and the residual are read once and
+// memory is the bound: 16,384 rows of 5,120 with a residual take 100 us in bf16 (0.99 of the measured copy
+// rate) and 87-90 us to 8 bits (0.96-1.0); 48 rows take one pass's latency. The weights are read after the
+// sum, when the sum's loads have left their registers (4,096 rows of 17,408: 82 us against 125).
 template <int V, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const NormParams p) {
     __shared__ float buf[2][32];
@@ -186,8 +190,9 @@ __device__ __forceinline__ void turn8(float* a, float* b, const float* cs, const
     }
 }
 
-// One block per new row: its sequence, position and place in the cache once, then its heads'
-// 16-byte vectors, those of the two rotary halves in pairs.
+// One block per new row: its sequence, position and place in the cache once, then its heads' 16-byte
+// vectors, those of the two rotary halves in pairs. Bound by memory: 16,384 rows of 24 + 2 x 12 heads of
+// 256 take 129-133 us (0.89-0.92 of the measured copy rate) with 64 features turned, 129 with none.
 template <int N>
 __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendParams p,
                                                         const __grid_constant__ SeqOffsets<N> o) {

@@ -285,6 +285,18 @@ def test_layouts_and_strides(layout, q):
         assert (out[:, :3] == 0).all() and (out[:, 3 + 2 * q:] == 0).all()
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 8, 2), (128, 12, 2), (256, 6, 3), (128, 96, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 3)])
+def test_queries_with_heads_outermost(dim, heads, kv_heads, window, sinks):
+    # a head's rows lie together: the row stride is the smaller one
+    for q_lens, kv_lens in (([1, 3], [700, 65]), ([130, 50, 1], [400, 50, 2000])):
+        c = Case(q_lens, kv_lens, heads, kv_heads, dim, 48, seed=dim + heads)
+        c.poison()
+        c.q = c.q.transpose(0, 1).contiguous().transpose(0, 1)
+        assert c.q.stride(0) < c.q.stride(1)
+        c.check(window, sinks)
+
+
 def test_scale_and_large_scores():
     for q in (1, 150):
         c = Case([q], [600], 4, 2, 128, 16, seed=3)
