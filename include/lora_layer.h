@@ -135,9 +135,10 @@ int lora_linear_attn_create(lora_attn** out, int n_heads, int n_kv_heads, int he
  *              overlap q or the cache.
  *   scale      > 0, finite.
  *   window     0 (none) or >= 1; sinks >= 0 (ignored when window = 0).
- * The cache holds the new rows' keys and values already (lora_linear_kv_append). Values of
- * tokens at or past kv_lens are never used, whatever they hold; a NaN or infinity in a token's
- * value that one row of a sequence sees may also reach rows of that sequence that do not see it.
+ * The cache holds the new rows' keys and values already (lora_linear_kv_append). What tokens hold
+ * that no row of their sequence sees (at or past kv_lens, between the sinks and the window) is
+ * never used; a NaN or infinity in the value of a token that one row of a sequence sees may also
+ * reach rows of that sequence that do not see it.
  * Sequences of at most 16 rows per key/value head (q_len * n_heads / n_kv_heads) and longer ones
  * run in different kernels of the same call; the sums' order depends on the batch, so results of
  * one row in two batches may differ in the last bit. The same call gives the same bits.

@@ -52,6 +52,19 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Zeros in place of the values of tokens [from, to) of a piece of TOK tokens in chunks of 64 features, where they
+// are one run of bytes each; thread `me` does chunk `me`. It is for tokens that no row sees (past the last one, or
+// between the sinks and the window): they may hold anything, and their weight of 0 needs them finite. The caller
+// fences.
+template <int D, int TOK>
+__device__ __forceinline__ void zero_tokens(uint32_t piece, int from, int to, int me) {
+    from = max(from, 0);
+    to = min(to, TOK);
+    if (me < D / 64 && from < to)
+        asm volatile("st.bulk.weak.shared::cta [%0], %1, 0;" ::"r"(piece + me * (TOK * 128) + from * 128), "l"((uint64_t)((to - from) * 128))
+                     : "memory");
+}
+
 // 2^x by the hardware's instruction (x = -inf gives 0).
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -361,14 +361,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             }
             wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
             const uint32_t vt = ring + (uint32_t)slot * S::kSlot;
-            if (r.len - j0 < kTk) {      // places past the last token may hold anything: their weight is 0, so they must be finite
-                const int valid = r.len - j0;
-                for (int v = valid * (D / 8) + tid; v < kTk * (D / 8); v += kConsumers) {
-                    const int tok = v / (D / 8), c = v % (D / 8);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vt + (c >> 3) * (kTk * 128) + tok * 128 + (c & 7) * 16),
-                                 "r"(0)
-                                 : "memory");
-                }
+            // tokens that no row sees: past the last one, or in the sinks' last tile and the window's first
+            if (r.len - j0 < kTk) {
+                zero_tokens<D, kTk>(vt, r.len - j0, kTk, tid);
+                fence_proxy_async_shared();
+            }
+            if (a.window && (unsigned)(t + 1 - r.s_tiles) < 2) {
+                zero_tokens<D, kTk>(vt, a.sinks - j0, r.len - list.q_len[w.i] - a.window + 1 - j0, tid);
                 fence_proxy_async_shared();
             }
             consumer_sync();

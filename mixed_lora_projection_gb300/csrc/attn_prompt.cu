@@ -17,11 +17,11 @@
 // turn, so that one tile's products run while the other's weights are computed; a head of 256 has one
 // tile (its O takes half of tensor memory) and two score buffers. A block is persistent: softmax warps,
 // an issuing warp or two, a TMA warp for K and V (one ring of pieces) that also hands out the work, and
-// one for the queries.
+// one for the queries and for blanking values that no row sees.
 //
 // Measured (one GB300, inputs past L2): a 4,096-row chunk at the end of 16,384 tokens 889 us with 24 / 12
 // heads of 256 (1.62 PFLOP/s, 0.84 of the measured bf16 rate) and 1.11 ms with 48 / 8 heads of 128 (0.67);
-// a 16,384-token prompt of 24 / 12 heads of 256, causal 2.01 ms (0.85), with a window of 4,096 0.96 ms (0.77);
+// a 16,384-token prompt of 24 / 12 heads of 256, causal 2.01 ms (0.85), with a window of 4,096 0.99 ms (0.75);
 // heads of 64 0.50 on a 4,096-row chunk.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,7 +57,7 @@ struct Shape {
     static constexpr int kPStep = kApart ? 64 : 128;
     static constexpr int kRing = kQ * kQBytes;
     static constexpr int kBars = kRing + kSlots * kPiece;
-    static constexpr int kPieceInfo = kBars + 384;        // [2] the pieces of work at hand
+    static constexpr int kPieceInfo = kBars + 512;        // [2] the pieces of work at hand
     static constexpr int kShare = kPieceInfo + 128;       // [kQ][128] floats between the two threads of a row
     static constexpr int kSmem = kShare + kQ * 512 + 1024;
 };
@@ -176,6 +176,7 @@ __device__ __forceinline__ Plan plan_rest(const PromptParams& p, uint32_t total,
     l.blocks = min((uint32_t)p.blocks, max(total, 1u));
     return l;
 }
+constexpr int kNoTile = -2;
 // A piece of work as the producer hands it to the other warps, through shared memory.
 struct Piece {
     int head, tok0, q_len, row0, len, s_tiles, lo_tile;     // its unit
@@ -183,8 +184,12 @@ struct Piece {
     int part;             // where its sums go in the workspace; -1: to the output
     int two;              // its rows reach into the second tile
     int k0;               // its first piece in the ring's order
-    int pad[4];
+    // Its tiles with tokens that no row of the unit sees: gap and the one after it between the sinks and the window,
+    // tail past the last token (kNoTile, or a tile outside [0, n): not in this piece).
+    int gap, tail;
+    int pad[2];
 };
+__device__ __forceinline__ bool at_edge(int gap, int tail, int t) { return (unsigned)(t - gap) < 2 || t == tail; }
 static_assert(sizeof(Piece) == 64, "two pieces fill their place in shared memory");
 
 // 32 bytes (a whole sector of L2) in one store; p is 32-byte aligned.
@@ -308,12 +313,13 @@ template <int D, int N>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
     using S = Shape<D>;
-    extern __shared__ __align__(1024) uint8_t raw[];
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t shared_bytes[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(shared_bytes) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + S::kBars);
     uint64_t* full = bars;                                // [kSlots] pieces of K and V
     uint64_t* empty = full + S::kSlots;
-    uint64_t* s_full = empty + S::kSlots;                 // [kQ * kS] scores
+    uint64_t* raw = empty + S::kSlots;                    // [kSlots] pieces of V with tokens to blank, in their own order
+    uint64_t* s_full = raw + S::kSlots;                   // [kQ * kS] scores
     uint64_t* p_full = s_full + 2;                        // [kQ * kS] weights (and O corrected)
     uint64_t* pv_done = p_full + 2;                       // [kQ * kS] product with V
     uint64_t* s_read = pv_done + 2;                       // [kQ] scores are in registers (kApart)
@@ -333,6 +339,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         for (int s = 0; s < S::kSlots; ++s) {
             mbar_init(smem_addr(&full[s]), 1);
             mbar_init(smem_addr(&empty[s]), S::kIssuers);   // every issuer that reads the piece
+            mbar_init(smem_addr(&raw[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&s_full[s]), 1);
@@ -383,10 +390,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             tok = j - pg * a.c.page_size;
             if (page < 0 || page >= a.c.n_pages) page = a.c.n_pages;    // out of the map's range: zeros
         };
-        int slot = 0, issued = 0;
-        uint32_t phase = 0;
-        // pieces of a tile of K (128 tokens x its share of the features) or of V (its share of the tokens x all)
-        auto load = [&](bool v, int page, int tok) -> bool {
+        int slot = 0, issued = 0, edges = 0;                  // edges: pieces of V with tokens to blank
+        uint32_t phase = 0, blanked = 0;                      // blanked: bit s, slot s holds one
+        // Pieces of a tile of K (128 tokens x its share of the features) or of V (its share of the tokens x all). Those
+        // of V at an edge are reported to the warp that blanks them, which reports them to the issuers.
+        auto load = [&](bool v, int page, int tok, bool edge) -> bool {
 #pragma unroll
             for (int x = 0; x < S::kPieces; ++x) {
                 const int chunks = v ? D / 64 : S::kKChunks;
@@ -397,7 +405,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 const bool mine = gi < grans && pg >= 0;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
                 if (!wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) return false;
-                const uint32_t bar = smem_addr(&full[slot]);
+                const uint32_t bar = smem_addr(edge ? &raw[edges % S::kSlots] : &full[slot]);
+                edges += edge;
+                blanked = (blanked & ~(1u << slot)) | (uint32_t)edge << slot;
                 mbar_arrive_expect_tx(bar, bytes, issuer);
                 __syncwarp();
                 if (mine)
@@ -480,6 +490,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 at += (uint32_t)(t1 - t0);
             }
             ok = wait_warp(smem_addr(&done[count & 1]), (uint32_t)((count >> 1) & 1) ^ 1, abort_flag, a.status, limit);
+            const int gap = a.window && u.r.first - a.window >= a.sinks ? u.r.s_tiles - 1 - t0 : kNoTile;
+            const int tail = u.len % kTk ? u.r.s_tiles + u.len / kTk - u.r.lo_tile - t0 : kNoTile;
             if (lane == 0) {             // after a wait that ran out: the end, for the warps that still listen
                 Piece& w = pieces[count & 1];
                 w.head = u.head;
@@ -493,6 +505,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 w.n = last || !ok ? -1 : t1 - t0;
                 w.part = part;
                 w.k0 = issued;
+                w.gap = gap;
+                w.tail = tail;
                 w.two = S::kIssuers == 2 || u.q_len - u.tok0 > p.tile_tokens;
                 mbar_arrive(smem_addr(&told[count & 1]));
             }
@@ -505,14 +519,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             int page, tok, npage, ntok;
             place(t0, page, tok);
             place(t0 + 1, npage, ntok);
-            ok = load(false, page, tok);
+            ok = load(false, page, tok, false);
             for (int t = t0; t < t1 && ok; ++t) {
                 int fpage, ftok;
                 place(t + 2, fpage, ftok);
+                const bool edge = at_edge(gap, tail, t - t0);
                 if (S::kS == 2 || S::kApart) {
-                    ok = (t + 1 == t1 || load(false, npage, ntok)) && load(true, page, tok);
+                    ok = (t + 1 == t1 || load(false, npage, ntok, false)) && load(true, page, tok, edge);
                 } else {
-                    ok = load(true, page, tok) && (t + 1 == t1 || load(false, npage, ntok));
+                    ok = load(true, page, tok, edge) && (t + 1 == t1 || load(false, npage, ntok, false));
                 }
                 page = npage;
                 tok = ntok;
@@ -520,21 +535,32 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 ntok = ftok;
             }
         }
-        if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
+        if (!ok && lane == 0) {          // gave up: wait for the copies in flight before the block may end
             for (int k = max(0, issued - S::kSlots); k < issued; ++k)
-                wait_bounded(smem_addr(&full[k % S::kSlots]), (uint32_t)((k / S::kSlots) & 1), abort_flag, a.status, limit, false);
+                if (!(blanked >> (k % S::kSlots) & 1))
+                    wait_bounded(smem_addr(&full[k % S::kSlots]), (uint32_t)((k / S::kSlots) & 1), abort_flag, a.status, limit, false);
+            for (int e = max(0, edges - S::kSlots); e < edges; ++e)
+                wait_bounded(smem_addr(&raw[e % S::kSlots]), (uint32_t)((e / S::kSlots) & 1), abort_flag, a.status, limit, false);
+        }
     } else if (warp == kQueryWarp) {
-        // ------------------------------------------------------------ queries
+        // ------------------------------------------------------------ queries, tokens to blank
         // Each piece's tiles of rows, as soon as the scores of the piece before are computed. (Loaded by the
         // softmax warps instead, a tile of 128 x 256 took 5 us: beside the ring the first cache level has
-        // little room for loads in flight.)
+        // little room for loads in flight.) Then zeros in place of the values of tokens that no row of the unit
+        // sees: they may hold anything, and their weight of 0 needs them finite. (By the softmax warps, before
+        // their weights go out: 1,150 against 1,130 us for 4,096 rows of 128 at the end of 16,384 tokens and 185
+        // against 175 for 16,384 rows of 128 with a window of 1,024; 985 against 994 with heads of 256 and a window
+        // of 4,096, where this warp's hand-over is felt.)
         uint32_t used[2] = {0, 0};
         bool ok = true;
+        int edges = 0;                                        // pieces of V blanked
         for (int count = 0; ok; ++count) {
             ok = wait_warp(smem_addr(&told[count & 1]), (uint32_t)(count >> 1) & 1, abort_flag, a.status, limit);
             if (!ok) break;
             const Piece& w = pieces[count & 1];
             const int n = w.n, head = w.head * p.group, two = w.two, row = w.row0 + w.tok0;
+            const int gap = w.gap, tail = w.tail, k0 = w.k0, t0 = w.t0, s_tiles = w.s_tiles, lo_tile = w.lo_tile, len = w.len;
+            const int lo = len - w.q_len + w.tok0 - a.window + 1;             // with a window: its first token
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[count & 1]));
             if (n < 0) break;
@@ -552,6 +578,25 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     tma_load_3d(q_smem + (uint32_t)(q * S::kQBytes + lane * (128 * 128)), &p.tm_q, bar, lane * 64, p.q_outer ? token : head,
                                 p.q_outer ? head : token);
                 ++used[q];
+            }
+            for (int i = 0; i < 3 && ok; ++i) {
+                const int t = i < 2 ? gap + i : tail;
+                if (t < 0 || t >= n || (i == 2 && t == gap + 1)) continue;
+                const int at = t0 + t, from = (at < s_tiles ? at : lo_tile + at - s_tiles) * kTk;
+                const int k = k0 + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
+#pragma unroll
+                for (int x = 0; x < S::kPieces; ++x, ++edges) {
+                    ok = ok && wait_warp(smem_addr(&raw[edges % S::kSlots]), (uint32_t)(edges / S::kSlots) & 1, abort_flag, a.status, limit);
+                    if (!ok) break;
+                    const uint32_t piece = ring + (uint32_t)((k + x) % S::kSlots) * S::kPiece;
+                    const int tok = from + x * S::kVTok;
+                    zero_tokens<D, S::kVTok>(piece, len - tok, S::kVTok, lane);
+                    if (a.window) zero_tokens<D, S::kVTok>(piece, a.sinks - tok, lo - tok, lane);
+                }
+                if (!ok) break;
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane < S::kPieces) mbar_arrive(smem_addr(&full[(k + lane) % S::kSlots]));
             }
         }
         if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
@@ -780,7 +825,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             const uint32_t par = (uint32_t)(S::kS == 2 ? ti >> 1 : ti) & 1;
             const volatile Piece& u = pieces[count & 1];
             const int at_tile = u.t0 + t, s_tiles = u.s_tiles, j0 = (at_tile < s_tiles ? at_tile : u.lo_tile + at_tile - s_tiles) * kTk;
-            const int tail = u.len - j0;                                 // tokens from the tile's first on
             wait_warp(smem_addr(&s_full[q * S::kS + b]), par, abort_flag, a.status, limit);
             tc_fence_after();
             const uint32_t s_addr = lanes + (uint32_t)(q * S::kS + b) * 128;
@@ -848,24 +892,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             l += sum;
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c) tmem_st16(p_addr + c * 16, v + c * 16);
-            if (tail < kTk) {
-                // places past the last token may hold anything: their weight is 0, so they must be finite
-                // (each tile of rows writes the same zeros before its own product)
-                const int k = u.k0 + (S::kS == 2 || S::kApart ? S::kPieces * (2 * t + (t + 1 == n ? 1 : 2)) : 1 + 2 * t);   // V's pieces
-                for (int x = 0; x < S::kPieces; ++x) {
-                    const int s = (k + x) % S::kSlots;
-                    wait_warp(smem_addr(&full[s]), (uint32_t)((k + x) / S::kSlots) & 1, abort_flag, a.status, limit);
-                    const int from = max(0, tail - x * S::kVTok);
-                    for (int e = from * (D / 8) + half * 128 + (tid & 127); e < S::kVTok * (D / 8); e += 256) {
-                        const int tk = e / (D / 8), c = e % (D / 8);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + (uint32_t)s * S::kPiece +
-                                                                                    (c >> 3) * (S::kVTok * 128) + tk * 128 + (c & 7) * 16),
-                                     "r"(0)
-                                     : "memory");
-                    }
-                }
-                fence_proxy_async_shared();
-            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();

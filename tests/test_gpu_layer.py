@@ -322,6 +322,20 @@ def test_pages_outside_the_window_may_be_gone():
         within(c.run(window=window, sinks=sinks), ref, bound(ref, w))
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 8, 4), (128, 6, 2), (256, 6, 3)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (40, 70), (300, 5), (1000, 200)])
+def test_bad_values_outside_the_window(dim, heads, kv_heads, window, sinks):
+    """Tokens between the sinks and the first row's window hold NaN and infinities: no row sees them."""
+    for q in (1, 5, 150, 333):
+        c = Case([q, q], [1601, 1350], heads, kv_heads, dim, 32, seed=q)
+        ref, w = c.ref(window, sinks)
+        for i, n in enumerate(c.kv_list):
+            pg, sl = (x[sinks:max(sinks, n - q - window + 1)] for x in c.slots(i, n))
+            c.k[pg, sl], c.v[pg, sl] = math.nan, math.inf
+            c.v[pg[::3], sl[::3]] = math.nan
+        within(c.run(window=window, sinks=sinks), ref, bound(ref, w))
+
+
 def test_same_bits_again_and_other_stream():
     for q, kv in ((1, 5000), (8, 3000), (260, 1500)):
         c = Case([q, q], [kv, kv // 3], 12, 4, 128, 64, seed=q)
