@@ -139,7 +139,7 @@ def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     if out is None:
         out = torch.empty_like(x, dtype=FP8)
     if scales is None:
-        scales = x.new_empty((x.shape[0], n), dtype=torch.float32)
+        scales = torch.empty((x.shape[0], n), dtype=torch.float32, device=x.device)
     elif scales.shape != (x.shape[0], n) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous with shape {(x.shape[0], n)}")
     if residual is not None and h_out is None:
