@@ -4,7 +4,8 @@ Compiles the library's translation units in parallel with nvcc for
 ``-gencode arch=compute_103a,code=sm_103a`` and links them into
 ``mixed_lora_projection_gb300/liblora_linear.so`` (CUDA runtime linked statically, no
 libcuda link: the tensor-map encoder is fetched through the runtime's driver entry
-point, so the library also loads on a machine without a GPU).
+point, so the library also loads on a machine without a GPU). The operators' Python
+binding, ``_layer_bind.so``, is the one unit compiled against PyTorch's headers.
 """
 from __future__ import annotations
 
@@ -13,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblora_linear.so")
+BIND = os.path.join(PKG, "_layer_bind.so")
+BIND_SOURCE = "layer_bind.cpp"
 SOURCES = ["kernels.cu", "kernels_w4.cu", "api.cpp", "planner.cpp", "noalloc.cu",
            "layer_ops.cu", "attn_decode.cu", "attn_prompt.cu", "layer_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,9 +40,9 @@ def _sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BIND)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
         os.path.join(ROOT, "include", h) for h in ("lora_linear.h", "lora_layer.h")]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
@@ -47,11 +51,17 @@ def _stale() -> bool:
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    torch_flags = ["-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
+                   f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     common = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include")]
 
     def compile_one(src):
         obj = os.path.join(BUILD, src + ".o")
         cmd = [nvcc, *ARCH, *common, "-c", os.path.join(CSRC, src), "-o", obj]
+        if src == BIND_SOURCE:
+            cmd += torch_flags
         if ptxas_info and src.endswith(".cu"):
             cmd += ["-Xptxas", "-v"]
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,18 +69,22 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    srcs = _sources()
+    srcs = [*_sources(), BIND_SOURCE]
     with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         results = list(ex.map(compile_one, srcs))
     for _, log in results:
         if (verbose or ptxas_info) and log.strip():
             print(log, file=sys.stderr)
-    tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    libs = os.path.join(torch_dir, "lib")
+    for target, objs, extra in (
+            (LIB, results[:-1], []),
+            (BIND, results[-1:], ["-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+                                  "-Xlinker", f"-rpath={libs}"])):
+        r = subprocess.run([nvcc, *ARCH, "-shared", "-o", target + ".tmp", *[o for o, _ in objs], *extra],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(target + ".tmp", target)
     return LIB
 
 

@@ -458,3 +458,39 @@ def test_kv_append_in_place_and_missing_pages():
     c.table[0, 2] = c.n_pages                                     # past the last page
     kv_append(None, y[:, 2:3], y[:, 3:], c.off, c.kv, c.table, c.k, c.v)
     assert torch.equal(c.k, kc)
+
+
+def test_binding_refusals_leave_outputs_untouched():
+    from mixed_lora_projection_gb300 import LoraError, PagedAttention, add_rms_norm, add_rms_norm_fp8, kv_append
+    x, w = torch.ones(4, 128, dtype=BF16, device=DEV), torch.ones(128, dtype=BF16, device=DEV)
+    y = torch.full_like(x, 7.0)
+    for bad, kw in ((TypeError, dict(weight=w.float())), (TypeError, dict(out=y.float())), (TypeError, dict(residual=1)),
+                    (ValueError, dict(weight=w[:64])), (ValueError, dict(residual=x[:3])), (ValueError, dict(weight=w.cpu())),
+                    (ValueError, dict(out=y.t().contiguous().t())), (LoraError, dict(eps=-1.0)), (LoraError, dict(h_out=y[:, :]))):
+        kw = {"weight": w, "out": y, **kw}
+        with pytest.raises(bad):
+            add_rms_norm(x, **kw)
+    with pytest.raises(ValueError):
+        add_rms_norm_fp8(x, w, group=48)
+    with pytest.raises(ValueError):
+        add_rms_norm_fp8(x, w, scales=torch.ones(4, device=DEV))
+    c = Case([2, 3], [20, 9], 4, 2, 64, 16)
+    o = torch.full_like(c.q, 7.0)
+    attn = PagedAttention(4, 2, 64, 16, 8, 4)
+    good = dict(q=c.q, k_cache=c.k, v_cache=c.v, q_offsets=c.off, kv_lens=c.kv, block_table=c.table, out=o)
+    for bad, kw in ((TypeError, dict(q=c.q.float())), (TypeError, dict(kv_lens=c.kv.long())), (TypeError, dict(q_offsets=3)),
+                    (TypeError, dict(q_offsets=[0, 1.5, 5])), (ValueError, dict(q_offsets=[0, 2])), (ValueError, dict(q_offsets=[0, 2, 6])),
+                    (ValueError, dict(q_offsets=[0, 2, 1 << 40])), (ValueError, dict(q=c.q[:, :2])), (ValueError, dict(out=o[:3])),
+                    (ValueError, dict(v_cache=c.v[1:])), (ValueError, dict(kv_lens=c.kv[:1])), (ValueError, dict(block_table=c.table[0])),
+                    (ValueError, dict(window=1 << 40)), (LoraError, dict(window=-1)), (LoraError, dict(scale=0.0)),
+                    (LoraError, dict(q_offsets=[0, 6, 5]))):
+        with pytest.raises(bad):
+            attn.forward(**{**good, **kw})
+    with pytest.raises(ValueError):
+        kv_append(c.q, c.k[0, :5], c.v[0, :5], c.off, c.kv, c.table, c.k, c.v, torch.ones(30, 8, device=DEV))
+    with pytest.raises(ValueError):
+        kv_append(c.q[:4], c.k[0, :5], c.v[0, :5], c.off, c.kv, c.table, c.k, c.v)
+    assert bool((o == 7).all()) and bool((y == 7).all())
+    attn.close()
+    with pytest.raises(LoraError):
+        attn.forward(**good)

@@ -138,3 +138,14 @@ def test_layer_signatures_match_the_header():
     assert names == [f[0] for f in _lib.KvCache._fields_]
     for m in re.finditer(r"int (lora_linear_\w+)\((.*?)\);", src, flags=re.S):
         assert len(_lib.SIGNATURES[m.group(1)][1]) == len(m.group(2).split(",")), m.group(1)
+
+
+def test_binding_refuses_what_is_no_tensor(lib):
+    from mixed_lora_projection_gb300 import add_rms_norm, add_rms_norm_fp8, kv_append
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        add_rms_norm([[1.0]], x[0])
+    with pytest.raises(ValueError):
+        add_rms_norm_fp8(x, x[0], group=-1)
+    with pytest.raises(TypeError):
+        kv_append(None, None, None, [0, 4], None, None, None, None)
