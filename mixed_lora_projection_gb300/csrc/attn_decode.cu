@@ -19,7 +19,7 @@
 //
 // Measured (one GB300): six chats of 3,000 to 32,768 tokens, 24 / 12 heads of 256, 221 us = 0.88 of the
 // measured copy rate; 64 chats of 700 to 15,820 tokens, 48 / 8 heads of 128, 360 us = 0.89; 64 of 700 to
-// 7,000 tokens, 16 heads of 64, 191 us = 0.78; one chat of 517 tokens 10 us with the join, by latency.
+// 7,000 tokens, 16 heads of 64, 191 us = 0.78; one chat of 517 tokens 9 us with the join, by latency.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
     // tiles of one head before each sequence
     const AttnParams& a = p.a;
+    griddep_wait();
     for (int i = tid; i < list.n; i += kDecodeThreads) {
         const int len = lens[i] = cache_len(a.c, list.seq[i]);
         prefix[i + 1] = (uint32_t)tile_range(len - list.q_len[i], len - 1, a.window, a.sinks, kTk).n;
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     const AttnParams& a = p.a;
     const int g = p.group, most = p.most_rows, per = a.c.n_kv * most;
     griddep_wait();
+    griddep_launch_dependents();
     const unsigned long long total = (unsigned long long)p.prefix[list.n] * a.c.n_kv;
     const unsigned grid = (unsigned)min((unsigned long long)p.grid, total);
     for (int x = blockIdx.x; x < list.n * per; x += gridDim.x) {
@@ -470,19 +472,10 @@ cudaError_t launch_n(const DecodeParams& p, const SeqList<kMaxSeqs>& all, cudaSt
         list.seq[i] = all.seq[i];
     }
     const size_t smem = decode_smem(D, p.slots, all.n);
-    decode_kernel<D, N><<<p.grid, kDecodeThreads, smem, stream>>>(p, list);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_chained(decode_kernel<D, N>, dim3(p.grid), kDecodeThreads, smem, stream, p, list);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>((long long)all.n * p.a.c.n_kv * p.most_rows, 8 * p.grid));
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, N>, p, list);
+    const unsigned joins = (unsigned)std::min<long long>((long long)all.n * p.a.c.n_kv * p.most_rows, 8 * p.grid);
+    return launch_chained(join_kernel<D, N>, dim3(joins), 128, 0, stream, p, list);
 }
 
 template <int D>

@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
     const AttnParams& a = p.a;
     const uint64_t limit = a.wait_limit_ns;
+    griddep_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -970,6 +971,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     using S = Shape<D>;
     const int rest = p.units - p.whole, g = p.group, d = p.q_outer ? p.tile_tokens : g;
     griddep_wait();
+    griddep_launch_dependents();
     const Plan plan = plan_rest(p, p.prefix[rest], p.prefix[rest + 1]);
     if (plan.total == 0) return;
     for (int i = blockIdx.x; i < rest * p.join_rows; i += gridDim.x) {
@@ -1002,19 +1004,10 @@ cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cud
         list.seq[i] = all.seq[i];
         list.unit0[i] = all.unit0[i];
     }
-    prompt_kernel<D, N><<<(unsigned)p.blocks, Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(p, list);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_chained(prompt_kernel<D, N>, dim3(p.blocks), Shape<D>::kThreads, Shape<D>::kSmem, stream, p, list);
     if (e != cudaSuccess || p.whole == p.units) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min((p.units - p.whole) * p.join_rows, 16 * p.blocks));
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D, N>, p, list);
+    const unsigned joins = (unsigned)std::min((p.units - p.whole) * p.join_rows, 16 * p.blocks);
+    return launch_chained(prompt_join_kernel<D, N>, dim3(joins), 128, 0, stream, p, list);
 }
 
 template <int D>

@@ -8,6 +8,26 @@
 
 namespace lora {
 
+// Launches a kernel that may begin while the stream's kernel before it ends: its blocks wait for that kernel
+// (griddep_wait) before they read or write global memory, and let the next one begin (griddep_launch_dependents).
+// Steps of decode are chains of kernels of a few microseconds, where the launches' latency counts: back to back,
+// the norm of 48 rows takes 2.2 us instead of 4.1 with ordinary launches, the append of 48 rows 3.8 instead of 6.2
+// (with its rows split), attention of one chat of 517 tokens 8.8 instead of 10.3.
+template <class... Params, class... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr int kMaxSeqs = 1024;          // sequences of one call: their row offsets travel in the kernel parameters
 constexpr int kSmallSeqs = 64;          // calls of at most this many take 16 times smaller parameters
 

@@ -6,6 +6,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
+#include "dev_common.cuh"
 #include "layer_internal.h"
 
 namespace lora {
@@ -82,7 +85,7 @@ __device__ __forceinline__ uint2 to_e4m3(const float* f, float inv) {
 // q = e4m3(y / s). One row per block (or per warp: WARP), V 16-byte vectors of it per thread. The row stays
 // in registers (fp32) between its sum of squares and its outputs, so x and the residual are read once and
 // memory is the bound: 16,384 rows of 5,120 with a residual take 100 us in bf16 (0.99 of the measured copy
-// rate) and 87-90 us to 8 bits (0.96-1.0); 48 rows take one pass's latency. The weights are read after the
+// rate) and 87-90 us to 8 bits (0.96-1.0); 48 rows take one pass's latency, 2.2 us back to back. The weights are read after the
 // sum, when the sum's loads have left their registers (4,096 rows of 17,408: 82 us against 125).
 template <int V, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const NormParams p) {
@@ -90,6 +93,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
     const int nt = WARP ? 32 : (int)blockDim.x;
     const int tid = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int row = WARP ? (int)(blockIdx.x * 4 + (threadIdx.x >> 5)) : (int)blockIdx.x;
+    dev::griddep_launch_dependents();
+    dev::griddep_wait();
     if (WARP && row >= p.rows) return;
     const int nvec = p.width >> 3;
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride);
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float b[8];
-        unpack8(tid + i * nt < nvec ? __ldg(w + tid + i * nt) : make_uint4(0, 0, 0, 0), b);
+        unpack8(tid + i * nt < nvec ? w[tid + i * nt] : make_uint4(0, 0, 0, 0), b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h[i][k] = h[i][k] * inv * (b[k] + p.weight_offset);
     }
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
 __device__ __forceinline__ void turn8(float* a, float* b, const float* cs, const float* sn) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + i)), s4 = __ldg(reinterpret_cast<const float4*>(sn + i));
+        const float4 c4 = *reinterpret_cast<const float4*>(cs + i), s4 = *reinterpret_cast<const float4*>(sn + i);
         const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -202,6 +207,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
         const int mid = (lo + hi + 1) >> 1;
         if (o.off[mid] <= t) lo = mid; else hi = mid - 1;
     }
+    dev::griddep_launch_dependents();
+    dev::griddep_wait();
     const long long cap = (long long)p.c.pages_per_seq * p.c.page_size;
     const int len = (int)min((long long)max(p.c.kv_lens[lo], 0), cap);
     const int pos = len - (o.off[lo + 1] - t);
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     typedef __nv_bfloat16 bf;
     bf* kd = static_cast<bf*>(p.c.k) + page * p.c.k_page + slot * p.c.k_token;
     bf* vd = static_cast<bf*>(p.c.v) + page * p.c.v_page + slot * p.c.v_token;
-    for (int i = threadIdx.x; i < end; i += blockDim.x) {
+    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < end; i += gridDim.y * blockDim.x) {
         if (i >= n_turned) {
             const int u = i - n_turned, h = u / per_v, c = u - h * per_v;
             const bf* s = static_cast<const bf*>(p.v) + t * p.v_stride + h * p.v_head;
@@ -257,25 +264,26 @@ cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream) {
     const int nvec = p.width >> 3;
     if (nvec <= 128) {
         const int grid = (p.rows + 3) / 4;
-        if (nvec <= 32) add_rms_norm_kernel<1, true><<<grid, 128, 0, stream>>>(p);
-        else if (nvec <= 64) add_rms_norm_kernel<2, true><<<grid, 128, 0, stream>>>(p);
-        else add_rms_norm_kernel<4, true><<<grid, 128, 0, stream>>>(p);
-    } else {
-        const int v = nvec > 2048 || p.rows > 304 ? 4 : nvec > 1024 ? 2 : 1;
-        const int nt = ((nvec + v - 1) / v + 31) / 32 * 32;
-        if (v == 1) add_rms_norm_kernel<1, false><<<p.rows, nt, 0, stream>>>(p);
-        else if (v == 2) add_rms_norm_kernel<2, false><<<p.rows, nt, 0, stream>>>(p);
-        else add_rms_norm_kernel<4, false><<<p.rows, nt, 0, stream>>>(p);
+        if (nvec <= 32) return launch_chained(add_rms_norm_kernel<1, true>, grid, 128, 0, stream, p);
+        if (nvec <= 64) return launch_chained(add_rms_norm_kernel<2, true>, grid, 128, 0, stream, p);
+        return launch_chained(add_rms_norm_kernel<4, true>, grid, 128, 0, stream, p);
     }
-    return cudaGetLastError();
+    const int v = nvec > 2048 || p.rows > 304 ? 4 : nvec > 1024 ? 2 : 1;
+    const int nt = ((nvec + v - 1) / v + 31) / 32 * 32;
+    if (v == 1) return launch_chained(add_rms_norm_kernel<1, false>, p.rows, nt, 0, stream, p);
+    if (v == 2) return launch_chained(add_rms_norm_kernel<2, false>, p.rows, nt, 0, stream, p);
+    return launch_chained(add_rms_norm_kernel<4, false>, p.rows, nt, 0, stream, p);
 }
 
 template <int N>
 static cudaError_t append(const AppendParams& p, const int32_t* off, cudaStream_t stream) {
     SeqOffsets<N> o;
     for (int i = 0; i <= p.c.n_seqs; ++i) o.off[i] = off[i];
-    kv_append_kernel<N><<<p.rows, 256, 0, stream>>>(p, o);
-    return cudaGetLastError();
+    // A few rows are shared out to several blocks each, one vector a thread (at most two blocks an SM): 48 rows of
+    // 24 + 2 x 12 heads of 256 take 2.6 us in a graph instead of 3.9 with a block a row.
+    const long long items = (long long)((p.q_out ? p.n_heads : 0) + 2 * p.c.n_kv) * (p.c.dim >> 3);
+    const unsigned per_row = (unsigned)std::max(1ll, std::min((items + 255) / 256, 304ll / p.rows));
+    return launch_chained(kv_append_kernel<N>, dim3(p.rows, per_row), 256, 0, stream, p, o);
 }
 
 cudaError_t launch_kv_append(const AppendParams& p, const int32_t* q_offsets, cudaStream_t stream) {
