@@ -494,3 +494,36 @@ def test_binding_refusals_leave_outputs_untouched():
     attn.close()
     with pytest.raises(LoraError):
         attn.forward(**good)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([8] * 6, [500, 9, 1300, 77, 2000, 640]), ([1], [517]), ([700, 1, 40], [900, 3000, 40])])
+def test_chained_kernels_wait_for_each_other(q_lens, kv_lens):
+    """Each call reads what the one before wrote, in place: the same bits with and without a wait between calls."""
+    from mixed_lora_projection_gb300 import PagedAttention, add_rms_norm, kv_append
+    c = Case(q_lens, kv_lens, 8, 4, 128, 64)
+    T, g = c.off[-1], gen(5)
+    x0, w = randn(g, T, 2048), randn(g, 1024)
+    cos, sin = torch.rand(3000, 32, generator=g, device=DEV), torch.rand(3000, 32, generator=g, device=DEV)
+    attn = PagedAttention(8, 4, 128, 64, T, len(q_lens))
+    k0, v0 = c.k.clone(), c.v.clone()
+
+    def run(wait):
+        c.k.copy_(k0), c.v.copy_(v0)
+        y = x0.clone()
+        h = torch.zeros(T, 1024, dtype=BF16, device=DEV)
+        for _ in range(12):
+            for step in (lambda: add_rms_norm(y[:, :1024], w, h, out=y[:, :1024], h_out=h),
+                         lambda: kv_append(y[:, :1024].view(T, 8, 128), y[:, 1024:1536].view(T, 4, 128), y[:, 1536:].view(T, 4, 128), c.off,
+                                           c.kv, c.table, c.k, c.v, cos, sin, q_out=y[:, :1024].view(T, 8, 128)),
+                         lambda: attn.forward(y[:, :1024].view(T, 8, 128), c.k, c.v, c.off, c.kv, c.table, out=h.view(T, 8, 128))):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return y, h, c.k.clone(), c.v.clone()
+
+    once = run(True)
+    for _ in range(5):
+        for a, b in zip(once, run(False)):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert attn.status() == 0
