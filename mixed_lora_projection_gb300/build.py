@@ -78,7 +78,8 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     libs = os.path.join(torch_dir, "lib")
     for target, objs, extra in (
             (LIB, results[:-1], []),
-            (BIND, results[-1:], ["-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            (BIND, results[-1:], ["-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+                                  "-ltorch_python",
                                   "-Xlinker", f"-rpath={libs}"])):
         r = subprocess.run([nvcc, *ARCH, "-shared", "-o", target + ".tmp", *[o for o, _ in objs], *extra],
                            capture_output=True, text=True)

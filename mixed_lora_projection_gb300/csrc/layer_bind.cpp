@@ -3,12 +3,12 @@
 //
 // A step of decode calls these every few microseconds of GPU work, so the marshalling is native. Host time of a
 // call with its outputs allocated, against the same checks in Python through ctypes (one core of Grace): norm of
-// 48 rows 4.7 and 15.3 us, in 8 bits by groups 5.9 and 20.6, append of 48 rows 4.0 and 20.9, attention of one row
-// 6.4 and 19.5.
+// 48 rows 4.2 and 15.3 us, in 8 bits by groups 5.0 and 20.6, append of 48 rows 3.7 and 20.9, attention of one row
+// 6.2 and 19.5.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -71,9 +71,9 @@ Heads heads_of(const at::Tensor& t, int64_t heads, int64_t dim, at::Device devic
     // an axis of one has no stride of its own
     return {p, t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), dim) / 8 * 8, heads > 1 ? t.stride(1) : dim};
 }
+// (through the dispatcher, at::empty, an output takes ~0.4 us more)
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType dtype, at::Device device) {
-    at::AutoDispatchBelowADInplaceOrView below;
-    return at::empty(sizes, at::TensorOptions().dtype(dtype).device(device));
+    return at::Tensor(at::detail::empty_cuda(sizes, dtype, device, std::nullopt));
 }
 int to_int(PyObject* o, const char* name) {
     const long long v = PyLong_AsLongLong(o);
