@@ -14,8 +14,8 @@
 // The products are the bound (4 D flops a pair of row and token), and beside them what surrounds them:
 // a product of N <= 128 costs its issuing warp ~90 cycles where the tensor cores need 64, and K and V
 // land in shared memory at ~61 bytes a cycle. Heads of 64 and 128 run two tiles of rows per block in
-// turn, so that one tile's products run while the other's weights are computed; a head of 256 has one
-// tile (its O takes half of tensor memory) and two score buffers. A block is persistent: softmax warps,
+// turn, so that one tile's products run while the other's weights are computed; a head of 256 (its O takes
+// half of tensor memory) and calls of few rows have one tile and two score buffers. A block is persistent: softmax warps,
 // an issuing warp or two, a TMA warp for K and V (one ring of pieces) that also hands out the work, and
 // one for the queries and for blanking values that no row sees.
 //
@@ -38,19 +38,23 @@ using namespace dev;
 
 constexpr int kTk = kPromptTile;
 
-template <int D>
+// Heads of D features; Q tiles of rows a block. (Heads of 64 and 128 have one where no sequence of the call needs
+// two: drafts to verify, short chunks. Its next scores then run beside its weights, as in heads of 256, and the
+// queries leave the ring more room: six chats with 8 draft rows over 60,000 tokens, 48 / 8 heads of 128 272 ->
+// 256 us, of 64 235 -> 172; 64 prompts of 100 tokens, 16 heads of 64, 43 -> 35; none slower.)
+template <int D, int Q>
 struct Shape {
-    static constexpr int kQ = D == 256 ? 1 : 2;           // tiles of rows per block
-    static constexpr int kS = D == 256 ? 2 : 1;           // score buffers per tile
+    static constexpr int kQ = Q;
+    static constexpr int kS = Q == 1 ? 2 : 1;             // score buffers per tile
     static constexpr int kPieces = D == 256 ? 2 : 1;      // ring pieces of one tile of K (or of V)
     static constexpr int kPiece = D == 64 ? 16384 : 32768;
-    static constexpr int kSlots = D == 64 ? 10 : 5;
+    static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 7 - Q : Q == 2 ? 10 : 13;
     static constexpr int kQBytes = kTk * D * 2;
     static constexpr int kVTok = kTk / kPieces;           // tokens of one V piece
     static constexpr int kKChunks = D / 64 / kPieces;     // 64-feature chunks of one K piece
     static constexpr int kSoftmax = kQ * 256;             // softmax threads: two per row of a tile
-    static constexpr bool kApart = D == 64;               // weights beside the scores, not over them
-    static constexpr int kIssuers = D == 64 ? 2 : 1;      // warps that issue products
+    static constexpr bool kApart = D == 64 && Q == 2;               // weights beside the scores, not over them
+    static constexpr int kIssuers = D == 64 && Q == 2 ? 2 : 1;      // warps that issue products
     static constexpr int kThreads = kSoftmax + kIssuers * 32 + 64;
     static constexpr int kO = 256;                        // first tensor-memory column of O (S: 128 each, from 0)
     static constexpr int kP = kApart ? 384 : 0;           // of the weights: 64 columns each, or in their scores' place
@@ -136,9 +140,9 @@ struct Unit {
     int seq, head, tok0, q_len, row0, len;
     TileRange r;
 };
-template <int D, int N>
+template <int D, int Q, int N>
 __device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptList<N>& list, int unit) {
-    using S = Shape<D>;
+    using S = Shape<D, Q>;
     Unit u;
     int lo = 0, hi = list.n - 1;
     while (lo < hi) {
@@ -309,10 +313,10 @@ __device__ __forceinline__ float weights(uint32_t* v, float scl, float ms) {
     return lo2(sum[0]) + hi2(sum[0]);
 }
 
-template <int D, int N>
-__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+template <int D, int Q, int N>
+__global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
-    using S = Shape<D>;
+    using S = Shape<D, Q>;
     extern __shared__ __align__(1024) uint8_t shared_bytes[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(shared_bytes) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + S::kBars);
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 const int i = k * 32 + lane;
                 before[k] = 0;
                 if (k * 32 >= rest) continue;
-                const uint32_t n = i < rest ? (uint32_t)find_unit<D>(p, list, p.whole + i).r.n : 0;
+                const uint32_t n = i < rest ? (uint32_t)find_unit<D, Q>(p, list, p.whole + i).r.n : 0;
                 uint32_t v = n;
                 longest = max(longest, n);
 #pragma unroll
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             int t0 = 0, t1 = 0, part = -1;
             const bool last = unit >= whole && at >= end;
             if (unit < whole) {
-                u = find_unit<D>(p, list, unit);
+                u = find_unit<D, Q>(p, list, unit);
                 t1 = u.r.n;
                 if (lane == 0) unit = p.blocks + atomicAdd(p.counter, 1);     // the next one, while this one loads
             } else if (!last) {
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                         from = x;
                     }
                 }
-                u = find_unit<D>(p, list, p.whole + lo);
+                u = find_unit<D, Q>(p, list, p.whole + lo);
                 t0 = (int)(at - from);
                 t1 = (int)min((uint32_t)u.r.n, t0 + (end - at));
                 if (t0 > 0 || t1 < u.r.n) part = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
@@ -715,12 +719,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     if (t + 1 < n) release(ks);
                 }
             } else {
-                // the ring's order: K(0), then per tile K(t + 1), V(t), two pieces each
+                // the ring's order: K(0), then per tile K(t + 1), V(t), one piece or two each
                 for (int t = -1; t < n && ok; ++t) {
                     if (t + 1 < n) {
                         const int b = (tt + t + 1) & 1, k = k0 + (t < 0 ? 0 : S::kPieces * (2 * t + 1));
                         // lanes 0 and 1 a piece of K each, 2 the queries
-                        const int kl = k + (lane & 1);
+                        const int kl = k + (lane & (S::kPieces - 1));
                         const bool first = t < 0 && lane == 2;
                         ok = wait_lanes(smem_addr(first ? q_full : &full[kl % S::kSlots]), (uint32_t)(first ? units : kl / S::kSlots) & 1,
                                         abort_flag, a.status, limit);
@@ -737,7 +741,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                     if (t < 0) continue;
                     const int b = (tt + t) & 1, k = k0 + S::kPieces * (2 * t + (t + 1 < n ? 2 : 1));
                     // lanes 0 and 1 a piece of V each, 2 the weights
-                    const int kl = k + (lane & 1);
+                    const int kl = k + (lane & (S::kPieces - 1));
                     ok = wait_lanes(smem_addr(lane == 2 ? &p_full[b] : &full[kl % S::kSlots]),
                                     (uint32_t)(lane == 2 ? (tt + t) >> 1 : kl / S::kSlots) & 1, abort_flag, a.status, limit);
                     if (!ok) break;
@@ -966,9 +970,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 
 // Joins the parts of the cut units, if they were cut: a block takes one row at a time. Also writes the
 // zeros of cut units without a tile.
-template <int D, int N>
+template <int D, int Q, int N>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptList<N> list) {
-    using S = Shape<D>;
+    using S = Shape<D, Q>;
     const int rest = p.units - p.whole, g = p.group, d = p.q_outer ? p.tile_tokens : g;
     griddep_wait();
     griddep_launch_dependents();
@@ -977,7 +981,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     for (int i = blockIdx.x; i < rest * p.join_rows; i += gridDim.x) {
         const int unit = i / p.join_rows, row = i - unit * p.join_rows;
         const int q = row >> 7, r = row & 127, x = r / d, y = r - x * d, hg = p.q_outer ? x : y;
-        const Unit u = find_unit<D>(p, list, p.whole + unit);
+        const Unit u = find_unit<D, Q>(p, list, p.whole + unit);
         const int tok = u.tok0 + q * p.tile_tokens + (p.q_outer ? y : x);
         if (r >= p.tile_tokens * g || tok >= u.q_len) continue;
         const uint32_t first = p.prefix[unit], n = p.prefix[unit + 1] - first;
@@ -994,7 +998,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     }
 }
 
-template <int D, int N>
+template <int D, int Q, int N>
 cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cudaStream_t stream) {
     PromptList<N> list;
     list.n = all.n;
@@ -1004,21 +1008,21 @@ cudaError_t launch_n(const PromptParams& p, const PromptList<kMaxSeqs>& all, cud
         list.seq[i] = all.seq[i];
         list.unit0[i] = all.unit0[i];
     }
-    const cudaError_t e = launch_chained(prompt_kernel<D, N>, dim3(p.blocks), Shape<D>::kThreads, Shape<D>::kSmem, stream, p, list);
+    const cudaError_t e = launch_chained(prompt_kernel<D, Q, N>, dim3(p.blocks), Shape<D, Q>::kThreads, Shape<D, Q>::kSmem, stream, p, list);
     if (e != cudaSuccess || p.whole == p.units) return e;
     const unsigned joins = (unsigned)std::min((p.units - p.whole) * p.join_rows, 16 * p.blocks);
-    return launch_chained(prompt_join_kernel<D, N>, dim3(joins), 128, 0, stream, p, list);
+    return launch_chained(prompt_join_kernel<D, Q, N>, dim3(joins), 128, 0, stream, p, list);
 }
 
-template <int D>
+template <int D, int Q>
 cudaError_t launch_d(const PromptParams& p, const PromptList<kMaxSeqs>& l, cudaStream_t s) {
-    return l.n <= kSmallSeqs ? launch_n<D, kSmallSeqs>(p, l, s) : launch_n<D, kMaxSeqs>(p, l, s);
+    return l.n <= kSmallSeqs ? launch_n<D, Q, kSmallSeqs>(p, l, s) : launch_n<D, Q, kMaxSeqs>(p, l, s);
 }
 
-template <int D>
+template <int D, int Q>
 cudaError_t opt_in() {
-    cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, kSmallSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(prompt_kernel<D, kMaxSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, Q, kSmallSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, Q>::kSmem);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(prompt_kernel<D, Q, kMaxSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, Q>::kSmem);
 }
 
 }  // namespace
@@ -1026,16 +1030,18 @@ cudaError_t opt_in() {
 int prompt_tiles(int dim) { return dim == 256 ? 1 : 2; }
 
 cudaError_t prompt_prepare_device() {
-    cudaError_t e = opt_in<64>();
-    if (e == cudaSuccess) e = opt_in<128>();
-    if (e == cudaSuccess) e = opt_in<256>();
+    cudaError_t e = opt_in<64, 1>();
+    if (e == cudaSuccess) e = opt_in<64, 2>();
+    if (e == cudaSuccess) e = opt_in<128, 1>();
+    if (e == cudaSuccess) e = opt_in<128, 2>();
+    if (e == cudaSuccess) e = opt_in<256, 1>();
     return e;
 }
 
 cudaError_t launch_prompt(const PromptParams& p, const PromptList<kMaxSeqs>& seqs, cudaStream_t stream) {
-    if (p.a.c.dim == 64) return launch_d<64>(p, seqs, stream);
-    if (p.a.c.dim == 128) return launch_d<128>(p, seqs, stream);
-    return launch_d<256>(p, seqs, stream);
+    if (p.a.c.dim == 64) return p.tiles == 1 ? launch_d<64, 1>(p, seqs, stream) : launch_d<64, 2>(p, seqs, stream);
+    if (p.a.c.dim == 128) return p.tiles == 1 ? launch_d<128, 1>(p, seqs, stream) : launch_d<128, 2>(p, seqs, stream);
+    return launch_d<256, 1>(p, seqs, stream);
 }
 
 }  // namespace lora

@@ -245,7 +245,10 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.granule = 64;
     while (h->page_size % p.granule) p.granule /= 2;
     p.q_outer = a.q_head > a.q_stride;
-    const int step = prompt_tiles(h->dim) * p.tile_tokens;
+    int most = 0;
+    for (int i = 0; i < list.n; ++i) most = std::max(most, (int)list.q_len[i]);
+    p.tiles = most > p.tile_tokens ? prompt_tiles(h->dim) : 1;
+    const int step = p.tiles * p.tile_tokens;
     long long units = 0;
     for (int i = 0; i < list.n; ++i) {
         list.unit0[i] = (int32_t)units;
@@ -255,9 +258,7 @@ int run_prompts(lora_attn* h, const AttnParams& a, PromptList<kMaxSeqs>& list) {
     p.units = (int)units;
     p.blocks = std::min(h->num_sms, kPromptBlocks);
     // rows that a unit may have: those of the longest sequence where they fit the first tile, else all
-    int most = 0;
-    for (int i = 0; i < list.n; ++i) most = std::max(most, (int)list.q_len[i]);
-    p.join_rows = most > p.tile_tokens ? prompt_tiles(h->dim) * kPromptTile : p.q_outer ? p.tile_tokens * p.group : most * p.group;
+    p.join_rows = most > p.tile_tokens ? p.tiles * kPromptTile : p.q_outer ? p.tile_tokens * p.group : most * p.group;
     p.whole = (int)(units / p.blocks * p.blocks);
     p.prefix = h->prefix + h->max_seqs + 1;
     p.counter = h->status + 1;

@@ -121,7 +121,7 @@ constexpr int kPromptBlocks = 152;      // most blocks of a launch, one per SM
 constexpr int kPromptTile = 128;        // the prompt kernel's tile of rows and of cache tokens
 
 // SeqList with the first unit of each sequence: a unit is one key/value head and the rows of
-// prompt_tiles(dim) tiles.
+// PromptParams::tiles tiles.
 template <int N>
 struct PromptList : SeqList<N> {
     int32_t unit0[N];
@@ -135,6 +135,7 @@ struct PromptParams {
     AttnParams a;
     int k_order, v_order, granule, group;
     int tile_tokens;                    // tokens of one tile of rows: 128 / group
+    int tiles;                          // tiles of rows of a unit: 1 where no sequence needs more, else prompt_tiles(dim)
     int out32;                          // every row of the output is 32-byte aligned
     int join_rows;                      // rows of a unit that may hold a token
     int units, whole, blocks;           // units from `whole` on, fewer than blocks, may be cut in parts
@@ -143,7 +144,7 @@ struct PromptParams {
     uint32_t* prefix;                   // [kPromptBlocks + 2]: tiles before each of these, all of them, the longest's
     int* counter;                       // [2] units handed out past the first of each block; blocks that have ended
 };
-int prompt_tiles(int dim);              // tiles of rows of a unit
+int prompt_tiles(int dim);              // most tiles of rows of a unit
 cudaError_t prompt_prepare_device();
 cudaError_t launch_prompt(const PromptParams& p, const PromptList<kMaxSeqs>& seqs, cudaStream_t stream);
 
