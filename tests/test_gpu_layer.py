@@ -527,3 +527,14 @@ def test_chained_kernels_wait_for_each_other(q_lens, kv_lens):
         for a, b in zip(once, run(False)):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
     assert attn.status() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(2, 2), (12, 2), (10, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
+def test_calls_at_the_edge_of_one_tile_of_rows(dim, heads, kv_heads, window, sinks):
+    """The longest sequence fills one tile of 128 rows, or needs one token more."""
+    most = 128 // (heads // kv_heads)
+    for longest in (most, most + 1):
+        q = [longest, 1, most // 2 + 9, 0, longest - 1]
+        Case(q, [longest, 300, 700, 40, 1285], heads, kv_heads, dim, 48, seed=longest).check(window, sinks)
