@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
 cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream) {
     const int nvec = p.width >> 3;
     if (nvec <= 128) {
-        const int grid = (p.rows + 3) / 4;
+        const int grid = p.rows / 4 + (p.rows % 4 != 0);
         if (nvec <= 32) return launch_chained(add_rms_norm_kernel<1, true>, grid, 128, 0, stream, p);
         if (nvec <= 64) return launch_chained(add_rms_norm_kernel<2, true>, grid, 128, 0, stream, p);
         return launch_chained(add_rms_norm_kernel<4, true>, grid, 128, 0, stream, p);
