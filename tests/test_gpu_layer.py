@@ -538,3 +538,24 @@ def test_calls_at_the_edge_of_one_tile_of_rows(dim, heads, kv_heads, window, sin
     for longest in (most, most + 1):
         q = [longest, 1, most // 2 + 9, 0, longest - 1]
         Case(q, [longest, 300, 700, 40, 1285], heads, kv_heads, dim, 48, seed=longest).check(window, sinks)
+
+
+def test_calls_without_rows_and_in_inference_mode():
+    from mixed_lora_projection_gb300 import PagedAttention, add_rms_norm, add_rms_norm_fp8, kv_append
+    x, w = torch.ones(0, 128, dtype=BF16, device=DEV), torch.ones(128, dtype=BF16, device=DEV)
+    y, h = add_rms_norm(x, w, x.clone())
+    q8, s, _ = add_rms_norm_fp8(x, w, group=32)
+    assert y.shape == h.shape == q8.shape == (0, 128) and s.shape == (0, 4)
+    c = Case([0, 0], [20, 0], 4, 2, 64, 16)
+    k0 = c.k.clone()
+    cos = torch.ones(32, 8, device=DEV)
+    assert kv_append(c.q, c.k[0, :0], c.v[0, :0], c.off, c.kv, c.table, c.k, c.v, cos, cos).shape == (0, 4, 64)
+    assert c.run().shape == (0, 4, 64) and torch.equal(c.k, k0)
+    c = Case([3, 40], [20, 60], 4, 2, 64, 16)
+    ref = c.run()
+    with torch.inference_mode():
+        with PagedAttention(4, 2, 64, 16, 64, 2) as attn:
+            assert torch.equal(c.run(attn), ref)
+        x = torch.ones(3, 128, dtype=BF16, device=DEV)
+        y, h = add_rms_norm(x, torch.nn.Parameter(w), x)
+        assert bool((h == 2).all()) and not y.requires_grad
