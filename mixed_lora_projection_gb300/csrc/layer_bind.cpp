@@ -86,15 +86,25 @@ double to_double(PyObject* o) {
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     return v;
 }
-void* stream_of(PyObject* o, at::Device device) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
-    static PyObject* const name = PyUnicode_InternFromString("cuda_stream");
-    THPObjectPtr v(PyObject_GetAttr(o, name));
-    if (!v) throw python_error();
-    void* p = PyLong_AsVoidPtr(v.get());
-    if (!p && PyErr_Occurred()) throw python_error();
-    return p;
-}
+// The stream a call runs on: `o`, or the device's current one. A given stream is the current one while the call lasts,
+// so that the outputs allocated in it come from that stream's memory: a block of another stream's may still be read by
+// work queued there, and would go back to it when the output is dropped, whether or not this call has run.
+struct OnStream {
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    void* handle;
+    OnStream(PyObject* o, at::Device device) {
+        if (o == Py_None) {
+            handle = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+            return;
+        }
+        static PyObject* const name = PyUnicode_InternFromString("cuda_stream");
+        THPObjectPtr v(PyObject_GetAttr(o, name));
+        if (!v) throw python_error();
+        handle = PyLong_AsVoidPtr(v.get());
+        if (!handle && PyErr_Occurred()) throw python_error();
+        guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), device.index()));
+    }
+};
 template <class F>
 int unlocked(F&& call) {                               // the call may wait for room in the stream's queue
     int rc;
@@ -200,6 +210,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float eps = (float)to_double(a[3]), offset = (float)to_double(a[4]);
     if (given(a[2])) rr = rows_of(tensor(a[2], "residual"), rows, width, kBf16, dev, "residual");
     const c10::cuda::CUDAGuard guard(dev);
+    const OnStream stream(a[9], dev);
     float* sp = nullptr;
     if (given(a[5])) out = tensor(a[5], "out");
     else out = empty({rows, width}, group < 0 ? kBf16 : kFp8, dev);
@@ -221,10 +232,9 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (given(a[6])) h = tensor(a[6], "h_out");
     else if (given(a[2])) h = empty({rows, width}, kBf16, dev);
     if (h.defined()) hr = rows_of(h, rows, width, kBf16, dev, "h_out");
-    void* const stream = stream_of(a[9], dev);
     check(unlocked([&] {
               return g_norm(xr.p, xr.stride, rr.p, rr.stride, wp, offset, eps, (int)rows, (int)width, hr.p, hr.stride, yr.p, yr.stride, qr.p,
-                            qr.stride, sp, group < 0 ? 0 : group, stream);
+                            qr.stride, sp, group < 0 ? 0 : group, stream.handle);
           }),
           "lora_linear_add_rms_norm");
     THPObjectPtr o(given(a[5]) ? same(a[5]) : THPVariable_Wrap(out));
@@ -263,6 +273,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Heads qr, orr;
     int heads = 0;
     const c10::cuda::CUDAGuard guard(dev);
+    const OnStream stream(a[11], dev);
     THPObjectPtr out(same(given(a[0]) && given(a[10]) ? a[10] : a[0]));
     if (given(a[0]) && (rot || given(a[10]))) {
         const at::Tensor& q = tensor(a[0], "q");
@@ -273,10 +284,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(o.sizes() == q.sizes(), "q_out must have q's shape");
         orr = heads_of(o, heads, c.head_dim, dev, "q_out");
     }
-    void* const stream = stream_of(a[11], dev);
     check(unlocked([&] {
               return g_append(&c, qr.p, qr.stride, qr.head, orr.p, orr.stride, orr.head, heads, kr.p, kr.stride, kr.head, vr.p, vr.stride,
-                              vr.head, cp, sp, rot, positions, stream);
+                              vr.head, cp, sp, rot, positions, stream.handle);
           }),
           "lora_linear_kv_append");
     return out.release();
@@ -298,13 +308,13 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Heads qr = heads_of(q, heads, dim, dev, "q");
     const float scale = given(a[10]) ? (float)to_double(a[10]) : (float)(1.0 / std::sqrt((double)dim));
     const int window = to_int(a[11], "window"), sinks = to_int(a[12], "sinks");
+    const OnStream stream(a[14], dev);
     THPObjectPtr out(given(a[13]) ? same(a[13]) : THPVariable_Wrap(empty(q.sizes(), kBf16, dev)));
     const at::Tensor& o = tensor(out.get(), "out");
     TORCH_CHECK_VALUE(o.sizes() == q.sizes(), "out must have q's shape");
     const Heads orr = heads_of(o, heads, dim, dev, "out");
-    void* const stream = stream_of(a[14], dev);
     check(unlocked([&] {
-              return g_attend(handle, &c, qr.p, qr.stride, qr.head, orr.p, orr.stride, orr.head, scale, window, sinks, stream);
+              return g_attend(handle, &c, qr.p, qr.stride, qr.head, orr.p, orr.stride, orr.head, scale, window, sinks, stream.handle);
           }),
           "lora_linear_attn_forward");
     return out.release();

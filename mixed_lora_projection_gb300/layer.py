@@ -8,6 +8,10 @@ Arguments are checked and marshalled by ``csrc/layer_bind.cpp``; every step runs
 ``q_offsets`` is the host list that ``LoraLinear.forward`` takes as ``seg_offsets``; ``kv_lens``
 and ``block_table`` are int32 tensors on the device, read when the call runs, so that a captured
 decode step can be replayed as the caches grow.
+
+``stream``: a call runs on it as under ``torch.cuda.stream(stream)``. What it allocates belongs to that
+stream; that the inputs are ready there, and that another stream waits before it uses the outputs, is the
+caller's to see to.
 """
 from __future__ import annotations
 

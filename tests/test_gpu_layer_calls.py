@@ -1,0 +1,67 @@
+"""How the operators between the projections are called, on a GPU: streams, aliases, refusals, calls of many
+sequences. Tolerances are those that test_gpu_layer.py derives."""
+import pytest
+import torch
+
+from test_gpu_layer import BF16, BF16_TOL, DEV, Case, gen, norm_ref, randn, within
+
+pytestmark = pytest.mark.gpu
+
+
+def stream_of_block(t):
+    """The stream whose pool a tensor's memory is from."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("no block of the allocator")
+
+
+# name -> call(stream), its outputs; inputs are made once
+def operators():
+    from mixed_lora_projection_gb300 import PagedAttention, add_rms_norm, add_rms_norm_fp8, kv_append
+    g = gen(1)
+    c = Case([1, 40], [90, 400], 8, 2, 128, 16)
+    x, r, w = randn(g, 256, 1024), randn(g, 256, 1024), randn(g, 1024)
+    k, v = randn(g, 41, 2, 128), randn(g, 41, 2, 128)
+    cos, sin = torch.rand(400, 32, generator=g, device=DEV), torch.rand(400, 32, generator=g, device=DEV)
+    attn = PagedAttention(8, 2, 128, 16, 41, 2)
+    return {
+        "norm": lambda s: add_rms_norm(x, w, r, stream=s),
+        "norm to 8 bits": lambda s: add_rms_norm_fp8(x, w, r, group=64, stream=s),
+        "append": lambda s: (kv_append(c.q, k, v, c.off, c.kv, c.table, c.k, c.v, cos, sin, stream=s),),
+        "attention": lambda s: (attn.forward(c.q, c.k, c.v, c.off, c.kv, c.table, stream=s),),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "norm to 8 bits", "append", "attention"])
+def test_outputs_belong_to_the_stream_of_the_call(name):
+    call = operators()[name]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    here = torch.cuda.current_stream().cuda_stream
+    for out in call(None):
+        assert stream_of_block(out) == here
+    torch.cuda.synchronize()                                  # one handle's calls go one after another
+    for out in call(s):
+        assert stream_of_block(out) == s.cuda_stream
+    assert torch.cuda.current_stream().cuda_stream == here
+    # a buffer of this stream, freed with its reader still queued, is not the call's to write
+    sizes = [(t.shape, t.dtype) for t in want]
+    old = [torch.full(shape, 3.0, device=DEV).to(dtype) for shape, dtype in sizes]
+    torch.cuda._sleep(20_000_000)
+    kept = [t.clone() for t in old]
+    del old
+    got = call(s)
+    torch.cuda.synchronize()
+    for k, g, w in zip(kept, got, want):
+        assert bool((k.float() == 3).all())
+        assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
+    # and outputs dropped before the call has run are not this stream's to write
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    del got
+    call(s)
+    new = [torch.full(shape, 5.0, device=DEV).to(dtype) for shape, dtype in sizes]
+    torch.cuda.synchronize()
+    assert all(bool((t.float() == 5).all()) for t in new)
