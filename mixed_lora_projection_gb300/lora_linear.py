@@ -107,6 +107,15 @@ def host_chunks(T) -> list:
     return [bounds[i] for i in range(n.value + 1)]
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on `stream` (None: the current one), from that stream's memory: a block of another
+    stream's may still be read by work queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def w4_repack(src: torch.Tensor, dst: torch.Tensor | None = None,
               stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """4-bit base weight, plain layout (uint8 [d_out, d_in/2], low nibble = even input,
@@ -115,7 +124,7 @@ def w4_repack(src: torch.Tensor, dst: torch.Tensor | None = None,
     if src.dtype != torch.uint8 or not src.is_contiguous() or src.device.type != "cuda":
         raise TypeError("src must be a contiguous uint8 CUDA tensor")
     if dst is None:
-        dst = torch.empty_like(src)
+        dst = _empty(src.shape, src.dtype, src.device, stream)
     if dst.dtype != torch.uint8 or not dst.is_contiguous() or dst.device != src.device or dst.numel() != src.numel():
         raise TypeError("dst must be a contiguous uint8 tensor of src's size on src's device")
     s = stream if stream is not None else torch.cuda.current_stream(src.device)
@@ -173,10 +182,11 @@ class LoraLinear:
 
     def forward(self, x: torch.Tensor, seg_offsets, seg_ids, W: torch.Tensor, A, B, scales,
                 y: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
-        """Y for the batch x [T, d_in]; enqueued on `stream` (default: the current stream)."""
+        """Y for the batch x [T, d_in]; enqueued on `stream` (default: the current stream), to which a Y allocated
+        here belongs, as under ``torch.cuda.stream(stream)``."""
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, self.d_out), dtype=torch.bfloat16, device=self.device)
+            y = _empty((T, self.d_out), torch.bfloat16, self.device, stream)
         off, _ = _i32(seg_offsets)
         ids, n = _i32(seg_ids)
         a_arr, b_arr, s_arr, na = self._adapters(A, B, scales)
@@ -195,7 +205,7 @@ class LoraLinear:
             raise TypeError("Wq must be a contiguous uint8 tensor on the handle's device")
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, self.d_out), dtype=torch.bfloat16, device=self.device)
+            y = _empty((T, self.d_out), torch.bfloat16, self.device, stream)
         off, _ = _i32(seg_offsets)
         ids, n = _i32(seg_ids)
         a_arr, b_arr, s_arr, na = self._adapters(A, B, scales)

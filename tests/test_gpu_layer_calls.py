@@ -33,9 +33,25 @@ def operators():
     }
 
 
-@pytest.mark.parametrize("name", ["norm", "norm to 8 bits", "append", "attention"])
+def projections():
+    from mixed_lora_projection_gb300 import LoraLinear, w4_repack
+    g = gen(2)
+    x, w = randn(g, 48, 256), randn(g, 512, 256)
+    a, b = randn(g, 16, 256), randn(g, 512, 16)
+    q = torch.randint(0, 256, (512, 128), generator=g, device=DEV, dtype=torch.uint8)
+    scales = randn(g, 2, 512)
+    ll = LoraLinear(256, 512, 16, 48)
+    packed = w4_repack(q)
+    return {
+        "projection": lambda s: (ll.forward(x, [0, 20, 48], [0, 1], w, [a], [b], [1.0], stream=s),),
+        "4-bit projection": lambda s: (ll.forward_w4(x, [0, 20, 48], [0, 1], packed, scales, [a], [b], [1.0], stream=s),),
+        "4-bit layout": lambda s: (w4_repack(q, stream=s),),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "norm to 8 bits", "append", "attention", "projection", "4-bit projection", "4-bit layout"])
 def test_outputs_belong_to_the_stream_of_the_call(name):
-    call = operators()[name]
+    call = {**operators(), **projections()}[name]
     want = [t.clone() for t in call(None)]
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
