@@ -230,7 +230,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         sp = static_cast<float*>(pointer(scales, at::kFloat, dev, "scales"));
     }
     if (given(a[6])) h = tensor(a[6], "h_out");
-    else if (given(a[2])) h = empty({rows, width}, kBf16, dev);
+    else if (given(a[2]) || (yr.p == xr.p && rows)) h = empty({rows, width}, kBf16, dev);   // (y over x: h is x no more)
     if (h.defined()) hr = rows_of(h, rows, width, kBf16, dev, "h_out");
     check(unlocked([&] {
               return g_norm(xr.p, xr.stride, rr.p, rr.stride, wp, offset, eps, (int)rows, (int)width, hr.p, hr.stride, yr.p, yr.stride, qr.p,

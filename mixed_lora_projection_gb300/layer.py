@@ -44,7 +44,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
                  weight_offset: float = 0.0, out: torch.Tensor | None = None, h_out: torch.Tensor | None = None,
                  stream: torch.cuda.Stream | None = None):
     """(y, h) of the rows x [rows, width]: h = x + residual (bf16) and its norm y (bf16). Without a
-    residual h is x itself and nothing is written for it. ``h_out`` may be ``residual`` or ``x``."""
+    residual h is x itself and nothing is written for it (a copy of x, where ``out`` is x). ``h_out`` may be
+    ``residual`` or ``x``."""
     return (_bind or _load()).norm(x, weight, residual, eps, weight_offset, out, h_out, None, -1, stream)
 
 

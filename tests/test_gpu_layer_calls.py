@@ -81,3 +81,16 @@ def test_outputs_belong_to_the_stream_of_the_call(name):
     new = [torch.full(shape, 5.0, device=DEV).to(dtype) for shape, dtype in sizes]
     torch.cuda.synchronize()
     assert all(bool((t.float() == 5).all()) for t in new)
+
+
+@pytest.mark.parametrize("rows,width", [(1, 64), (5, 520), (300, 5120), (0, 64)])
+def test_norm_over_its_input_returns_the_input_as_h(rows, width):
+    from mixed_lora_projection_gb300 import add_rms_norm
+    g = gen(rows)
+    big, w = randn(g, rows, width + 64), randn(g, width)
+    for x in (big[:, 64:], randn(g, rows, width)):
+        before = x.clone()
+        _, want = norm_ref(before, None, w, 0.0, 1e-6)
+        y, h = add_rms_norm(x, w, out=x)
+        assert y is x and torch.equal(h, before)
+        within(y, want, want.abs() * BF16_TOL)
