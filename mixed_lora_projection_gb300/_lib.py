@@ -67,6 +67,7 @@ SIGNATURES = {
     "lora_linear_attn_forward": (C.c_int, [P, CACHE, P, LL, LL, P, LL, LL, C.c_float, C.c_int, C.c_int, P]),
     "lora_linear_attn_validate": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, CACHE, P, LL, LL,
                                             P, LL, LL, C.c_float, C.c_int, C.c_int]),
+    "lora_linear_attn_set_option": (C.c_int, [P, C.c_int, C.c_longlong]),
     "lora_linear_attn_status": (C.c_int, [P, C.c_int]),
     "lora_linear_attn_destroy": (C.c_int, [P]),
 }

@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) {
+                    if ((a.debug_stall && issued + 1 >= a.debug_stall) ||
+                        !wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) {
                         ok = false;
                         break;
                     }
@@ -228,10 +229,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             w.at += t1 - t0;
             if ((unsigned long long)prefix[w.i + 1] * n_kv <= w.at) ++w.i;
         }
-        if (!ok)                         // gave up: wait for the copies in flight before the block may end
+        // The copies in flight land before the block may end, whoever gave up: consumers that did wait for none.
+        if (lane == 0)
             for (int k = max(0, issued - slots); k < issued; ++k)
-                if (lane == 0)
-                    wait_bounded(smem_addr(&full[k % slots]), (uint32_t)((k / slots) & 1), abort_flag, a.status, limit, false);
+                wait_bounded(smem_addr(&full[k % slots]), (uint32_t)((k / slots) & 1), abort_flag, a.status, limit, false);
         return;
     }
 
@@ -243,8 +244,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     const int g = p.group;
     int slot = 0;
     uint32_t phase = 0;
-    // after a wait that ran out the warps run on without data, so that their barriers stay matched;
-    // the status word says that the output is incomplete
+    // After a wait that ran out a warp runs on without data, so that the warps' barriers stay matched; the status
+    // word says that the output is incomplete. It frees no slot any more: what it did not wait for may still be in
+    // flight, and the producer would load over it.
+    bool ok = true;
     while (w.at < w.end) {
         const uint32_t nt = prefix[w.i + 1] - prefix[w.i];
         if (nt == 0) {
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 for (int n = 0; n < kOwn / 8; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[x][n][e] = 0.f;
-            wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
+            ok = ok && wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
             {
                 const int tok = warp * kOwn + (lane & 7) + ((lane >> 4) & 1) * 8;
                 const uint32_t krow = ring + (uint32_t)slot * S::kSlot + (uint32_t)tok * 128;
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 if (gc == 0) smax[warp * kRows + gr + 8 * h] = mx[h];
             }
             consumer_sync();
-            if (lane == 0) mbar_arrive(smem_addr(&empty[kslot]));
+            if (ok && lane == 0) mbar_arrive(smem_addr(&empty[kslot]));
             // ---- weights
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                     }
                 }
             }
-            wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
+            ok = ok && wait_warp(smem_addr(&full[slot]), phase, abort_flag, a.status, limit);
             const uint32_t vt = ring + (uint32_t)slot * S::kSlot;
             // tokens that no row sees: past the last one, or in the sinks' last tile and the window's first
             if (r.len - j0 < kTk) {
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&empty[slot]));
+            if (ok && lane == 0) mbar_arrive(smem_addr(&empty[slot]));
             if (++slot == slots) {
                 slot = 0;
                 phase ^= 1;

@@ -2,6 +2,7 @@
 // attention handle and its workspace, launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -186,6 +187,7 @@ struct lora_attn {
     int num_sms = 0;
     int* status = nullptr;              // status word; then the prompt kernel's two counters
     unsigned long long wait_limit_ns = 4000000000ull;
+    int debug_stall = 0;
     EncodeTiledFn encode = nullptr;
     float* part_o = nullptr;            // sums of split units, their maxima and sums of weights
     float2* part_ml = nullptr;
@@ -457,6 +459,7 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = h->status;
     p.wait_limit_ns = h->wait_limit_ns;
+    p.debug_stall = h->debug_stall;
     p.stream = static_cast<cudaStream_t>(stream);
     // sequences with few rows and long ones go to different kernels
     const int g = h->n_heads / h->n_kv;
@@ -487,6 +490,22 @@ extern "C" int lora_linear_attn_forward(lora_attn* h, const lora_kv_cache* cache
         if (rc != LORA_OK) return rc;
     }
     return few.n ? run_decode(h, p, few) : LORA_OK;
+}
+
+extern "C" int lora_linear_attn_set_option(lora_attn* h, int option, long long value) {
+    if (!h) return LORA_EINVAL;
+    switch (option) {
+        case LORA_OPT_WAIT_LIMIT_US:
+            if (value < 1000 || value > 60000000) return LORA_EINVAL;
+            h->wait_limit_ns = (unsigned long long)value * 1000ull;
+            return LORA_OK;
+        case LORA_OPT_DEBUG_STALL:
+            if (value < 0 || value > INT_MAX) return LORA_EINVAL;
+            h->debug_stall = (int)value;
+            return LORA_OK;
+        default:
+            return LORA_EINVAL;
+    }
 }
 
 extern "C" int lora_linear_attn_status(lora_attn* h, int reset) {

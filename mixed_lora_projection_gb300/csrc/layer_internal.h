@@ -85,6 +85,7 @@ struct AttnParams {
     float scale_log2;                   // softmax in base 2: scale * log2(e)
     int* status;
     unsigned long long wait_limit_ns;
+    int debug_stall;                    // n > 0: a load warp issues n - 1 pieces of K and V and no more (tests)
     cudaStream_t stream;
 };
 

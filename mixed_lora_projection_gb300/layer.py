@@ -116,5 +116,8 @@ class PagedAttention:
         return (_bind or _load()).attend(self._ptr, self.n_heads, self.head_dim, self.device.index, q, k_cache, v_cache,
                                          q_offsets, kv_lens, block_table, scale, window, sinks, out, stream)
 
+    def set_option(self, option: int, value: int) -> None:
+        _check(self._lib.lora_linear_attn_set_option(self._h, option, int(value)), "lora_linear_attn_set_option")
+
     def status(self, reset: bool = False) -> int:
         return self._lib.lora_linear_attn_status(self._h, 1 if reset else 0)

@@ -94,3 +94,39 @@ def test_norm_over_its_input_returns_the_input_as_h(rows, width):
         y, h = add_rms_norm(x, w, out=x)
         assert y is x and torch.equal(h, before)
         within(y, want, want.abs() * BF16_TOL)
+
+
+def give_up(c, stalls, **kw):
+    """A call whose load warps stop after some pieces ends with LORA_ETIMEOUT; the handle then works as before."""
+    from mixed_lora_projection_gb300 import PagedAttention, _lib as L
+    with PagedAttention(c.heads, c.kv_heads, c.dim, c.page, c.off[-1], len(c.q_lens)) as attn:
+        want = c.run(attn, **kw)
+        attn.set_option(L.OPT_WAIT_LIMIT_US, 20000)
+        for stall in stalls:
+            attn.set_option(L.OPT_DEBUG_STALL, stall)
+            attn.forward(c.q, c.k, c.v, c.off, c.kv, c.table, **kw)
+            assert attn.status() == L.LORA_ETIMEOUT
+            assert attn.status(reset=True) == L.LORA_ETIMEOUT
+            assert attn.status() == L.LORA_OK
+            attn.set_option(L.OPT_DEBUG_STALL, 0)
+            assert torch.equal(c.run(attn, **kw), want)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim", [
+    ([1], [20000], 8, 8, 128), ([1] * 3, [9000, 0, 12000], 16, 16, 64), ([8] * 2, [7000, 16000], 24, 12, 256),
+    ([1] * 70, [40 * i + 1 for i in range(70)], 8, 8, 128)])
+def test_decode_gives_up_and_goes_on(q_lens, kv_lens, heads, kv_heads, dim):
+    c = Case(q_lens, kv_lens, heads, kv_heads, dim, 64)
+    give_up(c, (1, 2, 3, 5))
+    give_up(c, (2, 4), window=3000, sinks=70)
+
+
+def test_attention_handle_options():
+    from mixed_lora_projection_gb300 import LoraError, PagedAttention, _lib as L
+    with PagedAttention(4, 2, 64, 16, 8, 4) as attn:
+        for option, value in ((L.OPT_WAIT_LIMIT_US, 999), (L.OPT_WAIT_LIMIT_US, 60000001), (L.OPT_DEBUG_STALL, -1),
+                              (L.OPT_DEBUG_STALL, 1 << 31), (L.OPT_TILE_N, 0), (0, 0)):
+            with pytest.raises(LoraError):
+                attn.set_option(option, value)
+        attn.set_option(L.OPT_WAIT_LIMIT_US, 1000)
+        attn.set_option(L.OPT_DEBUG_STALL, 0)

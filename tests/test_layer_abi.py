@@ -149,3 +149,8 @@ def test_binding_refuses_what_is_no_tensor(lib):
         add_rms_norm_fp8(x, x[0], group=-1)
     with pytest.raises(TypeError):
         kv_append(None, None, None, [0, 4], None, None, None, None)
+
+
+def test_handle_options_refuse_a_missing_handle(lib):
+    for option, value in ((2, 20000), (3, 1), (99, 0)):
+        assert lib.lora_linear_attn_set_option(None, option, value) == EINVAL
