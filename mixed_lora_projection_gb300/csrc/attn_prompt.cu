@@ -409,7 +409,9 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                 const int pg = __shfl_sync(0xffffffffu, page, from & 31), tk = __shfl_sync(0xffffffffu, tok, from & 31);
                 const bool mine = gi < grans && pg >= 0;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
-                if (!wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) return false;
+                if ((a.debug_stall && issued + 1 >= a.debug_stall) ||
+                    !wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit))
+                    return false;
                 const uint32_t bar = smem_addr(edge ? &raw[edges % S::kSlots] : &full[slot]);
                 edges += edge;
                 blanked = (blanked & ~(1u << slot)) | (uint32_t)edge << slot;
@@ -495,9 +497,12 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                 at += (uint32_t)(t1 - t0);
             }
             ok = wait_warp(smem_addr(&done[count & 1]), (uint32_t)((count >> 1) & 1) ^ 1, abort_flag, a.status, limit);
+            // After a wait that ran out nothing is written or told: a warp may still be at the piece in this place, and
+            // where its rows go is read from it to the end. The abort flag ends the warps that listen.
+            if (!ok) break;
             const int gap = a.window && u.r.first - a.window >= a.sinks ? u.r.s_tiles - 1 - t0 : kNoTile;
             const int tail = u.len % kTk ? u.r.s_tiles + u.len / kTk - u.r.lo_tile - t0 : kNoTile;
-            if (lane == 0) {             // after a wait that ran out: the end, for the warps that still listen
+            if (lane == 0) {
                 Piece& w = pieces[count & 1];
                 w.head = u.head;
                 w.tok0 = u.tok0;
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                 w.s_tiles = u.r.s_tiles;
                 w.lo_tile = u.r.lo_tile;
                 w.t0 = t0;
-                w.n = last || !ok ? -1 : t1 - t0;
+                w.n = last ? -1 : t1 - t0;
                 w.part = part;
                 w.k0 = issued;
                 w.gap = gap;
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
             __syncwarp();
             ++count;
             if (last) break;
-            if (!ok || t0 == t1) continue;
+            if (t0 == t1) continue;
             t_end = t1;
             table = a.c.table + u.seq * a.c.table_stride;
             int page, tok, npage, ntok;
@@ -540,12 +545,14 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                 ntok = ftok;
             }
         }
-        if (!ok && lane == 0) {          // gave up: wait for the copies in flight before the block may end
+        // The copies in flight land before the block may end, whoever gave up.
+        if (lane == 0) {
             for (int k = max(0, issued - S::kSlots); k < issued; ++k)
                 if (!(blanked >> (k % S::kSlots) & 1))
                     wait_bounded(smem_addr(&full[k % S::kSlots]), (uint32_t)((k / S::kSlots) & 1), abort_flag, a.status, limit, false);
             for (int e = max(0, edges - S::kSlots); e < edges; ++e)
                 wait_bounded(smem_addr(&raw[e % S::kSlots]), (uint32_t)((e / S::kSlots) & 1), abort_flag, a.status, limit, false);
+            if (!ok) __threadfence();    // a unit may have been asked for and not waited for: before the counter is reset
         }
     } else if (warp == kQueryWarp) {
         // ------------------------------------------------------------ queries, tokens to blank
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                 if (lane < S::kPieces) mbar_arrive(smem_addr(&full[(k + lane) % S::kSlots]));
             }
         }
-        if (!ok && lane == 0)            // gave up: wait for the copies in flight before the block may end
+        if (lane == 0)                   // as the producer's
             for (int q = 0; q < S::kQ; ++q)
                 if (used[q]) wait_bounded(smem_addr(&q_full[q]), (used[q] - 1) & 1, abort_flag, a.status, limit, false);
     } else if (warp >= kMmaWarp) {

@@ -121,6 +121,16 @@ def test_decode_gives_up_and_goes_on(q_lens, kv_lens, heads, kv_heads, dim):
     give_up(c, (2, 4), window=3000, sinks=70)
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim", [
+    ([300, 40, 700], [5000, 3000, 9000], 8, 8, 64), ([100, 90], [9000, 5000], 16, 16, 64),       # two tiles of rows, one
+    ([300, 40, 700], [5000, 3000, 9000], 12, 2, 128), ([20, 21], [9000, 5000], 24, 4, 128),
+    ([300, 40, 700], [5000, 3000, 9000], 6, 3, 256), ([260, 30, 1], [7000, 3000, 9000], 24, 12, 256)])
+def test_prompt_gives_up_and_goes_on(q_lens, kv_lens, heads, kv_heads, dim):
+    c = Case(q_lens, kv_lens, heads, kv_heads, dim, 64)
+    give_up(c, (1, 2, 3, 6))
+    give_up(c, (1, 2, 3, 4), window=3000, sinks=70)            # values to blank among the first pieces
+
+
 def test_attention_handle_options():
     from mixed_lora_projection_gb300 import LoraError, PagedAttention, _lib as L
     with PagedAttention(4, 2, 64, 16, 8, 4) as attn:
