@@ -96,7 +96,8 @@ typedef struct lora_kv_cache {
  *     (a_i, b_i) -> (a_i cos - b_i sin, b_i cos + a_i sin),  a = x[0 : rot/2], b = x[rot/2 : rot]
  * with cos, sin at [position][i]; features rot and up are copied.
  *   q, q_stride, q_head_stride          device bf16 [T, n_heads, head_dim], or NULL with q_out.
- *   q_out, qo_stride, qo_head_stride    device bf16; may be q itself (same strides).
+ *   q_out, qo_stride, qo_head_stride    device bf16; may be q itself (same strides), and shares no place with k
+ *                                       or v (which may lie beside it, as slices of one buffer).
  *   k, v and their strides              device bf16 [T, n_kv_heads, head_dim].
  *   cos, sin           device fp32 [n_positions, rot / 2], contiguous, 16-byte aligned; NULL when rot = 0. A
  *                      position outside [0, n_positions) uses the last row.

@@ -21,26 +21,37 @@ namespace {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// The bytes that a strided buffer covers: `outer` rows of `extent` bytes, `stride` bytes apart (a
-// row's inner axis may itself be strided; its extent then reaches the last byte of the row).
+// The bytes that a strided buffer covers: `outer` rows of `extent` bytes, `stride` bytes apart; a row is `inner`
+// vectors of `width` bytes, `step` bytes apart (0: one). A single row's vectors are the rows.
 struct Span {
-    uintptr_t first = 0, last = 0, stride = 0, extent = 0;
+    uintptr_t first = 0, last = 0, stride = 0, extent = 0, step = 0, width = 0;
 };
 Span span(const void* p, long long outer, long long so, long long inner, long long si, long long width, int elem) {
     Span s;
     if (!p || outer <= 0 || inner <= 0) return s;
+    if (outer == 1) {
+        outer = inner;
+        so = si;
+        inner = 1;
+    }
     s.first = reinterpret_cast<uintptr_t>(p);
-    s.stride = (uintptr_t)(so * elem);
+    s.stride = outer > 1 ? (uintptr_t)(so * elem) : 0;
+    s.step = inner > 1 ? (uintptr_t)(si * elem) : 0;
+    s.width = (uintptr_t)(width * elem);
     s.extent = (uintptr_t)(((inner - 1) * si + width) * elem);
     s.last = s.first + (uintptr_t)(outer - 1) * s.stride + s.extent;
     return s;
 }
-// Whether two buffers may share a byte. Column slices of one row-strided buffer do not.
+// Whether two buffers may share a byte. Column slices of one row-strided buffer do not, nor vectors that lie beside
+// one another within a row.
 bool meet(const Span& a, const Span& b) {
     if (!(a.first < b.last && b.first < a.last)) return false;
     if (a.stride == 0 || a.stride != b.stride) return true;
     const uintptr_t d = a.first <= b.first ? (b.first - a.first) % a.stride : (a.stride - (a.first - b.first) % a.stride) % a.stride;
-    return !(d >= a.extent && d + b.extent <= a.stride);
+    if (d >= a.extent && d + b.extent <= a.stride) return false;
+    if (a.step == 0 || a.step != b.step || a.stride % a.step) return true;
+    const uintptr_t e = d % a.step;
+    return !(e >= a.width && e + b.width <= a.step);
 }
 
 constexpr long long kMaxStride = 1ll << 38;   // elements: a tensor map's strides stay under 2^40 bytes
@@ -359,8 +370,8 @@ extern "C" int lora_linear_kv_append(const lora_kv_cache* cache, const void* q, 
         meet(vc, so))
         return LORA_EINVAL;
     const bool in_place = q && q == q_out && q_stride == qo_stride && q_head_stride == qo_head_stride;
-    // q, k and v may be slices of one buffer, so an output in place is checked against q alone
-    if (q && !in_place && (meet(so, sq) || meet(so, sk) || meet(so, sv))) return LORA_EINVAL;
+    // (q, k and v may be slices of one buffer)
+    if (q && ((!in_place && meet(so, sq)) || meet(so, sk) || meet(so, sv))) return LORA_EINVAL;
     AppendParams p;
     p.c = view(cache);
     p.q = q;

@@ -140,3 +140,20 @@ def test_attention_handle_options():
                 attn.set_option(option, value)
         attn.set_option(L.OPT_WAIT_LIMIT_US, 1000)
         attn.set_option(L.OPT_DEBUG_STALL, 0)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 70])
+def test_append_in_place_beside_keys_and_values(rows):
+    """q, k and v of each head side by side in one buffer; the turned queries over themselves."""
+    from mixed_lora_projection_gb300 import LoraError, kv_append
+    c = Case([rows], [90], 4, 4, 64, 16)
+    g = gen(rows)
+    y = randn(g, rows, 4, 3, 64)
+    q, k, v = y.clone().unbind(2)
+    cos, sin = torch.ones(90, 32, device=DEV), torch.zeros(90, 32, device=DEV)
+    out = kv_append(y[:, :, 0], y[:, :, 1], y[:, :, 2], c.off, c.kv, c.table, c.k, c.v, cos, sin, q_out=y[:, :, 0])
+    pg, sl = c.slots(0, 90)
+    assert torch.equal(out, q) and torch.equal(c.k[pg[-rows:], sl[-rows:]], k) and torch.equal(c.v[pg[-rows:], sl[-rows:]], v)
+    assert torch.equal(y[:, :, 1], k) and torch.equal(y[:, :, 2], v)
+    with pytest.raises(LoraError):                             # keys in the queries' place
+        kv_append(y[:, :, 0], y[:, :, 0], y[:, :, 2], c.off, c.kv, c.table, c.k, c.v, cos, sin, q_out=y[:, :, 0])

@@ -154,3 +154,49 @@ def test_binding_refuses_what_is_no_tensor(lib):
 def test_handle_options_refuse_a_missing_handle(lib):
     for option, value in ((2, 20000), (3, 1), (99, 0)):
         assert lib.lora_linear_attn_set_option(None, option, value) == EINVAL
+
+
+ECUDA = -3
+
+
+def accepts(lib, **kw):
+    """Whether an append passes the checks (on a machine without a GPU its launch fails; with one, these made-up
+    addresses must not be launched)."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses")
+    rc = append(lib, Cache(), **kw)
+    assert rc in (EINVAL, ECUDA)
+    return rc == ECUDA
+
+
+# queries over themselves, in rows of 4 + 2 + 2 heads of 64: q, k, v are slices, or share places they must not share
+FUSED = dict(q=5 * P, qs=512, qh=64, qo=5 * P, qos=512, qoh=64, k=5 * P + 512, ks=512, kh=64, v=5 * P + 768, vs=512, vh=64)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(k=5 * P), dict(v=5 * P), dict(k=5 * P + 384), dict(v=5 * P + 128), dict(k=5 * P + 1024), dict(v=5 * P + 512 - 128, vh=128),
+    dict(k=5 * P + 4 * 1024 + 256), dict(k=5 * P, ks=256)])
+def test_append_in_place_refuses_keys_and_values_in_the_queries(lib, bad):
+    assert append(lib, Cache(), **{**FUSED, **bad}) == EINVAL
+
+
+def test_append_in_place_takes_slices(lib):
+    assert accepts(lib, **FUSED)
+    # q, k and v of each head side by side: [rows, 2, 3, 64]
+    row = dict(heads=2, q=5 * P, qo=5 * P, k=5 * P + 128, v=5 * P + 256, **{n: 384 for n in ("qs", "qos", "ks", "vs")},
+               **{n: 192 for n in ("qh", "qoh", "kh", "vh")})
+    assert accepts(lib, **row)
+    assert not accepts(lib, **{**row, "k": 5 * P + 112})
+    assert not accepts(lib, **{**row, "v": 5 * P + 336})
+    # heads outermost, one after another
+    assert accepts(lib, **{**FUSED, **{n: 64 for n in ("qs", "qos", "ks", "vs")}, **{n: 320 for n in ("qh", "qoh", "kh", "vh")},
+                           "k": 5 * P + 4 * 640, "v": 5 * P + 6 * 640})
+
+
+def test_append_of_one_row_goes_by_its_heads(lib):
+    """A single row has no stride: q, k and v of each head side by side, whatever row strides are given."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses")
+    one = dict(heads=2, q=5 * P, qo=5 * P, k=5 * P + 128, v=5 * P + 256, qs=64, qos=64, ks=64, vs=64, qh=192, qoh=192, kh=192, vh=192)
+    assert append(lib, Cache(off=[0, 0, 0, 1]), **one) == ECUDA
+    assert append(lib, Cache(off=[0, 0, 0, 1]), **{**one, "k": 5 * P}) == EINVAL
