@@ -249,6 +249,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     ready(n, 12);
+    TORCH_CHECK_VALUE(given(a[0]) || !given(a[10]), "q_out goes with q");
     const at::Tensor &k = cuda_tensor(a[1], "k"), &v = tensor(a[2], "v");
     const at::Device dev = k.device();
     std::vector<int32_t> offsets;
@@ -274,7 +275,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int heads = 0;
     const c10::cuda::CUDAGuard guard(dev);
     const OnStream stream(a[11], dev);
-    THPObjectPtr out(same(given(a[0]) && given(a[10]) ? a[10] : a[0]));
+    THPObjectPtr out(same(given(a[10]) ? a[10] : a[0]));
     if (given(a[0]) && (rot || given(a[10]))) {
         const at::Tensor& q = tensor(a[0], "q");
         heads = (int)q.size(1);

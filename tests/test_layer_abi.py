@@ -200,3 +200,10 @@ def test_append_of_one_row_goes_by_its_heads(lib):
     one = dict(heads=2, q=5 * P, qo=5 * P, k=5 * P + 128, v=5 * P + 256, qs=64, qos=64, ks=64, vs=64, qh=192, qoh=192, kh=192, vh=192)
     assert append(lib, Cache(off=[0, 0, 0, 1]), **one) == ECUDA
     assert append(lib, Cache(off=[0, 0, 0, 1]), **{**one, "k": 5 * P}) == EINVAL
+
+
+def test_binding_refuses_an_output_for_no_queries(lib):
+    from mixed_lora_projection_gb300 import kv_append
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q_out"):
+        kv_append(None, x, x, [0, 4], None, None, None, None, q_out=x)
