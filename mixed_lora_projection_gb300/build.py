@@ -5,7 +5,8 @@ Compiles the library's translation units in parallel with nvcc for
 ``mixed_lora_projection_gb300/liblora_linear.so`` (CUDA runtime linked statically, no
 libcuda link: the tensor-map encoder is fetched through the runtime's driver entry
 point, so the library also loads on a machine without a GPU). The operators' Python
-binding, ``_layer_bind.so``, is the one unit compiled against PyTorch's headers.
+binding, ``_layer_bind.so``, is the one unit compiled against PyTorch's headers; where there is
+no PyTorch, run this file as a script, and the library alone is built.
 """
 from __future__ import annotations
 
@@ -40,52 +41,62 @@ def _sources():
 
 
 def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BIND)):
+    outputs = [LIB, BIND] if _torch_flags() else [LIB]
+    if not all(os.path.exists(f) for f in outputs):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    t = min(os.path.getmtime(f) for f in outputs)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
         os.path.join(ROOT, "include", h) for h in ("lora_linear.h", "lora_layer.h")]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _torch_flags() -> tuple[list, list] | None:
+    """How the binding is compiled and linked against PyTorch; None where there is no PyTorch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    root = os.path.dirname(torch.__file__)
+    libs = os.path.join(root, "lib")
+    return (["-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
+            ["-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Xlinker", f"-rpath={libs}"])
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Builds the library, and the binding where PyTorch is there. The library is linked first: it needs neither
+    PyTorch nor a binding that compiles."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
-    import torch
-    torch_dir = os.path.dirname(torch.__file__)
-    torch_flags = ["-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
-                   f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    torch_flags = _torch_flags()
     common = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include")]
 
-    def compile_one(src):
+    def compile_one(src, flags=()):
         obj = os.path.join(BUILD, src + ".o")
-        cmd = [nvcc, *ARCH, *common, "-c", os.path.join(CSRC, src), "-o", obj]
-        if src == BIND_SOURCE:
-            cmd += torch_flags
+        cmd = [nvcc, *ARCH, *common, "-c", os.path.join(CSRC, src), "-o", obj, *flags]
         if ptxas_info and src.endswith(".cu"):
             cmd += ["-Xptxas", "-v"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stdout + r.stderr
-
-    srcs = [*_sources(), BIND_SOURCE]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
-        results = list(ex.map(compile_one, srcs))
-    for _, log in results:
+        log = r.stdout + r.stderr
         if (verbose or ptxas_info) and log.strip():
             print(log, file=sys.stderr)
-    libs = os.path.join(torch_dir, "lib")
-    for target, objs, extra in (
-            (LIB, results[:-1], []),
-            (BIND, results[-1:], ["-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
-                                  "-ltorch_python",
-                                  "-Xlinker", f"-rpath={libs}"])):
-        r = subprocess.run([nvcc, *ARCH, "-shared", "-o", target + ".tmp", *[o for o, _ in objs], *extra],
-                           capture_output=True, text=True)
+        return obj
+
+    def link(target, objs, flags=()):
+        r = subprocess.run([nvcc, *ARCH, "-shared", "-o", target + ".tmp", *objs, *flags], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(target + ".tmp", target)
+
+    srcs = _sources()
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        objs = [ex.submit(compile_one, s) for s in srcs]
+        bind = ex.submit(compile_one, BIND_SOURCE, torch_flags[0]) if torch_flags else None
+        link(LIB, [o.result() for o in objs])
+        if bind:
+            link(BIND, [bind.result()], torch_flags[1])
     return LIB
 
 
