@@ -23,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblora_linear.so")
 BIND = os.path.join(PKG, "_layer_bind.so")
+BIND_FOR = os.path.join(BUILD, "layer_bind.for")       # the PyTorch and the Python that the binding was built for
 BIND_SOURCE = "layer_bind.cpp"
 SOURCES = ["kernels.cu", "kernels_w4.cu", "api.cpp", "planner.cpp", "noalloc.cu",
            "layer_ops.cu", "attn_decode.cu", "attn_prompt.cu", "layer_api.cpp"]
@@ -40,10 +41,22 @@ def _sources():
     return [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
 
 
+def bind_for() -> str:
+    """What a binding is built for; file times do not tell, so it says so itself (``built_for``)."""
+    import torch
+    return f"PyTorch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
 def _stale() -> bool:
-    outputs = [LIB, BIND] if _torch_flags() else [LIB]
+    outputs = [LIB]
+    if _torch_flags():
+        outputs += [BIND, BIND_FOR]
     if not all(os.path.exists(f) for f in outputs):
         return True
+    if BIND in outputs:
+        with open(BIND_FOR) as f:
+            if f.read() != bind_for():
+                return True
     t = min(os.path.getmtime(f) for f in outputs)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
         os.path.join(ROOT, "include", h) for h in ("lora_linear.h", "lora_layer.h")]
@@ -59,7 +72,7 @@ def _torch_flags() -> tuple[list, list] | None:
     root = os.path.dirname(torch.__file__)
     libs = os.path.join(root, "lib")
     return (["-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
-             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DLAYER_BIND_FOR="{bind_for()}"'],
             ["-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Xlinker", f"-rpath={libs}"])
 
 
@@ -97,6 +110,8 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         link(LIB, [o.result() for o in objs])
         if bind:
             link(BIND, [bind.result()], torch_flags[1])
+            with open(BIND_FOR, "w") as f:
+                f.write(bind_for())
     return LIB
 
 

@@ -335,4 +335,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_bind", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__layer_bind() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__layer_bind() {
+    PyObject* const m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", LAYER_BIND_FOR) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -20,6 +20,7 @@ import ctypes as C
 import torch
 
 from . import _lib as L
+from .build import bind_for
 from .lora_linear import LoraError, _check  # noqa: F401
 
 _bind = None
@@ -31,9 +32,12 @@ def _load():
     lib = L.load()
     try:
         from . import _layer_bind
+        built_for = getattr(_layer_bind, "built_for", "unknown")
     except ImportError as e:
-        raise RuntimeError("_layer_bind.so is not built for this PyTorch: run __graft_entry__.build() "
-                           "(or python -m mixed_lora_projection_gb300.build)") from e
+        built_for = str(e)
+    if built_for != bind_for():
+        raise RuntimeError(f"_layer_bind.so is not built for this PyTorch ({built_for}): run __graft_entry__.build() "
+                           "(or python -m mixed_lora_projection_gb300.build)")
     _layer_bind.bind(*(C.cast(f, C.c_void_p).value for f in (
         lib.lora_linear_add_rms_norm, lib.lora_linear_kv_append, lib.lora_linear_attn_forward)), _check)
     _bind = _layer_bind

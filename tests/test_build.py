@@ -15,6 +15,7 @@ b = importlib.util.module_from_spec(spec)
 spec.loader.exec_module(b)
 out = sys.argv[2]
 b.BUILD, b.LIB, b.BIND, b.SOURCES = out, os.path.join(out, "lib.so"), os.path.join(out, "bind.so"), ["planner.cpp"]
+b.BIND_FOR = os.path.join(out, "bind.for")
 """
 
 
@@ -34,3 +35,19 @@ def test_library_is_linked_whatever_becomes_of_the_binding(tmp_path):
     r = child(tmp_path, "b.BIND_SOURCE = os.path.join(out, 'broken.cpp')\nb.build()\n")
     assert r.returncode != 0 and "not this one" in r.stderr
     assert (tmp_path / "lib.so").exists() and not (tmp_path / "bind.so").exists()
+
+
+def test_binding_of_another_pytorch_is_stale_and_refused(lib, tmp_path, monkeypatch):
+    from mixed_lora_projection_gb300 import build, layer
+    assert not build._stale()
+    layer._load()
+    monkeypatch.setattr(layer, "_bind", None)
+    monkeypatch.setattr(layer, "bind_for", lambda: "PyTorch 1.0, cpython-30")
+    with pytest.raises(RuntimeError, match="not built for this PyTorch"):
+        layer._load()
+    assert layer._bind is None
+    other = tmp_path / "for"
+    monkeypatch.setattr(build, "BIND_FOR", str(other))
+    assert build._stale()                                      # one that does not say
+    other.write_text("PyTorch 1.0, cpython-30")
+    assert build._stale()
