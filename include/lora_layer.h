@@ -48,7 +48,8 @@ extern "C" {
  *                              `residual` or `x` itself (same pointer and stride).
  *   y, y_stride                device bf16 [rows, width], or NULL. May be `x` itself.
  *   q8, q8_stride              device e4m3 [rows, width], or NULL: y in 8 bits,
- *                              q = e4m3(y / s) (nearest even, saturating),
+ *                              q = e4m3(y r) (nearest even, saturating) with r = 1 / s rounded to
+ *                              fp32: beside a tie the code may be y / s's neighbour,
  *   scales, group              s = max(max|y| / 448, 2^-100), fp32: over the whole row
  *                              (group 0, scales [rows]) or over every `group` features
  *                              (32, 64, 128 or 256; scales [rows, ceil(width / group)], the last
@@ -100,7 +101,8 @@ typedef struct lora_kv_cache {
  *                                       or v (which may lie beside it, as slices of one buffer).
  *   k, v and their strides              device bf16 [T, n_kv_heads, head_dim].
  *   cos, sin           device fp32 [n_positions, rot / 2], contiguous, 16-byte aligned; NULL when rot = 0. A
- *                      position outside [0, n_positions) uses the last row.
+ *                      position past the last row uses the last one, a negative one (a query before its
+ *                      sequence's start, which is turned all the same) the first.
  *   rot                0, or a multiple of 16 up to head_dim.
  *   head_dim           a multiple of 8 up to 512; n_heads >= 0.
  * T = q_offsets[n_seqs]. Two rows never write one place unless a page is listed twice.

@@ -70,8 +70,9 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, q_offset
               stream: torch.cuda.Stream | None = None):
     """Writes the rows' keys and values k, v [T, n_kv_heads, head_dim] to their places in the paged cache
     (k_cache, v_cache [n_pages, page_size, n_kv_heads, head_dim]) and returns the turned queries (q [T, n_heads,
-    head_dim]; ``q_out`` may be q itself). ``cos``, ``sin``: fp32 [n_positions, rot / 2], or None for no rotary
-    turn (q is then returned as it is, unless ``q_out`` is given). ``kv_lens`` counts the new rows."""
+    head_dim]; ``q_out`` may be q itself). ``cos``, ``sin``: fp32 [n_positions, rot / 2] (positions past either end
+    use the row at that end), or None for no rotary turn (q is then returned as it is, unless ``q_out`` is given).
+    ``kv_lens`` counts the new rows."""
     return (_bind or _load()).append(q, k, v, q_offsets, kv_lens, block_table, k_cache, v_cache, cos, sin, q_out, stream)
 
 

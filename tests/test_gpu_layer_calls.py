@@ -3,7 +3,7 @@ sequences. Tolerances are those that test_gpu_layer.py derives."""
 import pytest
 import torch
 
-from test_gpu_layer import BF16, BF16_TOL, DEV, Case, gen, norm_ref, randn, within
+from test_gpu_layer import BF16_TOL, DEV, F64, U, Case, gen, norm_ref, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +157,24 @@ def test_append_in_place_beside_keys_and_values(rows):
     assert torch.equal(y[:, :, 1], k) and torch.equal(y[:, :, 2], v)
     with pytest.raises(LoraError):                             # keys in the queries' place
         kv_append(y[:, :, 0], y[:, :, 0], y[:, :, 2], c.off, c.kv, c.table, c.k, c.v, cos, sin, q_out=y[:, :, 0])
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,positions", [([6], [40], 37), ([6, 20], [1000, 15], 1), ([1, 300], [600, 290], 200)])
+def test_positions_past_the_rotary_tables_use_the_row_at_that_end(q_lens, kv_lens, positions):
+    from mixed_lora_projection_gb300 import kv_append
+    c = Case(q_lens, kv_lens, 2, 1, 64, 16)
+    g = gen(positions)
+    y = randn(g, c.off[-1], 4, 64)
+    cos, sin = torch.rand(positions, 16, generator=g, device=DEV), torch.rand(positions, 16, generator=g, device=DEV)
+    out = kv_append(y[:, :2], y[:, 2:3], y[:, 3:], c.off, c.kv, c.table, c.k, c.v, cos, sin)
+    for i, (nq, nk) in enumerate(zip(q_lens, kv_lens)):
+        pos = torch.arange(nk - nq, nk, device=DEV)
+        at = pos.clamp(0, positions - 1)
+        cs, sn = cos[at].to(F64)[:, None], sin[at].to(F64)[:, None]
+        a, b = y[c.off[i]:c.off[i + 1], :3, :16].to(F64), y[c.off[i]:c.off[i + 1], :3, 16:32].to(F64)
+        ref = torch.cat([a * cs - b * sn, b * cs + a * sn], -1)
+        most = ref.abs() * U + torch.cat([a.abs() + b.abs()] * 2, -1) * 2.0 ** -22
+        within(out[c.off[i]:c.off[i + 1], :, :32], ref[:, :2], most[:, :2])
+        real = pos >= 0
+        pg, sl = c.table[i].long()[pos[real] // 16], pos[real] % 16
+        within(c.k[pg, sl][:, :, :32], ref[real][:, 2:], most[real][:, 2:])
