@@ -178,3 +178,73 @@ def test_positions_past_the_rotary_tables_use_the_row_at_that_end(q_lens, kv_len
         real = pos >= 0
         pg, sl = c.table[i].long()[pos[real] // 16], pos[real] % 16
         within(c.k[pg, sl][:, :, :32], ref[real][:, 2:], most[real][:, 2:])
+
+
+# more sequences than the small parameter lists hold; near 1,024 the decode ring of heads of 256 has two slots
+MANY = [65, 300, 1024]
+SHAPES = [(4, 4, 64), (6, 1, 128), (4, 2, 256)]
+
+
+@pytest.mark.parametrize("n", MANY)
+@pytest.mark.parametrize("heads,kv_heads,dim", SHAPES)
+def test_decode_of_many_sequences(n, heads, kv_heads, dim):
+    c = Case([i % 3 for i in range(n)], [2 + (i * 37) % 200 for i in range(n)], heads, kv_heads, dim, 32, seed=n)
+    c.poison()
+    c.check()
+    c.check(50, 2)
+
+
+@pytest.mark.parametrize("n", MANY)
+@pytest.mark.parametrize("most", [20, 150])                    # one tile of rows, two
+@pytest.mark.parametrize("heads,kv_heads,dim", SHAPES)
+def test_prompts_of_many_sequences(n, most, heads, kv_heads, dim):
+    q = [17 + i % (most - 16) if i % 5 else 0 for i in range(n)]
+    c = Case(q, [a + (i * 13) % 40 for i, a in enumerate(q)], heads, kv_heads, dim, 32, seed=n + most)
+    c.poison()
+    c.check()
+    c.check(30, 2)
+
+
+@pytest.mark.parametrize("n", MANY)
+def test_decode_rows_beside_prompts_of_many_sequences(n):
+    q = [(1, 0, 40, 3)[i % 4] for i in range(n)]
+    c = Case(q, [a + (i * 29) % 300 for i, a in enumerate(q)], 6, 2, 128, 16, seed=n)
+    c.poison()
+    c.check()
+
+
+@pytest.mark.parametrize("n", MANY)
+def test_append_of_many_sequences(n):
+    from mixed_lora_projection_gb300 import kv_append
+    q = [i % 4 for i in range(n)]
+    c = Case(q, [a + i % 30 for i, a in enumerate(q)], 2, 2, 64, 16, seed=n)
+    new = randn(gen(n), c.off[-1], 2, 64)
+    want = c.k.clone()
+    kv_append(None, new, new, c.off, c.kv, c.table, c.k, c.v)
+    for i, rows in enumerate(q):
+        if rows:
+            pg, sl = c.slots(i, c.kv_list[i])
+            want[pg[-rows:], sl[-rows:]] = new[c.off[i]:c.off[i + 1]]
+    assert torch.equal(c.k, want)
+
+
+@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (4, 2)])
+def test_cache_of_one_page(q, heads, kv_heads):
+    c = Case([q], [60], heads, kv_heads, 128, 64, seed=q, spare=0)
+    assert c.k.shape[0] == 1
+    c.check()
+    c.check(20, 3)
+
+
+@pytest.mark.parametrize("q", [1, 100])
+@pytest.mark.parametrize("token_pad,page_pad", [(8, 0), (8, 24), (0, 8), (40, 64)])
+def test_cache_with_gaps_between_tokens_and_pages(q, token_pad, page_pad):
+    c = Case([q, q], [300, 129], 4, 2, 64, 16, seed=token_pad)
+    n, page, kv_heads, dim = c.k.shape
+    token = kv_heads * dim + token_pad
+    per = page * token + page_pad
+    for name in ("k", "v"):
+        t = torch.zeros(n * per, dtype=c.k.dtype, device=DEV).as_strided((n, page, kv_heads, dim), (per, token, dim, 1))
+        setattr(c, name, t.copy_(getattr(c, name)))
+    c.check()
