@@ -53,16 +53,20 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 }
 
 // Zeros in place of the values of tokens [from, to) of a piece of TOK tokens in chunks of 64 features, where they
-// are one run of bytes each; thread `me` does chunk `me`. It is for tokens that no row sees (past the last one, or
-// between the sinks and the window): they may hold anything, and their weight of 0 needs them finite. The caller
-// fences.
+// are one run of bytes each, by n threads of which this is `me`. It is for tokens that no row sees (past the last
+// one, or between the sinks and the window): they may hold anything, and their weight of 0 needs them finite. The
+// caller fences. (Stores of 16 bytes, which the fence and the barriers order like any other. As one st.bulk a chunk
+// the same call gave other bits once in 270 runs of two sequences of 8 rows, heads of 256, window 3,000.)
 template <int D, int TOK>
-__device__ __forceinline__ void zero_tokens(uint32_t piece, int from, int to, int me) {
+__device__ __forceinline__ void zero_tokens(uint32_t piece, int from, int to, int me, int n) {
     from = max(from, 0);
     to = min(to, TOK);
-    if (me < D / 64 && from < to)
-        asm volatile("st.bulk.weak.shared::cta [%0], %1, 0;" ::"r"(piece + me * (TOK * 128) + from * 128), "l"((uint64_t)((to - from) * 128))
-                     : "memory");
+#pragma unroll 1
+    for (int i = me; i < (to - from) * 8; i += n)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece + c * (TOK * 128) + from * 128 + i * 16), "r"(0)
+                         : "memory");
 }
 
 // 2^x by the hardware's instruction (x = -inf gives 0).

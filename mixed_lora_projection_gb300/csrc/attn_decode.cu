@@ -367,11 +367,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             const uint32_t vt = ring + (uint32_t)slot * S::kSlot;
             // tokens that no row sees: past the last one, or in the sinks' last tile and the window's first
             if (r.len - j0 < kTk) {
-                zero_tokens<D, kTk>(vt, r.len - j0, kTk, tid);
+                zero_tokens<D, kTk>(vt, r.len - j0, kTk, tid, kConsumers);
                 fence_proxy_async_shared();
             }
             if (a.window && (unsigned)(t + 1 - r.s_tiles) < 2) {
-                zero_tokens<D, kTk>(vt, a.sinks - j0, r.len - list.q_len[w.i] - a.window + 1 - j0, tid);
+                zero_tokens<D, kTk>(vt, a.sinks - j0, r.len - list.q_len[w.i] - a.window + 1 - j0, tid, kConsumers);
                 fence_proxy_async_shared();
             }
             consumer_sync();

@@ -602,8 +602,8 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                     if (!ok) break;
                     const uint32_t piece = ring + (uint32_t)((k + x) % S::kSlots) * S::kPiece;
                     const int tok = from + x * S::kVTok;
-                    zero_tokens<D, S::kVTok>(piece, len - tok, S::kVTok, lane);
-                    if (a.window) zero_tokens<D, S::kVTok>(piece, a.sinks - tok, lo - tok, lane);
+                    zero_tokens<D, S::kVTok>(piece, len - tok, S::kVTok, lane, 32);
+                    if (a.window) zero_tokens<D, S::kVTok>(piece, a.sinks - tok, lo - tok, lane, 32);
                 }
                 if (!ok) break;
                 fence_proxy_async_shared();
