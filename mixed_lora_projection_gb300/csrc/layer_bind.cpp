@@ -123,6 +123,10 @@ void ready(Py_ssize_t n, Py_ssize_t want) {
     TORCH_CHECK_TYPE(n == want, "wrong number of arguments");
 }
 bool given(PyObject* o) { return o != Py_None; }
+// A tensor of the caller's has been written: autograd's check of saved tensors goes by this count.
+void wrote(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 PyObject* same(PyObject* o) {
     Py_INCREF(o);
     return o;
@@ -237,6 +241,9 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             qr.stride, sp, group < 0 ? 0 : group, stream.handle);
           }),
           "lora_linear_add_rms_norm");
+    if (given(a[5])) wrote(out);
+    if (given(a[6])) wrote(h);
+    if (group >= 0 && given(a[7])) wrote(scales);
     THPObjectPtr o(given(a[5]) ? same(a[5]) : THPVariable_Wrap(out));
     THPObjectPtr hh(given(a[6]) ? same(a[6]) : h.defined() ? THPVariable_Wrap(h) : same(a[0]));
     if (group < 0) return PyTuple_Pack(2, o.get(), hh.get());
@@ -290,6 +297,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               vr.head, cp, sp, rot, positions, stream.handle);
           }),
           "lora_linear_kv_append");
+    wrote(tensor(a[6], "k_cache"));
+    wrote(tensor(a[7], "v_cache"));
+    if (given(a[10])) wrote(tensor(a[10], "q_out"));
     return out.release();
     END_HANDLE_TH_ERRORS
 }
@@ -318,6 +328,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
               return g_attend(handle, &c, qr.p, qr.stride, qr.head, orr.p, orr.stride, orr.head, scale, window, sinks, stream.handle);
           }),
           "lora_linear_attn_forward");
+    if (given(a[13])) wrote(o);
     return out.release();
     END_HANDLE_TH_ERRORS
 }

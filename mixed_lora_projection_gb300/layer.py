@@ -9,6 +9,9 @@ Arguments are checked and marshalled by ``csrc/layer_bind.cpp``; every step runs
 and ``block_table`` are int32 tensors on the device, read when the call runs, so that a captured
 decode step can be replayed as the caches grow.
 
+The operators serve: no gradient passes through them, whatever their inputs require. A tensor that a
+call writes counts as modified in place.
+
 ``stream``: a call runs on it as under ``torch.cuda.stream(stream)``. What it allocates belongs to that
 stream; that the inputs are ready there, and that another stream waits before it uses the outputs, is the
 caller's to see to.

@@ -272,3 +272,35 @@ def test_blanked_values_give_the_same_bits_every_time(q_lens, kv_lens, heads, kv
             o = attn.forward(c.q, c.k, c.v, c.off, c.kv, c.table, window=window, sinks=sinks)
             other += (o.view(torch.int16) != first.view(torch.int16)).any()
         assert attn.status() == 0 and other.item() == 0
+
+
+def test_tensors_written_in_place_count_as_modified():
+    from mixed_lora_projection_gb300 import PagedAttention, add_rms_norm, add_rms_norm_fp8, kv_append
+    c = Case([2, 20], [20, 30], 4, 2, 64, 16)
+    g = gen(8)
+    x, w, new = randn(g, 4, 64), randn(g, 64), randn(g, 22, 2, 64)
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    q8, s, o = torch.empty(4, 64, dtype=torch.float8_e4m3fn, device=DEV), torch.empty(4, 2, device=DEV), torch.empty_like(c.q)
+
+    def grew(tensors, call):
+        before = [t._version for t in tensors]
+        call()
+        assert all(t._version > b for t, b in zip(tensors, before))
+
+    grew([y, h], lambda: add_rms_norm(x, w, x, out=y, h_out=h))
+    grew([q8, s, h], lambda: add_rms_norm_fp8(x, w, group=32, out=q8, scales=s, h_out=h))
+    grew([c.k, c.v, o], lambda: kv_append(c.q, new, new, c.off, c.kv, c.table, c.k, c.v, q_out=o))
+    with PagedAttention(4, 2, 64, 16, 22, 2) as attn:
+        grew([o], lambda: attn.forward(c.q, c.k, c.v, c.off, c.kv, c.table, out=o))
+    read = [t._version for t in (x, w, c.q, new, c.kv, c.table)]
+    add_rms_norm(x, w, x)
+    kv_append(c.q, new, new, c.off, c.kv, c.table, c.k, c.v)
+    assert read == [t._version for t in (x, w, c.q, new, c.kv, c.table)]
+    # a value that a gradient needs is not overwritten unnoticed
+    a = torch.ones(4, 64, dtype=x.dtype, device=DEV, requires_grad=True) * 2
+    loss = (a * a).sum()
+    add_rms_norm(x, w, out=a)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        add_rms_norm(x, w, out=torch.empty_like(x))
