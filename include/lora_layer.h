@@ -19,7 +19,7 @@
  * Errors, streams and codes are those of lora_linear.h: arguments are checked on the host before
  * any launch, a failed check launches nothing and leaves outputs untouched, calls are enqueued
  * on `stream` and return without waiting (their kernels may be scheduled while the stream's kernel
- * before them ends, and wait for it before they touch memory). Values that live on the device
+ * before them ends, and wait for it before they touch memory or let the next one begin). Values that live on the device
  * (cache lengths, page tables) cannot be checked there: a length is used as if clamped to
  * [0, pages x page_size], and a page number outside [0, n_pages) is read as zeros and never written.
  */

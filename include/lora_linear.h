@@ -255,7 +255,8 @@ enum {
                                    one launch): the launch may start on SMs the previous kernel of the stream
                                    leaves, requests its first W tiles, and waits for that kernel before it
                                    reads or writes anything else; it lets the next kernel start early in turn.
-                                   The previous kernel must not write this call's W. 0 (default) = off.
+                                   The previous kernel must not write this call's W; nor, where that is itself a
+                                   call with this option, the kernel before it, and so on. 0 (default) = off.
                                    Does not change any result */
     LORA_OPT_TOKEN_COLUMNS = 17, /* bf16 base: token-column units for batches of at most 512 rows whose rows
                                    all name one adapter (or none), on handles that sum whole K: each unit of

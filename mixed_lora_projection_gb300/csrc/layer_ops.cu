@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const N
     const int nt = WARP ? 32 : (int)blockDim.x;
     const int tid = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int row = WARP ? (int)(blockIdx.x * 4 + (threadIdx.x >> 5)) : (int)blockIdx.x;
-    dev::griddep_launch_dependents();
     dev::griddep_wait();
+    dev::griddep_launch_dependents();
     if (WARP && row >= p.rows) return;
     const int nvec = p.width >> 3;
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride);
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
         const int mid = (lo + hi + 1) >> 1;
         if (o.off[mid] <= t) lo = mid; else hi = mid - 1;
     }
-    dev::griddep_launch_dependents();
     dev::griddep_wait();
+    dev::griddep_launch_dependents();
     const long long cap = (long long)p.c.pages_per_seq * p.c.page_size;
     const int len = (int)min((long long)max(p.c.kv_lens[lo], 0), cap);
     const int pos = len - (o.off[lo + 1] - t);

@@ -304,3 +304,28 @@ def test_tensors_written_in_place_count_as_modified():
         loss.backward()
     with torch.inference_mode():
         add_rms_norm(x, w, out=torch.empty_like(x))
+
+
+def test_projection_launched_early_reads_weights_written_before_the_norm():
+    """W's writer, the norm, then a projection that may request W before it waits for the norm."""
+    from mixed_lora_projection_gb300 import LoraLinear, _lib as L, add_rms_norm
+    g = gen(3)
+    x, w, weights = randn(g, 48, 1024), randn(g, 1024), randn(g, 4, 2048, 1024)
+    a, b = randn(g, 16, 1024), randn(g, 2048, 16)
+    W = torch.empty(2048, 1024, dtype=x.dtype, device=DEV)
+    with LoraLinear(1024, 2048, 16, 48) as ll:
+        ll.set_option(L.OPT_PDL, 1)
+
+        def step(i):
+            W.copy_(weights[i])
+            y, _ = add_rms_norm(x, w)
+            return ll.forward(y, [0, 48], [0], W, [a], [b], [1.0])
+
+        want = []
+        for i in range(4):
+            want.append(step(i))
+            torch.cuda.synchronize()
+        for _ in range(50):
+            got = [step(i) for i in range(4)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
