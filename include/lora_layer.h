@@ -161,8 +161,8 @@ int lora_linear_attn_validate(int n_heads, int n_kv_heads, int head_dim, int pag
 /*
  * lora_linear_attn_set_option -- options of an attention handle, for later calls (anything else: LORA_EINVAL):
  *   LORA_OPT_WAIT_LIMIT_US   bound of every wait in a kernel, 1,000 to 60,000,000 microseconds (default 4,000,000).
- *   LORA_OPT_DEBUG_STALL     tests only: n > 0 = a block's load warp issues n - 1 pieces of K and V and no more, so
- *                            that the other warps' waits run out; 0 = off.
+ *   LORA_OPT_DEBUG_STALL     tests only: n > 0 = a block's load warp stops after n - 1 tiles of K and V, so that the
+ *                            other warps' waits run out; 0 = off.
  */
 int lora_linear_attn_set_option(lora_attn* h, int option, long long value);
 

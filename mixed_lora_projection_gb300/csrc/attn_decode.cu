@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         const int chunks = D / 64, boxes = (kTk / p.granule) * chunks;
         const int gi = lane / chunks, ch = lane % chunks;
         const uint32_t box_bytes = (uint32_t)p.granule * 128;
-        int slot = 0, issued = 0;
+        int slot = 0, issued = 0, allowed = a.debug_stall ? a.debug_stall - 1 : kNoStall;    // tiles until a test's stall
         uint32_t phase = 0;
         bool ok = true;
         while (ok && w.at < w.end) {
@@ -200,14 +200,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             };
             int page, tok;
             place(t0, page, tok);
-            for (int t = t0; t < t1 && ok; ++t) {
+            const int t_stop = min(t1, t0 + allowed);
+            if (a.debug_stall) allowed -= t_stop - t0;
+            for (int t = t0; t < t_stop && ok; ++t) {
                 int npage = -1, ntok = 0;
                 if (t + 1 < t1) place(t + 1, npage, ntok);       // the next tile's pages, ahead of its turn
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if ((a.debug_stall && issued + 1 >= a.debug_stall) ||
-                        !wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) {
+                    if (!wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) {
                         ok = false;
                         break;
                     }
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 page = npage;
                 tok = ntok;
             }
+            ok = ok && t_stop == t1;
             w.at += t1 - t0;
             if ((unsigned long long)prefix[w.i + 1] * n_kv <= w.at) ++w.i;
         }

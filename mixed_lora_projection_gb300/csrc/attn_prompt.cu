@@ -395,6 +395,9 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
             tok = j - pg * a.c.page_size;
             if (page < 0 || page >= a.c.n_pages) page = a.c.n_pages;    // out of the map's range: zeros
         };
+        // tiles until a stall that a test asks for (by units, not by pieces: a check in `load` cost a tenth of a
+        // 4,096-row chunk's time with heads of 256)
+        int allowed = a.debug_stall ? a.debug_stall - 1 : kNoStall;
         int slot = 0, issued = 0, edges = 0;                  // edges: pieces of V with tokens to blank
         uint32_t phase = 0, blanked = 0;                      // blanked: bit s, slot s holds one
         // Pieces of a tile of K (128 tokens x its share of the features) or of V (its share of the tokens x all). Those
@@ -409,9 +412,7 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                 const int pg = __shfl_sync(0xffffffffu, page, from & 31), tk = __shfl_sync(0xffffffffu, tok, from & 31);
                 const bool mine = gi < grans && pg >= 0;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
-                if ((a.debug_stall && issued + 1 >= a.debug_stall) ||
-                    !wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit))
-                    return false;
+                if (!wait_warp(smem_addr(&empty[slot]), phase ^ 1, abort_flag, a.status, limit)) return false;
                 const uint32_t bar = smem_addr(edge ? &raw[edges % S::kSlots] : &full[slot]);
                 edges += edge;
                 blanked = (blanked & ~(1u << slot)) | (uint32_t)edge << slot;
@@ -526,11 +527,13 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
             if (t0 == t1) continue;
             t_end = t1;
             table = a.c.table + u.seq * a.c.table_stride;
+            const int t_stop = min(t1, t0 + allowed);
+            if (a.debug_stall) allowed -= t_stop - t0;
             int page, tok, npage, ntok;
             place(t0, page, tok);
             place(t0 + 1, npage, ntok);
-            ok = load(false, page, tok, false);
-            for (int t = t0; t < t1 && ok; ++t) {
+            ok = t0 < t_stop && load(false, page, tok, false);
+            for (int t = t0; t < t_stop && ok; ++t) {
                 int fpage, ftok;
                 place(t + 2, fpage, ftok);
                 const bool edge = at_edge(gap, tail, t - t0);
@@ -544,6 +547,7 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
                 npage = fpage;
                 ntok = ftok;
             }
+            ok = ok && t_stop == t1;
         }
         // The copies in flight land before the block may end, whoever gave up.
         if (lane == 0) {

@@ -2,7 +2,6 @@
 // attention handle and its workspace, launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -511,7 +510,7 @@ extern "C" int lora_linear_attn_set_option(lora_attn* h, int option, long long v
             h->wait_limit_ns = (unsigned long long)value * 1000ull;
             return LORA_OK;
         case LORA_OPT_DEBUG_STALL:
-            if (value < 0 || value > INT_MAX) return LORA_EINVAL;
+            if (value < 0 || value > kNoStall) return LORA_EINVAL;
             h->debug_stall = (int)value;
             return LORA_OK;
         default:

@@ -77,6 +77,8 @@ struct AppendParams {
 };
 cudaError_t launch_kv_append(const AppendParams& p, const int32_t* q_offsets, cudaStream_t stream);
 
+constexpr int kNoStall = 1 << 30;       // more tiles than a unit has
+
 struct AttnParams {
     CacheView c;
     const void* q;
@@ -86,7 +88,7 @@ struct AttnParams {
     float scale_log2;                   // softmax in base 2: scale * log2(e)
     int* status;
     unsigned long long wait_limit_ns;
-    int debug_stall;                    // n > 0: a load warp issues n - 1 pieces of K and V and no more (tests)
+    int debug_stall;                    // n > 0: a load warp stops after n - 1 tiles of K and V (tests)
     cudaStream_t stream;
 };
 

@@ -97,7 +97,7 @@ def test_norm_over_its_input_returns_the_input_as_h(rows, width):
 
 
 def give_up(c, stalls, **kw):
-    """A call whose load warps stop after some pieces ends with LORA_ETIMEOUT; the handle then works as before."""
+    """A call whose load warps stop after some tiles ends with LORA_ETIMEOUT; the handle then works as before."""
     from mixed_lora_projection_gb300 import PagedAttention, _lib as L
     with PagedAttention(c.heads, c.kv_heads, c.dim, c.page, c.off[-1], len(c.q_lens)) as attn:
         want = c.run(attn, **kw)
@@ -118,7 +118,7 @@ def give_up(c, stalls, **kw):
 def test_decode_gives_up_and_goes_on(q_lens, kv_lens, heads, kv_heads, dim):
     c = Case(q_lens, kv_lens, heads, kv_heads, dim, 64)
     give_up(c, (1, 2, 3, 5))
-    give_up(c, (2, 4), window=3000, sinks=70)
+    give_up(c, (1, 2), window=3000, sinks=70)
 
 
 @pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,dim", [
@@ -127,8 +127,8 @@ def test_decode_gives_up_and_goes_on(q_lens, kv_lens, heads, kv_heads, dim):
     ([300, 40, 700], [5000, 3000, 9000], 6, 3, 256), ([260, 30, 1], [7000, 3000, 9000], 24, 12, 256)])
 def test_prompt_gives_up_and_goes_on(q_lens, kv_lens, heads, kv_heads, dim):
     c = Case(q_lens, kv_lens, heads, kv_heads, dim, 64)
-    give_up(c, (1, 2, 3, 6))
-    give_up(c, (1, 2, 3, 4), window=3000, sinks=70)            # values to blank among the first pieces
+    give_up(c, (1, 2, 3))
+    give_up(c, (1, 2), window=3000, sinks=70)                  # values to blank in the first tiles
 
 
 def test_attention_handle_options():
