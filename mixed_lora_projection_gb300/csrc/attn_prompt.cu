@@ -577,6 +577,7 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
             const int n = w.n, head = w.head * p.group, two = w.two, row = w.row0 + w.tok0;
             const int gap = w.gap, tail = w.tail, k0 = w.k0, t0 = w.t0, s_tiles = w.s_tiles, lo_tile = w.lo_tile, len = w.len;
             const int lo = len - w.q_len + w.tok0 - a.window + 1;             // with a window: its first token
+            __threadfence_block();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[count & 1]));
             if (n < 0) break;
@@ -660,6 +661,7 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
             if (!ok) break;
             const int n = pieces[count & 1].n, k0 = pieces[count & 1].k0;
             const bool two = pieces[count & 1].two;
+            __threadfence_block();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[count & 1]));
             if (n < 0) break;
@@ -800,7 +802,8 @@ __global__ void __launch_bounds__(Shape<D, Q>::kThreads, 1)
         auto out_row = [&](const Piece& u, int tok, int hg) {
             return static_cast<bf*>(a.out) + (long long)(u.row0 + tok) * a.o_stride + (u.head * g + hg) * a.o_head + half * kOut;
         };
-        auto finish = [&](int c) {       // this warp needs piece c no more
+        auto finish = [&](int c) {       // this warp needs piece c no more: what it has read of it is there
+            __threadfence_block();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&done[c & 1]));
         };

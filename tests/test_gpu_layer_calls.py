@@ -329,3 +329,24 @@ def test_projection_launched_early_reads_weights_written_before_the_norm():
             got = [step(i) for i in range(4)]
             torch.cuda.synchronize()
             assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("n,heads,kv_heads,dim,page,window", [
+    (70, 12, 12, 256, 128, 700), (2, 24, 12, 256, 64, 0), (70, 16, 4, 128, 48, 0), (20, 8, 8, 64, 16, 300)])
+def test_decode_gives_the_same_bits_beside_other_work(n, heads, kv_heads, dim, page, window):
+    """A slot of the ring is refilled only when its last reads are done, whatever keeps the block waiting."""
+    from mixed_lora_projection_gb300 import PagedAttention
+    c = Case([1 + i % 2 for i in range(n)], [2 + (i * 397) % (14000 // n + 300) for i in range(n)], heads, kv_heads, dim, page, seed=n)
+    c.poison()
+    first = c.check(window, 4)
+    side, a = torch.cuda.Stream(), torch.randn(2048, 2048, device=DEV).to(torch.bfloat16)
+    other = torch.zeros((), dtype=torch.int64, device=DEV)
+    with PagedAttention(heads, kv_heads, dim, page, c.off[-1], n) as attn:
+        for i in range(4000):
+            if i % 40 == 0:
+                with torch.cuda.stream(side):
+                    for _ in range(40):
+                        a @ a
+            o = attn.forward(c.q, c.k, c.v, c.off, c.kv, c.table, window=window, sinks=4)
+            other += (o.view(torch.int16) != first.view(torch.int16)).any()
+        assert attn.status() == 0 and other.item() == 0
