@@ -19,9 +19,9 @@
 // an issuing warp or two, a TMA warp for K and V (one ring of pieces) that also hands out the work, and
 // one for the queries and for blanking values that no row sees.
 //
-// Measured (one GB300, inputs past L2): a 4,096-row chunk at the end of 16,384 tokens 889 us with 24 / 12
-// heads of 256 (1.62 PFLOP/s, 0.84 of the measured bf16 rate) and 1.11 ms with 48 / 8 heads of 128 (0.67);
-// a 16,384-token prompt of 24 / 12 heads of 256, causal 2.01 ms (0.85), with a window of 4,096 0.99 ms (0.75);
+// Measured (one GB300, inputs past L2): a 4,096-row chunk at the end of 16,384 tokens 915 us with 24 / 12
+// heads of 256 (1.58 PFLOP/s, 0.81 of the measured bf16 rate) and 1.13 to 1.16 ms with 48 / 8 heads of 128 (0.65);
+// a 16,384-token prompt of 24 / 12 heads of 256, causal 2.01 ms (0.85), with a window of 4,096 1.00 ms (0.75);
 // heads of 64 0.50 on a 4,096-row chunk.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -164,7 +164,10 @@ __device__ __forceinline__ Unit find_unit(const PromptParams& p, const PromptLis
 // The units are handed out one by one, those that see most first (a counter in global memory; which block
 // has a unit does not change its output). Of the last ones, fewer than one a block, all tiles form one line
 // that is cut into equal parts, one a block, where that saves more time than the join takes (kWorth tiles
-// a block): a part may end inside a unit, whose sums then go to the workspace.
+// a block): a part may end inside a unit, whose sums then go to the workspace. Cut at any gain, or from 4 tiles on,
+// 512 rows at the end of 2,048 tokens (48 / 8 heads of 128) take 86 us instead of 49, 8,192 causal rows of 16 heads
+// of 128 279 instead of 248; never cut, six chats of 8 draft rows take 256 us instead of 72, a 4,096-row chunk at the
+// end of 16,384 tokens 1,286 instead of 1,161. From 16 on gives what 8 gives in all of these.
 constexpr int kWorth = 8;
 struct Plan {
     uint32_t total;       // tiles of the last units, if they are cut (else 0)

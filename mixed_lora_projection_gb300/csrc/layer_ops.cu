@@ -85,7 +85,7 @@ __device__ __forceinline__ uint2 to_e4m3(const float* f, float inv) {
 // q = e4m3(y / s). One row per block (or per warp: WARP), V 16-byte vectors of it per thread. The row stays
 // in registers (fp32) between its sum of squares and its outputs, so x and the residual are read once and
 // memory is the bound: 16,384 rows of 5,120 with a residual take 100 us in bf16 (0.99 of the measured copy
-// rate) and 87-90 us to 8 bits (0.96-1.0); 48 rows take one pass's latency, 2.2 us back to back. The weights are read after the
+// rate) and 87-90 us to 8 bits (0.96-1.0); 48 rows take one pass's latency, 1.8 us back to back in a graph. The weights are read after the
 // sum, when the sum's loads have left their registers (4,096 rows of 17,408: 82 us against 125).
 template <int V, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) add_rms_norm_kernel(const NormParams p) {
@@ -268,6 +268,10 @@ cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream) {
         if (nvec <= 64) return launch_chained(add_rms_norm_kernel<2, true>, grid, 128, 0, stream, p);
         return launch_chained(add_rms_norm_kernel<4, true>, grid, 128, 0, stream, p);
     }
+    // Vectors a thread. On few rows the latency counts: 48 rows of 5,120 back to back 1.8 us with one against 2.1 with
+    // four, 304 rows of 12,288 3.8 with two against 4.8. On many, the rows in flight: 1,601 rows of 5,120 6.6 us with
+    // four against 8.2 with one, of 16,384 from HBM 37 with four against 43 with two. Around 304 rows (two blocks an SM)
+    // it goes either way: 304 of 5,120 2.9 with one against 2.6, 608 4.2 against 4.5 with four.
     const int v = nvec > 2048 || p.rows > 304 ? 4 : nvec > 1024 ? 2 : 1;
     const int nt = ((nvec + v - 1) / v + 31) / 32 * 32;
     if (v == 1) return launch_chained(add_rms_norm_kernel<1, false>, p.rows, nt, 0, stream, p);
@@ -280,7 +284,8 @@ static cudaError_t append(const AppendParams& p, const int32_t* off, cudaStream_
     SeqOffsets<N> o;
     for (int i = 0; i <= p.c.n_seqs; ++i) o.off[i] = off[i];
     // A few rows are shared out to several blocks each, one vector a thread (at most two blocks an SM): 48 rows of
-    // 24 + 2 x 12 heads of 256 take 2.6 us in a graph instead of 3.9 with a block a row.
+    // 24 + 2 x 12 heads of 256 take 2.2 us in a graph (3.9 with a block a row, before the kernels' order of
+    // waiting changed; 2.6 with several then).
     const long long items = (long long)((p.q_out ? p.n_heads : 0) + 2 * p.c.n_kv) * (p.c.dim >> 3);
     const unsigned per_row = (unsigned)std::max(1ll, std::min((items + 255) / 256, 304ll / p.rows));
     return launch_chained(kv_append_kernel<N>, dim3(p.rows, per_row), 256, 0, stream, p, o);

@@ -80,7 +80,8 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, q_offset
 
 
 class PagedAttention:
-    """One handle: attention of n_heads query heads over a paged cache with n_kv_heads heads."""
+    """One handle: attention of n_heads query heads over a paged cache with n_kv_heads heads. Its calls share a
+    workspace, so they go one after another: on one stream, or on streams that wait for each other."""
 
     def __init__(self, n_heads: int, n_kv_heads: int, head_dim: int, page_size: int, max_tokens: int,
                  max_seqs: int = 64, device: int | torch.device | None = None):
@@ -120,7 +121,8 @@ class PagedAttention:
                 sinks: int = 0, out: torch.Tensor | None = None,
                 stream: torch.cuda.Stream | None = None) -> torch.Tensor:
         """o [T, n_heads, head_dim] of the new rows q over the cache; a row sees the tokens up to its own, or
-        (window > 0) the last ``window`` of them and the first ``sinks`` tokens. scale: 1 / sqrt(head_dim)."""
+        (window > 0) the last ``window`` of them and the first ``sinks`` tokens. scale: 1 / sqrt(head_dim). The sums' order goes by
+        the batch: a row's last bit may differ in another one."""
         return (_bind or _load()).attend(self._ptr, self.n_heads, self.head_dim, self.device.index, q, k_cache, v_cache,
                                          q_offsets, kv_lens, block_table, scale, window, sinks, out, stream)
 
