@@ -171,6 +171,40 @@ int lora_linear_forward_w4(lora_linear* h, const void* x, int T,
                            const float* scale, int n_adapters, void* y, void* stream);
 
 /*
+ * lora_linear_forward_fp8 -- lora_linear_forward with 8-bit activations and an 8-bit base weight.
+ *   x8        device e4m3 [T, d_in], 16-byte aligned.
+ *   x_scales  device fp32 [T, ceil(d_in / 128)], contiguous: one scale per row and group of 128 input
+ *             features, as lora_linear_add_rms_norm, _silu_mul and _fp8_rows write them with group 128.
+ *   w8        device e4m3 [d_out, d_in], 16-byte aligned.
+ *   w_scales  device fp32 [ceil(d_out / 128), ceil(d_in / 128)], contiguous: one scale per block of 128
+ *             output and 128 input features, as lora_linear_fp8_blocks writes them.
+ *   x         device bf16 [T, d_in], 16-byte aligned: the same activations before they were brought to 8
+ *             bits; read for the adapters alone, whose A and B stay bf16. May be NULL where no row's
+ *             segment names an adapter.
+ * With X[t, k] = x8[t, k] x_scales[t, k / 128] and W[n, k] = w8[n, k] w_scales[n / 128, k / 128]:
+ *     Y[t, :] = X[t, :] W^T (+ s_a (x[t, :] A_a^T) B_a^T)
+ * A group's 128 products are exact and summed in fp32 by the tensor cores; the groups' sums, each times its
+ * two scales' product, are added in fp32. Requires d_in to be a multiple of 16 (else LORA_EINVAL); all other
+ * arguments, layouts and errors as lora_linear_forward, except that the base product may be summed in parts
+ * of K chosen by the batch: the same call gives the same bits, but a row's last bit may differ in another batch.
+ * Stream capture as lora_linear_forward. Of the options, those of the launch's shape (tile widths, K parts,
+ * clusters, unit orders) do not apply; LORA_OPT_MAX_CTAS does to batches of four row tiles and more.
+ * Source: no counterpart on the pages (their base is 4-bit); the scales' layout is the one that this library's
+ * 8-bit norm writes.
+ */
+int lora_linear_forward_fp8(lora_linear* h, const void* x8, const float* x_scales, const void* x, int T,
+                            const int32_t* seg_offsets, const int32_t* seg_adapter_ids, int n_seg,
+                            const void* w8, const float* w_scales, const void* const* A, const void* const* B,
+                            const float* scale, int n_adapters, void* y, void* stream);
+
+/* lora_linear_validate_fp8 -- the host checks of lora_linear_forward_fp8, without a handle or a GPU. */
+int lora_linear_validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments, const void* x8,
+                             const float* x_scales, const void* x, int T, const int32_t* seg_offsets,
+                             const int32_t* seg_adapter_ids, int n_seg, const void* w8, const float* w_scales,
+                             const void* const* A, const void* const* B, const float* scale, int n_adapters,
+                             const void* y);
+
+/*
  * lora_linear_forward_host_w4 -- lora_linear_forward_host with the 4-bit base of
  * lora_linear_forward_w4 (Wq, Ws device pointers; X and Y host buffers).
  * Source: as lora_linear_forward_w4.

@@ -40,6 +40,10 @@ SIGNATURES = {
     "lora_linear_w4_repack": (C.c_int, [P, P, C.c_longlong, P]),
     "lora_linear_forward_w4": (C.c_int, [P, P, C.c_int, I32P, I32P, C.c_int, P, P, C.POINTER(P), C.POINTER(P),
                                          C.POINTER(C.c_float), C.c_int, P, P]),
+    "lora_linear_forward_fp8": (C.c_int, [P, P, P, P, C.c_int, I32P, I32P, C.c_int, P, P, C.POINTER(P), C.POINTER(P),
+                                          C.POINTER(C.c_float), C.c_int, P, P]),
+    "lora_linear_validate_fp8": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, P, P, P, C.c_int, I32P, I32P,
+                                           C.c_int, P, P, C.POINTER(P), C.POINTER(P), C.POINTER(C.c_float), C.c_int, P]),
     "lora_linear_forward_host_w4": (C.c_int, [P, P, C.c_int, I32P, I32P, C.c_int, P, P, C.POINTER(P),
                                               C.POINTER(P), C.POINTER(C.c_float), C.c_int, P, P]),
     "lora_linear_destroy": (C.c_int, [P]),

@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "liblora_linear.so")
 BIND = os.path.join(PKG, "_layer_bind.so")
 BIND_FOR = os.path.join(BUILD, "layer_bind.for")       # the PyTorch and the Python that the binding was built for
 BIND_SOURCE = "layer_bind.cpp"
-SOURCES = ["kernels.cu", "kernels_w4.cu", "api.cpp", "planner.cpp", "noalloc.cu",
+SOURCES = ["kernels.cu", "kernels_w4.cu", "kernels_fp8.cu", "api.cpp", "planner.cpp", "noalloc.cu",
            "layer_ops.cu", "attn_decode.cu", "attn_prompt.cu", "layer_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/lora_linear.h"
+#include "lora_fp8.h"
 #include "lora_internal.h"
 #include "lora_w4.h"
 
@@ -774,8 +775,8 @@ const char* lora_linear_error_string(int code) {
 
 }  // extern "C"
 
-static int validate_impl(int d_in, int d_out, int rank, int max_tokens, int max_segments, const void* x, int T,
-                         const int32_t* seg_offsets, const int32_t* seg_adapter_ids, int n_seg, const void* W,
+static int validate_impl(int d_in, int d_out, int rank, int max_tokens, int max_segments, const void* x,
+                         size_t x_row_bytes, int T, const int32_t* seg_offsets, const int32_t* seg_adapter_ids, int n_seg, const void* W,
                          size_t w_bytes, const void* const* A, const void* const* B, const float* scale,
                          int n_adapters, const void* y) {
     int rc = check_shape(d_in, d_out, rank, max_tokens, max_segments);
@@ -794,7 +795,7 @@ static int validate_impl(int d_in, int d_out, int rank, int max_tokens, int max_
     if (n_seg < 1 || !seg_offsets || !seg_adapter_ids) return LORA_EINVAL;
     if (!x || !y || !W || !aligned16(x) || !aligned16(y) || !aligned16(W)) return LORA_EINVAL;
     if (seg_offsets[0] != 0 || seg_offsets[n_seg] != T) return LORA_EINVAL;
-    const size_t xb = (size_t)T * d_in * 2, yb = (size_t)T * d_out * 2, wb = w_bytes;
+    const size_t xb = (size_t)T * x_row_bytes, yb = (size_t)T * d_out * 2, wb = w_bytes;
     const size_t ab = (size_t)rank * d_in * 2, bb = (size_t)d_out * rank * 2;
     if (overlaps(y, yb, x, xb) || overlaps(y, yb, W, wb)) return LORA_EINVAL;
     for (int i = 0; i < n_seg; ++i) {
@@ -819,8 +820,8 @@ int lora_linear_validate(int d_in, int d_out, int rank, int max_tokens, int max_
                          const int32_t* seg_adapter_ids, int n_seg, const void* W,
                          const void* const* A, const void* const* B, const float* scale,
                          int n_adapters, const void* y) {
-    return validate_impl(d_in, d_out, rank, max_tokens, max_segments, x, T, seg_offsets, seg_adapter_ids, n_seg, W,
-                         (size_t)d_out * d_in * 2, A, B, scale, n_adapters, y);
+    return validate_impl(d_in, d_out, rank, max_tokens, max_segments, x, (size_t)d_in * 2, T, seg_offsets,
+                         seg_adapter_ids, n_seg, W, (size_t)d_out * d_in * 2, A, B, scale, n_adapters, y);
 }
 
 int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max_tokens,
@@ -857,7 +858,8 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
         return LORA_ECUDA;
     }
     h->encode = reinterpret_cast<EncodeTiledFn>(fn);
-    if (gemm_prepare_device() != cudaSuccess || w4_prepare_device() != cudaSuccess) {
+    if (gemm_prepare_device() != cudaSuccess || w4_prepare_device() != cudaSuccess ||
+        fp8_prepare_device() != cudaSuccess) {
         free_handle(h);
         return LORA_ECUDA;
     }
@@ -1117,8 +1119,8 @@ int forward_impl(lora_linear* h, const void* x, int T, const int32_t* seg_offset
                  cudaStream_t upload, const void* x_src, cudaEvent_t ready, const void* Wq = nullptr,
                  const void* Ws = nullptr) {
     if (!h) return LORA_EINVAL;
-    int rc = validate_impl(h->d_in, h->d_out, h->rank, h->max_tokens, h->max_segments, x, T, seg_offsets,
-                           seg_adapter_ids, n_seg, Wq ? Wq : W,
+    int rc = validate_impl(h->d_in, h->d_out, h->rank, h->max_tokens, h->max_segments, x, (size_t)h->d_in * 2, T,
+                           seg_offsets, seg_adapter_ids, n_seg, Wq ? Wq : W,
                            Wq ? (size_t)h->d_out * h->d_in / 2 : (size_t)h->d_out * h->d_in * 2, A, B, scale,
                            n_adapters, y);
     if (rc != LORA_OK) return rc;
@@ -1514,6 +1516,262 @@ int lora_linear_forward_w4(lora_linear* h, const void* x, int T, const int32_t* 
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- 8-bit base
+namespace {
+
+// Launch shape of the 8-bit kernel for a plan.
+struct Fp8Shape {
+    int wide = 0, tile_n = 128, parts = 1, a_rows = kTileM, stages = 0, n_ntiles = 0, raster_group = 1, groups = 0;
+};
+
+Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
+    Fp8Shape s;
+    const int nf = (int)plan.fused.size(), k_blocks = ceil_div(h->d_in, kFp8Group);
+    s.wide = nf >= 4;
+    if (s.wide) {
+        s.tile_n = 256;
+        s.n_ntiles = ceil_div(h->d_out, s.tile_n);
+        s.raster_group = ceil_div(s.n_ntiles, 2);
+        while (s.stages < kMaxStages && fp8_smem_bytes(s.tile_n / 2, s.a_rows, s.stages + 1) <= (size_t)kSmemLimit) ++s.stages;
+        return s;
+    }
+    // two CTAs an SM
+    const int room = 2 * usable_sms(h);
+    s.tile_n = 128;
+    s.n_ntiles = ceil_div(h->d_out, s.tile_n);
+    while (s.parts < kFp8MaxParts && nf * s.n_ntiles * s.parts * 2 <= room && s.parts * 2 <= k_blocks) s.parts *= 2;
+    if (nf == 1) s.a_rows = std::max(16, ceil_div(plan.fused[0].nrows, 16) * 16);
+    while (s.stages < kMaxStages && fp8_smem_bytes(s.tile_n, s.a_rows, s.stages + 1) <= (size_t)kFp8SmemTwo) ++s.stages;
+    return s;
+}
+
+struct Fp8Operands {
+    const void *x8, *w8;
+    const float *xs, *ws;
+};
+
+int validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments, const Fp8Operands& f, const void* x,
+                 int T, const int32_t* seg_offsets, const int32_t* seg_adapter_ids, int n_seg, const void* const* A,
+                 const void* const* B, const float* scale, int n_adapters, const void* y) {
+    if (d_in % 16) return LORA_EINVAL;
+    const int rc = validate_impl(d_in, d_out, rank, max_tokens, max_segments, f.x8, (size_t)d_in, T, seg_offsets,
+                                 seg_adapter_ids, n_seg, f.w8, (size_t)d_out * d_in, A, B, scale, n_adapters, y);
+    if (rc != LORA_OK || T == 0) return rc;
+    if (!f.xs || !f.ws || (reinterpret_cast<uintptr_t>(f.xs) & 3) || (reinterpret_cast<uintptr_t>(f.ws) & 3)) return LORA_EINVAL;
+    const size_t groups = ceil_div(d_in, kFp8Group), yb = (size_t)T * d_out * 2;
+    if (overlaps(y, yb, f.xs, groups * T * 4) || overlaps(y, yb, f.ws, groups * ceil_div(d_out, kFp8Group) * 4)) return LORA_EINVAL;
+    for (int i = 0; i < n_seg; ++i)
+        if (seg_adapter_ids[i] && seg_offsets[i + 1] > seg_offsets[i]) {
+            // the adapters' rows are read in bf16
+            if (!x || !aligned16(x) || overlaps(y, yb, x, (size_t)T * d_in * 2)) return LORA_EINVAL;
+            break;
+        }
+    return LORA_OK;
+}
+
+int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T, const int32_t* seg_offsets,
+                     const int32_t* seg_adapter_ids, int n_seg, const void* const* A, const void* const* B,
+                     const float* scale, int n_adapters, void* y, cudaStream_t stream) {
+    if (!h) return LORA_EINVAL;
+    int rc = validate_fp8(h->d_in, h->d_out, h->rank, h->max_tokens, h->max_segments, f, x, T, seg_offsets,
+                          seg_adapter_ids, n_seg, A, B, scale, n_adapters, y);
+    if (rc != LORA_OK || T == 0) return rc;
+    Plan plan;
+    rc = plan_segments(seg_offsets, seg_adapter_ids, n_seg, T, n_adapters, &plan);
+    if (rc != LORA_OK) return rc;
+    const int nf = (int)plan.fused.size(), n_m = (int)plan.seg_id.size();
+    if (nf > h->max_fused) return LORA_EINVAL;
+    const int n_used = (int)plan.used_adapters.size();
+    std::vector<int> compact(n_adapters + 1, 0);
+    for (int k = 0; k < n_used; ++k) compact[plan.used_adapters[k] + 1] = k + 1;
+    for (Tile& t : plan.fused) t.adapter = compact[t.adapter];
+    for (Tile& t : plan.shrink) t.adapter = compact[t.adapter];
+    for (int32_t& a : plan.seg_id) a = compact[a];
+    for (int i = 0; i < nf; ++i) plan.fused[i].fused_index = plan.fused[i].split_index = i;
+
+    DeviceGuard guard(h->device);
+    const Fp8Shape s8 = fp8_shape(h, plan);
+    const int cg = s8.wide ? 2 : 1;
+    std::vector<Tile> groups;
+    make_groups(plan.fused, cg, false, h->u_rows - kTileM, &groups);
+    const int nft = (int)groups.size();
+
+    // the shrink (bf16): launched ahead, over rank tiles so that a few groups still find most SMs
+    Shape sh;
+    int rank_tiles = 1;
+    if (n_used) {
+        sh = choose_shape(h, plan, false);
+        sh.bk = 64;
+        sh.a_rows = kTileM;
+        const int sg = (int)(sh.shrink_groups.size() / sh.cs);
+        const int room = std::max(1, usable_sms(h) / sh.cs / sg);
+        const int width = std::max(32, ceil_div(ceil_div(h->rank, std::min(room, 8)), 32) * 32);
+        if (width < sh.shrink_n) {
+            rank_tiles = ceil_div(h->rank, width);
+            sh.shrink_n = width;
+        }
+        sh.tile_n = sh.shrink_n;
+        sh.stages = stages_for(sh.shrink_n / sh.cs, sh.bk);
+    }
+    const int nst = n_used ? (int)sh.shrink_groups.size() : 0;
+    for (const Tile& t : groups)
+        if (t.adapter < 0 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T ||
+            (t.adapter && t.u_row != t.row0 && t.u_row != h->u_rows - kTileM))
+            return LORA_EINVAL;
+    for (int i = 0; i < nst; ++i) {
+        const Tile& t = sh.shrink_groups[i];
+        if (t.adapter < 1 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T) return LORA_EINVAL;
+    }
+
+    const bool inline_wl = h->allow_inline && nft + nst <= kInlineTiles && n_m <= kInlineSegs && n_used <= kInlineAdapters;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return LORA_ECUDA;
+    if (capture != cudaStreamCaptureStatusNone && !inline_wl) return LORA_EUNSUPPORTED;   // as lora_linear_forward
+
+    Fp8Params q;
+    memset(&q, 0, sizeof(q));
+    GemmParams p;
+    if (n_used) memset(&p, 0, sizeof(p));
+    Slot* slot = nullptr;
+    // B_a's maps for this kernel's boxes, A_a's for the shrink's
+    auto maps = [&](CUtensorMap* b, CUtensorMap* a) {
+        for (int k = 0; k < n_used; ++k) {
+            const int i = plan.used_adapters[k];
+            if (encode_2d(h, &b[k], B[i], h->rank, h->d_out, 64, s8.tile_n / cg) != CUDA_SUCCESS ||
+                encode_2d(h, &a[k], A[i], h->d_in, h->rank, 64, sh.shrink_n / sh.cs) != CUDA_SUCCESS)
+                return false;
+        }
+        return true;
+    };
+    if (inline_wl) {
+        memcpy(q.inline_tiles, groups.data(), (size_t)nft * sizeof(Tile));
+        q.inline_wl = 1;
+        if (n_used) {
+            if (!maps(q.inline_bmaps, p.inline_maps + kInlineAdapters)) return LORA_ECUDA;
+            memcpy(p.inline_tiles, sh.shrink_groups.data(), (size_t)nst * sizeof(Tile));
+            memcpy(p.inline_seg, plan.seg_off.data(), 4 * (size_t)(n_m + 1));
+            memcpy(p.inline_seg + n_m + 1, plan.seg_id.data(), 4 * (size_t)n_m);
+            for (int k = 0; k < n_used; ++k) p.inline_scales[k] = scale[plan.used_adapters[k]];
+            p.inline_wl = 1;
+        }
+    } else {
+        slot = acquire_slot(h);
+        if (!slot) return LORA_ECUDA;
+        // work list: [B_a maps][A_a maps][row groups][shrink groups][seg_off][seg_id][scales]
+        const size_t off_a = (size_t)n_used * sizeof(CUtensorMap), off_tiles = align_up(2 * off_a, 128);
+        const size_t off_shrink = off_tiles + (size_t)nft * sizeof(Tile);
+        const size_t off_seg = align_up(off_shrink + (size_t)nst * sizeof(Tile), 16);
+        const size_t off_id = off_seg + 4 * (size_t)(n_m + 1), off_scale = align_up(off_id + 4 * (size_t)n_m, 16);
+        const size_t bytes = off_scale + 4 * (size_t)n_used;
+        if (bytes > h->slot_bytes) return LORA_EINVAL;
+        uint8_t* hb = slot->host;
+        if (!maps(reinterpret_cast<CUtensorMap*>(hb), reinterpret_cast<CUtensorMap*>(hb + off_a))) return LORA_ECUDA;
+        memcpy(hb + off_tiles, groups.data(), (size_t)nft * sizeof(Tile));
+        if (nst) memcpy(hb + off_shrink, sh.shrink_groups.data(), (size_t)nst * sizeof(Tile));
+        memcpy(hb + off_seg, plan.seg_off.data(), 4 * (size_t)(n_m + 1));
+        memcpy(hb + off_id, plan.seg_id.data(), 4 * (size_t)n_m);
+        for (int k = 0; k < n_used; ++k) reinterpret_cast<float*>(hb + off_scale)[k] = scale[plan.used_adapters[k]];
+        if (cudaMemcpyAsync(slot->dev, hb, bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess) return LORA_ECUDA;
+        q.tm_b = reinterpret_cast<const CUtensorMap*>(slot->dev);
+        q.tiles = reinterpret_cast<const Tile*>(slot->dev + off_tiles);
+        if (n_used) {
+            p.tm_a = reinterpret_cast<const CUtensorMap*>(slot->dev + off_a);
+            p.shrink_tiles = reinterpret_cast<const Tile*>(slot->dev + off_shrink);
+            p.seg_off = reinterpret_cast<const int32_t*>(slot->dev + off_seg);
+            p.seg_id = reinterpret_cast<const int32_t*>(slot->dev + off_id);
+            p.scales = reinterpret_cast<const float*>(slot->dev + off_scale);
+        }
+    }
+    TimingRec rec{};
+    const bool timing = h->timing && capture == cudaStreamCaptureStatusNone;
+    if (timing) {
+        for (int i = 0; i < 3; ++i) {
+            rec.ev[i] = take_event(h);
+            if (!rec.ev[i]) return LORA_ECUDA;
+        }
+        cudaEventRecord(rec.ev[0], stream);
+    }
+    if (n_used) {
+        if (encode_2d(h, &p.tm_x, x, h->d_in, T, 64, kTileM) != CUDA_SUCCESS) return LORA_ECUDA;
+        p.u = h->u_ws;
+        p.status = h->status;
+        p.wait_limit_ns = h->wait_limit_ns;
+        p.n_seg = n_m;
+        p.n_shrink = nst / sh.cs;
+        p.shrink_ntiles = rank_tiles;
+        p.tile_n = sh.tile_n;
+        p.shrink_n = sh.shrink_n;
+        p.stages = sh.stages;
+        p.k_main_blocks = ceil_div(h->d_in, 64);
+        p.k_lora_blocks = ceil_div(h->rank, 64);
+        p.bk = 64;
+        p.mma_group = h->mma_group ? h->mma_group : (sh.cs > 1 || nf == 1) ? 2 : 1;
+        p.d_out = h->d_out;
+        p.rank = h->rank;
+        p.cluster_size = sh.cs;
+        p.debug_stall = h->debug_stall;
+        const int slots = sh.cs > 1 ? std::min(max_clusters(h, p), usable_sms(h) / sh.cs) : usable_sms(h);
+        if (slots < 1) return LORA_ECUDA;
+        if (launch_gemm(p, std::min(p.n_shrink * rank_tiles, slots) * sh.cs, stream) != cudaSuccess) return LORA_ECUDA;
+        ++h->launches;
+        rec.has_shrink = true;
+    }
+    if (timing) cudaEventRecord(rec.ev[1], stream);
+    if (encode_u8_sw128(h, &q.tm_x, f.x8, h->d_in, T, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
+        encode_u8_sw128(h, &q.tm_w, f.w8, h->d_in, h->d_out, (uint32_t)(s8.tile_n / cg)) != CUDA_SUCCESS ||
+        encode_2d(h, &q.tm_u, h->u_ws, h->rank, h->u_rows, 64, (uint32_t)s8.a_rows) != CUDA_SUCCESS)
+        return LORA_ECUDA;
+    q.xs = f.xs;
+    q.ws = f.ws;
+    q.y = y;
+    q.status = h->status;
+    q.wait_limit_ns = h->wait_limit_ns;
+    q.n_groups = nft / cg;
+    q.n_ntiles = s8.n_ntiles;
+    q.tile_n = s8.tile_n;
+    q.raster_group = s8.raster_group;
+    q.k_blocks = ceil_div(h->d_in, kFp8Group);
+    q.k_lora = ceil_div(h->rank, 64);
+    q.d_out = h->d_out;
+    q.parts = s8.parts;
+    q.a_rows = s8.a_rows;
+    q.stages = s8.stages;
+    q.wide = s8.wide;
+    q.debug_stall = h->debug_stall;
+    const int units = q.n_groups * q.n_ntiles;
+    const int grid = s8.wide ? std::min(units, usable_sms(h) / 2) * 2 : units * s8.parts;
+    if (launch_fp8(q, grid, stream) != cudaSuccess) return LORA_ECUDA;
+    ++h->launches;
+    if (timing) {
+        cudaEventRecord(rec.ev[2], stream);
+        h->trec.push_back(rec);
+    }
+    if (slot) {
+        if (cudaEventRecord(slot->done, stream) != cudaSuccess) return LORA_ECUDA;
+        slot->pending = true;
+    }
+    return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" int lora_linear_forward_fp8(lora_linear* h, const void* x8, const float* x_scales, const void* x, int T,
+                                       const int32_t* seg_offsets, const int32_t* seg_adapter_ids, int n_seg,
+                                       const void* w8, const float* w_scales, const void* const* A,
+                                       const void* const* B, const float* scale, int n_adapters, void* y, void* stream) {
+    return forward_fp8_impl(h, Fp8Operands{x8, w8, x_scales, w_scales}, x, T, seg_offsets, seg_adapter_ids, n_seg, A, B,
+                            scale, n_adapters, y, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int lora_linear_validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments, const void* x8,
+                                        const float* x_scales, const void* x, int T, const int32_t* seg_offsets,
+                                        const int32_t* seg_adapter_ids, int n_seg, const void* w8, const float* w_scales,
+                                        const void* const* A, const void* const* B, const float* scale, int n_adapters,
+                                        const void* y) {
+    return validate_fp8(d_in, d_out, rank, max_tokens, max_segments, Fp8Operands{x8, w8, x_scales, w_scales}, x, T,
+                        seg_offsets, seg_adapter_ids, n_seg, A, B, scale, n_adapters, y);
+}
 
 // Row boundaries of the host-buffer path's chunks: {0, T} below 2,048 rows; else chunks of up to
 // max(1024, T / 8) rows (multiples of 128) between ramps that halve down to max(256, T / 32) rows

@@ -1,0 +1,50 @@
+// Internal declarations of the 8-bit-base kernel (kernels_fp8.cu) and its host side (not
+// installed). Kept apart from lora_internal.h so that the other kernels' sources do not change
+// when only this kernel's parameters do.
+#pragma once
+
+#include "lora_internal.h"
+
+namespace lora {
+
+constexpr int kFp8Group = 128;        // input features per scale; a base weight's block is 128 x 128
+constexpr int kFp8Threads = 384;      // warp 0 TMA, 1 and 2 MMA, 3 owns TMEM, 4..11 epilogue
+constexpr int kFp8MaxParts = 8;       // most parts of K: one CTA of a cluster each
+constexpr int kFp8SmemTwo = 115200;   // the most dynamic shared memory that lets two CTAs share an SM
+constexpr int kFp8StageRow = 128;     // bytes of a stage's row: one group of e4m3, 64 bf16 of the expand
+
+// One launch. Units are (row group, output tile) blocks of Y; a row group is one planner tile, or two
+// that share the weight's tile on an SM pair (wide form).
+struct Fp8Params {
+    CUtensorMap inline_bmaps[kInlineAdapters];   // B_a [d_out, rank] bf16 (inline work list)
+    Tile inline_tiles[kInlineTiles];
+    int inline_wl;
+    CUtensorMap tm_x;                 // X [T, d_in] e4m3, box 128 x a_rows, 128-byte swizzle
+    CUtensorMap tm_w;                 // W [d_out, d_in] e4m3, box 128 x tile_n / CTAs of the group
+    CUtensorMap tm_u;                 // U [u_rows, rank] bf16, box 64 x a_rows
+    const CUtensorMap* tm_b;          // device array per compact adapter (when not inline)
+    const Tile* tiles;                // device array (when not inline)
+    const float* xs;                  // [T, k_blocks]
+    const float* ws;                  // [ceil(d_out / 128), k_blocks]
+    void* y;                          // [T, d_out] bf16
+    int* status;
+    unsigned long long wait_limit_ns;
+    int n_groups;                     // row groups
+    int n_ntiles, tile_n;             // output tiles: a multiple of 32 up to 128; 256 in the wide form
+    int raster_group;                 // column tiles whose row groups run before the next column tiles
+    int k_blocks;                     // ceil(d_in / 128)
+    int k_lora;                       // ceil(rank / 64)
+    int d_out;
+    int parts;                        // K parts of a unit (1 in the wide form)
+    int a_rows;                       // rows of an A box: 128, or fewer (a multiple of 16) for a batch of one tile
+    int stages;
+    int wide;                         // SM pairs, 256 x 256 blocks, persistent
+    int debug_stall;
+};
+
+// kernels_fp8.cu
+size_t fp8_smem_bytes(int tile_rows, int a_rows, int stages);   // tile_rows: rows of a stage's weight tile
+cudaError_t fp8_prepare_device();
+cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream);
+
+}  // namespace lora

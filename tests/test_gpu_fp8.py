@@ -1,0 +1,230 @@
+"""The projection with 8-bit activations and base (lora_linear_forward_fp8) against 64 bits on the values that its
+operands stand for.
+
+Bound of an output: it is rounded to bf16 once, half a step, 2^-8 of the value; products of e4m3 values are exact in
+fp32, and a sum of n fp32 terms in any order is off by at most n 2^-24 of the sum of their magnitudes, S: the 128 of a
+group's products, the groups' scaled sums (each with the rounding of its scales' product and its own) and the expand
+make at most n = 128 + 2 x 136 + 256 < 2^10 roundings on the way of one term, 2^-14 S. The tensor cores' own sums carry
+fewer guard bits than an fp32 addition: 2^-13 S allows for two of them. U is rounded to bf16: 2^-8 of |U| |B|^T."""
+import pytest
+import torch
+
+from mixed_lora_projection_gb300 import LoraLinear
+
+pytestmark = pytest.mark.gpu
+
+F64, BF16, FP8 = torch.float64, torch.bfloat16, torch.float8_e4m3fn
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+class Case:
+    def __init__(self, d_in, d_out, rank, rows, ids, seed=0, spread=6):
+        g = gen(seed)
+        dev = torch.device("cuda")
+        self.d_in, self.d_out, self.rank, self.ids = d_in, d_out, rank, list(ids)
+        self.off = [0]
+        for n in rows:
+            self.off.append(self.off[-1] + n)
+        self.T = T = self.off[-1]
+        G, NB = -(-d_in // 128), -(-d_out // 128)
+        # codes over the whole range of e4m3, scales over 2^spread
+        def codes(r, c):
+            return (torch.randn(r, c, generator=g, device=dev) * 60).clamp(-448, 448).to(FP8)
+        def scales(*s):
+            return torch.exp2(torch.rand(s, generator=g, device=dev) * spread - spread / 2)
+        self.x8, self.xs = codes(T, d_in), scales(T, G) / 60
+        self.w8, self.ws = codes(d_out, d_in), scales(NB, G) / 60 * d_in ** -0.5
+        na = max(ids, default=0)
+        self.x = torch.randn(T, d_in, generator=g, device=dev).to(BF16)
+        self.a = [(torch.randn(rank, d_in, generator=g, device=dev) * d_in ** -0.5).to(BF16) for _ in range(na)]
+        self.b = [(torch.randn(d_out, rank, generator=g, device=dev) * rank ** -0.5).to(BF16) for _ in range(na)]
+        self.s = [1.0, -0.5, 2.0, 0.25, 1.5, 0.75][:na] + [1.0] * max(0, na - 6)
+        self.linear = LoraLinear(d_in, d_out, rank, max(T, 1), max(1, len(ids)))
+
+    def run(self, **kw):
+        kw.setdefault("x", self.x)
+        return self.linear.forward_fp8(self.x8, self.xs, self.off, self.ids, self.w8, self.ws, self.a, self.b, self.s, **kw)
+
+    def reference(self):
+        """(y, bound) in 64 bits."""
+        x = self.x8.to(F64) * self.xs.to(F64).repeat_interleave(128, 1)[:, :self.d_in]
+        w = self.w8.to(F64) * self.ws.to(F64).repeat_interleave(128, 0)[:self.d_out].repeat_interleave(128, 1)[:, :self.d_in]
+        y, S, more = x @ w.T, x.abs() @ w.abs().T, torch.zeros(self.T, self.d_out, dtype=F64, device=x.device)
+        for i, a in enumerate(self.ids):
+            r = slice(self.off[i], self.off[i + 1])
+            if a:
+                A, B, xr = self.a[a - 1].to(F64), self.b[a - 1].to(F64), self.x[r].to(F64)
+                u = xr @ A.T * self.s[a - 1]
+                y[r] += u @ B.T
+                S[r] += u.abs() @ B.abs().T
+                more[r] = (2.0 ** -8 * u.abs() + 2.0 ** -13 * abs(self.s[a - 1]) * (xr.abs() @ A.abs().T)) @ B.abs().T
+        return y, 2.0 ** -8 * y.abs() + 2.0 ** -13 * S + 1.01 * more
+
+    def check(self, y):
+        assert self.linear.status() == 0
+        ref, bound = self.reference()
+        assert y.shape == ref.shape and y.dtype == BF16
+        worst = ((y.to(F64) - ref).abs() / (bound + 1e-300)).max().item()
+        assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("d_in,d_out,rank,rows,ids", [
+    (128, 128, 16, [1], [0]),
+    (16, 8, 8, [1], [0]),
+    (16, 8, 8, [1], [1]),
+    (144, 136, 8, [3], [1]),
+    (256, 512, 16, [32, 32], [0, 1]),
+    (6144, 5120, 256, [1], [0]),
+    (6144, 5120, 256, [1], [1]),
+    (1040, 1288, 40, [127], [0]),
+    (5120, 1288, 200, [48], [0]),
+    (17408, 640, 256, [8, 0, 9], [1, 2, 0]),
+    (1280, 2568, 256, [129], [1]),
+    (640, 520, 64, [100, 100, 100], [0, 2, 1]),
+    (256, 136, 16, [384], [0]),
+    (2064, 1032, 72, [385], [1]),
+    (640, 520, 256, [200, 1, 400, 33], [0, 1, 0, 2]),
+    (512, 264, 24, [128, 128, 128, 128, 7], [0, 1, 0, 1, 2]),
+    (1024, 8, 8, [700], [1]),
+    (5120, 2056, 256, [2049], [1]),
+    (384, 40, 16, [16384], [0]),
+])
+def test_against_64_bits(d_in, d_out, rank, rows, ids):
+    c = Case(d_in, d_out, rank, rows, ids, seed=d_in + d_out + rank)
+    y = c.run()
+    c.check(y)
+    assert torch.equal(c.run(), y)                          # the same call, the same bits
+
+
+@pytest.mark.parametrize("T", list(range(1, 20)) + [31, 63, 64, 65, 96, 111, 128, 130, 255, 256, 257, 383, 511, 512, 513])
+def test_row_counts(T):
+    c = Case(384, 264, 16, [T], [T % 2], seed=T)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("d_out", [8, 24, 32, 40, 64, 96, 120, 128, 136, 160, 256, 264, 384, 1000, 4104])
+def test_output_widths(d_out):
+    for T in (5, 520):
+        c = Case(1536, d_out, 32, [T], [1], seed=d_out)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("d_in", [16, 32, 112, 128, 144, 240, 256, 272, 384, 1000 // 16 * 16, 2048, 2064])
+def test_input_widths(d_in):
+    for T in (17, 600):
+        c = Case(d_in, 200, 8, [T], [0], seed=d_in)
+        c.check(c.run())
+
+
+def test_many_segments_travel_in_an_uploaded_list():
+    ids = [i % 6 for i in range(90)]
+    c = Case(256, 136, 32, [1 + 7 * i % 50 for i in range(90)], ids, seed=3)
+    y = c.run()
+    c.check(y)
+    # the host's lists are read before the call returns, and calls in a row keep their own
+    ys = [c.run() for _ in range(12)]
+    assert all(torch.equal(v, y) for v in ys)
+
+
+def test_rows_around_the_output_stay():
+    for T in (5, 700):
+        c = Case(256, 264, 16, [T], [1], seed=T)
+        room = torch.full((T + 2, 264), 7.0, dtype=BF16, device="cuda")
+        c.check(c.run(y=room[1:T + 1]))
+        assert (room[0] == 7).all() and (room[T + 1] == 7).all()
+
+
+def test_a_row_with_nan_or_infinity_stays_alone():
+    for T in (60, 600):
+        c = Case(640, 264, 16, [T], [0], seed=9)
+        c.x8.view(torch.uint8)[3, 200] = 0x7f                # NaN
+        c.xs[5, 1] = float("inf")
+        c.xs[7, 2] = float("nan")
+        y = c.run()
+        assert torch.isnan(y[3]).all() and torch.isnan(y[7]).all() and not torch.isfinite(y[5]).any()
+        rest = [t for t in range(T) if t not in (3, 5, 7)]
+        ref, bound = c.reference()
+        assert ((y.to(F64) - ref).abs() <= bound)[rest].all()
+
+
+def test_zero_scales_give_zeros():
+    c = Case(256, 136, 16, [40], [0], seed=2)
+    c.xs.zero_()
+    assert (c.run() == 0).all()
+
+
+def test_rows_without_adapters_need_no_bf16_input():
+    c = Case(256, 136, 16, [3, 4], [0, 0], seed=2)
+    c.check(c.run(x=None))
+    # segments without rows name adapters in vain
+    d = Case(256, 136, 16, [3, 0], [0, 1], seed=2)
+    d.check(d.run(x=None))
+    e = Case(256, 136, 16, [3, 4], [0, 1], seed=2)
+    with pytest.raises(Exception, match="invalid argument"):
+        e.run(x=None)
+
+
+def test_no_rows():
+    c = Case(256, 136, 16, [0], [0])
+    assert c.run().shape == (0, 136)
+
+
+def test_graph_and_streams():
+    cases = [Case(1280, 520, 32, rows, ids, seed=i) for i, (rows, ids) in enumerate([([8] * 6, [0] * 6), ([8, 300], [0, 1]), ([700], [1])])]
+    want = [c.run() for c in cases]
+    outs = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c, o in zip(cases, outs):
+            c.run(y=o)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    # each on a stream of its own, side by side, and through the stream argument
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in cases]
+    for _ in range(20):
+        for g, c, s in zip(got, cases, streams):
+            g.append(c.run(stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for g, w in zip(got, want) for y in g)
+
+
+def test_chained_calls_read_what_the_call_before_wrote():
+    # the second projection's activations are brought to 8 bits by torch in between, on one stream, without a wait
+    a = Case(512, 512, 16, [48], [0], seed=1)
+    b = Case(512, 264, 16, [48], [0], seed=2)
+    want = None
+    for _ in range(50):
+        y = a.run()
+        b.x8.copy_(y.clamp(-448, 448).to(FP8))
+        z = b.run()
+        want = z if want is None else want
+        assert torch.equal(z, want)
+    b.check(want)
+
+
+@pytest.mark.parametrize("T,ids", [(48, 0), (700, 1)])
+def test_a_wait_that_runs_out_is_reported(T, ids):
+    from mixed_lora_projection_gb300 import _lib
+    c = Case(640, 264, 16, [T], [ids], seed=1)
+    y = c.run()
+    c.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 2000)
+    c.linear.set_option(_lib.OPT_DEBUG_STALL, 1)
+    c.run()
+    assert c.linear.status() == _lib.LORA_ETIMEOUT
+    c.linear.set_option(_lib.OPT_DEBUG_STALL, 0)
+    assert c.linear.status(reset=True) == _lib.LORA_ETIMEOUT
+    c.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 4000000)
+    assert torch.equal(c.run(), y) and c.linear.status() == 0
