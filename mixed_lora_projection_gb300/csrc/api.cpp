@@ -1529,20 +1529,12 @@ Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
     Fp8Shape s;
     const int nf = (int)plan.fused.size(), k_blocks = ceil_div(h->d_in, kFp8Group);
     s.wide = nf >= 4;
-    if (s.wide) {
-        s.tile_n = 256;
-        s.n_ntiles = ceil_div(h->d_out, s.tile_n);
-        s.raster_group = ceil_div(s.n_ntiles, 2);
-        while (s.stages < kMaxStages && fp8_smem_bytes(s.tile_n / 2, s.a_rows, s.stages + 1) <= (size_t)kSmemLimit) ++s.stages;
-        return s;
-    }
-    // two CTAs an SM
-    const int room = 2 * usable_sms(h);
-    s.tile_n = 128;
+    s.tile_n = s.wide ? 256 : 128;
     s.n_ntiles = ceil_div(h->d_out, s.tile_n);
-    while (s.parts < kFp8MaxParts && nf * s.n_ntiles * s.parts * 2 <= room && s.parts * 2 <= k_blocks) s.parts *= 2;
-    if (nf == 1) s.a_rows = std::max(16, ceil_div(plan.fused[0].nrows, 16) * 16);
-    while (s.stages < kMaxStages && fp8_smem_bytes(s.tile_n, s.a_rows, s.stages + 1) <= (size_t)kFp8SmemTwo) ++s.stages;
+    if (s.wide) s.raster_group = ceil_div(s.n_ntiles, 2);
+    else if (nf == 1) s.a_rows = std::max(16, ceil_div(plan.fused[0].nrows, 16) * 16);
+    while (s.stages < kMaxStages && fp8_smem_bytes(s.wide, s.tile_n, s.a_rows, s.stages + 1) <= (size_t)kSmemLimit) ++s.stages;
+    (void)k_blocks;
     return s;
 }
 
@@ -1629,6 +1621,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return LORA_ECUDA;
     if (capture != cudaStreamCaptureStatusNone && !inline_wl) return LORA_EUNSUPPORTED;   // as lora_linear_forward
 
+    const int q_groups = ceil_div(h->d_in, kFp8Group);
     Fp8Params q;
     memset(&q, 0, sizeof(q));
     GemmParams p;
@@ -1720,9 +1713,12 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     if (timing) cudaEventRecord(rec.ev[1], stream);
     if (encode_u8_sw128(h, &q.tm_x, f.x8, h->d_in, T, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_u8_sw128(h, &q.tm_w, f.w8, h->d_in, h->d_out, (uint32_t)(s8.tile_n / cg)) != CUDA_SUCCESS ||
-        encode_2d(h, &q.tm_u, h->u_ws, h->rank, h->u_rows, 64, (uint32_t)s8.a_rows) != CUDA_SUCCESS)
+        encode_2d(h, &q.tm_u, h->u_ws, h->rank, h->u_rows, 64, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
+        encode_2d(h, &q.tm_y, y, h->d_out, T, s8.wide ? 64 : 32, 32) != CUDA_SUCCESS)
         return LORA_ECUDA;
     q.xs = f.xs;
+    q.rows = T;
+    q.vec_scales = q_groups % 4 == 0 && aligned16(f.xs) && aligned16(f.ws);
     q.ws = f.ws;
     q.y = y;
     q.status = h->status;
@@ -1731,7 +1727,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.n_ntiles = s8.n_ntiles;
     q.tile_n = s8.tile_n;
     q.raster_group = s8.raster_group;
-    q.k_blocks = ceil_div(h->d_in, kFp8Group);
+    q.k_blocks = q_groups;
     q.k_lora = ceil_div(h->rank, 64);
     q.d_out = h->d_out;
     q.parts = s8.parts;
@@ -1740,7 +1736,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.wide = s8.wide;
     q.debug_stall = h->debug_stall;
     const int units = q.n_groups * q.n_ntiles;
-    const int grid = s8.wide ? std::min(units, usable_sms(h) / 2) * 2 : units * s8.parts;
+    const int grid = s8.wide ? std::min(units, usable_sms(h) / 2) * 2 : s8.parts > 1 ? units * s8.parts : std::min(units, usable_sms(h));
     if (launch_fp8(q, grid, stream) != cudaSuccess) return LORA_ECUDA;
     ++h->launches;
     if (timing) {

@@ -6,13 +6,13 @@
 //
 // A group's 128 products are summed by tcgen05.mma kind::f8f6f4 in tensor memory; each group has a scale of
 // its own per row and block of columns, so its sums leave tensor memory and are added, times that scale, to
-// fp32 accumulators in the epilogue warps' registers. The expand is one more such block (kind::f16, bf16
-// operands, all of the rank) with scale 1.
+// fp32 accumulators in the epilogue warps' registers. The expand's 64-wide K-steps are more such blocks (kind::f16,
+// bf16 operands) with scale 1.
 //
 // Per CTA: warp 0 loads the stages (TMA, rows of 128 bytes, 128-byte swizzle: 128 e4m3 or 64 bf16); warps 1 and
 // 2 issue the even and the odd blocks' MMAs into the two TMEM buffers (a warp's barrier wait completes after the
-// MMAs that it issued, so one warp's waits run under the other's MMAs); warp 3 owns TMEM; warps 4..11 are the
-// epilogue, two per TMEM lane quadrant, half of the columns each.
+// MMAs that it issued, so one warp's waits run under the other's MMAs); warp 3 owns TMEM and lays the blocks'
+// scales out in shared memory; the others are the epilogue, two per TMEM lane quadrant, half of the columns each.
 //
 // Every mbarrier wait is bounded by a wall-clock limit; a wait that runs out sets bit 0 of the status word and a
 // CTA-wide abort flag, and all roles leave their loops, wait (bounded) for their own copies and MMAs in flight,
@@ -62,6 +62,35 @@ __device__ __forceinline__ void tmem_wait16(uint32_t* v) {   // v, of the thread
                  :
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+// The warp's rows of Y in shared memory to global memory; the elected lane's group of copies.
+__device__ __forceinline__ void store_rows(const CUtensorMap* map, uint32_t src, int col, int row) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(col), "r"(row), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Two fp32 values in one instruction.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -76,6 +105,20 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
+}
+
+// Arrive on another CTA's barrier without a release: what it orders is this warp's reads of tensor memory, which have
+// completed (tcgen05.wait::ld, then the fence before it), and no write of this thread's. With the release, which waits
+// for the thread's outstanding loads of scales, a block of the wide form took twice as long.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// One lane of a converged warp, the same one each time: commits are for the MMAs of the lane that issues them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 template <int N>
@@ -111,48 +154,63 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// The blocks of one unit as every role walks them: base groups [kb0, kb0 + nk), then the expand's block.
+// The blocks of one unit as every role walks them: base groups [kb0, kb0 + nk), then the expand's K-steps; nb in all.
 struct Work {
     Tile tile;
-    int n0, kb0, nk, expand;
+    int n0, kb0, nk, nb;
 };
-template <int CG>
+template <int CG, int NT>
 __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, int u, int rank, int part) {
     Work w;
     const int per = p.n_groups * p.raster_group;
     const int g = u / per, r = u - g * per;
     const int gw = min(p.raster_group, p.n_ntiles - g * p.raster_group);
     w.tile = tiles[(r / gw) * CG + rank];
-    w.n0 = (g * p.raster_group + r % gw) * p.tile_n;
+    w.n0 = (g * p.raster_group + r % gw) * NT;
     w.kb0 = part * p.k_blocks / p.parts;
     w.nk = (part + 1) * p.k_blocks / p.parts - w.kb0;
-    w.expand = w.tile.adapter && part == p.parts - 1;
+    w.nb = w.nk + (w.tile.adapter && part == p.parts - 1 ? p.k_lora : 0);
     return w;
 }
 
-// NT: columns of a TMEM buffer, NT / 2 of them in each epilogue thread's registers. Registers of the launch are
-// dealt out anew: the loading warps' to the epilogue's accumulators (LOW x 128 + HIGH x 256 <= 384 x the launch's).
-template <int CG, int NT, int BLOCKS, int LOW, int HIGH>
-__global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __grid_constant__ Fp8Params p) {
-    static_assert(CG == 1 || NT == 256, "SM pairs run 256-column blocks");
-    constexpr int kHalf = NT / 2, kChunks = kHalf / 16;
+// The scales of four blocks of a unit, as warp 3 lays them out for the epilogue, and the unit's place.
+struct ScaleSlot {
+    float f[4][2][kTileM];                             // per block, half of the columns and row: xs ws
+    int row0, nrows, n0, nb;
+};
+
+// CG: CTAs of the MMA's group; NT: columns of a TMEM buffer, half of them in each epilogue thread's registers. Registers
+// of the launch are dealt out anew: the loading warps' to the accumulators (LOW x 128 + HIGH x 256 <= 384 x the launch's).
+template <int CG, int NT, int LOW, int HIGH>
+__global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_constant__ Fp8Params p) {
+    constexpr int EW = 8;                              // epilogue warps
+    constexpr int kCols = NT / 2;                      // columns of an epilogue thread
+    constexpr int kBufs = 512 / NT;                    // TMEM buffers
+    constexpr int kYCols = CG > 1 ? 64 : 32;           // columns of a warp's part of the output at a time
+    constexpr int kYStage = 64 * kYCols;               // its bytes
+    static_assert(NT == 256 || (CG == 1 && NT == 128), "SM pairs run 256-column blocks");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int stages = p.stages;
     const uint32_t a_bytes = (uint32_t)p.a_rows * kFp8StageRow;
-    const uint32_t b_bytes = (uint32_t)(p.tile_n / CG) * kFp8StageRow;
+    const uint32_t b_bytes = (uint32_t)(NT / CG) * kFp8StageRow;
     // an A stage of fewer than 128 rows: the MMA's other rows read what follows in the rings, and are never stored
     uint8_t* a_ring = base;
     uint8_t* b_ring = a_ring + (size_t)stages * a_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(b_ring + (size_t)stages * b_bytes);
+    uint8_t* after = b_ring + (size_t)stages * b_bytes;
+    uint8_t* y_stage = after;                          // the epilogue's output rows
+    ScaleSlot* slots = reinterpret_cast<ScaleSlot*>(after + EW * kYStage);
+    uint64_t* full = reinterpret_cast<uint64_t*>(slots + 2);
     uint64_t* empty = full + stages;
     uint64_t* tfull = empty + stages;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* drain = tempty + 2;
+    uint64_t* tempty = tfull + kBufs;
+    uint64_t* sfull = tempty + kBufs;
+    uint64_t* sempty = sfull + 2;
+    uint64_t* drain = sempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (uniform for the compiler too)
     const int cta = p.parts > 1 || CG > 1 ? (int)cluster_ctarank() : 0;
     const int rank = CG > 1 ? cta : 0, part = CG > 1 ? 0 : cta;
     const bool leader = rank == 0;
@@ -165,15 +223,19 @@ __global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __g
             mbar_init(smem_addr(&full[s]), 1);
             mbar_init(smem_addr(&empty[s]), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kBufs; ++b) {
             mbar_init(smem_addr(&tfull[b]), 1);
-            mbar_init(smem_addr(&tempty[b]), CG * 8);
+            mbar_init(smem_addr(&tempty[b]), CG * EW);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&sfull[b]), 1);
+            mbar_init(smem_addr(&sempty[b]), EW);
         }
         mbar_init(smem_addr(drain), 2);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 3) tmem_alloc<CG>(smem_addr(tmem_slot), 2 * NT);
+    if (warp == 3) tmem_alloc<CG>(smem_addr(tmem_slot), 512);
     tc_fence_before();
     if (CG > 1) cluster_sync();
     else __syncthreads();
@@ -187,34 +249,35 @@ __global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __g
 
     if (warp < 4) {
         regs_dec<LOW>();
-        const uint32_t issuer = lane == 0 ? 1u : 0u;
         if (warp == 0 && !p.debug_stall) {
-            // ------------------------------------------------------------ TMA producer (lane 0 issues)
+            // ------------------------------------------------------------ TMA producer
             int stage = 0, issued = 0, acquired = 0;
             uint32_t phase = 0;
             bool ok = true;
             const uint32_t tx = CG * (a_bytes + b_bytes);
             for (int u = first; u < n_units && ok; u += step) {
-                const Work w = decode<CG>(p, tiles, u, rank, part);
-                const int nb = w.nk + (w.expand ? p.k_lora : 0);
-                const CUtensorMap* bm = &bmaps[w.expand ? w.tile.adapter - 1 : 0];
-                if (w.expand && !p.inline_wl && acquired != w.tile.adapter) {
+                const Work w = decode<CG, NT>(p, tiles, u, rank, part);
+                const CUtensorMap* bm = &bmaps[w.nb > w.nk ? w.tile.adapter - 1 : 0];
+                if (w.nb > w.nk && !p.inline_wl && acquired != w.tile.adapter) {
                     tensormap_acquire(bm);
                     acquired = w.tile.adapter;
                 }
-                for (int b = 0; b < nb; ++b) {
+                for (int b = 0; b < w.nb; ++b) {
                     if (!wait_all(smem_addr(&empty[stage]), phase ^ 1, abort_flag, p.status, limit)) {
                         ok = false;
                         break;
                     }
                     const uint32_t bar = smem_addr(&full[stage]);
-                    mbar_arrive_expect_tx(bar, tx, leader ? issuer : 0u);
                     const uint32_t fb = CG > 1 ? map_to_rank(bar, 0) : bar;
                     const uint32_t sa = smem_addr(a_ring + (size_t)stage * a_bytes), sb = smem_addr(b_ring + (size_t)stage * b_bytes);
                     const bool main = b < w.nk;
                     const int k = main ? (w.kb0 + b) * kFp8Group : (b - w.nk) * 64;
-                    tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : w.tile.u_row, issuer);
-                    tma_load_2d<CG>(sb, main ? &p.tm_w : bm, fb, k, w.n0 + rank * (p.tile_n / CG), issuer);
+                    if (elect_one()) {
+                        if (leader) mbar_arrive_expect_tx(bar, tx, 1u);
+                        tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : w.tile.u_row, 1u);
+                        tma_load_2d<CG>(sb, main ? &p.tm_w : bm, fb, k, w.n0 + rank * (NT / CG), 1u);
+                    }
+                    __syncwarp();
                     ++issued;
                     if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
@@ -232,54 +295,107 @@ __global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __g
             }
         } else if ((warp == 1 || warp == 2) && leader) {
             // ------------------------------------------------------------ MMA issuers
-            const uint32_t idesc8 = instr_desc_e4m3(kTileM * CG, p.tile_n), idesc16 = instr_desc_bf16(kTileM * CG, p.tile_n);
-            const int mine = warp - 1;                       // parity of the blocks this warp issues, and their buffer
-            const uint32_t d = tmem_base + (uint32_t)(mine * NT);
+            const uint32_t idesc8 = instr_desc_e4m3(kTileM * CG, NT), idesc16 = instr_desc_bf16(kTileM * CG, NT);
+            const int mine = warp - 1;                       // parity of the blocks this warp issues
             int stage = 0, blk = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int u = first; u < n_units && ok; u += step) {
-                const Work w = decode<CG>(p, tiles, u, rank, part);
-                const int nb = w.nk + w.expand;
-                for (int b = 0; b < nb; ++b, ++blk) {
-                    const bool main = b < w.nk;
-                    const int ns = main ? 1 : p.k_lora;
-                    const bool act = (blk & 1) == mine;
-                    if (act && !wait_all(smem_addr(&tempty[mine]), ((blk >> 1) & 1) ^ 1, abort_flag, p.status, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int s = 0; s < ns; ++s) {
-                        if (act) {
-                            if (!wait_all(smem_addr(&full[stage]), phase, abort_flag, p.status, limit)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
-                            const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
-                            // 32 bytes along K inside the swizzled rows a step
-                            if (main) {
+                const Work w = decode<CG, NT>(p, tiles, u, rank, part);
+                for (int b = 0; b < w.nb; ++b, ++blk) {
+                    if ((blk & 1) == mine) {
+                        // The buffer first: it is free when the epilogue has taken block blk - kBufs, and so every stage up
+                        // to that block's has been filled and read. Only then does this stage's parity tell this fill
+                        // from the one a lap (kBufs stages at least) before.
+                        const int buf = blk % kBufs;
+                        const uint32_t d = tmem_base + (uint32_t)(buf * NT);
+                        if (!wait_all(smem_addr(&tempty[buf]), ((blk / kBufs) & 1) ^ 1, abort_flag, p.status, limit) ||
+                            !wait_all(smem_addr(&full[stage]), phase, abort_flag, p.status, limit)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
+                        const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
+                        // 32 bytes along K inside the swizzled rows a step
+                        // (one elected lane, in a branch of its own: 4 MMAs issue in ~100 cycles; under a predicate that the
+                        // compiler cannot tell to be one lane's, in ~550)
+                        if (elect_one()) {
+                            if (b < w.nk) {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    mma_e4m3<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc8, k > 0 ? 1u : 0u, issuer);
+                                    mma_e4m3<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc8, k > 0 ? 1u : 0u, 1u);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    mma_bf16<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc16, (s > 0 || k > 0) ? 1u : 0u,
-                                                 issuer);
+                                    mma_bf16<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc16, k > 0 ? 1u : 0u, 1u);
                             }
-                            mma_commit<CG>(smem_addr(&empty[stage]), issuer);
+                            mma_commit<CG>(smem_addr(&tfull[buf]), 1u);
+                            mma_commit<CG>(smem_addr(&empty[stage]), 1u);
                         }
-                        if (++stage == stages) { stage = 0; phase ^= 1; }
+                        __syncwarp();
                     }
-                    if (!ok) break;
-                    if (act) mma_commit<CG>(smem_addr(&tfull[mine]), issuer);
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
             }
             // every MMA this warp issued has completed before TMEM is released
-            mma_commit_local<CG>(smem_addr(drain), issuer);
+            if (elect_one()) mma_commit_local<CG>(smem_addr(drain), 1u);
+            __syncwarp();
             if (lane == 0) wait_lane(smem_addr(drain), 0, abort_flag, p.status, limit, false);
+        }
+        if (warp == 3) {
+            // ------------------------------------------------------------ scales, up to eight blocks ahead
+            const int G = p.k_blocks;
+            int quad = 0;
+            bool ok = true;
+            for (int u = first; u < n_units && ok; u += step) {
+                const Work w = decode<CG, NT>(p, tiles, u, rank, part);
+                // (rows and columns past the unit's last take that one's)
+                const float *xs[4], *ws[2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    xs[i] = p.xs + (long long)min(w.tile.row0 + min(lane + 32 * i, max(w.tile.nrows - 1, 0)), p.rows - 1) * G;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) ws[h] = p.ws + (long long)(min(w.n0 + h * kCols, p.d_out - 1) >> 7) * G;
+                for (int b = 0; b < w.nb; b += 4, ++quad) {
+                    ScaleSlot& slot = slots[quad & 1];
+                    if (!wait_all(smem_addr(&sempty[quad & 1]), ((quad >> 1) & 1) ^ 1, abort_flag, p.status, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const int g = w.kb0 + b;
+                    // past the last group: the expand's 1
+                    auto take = [&](const float* s, float* v) {
+                        if (p.vec_scales && (g & 3) == 0 && g < G) {
+                            *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(s + g));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) v[k] = __ldg(s + min(g + k, G - 1));
+                        }
+                    };
+                    float c[2][4];
+                    take(ws[0], c[0]);
+                    take(ws[1], c[1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (32 * i >= w.tile.nrows) break;
+                        float x[4];
+                        take(xs[i], x);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) slot.f[k][h][lane + 32 * i] = b + k < w.nk ? x[k] * c[h][k] : 1.f;
+                    }
+                    if (lane == 0) {
+                        slot.row0 = w.tile.row0;
+                        slot.nrows = w.tile.nrows;
+                        slot.n0 = w.n0;
+                        slot.nb = w.nb;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sfull[quad & 1]));
+                }
+            }
         }
         __syncwarp();
         if (CG == 1 && p.parts > 1) {
@@ -289,92 +405,111 @@ __global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __g
     } else {
         // ------------------------------------------------------------ epilogue
         regs_inc<HIGH>();
-        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int q = warp & 3, cg = (warp - 4) >> 2;        // TMEM lane quadrant, group of columns
         const int r_local = q * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-        const int cols = CG > 1 ? kHalf : p.tile_n >> 1;     // of this thread: a multiple of 16
-        const int nblk = (p.d_out + kFp8Group - 1) / kFp8Group;
-        int blk = 0;
+        const uint32_t t0 = tmem_base + (uint32_t)(cg * kCols) + ((uint32_t)(q * 32) << 16);
+        uint8_t* const mine = y_stage + (warp - 4) * kYStage;
+        const uint32_t my_scale = smem_addr(&slots[0].f[0][cg][r_local]);
+        const uint32_t tfull0 = smem_addr(tfull), tempty0 = CG > 1 ? map_to_rank(smem_addr(tempty), 0) : smem_addr(tempty);
+        uint32_t buf = 0, phase = 0, quad = 0;
         bool ok = true;
-        for (int u = first; u < n_units && ok; u += step) {
-            const Work w = decode<CG>(p, tiles, u, rank, part);
-            const int row = w.tile.row0 + r_local;
-            const bool row_ok = r_local < w.tile.nrows;
-            const int c0 = w.n0 + half * cols;
-            // the thread's columns lie in at most two blocks of 128 output features
-            const int b0 = min(c0 >> 7, nblk - 1), b1 = min((c0 + cols - 1) >> 7, nblk - 1);
-            const float* xs = p.xs + (long long)(row_ok ? row : w.tile.row0) * p.k_blocks + w.kb0;
-            const float* ws0 = p.ws + (long long)b0 * p.k_blocks + w.kb0;
-            const float* ws1 = p.ws + (long long)b1 * p.k_blocks + w.kb0;
-            const int cut = (((c0 >> 7) + 1) << 7) - c0;     // columns before the second block's
-            const bool any = w.tile.nrows > 0;
-            uint64_t acc[kHalf / 2];
+        uint64_t acc[kCols / 2];
 #pragma unroll
-            for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
-            const int nb = w.nk + w.expand;
-            float sx = 0.f, s0 = 0.f, s1 = 0.f;
-            if (any && w.nk > 0) { sx = __ldg(xs); s0 = __ldg(ws0); s1 = __ldg(ws1); }
-            for (int b = 0; b < nb; ++b, ++blk) {
-                float f0 = sx * s0, f1 = sx * s1;
-                if (b >= w.nk) f0 = f1 = 1.f;
-                if (any && b + 1 < w.nk) {                   // the next block's scales, under this one's wait
-                    sx = __ldg(xs + b + 1);
-                    s0 = __ldg(ws0 + b + 1);
-                    s1 = __ldg(ws1 + b + 1);
-                }
-                const int buf = blk & 1;
-                if (!wait_all(smem_addr(&tfull[buf]), (blk >> 1) & 1, abort_flag, p.status, limit)) {
+        for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
+        for (int u = first; u < n_units && ok; u += step) {
+            int row0 = 0, nrows = 0, n0 = 0, nb = 1;
+            for (int b0 = 0; b0 < nb; b0 += 4, ++quad) {
+                ScaleSlot& slot = slots[quad & 1];
+                if (!wait_all(smem_addr(&sfull[quad & 1]), (quad >> 1) & 1, abort_flag, p.status, limit)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t t = tmem_base + (uint32_t)(buf * NT + half * cols) + lane_off;
-                const uint64_t g0 = pair(__float_as_uint(f0), __float_as_uint(f0)), g1 = pair(__float_as_uint(f1), __float_as_uint(f1));
-                if (CG > 1) {                                // the next columns' load runs under this one's sums
-                    uint32_t v[2][16];
-                    tmem_ld16(t, v[0]);
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        tmem_wait16(v[c & 1]);
-                        if (c + 1 < kChunks) tmem_ld16(t + 16 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            acc[8 * c + i] = fma2(pair(v[c & 1][2 * i], v[c & 1][2 * i + 1]), g0, acc[8 * c + i]);
+                row0 = slot.row0;
+                nrows = slot.nrows;
+                n0 = slot.n0;
+                nb = slot.nb;
+                const int m = min(4, nb - b0);
+                uint32_t at = my_scale + (quad & 1) * (uint32_t)sizeof(ScaleSlot);
+#pragma unroll 1
+                for (int k = 0; k < m; ++k, at += sizeof(slot.f[0])) {
+                    float f;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at));
+                    if (!wait_all(tfull0 + 8 * buf, phase, abort_flag, p.status, limit)) {
+                        ok = false;
+                        break;
                     }
-                } else {
+                    tc_fence_after();
+                    const uint32_t t = t0 + buf * NT;
+                    const uint64_t f2 = pair(__float_as_uint(f), __float_as_uint(f));
+                    auto release = [&] {                     // this warp has read the buffer
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (CG > 1) arrive_relaxed(tempty0 + 8 * buf);
+                            else mbar_arrive(tempty0 + 8 * buf);
+                        }
+                    };
+                    if (q * 32 >= nrows) {                   // no row of the unit's lies here
+                        release();
+                    } else {                                 // the next columns' load runs under these ones' sums
+                        uint32_t v[2][16];
+                        tmem_ld16(t, v[0]);
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (16 * c < cols) {
-                            uint32_t v[16];
-                            tmem_ld16(t + 16 * c, v);
-                            tmem_wait16(v);
-                            const uint64_t g = 16 * c < cut ? g0 : g1;
+                        for (int c = 0; c < kCols / 16; ++c) {
+                            tmem_wait16(v[c & 1]);
+                            if (c + 1 < kCols / 16) tmem_ld16(t + 16 * (c + 1), v[(c + 1) & 1]);
+                            else release();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) acc[8 * c + i] = fma2(pair(v[2 * i], v[2 * i + 1]), g, acc[8 * c + i]);
+                            for (int i = 0; i < 8; ++i)
+                                acc[8 * c + i] = fma2(pair(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f2, acc[8 * c + i]);
                         }
                     }
+                    if (++buf == kBufs) { buf = 0; phase ^= 1; }
                 }
-                tc_fence_before();
+                if (!ok) break;
                 __syncwarp();
-                if (lane == 0) {
-                    if (CG > 1) mbar_arrive_cluster(map_to_rank(smem_addr(&tempty[buf]), 0));
-                    else mbar_arrive(smem_addr(&tempty[buf]));
-                }
+                if (lane == 0) mbar_arrive(smem_addr(&sempty[quad & 1]));
             }
             if (!ok) break;
             if (CG > 1 || p.parts == 1) {
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.y) + (long long)row * p.d_out + c0;
-                if (row_ok) {
+                // The thread's row goes through the warp's part of shared memory, kYCols columns of 32 rows at a time, its 16-byte
+                // pieces swizzled by row as a tensor map's. A tile whose last row is its 128th or the batch's last leaves it
+                // as TMA copies (clipped at the batch's end); another one's rows are followed by the next tile's, and kYCols / 8
+                // lanes write a row together. (Rows stored by their threads, 16 bytes here and there, took 9,400 cycles a
+                // 256 x 256 unit, lanes together 2,600.)
+                constexpr int kPieces = kYCols / 8, kShift = kPieces == 4 ? 1 : 0;
+                const bool copy = (nrows == kTileM || row0 + nrows == p.rows) && q * 32 < nrows;
 #pragma unroll
-                    for (int c = 0; c < kHalf / 8; ++c) {
-                        if (8 * c < cols && c0 + 8 * c < p.d_out) {
-                            uint4 o;
-                            o.x = pack_bf16x2(lo2(acc[4 * c]), hi2(acc[4 * c]));
-                            o.y = pack_bf16x2(lo2(acc[4 * c + 1]), hi2(acc[4 * c + 1]));
-                            o.z = pack_bf16x2(lo2(acc[4 * c + 2]), hi2(acc[4 * c + 2]));
-                            o.w = pack_bf16x2(lo2(acc[4 * c + 3]), hi2(acc[4 * c + 3]));
-                            *reinterpret_cast<uint4*>(out + 8 * c) = o;
+                for (int h = 0; h < kCols / kYCols; ++h) {
+                    if (lane == 0) stores_read();            // (the group before has left the buffer)
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c) {
+                        {
+                            uint64_t* a = acc + kYCols / 2 * h + 4 * c;
+                            *reinterpret_cast<uint4*>(mine + lane * kYCols * 2 + ((c ^ ((lane >> kShift) & (kPieces - 1))) << 4)) =
+                                make_uint4(pack_bf16x2(lo2(a[0]), hi2(a[0])), pack_bf16x2(lo2(a[1]), hi2(a[1])),
+                                           pack_bf16x2(lo2(a[2]), hi2(a[2])), pack_bf16x2(lo2(a[3]), hi2(a[3])));
+                            a[0] = a[1] = a[2] = a[3] = 0;
                         }
+                    }
+                    const int first_col = n0 + cg * kCols + kYCols * h;
+                    if (copy) {
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0 && first_col < p.d_out) store_rows(&p.tm_y, smem_addr(mine), first_col, row0 + q * 32);
+                        continue;
+                    }
+                    __syncwarp();
+                    const int c = lane & (kPieces - 1), col = first_col + 8 * c;
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.y) + (long long)(row0 + q * 32) * p.d_out + col;
+                    const int n = col < p.d_out ? nrows - q * 32 : 0;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int r = 32 / kPieces * i + lane / kPieces;
+                        if (r < n)
+                            *reinterpret_cast<uint4*>(out + (long long)r * p.d_out) =
+                                *reinterpret_cast<const uint4*>(mine + r * kYCols * 2 + ((c ^ ((r >> kShift) & (kPieces - 1))) << 4));
                     }
                 }
             } else {
@@ -382,30 +517,37 @@ __global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __g
                 // columns of the 128 rows side by side
                 float4* sums = reinterpret_cast<float4*>(base);
 #pragma unroll
-                for (int c = 0; c < kHalf / 4; ++c)
-                    if (4 * c < cols)
-                        sums[(half * (cols >> 2) + c) * 128 + r_local] =
+                for (int c = 0; c < kCols / 4; ++c)
+                    if (q * 32 < nrows)
+                        sums[(cg * (kCols >> 2) + c) * 128 + r_local] =
                             make_float4(lo2(acc[2 * c]), hi2(acc[2 * c]), lo2(acc[2 * c + 1]), hi2(acc[2 * c + 1]));
             }
         }
+        if (lane == 0) stores_read();                        // before the CTA's shared memory goes
         if (CG == 1 && p.parts > 1) {
+            __syncwarp();
             cluster_sync();
             if (ok) {
                 // each CTA adds its share of the columns over the parts, in their order
-                const Work w = decode<CG>(p, tiles, first, rank, part);
-                const int per = p.tile_n / p.parts, vecs = per >> 3, t = (int)threadIdx.x - 128;
-                for (int i = t; i < w.tile.nrows * vecs; i += 256) {
-                    const int r = i / vecs, c = part * per + 8 * (i - r * vecs);
+                const Work w = decode<CG, NT>(p, tiles, first, rank, part);
+                const int v0 = part * (NT / 8) / p.parts, vecs = (part + 1) * (NT / 8) / p.parts - v0;
+                for (int i = (int)threadIdx.x - 128; i < w.tile.nrows * vecs; i += 32 * EW) {
+                    const int r = i / vecs, c = 8 * (v0 + i - r * vecs);
                     if (w.n0 + c >= p.d_out) continue;
+                    const uint32_t at = smem_addr(base) + (uint32_t)(((c >> 2) * 128 + r) * 16);
                     float s[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) s[k] = 0.f;
-                    const uint32_t at = smem_addr(base) + (uint32_t)(((c >> 2) * 128 + r) * 16);
-                    for (int j = 0; j < p.parts; ++j) {
-                        const uint32_t a = map_to_rank(at, (uint32_t)j);
-                        const float4 x = ld_cluster(a), y = ld_cluster(a + 128 * 16);
-                        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
-                        s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+                    for (int j0 = 0; j0 < p.parts; j0 += 2) {   // two parts' loads in flight
+                        const int j1 = min(j0 + 1, p.parts - 1);
+                        const uint32_t a0 = map_to_rank(at, (uint32_t)j0), a1 = map_to_rank(at, (uint32_t)j1);
+                        const float4 x0 = ld_cluster(a0), y0 = ld_cluster(a0 + 128 * 16), x1 = ld_cluster(a1), y1 = ld_cluster(a1 + 128 * 16);
+                        s[0] += x0.x; s[1] += x0.y; s[2] += x0.z; s[3] += x0.w;
+                        s[4] += y0.x; s[5] += y0.y; s[6] += y0.z; s[7] += y0.w;
+                        if (j1 > j0) {
+                            s[0] += x1.x; s[1] += x1.y; s[2] += x1.z; s[3] += x1.w;
+                            s[4] += y1.x; s[5] += y1.y; s[6] += y1.z; s[7] += y1.w;
+                        }
                     }
                     uint4 o;
                     o.x = pack_bf16x2(s[0], s[1]);
@@ -425,7 +567,7 @@ __global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __g
     else __syncthreads();
     if (warp == 3) {
         tc_fence_after();
-        tmem_dealloc<CG>(tmem_base, 2 * NT);
+        tmem_dealloc<CG>(tmem_base, 512);
     }
 }
 
@@ -433,45 +575,77 @@ __global__ void __launch_bounds__(kFp8Threads, BLOCKS) lora_fp8_kernel(const __g
 }  // namespace dev
 
 namespace {
-constexpr auto kNarrow = dev::lora_fp8_kernel<1, 128, 2, 32, 104>;
-constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 1, 40, 232>;
+// 384 threads of 168 registers, dealt out anew: 72 x 128 + 216 x 256 = 168 x 384
+constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 72, 216>;
+constexpr auto kSingle = dev::lora_fp8_kernel<1, 256, 72, 216>;
+constexpr auto kNarrow = dev::lora_fp8_kernel<1, 128, 72, 216>;
+inline auto kernel_of(int wide, int tile_n) { return wide ? kWide : tile_n == 256 ? kSingle : kNarrow; }
 }  // namespace
 
-size_t fp8_smem_bytes(int tile_rows, int a_rows, int stages) {
-    return 1024 + (size_t)stages * (a_rows + tile_rows) * kFp8StageRow + 8 * (2 * (size_t)stages + 5) + 16;
+size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages) {
+    return 1024 + (size_t)stages * (a_rows + tile_n / (wide ? 2 : 1)) * kFp8StageRow + 8 * 64 * (wide ? 64 : 32) +
+           2 * sizeof(dev::ScaleSlot) + 8 * (2 * (size_t)stages + 2 * 512 / tile_n + 5) + 16;
 }
 
 cudaError_t fp8_prepare_device() {
-    const cudaError_t e = cudaFuncSetAttribute(kNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(kWide, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    for (const auto k : {kWide, kSingle, kNarrow}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+static void config(const Fp8Params& p, int grid, cudaStream_t stream, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr /* [2] */) {
+    *cfg = cudaLaunchConfig_t{};
+    cfg->gridDim = dim3(grid);
+    cfg->blockDim = dim3(kFp8Threads);
+    cfg->dynamicSmemBytes = fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages);
+    cfg->stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)(p.wide ? 2 : p.parts), 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+}
+
+// Clusters of `parts` CTAs of the single-CTA forms that the GPU holds at once.
+int fp8_max_clusters(int tile_n, int parts) {
+    Fp8Params p = {};
+    p.tile_n = tile_n;
+    p.parts = parts;
+    p.a_rows = kTileM;
+    p.stages = 3;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    config(p, parts, nullptr, &cfg, attr);
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel_of(0, tile_n), &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
 }
 
 cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream) {
-    const int cg = p.wide ? 2 : 1, tile_rows = p.tile_n / cg;
-    const size_t smem = fp8_smem_bytes(tile_rows, p.a_rows, p.stages);
-    if (p.wide ? (p.tile_n != 256 || p.parts != 1 || p.a_rows != kTileM)
-               : (p.tile_n < 32 || p.tile_n > 128 || p.tile_n % 32 || p.parts < 1 || p.parts > kFp8MaxParts || p.tile_n % (8 * p.parts)))
+    const int tile_rows = p.tile_n / (p.wide ? 2 : 1);
+    if ((p.tile_n != 256 && (p.wide || p.tile_n != 128)) || p.parts < 1 || p.parts > kFp8MaxParts || p.parts > p.k_blocks ||
+        (p.wide && (p.parts != 1 || p.a_rows != kTileM)) || p.a_rows < 16 || p.a_rows > kTileM || p.a_rows % 16)
         return cudaErrorInvalidValue;
-    // an A stage's 128 rows lie inside the rings; the parts' sums (parts > 1) take the rings' place
+    // stages: a lap is at least as long as the TMEM buffers are many; an A stage's 128 rows lie inside the rings; the
+    // parts' sums take the rings' place
     const size_t rings = (size_t)p.stages * (p.a_rows + tile_rows) * kFp8StageRow;
-    if (p.stages < 2 || smem > (size_t)kSmemLimit || p.a_rows < 16 || p.a_rows > kTileM || p.a_rows % 16 ||
-        (size_t)p.stages * tile_rows * kFp8StageRow < (size_t)(kTileM - p.a_rows) * kFp8StageRow ||
-        (p.parts > 1 && rings < (size_t)p.tile_n * kTileM * 4) || grid < 1 || grid % (cg * p.parts) ||
-        (!p.wide && grid != p.n_groups * p.n_ntiles * p.parts))
+    if (p.stages < 512 / p.tile_n || fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages) > (size_t)kSmemLimit ||
+        (size_t)p.stages * tile_rows < (size_t)(kTileM - p.a_rows) || (p.parts > 1 && rings < (size_t)p.tile_n * kTileM * 4))
         return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
+    // units of K parts: one a cluster (the rings hold its sums at its end)
+    const int span = p.wide ? 2 : p.parts;
+    if (grid < 1 || grid % span || (p.parts > 1 && grid != p.n_groups * p.n_ntiles * p.parts)) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kFp8Threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)(cg * p.parts), 1, 1};
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, p.wide ? kWide : kNarrow, p);
+    config(p, grid, stream, &cfg, attr);
+    return cudaLaunchKernelEx(&cfg, kernel_of(p.wide, p.tile_n), p);
 }
 
 }  // namespace lora

@@ -8,9 +8,8 @@
 namespace lora {
 
 constexpr int kFp8Group = 128;        // input features per scale; a base weight's block is 128 x 128
-constexpr int kFp8Threads = 384;      // warp 0 TMA, 1 and 2 MMA, 3 owns TMEM, 4..11 epilogue
+constexpr int kFp8Threads = 384;      // warp 0 TMA, 1 and 2 MMA, 3 scales (and owns TMEM), 4..11 epilogue
 constexpr int kFp8MaxParts = 8;       // most parts of K: one CTA of a cluster each
-constexpr int kFp8SmemTwo = 115200;   // the most dynamic shared memory that lets two CTAs share an SM
 constexpr int kFp8StageRow = 128;     // bytes of a stage's row: one group of e4m3, 64 bf16 of the expand
 
 // One launch. Units are (row group, output tile) blocks of Y; a row group is one planner tile, or two
@@ -22,6 +21,7 @@ struct Fp8Params {
     CUtensorMap tm_x;                 // X [T, d_in] e4m3, box 128 x a_rows, 128-byte swizzle
     CUtensorMap tm_w;                 // W [d_out, d_in] e4m3, box 128 x tile_n / CTAs of the group
     CUtensorMap tm_u;                 // U [u_rows, rank] bf16, box 64 x a_rows
+    CUtensorMap tm_y;                 // Y [T, d_out] bf16, box 64 x 32, 128-byte swizzle; single CTAs 32 x 32, 64-byte
     const CUtensorMap* tm_b;          // device array per compact adapter (when not inline)
     const Tile* tiles;                // device array (when not inline)
     const float* xs;                  // [T, k_blocks]
@@ -30,7 +30,7 @@ struct Fp8Params {
     int* status;
     unsigned long long wait_limit_ns;
     int n_groups;                     // row groups
-    int n_ntiles, tile_n;             // output tiles: a multiple of 32 up to 128; 256 in the wide form
+    int n_ntiles, tile_n;             // output tiles: 128 or 256 columns; 256 in the wide form
     int raster_group;                 // column tiles whose row groups run before the next column tiles
     int k_blocks;                     // ceil(d_in / 128)
     int k_lora;                       // ceil(rank / 64)
@@ -38,12 +38,15 @@ struct Fp8Params {
     int parts;                        // K parts of a unit (1 in the wide form)
     int a_rows;                       // rows of an A box: 128, or fewer (a multiple of 16) for a batch of one tile
     int stages;
+    int rows;                         // T
+    int vec_scales;                   // both scales' rows are 16-byte aligned
     int wide;                         // SM pairs, 256 x 256 blocks, persistent
     int debug_stall;
 };
 
 // kernels_fp8.cu
-size_t fp8_smem_bytes(int tile_rows, int a_rows, int stages);   // tile_rows: rows of a stage's weight tile
+size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages);
+int fp8_max_clusters(int tile_n, int parts);
 cudaError_t fp8_prepare_device();
 cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream);
 
