@@ -2,7 +2,9 @@
  * lora_layer.h -- the operators between the projections of an adapted layer, on one GB300
  * (sm_103a): the residual's addition with the root-mean-square norm ahead of a projection, the
  * append of new keys and values to a paged cache, and attention of the batch's new rows over
- * that cache, with an optional sliding window and first tokens that stay visible (sinks).
+ * that cache, with an optional sliding window and first tokens that stay visible (sinks); the gated
+ * activation, rows and weights in 8 bits, for 8-bit projections (lora_linear_forward_fp8); and, behind
+ * the last projection, log probabilities of given tokens.
  *
  * They serve the same batches as lora_linear_forward: rows grouped into request segments, a few
  * chats with 1 to 8 new rows each beside prompts of thousands. `q_offsets` below is the host
@@ -34,6 +36,8 @@ extern "C" {
 
 #define LORA_LAYER_MAX_WIDTH 32768 /* features of a normalised row */
 #define LORA_LAYER_MAX_SEQS 1024   /* sequences of one call */
+#define LORA_LAYER_MAX_TOP 32      /* alternatives of a row of logits */
+#define LORA_LAYER_MAX_VOCAB (1 << 24) /* entries of a row of logits */
 #define LORA_LAYER_MAX_CONTEXT (1 << 27) /* pages_per_seq x page_size: tokens a sequence's table can hold */
 
 /*
@@ -62,6 +66,57 @@ int lora_linear_add_rms_norm(const void* x, long long x_stride, const void* resi
                              const void* weight, float weight_offset, float eps, int rows, int width,
                              void* h_out, long long h_stride, void* y, long long y_stride,
                              void* q8, long long q8_stride, float* scales, int group, void* stream);
+
+/*
+ * lora_linear_silu_mul -- the gated activation between the gate_up and down projections, for every row t:
+ *     y = g / (1 + e^(-g)) * u,   g = x[t, 0 : width], u = x[t, width : 2 width]
+ *   x, x_stride    device bf16 [rows, 2 width]: row stride >= 2 width.
+ *   y, y_stride    device bf16 [rows, width], or NULL.
+ *   q8, q8_stride, scales, group   device e4m3 [rows, width], or NULL: y in 8 bits, as lora_linear_add_rms_norm's.
+ *                  At least one of y and q8 is given; both are for a projection whose adapters read bf16.
+ *   rows >= 0; width a multiple of 8 in [8, LORA_LAYER_MAX_WIDTH]. No output may overlap another buffer.
+ * A NaN or an infinity gives a NaN or a scale of infinity in its row's group (group 0: its row) alone.
+ */
+int lora_linear_silu_mul(const void* x, long long x_stride, int rows, int width, void* y, long long y_stride,
+                         void* q8, long long q8_stride, float* scales, int group, void* stream);
+
+/*
+ * lora_linear_fp8_rows -- rows of bf16 in 8 bits: q8, scales and group as lora_linear_add_rms_norm writes them for y = x.
+ *   x, x_stride    device bf16 [rows, width]; limits as lora_linear_silu_mul.
+ */
+int lora_linear_fp8_rows(const void* x, long long x_stride, int rows, int width, void* q8, long long q8_stride,
+                         float* scales, int group, void* stream);
+
+/*
+ * lora_linear_fp8_blocks -- a weight in 8 bits, for lora_linear_forward_fp8; run once when it is loaded.
+ *   w, w_stride    device bf16 [rows, cols]: rows >= 0, cols a multiple of 8, both at most LORA_MAX_FEATURES.
+ *   q8, q8_stride  device e4m3 [rows, cols]: q = e4m3(w r), r = 1 / s rounded to fp32 (nearest even, saturating).
+ *   scales         device fp32 [ceil(rows / 128), ceil(cols / 128)], contiguous: s = max(max|w| / 448, 2^-100) over
+ *                  every block of 128 x 128 (the last ones may be smaller).
+ * No output may overlap another buffer. A NaN or an infinity leaves nothing of its block.
+ */
+int lora_linear_fp8_blocks(const void* w, long long w_stride, int rows, int cols, void* q8, long long q8_stride,
+                           float* scales, void* stream);
+
+/*
+ * lora_linear_token_logprobs -- for every row of logits x, with z = x / temperature:
+ *   logprobs[t]     z_i - log sum_j e^(z_j) of the given token i = tokens[t]; NaN where i is not in [0, vocab).
+ *   ranks[t]        entries before i in the order of falling x, ties by rising index (0: the most likely); -1 there.
+ *   entropy[t]      -sum_j p_j log p_j, p = softmax(z), in nats.
+ *   top_logprobs, top_tokens   [rows, top]: the first `top` entries of that order.
+ *   logits, stride  device bf16 (is_fp32 0) or fp32 (1) [rows, vocab], row stride >= vocab elements; no alignment
+ *                   beyond the element's. Entries of -inf (tokens ruled out) have probability 0.
+ *   tokens          device int32 (tokens64 0) or int64 (1) [rows]; NULL where logprobs and ranks are.
+ *   temperature     > 0, finite, as its reciprocal.
+ *   top             0 to LORA_LAYER_MAX_TOP, at most vocab.
+ * Any of logprobs, ranks and entropy may be NULL, but not all outputs. They are contiguous and overlap nothing.
+ * z is rounded to fp32 by its factor 1 / temperature and less its maximum; sums are fp32. A row of -inf alone has log
+ * probabilities of -inf and entropy 0; one with a NaN or +inf has NaN for both, and its ranks and alternatives go by
+ * the order, in which a NaN is behind -inf. The same call gives the same bits.
+ */
+int lora_linear_token_logprobs(const void* logits, long long stride, int is_fp32, int rows, int vocab,
+                               const void* tokens, int tokens64, float temperature, int top, float* logprobs,
+                               int32_t* ranks, float* entropy, float* top_logprobs, int32_t* top_tokens, void* stream);
 
 /*
  * The paged cache and the batch, as the calls below take them.

@@ -9,7 +9,10 @@ not load the library; ``LoraLinear`` and ``plan`` do, and raise if it is missing
 
 Between the projections of an adapted layer: ``add_rms_norm`` and ``add_rms_norm_fp8`` (the
 residual's addition with the norm), ``kv_append`` (new keys and values into a paged cache, with
-the rotary turn) and ``PagedAttention`` (the batch's new rows over that cache).
+the rotary turn), ``PagedAttention`` (the batch's new rows over that cache) and ``silu_mul`` (the gated
+activation). ``LoraLinear.forward_fp8`` takes 8-bit activations, which ``add_rms_norm_fp8``,
+``silu_mul_fp8`` and ``fp8_rows`` write, and a weight from ``fp8_blocks``; behind the last projection
+``token_logprobs`` scores given tokens.
 """
 from .synth import WORKLOADS, Workload, make_inputs  # noqa: F401
 
@@ -18,7 +21,8 @@ def __getattr__(name):
     if name in ("LoraLinear", "plan", "LoraError", "validate", "w4_repack", "launch_shape", "host_chunks", "k_split"):
         from . import lora_linear as _ll
         return getattr(_ll, name)
-    if name in ("add_rms_norm", "add_rms_norm_fp8", "kv_append", "PagedAttention"):
+    if name in ("add_rms_norm", "add_rms_norm_fp8", "kv_append", "PagedAttention", "silu_mul", "silu_mul_fp8", "fp8_rows",
+                "fp8_blocks", "token_logprobs", "TokenLogprobs"):
         from . import layer as _layer
         return getattr(_layer, name)
     raise AttributeError(name)

@@ -64,6 +64,11 @@ SIGNATURES = {
                                               C.POINTER(P), C.POINTER(P), C.POINTER(C.c_float), C.c_int, P, P]),
     "lora_linear_add_rms_norm": (C.c_int, [P, LL, P, LL, P, C.c_float, C.c_float, C.c_int, C.c_int, P, LL, P, LL,
                                            P, LL, P, C.c_int, P]),
+    "lora_linear_silu_mul": (C.c_int, [P, LL, C.c_int, C.c_int, P, LL, P, LL, P, C.c_int, P]),
+    "lora_linear_fp8_rows": (C.c_int, [P, LL, C.c_int, C.c_int, P, LL, P, C.c_int, P]),
+    "lora_linear_fp8_blocks": (C.c_int, [P, LL, C.c_int, C.c_int, P, LL, P, P]),
+    "lora_linear_token_logprobs": (C.c_int, [P, LL, C.c_int, C.c_int, C.c_int, P, C.c_int, C.c_float, C.c_int, P, P, P, P,
+                                             P, P]),
     "lora_linear_kv_append": (C.c_int, [CACHE, P, LL, LL, P, LL, LL, C.c_int, P, LL, LL, P, LL, LL, P, P, C.c_int,
                                         C.c_int, P]),
     "lora_linear_attn_create": (C.c_int, [C.POINTER(P), C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,

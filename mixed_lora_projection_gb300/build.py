@@ -26,7 +26,7 @@ BIND = os.path.join(PKG, "_layer_bind.so")
 BIND_FOR = os.path.join(BUILD, "layer_bind.for")       # the PyTorch and the Python that the binding was built for
 BIND_SOURCE = "layer_bind.cpp"
 SOURCES = ["kernels.cu", "kernels_w4.cu", "kernels_fp8.cu", "api.cpp", "planner.cpp", "noalloc.cu",
-           "layer_ops.cu", "attn_decode.cu", "attn_prompt.cu", "layer_api.cpp"]
+           "layer_ops.cu", "act_fp8.cu", "logprobs.cu", "attn_decode.cu", "attn_prompt.cu", "layer_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

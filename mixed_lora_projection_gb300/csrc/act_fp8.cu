@@ -1,0 +1,225 @@
+// What stands before an 8-bit projection: the gated activation between gate_up and down (bf16 or 8-bit output), rows
+// and weights brought to 8 bits. Each reads its input once and is bound by memory (on a few rows by one pass's latency).
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "dev_common.cuh"
+#include "layer_internal.h"
+
+namespace lora {
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(dev::pack_bf16x2(f[0], f[1]), dev::pack_bf16x2(f[2], f[3]), dev::pack_bf16x2(f[4], f[5]),
+                      dev::pack_bf16x2(f[6], f[7]));
+}
+// max that keeps a NaN of either side, so that a group with one gets a NaN scale
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float amax8(const float* f) {
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(f[k]));
+    return m;
+}
+// scale of a maximum, floored so that its reciprocal is finite and zeros are exact (as the norm's in 8 bits)
+__device__ __forceinline__ float scale_of(float amax) {
+    const float s = amax * (1.0f / 448.f);
+    return s < 7.888609052210118e-31f ? 7.888609052210118e-31f : s;   // 2^-100; a NaN stays
+}
+__device__ __forceinline__ uint2 to_e4m3(const float* f, float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | hi << 16;
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// g / (1 + e^-g) * u. Past e^-g's range the quotient is -0, its limit.
+__device__ __forceinline__ void silu_mul8(const uint4& gate, const uint4& up, float* y) {
+    float g[8], u[8];
+    unpack8(gate, g);
+    unpack8(up, u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = __fdividef(g[k], 1.f + __expf(-g[k])) * u[k];
+}
+
+// One row's vector c (8 features) of the operator's values in fp32.
+template <bool GATE>
+__device__ __forceinline__ void values8(const uint4& a, const uint4& b, float* y) {
+    if (GATE) silu_mul8(a, b, y);
+    else unpack8(a, y);
+}
+
+// Scales by groups, or bf16 alone: a warp takes 32 vectors of a row (256 features, whole groups) at a time, four such
+// pieces in flight.
+template <bool GATE>
+__global__ void __launch_bounds__(256) act_groups_kernel(const __grid_constant__ ActParams p) {
+    dev::griddep_wait();
+    dev::griddep_launch_dependents();
+    const int nvec = p.width >> 3, per_row = (nvec + 31) >> 5, lane = threadIdx.x & 31;
+    const long long pieces = (long long)p.rows * per_row, warps = (long long)gridDim.x * 8;
+    const int lanes = p.group >> 3, shift = p.group ? 31 - __clz(lanes) : 0, ng = p.group ? (nvec + lanes - 1) >> shift : 0;
+    constexpr int N = 4;
+    for (long long first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); first < pieces; first += N * warps) {
+        uint4 a[N], b[N];
+        long long row[N];
+        int c[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const long long piece = first + i * warps;
+            row[i] = piece / per_row;
+            c[i] = (int)(piece - row[i] * per_row) * 32 + lane;
+            if (piece >= pieces) c[i] = nvec;
+            a[i] = b[i] = make_uint4(0, 0, 0, 0);
+            if (c[i] < nvec) {
+                const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row[i] * p.x_stride;
+                a[i] = __ldcs(reinterpret_cast<const uint4*>(x) + c[i]);
+                if (GATE) b[i] = __ldcs(reinterpret_cast<const uint4*>(x + p.width) + c[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float y[8];
+            values8<GATE>(a[i], b[i], y);
+            if (p.y && c[i] < nvec) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + row[i] * p.y_stride)[c[i]] = pack8(y);
+            if (!p.q8) continue;
+            float m = amax8(y);
+            for (int o = lanes >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (c[i] < nvec) {
+                const float s = scale_of(m);
+                reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q8) + row[i] * p.q8_stride)[c[i]] = to_e4m3(y, __frcp_rn(s));
+                if ((c[i] & (lanes - 1)) == 0) p.scales[row[i] * ng + (c[i] >> shift)] = s;
+            }
+        }
+    }
+}
+
+// One scale a row: a block a row, which stays in registers between its maximum and its output.
+template <bool GATE, int V>
+__global__ void __launch_bounds__(1024) act_rows_kernel(const __grid_constant__ ActParams p) {
+    __shared__ float buf[32];
+    dev::griddep_wait();
+    dev::griddep_launch_dependents();
+    const long long row = blockIdx.x;
+    const int nvec = p.width >> 3, tid = threadIdx.x, nt = blockDim.x;
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride;
+    uint4 a[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        a[i] = b[i] = make_uint4(0, 0, 0, 0);
+        if (c < nvec) {
+            a[i] = reinterpret_cast<const uint4*>(x)[c];
+            if (GATE) b[i] = reinterpret_cast<const uint4*>(x + p.width)[c];
+        }
+    }
+    float y[V][8], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        values8<GATE>(a[i], b[i], y[i]);
+        m = max_nan(m, amax8(y[i]));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) buf[tid >> 5] = m;
+    __syncthreads();
+    m = (tid & 31) < (nt >> 5) ? buf[tid & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = scale_of(m), inv = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nt;
+        if (c >= nvec) continue;
+        if (p.y) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + row * p.y_stride)[c] = pack8(y[i]);
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q8) + row * p.q8_stride)[c] = to_e4m3(y[i], inv);
+    }
+    if (tid == 0) p.scales[row] = s;
+}
+
+// A weight's block of 128 x 128: 256 threads hold it (8 vectors each) between its maximum and its output.
+__global__ void __launch_bounds__(256) fp8_blocks_kernel(const __grid_constant__ BlocksParams p) {
+    __shared__ float buf[8];
+    dev::griddep_wait();
+    dev::griddep_launch_dependents();
+    const int nc = (p.cols + 127) >> 7, br = (int)(blockIdx.x / nc), bc = (int)(blockIdx.x % nc);
+    const int col = bc * 128 + (threadIdx.x & 15) * 8, r0 = br * 128 + (threadIdx.x >> 4);
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r < p.rows && col < p.cols)
+            v[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w) + (long long)r * p.w_stride + col));
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float f[8];
+        unpack8(v[i], f);
+        m = max_nan(m, amax8(f));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = buf[threadIdx.x & 7];
+#pragma unroll
+    for (int o = 4; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = scale_of(m), inv = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r >= p.rows || col >= p.cols) continue;
+        float f[8];
+        unpack8(v[i], f);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q8) + (long long)r * p.q8_stride + col) = to_e4m3(f, inv);
+    }
+    if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
+}
+
+template <bool GATE>
+cudaError_t launch(const ActParams& p, cudaStream_t stream) {
+    const int nvec = p.width >> 3;
+    if (p.q8 && p.group == 0) {
+        const int v = nvec > 2048 ? 4 : nvec > 1024 ? 2 : 1, nt = ((nvec + v - 1) / v + 31) / 32 * 32;
+        if (v == 1) return launch_chained(act_rows_kernel<GATE, 1>, p.rows, nt, 0, stream, p);
+        if (v == 2) return launch_chained(act_rows_kernel<GATE, 2>, p.rows, nt, 0, stream, p);
+        return launch_chained(act_rows_kernel<GATE, 4>, p.rows, nt, 0, stream, p);
+    }
+    // a warp a piece while there are few, at most eight blocks an SM
+    const long long pieces = (long long)p.rows * ((nvec + 31) / 32);
+    return launch_chained(act_groups_kernel<GATE>, (unsigned)std::min<long long>((pieces + 7) / 8, 152 * 8), 256, 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_act(const ActParams& p, bool gate, cudaStream_t stream) {
+    return gate ? launch<true>(p, stream) : launch<false>(p, stream);
+}
+
+cudaError_t launch_fp8_blocks(const BlocksParams& p, cudaStream_t stream) {
+    const long long blocks = (long long)((p.rows + 127) / 128) * ((p.cols + 127) / 128);
+    return launch_chained(fp8_blocks_kernel, (unsigned)blocks, 256, 0, stream, p);
+}
+
+}  // namespace lora

@@ -86,6 +86,7 @@ struct lora_linear {
     int yt_mode = 0;            // LORA_OPT_TOKEN_COLUMNS: 0 = auto, 1 = never, 2 = whenever a batch allows
     int wide_mode = 0;          // LORA_OPT_WIDE_TILES: 0 = auto, 1 = never
     // 4-bit base K parts: chosen once per handle like k_split
+    int fp8_clusters[2][kFp8MaxParts + 1] = {};   // clusters of 2.. CTAs of the 8-bit kernel (128, 256 columns) that fit at once
     int w4_k_split = 1;         // 1..4: every 4-bit block runs as that many units over parts of K
     int w4_k_split_opt = 0;     // LORA_OPT_W4_K_SPLIT: 0 = the handle's own choice
     float* w4_partials = nullptr;                 // [part][max_tokens][d_out] fp32
@@ -864,6 +865,9 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
         return LORA_ECUDA;
     }
 
+    for (int i = 0; i < 2; ++i)
+        for (int n = 2; n <= kFp8MaxParts; ++n) h->fp8_clusters[i][n] = fp8_max_clusters(128 * (i + 1), n);
+
     h->u_rows = ceil_div(max_tokens, kTileM) * kTileM + kTileM;
     h->max_fused = ceil_div(max_tokens, kTileM) + max_segments + 1;
     h->k_split = choose_k_split(h);
@@ -1522,19 +1526,44 @@ namespace {
 
 // Launch shape of the 8-bit kernel for a plan.
 struct Fp8Shape {
-    int wide = 0, tile_n = 128, parts = 1, a_rows = kTileM, stages = 0, n_ntiles = 0, raster_group = 1, groups = 0;
+    int wide = 0, tile_n = 128, parts = 1, a_rows = kTileM, stages = 0, n_ntiles = 0, raster_group = 1;
 };
 
+// Three forms, each with one CTA (or pair) an SM: blocks of 128 x 128 and 128 x 256 on single CTAs, whose units a cluster
+// of up to eight CTAs may split by K where they would leave SMs idle, and of 256 x 256 on SM pairs. The one that the
+// units' waves times a block's measured time, per 128-wide K step, would finish first: 0.36 us at 128 columns, 0.61 at
+// 256, 0.54 on pairs, 2 us beside the blocks and 2 more where parts are joined. That picks the fastest or one within 8 %
+// of it on 28 of 30 batches timed (1 to 2,048 rows of the four projections): one row of 6,144 -> 5,120 in three parts of
+// 128 columns 10.7 us against 12.4 (256 columns, five parts), 48 rows of 5,120 -> 34,816 in 128 columns 32.6 against 33.8,
+// 348 rows of 5,120 -> 12,288 in 256 columns 28.4 against 31.0 and, on pairs, 45.1; 2,048 rows there on pairs 124 against 142.
 Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
+    const int nf = (int)plan.fused.size(), k_blocks = ceil_div(h->d_in, kFp8Group), sms = usable_sms(h);
     Fp8Shape s;
-    const int nf = (int)plan.fused.size(), k_blocks = ceil_div(h->d_in, kFp8Group);
-    s.wide = nf >= 4;
-    s.tile_n = s.wide ? 256 : 128;
+    double best = -1;
+    auto weigh = [&](int wide, int tile_n, int parts, long long units, int slots, double block_us) {
+        const double t = (double)ceil_div(units, std::max(slots, 1)) * ceil_div(k_blocks, parts) * block_us + (parts > 1 ? 2.0 : 0.0);
+        if (best >= 0 && t >= best) return;
+        best = t;
+        s.wide = wide;
+        s.tile_n = tile_n;
+        s.parts = parts;
+    };
+    for (int tile_n = 128; tile_n <= 256; tile_n += 128) {
+        const long long units = (long long)nf * ceil_div(h->d_out, tile_n);
+        const double us = tile_n == 128 ? 0.36 : 0.61;
+        weigh(0, tile_n, 1, units, sms, us);
+        for (int parts = 2; parts <= std::min(kFp8MaxParts, k_blocks); ++parts)
+            if (units <= h->fp8_clusters[tile_n / 256][parts] && units * parts <= sms) weigh(0, tile_n, parts, units, (int)units, us);
+    }
+    // (pairs: neighbouring tiles, less where two adapters meet; near enough for the choice)
+    if (nf >= 2 && sms >= 2) weigh(1, 256, 1, (long long)((nf + 1) / 2) * ceil_div(h->d_out, 256), sms / 2, 0.54);
     s.n_ntiles = ceil_div(h->d_out, s.tile_n);
-    if (s.wide) s.raster_group = ceil_div(s.n_ntiles, 2);
-    else if (nf == 1) s.a_rows = std::max(16, ceil_div(plan.fused[0].nrows, 16) * 16);
+    // pairs walk the column tiles in groups of up to 20, all rows of a group first (16,384 rows of 5,120 -> 5,120: groups of
+    // 20 357 us, of 4 369; 4,144 of 5,120 -> 34,816: of 20 625, of 4 636, of all 136 664); single CTAs all rows of a column
+    // tile first, so that its weights are read from memory once
+    if (s.wide) s.raster_group = std::min(s.n_ntiles, 20);
+    if (!s.wide && nf == 1) s.a_rows = std::max(16, ceil_div(plan.fused[0].nrows, 16) * 16);
     while (s.stages < kMaxStages && fp8_smem_bytes(s.wide, s.tile_n, s.a_rows, s.stages + 1) <= (size_t)kSmemLimit) ++s.stages;
-    (void)k_blocks;
     return s;
 }
 
@@ -1756,8 +1785,12 @@ extern "C" int lora_linear_forward_fp8(lora_linear* h, const void* x8, const flo
                                        const int32_t* seg_offsets, const int32_t* seg_adapter_ids, int n_seg,
                                        const void* w8, const float* w_scales, const void* const* A,
                                        const void* const* B, const float* scale, int n_adapters, void* y, void* stream) {
-    return forward_fp8_impl(h, Fp8Operands{x8, w8, x_scales, w_scales}, x, T, seg_offsets, seg_adapter_ids, n_seg, A, B,
-                            scale, n_adapters, y, reinterpret_cast<cudaStream_t>(stream));
+    try {
+        return forward_fp8_impl(h, Fp8Operands{x8, w8, x_scales, w_scales}, x, T, seg_offsets, seg_adapter_ids, n_seg, A, B,
+                                scale, n_adapters, y, reinterpret_cast<cudaStream_t>(stream));
+    } catch (...) {   // host memory for the plan
+        return LORA_ENOMEM;
+    }
 }
 
 extern "C" int lora_linear_validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments, const void* x8,

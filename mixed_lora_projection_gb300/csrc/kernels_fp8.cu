@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                             else mbar_arrive(tempty0 + 8 * buf);
                         }
                     };
-                    if (q * 32 >= nrows) {                   // no row of the unit's lies here
+                    if (CG == 1 && q * 32 >= nrows) {        // no row of the unit's lies here
                         release();
                     } else {                                 // the next columns' load runs under these ones' sums
                         uint32_t v[2][16];

@@ -340,6 +340,103 @@ extern "C" int lora_linear_add_rms_norm(const void* x, long long x_stride, const
     return launch_add_rms_norm(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
 }
 
+namespace {
+
+bool group_ok(int group) { return group == 0 || group == 32 || group == 64 || group == 128 || group == 256; }
+
+// lora_linear_silu_mul and lora_linear_fp8_rows.
+int activation(bool gate, const void* x, long long x_stride, int rows, int width, void* y, long long y_stride, void* q8,
+               long long q8_stride, float* scales, int group, void* stream) {
+    if (rows < 0 || width < 8 || width > LORA_LAYER_MAX_WIDTH || width % 8) return LORA_EINVAL;
+    if (rows == 0) return LORA_OK;
+    if (!x || (!y && !q8) || !aligned16(x) || !aligned16(y) || !aligned16(q8)) return LORA_EINVAL;
+    const int in = gate ? 2 * width : width, per = group ? (width + group - 1) / group : 1;
+    if (!stride_ok(x_stride, in, 8) || (y && !stride_ok(y_stride, width, 8))) return LORA_EINVAL;
+    if (q8 && (!stride_ok(q8_stride, width, 8) || !scales || !aligned4(scales) || !group_ok(group))) return LORA_EINVAL;
+    const Span sx = span(x, rows, x_stride, 1, 0, in, 2);
+    const Span outs[3] = {span(y, rows, y_stride, 1, 0, width, 2), span(q8, rows, q8_stride, 1, 0, width, 1),
+                          q8 ? span(scales, rows, per, 1, 0, per, 4) : Span()};
+    for (int i = 0; i < 3; ++i) {
+        if (meet(outs[i], sx)) return LORA_EINVAL;
+        for (int k = i + 1; k < 3; ++k)
+            if (meet(outs[i], outs[k])) return LORA_EINVAL;
+    }
+    const ActParams p = {x, y, q8, scales, x_stride, y_stride, q8_stride, rows, width, q8 ? group : 0};
+    return launch_act(p, gate, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+}  // namespace
+
+extern "C" int lora_linear_silu_mul(const void* x, long long x_stride, int rows, int width, void* y, long long y_stride,
+                                    void* q8, long long q8_stride, float* scales, int group, void* stream) {
+    return activation(true, x, x_stride, rows, width, y, y_stride, q8, q8_stride, scales, group, stream);
+}
+
+extern "C" int lora_linear_fp8_rows(const void* x, long long x_stride, int rows, int width, void* q8, long long q8_stride,
+                                    float* scales, int group, void* stream) {
+    if (rows > 0 && !q8) return LORA_EINVAL;
+    return activation(false, x, x_stride, rows, width, nullptr, 0, q8, q8_stride, scales, group, stream);
+}
+
+extern "C" int lora_linear_fp8_blocks(const void* w, long long w_stride, int rows, int cols, void* q8, long long q8_stride,
+                                      float* scales, void* stream) {
+    if (rows < 0 || cols < 8 || rows > LORA_MAX_FEATURES || cols > LORA_MAX_FEATURES || cols % 8) return LORA_EINVAL;
+    if (rows == 0) return LORA_OK;
+    if (!w || !q8 || !scales || !aligned16(w) || !aligned16(q8) || !aligned4(scales)) return LORA_EINVAL;
+    if (!stride_ok(w_stride, cols, 8) || !stride_ok(q8_stride, cols, 8)) return LORA_EINVAL;
+    const long long blocks = (long long)((rows + 127) / 128) * ((cols + 127) / 128);
+    const Span sw = span(w, rows, w_stride, 1, 0, cols, 2), sq = span(q8, rows, q8_stride, 1, 0, cols, 1);
+    const Span ss = span(scales, 1, 0, 1, 0, blocks, 4);
+    if (meet(sq, sw) || meet(ss, sw) || meet(ss, sq)) return LORA_EINVAL;
+    const BlocksParams p = {w, q8, scales, w_stride, q8_stride, rows, cols};
+    return launch_fp8_blocks(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
+extern "C" int lora_linear_token_logprobs(const void* logits, long long stride, int is_fp32, int rows, int vocab,
+                                          const void* tokens, int tokens64, float temperature, int top, float* logprobs,
+                                          int32_t* ranks, float* entropy, float* top_logprobs, int32_t* top_tokens,
+                                          void* stream) {
+    static_assert(kMaxTop == LORA_LAYER_MAX_TOP, "the kernel's limit is the header's");
+    if (rows < 0 || rows > LORA_MAX_TOKENS || vocab < 1 || vocab > LORA_LAYER_MAX_VOCAB) return LORA_EINVAL;
+    if (top < 0 || top > LORA_LAYER_MAX_TOP || top > vocab || (is_fp32 != 0 && is_fp32 != 1) || (tokens64 != 0 && tokens64 != 1))
+        return LORA_EINVAL;
+    const float inv = (float)(1.0 / (double)temperature);
+    if (!isfinite(temperature) || temperature <= 0.f || !isfinite(inv) || inv <= 0.f) return LORA_EINVAL;
+    if (rows == 0) return LORA_OK;
+    const int elem = is_fp32 ? 4 : 2;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(logits), t = reinterpret_cast<uintptr_t>(tokens);
+    if (!logits || at % elem || stride < vocab || stride > kMaxStride) return LORA_EINVAL;
+    if (t % (tokens64 ? 8 : 4) || ((logprobs || ranks) && !tokens)) return LORA_EINVAL;
+    if (!aligned4(logprobs) || !aligned4(ranks) || !aligned4(entropy) || !aligned4(top_logprobs) || !aligned4(top_tokens)) return LORA_EINVAL;
+    if (top && (!top_logprobs || !top_tokens)) return LORA_EINVAL;
+    if (!logprobs && !ranks && !entropy && !top) return LORA_EINVAL;
+    const Span ins[2] = {span(logits, rows, stride, 1, 0, vocab, elem), span(tokens, 1, 0, 1, 0, rows, tokens64 ? 8 : 4)};
+    const Span outs[5] = {span(logprobs, 1, 0, 1, 0, rows, 4), span(ranks, 1, 0, 1, 0, rows, 4), span(entropy, 1, 0, 1, 0, rows, 4),
+                          top ? span(top_logprobs, 1, 0, 1, 0, (long long)rows * top, 4) : Span(),
+                          top ? span(top_tokens, 1, 0, 1, 0, (long long)rows * top, 4) : Span()};
+    for (int i = 0; i < 5; ++i) {
+        if (meet(outs[i], ins[0]) || meet(outs[i], ins[1])) return LORA_EINVAL;
+        for (int k = i + 1; k < 5; ++k)
+            if (meet(outs[i], outs[k])) return LORA_EINVAL;
+    }
+    ScoreParams p;
+    p.logits = logits;
+    p.tokens = tokens;
+    p.logprobs = logprobs;
+    p.ranks = ranks;
+    p.entropy = entropy;
+    p.top_logprobs = top_logprobs;
+    p.top_tokens = top_tokens;
+    p.stride = stride;
+    p.inv_temperature = inv;
+    p.rows = rows;
+    p.vocab = vocab;
+    p.top = top;
+    p.is_fp32 = is_fp32;
+    p.tokens64 = tokens64;
+    return launch_token_logprobs(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LORA_OK : LORA_ECUDA;
+}
+
 extern "C" int lora_linear_kv_append(const lora_kv_cache* cache, const void* q, long long q_stride,
                                      long long q_head_stride, void* q_out, long long qo_stride,
                                      long long qo_head_stride, int n_heads, const void* k, long long k_stride,

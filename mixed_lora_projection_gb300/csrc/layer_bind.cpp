@@ -27,6 +27,10 @@ namespace {
 decltype(&lora_linear_add_rms_norm) g_norm;
 decltype(&lora_linear_kv_append) g_append;
 decltype(&lora_linear_attn_forward) g_attend;
+decltype(&lora_linear_silu_mul) g_silu_mul;
+decltype(&lora_linear_fp8_rows) g_fp8_rows;
+decltype(&lora_linear_fp8_blocks) g_fp8_blocks;
+decltype(&lora_linear_token_logprobs) g_logprobs;
 PyObject* g_check;                                     // (code, entry point) -> raises
 
 constexpr auto kBf16 = at::kBFloat16;
@@ -181,23 +185,28 @@ void* address(PyObject* o) {
     return p;
 }
 
-// bind(add_rms_norm, kv_append, attn_forward, check): addresses of the entry points, and what raises their errors
+// bind(add_rms_norm, kv_append, attn_forward, silu_mul, fp8_rows, fp8_blocks, token_logprobs, check): addresses of the
+// entry points, and what raises their errors
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    TORCH_CHECK_TYPE(n == 4, "wrong number of arguments");
+    TORCH_CHECK_TYPE(n == 8, "wrong number of arguments");
     g_norm = reinterpret_cast<decltype(g_norm)>(address(a[0]));
     g_append = reinterpret_cast<decltype(g_append)>(address(a[1]));
     g_attend = reinterpret_cast<decltype(g_attend)>(address(a[2]));
-    Py_XSETREF(g_check, same(a[3]));
+    g_silu_mul = reinterpret_cast<decltype(g_silu_mul)>(address(a[3]));
+    g_fp8_rows = reinterpret_cast<decltype(g_fp8_rows)>(address(a[4]));
+    g_fp8_blocks = reinterpret_cast<decltype(g_fp8_blocks)>(address(a[5]));
+    g_logprobs = reinterpret_cast<decltype(g_logprobs)>(address(a[6]));
+    Py_XSETREF(g_check, same(a[7]));
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
 
-// norm(x, weight, residual, eps, weight_offset, out, h_out, scales, group, stream); group -1: bf16, (y, h);
-// else 8 bits, (q, scales, h)
+// norm(x, weight, residual, eps, weight_offset, out, h_out, scales, group, stream, y_out); group -1: bf16, (y, h);
+// else 8 bits, (q, scales, h), and y where y_out is given
 PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    ready(n, 10);
+    ready(n, 11);
     const at::Tensor& x = cuda_tensor(a[0], "x");
     const at::Device dev = x.device();
     const int group = to_int(a[8], "group");
@@ -232,6 +241,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
             scales = empty({rows, per}, at::kFloat, dev);
         }
         sp = static_cast<float*>(pointer(scales, at::kFloat, dev, "scales"));
+        if (given(a[10])) yr = rows_of(tensor(a[10], "y_out"), rows, width, kBf16, dev, "y_out");
     }
     if (given(a[6])) h = tensor(a[6], "h_out");
     else if (given(a[2]) || (yr.p == xr.p && rows)) h = empty({rows, width}, kBf16, dev);   // (y over x: h is x no more)
@@ -244,11 +254,132 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (given(a[5])) wrote(out);
     if (given(a[6])) wrote(h);
     if (group >= 0 && given(a[7])) wrote(scales);
+    if (group >= 0 && given(a[10])) wrote(tensor(a[10], "y_out"));
     THPObjectPtr o(given(a[5]) ? same(a[5]) : THPVariable_Wrap(out));
     THPObjectPtr hh(given(a[6]) ? same(a[6]) : h.defined() ? THPVariable_Wrap(h) : same(a[0]));
     if (group < 0) return PyTuple_Pack(2, o.get(), hh.get());
     THPObjectPtr s(given(a[7]) ? same(a[7]) : THPVariable_Wrap(scales));
     return PyTuple_Pack(3, o.get(), s.get(), hh.get());
+    END_HANDLE_TH_ERRORS
+}
+
+// activate(x, gate, group, out, scales, y_out, stream): gate: x [rows, 2 width]; group -1: bf16, y; else 8 bits, (q, scales)
+PyObject* activate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 7);
+    const at::Tensor& x = cuda_tensor(a[0], "x");
+    const at::Device dev = x.device();
+    const bool gate = PyObject_IsTrue(a[1]);
+    const int group = to_int(a[2], "group");
+    TORCH_CHECK_VALUE(x.dim() == 2 && (!gate || x.size(1) % 2 == 0), "x must have shape [rows, ", gate ? "2 width" : "width", "]");
+    const int64_t rows = x.size(0), width = gate ? x.size(1) / 2 : x.size(1);
+    TORCH_CHECK_VALUE(rows <= INT_MAX && x.size(1) <= INT_MAX, "x is too large");
+    const Rows xr = rows_of(x, rows, x.size(1), kBf16, dev, "x");
+    Rows yr, qr;
+    at::Tensor out, scales;
+    float* sp = nullptr;
+    const c10::cuda::CUDAGuard guard(dev);
+    const OnStream stream(a[6], dev);
+    out = given(a[3]) ? tensor(a[3], "out") : empty({rows, width}, group < 0 ? kBf16 : kFp8, dev);
+    if (group < 0) {
+        yr = rows_of(out, rows, width, kBf16, dev, "out");
+    } else {
+        TORCH_CHECK_VALUE(group == 0 || group == 32 || group == 64 || group == 128 || group == 256, "group must be 0, 32, 64, 128 or 256");
+        const int64_t per = group ? (width + group - 1) / group : 1;
+        qr = rows_of(out, rows, width, kFp8, dev, "out");
+        scales = given(a[4]) ? tensor(a[4], "scales") : empty({rows, per}, at::kFloat, dev);
+        TORCH_CHECK_VALUE(scales.dim() == 2 && scales.size(0) == rows && scales.size(1) == per && scales.is_contiguous(),
+                          "scales must be contiguous with shape (", rows, ", ", per, ")");
+        sp = static_cast<float*>(pointer(scales, at::kFloat, dev, "scales"));
+        if (given(a[5])) yr = rows_of(tensor(a[5], "y_out"), rows, width, kBf16, dev, "y_out");
+    }
+    check(unlocked([&] {
+              return gate ? g_silu_mul(xr.p, xr.stride, (int)rows, (int)width, yr.p, yr.stride, qr.p, qr.stride, sp, group < 0 ? 0 : group, stream.handle)
+                          : g_fp8_rows(xr.p, xr.stride, (int)rows, (int)width, qr.p, qr.stride, sp, group, stream.handle);
+          }),
+          gate ? "lora_linear_silu_mul" : "lora_linear_fp8_rows");
+    if (given(a[3])) wrote(out);
+    if (given(a[5])) wrote(tensor(a[5], "y_out"));
+    THPObjectPtr o(given(a[3]) ? same(a[3]) : THPVariable_Wrap(out));
+    if (group < 0) return o.release();
+    if (given(a[4])) wrote(scales);
+    THPObjectPtr s(given(a[4]) ? same(a[4]) : THPVariable_Wrap(scales));
+    return PyTuple_Pack(2, o.get(), s.get());
+    END_HANDLE_TH_ERRORS
+}
+
+// blocks(w, out, scales, stream) -> (q, scales)
+PyObject* blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 4);
+    const at::Tensor& w = cuda_tensor(a[0], "w");
+    const at::Device dev = w.device();
+    TORCH_CHECK_VALUE(w.dim() == 2, "w must have shape [rows, cols]");
+    const int64_t rows = w.size(0), cols = w.size(1);
+    TORCH_CHECK_VALUE(rows <= INT_MAX && cols <= INT_MAX, "w is too large");
+    const Rows wr = rows_of(w, rows, cols, kBf16, dev, "w");
+    const c10::cuda::CUDAGuard guard(dev);
+    const OnStream stream(a[3], dev);
+    const at::Tensor out = given(a[1]) ? tensor(a[1], "out") : empty({rows, cols}, kFp8, dev);
+    const int64_t nr = (rows + 127) / 128, nc = (cols + 127) / 128;
+    const at::Tensor scales = given(a[2]) ? tensor(a[2], "scales") : empty({nr, nc}, at::kFloat, dev);
+    const Rows qr = rows_of(out, rows, cols, kFp8, dev, "out");
+    TORCH_CHECK_VALUE(scales.dim() == 2 && scales.size(0) == nr && scales.size(1) == nc && scales.is_contiguous(),
+                      "scales must be contiguous with shape (", nr, ", ", nc, ")");
+    float* const sp = static_cast<float*>(pointer(scales, at::kFloat, dev, "scales"));
+    check(unlocked([&] { return g_fp8_blocks(wr.p, wr.stride, (int)rows, (int)cols, qr.p, qr.stride, sp, stream.handle); }),
+          "lora_linear_fp8_blocks");
+    if (given(a[1])) wrote(out);
+    if (given(a[2])) wrote(scales);
+    THPObjectPtr o(given(a[1]) ? same(a[1]) : THPVariable_Wrap(out)), s(given(a[2]) ? same(a[2]) : THPVariable_Wrap(scales));
+    return PyTuple_Pack(2, o.get(), s.get());
+    END_HANDLE_TH_ERRORS
+}
+
+// score(logits, tokens, top, temperature, stream) -> (logprobs, ranks, entropy, top_logprobs, top_tokens)
+PyObject* score(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 5);
+    const at::Tensor& x = cuda_tensor(a[0], "logits");
+    const at::Device dev = x.device();
+    const bool fp32 = x.scalar_type() == at::kFloat;
+    TORCH_CHECK_TYPE(fp32 || x.scalar_type() == kBf16, "logits must be BFloat16 or Float, got ", x.scalar_type());
+    TORCH_CHECK_VALUE(x.dim() == 2, "logits must have shape [rows, vocab]");
+    const int64_t rows = x.size(0), vocab = x.size(1);
+    TORCH_CHECK_VALUE(rows <= INT_MAX && vocab <= INT_MAX, "logits are too large");
+    const Rows xr = rows_of(x, rows, vocab, x.scalar_type(), dev, "logits");
+    const int top = to_int(a[2], "top");
+    TORCH_CHECK_VALUE(top >= 0 && top <= LORA_LAYER_MAX_TOP && top <= vocab, "top must be 0 to ", LORA_LAYER_MAX_TOP, ", at most the vocabulary");
+    const float temperature = (float)to_double(a[3]);
+    const void* tp = nullptr;
+    int tokens64 = 0;
+    if (given(a[1])) {
+        const at::Tensor& t = tensor(a[1], "tokens");
+        TORCH_CHECK_TYPE(t.scalar_type() == at::kInt || t.scalar_type() == at::kLong, "tokens must be Int or Long, got ", t.scalar_type());
+        TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == rows && (rows <= 1 || t.stride(0) == 1), "tokens must be contiguous with shape (", rows, ",)");
+        tokens64 = t.scalar_type() == at::kLong;
+        tp = pointer(t, t.scalar_type(), dev, "tokens");
+    }
+    const c10::cuda::CUDAGuard guard(dev);
+    const OnStream stream(a[4], dev);
+    at::Tensor lp, ranks, top_lp, top_tokens;
+    if (given(a[1])) {
+        lp = empty({rows}, at::kFloat, dev);
+        ranks = empty({rows}, at::kInt, dev);
+    }
+    const at::Tensor entropy = empty({rows}, at::kFloat, dev);
+    top_lp = empty({rows, top}, at::kFloat, dev);
+    top_tokens = empty({rows, top}, at::kInt, dev);
+    check(unlocked([&] {
+              return g_logprobs(xr.p, xr.stride, fp32, (int)rows, (int)vocab, tp, tokens64, temperature, top,
+                                lp.defined() ? lp.data_ptr<float>() : nullptr, ranks.defined() ? ranks.data_ptr<int32_t>() : nullptr,
+                                entropy.data_ptr<float>(), top ? top_lp.data_ptr<float>() : nullptr,
+                                top ? top_tokens.data_ptr<int32_t>() : nullptr, stream.handle);
+          }),
+          "lora_linear_token_logprobs");
+    THPObjectPtr l(lp.defined() ? THPVariable_Wrap(lp) : same(Py_None)), r(ranks.defined() ? THPVariable_Wrap(ranks) : same(Py_None));
+    THPObjectPtr e(THPVariable_Wrap(entropy)), tl(THPVariable_Wrap(top_lp)), tt(THPVariable_Wrap(top_tokens));
+    return PyTuple_Pack(5, l.get(), r.get(), e.get(), tl.get(), tt.get());
     END_HANDLE_TH_ERRORS
 }
 
@@ -341,6 +472,9 @@ PyMethodDef methods[] = {{"bind", fast<bind>(), METH_FASTCALL, nullptr},
                          {"norm", fast<norm>(), METH_FASTCALL, nullptr},
                          {"append", fast<append>(), METH_FASTCALL, nullptr},
                          {"attend", fast<attend>(), METH_FASTCALL, nullptr},
+                         {"activate", fast<activate>(), METH_FASTCALL, nullptr},
+                         {"blocks", fast<blocks>(), METH_FASTCALL, nullptr},
+                         {"score", fast<score>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -46,6 +46,43 @@ struct NormParams {
 };
 cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream);
 
+// The gated activation (x [rows, 2 width]: gate, then up), or rows as they are, to bf16 and / or 8 bits.
+struct ActParams {
+    const void* x;
+    void* y;
+    void* q8;
+    float* scales;
+    long long x_stride, y_stride, q8_stride;
+    int rows, width, group;
+};
+cudaError_t launch_act(const ActParams& p, bool gate, cudaStream_t stream);
+
+// A weight to 8 bits, one scale per block of 128 x 128.
+struct BlocksParams {
+    const void* w;
+    void* q8;
+    float* scales;
+    long long w_stride, q8_stride;
+    int rows, cols;
+};
+cudaError_t launch_fp8_blocks(const BlocksParams& p, cudaStream_t stream);
+
+constexpr int kMaxTop = 32;             // most alternatives of a row: one a lane
+
+struct ScoreParams {
+    const void* logits;
+    const void* tokens;                 // or nullptr
+    float* logprobs;
+    int32_t* ranks;
+    float* entropy;
+    float* top_logprobs;                // [rows, top]
+    int32_t* top_tokens;
+    long long stride;
+    float inv_temperature;
+    int rows, vocab, top, is_fp32, tokens64;
+};
+cudaError_t launch_token_logprobs(const ScoreParams& p, cudaStream_t stream);
+
 // Where the tokens of the cached sequences are (lora_kv_cache).
 struct CacheView {
     void* k;
