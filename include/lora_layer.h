@@ -107,10 +107,10 @@ int lora_linear_fp8_blocks(const void* w, long long w_stride, int rows, int cols
  *   logits, stride  device bf16 (is_fp32 0) or fp32 (1) [rows, vocab], row stride >= vocab elements; no alignment
  *                   beyond the element's. Entries of -inf (tokens ruled out) have probability 0.
  *   tokens          device int32 (tokens64 0) or int64 (1) [rows]; NULL where logprobs and ranks are.
- *   temperature     > 0, finite, as its reciprocal.
+ *   temperature     in [2^-64, 2^64].
  *   top             0 to LORA_LAYER_MAX_TOP, at most vocab.
  * Any of logprobs, ranks and entropy may be NULL, but not all outputs. They are contiguous and overlap nothing.
- * z is rounded to fp32 by its factor 1 / temperature and less its maximum; sums are fp32. A row of -inf alone has log
+ * Sums, and the exponentials in them, are fp32. A row of -inf alone has log
  * probabilities of -inf and entropy 0; one with a NaN or +inf has NaN for both, and its ranks and alternatives go by
  * the order, in which a NaN is behind -inf. The same call gives the same bits.
  */

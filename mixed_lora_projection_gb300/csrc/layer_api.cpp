@@ -400,8 +400,8 @@ extern "C" int lora_linear_token_logprobs(const void* logits, long long stride, 
     if (rows < 0 || rows > LORA_MAX_TOKENS || vocab < 1 || vocab > LORA_LAYER_MAX_VOCAB) return LORA_EINVAL;
     if (top < 0 || top > LORA_LAYER_MAX_TOP || top > vocab || (is_fp32 != 0 && is_fp32 != 1) || (tokens64 != 0 && tokens64 != 1))
         return LORA_EINVAL;
+    if (!(temperature >= 5.421010862427522e-20f && temperature <= 18446744073709551616.f)) return LORA_EINVAL;   // 2^-64 .. 2^64
     const float inv = (float)(1.0 / (double)temperature);
-    if (!isfinite(temperature) || temperature <= 0.f || !isfinite(inv) || inv <= 0.f) return LORA_EINVAL;
     if (rows == 0) return LORA_OK;
     const int elem = is_fp32 ? 4 : 2;
     const uintptr_t at = reinterpret_cast<uintptr_t>(logits), t = reinterpret_cast<uintptr_t>(tokens);

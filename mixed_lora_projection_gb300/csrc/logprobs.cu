@@ -2,15 +2,17 @@
 // the logits:
 //
 //     z = x / temperature, m = max z, s = sum e^(z - m), lp_i = z_i - m - log s
-//     entropy = log s - (1 / s) sum (z - m) e^(z - m)
+//     entropy = log s - (1 / s) sum (z - m) e^(z - m)        (any reference m gives the same; in base 2 below)
 //     rank of token t: the entries before it in the order of falling x, ties by rising index; the first `top` of that
 //     order are the alternatives
 //
-// A row is a cluster of 1 to 8 CTAs' (one where there are rows enough), its parts joined through distributed shared
-// memory: no workspace, no second launch, and the same order of sums in every run. Each thread keeps a running maximum
-// and its two sums; a warp keeps the 32 largest entries that it has seen as 64-bit keys (value, then index), one a lane.
-// Entries that may be among the first `top` are rare once the warp's own `top`-th and those of the block's other warps
-// are known; they are collected in shared memory and merged 32 at a time.
+// A row is a cluster's of 1 to 8 CTAs (one where there are rows enough), its parts joined through distributed shared
+// memory: no workspace, no second launch, and the same order of sums in every run. Each thread keeps a reference and its
+// two sums. Vectors of eight entries that may hold some of the first `top` are collected as 64-bit keys (their largest
+// entry, then their index): every lane knows its largest entry, a warp the share-th largest of its lanes' (share = top /
+// 8, rounded up; a few warp reductions), and no entry below the smallest of the CTA's eight is among its first `top`. That
+// leaves about 24 + 24 ln(n / 4096) of n entries for `top` 20. The first `top` of those vectors hold the first `top`
+// entries; they are read once more, and a key's place is the number of larger ones.
 //
 // Bound by memory; 2-byte logits at the copy rate leave 11 lane instructions and 1.4 exponentials' time an entry.
 #include <cuda_bf16.h>
@@ -74,57 +76,102 @@ __device__ __forceinline__ float exp2_of(float t) {      // 2^-22 of the value; 
     return e;
 }
 
-// A part's sums: of 2^t and of t 2^t, t = (x - m) log2(e) / temperature; m = -inf: none yet.
+// A part's sums: of 2^t and of t 2^t, t = (x - m) log2(e) / temperature; the reference m is an entry; -inf: none yet.
 struct Sums {
     float m, s, w;
 };
 __device__ __forceinline__ float from(float m) { return m == -INFINITY ? 0.f : m; }
-// Both parts' sums under the larger maximum.
+// Both parts' sums from the larger reference.
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
-    Sums r;
-    r.m = fmaxf(a.m, b.m);
-    const float base = from(r.m), ta = fmaxf((a.m - base) * c, -1000.f), tb = fmaxf((b.m - base) * c, -1000.f);
+    Sums j;
+    j.m = fmaxf(a.m, b.m);
+    const float base = from(j.m), ta = fmaxf((a.m - base) * c, -1000.f), tb = fmaxf((b.m - base) * c, -1000.f);
     const float ea = exp2_of(ta), eb = exp2_of(tb);
-    r.s = a.s * ea + b.s * eb;
-    r.w = (a.w + a.s * ta) * ea + (b.w + b.s * tb) * eb;
-    return r;
+    j.s = a.s * ea + b.s * eb;
+    j.w = (a.w + a.s * ta) * ea + (b.w + b.s * tb) * eb;
+    return j;
 }
 
 struct Part {                          // of a CTA, or of a warp
     Sums sums;
     int ahead;                         // entries before the given token
 };
+constexpr int kKeep = 64;              // vectors that a warp collects before it sorts them
+constexpr int kPending = kKeep + 2 * 32;    // fewer than kKeep, and an iteration's
 struct Shared {
-    uint64_t list[kWarps][32];
-    uint64_t pending[kWarps][64];
+    alignas(16) uint64_t pending[kWarps][kPending];
+    alignas(16) uint64_t pool[kWarps * 32];   // what the warps, or the cluster's CTAs, bring to the last choice
+    uint64_t list[32];                 // its outcome
     Part part[kWarps];
-    uint64_t cta_list[32];
+    float bound[kWarps];               // at least `share` entries of the warp are as large
+    int count[kWarps];                 // keys in `pending`
+    int pooled;
     Part cta_part;
-    uint32_t bound;                    // the largest of the warps' `top`-th values, ordered
 };
 
-// A warp's 32 largest, and entries that wait to be merged into them.
-struct Top {
-    uint64_t mine;                     // this lane's of the list
-    float own;                         // value of the list's `top`-th entry: a later entry has to be larger
-    int count;                         // entries that wait
-    bool full;                         // the list holds `top` entries
-    __device__ __forceinline__ void merge(uint64_t* pending, int top, uint32_t* bound) {
-        const int lane = threadIdx.x & 31;
-        __syncwarp();
-        uint64_t v = lane < count ? pending[lane] : 0;
-        const uint64_t rest = lane + 32 < count ? pending[lane + 32] : 0;
-        __syncwarp();
-        pending[lane] = rest;
-        count = max(0, count - 32);
-        __syncwarp();
-        mine = merge32(mine, sort32(v));
-        const uint32_t hi = __shfl_sync(kAll, (uint32_t)(mine >> 32), top - 1);
-        full = hi != 0;                // (a NaN's: any number is before it)
-        own = unordered(hi);
-        if (full && lane == 0) atomicMax(bound, hi);
+// The 32 largest of a warp's keys, sorted, in their first places; returns how many those are.
+__device__ __noinline__ int sort_pending(uint64_t* pending, int count) {
+    const int lane = threadIdx.x & 31;
+    uint64_t best = 0;
+    for (int i = 0; i < count; i += 32) best = merge32(best, sort32(i + lane < count ? pending[i + lane] : 0));
+    __syncwarp();
+    pending[lane] = best;
+    __syncwarp();
+    return min(count, 32);
+}
+
+// Every thread's key, where it has one (not 0), to the pool, side by side; the last list is cleared. All threads.
+__device__ __forceinline__ void gather(Shared& sh, uint64_t key) {
+    const int lane = threadIdx.x & 31;
+    __syncthreads();                                           // the pool, its count and the list have been read
+    if (threadIdx.x == 0) sh.pooled = 0;
+    if (threadIdx.x < 32) sh.list[lane] = 0;
+    __syncthreads();
+    const uint32_t have = __ballot_sync(kAll, key != 0);
+    int at = 0;
+    if (lane == 0 && have) at = atomicAdd(&sh.pooled, __popc(have));
+    at = __shfl_sync(kAll, at, 0);
+    if (key) sh.pool[at + __popc(have & ((1u << lane) - 1))] = key;
+    __syncthreads();
+}
+
+// The first `top` of the n keys (n <= 256) in the pool, in their order, to sh.list: a key's place is the number of larger
+// ones. All threads; sh.list is theirs to read after a barrier.
+__device__ __forceinline__ void choose(Shared& sh, int n, int top) {
+    const int tid = threadIdx.x;
+    if (tid < n) {
+        const uint64_t mine = sh.pool[tid];
+        int place = 0;
+        const ulonglong2* all = reinterpret_cast<const ulonglong2*>(sh.pool);
+#pragma unroll 4
+        for (int i = 0; i < n / 2; ++i) {
+            const ulonglong2 k = all[i];
+            place += (k.x > mine) + (k.y > mine);
+        }
+        if (n & 1) place += sh.pool[n - 1] > mine;
+        if (place < top && mine) sh.list[place] = mine;        // (0: none; keys differ by their index)
     }
-};
+}
+
+// Two fp32 values in one instruction.
+__device__ __forceinline__ uint64_t two(float x, float y) { return (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x); }
+__device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 
 template <typename T>
 struct Vec;
@@ -132,6 +179,7 @@ template <>
 struct Vec<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void none() { u = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }   // -inf
     __device__ __forceinline__ void get(float* f) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -149,175 +197,343 @@ struct Vec<float> {
         a = __ldcs(reinterpret_cast<const float4*>(p));
         b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
+    __device__ __forceinline__ void none() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ void get(float* f) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
     static __device__ __forceinline__ float one(const float* p) { return *p; }
 };
+__device__ __forceinline__ float max8(const float* f) {   // (a NaN counts as none)
+    return fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+}
 
+// A thread's pass over its vectors of 8 entries.
 template <typename T>
-__global__ void __launch_bounds__(kThreadsScore) token_logprobs_kernel(const __grid_constant__ ScoreParams p) {
+struct Pass {
+    const ScoreParams& p;
+    Shared& sh;
+    float c, xt;                       // log2(e) / temperature; the given token's logit
+    int tok;
+    bool nan_token;
+    uint64_t c2, base2;                // c, and minus the reference, twice each
+    float limit;                       // an entry over it moves the reference; -inf: no reference yet
+    uint64_t s2, w2;                   // both sums, of even and of odd entries
+    int ahead;
+    float largest;                     // of this lane's entries
+    float bound;                       // at least `top` entries of the CTA are as large: no smaller one is among its first
+    uint64_t own;                      // the warp's top-th largest key, once it has sorted its keys: no vector behind it
+                                       // is wanted either (0: not sorted yet)
+    float least;                       // by both: a vector without an entry as large is not wanted
+    bool any_nan;                      // unless it has NaNs
+
+    __device__ __forceinline__ Pass(const ScoreParams& p, Shared& sh) : p(p), sh(sh) {}
+
+    // Sums of eight entries. The reference stays while no entry is more than 2^8 times its weight (an exponent's rounding
+    // then stays below 2^-21), so that it moves a few times a row and not with every new maximum.
+    __device__ __forceinline__ void sum(const float* f, float vm) {
+        if (vm > limit) {
+            const float m = limit == -INFINITY ? -INFINITY : -lo2(base2), ta = fmaxf((m - vm) * c, -1000.f), ea = exp2_of(ta);
+            w2 = mul2(fma2(s2, two(ta, ta), w2), two(ea, ea));
+            s2 = mul2(s2, two(ea, ea));
+            base2 = two(-vm, -vm);
+            limit = vm + 8.f / c;
+        }
+        uint64_t t[4], e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            t[k] = mul2(add2(two(f[2 * k], f[2 * k + 1]), base2), c2);
+            e[k] = two(exp2_of(lo2(t[k])), exp2_of(hi2(t[k])));
+            s2 = add2(s2, e[k]);
+        }
+        uint64_t w = w2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w = fma2(e[k], t[k], w);
+        const float both = lo2(w) + hi2(w);
+        if (both != both) {                                    // an entry of -inf, of weight 0 (a NaN is in its exponential too)
+            w = w2;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w = fma2(e[k], two(fmaxf(lo2(t[k]), -1000.f), fmaxf(hi2(t[k]), -1000.f)), w);
+        }
+        w2 = w;
+    }
+    __device__ __forceinline__ float weights() const { return lo2(s2) + hi2(s2); }
+    __device__ __forceinline__ Sums sums() const { return Sums{limit == -INFINITY ? -INFINITY : -lo2(base2), weights(), lo2(w2) + hi2(w2)}; }
+
+    // Entries before the given token among eight, the first at index i0.
+    __device__ __forceinline__ void count(const float* f, float vm, int i0, uint32_t valid) {
+        if (nan_token) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ahead += (valid >> k & 1) && (f[k] == f[k] || i0 + k < tok);
+        } else if (vm >= xt) {
+            if (i0 + 8 <= tok && valid == 0xff) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) ahead += f[k] >= xt;
+            } else if (i0 > tok) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) ahead += f[k] > xt;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) ahead += f[k] > xt || (f[k] == xt && i0 + k < tok && (valid >> k & 1));
+            }
+        }
+    }
+
+    // Whether a vector, its largest entry vm, may hold some of the first `top`. (NaNs, which a lane that has met one has in
+    // its sum, are among them only where there are fewer numbers.)
+    __device__ __forceinline__ bool wanted(float vm) const { return vm >= least || (any_nan && weights() != weights()); }
+    __device__ __forceinline__ void push(float vm, int vector) {
+        const int warp = threadIdx.x >> 5;
+        const uint64_t key = key_of(vm, vector);
+        if (key > own) sh.pending[warp][atomicAdd(&sh.count[warp], 1)] = key;
+    }
+    // Where much waits, the warp keeps its 32 first: the first `top` entries are in the `top` first vectors.
+    __device__ __forceinline__ void thin() {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        __syncwarp();
+        const int n = sh.count[warp];
+        if (n < kKeep) return;
+        const int left = sort_pending(sh.pending[warp], n);
+        own = sh.pending[warp][p.top - 1];
+        __syncwarp();
+        if (lane == 0) sh.count[warp] = left;
+        __syncwarp();
+        raise();
+    }
+    // (a vector equal to the warp's top-th comes behind it: a warp's vectors come in rising order)
+    __device__ __forceinline__ void raise() {
+        const uint32_t hi = (uint32_t)(own >> 32);
+        least = fmaxf(bound, hi ? unordered(hi + 1) : -INFINITY);
+        any_nan = own == 0 && bound == -INFINITY;
+    }
+    // The warp's share-th largest of its lanes' largest entries.
+    __device__ __forceinline__ void mark(int share) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        uint32_t v = ordered(largest), m = 0;
+        for (int i = 0; i < share; ++i) {
+            m = __reduce_max_sync(kAll, v);
+            if (lane == __ffs(__ballot_sync(kAll, v == m)) - 1) v = 0;
+        }
+        if (lane == 0 && m) sh.bound[warp] = unordered(m);
+    }
+    __device__ __forceinline__ void renew() {
+        float b = *const_cast<volatile float*>(&sh.bound[0]);
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) b = fminf(b, *const_cast<volatile float*>(&sh.bound[i]));
+        bound = b;
+        raise();
+    }
+};
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreadsScore, 4) token_logprobs_kernel(const __grid_constant__ ScoreParams p) {
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int parts, part;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
     part = parts > 1 ? (int)dev::cluster_ctarank() : 0;
     const long long row = blockIdx.x / parts;
-    if (tid == 0) sh.bound = 0;
-    __syncthreads();
+    if (tid < 32) sh.list[tid] = 0;
+    if (tid == 0) sh.pooled = 0;
+    if (tid < kWarps) {
+        sh.count[tid] = 0;
+        sh.bound[tid] = -INFINITY;
+    }
     dev::griddep_wait();
     dev::griddep_launch_dependents();
 
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
-    const float c = p.inv_temperature * kLog2e;
     long long token = -1;
     if (p.tokens) token = p.tokens64 ? static_cast<const long long*>(p.tokens)[row] : static_cast<const int32_t*>(p.tokens)[row];
     const bool given = token >= 0 && token < p.vocab;
-    const int tok = given ? (int)token : p.vocab;
-    const float xt = given ? Vec<T>::one(x + tok) : INFINITY;
-    const bool nan_token = xt != xt;
+    Pass<T> me(p, sh);
+    me.c = p.inv_temperature * kLog2e;
+    me.tok = given ? (int)token : p.vocab;
+    me.xt = given ? Vec<T>::one(x + me.tok) : INFINITY;
+    me.nan_token = me.xt != me.xt;
+    me.c2 = two(me.c, me.c);
+    me.base2 = 0;
+    me.limit = -INFINITY;
+    me.s2 = me.w2 = 0;
+    me.ahead = 0;
+    me.largest = me.bound = me.least = -INFINITY;
+    me.own = 0;
+    me.any_nan = true;
+    const int share = TOP ? (p.top + kWarps - 1) / kWarps : 1;
 
-    // Entries [0, head) before the row's first 16-byte boundary (16 bytes: 8 or 4 entries), then vectors of 8, then the rest.
+    // Entries [0, head) before the row's first 16-byte boundary, then vectors of 8, then the rest.
     const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T), p.vocab);
     const int n_vec = (p.vocab - head) >> 3, tail = head + 8 * n_vec;
     const int v0 = (int)((long long)n_vec * part / parts), v1 = (int)((long long)n_vec * (part + 1) / parts);
-
-    Sums a = {-INFINITY, 0.f, 0.f};
-    int ahead = 0;
-    Top best = {0, 0.f, 0, false};
-    float lane_bound = -INFINITY;          // no entry below it is among the warp's first `top`
-
-    // Eight entries of this lane, the first at index i0; a missing one is -inf with no bit in `valid`. An entry equal to the
-    // list's `top`-th is behind it, unless it was kept for the end (`late`).
-    auto take = [&](const float* f, int i0, uint32_t valid, bool late) {
-        float vm = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
-        if (vm > a.m) {
-            const Sums none = {vm, 0.f, 0.f};
-            a = join(a, none, c);
-        }
-        const float base = from(a.m);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float t = (f[k] - base) * c, e = exp2_of(t);
-            a.s += e;
-            a.w = fmaf(e, fmaxf(t, -1000.f), a.w);             // (0 for -inf; a NaN is in e)
-        }
-        if (nan_token) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ahead += (valid >> k & 1) && (f[k] == f[k] || i0 + k < tok);
-        } else if (vm >= xt) {
-            if (i0 + 8 <= tok) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) ahead += f[k] >= xt && (valid >> k & 1);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) ahead += f[k] > xt || (f[k] == xt && i0 + k < tok && (valid >> k & 1));
-            }
-        }
-        if (p.top == 0) return;                                // (the whole warp)
-        const float least = fmaxf(lane_bound, unordered(max(*const_cast<volatile uint32_t*>(&sh.bound), 0x007fffffu)));
-        uint32_t pass = 0;
-        if (!best.full || late || (vm > best.own && vm >= least)) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                pass |= (uint32_t)(!best.full || late ? !(f[k] < least) : f[k] > best.own && f[k] >= least) << k;
-            pass &= valid;
-        }
-        if (!__any_sync(kAll, pass)) return;
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t who = __ballot_sync(kAll, pass >> k & 1);
-            if (!who) continue;
-            float v = f[0];                                    // (f[k] without an array in memory)
-#pragma unroll
-            for (int j = 1; j < 8; ++j) v = j == k ? f[j] : v;
-            if (pass >> k & 1) sh.pending[warp][best.count + __popc(who & ((1u << lane) - 1))] = key_of(v, i0 + k);
-            best.count += __popc(who);
-            if (best.count >= 32) best.merge(sh.pending[warp], p.top, &sh.bound);
-        }
-    };
-
-    constexpr int N = 4;                                       // vectors in flight
     const T* xv = x + head;
-    for (int v = v0 + warp * 32; v < v1; v += N * kThreadsScore) {
-        Vec<T> u[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = v + i * kThreadsScore + lane;
-            if (at < v1) u[i].load(xv + 8ll * at);
+
+    // Two vectors an iteration, the next two in flight; all of the CTA's are there but in the last iteration.
+    Vec<T> u0, u1;
+    const int last = v1 - 2 * kThreadsScore;
+    auto load = [&](int at) {
+        if (at - tid <= last) {
+            u0.load(xv + 8ll * at);
+            u1.load(xv + 8ll * (at + kThreadsScore));
+            return;
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = v + i * kThreadsScore + lane;
-            if (v + i * kThreadsScore >= v1) break;
-            float f[8];
-            if (at < v1) {
-                u[i].get(f);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = -INFINITY;
+        u0.none();
+        u1.none();
+        if (at < v1) u0.load(xv + 8ll * at);
+        if (at + kThreadsScore < v1) u1.load(xv + 8ll * (at + kThreadsScore));
+    };
+    int at = v0 + tid;
+    load(at);
+    if (TOP) {
+        // The CTA's bound from its first vectors: `share` lanes of every warp have an entry as large.
+        float f[8];
+        u0.get(f);
+        me.largest = max8(f);
+        u1.get(f);
+        me.largest = fmaxf(fmaxf(me.largest, max8(f)), -INFINITY);
+        __syncthreads();
+        me.mark(share);
+        __syncthreads();
+        me.renew();
+    }
+#pragma unroll 1
+    for (int it = 1; at - tid < v1; at += 2 * kThreadsScore, ++it) {
+        const Vec<T> c0 = u0, c1 = u1;
+        load(at + 2 * kThreadsScore);
+        const bool whole = at - tid <= last;
+        const uint32_t valid0 = whole || at < v1 ? 0xffu : 0u, valid1 = whole || at + kThreadsScore < v1 ? 0xffu : 0u;
+        float f[8];
+        c0.get(f);
+        const float vm0 = max8(f);
+        me.sum(f, vm0);
+        me.count(f, vm0, head + 8 * at, valid0);
+        c1.get(f);
+        const float vm1 = max8(f);
+        me.sum(f, vm1);
+        me.count(f, vm1, head + 8 * (at + kThreadsScore), valid1);
+        if (TOP) {
+            const float vm = fmaxf(vm0, vm1);
+            me.largest = fmaxf(me.largest, vm);
+            if (__any_sync(kAll, me.wanted(vm))) {
+                if (valid0 && me.wanted(vm0)) me.push(vm0, at + 1);
+                if (valid1 && me.wanted(vm1)) me.push(vm1, at + kThreadsScore + 1);
+                me.thin();
             }
-            if (p.top && lane_bound == -INFINITY && !best.full && at - lane + 32 <= v1) {
-                // the warp's first vectors: `top` lanes have a largest entry of at least the `top`-th of those
-                const float vm = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
-                const uint32_t hi = (uint32_t)(sort32((uint64_t)ordered(vm) << 32 | lane) >> 32);
-                lane_bound = fmaxf(unordered(__shfl_sync(kAll, hi, p.top - 1)), -INFINITY);
+            // (after 1, 2, 4, 8 and every 8 iterations)
+            if (it < 8 ? (it & (it - 1)) == 0 : (it & 7) == 0) {
+                me.mark(share);
+                __syncwarp();
+                me.renew();
             }
-            take(f, head + 8 * at, at < v1 ? 0xffu : 0u, false);
         }
     }
-    // The head and the tail: one entry a lane, of the first part's first warp.
+    // The head and the tail, as vectors 0 and n_vec + 1: two lanes of the first part's first warp.
     if (part == 0 && warp == 0) {
-        const int n = p.vocab - tail, i = lane < head ? lane : lane - 16 >= 0 && lane - 16 < n ? tail + lane - 16 : -1;
+        const int i0 = lane == 0 ? 0 : tail, n = lane == 0 ? head : lane == 1 ? p.vocab - tail : 0;
         float f[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = -INFINITY;
-        if (i >= 0) f[0] = Vec<T>::one(x + i);
-        take(f, i >= 0 ? i : 0, i >= 0 ? 1u : 0u, true);
+        for (int k = 0; k < 8; ++k) f[k] = k < n ? Vec<T>::one(x + i0 + k) : -INFINITY;
+        me.sum(f, max8(f));
+        if (n) {
+            float vm = f[0];                                   // (of entries that are there: a NaN is less than -inf)
+#pragma unroll
+            for (int k = 1; k < 8; ++k) vm = k < n ? fmaxf(vm, f[k]) : vm;
+            me.count(f, vm, i0, (1u << n) - 1);
+            if (TOP) me.push(vm, lane == 0 ? 0 : n_vec + 1);
+        }
     }
-    if (p.top)
-        while (best.count) best.merge(sh.pending[warp], p.top, &sh.bound);
 
     // the warp's sums, then the block's, then the cluster's
-#pragma unroll
+    Sums a = me.sums();
+    int ahead = me.ahead;
+#pragma unroll 1
     for (int o = 16; o; o >>= 1) {
         const Sums b = {__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.s, o), __shfl_xor_sync(kAll, a.w, o)};
         // (the lower lane's first in both, so that both have the same bits)
-        a = lane & o ? join(b, a, c) : join(a, b, c);
+        const bool upper = lane & o;
+        a = join(upper ? b : a, upper ? a : b, me.c);
         ahead += __shfl_xor_sync(kAll, ahead, o);
     }
-    sh.list[warp][lane] = best.mine;
     if (lane == 0) sh.part[warp] = Part{a, ahead};
+    if (TOP) {
+        // the warp's last bound, and what it leaves of the entries that wait, at most 32 of a warp, to the pool
+        me.mark(share);
+        __syncthreads();
+        me.renew();
+        int n = sh.count[warp], left = 0;
+        uint64_t* mine = sh.pending[warp];
+        const uint64_t floor = (uint64_t)(me.bound == -INFINITY ? 0 : ordered(me.bound)) << 32;
+        for (int i = 0; i < n; i += 32) {                      // (in place: what moves goes down)
+            const uint64_t k = i + lane < n ? mine[i + lane] : 0;
+            const uint32_t keep = __ballot_sync(kAll, k >= floor && k);
+            __syncwarp();
+            if (keep >> lane & 1) mine[left + __popc(keep & ((1u << lane) - 1))] = k;
+            __syncwarp();
+            left += __popc(keep);
+        }
+        if (left > 32) left = sort_pending(mine, left);
+        int place = 0;
+        if (lane == 0) place = atomicAdd(&sh.pooled, left);
+        place = __shfl_sync(kAll, place, 0);
+        if (lane < left) sh.pool[place + lane] = mine[lane];
+        __syncthreads();
+        choose(sh, sh.pooled, p.top);
+        __syncthreads();
+        // the vectors' entries, one a thread
+        const uint64_t key = sh.list[tid >> 3];
+        const int vector = key_index(key), entry = (vector ? head + 8 * (vector - 1) : 0) + (tid & 7);
+        const bool on = key && (tid >> 3) < p.top && entry < (vector ? p.vocab : head);
+        const uint64_t found = on ? key_of(Vec<T>::one(x + entry), entry) : 0;
+        gather(sh, found >= floor ? found : 0);
+        choose(sh, sh.pooled, p.top);
+    }
     __syncthreads();
     if (warp == 0) {
-        uint64_t v = best.mine;
+#pragma unroll 1
         for (int i = 1; i < kWarps; ++i) {
-            a = join(a, sh.part[i].sums, c);
+            a = join(a, sh.part[i].sums, me.c);
             ahead += sh.part[i].ahead;
-            if (p.top) v = merge32(v, sh.list[i][lane]);
         }
-        best.mine = v;
-        sh.cta_list[lane] = v;
-        if (lane == 0) sh.cta_part = Part{a, ahead};
     }
     if (parts > 1) {
+        if (tid == 0) sh.cta_part = Part{a, ahead};
         dev::cluster_sync();
-        if (part == 0 && warp == 0) {
-            const uint32_t list = dev::smem_addr(&sh.cta_list[lane]), from_part = dev::smem_addr(&sh.cta_part);
-            for (int i = 1; i < parts; ++i) {
-                Part b;
-                uint64_t v;
-                const uint32_t pa = dev::map_to_rank(from_part, (uint32_t)i);
-                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(dev::map_to_rank(list, (uint32_t)i)) : "memory");
+        if (part == 0) {
+            // warp w takes part w's
+            uint64_t key = 0;
+            Part b = {{-INFINITY, 0.f, 0.f}, 0};
+            if (warp < parts) {
+                const uint32_t pa = dev::map_to_rank(dev::smem_addr(&sh.cta_part), (uint32_t)warp);
+                if (TOP)
+                    asm volatile("ld.shared::cluster.u64 %0, [%1];"
+                                 : "=l"(key)
+                                 : "r"(dev::map_to_rank(dev::smem_addr(&sh.list[lane]), (uint32_t)warp))
+                                 : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.sums.m) : "r"(pa) : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1+4];" : "=f"(b.sums.s) : "r"(pa) : "memory");
                 asm volatile("ld.shared::cluster.f32 %0, [%1+8];" : "=f"(b.sums.w) : "r"(pa) : "memory");
                 asm volatile("ld.shared::cluster.u32 %0, [%1+12];" : "=r"(b.ahead) : "r"(pa) : "memory");
-                a = join(a, b.sums, c);
-                ahead += b.ahead;
-                if (p.top) best.mine = merge32(best.mine, v);
             }
+            if (lane == 0) sh.part[warp] = b;
+            if (TOP) {
+                // no key behind some part's top-th is among the first
+                const uint64_t last = (uint64_t)__shfl_sync(kAll, (uint32_t)(key >> 32), p.top - 1) << 32 | __shfl_sync(kAll, (uint32_t)key, p.top - 1);
+                if (lane == 0) sh.pending[0][warp] = last;
+                __syncthreads();
+                uint64_t floor = 0;
+                for (int i = 0; i < parts; ++i) floor = max(floor, sh.pending[0][i]);
+                gather(sh, lane < p.top && key >= floor ? key : 0);
+                choose(sh, sh.pooled, p.top);
+            } else {
+                __syncthreads();
+            }
+            if (warp == 0) {
+#pragma unroll 1
+                for (int i = 1; i < parts; ++i) {
+                    a = join(a, sh.part[i].sums, me.c);
+                    ahead += sh.part[i].ahead;
+                }
+            }
+            __syncthreads();
         }
         dev::cluster_sync();                                   // the parts have been read
     }
@@ -325,13 +541,14 @@ __global__ void __launch_bounds__(kThreadsScore) token_logprobs_kernel(const __g
     const float log_s = logf(a.s);                             // (a row of -inf alone: log 0)
     auto lp = [&](float v) { return v == -INFINITY && a.s == a.s ? v : (v - from(a.m)) * p.inv_temperature - log_s; };
     if (lane == 0) {
-        if (p.entropy) p.entropy[row] = a.s == 0.f ? 0.f : log_s - kLn2 * a.w / a.s;
-        if (p.logprobs) p.logprobs[row] = given ? lp(xt) : __uint_as_float(0x7fc00000u);
+        if (p.entropy) p.entropy[row] = a.s == 0.f ? 0.f : log_s - kLn2 * (a.w / a.s);
+        if (p.logprobs) p.logprobs[row] = given ? lp(me.xt) : __uint_as_float(0x7fc00000u);
         if (p.ranks) p.ranks[row] = given ? ahead : -1;
     }
-    if (lane < p.top) {
-        p.top_logprobs[row * p.top + lane] = lp(key_value(best.mine));
-        p.top_tokens[row * p.top + lane] = key_index(best.mine);
+    if (TOP && lane < p.top) {
+        const uint64_t key = sh.list[lane];
+        p.top_logprobs[row * p.top + lane] = lp(key_value(key));
+        p.top_tokens[row * p.top + lane] = key_index(key);
     }
 }
 
@@ -353,8 +570,8 @@ cudaError_t launch_token_logprobs(const ScoreParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return p.is_fp32 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<float>, p)
-                     : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<__nv_bfloat16>, p);
+    if (p.top) return cudaLaunchKernelEx(&cfg, p.is_fp32 ? token_logprobs_kernel<float, true> : token_logprobs_kernel<__nv_bfloat16, true>, p);
+    return cudaLaunchKernelEx(&cfg, p.is_fp32 ? token_logprobs_kernel<float, false> : token_logprobs_kernel<__nv_bfloat16, false>, p);
 }
 
 }  // namespace lora
