@@ -62,26 +62,6 @@ __device__ __forceinline__ void tmem_wait16(uint32_t* v) {   // v, of the thread
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32"
-        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait32(uint32_t* v) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
-                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
-                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
-                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
-                 :
-                 : "memory");
-}
 // The warp's rows of Y in shared memory to global memory; the elected lane's group of copies.
 __device__ __forceinline__ void store_rows(const CUtensorMap* map, uint32_t src, int col, int row) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
@@ -173,10 +153,10 @@ __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, in
     return w;
 }
 
-// The scales of four blocks of a unit, as warp 3 lays them out for the epilogue, and the unit's place.
+// The scales of a block, as warp 3 lays them out for the epilogue, and its unit's place.
 struct ScaleSlot {
-    float f[4][2][kTileM];                             // per block, half of the columns and row: xs ws
-    int row0, nrows, n0, nb;
+    float f[2][kTileM];                                // per half of the columns and row: xs ws
+    int4 unit;                                         // first row, rows, first column, blocks
 };
 
 // CG: CTAs of the MMA's group; NT: columns of a TMEM buffer, half of them in each epilogue thread's registers. Registers
@@ -185,7 +165,7 @@ template <int CG, int NT, int LOW, int HIGH>
 __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_constant__ Fp8Params p) {
     constexpr int EW = 8;                              // epilogue warps
     constexpr int kCols = NT / 2;                      // columns of an epilogue thread
-    constexpr int kBufs = 512 / NT;                    // TMEM buffers
+    constexpr int kBufs = 512 / NT, kSlots = 2 * kBufs;   // TMEM buffers, places of scales
     constexpr int kYCols = CG > 1 ? 64 : 32;           // columns of a warp's part of the output at a time
     constexpr int kYStage = 64 * kYCols;               // its bytes
     static_assert(NT == 256 || (CG == 1 && NT == 128), "SM pairs run 256-column blocks");
@@ -200,13 +180,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     uint8_t* after = b_ring + (size_t)stages * b_bytes;
     uint8_t* y_stage = after;                          // the epilogue's output rows
     ScaleSlot* slots = reinterpret_cast<ScaleSlot*>(after + EW * kYStage);
-    uint64_t* full = reinterpret_cast<uint64_t*>(slots + 2);
+    uint64_t* full = reinterpret_cast<uint64_t*>(slots + kSlots);
     uint64_t* empty = full + stages;
     uint64_t* tfull = empty + stages;
     uint64_t* tempty = tfull + kBufs;
-    uint64_t* sfull = tempty + kBufs;
-    uint64_t* sempty = sfull + 2;
-    uint64_t* drain = sempty + 2;
+    uint64_t* drain = tempty + kBufs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -224,12 +202,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             mbar_init(smem_addr(&empty[s]), 1);
         }
         for (int b = 0; b < kBufs; ++b) {
-            mbar_init(smem_addr(&tfull[b]), 1);
+            mbar_init(smem_addr(&tfull[b]), 2);              // the MMAs' commit, the scales
             mbar_init(smem_addr(&tempty[b]), CG * EW);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_addr(&sfull[b]), 1);
-            mbar_init(smem_addr(&sempty[b]), EW);
         }
         mbar_init(smem_addr(drain), 2);
         *abort_flag = 0;
@@ -344,9 +318,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             if (lane == 0) wait_lane(smem_addr(drain), 0, abort_flag, p.status, limit, false);
         }
         if (warp == 3) {
-            // ------------------------------------------------------------ scales, up to eight blocks ahead
+            // ------------------------------------------------------------ scales, kBufs blocks ahead
             const int G = p.k_blocks;
-            int quad = 0;
+            int blk = 0;
             bool ok = true;
             for (int u = first; u < n_units && ok; u += step) {
                 const Work w = decode<CG, NT>(p, tiles, u, rank, part);
@@ -357,15 +331,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     xs[i] = p.xs + (long long)min(w.tile.row0 + min(lane + 32 * i, max(w.tile.nrows - 1, 0)), p.rows - 1) * G;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) ws[h] = p.ws + (long long)(min(w.n0 + h * kCols, p.d_out - 1) >> 7) * G;
-                for (int b = 0; b < w.nb; b += 4, ++quad) {
-                    ScaleSlot& slot = slots[quad & 1];
-                    if (!wait_all(smem_addr(&sempty[quad & 1]), ((quad >> 1) & 1) ^ 1, abort_flag, p.status, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    const int g = w.kb0 + b;
-                    // past the last group: the expand's 1
-                    auto take = [&](const float* s, float* v) {
+                for (int b0 = 0; b0 < w.nb && ok; b0 += 4) {
+                    const int g = w.kb0 + b0;
+                    auto take = [&](const float* s, float* v) {   // (past the last group: never used)
                         if (p.vec_scales && (g & 3) == 0 && g < G) {
                             *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(s + g));
                         } else {
@@ -373,27 +341,31 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                             for (int k = 0; k < 4; ++k) v[k] = __ldg(s + min(g + k, G - 1));
                         }
                     };
-                    float c[2][4];
+                    float c[2][4], x[4][4];                  // four blocks' loads in flight
                     take(ws[0], c[0]);
                     take(ws[1], c[1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (32 * i >= w.tile.nrows) break;
-                        float x[4];
-                        take(xs[i], x);
+                    for (int i = 0; i < 4; ++i) take(xs[i], x[i]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
+                        if (b0 + k >= w.nb) break;
+                        // Block blk - kBufs's sums are there: its MMAs began when the epilogue had read block blk - 2 kBufs,
+                        // its scales with it. And blk's phase of the barrier has begun.
+                        const int buf = blk % kBufs;
+                        if (blk >= kBufs && !wait_all(smem_addr(&tfull[buf]), (blk / kBufs - 1) & 1, abort_flag, p.status, limit)) {
+                            ok = false;
+                            break;
+                        }
+                        ScaleSlot& slot = slots[blk % kSlots];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) slot.f[k][h][lane + 32 * i] = b + k < w.nk ? x[k] * c[h][k] : 1.f;
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) slot.f[h][lane + 32 * i] = b0 + k < w.nk ? x[i][k] * c[h][k] : 1.f;
+                        if (lane == 0) slot.unit = make_int4(w.tile.row0, w.tile.nrows, w.n0, w.nb);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&tfull[buf]));
+                        ++blk;
                     }
-                    if (lane == 0) {
-                        slot.row0 = w.tile.row0;
-                        slot.nrows = w.tile.nrows;
-                        slot.n0 = w.n0;
-                        slot.nb = w.nb;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sfull[quad & 1]));
                 }
             }
         }
@@ -409,36 +381,32 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
         const int r_local = q * 32 + lane;
         const uint32_t t0 = tmem_base + (uint32_t)(cg * kCols) + ((uint32_t)(q * 32) << 16);
         uint8_t* const mine = y_stage + (warp - 4) * kYStage;
-        const uint32_t my_scale = smem_addr(&slots[0].f[0][cg][r_local]);
+        const uint32_t my_scale = smem_addr(&slots[0].f[cg][r_local]);
         const uint32_t tfull0 = smem_addr(tfull), tempty0 = CG > 1 ? map_to_rank(smem_addr(tempty), 0) : smem_addr(tempty);
-        uint32_t buf = 0, phase = 0, quad = 0;
+        uint32_t buf = 0, phase = 0, place = 0;
         bool ok = true;
         uint64_t acc[kCols / 2];
 #pragma unroll
         for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
         for (int u = first; u < n_units && ok; u += step) {
             int row0 = 0, nrows = 0, n0 = 0, nb = 1;
-            for (int b0 = 0; b0 < nb; b0 += 4, ++quad) {
-                ScaleSlot& slot = slots[quad & 1];
-                if (!wait_all(smem_addr(&sfull[quad & 1]), (quad >> 1) & 1, abort_flag, p.status, limit)) {
+#pragma unroll 1
+            for (int b = 0; b < nb; ++b) {
+                if (!wait_all(tfull0 + 8 * buf, phase, abort_flag, p.status, limit)) {
                     ok = false;
                     break;
                 }
-                row0 = slot.row0;
-                nrows = slot.nrows;
-                n0 = slot.n0;
-                nb = slot.nb;
-                const int m = min(4, nb - b0);
-                uint32_t at = my_scale + (quad & 1) * (uint32_t)sizeof(ScaleSlot);
-#pragma unroll 1
-                for (int k = 0; k < m; ++k, at += sizeof(slot.f[0])) {
+                tc_fence_after();
+                {
                     float f;
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at));
-                    if (!wait_all(tfull0 + 8 * buf, phase, abort_flag, p.status, limit)) {
-                        ok = false;
-                        break;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(my_scale + place * (uint32_t)sizeof(ScaleSlot)));
+                    if (b == 0) {
+                        const int4 unit = slots[place].unit;
+                        row0 = unit.x;
+                        nrows = unit.y;
+                        n0 = unit.z;
+                        nb = unit.w;
                     }
-                    tc_fence_after();
                     const uint32_t t = t0 + buf * NT;
                     const uint64_t f2 = pair(__float_as_uint(f), __float_as_uint(f));
                     auto release = [&] {                     // this warp has read the buffer
@@ -465,10 +433,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                         }
                     }
                     if (++buf == kBufs) { buf = 0; phase ^= 1; }
+                    place = place + 1 == kSlots ? 0 : place + 1;
                 }
-                if (!ok) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sempty[quad & 1]));
             }
             if (!ok) break;
             if (CG > 1 || p.parts == 1) {
@@ -584,7 +550,7 @@ inline auto kernel_of(int wide, int tile_n) { return wide ? kWide : tile_n == 25
 
 size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages) {
     return 1024 + (size_t)stages * (a_rows + tile_n / (wide ? 2 : 1)) * kFp8StageRow + 8 * 64 * (wide ? 64 : 32) +
-           2 * sizeof(dev::ScaleSlot) + 8 * (2 * (size_t)stages + 2 * 512 / tile_n + 5) + 16;
+           2 * (512 / tile_n) * sizeof(dev::ScaleSlot) + 8 * (2 * (size_t)stages + 2 * 512 / tile_n + 1) + 16;
 }
 
 cudaError_t fp8_prepare_device() {
