@@ -1618,24 +1618,36 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     make_groups(plan.fused, cg, false, h->u_rows - kTileM, &groups);
     const int nft = (int)groups.size();
 
-    // the shrink (bf16): launched ahead, over rank tiles so that a few groups still find most SMs
+    // The shrink (bf16) is launched ahead: the bf16 kernel's units over rank tiles, or, where that finishes sooner, one
+    // tile and one part of K a CTA (by the K steps' cycles that its units were measured at).
     Shape sh;
-    int rank_tiles = 1;
+    int rank_tiles = 1, parts = 0;
     if (n_used) {
         sh = choose_shape(h, plan, false);
         sh.bk = 64;
         sh.a_rows = kTileM;
-        const int sg = (int)(sh.shrink_groups.size() / sh.cs);
-        const int room = std::max(1, usable_sms(h) / sh.cs / sg);
-        const int width = std::max(32, ceil_div(ceil_div(h->rank, std::min(room, 8)), 32) * 32);
+        const int sg = (int)(sh.shrink_groups.size() / sh.cs), slots = std::max(1, usable_sms(h) / sh.cs);
+        const int width = std::max(32, ceil_div(ceil_div(h->rank, std::min(std::max(1, slots / sg), 8)), 32) * 32);
         if (width < sh.shrink_n) {
             rank_tiles = ceil_div(h->rank, width);
             sh.shrink_n = width;
         }
         sh.tile_n = sh.shrink_n;
         sh.stages = stages_for(sh.shrink_n / sh.cs, sh.bk);
+        const int steps = ceil_div(h->d_in, 64), n = ceil_div(h->rank, 16) * 16, tiles = (int)plan.shrink.size();
+        double best = (double)ceil_div((long long)sg * rank_tiles, slots) * steps * kstep_cycles(sh.cs, sh.shrink_n);
+        for (int q = 1; q <= std::min(kFp8MaxParts, steps); ++q) {
+            if (q > 1 && (tiles > h->fp8_clusters[1][q] || tiles * q > usable_sms(h))) continue;
+            const double t = (double)ceil_div(tiles, q > 1 ? tiles : usable_sms(h)) * ceil_div(steps, q) * kstep_cycles(1, n) + (q > 1 ? 4000 : 0);
+            if (t < best) {
+                best = t;
+                parts = q;
+            }
+        }
+        if (parts) sh.shrink_groups = plan.shrink;
     }
     const int nst = n_used ? (int)sh.shrink_groups.size() : 0;
+    const int a_rows = parts ? ceil_div(h->rank, 16) * 16 : sh.shrink_n / sh.cs;   // of an A_a box
     for (const Tile& t : groups)
         if (t.adapter < 0 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T ||
             (t.adapter && t.u_row != t.row0 && t.u_row != h->u_rows - kTileM))
@@ -1654,14 +1666,16 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     Fp8Params q;
     memset(&q, 0, sizeof(q));
     GemmParams p;
-    if (n_used) memset(&p, 0, sizeof(p));
+    ShrinkParams r;
+    if (parts) memset(&r, 0, sizeof(r));
+    else if (n_used) memset(&p, 0, sizeof(p));
     Slot* slot = nullptr;
     // B_a's maps for this kernel's boxes, A_a's for the shrink's
     auto maps = [&](CUtensorMap* b, CUtensorMap* a) {
         for (int k = 0; k < n_used; ++k) {
             const int i = plan.used_adapters[k];
             if (encode_2d(h, &b[k], B[i], h->rank, h->d_out, 64, s8.tile_n / cg) != CUDA_SUCCESS ||
-                encode_2d(h, &a[k], A[i], h->d_in, h->rank, 64, sh.shrink_n / sh.cs) != CUDA_SUCCESS)
+                encode_2d(h, &a[k], A[i], h->d_in, h->rank, 64, (uint32_t)a_rows) != CUDA_SUCCESS)
                 return false;
         }
         return true;
@@ -1670,12 +1684,13 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         memcpy(q.inline_tiles, groups.data(), (size_t)nft * sizeof(Tile));
         q.inline_wl = 1;
         if (n_used) {
-            if (!maps(q.inline_bmaps, p.inline_maps + kInlineAdapters)) return LORA_ECUDA;
-            memcpy(p.inline_tiles, sh.shrink_groups.data(), (size_t)nst * sizeof(Tile));
-            memcpy(p.inline_seg, plan.seg_off.data(), 4 * (size_t)(n_m + 1));
-            memcpy(p.inline_seg + n_m + 1, plan.seg_id.data(), 4 * (size_t)n_m);
-            for (int k = 0; k < n_used; ++k) p.inline_scales[k] = scale[plan.used_adapters[k]];
-            p.inline_wl = 1;
+            if (!maps(q.inline_bmaps, parts ? r.inline_amaps : p.inline_maps + kInlineAdapters)) return LORA_ECUDA;
+            memcpy(parts ? r.inline_tiles : p.inline_tiles, sh.shrink_groups.data(), (size_t)nst * sizeof(Tile));
+            int32_t* seg = parts ? r.inline_seg : p.inline_seg;
+            memcpy(seg, plan.seg_off.data(), 4 * (size_t)(n_m + 1));
+            memcpy(seg + n_m + 1, plan.seg_id.data(), 4 * (size_t)n_m);
+            for (int k = 0; k < n_used; ++k) (parts ? r.inline_scales : p.inline_scales)[k] = scale[plan.used_adapters[k]];
+            (parts ? r.inline_wl : p.inline_wl) = 1;
         }
     } else {
         slot = acquire_slot(h);
@@ -1697,12 +1712,22 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         if (cudaMemcpyAsync(slot->dev, hb, bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess) return LORA_ECUDA;
         q.tm_b = reinterpret_cast<const CUtensorMap*>(slot->dev);
         q.tiles = reinterpret_cast<const Tile*>(slot->dev + off_tiles);
-        if (n_used) {
-            p.tm_a = reinterpret_cast<const CUtensorMap*>(slot->dev + off_a);
-            p.shrink_tiles = reinterpret_cast<const Tile*>(slot->dev + off_shrink);
-            p.seg_off = reinterpret_cast<const int32_t*>(slot->dev + off_seg);
-            p.seg_id = reinterpret_cast<const int32_t*>(slot->dev + off_id);
-            p.scales = reinterpret_cast<const float*>(slot->dev + off_scale);
+        const auto* tm_a = reinterpret_cast<const CUtensorMap*>(slot->dev + off_a);
+        const auto* tiles = reinterpret_cast<const Tile*>(slot->dev + off_shrink);
+        const auto *seg_off = reinterpret_cast<const int32_t*>(slot->dev + off_seg), *seg_id = reinterpret_cast<const int32_t*>(slot->dev + off_id);
+        const auto* sc = reinterpret_cast<const float*>(slot->dev + off_scale);
+        if (parts) {
+            r.tm_a = tm_a;
+            r.tiles = tiles;
+            r.seg_off = seg_off;
+            r.seg_id = seg_id;
+            r.scales = sc;
+        } else if (n_used) {
+            p.tm_a = tm_a;
+            p.shrink_tiles = tiles;
+            p.seg_off = seg_off;
+            p.seg_id = seg_id;
+            p.scales = sc;
         }
     }
     TimingRec rec{};
@@ -1714,7 +1739,23 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         }
         cudaEventRecord(rec.ev[0], stream);
     }
-    if (n_used) {
+    if (parts) {
+        if (encode_2d(h, &r.tm_x, x, h->d_in, T, 64, kTileM) != CUDA_SUCCESS) return LORA_ECUDA;
+        r.u = h->u_ws;
+        r.status = h->status;
+        r.wait_limit_ns = h->wait_limit_ns;
+        r.n_tiles = nst;
+        r.n_seg = n_m;
+        r.rank = h->rank;
+        r.n = a_rows;
+        r.k_steps = ceil_div(h->d_in, 64);
+        r.parts = parts;
+        r.stages = shrink_stages(a_rows);
+        r.debug_stall = h->debug_stall;
+        if (launch_shrink(r, stream) != cudaSuccess) return LORA_ECUDA;
+        ++h->launches;
+        rec.has_shrink = true;
+    } else if (n_used) {
         if (encode_2d(h, &p.tm_x, x, h->d_in, T, 64, kTileM) != CUDA_SUCCESS) return LORA_ECUDA;
         p.u = h->u_ws;
         p.status = h->status;
@@ -1758,6 +1799,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.raster_group = s8.raster_group;
     q.k_blocks = q_groups;
     q.k_lora = ceil_div(h->rank, 64);
+    q.lora_stages = s8.stages >= q.k_lora + 512 / s8.tile_n - 1 ? q.k_lora : 1;
     q.d_out = h->d_out;
     q.parts = s8.parts;
     q.a_rows = s8.a_rows;

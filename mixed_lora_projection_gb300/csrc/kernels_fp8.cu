@@ -6,8 +6,8 @@
 //
 // A group's 128 products are summed by tcgen05.mma kind::f8f6f4 in tensor memory; each group has a scale of
 // its own per row and block of columns, so its sums leave tensor memory and are added, times that scale, to
-// fp32 accumulators in the epilogue warps' registers. The expand's 64-wide K-steps are more such blocks (kind::f16,
-// bf16 operands) with scale 1.
+// fp32 accumulators in the epilogue warps' registers. The expand is one more such block (kind::f16, bf16 operands, the
+// stages of the whole rank) with scale 1.
 //
 // Per CTA: warp 0 loads the stages (TMA, rows of 128 bytes, 128-byte swizzle: 128 e4m3 or 64 bf16); warps 1 and
 // 2 issue the even and the odd blocks' MMAs into the two TMEM buffers (a warp's barrier wait completes after the
@@ -134,10 +134,11 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// The blocks of one unit as every role walks them: base groups [kb0, kb0 + nk), then the expand's K-steps; nb in all.
+// The blocks of one unit as every role walks them: base groups [kb0, kb0 + nk), a stage each, then the expand's, of
+// lora_stages stages; nb blocks and ns stages in all.
 struct Work {
     Tile tile;
-    int n0, kb0, nk, nb;
+    int n0, kb0, nk, nb, ns;
 };
 template <int CG, int NT>
 __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, int u, int rank, int part) {
@@ -149,7 +150,9 @@ __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, in
     w.n0 = (g * p.raster_group + r % gw) * NT;
     w.kb0 = part * p.k_blocks / p.parts;
     w.nk = (part + 1) * p.k_blocks / p.parts - w.kb0;
-    w.nb = w.nk + (w.tile.adapter && part == p.parts - 1 ? p.k_lora : 0);
+    const bool expand = w.tile.adapter && part == p.parts - 1;
+    w.nb = w.nk + (expand ? p.k_lora / p.lora_stages : 0);
+    w.ns = w.nk + (expand ? p.k_lora : 0);
     return w;
 }
 
@@ -231,12 +234,12 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             const uint32_t tx = CG * (a_bytes + b_bytes);
             for (int u = first; u < n_units && ok; u += step) {
                 const Work w = decode<CG, NT>(p, tiles, u, rank, part);
-                const CUtensorMap* bm = &bmaps[w.nb > w.nk ? w.tile.adapter - 1 : 0];
-                if (w.nb > w.nk && !p.inline_wl && acquired != w.tile.adapter) {
+                const CUtensorMap* bm = &bmaps[w.ns > w.nk ? w.tile.adapter - 1 : 0];
+                if (w.ns > w.nk && !p.inline_wl && acquired != w.tile.adapter) {
                     tensormap_acquire(bm);
                     acquired = w.tile.adapter;
                 }
-                for (int b = 0; b < w.nb; ++b) {
+                for (int b = 0; b < w.ns; ++b) {
                     if (!wait_all(smem_addr(&empty[stage]), phase ^ 1, abort_flag, p.status, limit)) {
                         ok = false;
                         break;
@@ -277,39 +280,45 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             for (int u = first; u < n_units && ok; u += step) {
                 const Work w = decode<CG, NT>(p, tiles, u, rank, part);
                 for (int b = 0; b < w.nb; ++b, ++blk) {
+                    const bool main = b < w.nk;
+                    const int ns = main ? 1 : p.lora_stages;
                     if ((blk & 1) == mine) {
                         // The buffer first: it is free when the epilogue has taken block blk - kBufs, and so every stage up
-                        // to that block's has been filled and read. Only then does this stage's parity tell this fill
-                        // from the one a lap (kBufs stages at least) before.
+                        // to that block's has been filled and read. Only then does a stage's parity tell this fill from the
+                        // one a lap before, where a lap is longer than the stages of the blocks since (launch_fp8).
                         const int buf = blk % kBufs;
                         const uint32_t d = tmem_base + (uint32_t)(buf * NT);
-                        if (!wait_all(smem_addr(&tempty[buf]), ((blk / kBufs) & 1) ^ 1, abort_flag, p.status, limit) ||
-                            !wait_all(smem_addr(&full[stage]), phase, abort_flag, p.status, limit)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
-                        const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
-                        // 32 bytes along K inside the swizzled rows a step
-                        // (one elected lane, in a branch of its own: 4 MMAs issue in ~100 cycles; under a predicate that the
-                        // compiler cannot tell to be one lane's, in ~550)
-                        if (elect_one()) {
-                            if (b < w.nk) {
+                        ok = wait_all(smem_addr(&tempty[buf]), ((blk / kBufs) & 1) ^ 1, abort_flag, p.status, limit);
+                        for (int s = 0; s < ns && ok; ++s) {
+                            ok = wait_all(smem_addr(&full[stage]), phase, abort_flag, p.status, limit);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
+                            const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
+                            // 32 bytes along K inside the swizzled rows a step
+                            // (one elected lane, in a branch of its own: 4 MMAs issue in ~100 cycles; under a predicate that
+                            // the compiler cannot tell to be one lane's, in ~550)
+                            if (elect_one()) {
+                                if (main) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_e4m3<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc8, k > 0 ? 1u : 0u, 1u);
-                            } else {
+                                    for (int k = 0; k < 4; ++k)
+                                        mma_e4m3<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc8, k > 0 ? 1u : 0u, 1u);
+                                } else {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_bf16<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc16, k > 0 ? 1u : 0u, 1u);
+                                    for (int k = 0; k < 4; ++k)
+                                        mma_bf16<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc16, (s > 0 || k > 0) ? 1u : 0u, 1u);
+                                }
+                                if (s == ns - 1) mma_commit<CG>(smem_addr(&tfull[buf]), 1u);
+                                mma_commit<CG>(smem_addr(&empty[stage]), 1u);
                             }
-                            mma_commit<CG>(smem_addr(&tfull[buf]), 1u);
-                            mma_commit<CG>(smem_addr(&empty[stage]), 1u);
+                            __syncwarp();
+                            if (++stage == stages) { stage = 0; phase ^= 1; }
                         }
-                        __syncwarp();
+                        if (!ok) break;
+                    } else {
+                        stage += ns;
+                        if (stage >= stages) { stage -= stages; phase ^= 1; }
                     }
-                    if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
             }
             // every MMA this warp issued has completed before TMEM is released
@@ -537,11 +546,161 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     }
 }
 
+// U[t, :] = bf16(s_a X[t, :] A_a^T) for one tile of 128 rows and one part of K a CTA, the parts of a tile a cluster: the
+// bf16 kernel's shrink units take a tile each, 272 K steps of it at d_in 17,408 (1,553 rows of rank 64 there 80 us; in 8
+// parts 12). Bound by the fill of shared memory, 61 bytes a cycle, or by a few rows' latency.
+__global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int stages = p.stages;
+    const uint32_t a_bytes = kTileM * kFp8StageRow, b_bytes = (uint32_t)p.n * kFp8StageRow;
+    uint8_t* a_ring = base;
+    uint8_t* b_ring = a_ring + (size_t)stages * a_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(b_ring + (size_t)stages * b_bytes);
+    uint64_t* empty = full + stages;
+    uint64_t* done = empty + stages;                   // every MMA has completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int part = p.parts > 1 ? (int)cluster_ctarank() : 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(smem_addr(&full[s]), 1);
+            mbar_init(smem_addr(&empty[s]), 1);
+        }
+        mbar_init(smem_addr(done), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc<1>(smem_addr(tmem_slot), 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint64_t limit = p.wait_limit_ns;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const Tile tile = (p.inline_wl ? p.inline_tiles : p.tiles)[blockIdx.x / p.parts];
+    const int k0 = part * p.k_steps / p.parts, nk = (part + 1) * p.k_steps / p.parts - k0;
+    bool ok = true;
+    if (warp == 0 && !p.debug_stall) {
+        const CUtensorMap* am = &(p.inline_wl ? p.inline_amaps : p.tm_a)[tile.adapter - 1];
+        if (!p.inline_wl) tensormap_acquire(am);
+        int issued = 0;
+        for (int k = 0; k < nk; ++k) {
+            const int stage = k % stages;
+            if (!wait_all(smem_addr(&empty[stage]), ((k / stages) & 1) ^ 1, abort_flag, p.status, limit)) {
+                ok = false;
+                break;
+            }
+            const uint32_t bar = smem_addr(&full[stage]);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar, a_bytes + b_bytes, 1u);
+                tma_load_2d<1>(smem_addr(a_ring + (size_t)stage * a_bytes), &p.tm_x, bar, (k0 + k) * 64, tile.row0, 1u);
+                tma_load_2d<1>(smem_addr(b_ring + (size_t)stage * b_bytes), am, bar, (k0 + k) * 64, 0, 1u);
+            }
+            __syncwarp();
+            ++issued;
+        }
+        if (!ok && lane == 0)                              // copies in flight (bounded, whatever the abort flag says)
+            for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
+                wait_lane(smem_addr(&full[j % stages]), (uint32_t)((j / stages) & 1), abort_flag, p.status, limit, false);
+    } else if (warp == 1) {
+        const uint32_t idesc = instr_desc_bf16(kTileM, p.n);
+        for (int k = 0; k < nk; ++k) {
+            const int stage = k % stages;
+            if (!wait_all(smem_addr(&full[stage]), (k / stages) & 1, abort_flag, p.status, limit)) break;
+            tc_fence_after();
+            const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
+            const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_bf16<1>(tmem_base, ad + (uint64_t)(2 * i), bd + (uint64_t)(2 * i), idesc, (k > 0 || i > 0) ? 1u : 0u, 1u);
+                mma_commit<1>(smem_addr(&empty[stage]), 1u);
+            }
+            __syncwarp();
+        }
+        // (also where a wait ran out: every MMA this warp issued completes before TMEM is released)
+        if (elect_one()) mma_commit<1>(smem_addr(done), 1u);
+        __syncwarp();
+        if (lane == 0) wait_lane(smem_addr(done), 0, abort_flag, p.status, limit, false);
+    }
+    __syncwarp();
+    float4* sums = reinterpret_cast<float4*>(base);
+    if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue: row 32 q + lane
+        const int q = warp & 3, r_local = q * 32 + lane, row = tile.row0 + r_local;
+        ok = wait_all(smem_addr(done), 0, abort_flag, p.status, limit) && !*abort_flag;
+        tc_fence_after();
+        if (ok && q * 32 < tile.nrows) {
+            const bool mine = r_local < tile.nrows;
+            const int32_t* seg_off = p.inline_wl ? p.inline_seg : p.seg_off;
+            const int32_t* seg_id = p.inline_wl ? p.inline_seg + p.n_seg + 1 : p.seg_id;
+            const float s = mine && row_adapter(seg_off, seg_id, p.n_seg, row) == tile.adapter
+                                ? (p.inline_wl ? p.inline_scales : p.scales)[tile.adapter - 1] : 0.f;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.u) + (long long)row * p.rank;
+            for (int c = 0; c < p.n; c += 16) {
+                uint32_t v[16];
+                if (nk) tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+                tmem_wait16(v);
+                float f[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = nk && s != 0.f ? __uint_as_float(v[i]) * s : 0.f;
+                if (p.parts > 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sums[((c >> 2) + i) * kTileM + r_local] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                } else if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (c + 8 * i < p.rank)
+                            *reinterpret_cast<uint4*>(out + c + 8 * i) =
+                                make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                                           pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+                }
+            }
+        }
+    }
+    if (p.parts > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 4 && ok) {
+            // each CTA adds its share of the columns over the parts, in their order
+            const int v0 = part * (p.rank / 8) / p.parts, vecs = (part + 1) * (p.rank / 8) / p.parts - v0;
+            for (int i = (int)threadIdx.x - 128; i < tile.nrows * vecs; i += 128) {
+                const int r = i / vecs, c = 8 * (v0 + i - r * vecs);
+                const uint32_t at = smem_addr(base) + (uint32_t)(((c >> 2) * kTileM + r) * 16);
+                float s[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s[k] = 0.f;
+                for (int j = 0; j < p.parts; ++j) {
+                    const uint32_t a = map_to_rank(at, (uint32_t)j);
+                    const float4 x = ld_cluster(a), y = ld_cluster(a + kTileM * 16);
+                    s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+                    s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+                }
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.u) + (long long)(tile.row0 + r) * p.rank + c) =
+                    make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+            }
+        }
+        __syncwarp();
+        cluster_sync();                                    // the parts' sums have been read
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc<1>(tmem_base, 256);
+    }
+}
+
 }  // namespace
 }  // namespace dev
 
 namespace {
-// 384 threads of 168 registers, dealt out anew: 72 x 128 + 216 x 256 = 168 x 384
+// 384 threads of 168 registers, dealt out anew: 72 x 128 + 216 x 256 = 168 x 384. A few bytes spilled in the loading warps
+// cost a tenth to a fifth of all (pairs, 9,728 rows of 5,120 -> 5,120: 198 us; with 64 and 216, 40 bytes, 223).
 constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 72, 216>;
 constexpr auto kSingle = dev::lora_fp8_kernel<1, 256, 72, 216>;
 constexpr auto kNarrow = dev::lora_fp8_kernel<1, 128, 72, 216>;
@@ -553,7 +712,39 @@ size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages) {
            2 * (512 / tile_n) * sizeof(dev::ScaleSlot) + 8 * (2 * (size_t)stages + 2 * 512 / tile_n + 1) + 16;
 }
 
+static size_t shrink_smem_bytes(int n, int stages) {
+    return 1024 + (size_t)stages * (kTileM + n) * kFp8StageRow + 8 * (2 * (size_t)stages + 1) + 16;
+}
+int shrink_stages(int n) {
+    int s = 2;
+    while (s < 8 && shrink_smem_bytes(n, s + 1) <= (size_t)kSmemLimit) ++s;
+    return s;
+}
+
+cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
+    // the parts' sums take the rings' place
+    if (p.n < 16 || p.n > 256 || p.n % 16 || p.rank < 8 || p.rank > p.n || p.rank % 8 || p.parts < 1 || p.parts > kFp8MaxParts ||
+        p.parts > p.k_steps || p.n_tiles < 1 || p.stages < 2 || shrink_smem_bytes(p.n, p.stages) > (size_t)kSmemLimit ||
+        (p.parts > 1 && (size_t)p.stages * (kTileM + p.n) * kFp8StageRow < (size_t)p.n * kTileM * 4))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(p.n_tiles * p.parts);
+    cfg.blockDim = dim3(kShrinkThreads);
+    cfg.dynamicSmemBytes = shrink_smem_bytes(p.n, p.stages);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)p.parts, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, dev::lora_shrink_kernel, p);
+}
+
 cudaError_t fp8_prepare_device() {
+    cudaError_t r = cudaFuncSetAttribute(dev::lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (r != cudaSuccess) return r;
     for (const auto k : {kWide, kSingle, kNarrow}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
@@ -599,10 +790,10 @@ cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream) {
     if ((p.tile_n != 256 && (p.wide || p.tile_n != 128)) || p.parts < 1 || p.parts > kFp8MaxParts || p.parts > p.k_blocks ||
         (p.wide && (p.parts != 1 || p.a_rows != kTileM)) || p.a_rows < 16 || p.a_rows > kTileM || p.a_rows % 16)
         return cudaErrorInvalidValue;
-    // stages: a lap is at least as long as the TMEM buffers are many; an A stage's 128 rows lie inside the rings; the
-    // parts' sums take the rings' place
+    // stages: a lap is longer than the stages of the blocks between two uses of a TMEM buffer; an A stage's 128 rows lie
+    // inside the rings; the parts' sums take the rings' place
     const size_t rings = (size_t)p.stages * (p.a_rows + tile_rows) * kFp8StageRow;
-    if (p.stages < 512 / p.tile_n || fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages) > (size_t)kSmemLimit ||
+    if (p.lora_stages < 1 || p.k_lora % p.lora_stages || p.stages < p.lora_stages + 512 / p.tile_n - 1 || fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages) > (size_t)kSmemLimit ||
         (size_t)p.stages * tile_rows < (size_t)(kTileM - p.a_rows) || (p.parts > 1 && rings < (size_t)p.tile_n * kTileM * 4))
         return cudaErrorInvalidValue;
     // units of K parts: one a cluster (the rings hold its sums at its end)

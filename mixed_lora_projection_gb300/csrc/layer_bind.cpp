@@ -31,6 +31,7 @@ decltype(&lora_linear_silu_mul) g_silu_mul;
 decltype(&lora_linear_fp8_rows) g_fp8_rows;
 decltype(&lora_linear_fp8_blocks) g_fp8_blocks;
 decltype(&lora_linear_token_logprobs) g_logprobs;
+decltype(&lora_linear_forward_fp8) g_project;
 PyObject* g_check;                                     // (code, entry point) -> raises
 
 constexpr auto kBf16 = at::kBFloat16;
@@ -185,11 +186,11 @@ void* address(PyObject* o) {
     return p;
 }
 
-// bind(add_rms_norm, kv_append, attn_forward, silu_mul, fp8_rows, fp8_blocks, token_logprobs, check): addresses of the
-// entry points, and what raises their errors
+// bind(add_rms_norm, kv_append, attn_forward, silu_mul, fp8_rows, fp8_blocks, token_logprobs, forward_fp8, check): addresses
+// of the entry points, and what raises their errors
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    TORCH_CHECK_TYPE(n == 8, "wrong number of arguments");
+    TORCH_CHECK_TYPE(n == 9, "wrong number of arguments");
     g_norm = reinterpret_cast<decltype(g_norm)>(address(a[0]));
     g_append = reinterpret_cast<decltype(g_append)>(address(a[1]));
     g_attend = reinterpret_cast<decltype(g_attend)>(address(a[2]));
@@ -197,7 +198,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_fp8_rows = reinterpret_cast<decltype(g_fp8_rows)>(address(a[4]));
     g_fp8_blocks = reinterpret_cast<decltype(g_fp8_blocks)>(address(a[5]));
     g_logprobs = reinterpret_cast<decltype(g_logprobs)>(address(a[6]));
-    Py_XSETREF(g_check, same(a[7]));
+    g_project = reinterpret_cast<decltype(g_project)>(address(a[7]));
+    Py_XSETREF(g_check, same(a[8]));
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -383,6 +385,67 @@ PyObject* score(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// Integers of a Python sequence.
+std::vector<int32_t> ints(PyObject* o, const char* name) {
+    THPObjectPtr seq(PySequence_Fast(o, "a sequence of integers is expected"));
+    if (!seq) throw python_error();
+    std::vector<int32_t> v(PySequence_Fast_GET_SIZE(seq.get()));
+    for (size_t i = 0; i < v.size(); ++i) v[i] = to_int(PySequence_Fast_GET_ITEM(seq.get(), i), name);
+    return v;
+}
+// A contiguous tensor of these sizes.
+void* whole(const at::Tensor& t, at::IntArrayRef sizes, at::ScalarType dtype, at::Device device, const char* name) {
+    void* p = pointer(t, dtype, device, name);
+    TORCH_CHECK_VALUE(t.sizes() == sizes && t.is_contiguous(), name, " must be contiguous with shape ", sizes, ", has ", t.sizes());
+    return p;
+}
+
+// project_fp8(handle, d_in, d_out, rank, device, x8, x_scales, seg_offsets, seg_ids, W8, W_scales, A, B, scales, x, y, stream) -> y
+PyObject* project_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 17);
+    lora_linear* const handle = static_cast<lora_linear*>(given(a[0]) ? address(a[0]) : nullptr);
+    const int64_t d_in = to_int(a[1], "d_in"), d_out = to_int(a[2], "d_out"), rank = to_int(a[3], "rank");
+    const at::Device dev(at::kCUDA, (c10::DeviceIndex)to_int(a[4], "device"));
+    const at::Tensor& x8 = tensor(a[5], "x8");
+    TORCH_CHECK_VALUE(x8.dim() == 2 && x8.size(0) <= INT_MAX, "x8 must have shape [rows, d_in]");
+    const int64_t T = x8.size(0), groups = (d_in + 127) / 128;
+    const void* const x8p = whole(x8, {T, d_in}, kFp8, dev, "x8");
+    const void* const xsp = whole(tensor(a[6], "x_scales"), {T, groups}, at::kFloat, dev, "x_scales");
+    const std::vector<int32_t> off = ints(a[7], "seg_offsets"), ids = ints(a[8], "seg_ids");
+    TORCH_CHECK_VALUE(off.size() == ids.size() + 1, "seg_offsets must hold one more entry than seg_ids");
+    TORCH_CHECK_VALUE(off.back() == T, "seg_offsets must end at the number of rows");
+    const void* const w8p = whole(tensor(a[9], "W8"), {d_out, d_in}, kFp8, dev, "W8");
+    const void* const wsp = whole(tensor(a[10], "W_scales"), {(d_out + 127) / 128, groups}, at::kFloat, dev, "W_scales");
+    THPObjectPtr A(PySequence_Fast(a[11], "A must be a sequence")), B(A ? PySequence_Fast(a[12], "B must be a sequence") : nullptr);
+    THPObjectPtr S(B ? PySequence_Fast(a[13], "scales must be a sequence") : nullptr);
+    if (!S) throw python_error();
+    const Py_ssize_t na = PySequence_Fast_GET_SIZE(A.get());
+    TORCH_CHECK_VALUE(PySequence_Fast_GET_SIZE(B.get()) == na && PySequence_Fast_GET_SIZE(S.get()) == na,
+                      "A, B and scales must have one entry per adapter");
+    std::vector<const void*> ap(na), bp(na);
+    std::vector<float> scales(na);
+    for (Py_ssize_t i = 0; i < na; ++i) {
+        PyObject *ao = PySequence_Fast_GET_ITEM(A.get(), i), *bo = PySequence_Fast_GET_ITEM(B.get(), i);
+        if (given(ao)) ap[i] = whole(tensor(ao, "A"), {rank, d_in}, kBf16, dev, "A");
+        if (given(bo)) bp[i] = whole(tensor(bo, "B"), {d_out, rank}, kBf16, dev, "B");
+        scales[i] = (float)to_double(PySequence_Fast_GET_ITEM(S.get(), i));
+    }
+    const void* const xp = given(a[14]) ? whole(tensor(a[14], "x"), {T, d_in}, kBf16, dev, "x") : nullptr;
+    const OnStream stream(a[16], dev);
+    THPObjectPtr out(given(a[15]) ? same(a[15]) : THPVariable_Wrap(empty({T, d_out}, kBf16, dev)));
+    const at::Tensor& y = tensor(out.get(), "y");
+    void* const yp = whole(y, {T, d_out}, kBf16, dev, "y");
+    check(unlocked([&] {
+              return g_project(handle, x8p, static_cast<const float*>(xsp), xp, (int)T, off.data(), ids.data(), (int)ids.size(), w8p,
+                               static_cast<const float*>(wsp), ap.data(), bp.data(), scales.data(), (int)na, yp, stream.handle);
+          }),
+          "lora_linear_forward_fp8");
+    if (given(a[15])) wrote(y);
+    return out.release();
+    END_HANDLE_TH_ERRORS
+}
+
 // append(q, k, v, q_offsets, kv_lens, block_table, k_cache, v_cache, cos, sin, q_out, stream) -> q_out
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -475,6 +538,7 @@ PyMethodDef methods[] = {{"bind", fast<bind>(), METH_FASTCALL, nullptr},
                          {"activate", fast<activate>(), METH_FASTCALL, nullptr},
                          {"blocks", fast<blocks>(), METH_FASTCALL, nullptr},
                          {"score", fast<score>(), METH_FASTCALL, nullptr},
+                         {"project_fp8", fast<project_fp8>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

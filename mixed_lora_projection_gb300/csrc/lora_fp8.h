@@ -34,6 +34,7 @@ struct Fp8Params {
     int raster_group;                 // column tiles whose row groups run before the next column tiles
     int k_blocks;                     // ceil(d_in / 128)
     int k_lora;                       // ceil(rank / 64)
+    int lora_stages;                  // of an expand's block: all k_lora where the ring is long enough, else 1
     int d_out;
     int parts;                        // K parts of a unit (1 in the wide form)
     int a_rows;                       // rows of an A box: 128, or fewer (a multiple of 16) for a batch of one tile
@@ -44,7 +45,33 @@ struct Fp8Params {
     int debug_stall;
 };
 
+// The adapters' shrink ahead of it, U[t, :] = bf16(s_a X[t, :] A_a^T), for batches of few tiles: a tile's K is split over
+// the CTAs of a cluster, so that a few tiles find most SMs.
+constexpr int kShrinkThreads = 256;   // warp 0 TMA, 1 MMA, 2 owns TMEM, 4..7 epilogue
+struct ShrinkParams {
+    CUtensorMap inline_amaps[kInlineAdapters];   // A_a [rank, d_in] bf16, box 64 x n
+    Tile inline_tiles[kInlineTiles];
+    int32_t inline_seg[2 * kInlineSegs + 1];     // merged segments: offsets, then compact ids
+    float inline_scales[kInlineAdapters];
+    int inline_wl;
+    CUtensorMap tm_x;                 // X [T, d_in] bf16, box 64 x 128
+    const CUtensorMap* tm_a;          // device arrays (when not inline)
+    const Tile* tiles;
+    const int32_t* seg_off;
+    const int32_t* seg_id;
+    const float* scales;
+    void* u;                          // [u_rows, rank] bf16
+    int* status;
+    unsigned long long wait_limit_ns;
+    int n_tiles, n_seg, rank;
+    int n;                            // rank rounded up to 16
+    int k_steps;                      // ceil(d_in / 64)
+    int parts, stages, debug_stall;
+};
+
 // kernels_fp8.cu
+int shrink_stages(int n);
+cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream);
 size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages);
 int fp8_max_clusters(int tile_n, int parts);
 cudaError_t fp8_prepare_device();

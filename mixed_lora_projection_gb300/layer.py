@@ -47,7 +47,7 @@ def _load():
                            "(or python -m mixed_lora_projection_gb300.build)")
     _layer_bind.bind(*(C.cast(f, C.c_void_p).value for f in (
         lib.lora_linear_add_rms_norm, lib.lora_linear_kv_append, lib.lora_linear_attn_forward, lib.lora_linear_silu_mul,
-        lib.lora_linear_fp8_rows, lib.lora_linear_fp8_blocks, lib.lora_linear_token_logprobs)), _check)
+        lib.lora_linear_fp8_rows, lib.lora_linear_fp8_blocks, lib.lora_linear_token_logprobs, lib.lora_linear_forward_fp8)), _check)
     _bind = _layer_bind
     return _bind
 

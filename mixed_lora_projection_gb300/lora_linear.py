@@ -223,31 +223,10 @@ class LoraLinear:
         and 128 features: ``add_rms_norm_fp8``, ``silu_mul_fp8`` or ``fp8_rows`` with group 128), W8 e4m3 [d_out, d_in]
         with fp32 scales [ceil(d_out / 128), ceil(d_in / 128)] (``fp8_blocks``). The adapters stay bf16 and read the
         activations in bf16, ``x``, which may be None where no segment names one. d_in is a multiple of 16."""
-        T = x8.shape[0]
-        groups = -(-self.d_in // 128)
-        if y is None:
-            y = _empty((T, self.d_out), torch.bfloat16, self.device, stream)
-        for t, dtype, shape, name in ((x8, torch.float8_e4m3fn, (T, self.d_in), "x8"),
-                                      (x_scales, torch.float32, (T, groups), "x_scales"),
-                                      (W8, torch.float8_e4m3fn, (self.d_out, self.d_in), "W8"),
-                                      (W_scales, torch.float32, (-(-self.d_out // 128), groups), "W_scales"),
-                                      (x, torch.bfloat16, (T, self.d_in), "x"), (y, torch.bfloat16, (T, self.d_out), "y")):
-            if t is None and name == "x":
-                continue
-            if t.dtype != dtype:
-                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-            if tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
-                raise ValueError(f"{name} must be contiguous with shape {shape} on {self.device}")
-        off, _ = _i32(seg_offsets)
-        ids, n = _i32(seg_ids)
-        a_arr, b_arr, s_arr, na = self._adapters(A, B, scales)
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        rc = self._lib.lora_linear_forward_fp8(self._h, x8.data_ptr(), x_scales.data_ptr(),
-                                               x.data_ptr() if x is not None else None, T, off, ids, n, W8.data_ptr(),
-                                               W_scales.data_ptr(), a_arr, b_arr, s_arr, na, y.data_ptr(),
-                                               C.c_void_p(s.cuda_stream))
-        _check(rc, "lora_linear_forward_fp8")
-        return y
+        from . import layer
+        return (layer._bind or layer._load()).project_fp8(
+            self._h.value if self._h else None, self.d_in, self.d_out, self.rank, self.device.index, x8, x_scales, seg_offsets,
+            seg_ids, W8, W_scales, A, B, scales, x, y, stream)
 
     def forward_host_w4(self, x_host: torch.Tensor, seg_offsets, seg_ids, Wq: torch.Tensor, Ws: torch.Tensor, A, B,
                         scales, y_host: torch.Tensor, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
