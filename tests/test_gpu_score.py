@@ -179,3 +179,24 @@ def test_graph_and_streams():
     got = [token_logprobs(x, t, top=20, stream=s) for _ in range(20) for x, t, s in zip(xs, ts, streams)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for i, o in enumerate(got) for a, b in zip(o, want[i % 3]))
+
+
+# Blocks of four warps: a thread sums every 128th vector, V / 256 additions of pairs, so that the bounds above hold.
+@pytest.mark.parametrize("name", list(PATTERNS))
+@pytest.mark.parametrize("rows,vocab", [(611, 2003), (609, 20011)])
+def test_patterns_of_many_rows(name, rows, vocab):
+    g = gen(rows)
+    for dtype in (BF16, torch.float32):
+        x = PATTERNS[name](torch.randn(rows, vocab, generator=g, device="cuda")).to(dtype)
+        for top in (1, 20, 32):
+            check(x, torch.randint(vocab, (rows,), generator=g, device="cuda"), top)
+        check(x, torch.full((rows,), 11, device="cuda"), 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("rows,vocab", [(2047, 33001), (2048, 33001), (609, 32768), (609, 32769), (2500, 1), (2500, 1023)])
+def test_where_the_blocks_change(rows, vocab, dtype):
+    g = gen(vocab)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 3).to(dtype)
+    for top in (min(32, vocab), 0):
+        check(x, torch.randint(vocab, (rows,), generator=g, device="cuda"), top)
