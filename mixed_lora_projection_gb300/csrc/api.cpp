@@ -1621,7 +1621,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     // The shrink (bf16) is launched ahead: the bf16 kernel's units over rank tiles, or, where that finishes sooner, one
     // tile and one part of K a CTA (by the K steps' cycles that its units were measured at).
     Shape sh;
-    int rank_tiles = 1, parts = 0;
+    int rank_tiles = 1, parts = 0, shrink_n = 0;
     if (n_used) {
         sh = choose_shape(h, plan, false);
         sh.bk = 64;
@@ -1634,20 +1634,26 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         }
         sh.tile_n = sh.shrink_n;
         sh.stages = stages_for(sh.shrink_n / sh.cs, sh.bk);
-        const int steps = ceil_div(h->d_in, 64), n = ceil_div(h->rank, 16) * 16, tiles = (int)plan.shrink.size();
+        // (a call of 48 rows of 17,408 -> 5,120, rank 256: with 256 columns of the rank a CTA 40 us, with 32 38; of 6,144 24 and 23)
+        const int steps = ceil_div(h->d_in, 64), tiles = (int)plan.shrink.size(), whole = ceil_div(h->rank, 16) * 16;
         double best = (double)ceil_div((long long)sg * rank_tiles, slots) * steps * kstep_cycles(sh.cs, sh.shrink_n);
-        for (int q = 1; q <= std::min(kFp8MaxParts, steps); ++q) {
-            if (q > 1 && (tiles > h->fp8_clusters[1][q] || tiles * q > usable_sms(h))) continue;
-            const double t = (double)ceil_div(tiles, q > 1 ? tiles : usable_sms(h)) * ceil_div(steps, q) * kstep_cycles(1, n) + (q > 1 ? 4000 : 0);
-            if (t < best) {
-                best = t;
-                parts = q;
+        for (int n = whole; n >= 32 || n == whole; n = std::min(n - 16, ceil_div(n / 2, 16) * 16)) {
+            const int units = tiles * ceil_div(h->rank, n);
+            const double step = std::max((std::min(T, kTileM) + n) * 128.0 / 61.0, 4.0 * std::max(n / 2.0, 48.0) + 130.0);
+            for (int q = 1; q <= std::min(kFp8MaxParts, steps); ++q) {
+                if (q > 1 && (units > h->fp8_clusters[1][q] || units * q > usable_sms(h))) continue;
+                const double t = (double)ceil_div(units, q > 1 ? units : usable_sms(h)) * ceil_div(steps, q) * step + (q > 1 ? 4000 : 0);
+                if (t < best) {
+                    best = t;
+                    parts = q;
+                    shrink_n = n;
+                }
             }
         }
         if (parts) sh.shrink_groups = plan.shrink;
     }
     const int nst = n_used ? (int)sh.shrink_groups.size() : 0;
-    const int a_rows = parts ? ceil_div(h->rank, 16) * 16 : sh.shrink_n / sh.cs;   // of an A_a box
+    const int a_rows = parts ? shrink_n : sh.shrink_n / sh.cs;   // of an A_a box
     for (const Tile& t : groups)
         if (t.adapter < 0 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T ||
             (t.adapter && t.u_row != t.row0 && t.u_row != h->u_rows - kTileM))
@@ -1747,10 +1753,11 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         r.n_tiles = nst;
         r.n_seg = n_m;
         r.rank = h->rank;
-        r.n = a_rows;
+        r.n = shrink_n;
+        r.rank_tiles = ceil_div(h->rank, shrink_n);
         r.k_steps = ceil_div(h->d_in, 64);
         r.parts = parts;
-        r.stages = shrink_stages(a_rows);
+        r.stages = shrink_stages(shrink_n);
         r.debug_stall = h->debug_stall;
         if (launch_shrink(r, stream) != cudaSuccess) return LORA_ECUDA;
         ++h->launches;
@@ -1805,6 +1812,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.a_rows = s8.a_rows;
     q.stages = s8.stages;
     q.wide = s8.wide;
+    q.late_u = parts && inline_wl;                     // (a list that was copied is read after the wait)
     q.debug_stall = h->debug_stall;
     const int units = q.n_groups * q.n_ntiles;
     const int grid = s8.wide ? std::min(units, usable_sms(h) / 2) * 2 : s8.parts > 1 ? units * s8.parts : std::min(units, usable_sms(h));

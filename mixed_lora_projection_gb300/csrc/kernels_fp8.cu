@@ -221,7 +221,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     const uint64_t limit = p.wait_limit_ns;
     const Tile* tiles = p.inline_wl ? p.inline_tiles : p.tiles;
     const CUtensorMap* bmaps = p.inline_wl ? p.inline_bmaps : p.tm_b;
-    griddep_wait();
+    // Behind this call's own shrink, which began when the kernel before it had completed, the base runs beside the shrink:
+    // only the warp that loads U waits for it (rank 256, 48 rows of 5,120 -> 12,288 25 -> 19 us, 2,048 rows of 6,144 -> 5,120
+    // 93 -> 77, of 17,408 -> 5,120 220 -> 198).
+    if (!p.late_u) griddep_wait();
     griddep_launch_dependents();
 
     if (warp < 4) {
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     const uint32_t sa = smem_addr(a_ring + (size_t)stage * a_bytes), sb = smem_addr(b_ring + (size_t)stage * b_bytes);
                     const bool main = b < w.nk;
                     const int k = main ? (w.kb0 + b) * kFp8Group : (b - w.nk) * 64;
+                    if (!main && p.late_u) griddep_wait();
                     if (elect_one()) {
                         if (leader) mbar_arrive_expect_tx(bar, tx, 1u);
                         tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : w.tile.u_row, 1u);
@@ -333,7 +337,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             bool ok = true;
             for (int u = first; u < n_units && ok; u += step) {
                 const Work w = decode<CG, NT>(p, tiles, u, rank, part);
-                // (rows and columns past the unit's last take that one's)
+                // (rows and columns past the unit's last take that one's; read from L2, as TMA reads: nothing of an earlier launch's
+                // L1 is used where this one did not wait)
                 const float *xs[4], *ws[2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -344,10 +349,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     const int g = w.kb0 + b0;
                     auto take = [&](const float* s, float* v) {   // (past the last group: never used)
                         if (p.vec_scales && (g & 3) == 0 && g < G) {
-                            *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(s + g));
+                            *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(s + g));
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = __ldg(s + min(g + k, G - 1));
+                            for (int k = 0; k < 4; ++k) v[k] = __ldcg(s + min(g + k, G - 1));
                         }
                     };
                     float c[2][4], x[4][4];                  // four blocks' loads in flight
@@ -379,6 +384,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             }
         }
         __syncwarp();
+        if (p.late_u && warp == 0) griddep_wait();           // (this launch does not end before the shrink, whatever it met)
         if (CG == 1 && p.parts > 1) {
             cluster_sync();
             cluster_sync();
@@ -546,9 +552,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     }
 }
 
-// U[t, :] = bf16(s_a X[t, :] A_a^T) for one tile of 128 rows and one part of K a CTA, the parts of a tile a cluster: the
-// bf16 kernel's shrink units take a tile each, 272 K steps of it at d_in 17,408 (1,553 rows of rank 64 there 80 us; in 8
-// parts 12). Bound by the fill of shared memory, 61 bytes a cycle, or by a few rows' latency.
+// U[t, :] = bf16(s_a X[t, :] A_a^T) for one tile of 128 rows, n columns of the rank and one part of K a CTA, the parts of a
+// tile a cluster: the bf16 kernel's shrink units take a tile's whole K each, 272 K steps of it at d_in 17,408 (1,553 rows
+// of rank 64 there 80 us; in 8 parts 12). Bound by the fill of shared memory, 61 bytes a cycle and SM.
 __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -581,7 +587,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     griddep_wait();
     griddep_launch_dependents();
 
-    const Tile tile = (p.inline_wl ? p.inline_tiles : p.tiles)[blockIdx.x / p.parts];
+    const int unit = (int)blockIdx.x / p.parts, c0 = unit % p.rank_tiles * p.n, cols = min(p.n, p.rank - c0);
+    const Tile tile = (p.inline_wl ? p.inline_tiles : p.tiles)[unit / p.rank_tiles];
     const int k0 = part * p.k_steps / p.parts, nk = (part + 1) * p.k_steps / p.parts - k0;
     bool ok = true;
     if (warp == 0 && !p.debug_stall) {
@@ -598,7 +605,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar, a_bytes + b_bytes, 1u);
                 tma_load_2d<1>(smem_addr(a_ring + (size_t)stage * a_bytes), &p.tm_x, bar, (k0 + k) * 64, tile.row0, 1u);
-                tma_load_2d<1>(smem_addr(b_ring + (size_t)stage * b_bytes), am, bar, (k0 + k) * 64, 0, 1u);
+                tma_load_2d<1>(smem_addr(b_ring + (size_t)stage * b_bytes), am, bar, (k0 + k) * 64, c0, 1u);
             }
             __syncwarp();
             ++issued;
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
             const int32_t* seg_id = p.inline_wl ? p.inline_seg + p.n_seg + 1 : p.seg_id;
             const float s = mine && row_adapter(seg_off, seg_id, p.n_seg, row) == tile.adapter
                                 ? (p.inline_wl ? p.inline_scales : p.scales)[tile.adapter - 1] : 0.f;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.u) + (long long)row * p.rank;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.u) + (long long)row * p.rank + c0;
             for (int c = 0; c < p.n; c += 16) {
                 uint32_t v[16];
                 if (nk) tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
                 } else if (mine) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (c + 8 * i < p.rank)
+                        if (c + 8 * i < cols)
                             *reinterpret_cast<uint4*>(out + c + 8 * i) =
                                 make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
                                            pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
@@ -667,7 +674,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
         cluster_sync();
         if (warp >= 4 && ok) {
             // each CTA adds its share of the columns over the parts, in their order
-            const int v0 = part * (p.rank / 8) / p.parts, vecs = (part + 1) * (p.rank / 8) / p.parts - v0;
+            const int v0 = part * (cols / 8) / p.parts, vecs = (part + 1) * (cols / 8) / p.parts - v0;
             for (int i = (int)threadIdx.x - 128; i < tile.nrows * vecs; i += 128) {
                 const int r = i / vecs, c = 8 * (v0 + i - r * vecs);
                 const uint32_t at = smem_addr(base) + (uint32_t)(((c >> 2) * kTileM + r) * 16);
@@ -680,7 +687,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
                     s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
                     s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
                 }
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.u) + (long long)(tile.row0 + r) * p.rank + c) =
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.u) + (long long)(tile.row0 + r) * p.rank + c0 + c) =
                     make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
             }
         }
@@ -723,13 +730,13 @@ int shrink_stages(int n) {
 
 cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
     // the parts' sums take the rings' place
-    if (p.n < 16 || p.n > 256 || p.n % 16 || p.rank < 8 || p.rank > p.n || p.rank % 8 || p.parts < 1 || p.parts > kFp8MaxParts ||
+    if (p.n < 16 || p.n > 256 || p.n % 16 || p.rank < 8 || p.rank % 8 || p.rank_tiles != (p.rank + p.n - 1) / p.n || p.parts < 1 || p.parts > kFp8MaxParts ||
         p.parts > p.k_steps || p.n_tiles < 1 || p.stages < 2 || shrink_smem_bytes(p.n, p.stages) > (size_t)kSmemLimit ||
         (p.parts > 1 && (size_t)p.stages * (kTileM + p.n) * kFp8StageRow < (size_t)p.n * kTileM * 4))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3(p.n_tiles * p.parts);
+    cfg.gridDim = dim3(p.n_tiles * p.rank_tiles * p.parts);
     cfg.blockDim = dim3(kShrinkThreads);
     cfg.dynamicSmemBytes = shrink_smem_bytes(p.n, p.stages);
     cfg.stream = stream;

@@ -41,6 +41,7 @@ struct Fp8Params {
     int stages;
     int rows;                         // T
     int vec_scales;                   // both scales' rows are 16-byte aligned
+    int late_u;                       // launched beside the call's own shrink, which it waits for ahead of U alone
     int wide;                         // SM pairs, 256 x 256 blocks, persistent
     int debug_stall;
 };
@@ -64,7 +65,7 @@ struct ShrinkParams {
     int* status;
     unsigned long long wait_limit_ns;
     int n_tiles, n_seg, rank;
-    int n;                            // rank rounded up to 16
+    int n, rank_tiles;                // columns of a CTA, a multiple of 16; CTAs side by side
     int k_steps;                      // ceil(d_in / 64)
     int parts, stages, debug_stall;
 };
