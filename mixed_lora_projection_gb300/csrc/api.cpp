@@ -1530,18 +1530,23 @@ struct Fp8Shape {
 };
 
 // Three forms, each with one CTA (or pair) an SM: blocks of 128 x 128 and 128 x 256 on single CTAs, whose units a cluster
-// of up to eight CTAs may split by K where they would leave SMs idle, and of 256 x 256 on SM pairs. The one that the
-// units' waves times a block's measured time, per 128-wide K step, would finish first: 0.36 us at 128 columns, 0.61 at
-// 256, 0.54 on pairs, 2 us beside the blocks and 2 more where parts are joined. That picks the fastest or one within 8 %
-// of it on 28 of 30 batches timed (1 to 2,048 rows of the four projections): one row of 6,144 -> 5,120 in three parts of
-// 128 columns 10.7 us against 12.4 (256 columns, five parts), 48 rows of 5,120 -> 34,816 in 128 columns 32.6 against 33.8,
-// 348 rows of 5,120 -> 12,288 in 256 columns 28.4 against 31.0 and, on pairs, 45.1; 2,048 rows there on pairs 124 against 142.
+// of up to eight CTAs may split by K where they would leave SMs idle, and of 256 x 256 on SM pairs. The one that would end
+// first: the units' waves times a block's time, per 128-wide K step (0.28 us at 128 columns, 0.46 at 256, 0.43 on pairs),
+// or the weight at 6.5 TB/s, and 1.2 us and up to 5 for the sums of joined parts, by their size. On 44 batches timed (1 to
+// 2,048 rows of four projections) that picks the fastest or one within 3 %: one row of 6,144 -> 5,120 in three parts of 128
+// columns 10.8 us against 11.5 (256 columns, six parts), 128 rows there 13.4 against 17.3 (four), 48 rows of 5,120 ->
+// 12,288 in 128 columns 17.0 against 17.8 (256, two parts), 348 rows in 256 columns 24.0 against 27.5 and, on pairs, 40.6;
+// 2,048 rows there on pairs 113 against 120 (256 columns).
 Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
     const int nf = (int)plan.fused.size(), k_blocks = ceil_div(h->d_in, kFp8Group), sms = usable_sms(h);
     Fp8Shape s;
     double best = -1;
+    const double fetch = (double)h->d_in * h->d_out / 6.5e6;
+    int rows = 0;
+    for (const Tile& t : plan.fused) rows = std::max(rows, (int)t.nrows);
     auto weigh = [&](int wide, int tile_n, int parts, long long units, int slots, double block_us) {
-        const double t = (double)ceil_div(units, std::max(slots, 1)) * ceil_div(k_blocks, parts) * block_us + (parts > 1 ? 2.0 : 0.0);
+        const double join = parts > 1 ? 1.2 + 5.0 * rows / kTileM * tile_n / 256 : 0.0;
+        const double t = std::max((double)ceil_div(units, std::max(slots, 1)) * ceil_div(k_blocks, parts) * block_us, fetch) + join;
         if (best >= 0 && t >= best) return;
         best = t;
         s.wide = wide;
@@ -1550,13 +1555,13 @@ Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
     };
     for (int tile_n = 128; tile_n <= 256; tile_n += 128) {
         const long long units = (long long)nf * ceil_div(h->d_out, tile_n);
-        const double us = tile_n == 128 ? 0.36 : 0.61;
+        const double us = tile_n == 128 ? 0.28 : 0.46;
         weigh(0, tile_n, 1, units, sms, us);
         for (int parts = 2; parts <= std::min(kFp8MaxParts, k_blocks); ++parts)
             if (units <= h->fp8_clusters[tile_n / 256][parts] && units * parts <= sms) weigh(0, tile_n, parts, units, (int)units, us);
     }
     // (pairs: neighbouring tiles, less where two adapters meet; near enough for the choice)
-    if (nf >= 2 && sms >= 2) weigh(1, 256, 1, (long long)((nf + 1) / 2) * ceil_div(h->d_out, 256), sms / 2, 0.54);
+    if (nf >= 2 && sms >= 2) weigh(1, 256, 1, (long long)((nf + 1) / 2) * ceil_div(h->d_out, 256), sms / 2, 0.43);
     s.n_ntiles = ceil_div(h->d_out, s.tile_n);
     // pairs walk the column tiles in groups of up to 20, all rows of a group first (16,384 rows of 5,120 -> 5,120: groups of
     // 20 357 us, of 4 369; 4,144 of 5,120 -> 34,816: of 20 625, of 4 636, of all 136 664); single CTAs all rows of a column
