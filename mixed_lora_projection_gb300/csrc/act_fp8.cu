@@ -37,6 +37,11 @@ __device__ __forceinline__ float amax8(const float* f) {
     for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(f[k]));
     return m;
 }
+__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w) {   // of two bf16's magnitudes each; keeps a NaN
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w & 0x7fff7fffu));
+    return r;
+}
 // scale of a maximum, floored so that its reciprocal is finite and zeros are exact (as the norm's in 8 bits)
 __device__ __forceinline__ float scale_of(float amax) {
     const float s = amax * (1.0f / 448.f);
@@ -69,51 +74,61 @@ __device__ __forceinline__ void values8(const uint4& a, const uint4& b, float* y
     else unpack8(a, y);
 }
 
-// Scales by groups, or bf16 alone: a warp takes 32 vectors of a row (256 features, whole groups) at a time, four such
-// pieces in flight.
-template <bool GATE>
-__global__ void __launch_bounds__(256) act_groups_kernel(const __grid_constant__ ActParams p) {
+// Scales by groups, or bf16 alone: a warp takes pieces of 32 vectors of a row (256 features, whole groups), one where
+// there are few and N beside one another, all in flight, where there are many. No loop: as blocks end others begin, so
+// that loads and stores of an SM overlap (blocks that stayed and looped over their pieces: 4,001 rows of 17,408 to bf16
+// 67.2 us for 60.6, 1,601 rows of 5,120 to 8 bits 7.9 for 6.4). To bf16 bound by memory (4,001 rows: 6.9 TB/s), to 8 bits
+// by instructions beside it (5.1 to 5.5 TB/s).
+template <bool GATE, int N, int B>
+__global__ void __launch_bounds__(256, B) act_groups_kernel(const __grid_constant__ ActParams p) {
     dev::griddep_wait();
     dev::griddep_launch_dependents();
     const int nvec = p.width >> 3, per_row = (nvec + 31) >> 5, lane = threadIdx.x & 31;
-    const long long pieces = (long long)p.rows * per_row, warps = (long long)gridDim.x * 8;
     const int lanes = p.group >> 3, shift = p.group ? 31 - __clz(lanes) : 0, ng = p.group ? (nvec + lanes - 1) >> shift : 0;
-    constexpr int N = 4;
-    for (long long first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); first < pieces; first += N * warps) {
-        uint4 a[N], b[N];
-        long long row[N];
-        int c[N];
+    const long long first = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * N;
+    int row = first < (1ll << 31) ? (int)((uint32_t)first / (uint32_t)per_row) : (int)(first / per_row), at = (int)(first - (long long)row * per_row);
+    uint4 a[N], b[N];
+    int rows[N], c[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const long long piece = first + i * warps;
-            row[i] = piece / per_row;
-            c[i] = (int)(piece - row[i] * per_row) * 32 + lane;
-            if (piece >= pieces) c[i] = nvec;
-            a[i] = b[i] = make_uint4(0, 0, 0, 0);
-            if (c[i] < nvec) {
-                const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row[i] * p.x_stride;
-                a[i] = __ldcs(reinterpret_cast<const uint4*>(x) + c[i]);
-                if (GATE) b[i] = __ldcs(reinterpret_cast<const uint4*>(x + p.width) + c[i]);
-            }
+    for (int i = 0; i < N; ++i) {
+        rows[i] = row;
+        c[i] = row < p.rows ? at * 32 + lane : nvec;
+        a[i] = b[i] = make_uint4(0, 0, 0, 0);
+        if (c[i] < nvec) {
+            const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride;
+            a[i] = __ldcs(reinterpret_cast<const uint4*>(x) + c[i]);
+            if (GATE) b[i] = __ldcs(reinterpret_cast<const uint4*>(x + p.width) + c[i]);
         }
+        if (++at == per_row) {
+            at = 0;
+            ++row;
+        }
+    }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float y[8];
-            values8<GATE>(a[i], b[i], y);
-            if (p.y && c[i] < nvec) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + row[i] * p.y_stride)[c[i]] = pack8(y);
-            if (!p.q8) continue;
-            float m = amax8(y);
-            for (int o = lanes >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (c[i] < nvec) {
-                const float s = scale_of(m);
-                reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q8) + row[i] * p.q8_stride)[c[i]] = to_e4m3(y, __frcp_rn(s));
-                if ((c[i] & (lanes - 1)) == 0) p.scales[row[i] * ng + (c[i] >> shift)] = s;
-            }
+    for (int i = 0; i < N; ++i) {
+        if (rows[i] >= p.rows) break;
+        float y[8];
+        values8<GATE>(a[i], b[i], y);
+        if (p.y && c[i] < nvec) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + rows[i] * p.y_stride)[c[i]] = pack8(y);
+        if (!p.q8) continue;
+        float m;
+        if (GATE) {
+            m = amax8(y);
+        } else {                                           // (exact in bf16)
+            const uint32_t m2 = amax2(amax2(amax2(a[i].x & 0x7fff7fffu, a[i].y), a[i].z), a[i].w);
+            m = max_nan(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+        }
+        for (int o = lanes >> 1; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (c[i] < nvec) {
+            const float s = scale_of(m);
+            reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q8) + rows[i] * p.q8_stride)[c[i]] = to_e4m3(y, __frcp_rn(s));
+            if ((c[i] & (lanes - 1)) == 0) p.scales[(long long)rows[i] * ng + (c[i] >> shift)] = s;
         }
     }
 }
 
-// One scale a row: a block a row, which stays in registers between its maximum and its output.
+// One scale a row: a block a row, which stays in registers between its maximum and its output (4,001 rows of 17,408 gated
+// 62 us, 5.6 TB/s; 48 rows 3.0).
 template <bool GATE, int V>
 __global__ void __launch_bounds__(1024) act_rows_kernel(const __grid_constant__ ActParams p) {
     __shared__ float buf[32];
@@ -156,39 +171,39 @@ __global__ void __launch_bounds__(1024) act_rows_kernel(const __grid_constant__ 
     if (tid == 0) p.scales[row] = s;
 }
 
-// A weight's block of 128 x 128: 256 threads hold it (8 vectors each) between its maximum and its output.
-__global__ void __launch_bounds__(256) fp8_blocks_kernel(const __grid_constant__ BlocksParams p) {
-    __shared__ float buf[8];
+// A weight's block of 128 x 128: 256 threads hold it, eight vectors each, between its maximum and its output; four blocks an
+// SM. Bound by memory: 34,816 x 5,120 in 77.5 us, 6.9 TB/s. (With the maximum taken of unpacked values, 88 registers a
+// thread and two blocks an SM, 95.7; 512 threads of four vectors 81.4; five blocks, which spill, 86.7.)
+__global__ void __launch_bounds__(256, 4) fp8_blocks_kernel(const __grid_constant__ BlocksParams p) {
+    constexpr int V = 8, kWarps = 64 / V, kRows = 128 / V;   // rows apart of a thread's vectors
+    __shared__ float buf[kWarps];
     dev::griddep_wait();
     dev::griddep_launch_dependents();
     const int nc = (p.cols + 127) >> 7, br = (int)(blockIdx.x / nc), bc = (int)(blockIdx.x % nc);
     const int col = bc * 128 + (threadIdx.x & 15) * 8, r0 = br * 128 + (threadIdx.x >> 4);
-    uint4 v[8];
+    uint4 v[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
+    for (int i = 0; i < V; ++i) {
+        const int r = r0 + kRows * i;
         v[i] = make_uint4(0, 0, 0, 0);
         if (r < p.rows && col < p.cols)
             v[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w) + (long long)r * p.w_stride + col));
     }
-    float m = 0.f;
+    uint32_t m2 = 0;                                       // two features' maxima (exact in bf16)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float f[8];
-        unpack8(v[i], f);
-        m = max_nan(m, amax8(f));
-    }
+    for (int i = 0; i < V; ++i) m2 = amax2(amax2(amax2(amax2(m2, v[i].x), v[i].y), v[i].z), v[i].w);
+    float m = max_nan(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = buf[threadIdx.x & 7];
+    m = buf[threadIdx.x & (kWarps - 1)];
 #pragma unroll
-    for (int o = 4; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = kWarps / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float s = scale_of(m), inv = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
+    for (int i = 0; i < V; ++i) {
+        const int r = r0 + kRows * i;
         if (r >= p.rows || col >= p.cols) continue;
         float f[8];
         unpack8(v[i], f);
@@ -206,9 +221,13 @@ cudaError_t launch(const ActParams& p, cudaStream_t stream) {
         if (v == 2) return launch_chained(act_rows_kernel<GATE, 2>, p.rows, nt, 0, stream, p);
         return launch_chained(act_rows_kernel<GATE, 4>, p.rows, nt, 0, stream, p);
     }
-    // a warp a piece while there are few, at most eight blocks an SM
     const long long pieces = (long long)p.rows * ((nvec + 31) / 32);
-    return launch_chained(act_groups_kernel<GATE>, (unsigned)std::min<long long>((pieces + 7) / 8, 152 * 8), 256, 0, stream, p);
+    auto go = [&](auto kernel, int n) { return launch_chained(kernel, (unsigned)((pieces + 8 * n - 1) / (8 * n)), 256, 0, stream, p); };
+    // Pieces of a warp 1, 2 and 4, to 8 bits: 48 rows of 17,408 gated 2.2 us with one; 300 rows 7.2, 6.9, 8.0; 4,001 rows 71.7,
+    // 67.1, 63.7; 600 rows of 5,120 as they are 3.4, 3.8, 3.4; 1,601 rows 7.3, 6.4, 6.7; 16,384 rows of 6,144 74.0, 58.4, 56.1.
+    if (pieces <= 12000) return go(act_groups_kernel<GATE, 1, 8>, 1);
+    if (pieces <= 65536) return go(act_groups_kernel<GATE, 2, 5>, 2);
+    return go(act_groups_kernel<GATE, 4, 4>, 4);
 }
 
 }  // namespace
