@@ -117,4 +117,8 @@ def test_kernels_wait_before_they_let_the_next_one_begin(name):
     kernels = re.split(r"__global__", src)[1:]
     assert kernels
     for k in kernels:
-        assert re.findall(r"griddep_(wait|launch_dependents)\(\)", k) == ["wait", "launch_dependents"], name
+        order = re.findall(r"griddep_(wait|launch_dependents)\(\)", k)
+        assert order[:2] == ["wait", "launch_dependents"] and order.count("launch_dependents") == 1, name
+        # the projection behind its own shrink, which has waited for all before both, waits for it ahead of U and at its end
+        assert len(order) == (4 if "late_u" in k else 2), name
+        assert k.count("if (!p.late_u) griddep_wait();") == ("late_u" in k), name

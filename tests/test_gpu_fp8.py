@@ -228,3 +228,106 @@ def test_a_wait_that_runs_out_is_reported(T, ids):
     assert c.linear.status(reset=True) == _lib.LORA_ETIMEOUT
     c.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 4000000)
     assert torch.equal(c.run(), y) and c.linear.status() == 0
+
+
+# the shrink's rank in several tiles of columns, whole and not, one and more parts of K
+@pytest.mark.parametrize("d_in,d_out,rank,rows,ids", [
+    (5120, 264, 200, [48], [1]),
+    (17408, 136, 256, [33], [1]),
+    (6144, 264, 248, [130, 5], [1, 2]),
+    (5120, 136, 40, [300], [1]),
+    (4096, 136, 72, [16], [1]),
+    (5120, 1032, 256, [8, 8, 8, 340, 8], [0, 1, 2, 3, 4]),
+    (1024, 520, 136, [2, 1, 1, 600, 90], [1, 0, 2, 1, 3]),
+])
+def test_adapters_of_few_rows(d_in, d_out, rank, rows, ids):
+    c = Case(d_in, d_out, rank, rows, ids, seed=d_in + rank)
+    y = c.run()
+    c.check(y)
+    assert torch.equal(c.run(), y)
+
+
+@pytest.mark.parametrize("rows,ids", [([48], [1]), ([5, 343], [0, 1]), ([700], [1]), ([2048], [1]), ([8] * 70, [0, 1] * 35)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_operands_written_right_before(rows, ids, captured):
+    # the base runs beside the shrink and waits for it alone: what the norm before both has written is what it reads
+    from mixed_lora_projection_gb300 import add_rms_norm_fp8
+    if captured and len(rows) > 60:
+        pytest.skip("a work list of 70 segments is uploaded, which a capture refuses")
+    c = Case(1024, 1288, 64, rows, ids, seed=len(rows))
+    g = gen(5)
+    n = 12
+    hs = [torch.randn(c.T, c.d_in, generator=g, device="cuda").to(BF16) for _ in range(n)]
+    w = torch.rand(c.d_in, generator=g, device="cuda").to(BF16)
+    ys = [torch.empty(c.T, c.d_out, dtype=BF16, device="cuda") for _ in range(n)]
+
+    def both():
+        for h, y in zip(hs, ys):
+            add_rms_norm_fp8(h, w, group=128, out=c.x8, scales=c.xs, y_out=c.x)
+            c.run(y=y)
+
+    both()
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            both()
+        for y in ys:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+    for h, y in zip(hs, ys):
+        add_rms_norm_fp8(h, w, group=128, out=c.x8, scales=c.xs, y_out=c.x)
+        torch.cuda.synchronize()
+        assert torch.equal(c.run(), y)
+        torch.cuda.synchronize()
+    c.check(ys[-1])
+
+
+def test_fewer_sms_and_timing():
+    from mixed_lora_projection_gb300 import _lib
+    for rows, ids in (([48], [1]), ([300, 48], [1, 0]), ([1500], [1])):
+        c = Case(2048, 1288, 64, rows, ids, seed=len(rows))
+        for most in (2, 9, 40, 0):
+            c.linear.set_option(_lib.OPT_MAX_CTAS, most)
+            c.check(c.run())
+        c.linear.set_option(_lib.OPT_TIMING, 1)
+        c.check(c.run())
+
+
+def test_refused_arguments():
+    c = Case(256, 136, 16, [3, 4], [0, 1], seed=2)
+    good = dict(x8=c.x8, x_scales=c.xs, seg_offsets=c.off, seg_ids=c.ids, W8=c.w8, W_scales=c.ws, A=c.a, B=c.b, scales=c.s, x=c.x, y=None)
+    wide = torch.zeros(7, 512, device="cuda")
+
+    def refused(error, **bad):
+        with pytest.raises(error):
+            c.linear.forward_fp8(**{**good, **bad})
+
+    refused(TypeError, x8=c.x)
+    refused(TypeError, x_scales=c.xs.to(BF16))
+    refused(TypeError, W8=c.w8.view(torch.uint8))
+    refused(TypeError, x=c.x.float())
+    refused(TypeError, A=[c.a[0].float()])
+    refused(TypeError, y=torch.zeros(7, 136, device="cuda"))
+    refused(TypeError, seg_ids=None)
+    refused(ValueError, x8=wide.to(FP8)[:, :256])
+    refused(ValueError, x8=c.x8[0])
+    refused(ValueError, x_scales=c.xs[:, :1])
+    refused(ValueError, W_scales=c.ws[:1])
+    refused(ValueError, W8=c.w8[:128])
+    refused(ValueError, W8=c.w8.cpu())
+    refused(ValueError, x=c.x.cpu())
+    refused(ValueError, x=c.x[:6])
+    refused(ValueError, B=[c.b[0].T])
+    refused(ValueError, scales=[1.0, 2.0])
+    refused(ValueError, seg_offsets=[0, 3])
+    refused(ValueError, seg_offsets=[0, 3, 6])
+    refused(ValueError, y=torch.zeros(6, 136, dtype=BF16, device="cuda"))
+    refused(Exception, seg_ids=[0, 2])                       # no such adapter
+    refused(Exception, seg_offsets=[0, 8, 7])
+    refused(Exception, y=c.x8.view(BF16).view(-1)[:7 * 120].view(7, 120))
+    c.check(c.run())
+    c.linear.close()
+    with pytest.raises(Exception):
+        c.run()
