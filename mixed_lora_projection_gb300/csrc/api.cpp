@@ -1531,7 +1531,7 @@ struct Fp8Shape {
 
 // Three forms, each with one CTA (or pair) an SM: blocks of 128 x 128 and 128 x 256 on single CTAs, whose units a cluster
 // of up to eight CTAs may split by K where they would leave SMs idle, and of 256 x 256 on SM pairs. The one that would end
-// first: the units' waves times a block's time, per 128-wide K step (0.28 us at 128 columns, 0.46 at 256, 0.43 on pairs),
+// first: the units' waves times a block's time, per 128-wide K step (0.28 us at 128 columns, 0.46 at 256, 0.39 on pairs),
 // or the weight at 6.5 TB/s, and 1.2 us and up to 5 for the sums of joined parts, by their size. On 44 batches timed (1 to
 // 2,048 rows of four projections) that picks the fastest or one within 3 %: one row of 6,144 -> 5,120 in three parts of 128
 // columns 10.8 us against 11.5 (256 columns, six parts), 128 rows there 13.4 against 17.3 (four), 48 rows of 5,120 ->
@@ -1561,7 +1561,7 @@ Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
             if (units <= h->fp8_clusters[tile_n / 256][parts] && units * parts <= sms) weigh(0, tile_n, parts, units, (int)units, us);
     }
     // (pairs: neighbouring tiles, less where two adapters meet; near enough for the choice)
-    if (nf >= 2 && sms >= 2) weigh(1, 256, 1, (long long)((nf + 1) / 2) * ceil_div(h->d_out, 256), sms / 2, 0.43);
+    if (nf >= 2 && sms >= 2) weigh(1, 256, 1, (long long)((nf + 1) / 2) * ceil_div(h->d_out, 256), sms / 2, 0.39);
     s.n_ntiles = ceil_div(h->d_out, s.tile_n);
     // pairs walk the column tiles in groups of up to 20, all rows of a group first (16,384 rows of 5,120 -> 5,120: groups of
     // 20 357 us, of 4 369; 4,144 of 5,120 -> 34,816: of 20 625, of 4 636, of all 136 664); single CTAs all rows of a column
@@ -1685,7 +1685,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     auto maps = [&](CUtensorMap* b, CUtensorMap* a) {
         for (int k = 0; k < n_used; ++k) {
             const int i = plan.used_adapters[k];
-            if (encode_2d(h, &b[k], B[i], h->rank, h->d_out, 64, s8.tile_n / cg) != CUDA_SUCCESS ||
+            if (encode_2d(h, &b[k], B[i], h->rank, h->d_out, 64, s8.wide ? 64 : s8.tile_n) != CUDA_SUCCESS ||
                 encode_2d(h, &a[k], A[i], h->d_in, h->rank, 64, (uint32_t)a_rows) != CUDA_SUCCESS)
                 return false;
         }
@@ -1794,7 +1794,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     }
     if (timing) cudaEventRecord(rec.ev[1], stream);
     if (encode_u8_sw128(h, &q.tm_x, f.x8, h->d_in, T, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
-        encode_u8_sw128(h, &q.tm_w, f.w8, h->d_in, h->d_out, (uint32_t)(s8.tile_n / cg)) != CUDA_SUCCESS ||
+        encode_u8_sw128(h, &q.tm_w, f.w8, h->d_in, h->d_out, (uint32_t)(s8.wide ? 64 : s8.tile_n)) != CUDA_SUCCESS ||
         encode_2d(h, &q.tm_u, h->u_ws, h->rank, h->u_rows, 64, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_2d(h, &q.tm_y, y, h->d_out, T, s8.wide ? 64 : 32, 32) != CUDA_SUCCESS)
         return LORA_ECUDA;

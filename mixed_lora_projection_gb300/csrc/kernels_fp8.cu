@@ -14,6 +14,12 @@
 // MMAs that it issued, so one warp's waits run under the other's MMAs); warp 3 owns TMEM and lays the blocks'
 // scales out in shared memory; the others are the epilogue, two per TMEM lane quadrant, half of the columns each.
 //
+// What bounds it. Single CTAs: the fill of shared memory, 61 bytes a cycle (256 columns 48 KB a block, 0.42 us of the
+// measured 0.46; 128 columns 0.28) or the weight's bytes. Pairs: a buffer's round trip, ~1,600 cycles from the issue of its
+// MMAs over their end, the sums' reading and the release back to the issuer, of which four run at once: two buffers of
+// two halves of 128 columns (9,728 rows of 5,120 -> 5,120 177 us, 0.43 us a block, 2.9 PFLOP/s; whole buffers of 256
+// columns 197). Without the sums' reading 146, with a quarter of the MMAs besides 116.
+//
 // Every mbarrier wait is bounded by a wall-clock limit; a wait that runs out sets bit 0 of the status word and a
 // CTA-wide abort flag, and all roles leave their loops, wait (bounded) for their own copies and MMAs in flight,
 // free TMEM and return.
@@ -169,6 +175,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     constexpr int EW = 8;                              // epilogue warps
     constexpr int kCols = NT / 2;                      // columns of an epilogue thread
     constexpr int kBufs = 512 / NT, kSlots = 2 * kBufs;   // TMEM buffers, places of scales
+    constexpr int kHalves = CG, kHalf = NT / kHalves;  // a pair's columns in halves, each with its own MMAs and barriers:
+                                                       // a warp of one half's sums waits for no other's (one issuing warp a half
+                                                       // 195 us, both halves by the blocks' parity 177: file's head)
     constexpr int kYCols = CG > 1 ? 64 : 32;           // columns of a warp's part of the output at a time
     constexpr int kYStage = 64 * kYCols;               // its bytes
     static_assert(NT == 256 || (CG == 1 && NT == 128), "SM pairs run 256-column blocks");
@@ -186,8 +195,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     uint64_t* full = reinterpret_cast<uint64_t*>(slots + kSlots);
     uint64_t* empty = full + stages;
     uint64_t* tfull = empty + stages;
-    uint64_t* tempty = tfull + kBufs;
-    uint64_t* drain = tempty + kBufs;
+    uint64_t* tempty = tfull + kBufs * kHalves;
+    uint64_t* drain = tempty + kBufs * kHalves;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -204,9 +213,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             mbar_init(smem_addr(&full[s]), 1);
             mbar_init(smem_addr(&empty[s]), 1);
         }
-        for (int b = 0; b < kBufs; ++b) {
+        for (int b = 0; b < kBufs * kHalves; ++b) {          // (buffer by buffer)
             mbar_init(smem_addr(&tfull[b]), 2);              // the MMAs' commit, the scales
-            mbar_init(smem_addr(&tempty[b]), CG * EW);
+            mbar_init(smem_addr(&tempty[b]), CG * EW / kHalves);
         }
         mbar_init(smem_addr(drain), 2);
         *abort_flag = 0;
@@ -256,7 +265,12 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     if (elect_one()) {
                         if (leader) mbar_arrive_expect_tx(bar, tx, 1u);
                         tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : w.tile.u_row, 1u);
-                        tma_load_2d<CG>(sb, main ? &p.tm_w : bm, fb, k, w.n0 + rank * (NT / CG), 1u);
+                        if (CG == 1) {
+                            tma_load_2d<CG>(sb, main ? &p.tm_w : bm, fb, k, w.n0, 1u);
+                        } else {                             // a pair's CTA holds half of the columns of each half
+                            tma_load_2d<CG>(sb, main ? &p.tm_w : bm, fb, k, w.n0 + rank * (kHalf / CG), 1u);
+                            tma_load_2d<CG>(sb + kHalf / CG * kFp8StageRow, main ? &p.tm_w : bm, fb, k, w.n0 + kHalf + rank * (kHalf / CG), 1u);
+                        }
                     }
                     __syncwarp();
                     ++issued;
@@ -276,7 +290,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             }
         } else if ((warp == 1 || warp == 2) && leader) {
             // ------------------------------------------------------------ MMA issuers
-            const uint32_t idesc8 = instr_desc_e4m3(kTileM * CG, NT), idesc16 = instr_desc_bf16(kTileM * CG, NT);
+            const uint32_t idesc8 = instr_desc_e4m3(kTileM * CG, kHalf), idesc16 = instr_desc_bf16(kTileM * CG, kHalf);
+            constexpr uint64_t kHalfDesc = kHalf / CG * kFp8StageRow / 16;   // from one half's rows of B to the other's
             const int mine = warp - 1;                       // parity of the blocks this warp issues
             int stage = 0, blk = 0;
             uint32_t phase = 0;
@@ -292,30 +307,41 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                         // one a lap before, where a lap is longer than the stages of the blocks since (launch_fp8).
                         const int buf = blk % kBufs;
                         const uint32_t d = tmem_base + (uint32_t)(buf * NT);
-                        ok = wait_all(smem_addr(&tempty[buf]), ((blk / kBufs) & 1) ^ 1, abort_flag, p.status, limit);
+                        const uint32_t free = ((blk / kBufs) & 1) ^ 1;
+                        ok = wait_all(smem_addr(&tempty[buf * kHalves]), free, abort_flag, p.status, limit);
                         for (int s = 0; s < ns && ok; ++s) {
                             ok = wait_all(smem_addr(&full[stage]), phase, abort_flag, p.status, limit);
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
                             const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
-                            // 32 bytes along K inside the swizzled rows a step
-                            // (one elected lane, in a branch of its own: 4 MMAs issue in ~100 cycles; under a predicate that
-                            // the compiler cannot tell to be one lane's, in ~550)
-                            if (elect_one()) {
-                                if (main) {
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        mma_e4m3<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc8, k > 0 ? 1u : 0u, 1u);
-                                } else {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        mma_bf16<CG>(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc16, (s > 0 || k > 0) ? 1u : 0u, 1u);
+                            for (int h = 0; h < kHalves; ++h) {
+                                if (h > 0 && s == 0) {
+                                    ok = wait_all(smem_addr(&tempty[buf * kHalves + h]), free, abort_flag, p.status, limit);
+                                    if (!ok) break;
+                                    tc_fence_after();
                                 }
-                                if (s == ns - 1) mma_commit<CG>(smem_addr(&tfull[buf]), 1u);
-                                mma_commit<CG>(smem_addr(&empty[stage]), 1u);
+                                // 32 bytes along K inside the swizzled rows a step
+                                // (one elected lane, in a branch of its own: 4 MMAs issue in ~100 cycles; under a predicate
+                                // that the compiler cannot tell to be one lane's, in ~550)
+                                if (elect_one()) {
+                                    const uint64_t hd = bd + h * kHalfDesc;
+                                    if (main) {
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k)
+                                            mma_e4m3<CG>(d + h * kHalf, ad + (uint64_t)(2 * k), hd + (uint64_t)(2 * k), idesc8, k > 0 ? 1u : 0u, 1u);
+                                    } else {
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k)
+                                            mma_bf16<CG>(d + h * kHalf, ad + (uint64_t)(2 * k), hd + (uint64_t)(2 * k), idesc16, (s > 0 || k > 0) ? 1u : 0u, 1u);
+                                    }
+                                    if (s == ns - 1) mma_commit<CG>(smem_addr(&tfull[buf * kHalves + h]), 1u);
+                                    if (h == kHalves - 1) mma_commit<CG>(smem_addr(&empty[stage]), 1u);
+                                }
+                                __syncwarp();
                             }
-                            __syncwarp();
+                            if (!ok) break;
                             if (++stage == stages) { stage = 0; phase ^= 1; }
                         }
                         if (!ok) break;
@@ -366,10 +392,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                         // Block blk - kBufs's sums are there: its MMAs began when the epilogue had read block blk - 2 kBufs,
                         // its scales with it. And blk's phase of the barrier has begun.
                         const int buf = blk % kBufs;
-                        if (blk >= kBufs && !wait_all(smem_addr(&tfull[buf]), (blk / kBufs - 1) & 1, abort_flag, p.status, limit)) {
-                            ok = false;
-                            break;
-                        }
+#pragma unroll
+                        for (int h = 0; h < kHalves && ok; ++h)
+                            if (blk >= kBufs) ok = wait_all(smem_addr(&tfull[buf * kHalves + h]), (blk / kBufs - 1) & 1, abort_flag, p.status, limit);
+                        if (!ok) break;
                         ScaleSlot& slot = slots[blk % kSlots];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -377,7 +403,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                             for (int h = 0; h < 2; ++h) slot.f[h][lane + 32 * i] = b0 + k < w.nk ? x[i][k] * c[h][k] : 1.f;
                         if (lane == 0) slot.unit = make_int4(w.tile.row0, w.tile.nrows, w.n0, w.nb);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&tfull[buf]));
+                        if (lane < kHalves) mbar_arrive(smem_addr(&tfull[buf * kHalves + lane]));
                         ++blk;
                     }
                 }
@@ -397,7 +423,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
         const uint32_t t0 = tmem_base + (uint32_t)(cg * kCols) + ((uint32_t)(q * 32) << 16);
         uint8_t* const mine = y_stage + (warp - 4) * kYStage;
         const uint32_t my_scale = smem_addr(&slots[0].f[cg][r_local]);
-        const uint32_t tfull0 = smem_addr(tfull), tempty0 = CG > 1 ? map_to_rank(smem_addr(tempty), 0) : smem_addr(tempty);
+        const int half = kHalves > 1 ? cg : 0;               // of the block's columns: this warp's barriers
+        const uint32_t tfull0 = smem_addr(tfull + half);
+        const uint32_t tempty0 = CG > 1 ? map_to_rank(smem_addr(tempty + half), 0) : smem_addr(tempty + half);
         uint32_t buf = 0, phase = 0, place = 0;
         bool ok = true;
         uint64_t acc[kCols / 2];
@@ -407,7 +435,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             int row0 = 0, nrows = 0, n0 = 0, nb = 1;
 #pragma unroll 1
             for (int b = 0; b < nb; ++b) {
-                if (!wait_all(tfull0 + 8 * buf, phase, abort_flag, p.status, limit)) {
+                if (!wait_all(tfull0 + 8 * kHalves * buf, phase, abort_flag, p.status, limit)) {
                     ok = false;
                     break;
                 }
@@ -428,8 +456,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            if (CG > 1) arrive_relaxed(tempty0 + 8 * buf);
-                            else mbar_arrive(tempty0 + 8 * buf);
+                            if (CG > 1) arrive_relaxed(tempty0 + 8 * kHalves * buf);
+                            else mbar_arrive(tempty0 + 8 * kHalves * buf);
                         }
                     };
                     if (CG == 1 && q * 32 >= nrows) {        // no row of the unit's lies here
@@ -707,7 +735,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
 
 namespace {
 // 384 threads of 168 registers, dealt out anew: 72 x 128 + 216 x 256 = 168 x 384. A few bytes spilled in the loading warps
-// cost a tenth to a fifth of all (pairs, 9,728 rows of 5,120 -> 5,120: 198 us; with 64 and 216, 40 bytes, 223).
+// cost a tenth to a fifth of all (pairs with buffers of 256 columns, 9,728 rows of 5,120 -> 5,120: 198 us; with 64 and 216,
+// 40 bytes, 223).
 constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 72, 216>;
 constexpr auto kSingle = dev::lora_fp8_kernel<1, 256, 72, 216>;
 constexpr auto kNarrow = dev::lora_fp8_kernel<1, 128, 72, 216>;
@@ -716,7 +745,7 @@ inline auto kernel_of(int wide, int tile_n) { return wide ? kWide : tile_n == 25
 
 size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages) {
     return 1024 + (size_t)stages * (a_rows + tile_n / (wide ? 2 : 1)) * kFp8StageRow + 8 * 64 * (wide ? 64 : 32) +
-           2 * (512 / tile_n) * sizeof(dev::ScaleSlot) + 8 * (2 * (size_t)stages + 2 * 512 / tile_n + 1) + 16;
+           2 * (512 / tile_n) * sizeof(dev::ScaleSlot) + 8 * (2 * (size_t)stages + 2 * 4 + 1) + 16;
 }
 
 static size_t shrink_smem_bytes(int n, int stages) {

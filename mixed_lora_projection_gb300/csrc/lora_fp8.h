@@ -19,7 +19,7 @@ struct Fp8Params {
     Tile inline_tiles[kInlineTiles];
     int inline_wl;
     CUtensorMap tm_x;                 // X [T, d_in] e4m3, box 128 x a_rows, 128-byte swizzle
-    CUtensorMap tm_w;                 // W [d_out, d_in] e4m3, box 128 x tile_n / CTAs of the group
+    CUtensorMap tm_w;                 // W [d_out, d_in] e4m3, box 128 x tile_n, on pairs 128 x 64
     CUtensorMap tm_u;                 // U [u_rows, rank] bf16, box 64 x a_rows
     CUtensorMap tm_y;                 // Y [T, d_out] bf16, box 64 x 32, 128-byte swizzle; single CTAs 32 x 32, 64-byte
     const CUtensorMap* tm_b;          // device array per compact adapter (when not inline)
