@@ -18,7 +18,7 @@
 // measured 0.46; 128 columns 0.28) or the weight's bytes. Pairs: a buffer's round trip, ~1,600 cycles from the issue of its
 // MMAs over their end, the sums' reading and the release back to the issuer, of which four run at once: two buffers of
 // two halves of 128 columns (9,728 rows of 5,120 -> 5,120 177 us, 0.43 us a block, 2.9 PFLOP/s; whole buffers of 256
-// columns 197). Without the sums' reading 146, with a quarter of the MMAs besides 116.
+// columns 197). Without the sums' reading 158.
 //
 // Every mbarrier wait is bounded by a wall-clock limit; a wait that runs out sets bit 0 of the status word and a
 // CTA-wide abort flag, and all roles leave their loops, wait (bounded) for their own copies and MMAs in flight,

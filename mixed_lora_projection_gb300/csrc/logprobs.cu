@@ -16,8 +16,8 @@
 //
 // 2-byte logits at the copy rate leave 11 lane instructions and 1.4 exponentials' time an entry; bound by the
 // instructions (nine an entry, thirteen with alternatives; 68 and 72 % of the issue slots used). 4,096 rows of 100,003 in
-// bf16: 161 us (5.1 TB/s), with 20 alternatives 213; 2,048 rows of 131,072 in fp32 168 (6.4 TB/s) and 208. Collecting by
-// a ballot and a shared count took 238 of those 213 us. Loads through shared memory (cp.async, four deep, in place of the
+// bf16: 156 us (5.3 TB/s), with 20 alternatives 209; 2,048 rows of 131,072 in fp32 168 (6.4 TB/s) and 208. Collecting by
+// a ballot and a shared count took 238 of those 209 us. Loads through shared memory (cp.async, four deep, in place of the
 // next iteration's in registers) took 248 and, in fp32, 264 for 168.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -350,6 +350,9 @@ struct Pass {
     }
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 template <typename T, bool TOP, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) token_logprobs_kernel(const __grid_constant__ ScoreParams p) {
     constexpr int kThreads = 32 * WARPS;
@@ -361,13 +364,35 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) token_logprobs_kernel(
     const long long row = blockIdx.x / parts;
     if (tid < 32) sh.list[tid] = 0;
     if (tid == 0) sh.pooled = 0;
-    if (tid < WARPS) {
-        sh.bound[tid] = -INFINITY;
-    }
+    if (tid < WARPS) sh.bound[tid] = -INFINITY;
     dev::griddep_wait();
     dev::griddep_launch_dependents();
 
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
+    // Entries [0, head) before the row's first 16-byte boundary, then vectors of 8, then the rest.
+    const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T), p.vocab);
+    const int n_vec = (p.vocab - head) >> 3, tail = head + 8 * n_vec;
+    const int v0 = (int)((long long)n_vec * part / parts), v1 = (int)((long long)n_vec * (part + 1) / parts);
+    const T* xv = x + head;
+    // (few rows: a thread's loads of one iteration would wait for the last one's, a memory's latency each)
+    if (WARPS == 8 && parts > 1 && tid == 0 && v1 > v0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(xv + 8ll * v0), "r"((uint32_t)min((long long)(v1 - v0) * 8 * (int)sizeof(T), 1ll << 18)) : "memory");
+
+    // Two vectors an iteration, the next two in flight; a vector that is not there is one of -inf.
+    Vec<T> u0, u1;
+    auto load = [&](int at) {
+        if (at - tid + 2 * kThreads <= v1) {                   // (all of the CTA's)
+            u0.load(xv + 8ll * at);
+            u1.load(xv + 8ll * (at + kThreads));
+            return;
+        }
+        u0.none();
+        u1.none();
+        if (at < v1) u0.load(xv + 8ll * at);
+        if (at + kThreads < v1) u1.load(xv + 8ll * (at + kThreads));
+    };
+    int at = v0 + tid;
+    load(at);
     long long token = -1;
     if (p.tokens) token = p.tokens64 ? static_cast<const long long*>(p.tokens)[row] : static_cast<const int32_t*>(p.tokens)[row];
     const bool given = token >= 0 && token < p.vocab;
@@ -385,28 +410,6 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) token_logprobs_kernel(
     me.own = 0;
     me.waiting = 0;
     const int share = TOP ? (p.top + WARPS - 1) / WARPS : 1;
-
-    // Entries [0, head) before the row's first 16-byte boundary, then vectors of 8, then the rest.
-    const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T), p.vocab);
-    const int n_vec = (p.vocab - head) >> 3, tail = head + 8 * n_vec;
-    const int v0 = (int)((long long)n_vec * part / parts), v1 = (int)((long long)n_vec * (part + 1) / parts);
-    const T* xv = x + head;
-
-    // Two vectors an iteration, the next two in flight; a vector that is not there is one of -inf.
-    Vec<T> u0, u1;
-    auto load = [&](int at) {
-        if (at - tid + 2 * kThreads <= v1) {                   // (all of the CTA's)
-            u0.load(xv + 8ll * at);
-            u1.load(xv + 8ll * (at + kThreads));
-            return;
-        }
-        u0.none();
-        u1.none();
-        if (at < v1) u0.load(xv + 8ll * at);
-        if (at + kThreads < v1) u1.load(xv + 8ll * (at + kThreads));
-    };
-    int at = v0 + tid;
-    load(at);
     if (TOP) {
         // The CTA's bound from its first vectors: `share` lanes of every warp have an entry as large.
         float f[8];
@@ -463,14 +466,17 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) token_logprobs_kernel(
     // the warp's sums, then the block's, then the cluster's
     Sums a = me.sums();
     int ahead = me.ahead;
+    auto reduce = [&](int lanes) {
 #pragma unroll 1
-    for (int o = 16; o; o >>= 1) {
-        const Sums b = {__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.s, o), __shfl_xor_sync(kAll, a.w, o)};
-        // (the lower lane's first in both, so that both have the same bits)
-        const bool upper = lane & o;
-        a = join(upper ? b : a, upper ? a : b, me.c);
-        ahead += __shfl_xor_sync(kAll, ahead, o);
-    }
+        for (int o = lanes >> 1; o; o >>= 1) {
+            const Sums b = {__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.s, o), __shfl_xor_sync(kAll, a.w, o)};
+            // (the lower lane's first in both, so that both have the same bits)
+            const bool upper = lane & o;
+            a = join(upper ? b : a, upper ? a : b, me.c);
+            ahead += __shfl_xor_sync(kAll, ahead, o);
+        }
+    };
+    reduce(32);
     if (lane == 0) sh.part[warp] = Part{a, ahead};
     if (TOP) {
         // the warp's last bound, and what it leaves of the entries that wait, at most 32 of a warp, to the pool
@@ -500,13 +506,12 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) token_logprobs_kernel(
         choose(sh, p.top);
     }
     __syncthreads();
-    if (warp == 0) {
-#pragma unroll 1
-        for (int i = 1; i < WARPS; ++i) {
-            a = join(a, sh.part[i].sums, me.c);
-            ahead += sh.part[i].ahead;
-        }
-    }
+    auto take = [&](int n) {                                   // the first n parts', every lane the same
+        a = sh.part[lane & (n - 1)].sums;
+        ahead = sh.part[lane & (n - 1)].ahead;
+        reduce(n);
+    };
+    if (warp == 0) take(WARPS);
     if (WARPS == 8 && parts > 1) {
         if (tid == 0) sh.cta_part = Part{a, ahead};
         dev::cluster_sync();
@@ -535,23 +540,23 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) token_logprobs_kernel(
                 uint64_t floor = 0;
                 for (int i = 0; i < parts; ++i) floor = max(floor, sh.pending[0][i]);
                 clear(sh);
+                cluster_arrive();                              // (the parts have been read)
                 bring(sh, lane < p.top && key >= floor ? key : 0);
                 choose(sh, p.top);
             } else {
                 __syncthreads();
+                cluster_arrive();
             }
-            if (warp == 0) {
-#pragma unroll 1
-                for (int i = 1; i < parts; ++i) {
-                    a = join(a, sh.part[i].sums, me.c);
-                    ahead += sh.part[i].ahead;
-                }
-            }
+            if (warp == 0) take(parts);
             __syncthreads();
+        } else {
+            cluster_arrive();
         }
-        dev::cluster_sync();                                   // the parts have been read
     }
-    if (part != 0 || warp != 0) return;
+    if (part != 0 || warp != 0) {
+        if (WARPS == 8 && parts > 1) cluster_wait();           // until the first part has read this one's
+        return;
+    }
     const float log_s = logf(a.s);                             // (a row of -inf alone: log 0)
     auto lp = [&](float v) { return v == -INFINITY && a.s == a.s ? v : (v - from(a.m)) * p.inv_temperature - log_s; };
     if (lane == 0) {
@@ -564,6 +569,8 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) token_logprobs_kernel(
         p.top_logprobs[row * p.top + lane] = lp(key_value(key));
         p.top_tokens[row * p.top + lane] = key_index(key);
     }
+    __syncwarp();
+    if (WARPS == 8 && parts > 1) cluster_wait();
 }
 
 }  // namespace
