@@ -18,11 +18,13 @@ from .synth import WORKLOADS, Workload, make_inputs  # noqa: F401
 
 
 def __getattr__(name):
+    # (once a name: a call of a decode step takes a few microseconds, a look-up through here more than one)
     if name in ("LoraLinear", "plan", "LoraError", "validate", "w4_repack", "launch_shape", "host_chunks", "k_split"):
-        from . import lora_linear as _ll
-        return getattr(_ll, name)
-    if name in ("add_rms_norm", "add_rms_norm_fp8", "kv_append", "PagedAttention", "silu_mul", "silu_mul_fp8", "fp8_rows",
-                "fp8_blocks", "token_logprobs", "TokenLogprobs"):
-        from . import layer as _layer
-        return getattr(_layer, name)
-    raise AttributeError(name)
+        from . import lora_linear as module
+    elif name in ("add_rms_norm", "add_rms_norm_fp8", "kv_append", "PagedAttention", "silu_mul", "silu_mul_fp8", "fp8_rows",
+                  "fp8_blocks", "token_logprobs", "TokenLogprobs"):
+        from . import layer as module
+    else:
+        raise AttributeError(name)
+    globals()[name] = value = getattr(module, name)
+    return value

@@ -385,12 +385,16 @@ PyObject* score(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// Integers of a Python sequence.
+// A sequence's items, held while they are read: an item's conversion may run Python code that changes a list.
+THPObjectPtr items(PyObject* o) {
+    THPObjectPtr t(PySequence_Tuple(o));
+    if (!t) throw python_error();
+    return t;
+}
 std::vector<int32_t> ints(PyObject* o, const char* name) {
-    THPObjectPtr seq(PySequence_Fast(o, "a sequence of integers is expected"));
-    if (!seq) throw python_error();
-    std::vector<int32_t> v(PySequence_Fast_GET_SIZE(seq.get()));
-    for (size_t i = 0; i < v.size(); ++i) v[i] = to_int(PySequence_Fast_GET_ITEM(seq.get(), i), name);
+    const THPObjectPtr seq = items(o);
+    std::vector<int32_t> v(PyTuple_GET_SIZE(seq.get()));
+    for (size_t i = 0; i < v.size(); ++i) v[i] = to_int(PyTuple_GET_ITEM(seq.get(), i), name);
     return v;
 }
 // A contiguous tensor of these sizes.
@@ -417,19 +421,17 @@ PyObject* project_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(off.back() == T, "seg_offsets must end at the number of rows");
     const void* const w8p = whole(tensor(a[9], "W8"), {d_out, d_in}, kFp8, dev, "W8");
     const void* const wsp = whole(tensor(a[10], "W_scales"), {(d_out + 127) / 128, groups}, at::kFloat, dev, "W_scales");
-    THPObjectPtr A(PySequence_Fast(a[11], "A must be a sequence")), B(A ? PySequence_Fast(a[12], "B must be a sequence") : nullptr);
-    THPObjectPtr S(B ? PySequence_Fast(a[13], "scales must be a sequence") : nullptr);
-    if (!S) throw python_error();
-    const Py_ssize_t na = PySequence_Fast_GET_SIZE(A.get());
-    TORCH_CHECK_VALUE(PySequence_Fast_GET_SIZE(B.get()) == na && PySequence_Fast_GET_SIZE(S.get()) == na,
+    const THPObjectPtr A = items(a[11]), B = items(a[12]), S = items(a[13]);
+    const Py_ssize_t na = PyTuple_GET_SIZE(A.get());
+    TORCH_CHECK_VALUE(PyTuple_GET_SIZE(B.get()) == na && PyTuple_GET_SIZE(S.get()) == na,
                       "A, B and scales must have one entry per adapter");
     std::vector<const void*> ap(na), bp(na);
     std::vector<float> scales(na);
     for (Py_ssize_t i = 0; i < na; ++i) {
-        PyObject *ao = PySequence_Fast_GET_ITEM(A.get(), i), *bo = PySequence_Fast_GET_ITEM(B.get(), i);
+        PyObject *ao = PyTuple_GET_ITEM(A.get(), i), *bo = PyTuple_GET_ITEM(B.get(), i);
         if (given(ao)) ap[i] = whole(tensor(ao, "A"), {rank, d_in}, kBf16, dev, "A");
         if (given(bo)) bp[i] = whole(tensor(bo, "B"), {d_out, rank}, kBf16, dev, "B");
-        scales[i] = (float)to_double(PySequence_Fast_GET_ITEM(S.get(), i));
+        scales[i] = (float)to_double(PyTuple_GET_ITEM(S.get(), i));
     }
     const void* const xp = given(a[14]) ? whole(tensor(a[14], "x"), {T, d_in}, kBf16, dev, "x") : nullptr;
     const OnStream stream(a[16], dev);

@@ -134,6 +134,16 @@ def w4_repack(src: torch.Tensor, dst: torch.Tensor | None = None,
     return dst
 
 
+_project_fp8 = None            # the native binding's, once it is loaded
+
+
+def _load_project_fp8():
+    global _project_fp8
+    from . import layer
+    _project_fp8 = (layer._bind or layer._load()).project_fp8
+    return _project_fp8
+
+
 class LoraLinear:
     """One handle: a projection shape (d_in -> d_out, rank r) on one CUDA device."""
 
@@ -223,8 +233,7 @@ class LoraLinear:
         and 128 features: ``add_rms_norm_fp8``, ``silu_mul_fp8`` or ``fp8_rows`` with group 128), W8 e4m3 [d_out, d_in]
         with fp32 scales [ceil(d_out / 128), ceil(d_in / 128)] (``fp8_blocks``). The adapters stay bf16 and read the
         activations in bf16, ``x``, which may be None where no segment names one. d_in is a multiple of 16."""
-        from . import layer
-        return (layer._bind or layer._load()).project_fp8(
+        return (_project_fp8 or _load_project_fp8())(
             self._h.value if self._h else None, self.d_in, self.d_out, self.rank, self.device.index, x8, x_scales, seg_offsets,
             seg_ids, W8, W_scales, A, B, scales, x, y, stream)
 
