@@ -67,6 +67,7 @@ struct lora_linear {
     int device = 0, d_in = 0, d_out = 0, rank = 0, max_tokens = 0, max_segments = 0;
     int num_sms = 0;
     void* u_ws = nullptr;       // bf16 [u_rows, rank]: shrink output, read by the fused pass
+    void* u_pairs = nullptr;    // bf16 [(kFp8Expands + 1) 128, rank]: the 8-bit kernel's, by tile and adapter; the last block zero
     int u_rows = 0;
     int* status = nullptr;      // device status word
     int* flags = nullptr;       // per fused tile: U rows ready (1) in the running launch; then the
@@ -140,6 +141,7 @@ void free_handle(lora_linear* h) {
         for (cudaEvent_t e : r.ev) h->ev_pool.push_back(e);
     for (cudaEvent_t e : h->ev_pool) cudaEventDestroy(e);
     if (h->u_ws) cudaFree(h->u_ws);
+    if (h->u_pairs) cudaFree(h->u_pairs);
     if (h->partials) cudaFree(h->partials);
     if (h->split_ctr) cudaFree(h->split_ctr);
     if (h->w4_partials) cudaFree(h->w4_partials);
@@ -879,6 +881,7 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
                     align_up((size_t)max_segments * sizeof(CUtensorMap), 128) +
                     (size_t)(h->max_fused / 2 + 1) * sizeof(W4Group) + 256;
     if (cudaMalloc(&h->u_ws, (size_t)h->u_rows * rank * 2) != cudaSuccess ||
+        cudaMalloc(&h->u_pairs, (size_t)(kFp8Expands + 1) * kTileM * rank * 2) != cudaSuccess ||
         cudaMalloc((void**)&h->status, sizeof(int)) != cudaSuccess ||
         cudaMalloc((void**)&h->flags, sizeof(int) * ((size_t)h->max_fused + 1)) != cudaSuccess ||
         cudaHostAlloc((void**)&h->status_host, sizeof(int), cudaHostAllocDefault) != cudaSuccess) {
@@ -909,7 +912,8 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
     }
     if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess ||
         cudaMemset(h->flags, 0, sizeof(int) * ((size_t)h->max_fused + 1)) != cudaSuccess ||
-        cudaMemset(h->u_ws, 0, (size_t)h->u_rows * rank * 2) != cudaSuccess) {
+        cudaMemset(h->u_ws, 0, (size_t)h->u_rows * rank * 2) != cudaSuccess ||
+        cudaMemset(h->u_pairs, 0, (size_t)(kFp8Expands + 1) * kTileM * rank * 2) != cudaSuccess) {
         free_handle(h);
         return LORA_ECUDA;
     }
@@ -1596,6 +1600,45 @@ int validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments
     return LORA_OK;
 }
 
+// The batch in whole tiles of 128 rows, whatever adapters their rows name: each pair of a tile and an adapter has a U block
+// of its own (zero in other rows) and an expand. Fewer tiles than the planner's, none of which holds two adapters, where a
+// few rows each name several (94 rows of nine segments and two adapters, 5,120 -> 12,288, rank 256: 26 us for 74; two rows
+// of two adapters, rank 16, 19 for 45), and fewer SM pairs, whose two tiles would otherwise share one (223 rows of five
+// segments 25 for 40). The tiles are in `plan`; the pairs, in the order of tiles, are the shrink's tiles. False where it
+// gains nothing or does not fit.
+bool merge_tiles(const lora_linear* h, int T, Plan* plan) {
+    const int nf = ceil_div(T, kTileM), n_used = (int)plan->used_adapters.size();
+    std::vector<Tile> by_two;
+    make_groups(plan->fused, 2, false, h->u_rows - kTileM, &by_two);
+    const int planned = (int)plan->fused.size(), planned_even = planned + planned % 2;
+    const int before = (int)by_two.size() > planned_even ? (int)by_two.size() : planned;
+    if (nf >= before || n_used < 2 || n_used > kFp8InlineAdapters || (int)plan->seg_id.size() > kInlineSegs) return false;
+    std::vector<Tile> tiles, pairs;
+    for (int i = 0; i < nf; ++i) {
+        Tile t{};
+        t.row0 = t.u_row = i * kTileM;
+        t.nrows = std::min(kTileM, T - t.row0);
+        tiles.push_back(t);
+        for (int a = 1; a <= n_used; ++a)
+            for (size_t s = 0; s < plan->seg_id.size(); ++s)
+                if (plan->seg_id[s] == a && plan->seg_off[s] < t.row0 + t.nrows && plan->seg_off[s + 1] > t.row0) {
+                    Tile p = t;
+                    p.adapter = a;
+                    p.u_row = (int)pairs.size() * kTileM;
+                    p.fused_index = i;
+                    pairs.push_back(p);
+                    break;
+                }
+    }
+    const int kb = ceil_div(h->d_in, kFp8Group), kl = ceil_div(h->rank, 64);
+    if ((int)pairs.size() > kFp8Expands || 2 * nf + (int)pairs.size() > kInlineTiles ||
+        nf * kb + (int)pairs.size() * kl >= before * kb + (int)plan->shrink.size() * kl)
+        return false;
+    plan->fused = tiles;
+    plan->shrink = pairs;
+    return true;
+}
+
 int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T, const int32_t* seg_offsets,
                      const int32_t* seg_adapter_ids, int n_seg, const void* const* A, const void* const* B,
                      const float* scale, int n_adapters, void* y, cudaStream_t stream) {
@@ -1617,10 +1660,31 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     for (int i = 0; i < nf; ++i) plan.fused[i].fused_index = plan.fused[i].split_index = i;
 
     DeviceGuard guard(h->device);
+    const bool merged = h->allow_inline && merge_tiles(h, T, &plan);
     const Fp8Shape s8 = fp8_shape(h, plan);
     const int cg = s8.wide ? 2 : 1;
     std::vector<Tile> groups;
-    make_groups(plan.fused, cg, false, h->u_rows - kTileM, &groups);
+    std::vector<Fp8Expand> expands;
+    if (merged) {
+        for (size_t i = 0; i < plan.fused.size(); i += cg) {
+            const int e0 = (int)expands.size();
+            for (int a = 1; a <= n_used; ++a) {
+                Fp8Expand e{(int16_t)a, {kFp8Expands, kFp8Expands}};
+                for (const Tile& t : plan.shrink)
+                    if (t.adapter == a && t.fused_index >= (int)i && t.fused_index < (int)i + cg) e.slot[t.fused_index - i] = (int16_t)(t.u_row / kTileM);
+                if (e.slot[0] < kFp8Expands || e.slot[1] < kFp8Expands) expands.push_back(e);
+            }
+            for (int c = 0; c < cg; ++c) {
+                Tile t = plan.fused[std::min(i + c, plan.fused.size() - 1)];
+                if (i + c >= plan.fused.size()) t.nrows = 0;
+                t.u_row = e0;
+                t.adapter = (int)expands.size() - e0;
+                groups.push_back(t);
+            }
+        }
+    } else {
+        make_groups(plan.fused, cg, false, h->u_rows - kTileM, &groups);
+    }
     const int nft = (int)groups.size();
 
     // The shrink (bf16) is launched ahead: the bf16 kernel's units over rank tiles, or, where that finishes sooner, one
@@ -1628,27 +1692,30 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     Shape sh;
     int rank_tiles = 1, parts = 0, shrink_n = 0;
     if (n_used) {
-        sh = choose_shape(h, plan, false);
-        sh.bk = 64;
-        sh.a_rows = kTileM;
-        const int sg = (int)(sh.shrink_groups.size() / sh.cs), slots = std::max(1, usable_sms(h) / sh.cs);
-        const int width = std::max(32, ceil_div(ceil_div(h->rank, std::min(std::max(1, slots / sg), 8)), 32) * 32);
-        if (width < sh.shrink_n) {
-            rank_tiles = ceil_div(h->rank, width);
-            sh.shrink_n = width;
+        double best = 0;                                   // of the bf16 kernel's units, which know no tiles of several adapters
+        if (!merged) {
+            sh = choose_shape(h, plan, false);
+            sh.bk = 64;
+            sh.a_rows = kTileM;
+            const int sg = (int)(sh.shrink_groups.size() / sh.cs), slots = std::max(1, usable_sms(h) / sh.cs);
+            const int width = std::max(32, ceil_div(ceil_div(h->rank, std::min(std::max(1, slots / sg), 8)), 32) * 32);
+            if (width < sh.shrink_n) {
+                rank_tiles = ceil_div(h->rank, width);
+                sh.shrink_n = width;
+            }
+            sh.tile_n = sh.shrink_n;
+            sh.stages = stages_for(sh.shrink_n / sh.cs, sh.bk);
+            best = (double)ceil_div((long long)sg * rank_tiles, slots) * ceil_div(h->d_in, 64) * kstep_cycles(sh.cs, sh.shrink_n);
         }
-        sh.tile_n = sh.shrink_n;
-        sh.stages = stages_for(sh.shrink_n / sh.cs, sh.bk);
         // (a call of 48 rows of 17,408 -> 5,120, rank 256: with 256 columns of the rank a CTA 40 us, with 32 38; of 6,144 24 and 23)
         const int steps = ceil_div(h->d_in, 64), tiles = (int)plan.shrink.size(), whole = ceil_div(h->rank, 16) * 16;
-        double best = (double)ceil_div((long long)sg * rank_tiles, slots) * steps * kstep_cycles(sh.cs, sh.shrink_n);
         for (int n = whole; n >= 32 || n == whole; n = std::min(n - 16, ceil_div(n / 2, 16) * 16)) {
             const int units = tiles * ceil_div(h->rank, n);
             const double step = std::max((std::min(T, kTileM) + n) * 128.0 / 61.0, 4.0 * std::max(n / 2.0, 48.0) + 130.0);
             for (int q = 1; q <= std::min(kFp8MaxParts, steps); ++q) {
                 if (q > 1 && (units > h->fp8_clusters[1][q] || units * q > usable_sms(h))) continue;
                 const double t = (double)ceil_div(units, q > 1 ? units : usable_sms(h)) * ceil_div(steps, q) * step + (q > 1 ? 4000 : 0);
-                if (t < best) {
+                if (t < best || best == 0) {
                     best = t;
                     parts = q;
                     shrink_n = n;
@@ -1660,17 +1727,21 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     const int nst = n_used ? (int)sh.shrink_groups.size() : 0;
     const int a_rows = parts ? shrink_n : sh.shrink_n / sh.cs;   // of an A_a box
     for (const Tile& t : groups)
-        if (t.adapter < 0 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T ||
-            (t.adapter && t.u_row != t.row0 && t.u_row != h->u_rows - kTileM))
+        if (t.adapter < 0 || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T ||
+            (merged ? t.u_row < 0 || t.u_row + t.adapter > (int)expands.size()
+                    : t.adapter > n_used || (t.adapter && t.u_row != t.row0 && t.u_row != h->u_rows - kTileM)))
             return LORA_EINVAL;
+    if (expands.size() > kFp8Expands) return LORA_EINVAL;
     for (int i = 0; i < nst; ++i) {
         const Tile& t = sh.shrink_groups[i];
+        if (parts && (t.u_row < 0 || t.u_row + t.nrows > (merged ? kFp8Expands * kTileM : h->u_rows))) return LORA_EINVAL;
         if (t.adapter < 1 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T) return LORA_EINVAL;
     }
 
-    const bool inline_wl = h->allow_inline && nft + nst <= kInlineTiles && n_m <= kInlineSegs && n_used <= kInlineAdapters;
+    const bool inline_wl = h->allow_inline && nft + nst <= kInlineTiles && n_m <= kInlineSegs && n_used <= (parts ? kFp8InlineAdapters : kInlineAdapters);
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return LORA_ECUDA;
+    if (merged && !inline_wl) return LORA_EINVAL;         // (merge_tiles has seen to it)
     if (capture != cudaStreamCaptureStatusNone && !inline_wl) return LORA_EUNSUPPORTED;   // as lora_linear_forward
 
     const int q_groups = ceil_div(h->d_in, kFp8Group);
@@ -1752,7 +1823,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     }
     if (parts) {
         if (encode_2d(h, &r.tm_x, x, h->d_in, T, 64, kTileM) != CUDA_SUCCESS) return LORA_ECUDA;
-        r.u = h->u_ws;
+        r.u = merged ? h->u_pairs : h->u_ws;
         r.status = h->status;
         r.wait_limit_ns = h->wait_limit_ns;
         r.n_tiles = nst;
@@ -1795,9 +1866,12 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     if (timing) cudaEventRecord(rec.ev[1], stream);
     if (encode_u8_sw128(h, &q.tm_x, f.x8, h->d_in, T, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_u8_sw128(h, &q.tm_w, f.w8, h->d_in, h->d_out, (uint32_t)(s8.wide ? 64 : s8.tile_n)) != CUDA_SUCCESS ||
-        encode_2d(h, &q.tm_u, h->u_ws, h->rank, h->u_rows, 64, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
+        encode_2d(h, &q.tm_u, merged ? h->u_pairs : h->u_ws, h->rank, merged ? (kFp8Expands + 1) * kTileM : h->u_rows, 64,
+                  (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_2d(h, &q.tm_y, y, h->d_out, T, s8.wide ? 64 : 32, 32) != CUDA_SUCCESS)
         return LORA_ECUDA;
+    q.merged = merged;
+    std::copy(expands.begin(), expands.end(), q.expand);
     q.xs = f.xs;
     q.rows = T;
     q.vec_scales = q_groups % 4 == 0 && aligned16(f.xs) && aligned16(f.ws);
@@ -1811,7 +1885,13 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.raster_group = s8.raster_group;
     q.k_blocks = q_groups;
     q.k_lora = ceil_div(h->rank, 64);
-    q.lora_stages = s8.stages >= q.k_lora + 512 / s8.tile_n - 1 ? q.k_lora : 1;
+    for (const Tile& t : groups) q.most_expands = std::max(q.most_expands, merged ? t.adapter : t.adapter ? 1 : 0);
+    for (q.lora_stages = q.k_lora;; --q.lora_stages)
+        if (q.k_lora % q.lora_stages == 0 &&
+            fp8_window(512 / s8.tile_n, q_groups / s8.parts, q.most_expands * (q.k_lora / q.lora_stages), q.lora_stages) <= s8.stages)
+            break;
+        else if (q.lora_stages == 1)
+            return LORA_EUNSUPPORTED;                      // (one stage a block: a ring is longer than the buffers are many)
     q.d_out = h->d_out;
     q.parts = s8.parts;
     q.a_rows = s8.a_rows;

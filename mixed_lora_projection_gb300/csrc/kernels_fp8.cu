@@ -7,7 +7,7 @@
 // A group's 128 products are summed by tcgen05.mma kind::f8f6f4 in tensor memory; each group has a scale of
 // its own per row and block of columns, so its sums leave tensor memory and are added, times that scale, to
 // fp32 accumulators in the epilogue warps' registers. The expand is one more such block (kind::f16, bf16 operands, the
-// stages of the whole rank) with scale 1.
+// stages of the whole rank where the ring is long enough) with scale 1, and one for each adapter of a tile that holds several.
 //
 // Per CTA: warp 0 loads the stages (TMA, rows of 128 bytes, 128-byte swizzle: 128 e4m3 or 64 bf16); warps 1 and
 // 2 issue the even and the odd blocks' MMAs into the two TMEM buffers (a warp's barrier wait completes after the
@@ -144,7 +144,7 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
 // lora_stages stages; nb blocks and ns stages in all.
 struct Work {
     Tile tile;
-    int n0, kb0, nk, nb, ns;
+    int n0, kb0, nk, nb, ns, e0;                       // e0: its first expand, where tiles hold several adapters
 };
 template <int CG, int NT>
 __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, int u, int rank, int part) {
@@ -156,9 +156,12 @@ __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, in
     w.n0 = (g * p.raster_group + r % gw) * NT;
     w.kb0 = part * p.k_blocks / p.parts;
     w.nk = (part + 1) * p.k_blocks / p.parts - w.kb0;
-    const bool expand = w.tile.adapter && part == p.parts - 1;
-    w.nb = w.nk + (expand ? p.k_lora / p.lora_stages : 0);
-    w.ns = w.nk + (expand ? p.k_lora : 0);
+    // the expands go to the parts of K in turn, a single one to the last
+    const int expands = p.merged ? w.tile.adapter : w.tile.adapter != 0, e = part * expands / p.parts;
+    const int mine = (part + 1) * expands / p.parts - e;
+    w.e0 = w.tile.u_row + e;
+    w.nb = w.nk + mine * (p.k_lora / p.lora_stages);
+    w.ns = w.nk + mine * p.k_lora;
     return w;
 }
 
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             const uint32_t tx = CG * (a_bytes + b_bytes);
             for (int u = first; u < n_units && ok; u += step) {
                 const Work w = decode<CG, NT>(p, tiles, u, rank, part);
-                const CUtensorMap* bm = &bmaps[w.ns > w.nk ? w.tile.adapter - 1 : 0];
+                const CUtensorMap* bm = &bmaps[w.ns > w.nk && !p.merged ? w.tile.adapter - 1 : 0];
+                int u_row = w.tile.u_row, e = w.e0, ku = 0;
                 if (w.ns > w.nk && !p.inline_wl && acquired != w.tile.adapter) {
                     tensormap_acquire(bm);
                     acquired = w.tile.adapter;
@@ -260,11 +264,18 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     const uint32_t fb = CG > 1 ? map_to_rank(bar, 0) : bar;
                     const uint32_t sa = smem_addr(a_ring + (size_t)stage * a_bytes), sb = smem_addr(b_ring + (size_t)stage * b_bytes);
                     const bool main = b < w.nk;
-                    const int k = main ? (w.kb0 + b) * kFp8Group : (b - w.nk) * 64;
-                    if (!main && p.late_u) griddep_wait();
+                    if (!main && ku == 0) {
+                        if (p.late_u) griddep_wait();
+                        if (p.merged) {
+                            bm = &bmaps[p.expand[e].adapter - 1];
+                            u_row = p.expand[e].slot[rank] * kTileM;
+                            ++e;
+                        }
+                    }
+                    const int k = main ? (w.kb0 + b) * kFp8Group : ku * 64;
                     if (elect_one()) {
                         if (leader) mbar_arrive_expect_tx(bar, tx, 1u);
-                        tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : w.tile.u_row, 1u);
+                        tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : u_row, 1u);
                         if (CG == 1) {
                             tma_load_2d<CG>(sb, main ? &p.tm_w : bm, fb, k, w.n0, 1u);
                         } else {                             // a pair's CTA holds half of the columns of each half
@@ -273,6 +284,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                         }
                     }
                     __syncwarp();
+                    if (!main && ++ku == p.k_lora) ku = 0;
                     ++issued;
                     if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
@@ -304,7 +316,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     if ((blk & 1) == mine) {
                         // The buffer first: it is free when the epilogue has taken block blk - kBufs, and so every stage up
                         // to that block's has been filled and read. Only then does a stage's parity tell this fill from the
-                        // one a lap before, where a lap is longer than the stages of the blocks since (launch_fp8).
+                        // one a lap before, where a lap is no shorter than the stages of the blocks since (fp8_window).
                         const int buf = blk % kBufs;
                         const uint32_t d = tmem_base + (uint32_t)(buf * NT);
                         const uint32_t free = ((blk / kBufs) & 1) ^ 1;
@@ -675,7 +687,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
             const int32_t* seg_id = p.inline_wl ? p.inline_seg + p.n_seg + 1 : p.seg_id;
             const float s = mine && row_adapter(seg_off, seg_id, p.n_seg, row) == tile.adapter
                                 ? (p.inline_wl ? p.inline_scales : p.scales)[tile.adapter - 1] : 0.f;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.u) + (long long)row * p.rank + c0;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.u) + (long long)(tile.u_row + r_local) * p.rank + c0;
             for (int c = 0; c < p.n; c += 16) {
                 uint32_t v[16];
                 if (nk) tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
@@ -715,7 +727,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
                     s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
                     s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
                 }
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.u) + (long long)(tile.row0 + r) * p.rank + c0 + c) =
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.u) + (long long)(tile.u_row + r) * p.rank + c0 + c) =
                     make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
             }
         }
@@ -821,15 +833,27 @@ int fp8_max_clusters(int tile_n, int parts) {
     return n;
 }
 
+int fp8_window(int bufs, int nk, int expands, int lora_stages) {
+    int most = 0;
+    for (int first = 0; first < nk + expands; ++first) {
+        int sum = 0;
+        for (int i = 0; i < bufs; ++i) sum += (first + i) % (nk + expands) < nk ? 1 : lora_stages;
+        most = sum > most ? sum : most;
+    }
+    return most;
+}
+
 cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream) {
     const int tile_rows = p.tile_n / (p.wide ? 2 : 1);
     if ((p.tile_n != 256 && (p.wide || p.tile_n != 128)) || p.parts < 1 || p.parts > kFp8MaxParts || p.parts > p.k_blocks ||
         (p.wide && (p.parts != 1 || p.a_rows != kTileM)) || p.a_rows < 16 || p.a_rows > kTileM || p.a_rows % 16)
         return cudaErrorInvalidValue;
-    // stages: a lap is longer than the stages of the blocks between two uses of a TMEM buffer; an A stage's 128 rows lie
+    // stages: a lap is no shorter than the stages of the blocks between two uses of a TMEM buffer; an A stage's 128 rows lie
     // inside the rings; the parts' sums take the rings' place
     const size_t rings = (size_t)p.stages * (p.a_rows + tile_rows) * kFp8StageRow;
-    if (p.lora_stages < 1 || p.k_lora % p.lora_stages || p.stages < p.lora_stages + 512 / p.tile_n - 1 || fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages) > (size_t)kSmemLimit ||
+    if (p.lora_stages < 1 || p.k_lora % p.lora_stages || p.most_expands < 0 ||
+        p.stages < fp8_window(512 / p.tile_n, p.k_blocks / p.parts, p.most_expands * (p.k_lora / p.lora_stages), p.lora_stages) ||
+        fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages) > (size_t)kSmemLimit ||
         (size_t)p.stages * tile_rows < (size_t)(kTileM - p.a_rows) || (p.parts > 1 && rings < (size_t)p.tile_n * kTileM * 4))
         return cudaErrorInvalidValue;
     // units of K parts: one a cluster (the rings hold its sums at its end)

@@ -10,13 +10,23 @@ namespace lora {
 constexpr int kFp8Group = 128;        // input features per scale; a base weight's block is 128 x 128
 constexpr int kFp8Threads = 384;      // warp 0 TMA, 1 and 2 MMA, 3 scales (and owns TMEM), 4..11 epilogue
 constexpr int kFp8MaxParts = 8;       // most parts of K: one CTA of a cluster each
+constexpr int kFp8InlineAdapters = 8; // named in a call whose work list travels in the parameters
+constexpr int kFp8Expands = 16;       // pairs of a row tile and an adapter, where tiles hold several
 constexpr int kFp8StageRow = 128;     // bytes of a stage's row: one group of e4m3, 64 bf16 of the expand
+
+// One expand of a row group whose tiles hold several adapters: U blocks of 128 rows, per CTA of a pair.
+struct Fp8Expand {
+    int16_t adapter, slot[2];
+};
 
 // One launch. Units are (row group, output tile) blocks of Y; a row group is one planner tile, or two
 // that share the weight's tile on an SM pair (wide form).
 struct Fp8Params {
-    CUtensorMap inline_bmaps[kInlineAdapters];   // B_a [d_out, rank] bf16 (inline work list)
+    CUtensorMap inline_bmaps[kFp8InlineAdapters];   // B_a [d_out, rank] bf16 (inline work list)
     Tile inline_tiles[kInlineTiles];
+    // merged: a tile's u_row is its group's first expand, its adapter their number; U blocks by `slot`
+    Fp8Expand expand[kFp8Expands];
+    int merged;
     int inline_wl;
     CUtensorMap tm_x;                 // X [T, d_in] e4m3, box 128 x a_rows, 128-byte swizzle
     CUtensorMap tm_w;                 // W [d_out, d_in] e4m3, box 128 x tile_n, on pairs 128 x 64
@@ -34,7 +44,8 @@ struct Fp8Params {
     int raster_group;                 // column tiles whose row groups run before the next column tiles
     int k_blocks;                     // ceil(d_in / 128)
     int k_lora;                       // ceil(rank / 64)
-    int lora_stages;                  // of an expand's block: all k_lora where the ring is long enough, else 1
+    int lora_stages;                  // of an expand's block: all k_lora where the ring is long enough, else a part of them
+    int most_expands;                 // of a unit
     int d_out;
     int parts;                        // K parts of a unit (1 in the wide form)
     int a_rows;                       // rows of an A box: 128, or fewer (a multiple of 16) for a batch of one tile
@@ -50,10 +61,10 @@ struct Fp8Params {
 // the CTAs of a cluster, so that a few tiles find most SMs.
 constexpr int kShrinkThreads = 256;   // warp 0 TMA, 1 MMA, 2 owns TMEM, 4..7 epilogue
 struct ShrinkParams {
-    CUtensorMap inline_amaps[kInlineAdapters];   // A_a [rank, d_in] bf16, box 64 x n
+    CUtensorMap inline_amaps[kFp8InlineAdapters];   // A_a [rank, d_in] bf16, box 64 x n
     Tile inline_tiles[kInlineTiles];
     int32_t inline_seg[2 * kInlineSegs + 1];     // merged segments: offsets, then compact ids
-    float inline_scales[kInlineAdapters];
+    float inline_scales[kFp8InlineAdapters];
     int inline_wl;
     CUtensorMap tm_x;                 // X [T, d_in] bf16, box 64 x 128
     const CUtensorMap* tm_a;          // device arrays (when not inline)
@@ -61,7 +72,7 @@ struct ShrinkParams {
     const int32_t* seg_off;
     const int32_t* seg_id;
     const float* scales;
-    void* u;                          // [u_rows, rank] bf16
+    void* u;                          // [u_rows, rank] bf16; a tile's rows from its u_row on
     int* status;
     unsigned long long wait_limit_ns;
     int n_tiles, n_seg, rank;
@@ -71,6 +82,9 @@ struct ShrinkParams {
 };
 
 // kernels_fp8.cu
+// The most stages of as many blocks in a row as there are TMEM buffers, where units of nk base blocks (a stage each) and
+// `expands` blocks of `lora_stages` follow one another: the ring is at least as long (the issuing warps' comment).
+int fp8_window(int bufs, int nk, int expands, int lora_stages);
 int shrink_stages(int n);
 cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream);
 size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages);

@@ -331,3 +331,86 @@ def test_refused_arguments():
     c.linear.close()
     with pytest.raises(Exception):
         c.run()
+
+
+# tiles that hold rows of several adapters: one expand each, over parts of K, single CTAs and pairs
+@pytest.mark.parametrize("d_in,d_out,rank,rows,ids", [
+    (256, 136, 16, [1, 1], [1, 2]),
+    (5120, 1288, 256, [1, 0, 1, 1, 0], [1, 0, 0, 2, 2]),
+    (6144, 5120, 256, [3, 1, 7, 2], [1, 2, 3, 4]),
+    (6144, 5120, 64, [1] * 8, [8, 7, 6, 5, 4, 3, 2, 1]),
+    (1024, 2568, 200, [0, 18, 5, 10, 3, 11, 6, 15, 26], [2, 2, 1, 0, 2, 2, 0, 1, 2]),
+    (1024, 2568, 40, [11, 1, 44, 86, 81], [0, 1, 1, 0, 2]),
+    (1024, 1288, 256, [100, 27, 1, 1, 126], [1, 2, 1, 2, 3]),
+    (640, 264, 24, [60, 60, 60, 60, 60, 60, 60], [1, 2, 1, 2, 1, 2, 1]),
+    (17408, 264, 256, [20, 20], [1, 2]),
+    (2064, 5128, 72, [64, 64, 64, 64, 300], [1, 0, 2, 1, 0]),
+    (1024, 34816, 64, [8, 8, 301, 8, 600], [0, 1, 2, 0, 1]),
+    (1024, 5120, 64, [70] * 9, [1, 2, 3, 1, 2, 3, 1, 2, 3]),
+    (384, 520, 16, [2] * 48, [1, 2] * 24),
+    (384, 520, 16, [2] * 50, [1, 2] * 25),                  # (more segments than the parameters hold)
+    (384, 520, 16, [4] * 9, list(range(1, 10))),            # (more adapters)
+])
+def test_tiles_of_several_adapters(d_in, d_out, rank, rows, ids):
+    c = Case(d_in, d_out, rank, rows, ids, seed=d_out + rank)
+    y = c.run()
+    c.check(y)
+    assert all(torch.equal(c.run(), y) for _ in range(3))
+
+
+def test_several_adapters_captured_and_in_turn():
+    # calls of one handle whose tiles are merged and not, in turn: the blocks of U are each call's own
+    cases = [Case(1024, 1288, 64, rows, ids, seed=i) for i, (rows, ids) in enumerate([
+        ([1] * 8, [1, 2, 3, 4, 5, 6, 7, 8]), ([128, 3], [1, 2]), ([300], [1]), ([9, 120, 30, 7], [2, 1, 0, 3])])]
+    for c in cases[1:]:
+        c.linear.close()
+    shared = LoraLinear(1024, 1288, 64, 400, 16)
+    for c in cases:
+        c.linear = shared
+    want = [c.run() for c in cases]
+    for c, y in zip(cases, want):
+        c.check(y)
+    outs = [torch.zeros_like(y) for y in want]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            for c, o in zip(cases, outs):
+                c.run(y=o)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, y) for o, y in zip(outs, want))
+
+
+def test_a_wait_that_runs_out_with_several_adapters():
+    from mixed_lora_projection_gb300 import _lib
+    c = Case(640, 264, 16, [4, 5, 6], [1, 2, 3], seed=1)
+    y = c.run()
+    c.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 2000)
+    c.linear.set_option(_lib.OPT_DEBUG_STALL, 1)
+    c.run()
+    assert c.linear.status() == _lib.LORA_ETIMEOUT
+    c.linear.set_option(_lib.OPT_DEBUG_STALL, 0)
+    assert c.linear.status(reset=True) == _lib.LORA_ETIMEOUT
+    c.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 4000000)
+    assert torch.equal(c.run(), y) and c.linear.status() == 0
+
+
+# several stages an expand beside few of the base, many units a block: the ring is no shorter than the stages that pass
+# between two uses of a buffer
+@pytest.mark.parametrize("d_in,d_out,rank,rows,ids", [
+    (128, 40960, 256, [48], [1]),
+    (256, 40960, 256, [40, 60], [1, 2]),
+    (128, 40960, 192, [20, 20, 8], [1, 2, 3]),
+    (5120, 34816, 256, [8] * 6, [1, 2, 3, 4, 0, 0]),
+    (384, 40960, 256, [100, 100, 100, 400], [1, 2, 1, 2]),
+    (128, 20480, 256, [1500], [1]),
+])
+def test_more_expands_than_base_blocks(d_in, d_out, rank, rows, ids):
+    c = Case(d_in, d_out, rank, rows, ids, seed=d_in + rank)
+    y = c.run()
+    c.check(y)
+    assert all(torch.equal(c.run(), y) for _ in range(3))
