@@ -187,9 +187,9 @@ int lora_linear_forward_w4(lora_linear* h, const void* x, int T,
  * two scales' product, are added in fp32. Requires d_in to be a multiple of 16 (else LORA_EINVAL); all other
  * arguments, layouts and errors as lora_linear_forward, except that the base product may be summed in parts
  * of K chosen by the batch: the same call gives the same bits, but a row's last bit may differ in another batch.
- * Stream capture as lora_linear_forward, with up to 8 adapters. Rows share tiles of 128 with their neighbours, whatever
- * adapters those name, and add zero times another adapter's B: an infinity or a NaN in an adapter can reach them.
- * Of the options, those of the launch's shape (tile widths, K parts,
+ * A row without an adapter may share a tile of 128 rows with an adapter's and adds zero times its values, as in
+ * lora_linear_forward (an infinity or a NaN in the adapter reaches it); rows of other adapters take nothing of it.
+ * Stream capture as lora_linear_forward, with up to 8 adapters. Of the options, those of the launch's shape (tile widths, K parts,
  * clusters, unit orders) apply to the adapters' shrink alone; LORA_OPT_MAX_CTAS to both launches. Also LORA_ENOMEM where
  * the host has no memory for the plan.
  * Source: no counterpart on the pages (their base is 4-bit); the scales' layout is the one that this library's

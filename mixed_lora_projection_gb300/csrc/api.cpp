@@ -67,7 +67,7 @@ struct lora_linear {
     int device = 0, d_in = 0, d_out = 0, rank = 0, max_tokens = 0, max_segments = 0;
     int num_sms = 0;
     void* u_ws = nullptr;       // bf16 [u_rows, rank]: shrink output, read by the fused pass
-    void* u_pairs = nullptr;    // bf16 [(kFp8Expands + 1) 128, rank]: the 8-bit kernel's, by tile and adapter; the last block zero
+    void* u_pairs = nullptr;    // bf16 [128 kFp8Expands, rank]: the 8-bit kernel's, by tile and adapter
     int u_rows = 0;
     int* status = nullptr;      // device status word
     int* flags = nullptr;       // per fused tile: U rows ready (1) in the running launch; then the
@@ -881,7 +881,7 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
                     align_up((size_t)max_segments * sizeof(CUtensorMap), 128) +
                     (size_t)(h->max_fused / 2 + 1) * sizeof(W4Group) + 256;
     if (cudaMalloc(&h->u_ws, (size_t)h->u_rows * rank * 2) != cudaSuccess ||
-        cudaMalloc(&h->u_pairs, (size_t)(kFp8Expands + 1) * kTileM * rank * 2) != cudaSuccess ||
+        cudaMalloc(&h->u_pairs, (size_t)kFp8Expands * kTileM * rank * 2) != cudaSuccess ||
         cudaMalloc((void**)&h->status, sizeof(int)) != cudaSuccess ||
         cudaMalloc((void**)&h->flags, sizeof(int) * ((size_t)h->max_fused + 1)) != cudaSuccess ||
         cudaHostAlloc((void**)&h->status_host, sizeof(int), cudaHostAllocDefault) != cudaSuccess) {
@@ -912,8 +912,7 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
     }
     if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess ||
         cudaMemset(h->flags, 0, sizeof(int) * ((size_t)h->max_fused + 1)) != cudaSuccess ||
-        cudaMemset(h->u_ws, 0, (size_t)h->u_rows * rank * 2) != cudaSuccess ||
-        cudaMemset(h->u_pairs, 0, (size_t)(kFp8Expands + 1) * kTileM * rank * 2) != cudaSuccess) {
+        cudaMemset(h->u_ws, 0, (size_t)h->u_rows * rank * 2) != cudaSuccess) {
         free_handle(h);
         return LORA_ECUDA;
     }
@@ -1531,6 +1530,7 @@ namespace {
 // Launch shape of the 8-bit kernel for a plan.
 struct Fp8Shape {
     int wide = 0, tile_n = 128, parts = 1, a_rows = kTileM, stages = 0, n_ntiles = 0, raster_group = 1;
+    double us = 0;                // its model's time, the expands with it
 };
 
 // Three forms, each with one CTA (or pair) an SM: blocks of 128 x 128 and 128 x 256 on single CTAs, whose units a cluster
@@ -1541,13 +1541,15 @@ struct Fp8Shape {
 // columns 10.8 us against 11.5 (256 columns, six parts), 128 rows there 13.4 against 17.3 (four), 48 rows of 5,120 ->
 // 12,288 in 128 columns 17.0 against 17.8 (256, two parts), 348 rows in 256 columns 24.0 against 27.5 and, on pairs, 40.6;
 // 2,048 rows there on pairs 113 against 120 (256 columns).
-Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
+Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan, bool merged) {
     const int nf = (int)plan.fused.size(), k_blocks = ceil_div(h->d_in, kFp8Group), sms = usable_sms(h);
     Fp8Shape s;
     double best = -1;
     const double fetch = (double)h->d_in * h->d_out / 6.5e6;
     int rows = 0;
     for (const Tile& t : plan.fused) rows = std::max(rows, (int)t.nrows);
+    // blocks of the expands: in the planner's tiles one a unit, in the last part of K; else a tile's share of the pairs
+    const double expand = (double)ceil_div(h->rank, 64) * (merged ? (double)plan.shrink.size() / nf : plan.shrink.empty() ? 0 : 1);
     auto weigh = [&](int wide, int tile_n, int parts, long long units, int slots, double block_us) {
         const double join = parts > 1 ? 1.2 + 5.0 * rows / kTileM * tile_n / 256 : 0.0;
         const double t = std::max((double)ceil_div(units, std::max(slots, 1)) * ceil_div(k_blocks, parts) * block_us, fetch) + join;
@@ -1556,6 +1558,7 @@ Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
         s.wide = wide;
         s.tile_n = tile_n;
         s.parts = parts;
+        s.us = t + ceil_div(units, std::max(slots, 1)) * (merged ? expand / parts : expand) * block_us;
     };
     for (int tile_n = 128; tile_n <= 256; tile_n += 128) {
         const long long units = (long long)nf * ceil_div(h->d_out, tile_n);
@@ -1564,8 +1567,11 @@ Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan) {
         for (int parts = 2; parts <= std::min(kFp8MaxParts, k_blocks); ++parts)
             if (units <= h->fp8_clusters[tile_n / 256][parts] && units * parts <= sms) weigh(0, tile_n, parts, units, (int)units, us);
     }
-    // (pairs: neighbouring tiles, less where two adapters meet; near enough for the choice)
-    if (nf >= 2 && sms >= 2) weigh(1, 256, 1, (long long)((nf + 1) / 2) * ceil_div(h->d_out, 256), sms / 2, 0.39);
+    if (nf >= 2 && sms >= 2 && !merged) {                  // (pairs: neighbouring tiles, but none of two adapters)
+        std::vector<Tile> groups;
+        make_groups(plan.fused, 2, false, h->u_rows - kTileM, &groups);
+        weigh(1, 256, 1, (long long)(groups.size() / 2) * ceil_div(h->d_out, 256), sms / 2, 0.39);
+    }
     s.n_ntiles = ceil_div(h->d_out, s.tile_n);
     // pairs walk the column tiles in groups of up to 20, all rows of a group first (16,384 rows of 5,120 -> 5,120: groups of
     // 20 357 us, of 4 369; 4,144 of 5,120 -> 34,816: of 20 625, of 4 636, of all 136 664); single CTAs all rows of a column
@@ -1601,18 +1607,13 @@ int validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments
 }
 
 // The batch in whole tiles of 128 rows, whatever adapters their rows name: each pair of a tile and an adapter has a U block
-// of its own (zero in other rows) and an expand. Fewer tiles than the planner's, none of which holds two adapters, where a
-// few rows each name several (94 rows of nine segments and two adapters, 5,120 -> 12,288, rank 256: 26 us for 74; two rows
-// of two adapters, rank 16, 19 for 45), and fewer SM pairs, whose two tiles would otherwise share one (223 rows of five
-// segments 25 for 40). The tiles are in `plan`; the pairs, in the order of tiles, are the shrink's tiles. False where it
-// gains nothing or does not fit.
-bool merge_tiles(const lora_linear* h, int T, Plan* plan) {
+// of its own and an expand that its rows alone take. Fewer tiles than the planner's, none of which holds two adapters: 94
+// rows of nine segments and two adapters, 5,120 -> 12,288, rank 256, 26 us for 74; two rows of two adapters, rank 16, 19 for
+// 45; and 223 rows of five segments, whose two tiles no SM pair may share, 25 for 40. The tiles are in `plan`; the pairs,
+// in the order of tiles, are the shrink's tiles. False where they do not fit.
+bool merge_tiles(int T, Plan* plan) {
     const int nf = ceil_div(T, kTileM), n_used = (int)plan->used_adapters.size();
-    std::vector<Tile> by_two;
-    make_groups(plan->fused, 2, false, h->u_rows - kTileM, &by_two);
-    const int planned = (int)plan->fused.size(), planned_even = planned + planned % 2;
-    const int before = (int)by_two.size() > planned_even ? (int)by_two.size() : planned;
-    if (nf >= before || n_used < 2 || n_used > kFp8InlineAdapters || (int)plan->seg_id.size() > kInlineSegs) return false;
+    if (n_used < 2 || n_used > kFp8InlineAdapters || nf > kFp8Expands || (int)plan->seg_id.size() > kInlineSegs) return false;
     std::vector<Tile> tiles, pairs;
     for (int i = 0; i < nf; ++i) {
         Tile t{};
@@ -1630,10 +1631,7 @@ bool merge_tiles(const lora_linear* h, int T, Plan* plan) {
                     break;
                 }
     }
-    const int kb = ceil_div(h->d_in, kFp8Group), kl = ceil_div(h->rank, 64);
-    if ((int)pairs.size() > kFp8Expands || 2 * nf + (int)pairs.size() > kInlineTiles ||
-        nf * kb + (int)pairs.size() * kl >= before * kb + (int)plan->shrink.size() * kl)
-        return false;
+    if ((int)pairs.size() > kFp8Expands || nf + (int)pairs.size() > kInlineTiles) return false;
     plan->fused = tiles;
     plan->shrink = pairs;
     return true;
@@ -1660,27 +1658,33 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     for (int i = 0; i < nf; ++i) plan.fused[i].fused_index = plan.fused[i].split_index = i;
 
     DeviceGuard guard(h->device);
-    const bool merged = h->allow_inline && merge_tiles(h, T, &plan);
-    const Fp8Shape s8 = fp8_shape(h, plan);
+    Fp8Shape s8 = fp8_shape(h, plan, false);
+    bool merged = false;
+    if (h->allow_inline && n_used > 1) {
+        Plan whole = plan;
+        if (merge_tiles(T, &whole)) {
+            const Fp8Shape s = fp8_shape(h, whole, true);
+            merged = s.us < s8.us;
+            if (merged) {
+                plan = whole;
+                s8 = s;
+            }
+        }
+    }
     const int cg = s8.wide ? 2 : 1;
     std::vector<Tile> groups;
     std::vector<Fp8Expand> expands;
     if (merged) {
-        for (size_t i = 0; i < plan.fused.size(); i += cg) {
-            const int e0 = (int)expands.size();
-            for (int a = 1; a <= n_used; ++a) {
-                Fp8Expand e{(int16_t)a, {kFp8Expands, kFp8Expands}};
-                for (const Tile& t : plan.shrink)
-                    if (t.adapter == a && t.fused_index >= (int)i && t.fused_index < (int)i + cg) e.slot[t.fused_index - i] = (int16_t)(t.u_row / kTileM);
-                if (e.slot[0] < kFp8Expands || e.slot[1] < kFp8Expands) expands.push_back(e);
-            }
-            for (int c = 0; c < cg; ++c) {
-                Tile t = plan.fused[std::min(i + c, plan.fused.size() - 1)];
-                if (i + c >= plan.fused.size()) t.nrows = 0;
-                t.u_row = e0;
-                t.adapter = (int)expands.size() - e0;
-                groups.push_back(t);
-            }
+        groups = plan.fused;
+        for (Tile& t : groups) t.adapter = t.u_row = 0;
+        for (const Tile& t : plan.shrink) {                    // (in the order of tiles)
+            Tile& g = groups[t.fused_index];
+            if (g.adapter++ == 0) g.u_row = (int)expands.size();
+            Fp8Expand e{t.adapter, t.u_row / kTileM, {}};
+            for (int s = 0; s < n_m; ++s)
+                for (int row = std::max(plan.seg_off[s], t.row0); plan.seg_id[s] == t.adapter && row < std::min(plan.seg_off[s + 1], t.row0 + t.nrows); ++row)
+                    e.rows[(row - t.row0) / 32] |= 1u << (row - t.row0) % 32;
+            expands.push_back(e);
         }
     } else {
         make_groups(plan.fused, cg, false, h->u_rows - kTileM, &groups);
@@ -1866,7 +1870,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     if (timing) cudaEventRecord(rec.ev[1], stream);
     if (encode_u8_sw128(h, &q.tm_x, f.x8, h->d_in, T, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_u8_sw128(h, &q.tm_w, f.w8, h->d_in, h->d_out, (uint32_t)(s8.wide ? 64 : s8.tile_n)) != CUDA_SUCCESS ||
-        encode_2d(h, &q.tm_u, merged ? h->u_pairs : h->u_ws, h->rank, merged ? (kFp8Expands + 1) * kTileM : h->u_rows, 64,
+        encode_2d(h, &q.tm_u, merged ? h->u_pairs : h->u_ws, h->rank, merged ? kFp8Expands * kTileM : h->u_rows, 64,
                   (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_2d(h, &q.tm_y, y, h->d_out, T, s8.wide ? 64 : 32, 32) != CUDA_SUCCESS)
         return LORA_ECUDA;
@@ -1886,12 +1890,13 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.k_blocks = q_groups;
     q.k_lora = ceil_div(h->rank, 64);
     for (const Tile& t : groups) q.most_expands = std::max(q.most_expands, merged ? t.adapter : t.adapter ? 1 : 0);
-    for (q.lora_stages = q.k_lora;; --q.lora_stages)
+    for (q.lora_stages = q.k_lora;; --q.lora_stages) {
         if (q.k_lora % q.lora_stages == 0 &&
             fp8_window(512 / s8.tile_n, q_groups / s8.parts, q.most_expands * (q.k_lora / q.lora_stages), q.lora_stages) <= s8.stages)
             break;
-        else if (q.lora_stages == 1)
-            return LORA_EUNSUPPORTED;                      // (one stage a block: a ring is longer than the buffers are many)
+        if (q.lora_stages == 1) return LORA_EUNSUPPORTED;  // (one stage a block: a ring is longer than the buffers are many)
+    }
+    q.expand_blocks = q.k_lora / q.lora_stages;
     q.d_out = h->d_out;
     q.parts = s8.parts;
     q.a_rows = s8.a_rows;

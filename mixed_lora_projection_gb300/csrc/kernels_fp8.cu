@@ -144,9 +144,10 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
 // lora_stages stages; nb blocks and ns stages in all.
 struct Work {
     Tile tile;
-    int n0, kb0, nk, nb, ns, e0;                       // e0: its first expand, where tiles hold several adapters
+    int n0, kb0, nk, nb, ns;
+    int e0;                                            // its first expand, where tiles hold several adapters
 };
-template <int CG, int NT>
+template <int CG, int NT, bool MERGED>
 __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, int u, int rank, int part) {
     Work w;
     const int per = p.n_groups * p.raster_group;
@@ -156,24 +157,32 @@ __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, in
     w.n0 = (g * p.raster_group + r % gw) * NT;
     w.kb0 = part * p.k_blocks / p.parts;
     w.nk = (part + 1) * p.k_blocks / p.parts - w.kb0;
-    // the expands go to the parts of K in turn, a single one to the last
-    const int expands = p.merged ? w.tile.adapter : w.tile.adapter != 0, e = part * expands / p.parts;
-    const int mine = (part + 1) * expands / p.parts - e;
-    w.e0 = w.tile.u_row + e;
-    w.nb = w.nk + mine * (p.k_lora / p.lora_stages);
-    w.ns = w.nk + mine * p.k_lora;
+    if (MERGED) {                                      // (the expands go to the parts of K in turn)
+        const int e = part * w.tile.adapter / p.parts, mine = (part + 1) * w.tile.adapter / p.parts - e;
+        w.e0 = w.tile.u_row + e;
+        w.nb = w.nk + mine * p.expand_blocks;
+        w.ns = w.nk + mine * p.k_lora;
+        return w;
+    }
+    const bool expand = w.tile.adapter && part == p.parts - 1;
+    w.nb = w.nk + (expand ? p.expand_blocks : 0);
+    w.ns = w.nk + (expand ? p.k_lora : 0);
     return w;
 }
 
+// In place of the scale of a row that takes nothing of an expand (a product's NaN is 0x7fffffff).
+constexpr uint32_t kNothing = 0xffffffffu;
+
 // The scales of a block, as warp 3 lays them out for the epilogue, and its unit's place.
 struct ScaleSlot {
-    float f[2][kTileM];                                // per half of the columns and row: xs ws
+    float f[2][kTileM];                                // per half of the columns and row: xs ws, or kNothing
     int4 unit;                                         // first row, rows, first column, blocks
 };
 
 // CG: CTAs of the MMA's group; NT: columns of a TMEM buffer, half of them in each epilogue thread's registers. Registers
 // of the launch are dealt out anew: the loading warps' to the accumulators (LOW x 128 + HIGH x 256 <= 384 x the launch's).
-template <int CG, int NT, int LOW, int HIGH>
+// MERGED: tiles hold several adapters. A form of its own: the same in all of them cost the pairs a tenth, and more.
+template <int CG, int NT, int LOW, int HIGH, bool MERGED>
 __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_constant__ Fp8Params p) {
     constexpr int EW = 8;                              // epilogue warps
     constexpr int kCols = NT / 2;                      // columns of an epilogue thread
@@ -248,8 +257,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             bool ok = true;
             const uint32_t tx = CG * (a_bytes + b_bytes);
             for (int u = first; u < n_units && ok; u += step) {
-                const Work w = decode<CG, NT>(p, tiles, u, rank, part);
-                const CUtensorMap* bm = &bmaps[w.ns > w.nk && !p.merged ? w.tile.adapter - 1 : 0];
+                const Work w = decode<CG, NT, MERGED>(p, tiles, u, rank, part);
+                const CUtensorMap* bm = &bmaps[w.ns > w.nk && !MERGED ? w.tile.adapter - 1 : 0];
                 int u_row = w.tile.u_row, e = w.e0, ku = 0;
                 if (w.ns > w.nk && !p.inline_wl && acquired != w.tile.adapter) {
                     tensormap_acquire(bm);
@@ -264,18 +273,18 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     const uint32_t fb = CG > 1 ? map_to_rank(bar, 0) : bar;
                     const uint32_t sa = smem_addr(a_ring + (size_t)stage * a_bytes), sb = smem_addr(b_ring + (size_t)stage * b_bytes);
                     const bool main = b < w.nk;
-                    if (!main && ku == 0) {
-                        if (p.late_u) griddep_wait();
-                        if (p.merged) {
+                    const int k = main ? (w.kb0 + b) * kFp8Group : (MERGED ? ku : b - w.nk) * 64;
+                    if (!main && p.late_u) griddep_wait();
+                    if (MERGED && !main) {
+                        if (ku == 0) {
                             bm = &bmaps[p.expand[e].adapter - 1];
-                            u_row = p.expand[e].slot[rank] * kTileM;
-                            ++e;
+                            u_row = p.expand[e++].slot * kTileM;
                         }
+                        if (++ku == p.k_lora) ku = 0;
                     }
-                    const int k = main ? (w.kb0 + b) * kFp8Group : ku * 64;
                     if (elect_one()) {
                         if (leader) mbar_arrive_expect_tx(bar, tx, 1u);
-                        tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : u_row, 1u);
+                        tma_load_2d<CG>(sa, main ? &p.tm_x : &p.tm_u, fb, k, main ? w.tile.row0 : MERGED ? u_row : w.tile.u_row, 1u);
                         if (CG == 1) {
                             tma_load_2d<CG>(sb, main ? &p.tm_w : bm, fb, k, w.n0, 1u);
                         } else {                             // a pair's CTA holds half of the columns of each half
@@ -284,7 +293,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                         }
                     }
                     __syncwarp();
-                    if (!main && ++ku == p.k_lora) ku = 0;
                     ++issued;
                     if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             uint32_t phase = 0;
             bool ok = true;
             for (int u = first; u < n_units && ok; u += step) {
-                const Work w = decode<CG, NT>(p, tiles, u, rank, part);
+                const Work w = decode<CG, NT, MERGED>(p, tiles, u, rank, part);
                 for (int b = 0; b < w.nb; ++b, ++blk) {
                     const bool main = b < w.nk;
                     const int ns = main ? 1 : p.lora_stages;
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             int blk = 0;
             bool ok = true;
             for (int u = first; u < n_units && ok; u += step) {
-                const Work w = decode<CG, NT>(p, tiles, u, rank, part);
+                const Work w = decode<CG, NT, MERGED>(p, tiles, u, rank, part);
                 // (rows and columns past the unit's last take that one's; read from L2, as TMA reads: nothing of an earlier launch's
                 // L1 is used where this one did not wait)
                 const float *xs[4], *ws[2];
@@ -409,10 +417,17 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                             if (blk >= kBufs) ok = wait_all(smem_addr(&tfull[buf * kHalves + h]), (blk / kBufs - 1) & 1, abort_flag, p.status, limit);
                         if (!ok) break;
                         ScaleSlot& slot = slots[blk % kSlots];
+                        if (MERGED && b0 + k >= w.nk) {
+                            const uint32_t* rows = p.expand[w.e0 + (b0 + k - w.nk) / p.expand_blocks].rows;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 4; ++i)
+                                slot.f[0][lane + 32 * i] = slot.f[1][lane + 32 * i] = rows[i] >> lane & 1 ? 1.f : __uint_as_float(kNothing);
+                        } else {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) slot.f[h][lane + 32 * i] = b0 + k < w.nk ? x[i][k] * c[h][k] : 1.f;
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) slot.f[h][lane + 32 * i] = b0 + k < w.nk ? x[i][k] * c[h][k] : 1.f;
+                        }
                         if (lane == 0) slot.unit = make_int4(w.tile.row0, w.tile.nrows, w.n0, w.nb);
                         __syncwarp();
                         if (lane < kHalves) mbar_arrive(smem_addr(&tfull[buf * kHalves + lane]));
@@ -474,6 +489,17 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                     };
                     if (CG == 1 && q * 32 >= nrows) {        // no row of the unit's lies here
                         release();
+                    } else if (MERGED && __any_sync(0xffffffffu, __float_as_uint(f) == kNothing)) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int c = 0; c < kCols / 16; ++c) {
+                            tmem_ld16(t + 16 * c, v);
+                            tmem_wait16(v);
+                            if (c + 1 == kCols / 16) release();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (__float_as_uint(f) != kNothing) acc[8 * c + i] = fma2(pair(v[2 * i], v[2 * i + 1]), f2, acc[8 * c + i]);
+                        }
                     } else {                                 // the next columns' load runs under these ones' sums
                         uint32_t v[2][16];
                         tmem_ld16(t, v[0]);
@@ -550,7 +576,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
             cluster_sync();
             if (ok) {
                 // each CTA adds its share of the columns over the parts, in their order
-                const Work w = decode<CG, NT>(p, tiles, first, rank, part);
+                const Work w = decode<CG, NT, MERGED>(p, tiles, first, rank, part);
                 const int v0 = part * (NT / 8) / p.parts, vecs = (part + 1) * (NT / 8) / p.parts - v0;
                 for (int i = (int)threadIdx.x - 128; i < w.tile.nrows * vecs; i += 32 * EW) {
                     const int r = i / vecs, c = 8 * (v0 + i - r * vecs);
@@ -749,10 +775,13 @@ namespace {
 // 384 threads of 168 registers, dealt out anew: 72 x 128 + 216 x 256 = 168 x 384. A few bytes spilled in the loading warps
 // cost a tenth to a fifth of all (pairs with buffers of 256 columns, 9,728 rows of 5,120 -> 5,120: 198 us; with 64 and 216,
 // 40 bytes, 223).
-constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 72, 216>;
-constexpr auto kSingle = dev::lora_fp8_kernel<1, 256, 72, 216>;
-constexpr auto kNarrow = dev::lora_fp8_kernel<1, 128, 72, 216>;
-inline auto kernel_of(int wide, int tile_n) { return wide ? kWide : tile_n == 256 ? kSingle : kNarrow; }
+constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 72, 216, false>;
+constexpr auto kSingle = dev::lora_fp8_kernel<1, 256, 72, 216, false>, kSingleMerged = dev::lora_fp8_kernel<1, 256, 72, 216, true>;
+constexpr auto kNarrow = dev::lora_fp8_kernel<1, 128, 72, 216, false>, kNarrowMerged = dev::lora_fp8_kernel<1, 128, 72, 216, true>;
+inline auto kernel_of(int wide, int tile_n, int merged) {
+    if (wide) return kWide;
+    return tile_n == 256 ? (merged ? kSingleMerged : kSingle) : merged ? kNarrowMerged : kNarrow;
+}
 }  // namespace
 
 size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages) {
@@ -793,7 +822,7 @@ cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
 cudaError_t fp8_prepare_device() {
     cudaError_t r = cudaFuncSetAttribute(dev::lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (r != cudaSuccess) return r;
-    for (const auto k : {kWide, kSingle, kNarrow}) {
+    for (const auto k : {kWide, kSingle, kNarrow, kSingleMerged, kNarrowMerged}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
     }
@@ -826,7 +855,7 @@ int fp8_max_clusters(int tile_n, int parts) {
     config(p, parts, nullptr, &cfg, attr);
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel_of(0, tile_n), &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel_of(0, tile_n, 0), &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
@@ -851,8 +880,8 @@ cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream) {
     // stages: a lap is no shorter than the stages of the blocks between two uses of a TMEM buffer; an A stage's 128 rows lie
     // inside the rings; the parts' sums take the rings' place
     const size_t rings = (size_t)p.stages * (p.a_rows + tile_rows) * kFp8StageRow;
-    if (p.lora_stages < 1 || p.k_lora % p.lora_stages || p.most_expands < 0 ||
-        p.stages < fp8_window(512 / p.tile_n, p.k_blocks / p.parts, p.most_expands * (p.k_lora / p.lora_stages), p.lora_stages) ||
+    if ((p.wide && p.merged) || p.lora_stages < 1 || p.k_lora % p.lora_stages || p.most_expands < 0 || p.expand_blocks != p.k_lora / p.lora_stages ||
+        p.stages < fp8_window(512 / p.tile_n, p.k_blocks / p.parts, p.most_expands * p.expand_blocks, p.lora_stages) ||
         fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages) > (size_t)kSmemLimit ||
         (size_t)p.stages * tile_rows < (size_t)(kTileM - p.a_rows) || (p.parts > 1 && rings < (size_t)p.tile_n * kTileM * 4))
         return cudaErrorInvalidValue;
@@ -862,7 +891,7 @@ cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     config(p, grid, stream, &cfg, attr);
-    return cudaLaunchKernelEx(&cfg, kernel_of(p.wide, p.tile_n), p);
+    return cudaLaunchKernelEx(&cfg, kernel_of(p.wide, p.tile_n, p.merged), p);
 }
 
 }  // namespace lora

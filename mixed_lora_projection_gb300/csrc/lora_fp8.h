@@ -14,9 +14,10 @@ constexpr int kFp8InlineAdapters = 8; // named in a call whose work list travels
 constexpr int kFp8Expands = 16;       // pairs of a row tile and an adapter, where tiles hold several
 constexpr int kFp8StageRow = 128;     // bytes of a stage's row: one group of e4m3, 64 bf16 of the expand
 
-// One expand of a row group whose tiles hold several adapters: U blocks of 128 rows, per CTA of a pair.
+// One expand of a tile that holds rows of several adapters.
 struct Fp8Expand {
-    int16_t adapter, slot[2];
+    int adapter, slot;                // its U is the 128 rows from 128 slot on
+    uint32_t rows[kTileM / 32];       // whose bit is clear take nothing of it, a NaN of the adapter's least of all
 };
 
 // One launch. Units are (row group, output tile) blocks of Y; a row group is one planner tile, or two
@@ -24,7 +25,7 @@ struct Fp8Expand {
 struct Fp8Params {
     CUtensorMap inline_bmaps[kFp8InlineAdapters];   // B_a [d_out, rank] bf16 (inline work list)
     Tile inline_tiles[kInlineTiles];
-    // merged: a tile's u_row is its group's first expand, its adapter their number; U blocks by `slot`
+    // merged (single CTAs): a tile's u_row is its first expand, its adapter their number
     Fp8Expand expand[kFp8Expands];
     int merged;
     int inline_wl;
@@ -46,6 +47,7 @@ struct Fp8Params {
     int k_lora;                       // ceil(rank / 64)
     int lora_stages;                  // of an expand's block: all k_lora where the ring is long enough, else a part of them
     int most_expands;                 // of a unit
+    int expand_blocks;                // of an expand: k_lora / lora_stages
     int d_out;
     int parts;                        // K parts of a unit (1 in the wide form)
     int a_rows;                       // rows of an A box: 128, or fewer (a multiple of 16) for a batch of one tile

@@ -414,3 +414,22 @@ def test_more_expands_than_base_blocks(d_in, d_out, rank, rows, ids):
     y = c.run()
     c.check(y)
     assert all(torch.equal(c.run(), y) for _ in range(3))
+
+
+@pytest.mark.parametrize("rows,d_out", [([5, 7, 4, 9], 1288), ([60, 100, 40, 80], 1288), ([90, 300, 100, 150, 90, 20], 20480)])
+def test_an_adapter_with_a_nan_stays_off_other_adapters_rows(rows, d_out):
+    # (rows without one may share a tile with it and add zero times its values, as in the bf16 projection)
+    ids = [1, 2, 0, 3, 1, 0][:len(rows)]
+    c = Case(1024, d_out, 64, rows, ids, seed=4)
+    y = c.run()
+    c.check(y)
+    c.b[1][5, 3] = float("nan")
+    c.b[1][9] = float("inf")
+    c.a[1][2, 2] = float("inf")
+    bad = c.run()
+    mine = slice(c.off[1], c.off[2])
+    assert torch.isnan(bad[mine, 5]).all()
+    for i, a in enumerate(ids):
+        if a not in (0, 2):
+            r = slice(c.off[i], c.off[i + 1])
+            assert torch.equal(bad[r], y[r])
