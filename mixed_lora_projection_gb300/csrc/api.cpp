@@ -1608,8 +1608,8 @@ int validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments
 
 // The batch in whole tiles of 128 rows, whatever adapters their rows name: each pair of a tile and an adapter has a U block
 // of its own and an expand that its rows alone take. Fewer tiles than the planner's, none of which holds two adapters: 94
-// rows of nine segments and two adapters, 5,120 -> 12,288, rank 256, 26 us for 74; two rows of two adapters, rank 16, 19 for
-// 45; and 223 rows of five segments, whose two tiles no SM pair may share, 25 for 40. The tiles are in `plan`; the pairs,
+// rows of nine segments and two adapters, 5,120 -> 12,288, rank 256, 28 us for 74; two rows of two adapters, rank 16, 18 for
+// 45; and 223 rows of five segments, whose two tiles no SM pair may share, 26 for 40. The tiles are in `plan`; the pairs,
 // in the order of tiles, are the shrink's tiles. False where they do not fit.
 bool merge_tiles(int T, Plan* plan) {
     const int nf = ceil_div(T, kTileM), n_used = (int)plan->used_adapters.size();
