@@ -341,6 +341,19 @@ int lora_linear_describe(lora_linear* h, int T, const int32_t* seg_offsets,
                          int* n_units, int* grid, int* stages, int* has_shrink, int* unit_order);
 
 /*
+ * lora_linear_describe_fp8 -- what lora_linear_forward_fp8 would launch for T rows in these segments, without
+ * launching. Of the projection: cluster (CTAs of a cluster: 2 on SM pairs, else its parts of K), tile_n (columns of a
+ * unit), k_parts (parts of K that are summed apart), grid (CTAs), merged (1: tiles hold rows of several adapters). Of the
+ * adapters' shrink ahead of it: shrink (0 none, 1 the kernel that splits K over a cluster, 2 the bf16 kernel's units),
+ * shrink_cluster (1: the parts of K; 2: 2 on SM pairs), shrink_grid. uploaded: 1 where the work list is copied to
+ * the device, which a capture refuses. Any pointer may be NULL; T = 0 gives zeros. Returns LORA_OK, LORA_EINVAL or
+ * LORA_ENOMEM. Diagnostics and tests.
+ */
+int lora_linear_describe_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* seg_adapter_ids,
+                             int n_seg, int* cluster, int* tile_n, int* k_parts, int* grid, int* merged, int* shrink,
+                             int* shrink_cluster, int* shrink_grid, int* uploaded);
+
+/*
  * lora_linear_shape -- the launch shape lora_linear_forward (w4 = 0) or
  * lora_linear_forward_w4 (w4 = 1) would choose, computed on the host alone (no device, no
  * handle): for d_in, d_out, rank as in lora_linear_create, a GPU with num_sms SMs (>= 2), the

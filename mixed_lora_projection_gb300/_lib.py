@@ -55,6 +55,7 @@ SIGNATURES = {
     "lora_linear_timing": (C.c_int, [P, C.c_int, C.POINTER(C.c_double), C.POINTER(C.c_longlong),
                                      C.POINTER(C.c_longlong)]),
     "lora_linear_describe": (C.c_int, [P, C.c_int, I32P, I32P, C.c_int, IP, IP, IP, IP, IP, IP, IP]),
+    "lora_linear_describe_fp8": (C.c_int, [P, C.c_int, I32P, I32P, C.c_int] + [IP] * 9),
     "lora_linear_error_string": (C.c_char_p, [C.c_int]),
     "lora_linear_shape": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, I32P, I32P, C.c_int, C.c_int,
                                     IP, IP, IP, IP, IP, IP, IP]),

@@ -1637,29 +1637,36 @@ bool merge_tiles(int T, Plan* plan) {
     return true;
 }
 
-int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T, const int32_t* seg_offsets,
-                     const int32_t* seg_adapter_ids, int n_seg, const void* const* A, const void* const* B,
-                     const float* scale, int n_adapters, void* y, cudaStream_t stream) {
-    if (!h) return LORA_EINVAL;
-    int rc = validate_fp8(h->d_in, h->d_out, h->rank, h->max_tokens, h->max_segments, f, x, T, seg_offsets,
-                          seg_adapter_ids, n_seg, A, B, scale, n_adapters, y);
-    if (rc != LORA_OK || T == 0) return rc;
-    Plan plan;
-    rc = plan_segments(seg_offsets, seg_adapter_ids, n_seg, T, n_adapters, &plan);
+// What a call launches.
+struct Fp8Call {
+    Plan plan;                    // adapters by their place among those that it names
+    Fp8Shape s8;
+    bool merged = false;
+    std::vector<Tile> groups;     // the base's row groups, two tiles each on SM pairs
+    std::vector<Fp8Expand> expands;
+    Shape sh;                     // the shrink: its tiles; of the bf16 kernel's units, where parts is 0, the launch's shape too
+    int rank_tiles = 1, parts = 0, shrink_n = 0;
+    bool inline_wl = false;
+};
+
+// n_adapters < 0: of any number. On the handle's device.
+int plan_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* seg_adapter_ids, int n_seg, int n_adapters, Fp8Call* call) {
+    Plan& plan = call->plan;
+    const int rc = plan_segments(seg_offsets, seg_adapter_ids, n_seg, T, n_adapters, &plan);
     if (rc != LORA_OK) return rc;
     const int nf = (int)plan.fused.size(), n_m = (int)plan.seg_id.size();
     if (nf > h->max_fused) return LORA_EINVAL;
     const int n_used = (int)plan.used_adapters.size();
-    std::vector<int> compact(n_adapters + 1, 0);
-    for (int k = 0; k < n_used; ++k) compact[plan.used_adapters[k] + 1] = k + 1;
-    for (Tile& t : plan.fused) t.adapter = compact[t.adapter];
-    for (Tile& t : plan.shrink) t.adapter = compact[t.adapter];
-    for (int32_t& a : plan.seg_id) a = compact[a];
+    const auto& used = plan.used_adapters;                 // (in rising order)
+    auto place = [&](int a) { return a ? (int)(std::lower_bound(used.begin(), used.end(), a - 1) - used.begin()) + 1 : 0; };
+    for (Tile& t : plan.fused) t.adapter = place(t.adapter);
+    for (Tile& t : plan.shrink) t.adapter = place(t.adapter);
+    for (int32_t& a : plan.seg_id) a = place(a);
     for (int i = 0; i < nf; ++i) plan.fused[i].fused_index = plan.fused[i].split_index = i;
 
-    DeviceGuard guard(h->device);
-    Fp8Shape s8 = fp8_shape(h, plan, false);
-    bool merged = false;
+    Fp8Shape& s8 = call->s8;
+    bool& merged = call->merged;
+    s8 = fp8_shape(h, plan, false);
     if (h->allow_inline && n_used > 1) {
         Plan whole = plan;
         if (merge_tiles(T, &whole)) {
@@ -1672,8 +1679,8 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         }
     }
     const int cg = s8.wide ? 2 : 1;
-    std::vector<Tile> groups;
-    std::vector<Fp8Expand> expands;
+    std::vector<Tile>& groups = call->groups;
+    std::vector<Fp8Expand>& expands = call->expands;
     if (merged) {
         groups = plan.fused;
         for (Tile& t : groups) t.adapter = t.u_row = 0;
@@ -1693,8 +1700,8 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
 
     // The shrink (bf16) is launched ahead: the bf16 kernel's units over rank tiles, or, where that finishes sooner, one
     // tile and one part of K a CTA (by the K steps' cycles that its units were measured at).
-    Shape sh;
-    int rank_tiles = 1, parts = 0, shrink_n = 0;
+    Shape& sh = call->sh;
+    int &rank_tiles = call->rank_tiles, &parts = call->parts, &shrink_n = call->shrink_n;
     if (n_used) {
         double best = 0;                                   // of the bf16 kernel's units, which know no tiles of several adapters
         if (!merged) {
@@ -1729,7 +1736,6 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         if (parts) sh.shrink_groups = plan.shrink;
     }
     const int nst = n_used ? (int)sh.shrink_groups.size() : 0;
-    const int a_rows = parts ? shrink_n : sh.shrink_n / sh.cs;   // of an A_a box
     for (const Tile& t : groups)
         if (t.adapter < 0 || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T ||
             (merged ? t.u_row < 0 || t.u_row + t.adapter > (int)expands.size()
@@ -1742,10 +1748,53 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         if (t.adapter < 1 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T) return LORA_EINVAL;
     }
 
-    const bool inline_wl = h->allow_inline && nft + nst <= kInlineTiles && n_m <= kInlineSegs && n_used <= (parts ? kFp8InlineAdapters : kInlineAdapters);
+    call->inline_wl = h->allow_inline && nft + nst <= kInlineTiles && n_m <= kInlineSegs && n_used <= (parts ? kFp8InlineAdapters : kInlineAdapters);
+    return merged && !call->inline_wl ? LORA_EINVAL : LORA_OK;   // (merge_tiles has seen to it)
+}
+
+// The base's grid.
+int fp8_grid(const lora_linear* h, const Fp8Call& c) {
+    const int units = (int)c.groups.size() / (c.s8.wide ? 2 : 1) * c.s8.n_ntiles;
+    return c.s8.wide ? std::min(units, usable_sms(h) / 2) * 2 : c.s8.parts > 1 ? units * c.s8.parts : std::min(units, usable_sms(h));
+}
+// The shrink's, of the K-part kernel.
+int shrink_grid(const Fp8Call& c, int rank) { return (int)c.plan.shrink.size() * ceil_div(rank, c.shrink_n) * c.parts; }
+// The shrink by the bf16 kernel's units: what its launch's shape depends on, and its grid (0: none).
+int fill_shrink_units(lora_linear* h, const Fp8Call& c, GemmParams* p) {
+    p->n_shrink = (int)c.sh.shrink_groups.size() / c.sh.cs;
+    p->shrink_ntiles = c.rank_tiles;
+    p->tile_n = c.sh.tile_n;
+    p->shrink_n = c.sh.shrink_n;
+    p->stages = c.sh.stages;
+    p->bk = 64;
+    p->cluster_size = c.sh.cs;
+    const int slots = c.sh.cs > 1 ? std::min(max_clusters(h, *p), usable_sms(h) / c.sh.cs) : usable_sms(h);
+    return std::min(p->n_shrink * c.rank_tiles, std::max(slots, 0)) * c.sh.cs;
+}
+
+int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T, const int32_t* seg_offsets,
+                     const int32_t* seg_adapter_ids, int n_seg, const void* const* A, const void* const* B,
+                     const float* scale, int n_adapters, void* y, cudaStream_t stream) {
+    if (!h) return LORA_EINVAL;
+    int rc = validate_fp8(h->d_in, h->d_out, h->rank, h->max_tokens, h->max_segments, f, x, T, seg_offsets,
+                          seg_adapter_ids, n_seg, A, B, scale, n_adapters, y);
+    if (rc != LORA_OK || T == 0) return rc;
+    DeviceGuard guard(h->device);
+    Fp8Call call;
+    rc = plan_fp8(h, T, seg_offsets, seg_adapter_ids, n_seg, n_adapters, &call);
+    if (rc != LORA_OK) return rc;
+    const Plan& plan = call.plan;
+    const Fp8Shape& s8 = call.s8;
+    const Shape& sh = call.sh;
+    const std::vector<Tile>& groups = call.groups;
+    const std::vector<Fp8Expand>& expands = call.expands;
+    const bool merged = call.merged, inline_wl = call.inline_wl;
+    const int parts = call.parts, shrink_n = call.shrink_n, cg = s8.wide ? 2 : 1;
+    const int nft = (int)groups.size(), n_m = (int)plan.seg_id.size(), n_used = (int)plan.used_adapters.size();
+    const int nst = n_used ? (int)sh.shrink_groups.size() : 0;
+    const int a_rows = parts ? shrink_n : sh.shrink_n / sh.cs;   // of an A_a box
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return LORA_ECUDA;
-    if (merged && !inline_wl) return LORA_EINVAL;         // (merge_tiles has seen to it)
     if (capture != cudaStreamCaptureStatusNone && !inline_wl) return LORA_EUNSUPPORTED;   // as lora_linear_forward
 
     const int q_groups = ceil_div(h->d_in, kFp8Group);
@@ -1848,22 +1897,14 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         p.status = h->status;
         p.wait_limit_ns = h->wait_limit_ns;
         p.n_seg = n_m;
-        p.n_shrink = nst / sh.cs;
-        p.shrink_ntiles = rank_tiles;
-        p.tile_n = sh.tile_n;
-        p.shrink_n = sh.shrink_n;
-        p.stages = sh.stages;
         p.k_main_blocks = ceil_div(h->d_in, 64);
         p.k_lora_blocks = ceil_div(h->rank, 64);
-        p.bk = 64;
-        p.mma_group = h->mma_group ? h->mma_group : (sh.cs > 1 || nf == 1) ? 2 : 1;
+        p.mma_group = h->mma_group ? h->mma_group : (sh.cs > 1 || plan.fused.size() == 1) ? 2 : 1;
         p.d_out = h->d_out;
         p.rank = h->rank;
-        p.cluster_size = sh.cs;
         p.debug_stall = h->debug_stall;
-        const int slots = sh.cs > 1 ? std::min(max_clusters(h, p), usable_sms(h) / sh.cs) : usable_sms(h);
-        if (slots < 1) return LORA_ECUDA;
-        if (launch_gemm(p, std::min(p.n_shrink * rank_tiles, slots) * sh.cs, stream) != cudaSuccess) return LORA_ECUDA;
+        const int grid = fill_shrink_units(h, call, &p);
+        if (grid < 1 || launch_gemm(p, grid, stream) != cudaSuccess) return LORA_ECUDA;
         ++h->launches;
         rec.has_shrink = true;
     }
@@ -1904,9 +1945,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.wide = s8.wide;
     q.late_u = parts && inline_wl;                     // (a list that was copied is read after the wait)
     q.debug_stall = h->debug_stall;
-    const int units = q.n_groups * q.n_ntiles;
-    const int grid = s8.wide ? std::min(units, usable_sms(h) / 2) * 2 : s8.parts > 1 ? units * s8.parts : std::min(units, usable_sms(h));
-    if (launch_fp8(q, grid, stream) != cudaSuccess) return LORA_ECUDA;
+    if (launch_fp8(q, fp8_grid(h, call), stream) != cudaSuccess) return LORA_ECUDA;
     ++h->launches;
     if (timing) {
         cudaEventRecord(rec.ev[2], stream);
@@ -1929,6 +1968,47 @@ extern "C" int lora_linear_forward_fp8(lora_linear* h, const void* x8, const flo
         return forward_fp8_impl(h, Fp8Operands{x8, w8, x_scales, w_scales}, x, T, seg_offsets, seg_adapter_ids, n_seg, A, B,
                                 scale, n_adapters, y, reinterpret_cast<cudaStream_t>(stream));
     } catch (...) {   // host memory for the plan
+        return LORA_ENOMEM;
+    }
+}
+
+extern "C" int lora_linear_describe_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* seg_adapter_ids,
+                                        int n_seg, int* cluster, int* tile_n, int* k_parts, int* grid, int* merged,
+                                        int* shrink, int* shrink_cluster, int* shrink_grid_, int* uploaded) {
+    if (!h || h->d_in % 16 || T > h->max_tokens || n_seg > h->max_segments) return LORA_EINVAL;
+    try {
+        DeviceGuard guard(h->device);
+        Fp8Call c;
+        int v[9] = {};
+        if (T == 0) {
+            const int rc = plan_segments(seg_offsets, seg_adapter_ids, n_seg, T, -1, &c.plan);
+            if (rc != LORA_OK) return rc;
+        } else {
+            const int rc = plan_fp8(h, T, seg_offsets, seg_adapter_ids, n_seg, -1, &c);
+            if (rc != LORA_OK) return rc;
+            v[0] = c.s8.wide ? 2 : c.s8.parts;
+            v[1] = c.s8.tile_n;
+            v[2] = c.s8.parts;
+            v[3] = fp8_grid(h, c);
+            v[4] = c.merged;
+            if (c.parts) {
+                v[5] = 1;
+                v[6] = c.parts;
+                v[7] = shrink_grid(c, h->rank);
+            } else if (!c.plan.shrink.empty()) {
+                GemmParams p;
+                memset(&p, 0, sizeof(p));
+                v[5] = 2;
+                v[6] = c.sh.cs;
+                v[7] = fill_shrink_units(h, c, &p);
+            }
+            v[8] = !c.inline_wl;
+        }
+        int* const out[9] = {cluster, tile_n, k_parts, grid, merged, shrink, shrink_cluster, shrink_grid_, uploaded};
+        for (int i = 0; i < 9; ++i)
+            if (out[i]) *out[i] = v[i];
+        return LORA_OK;
+    } catch (...) {
         return LORA_ENOMEM;
     }
 }

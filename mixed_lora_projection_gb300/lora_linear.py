@@ -292,3 +292,13 @@ class LoraLinear:
                "lora_linear_describe")
         return dict(zip(("tile_n", "n_tiles", "n_units", "grid", "stages", "has_shrink", "unit_order"),
                         [x.value for x in v]))
+
+    def describe_fp8(self, T, seg_offsets, seg_ids) -> dict:
+        """What ``forward_fp8`` would launch (lora_linear_describe_fp8)."""
+        off, _ = _i32(seg_offsets)
+        ids, n = _i32(seg_ids)
+        v = [C.c_int() for _ in range(9)]
+        _check(self._lib.lora_linear_describe_fp8(self._h, T, off, ids, n, *[C.byref(x) for x in v]),
+               "lora_linear_describe_fp8")
+        return dict(zip(("cluster", "tile_n", "k_parts", "grid", "merged", "shrink", "shrink_cluster", "shrink_grid",
+                         "uploaded"), [x.value for x in v]))

@@ -1,0 +1,50 @@
+"""What lora_linear_forward_fp8 launches (lora_linear_describe_fp8), and its forms that a batch's size alone selects, against
+64 bits under the bound of test_gpu_fp8.py."""
+import pytest
+import torch
+
+from mixed_lora_projection_gb300 import LoraLinear
+from test_gpu_fp8 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def described(c):
+    return c.linear.describe_fp8(c.T, c.off, c.ids)
+
+
+# long prompts: the bf16 kernel's units run the shrink, on SM pairs, from an uploaded list; groups of an odd number of tiles
+# are padded
+@pytest.mark.parametrize("rows,ids", [([16384], [1]), ([5400, 5150, 30, 4400], [1, 2, 0, 3]), ([48, 16300], [0, 1])])
+def test_shrink_of_a_long_prompt(rows, ids):
+    c = Case(5120, 2056, 256, rows, ids, seed=len(rows))
+    d = described(c)
+    assert (d["shrink"], d["shrink_cluster"], d["uploaded"]) == (2, 2, 1), d
+    y = c.run()
+    c.check(y)
+    assert torch.equal(c.run(), y)
+
+
+def test_what_is_described():
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ll = LoraLinear(5120, 12288, 256, 2048, 16)
+    none = ll.describe_fp8(0, [0], [])
+    assert not any(none.values())
+    base = ll.describe_fp8(48, [0, 48], [0])
+    assert base["shrink"] == base["shrink_grid"] == base["merged"] == base["uploaded"] == 0 and 1 <= base["grid"] <= sms
+    one = ll.describe_fp8(48, [0, 48], [1])
+    assert one["shrink"] == 1 and one["shrink_cluster"] >= 1 and 1 <= one["shrink_grid"] <= sms and one["merged"] == 0
+    many = ll.describe_fp8(48, list(range(0, 49, 8)), [1, 2, 3, 4, 5, 6])
+    assert many["merged"] == 1 and many["shrink"] == 1 and many["cluster"] == many["k_parts"]
+    wide = ll.describe_fp8(2048, [0, 2048], [0])
+    assert wide["cluster"] == 2 and wide["k_parts"] == 1 and wide["tile_n"] == 256 and wide["grid"] == sms // 2 * 2
+    assert ll.describe_fp8(48, [0, 48], [2 ** 31 - 1])["shrink"] == 1
+    for T, off, ids in ((2049, [0, 2049], [0]), (48, [0, 47], [0]), (48, [1, 48], [0]), (48, [0, 48], [-1]), (1, [0] + [1] * 17, [0] * 17)):
+        with pytest.raises(Exception, match="invalid argument"):
+            ll.describe_fp8(T, off, ids)
+    ll.close()
+    with pytest.raises(Exception):
+        ll.describe_fp8(48, [0, 48], [0])
+    odd = LoraLinear(264, 136, 16, 48, 4)                    # (d_in no multiple of 16: bf16 alone)
+    with pytest.raises(Exception, match="invalid argument"):
+        odd.describe_fp8(48, [0, 48], [0])
