@@ -1702,8 +1702,12 @@ int plan_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* s
     // tile and one part of K a CTA (by the K steps' cycles that its units were measured at).
     Shape& sh = call->sh;
     int &rank_tiles = call->rank_tiles, &parts = call->parts, &shrink_n = call->shrink_n;
+    auto fits = [&](size_t shrink_tiles, int adapters) {   // the work list in the launches' parameters
+        return h->allow_inline && nft + shrink_tiles <= (size_t)kInlineTiles && n_m <= kInlineSegs && n_used <= adapters;
+    };
     if (n_used) {
-        double best = 0;                                   // of the bf16 kernel's units, which know no tiles of several adapters
+        // of the bf16 kernel's units, which know no tiles of several adapters
+        double best = 0;
         if (!merged) {
             sh = choose_shape(h, plan, false);
             sh.bk = 64;
@@ -1716,7 +1720,10 @@ int plan_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* s
             }
             sh.tile_n = sh.shrink_n;
             sh.stages = stages_for(sh.shrink_n / sh.cs, sh.bk);
-            best = (double)ceil_div((long long)sg * rank_tiles, slots) * ceil_div(h->d_in, 64) * kstep_cycles(sh.cs, sh.shrink_n);
+            // (left out where their list of tiles and adapters would be uploaded and the other kernel's is not: a call that
+            // a capture takes must not hang on which of them is expected to end sooner)
+            if (fits(sh.shrink_groups.size(), kInlineAdapters) || !fits(plan.shrink.size(), kFp8InlineAdapters))
+                best = (double)ceil_div((long long)sg * rank_tiles, slots) * ceil_div(h->d_in, 64) * kstep_cycles(sh.cs, sh.shrink_n);
         }
         // (a call of 48 rows of 17,408 -> 5,120, rank 256: with 256 columns of the rank a CTA 40 us, with 32 38; of 6,144 24 and 23)
         const int steps = ceil_div(h->d_in, 64), tiles = (int)plan.shrink.size(), whole = ceil_div(h->rank, 16) * 16;
@@ -1748,7 +1755,7 @@ int plan_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* s
         if (t.adapter < 1 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T) return LORA_EINVAL;
     }
 
-    call->inline_wl = h->allow_inline && nft + nst <= kInlineTiles && n_m <= kInlineSegs && n_used <= (parts ? kFp8InlineAdapters : kInlineAdapters);
+    call->inline_wl = fits(nst, parts ? kFp8InlineAdapters : kInlineAdapters);
     return merged && !call->inline_wl ? LORA_EINVAL : LORA_OK;   // (merge_tiles has seen to it)
 }
 

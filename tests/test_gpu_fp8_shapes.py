@@ -48,3 +48,23 @@ def test_what_is_described():
     odd = LoraLinear(264, 136, 16, 48, 4)                    # (d_in no multiple of 16: bf16 alone)
     with pytest.raises(Exception, match="invalid argument"):
         odd.describe_fp8(48, [0, 48], [0])
+
+
+# five to eight adapters, of as many rows that no tile holds two and the bf16 kernel's units would run the shrink
+@pytest.mark.parametrize("d_in,rows,ids", [(1024, [768] * 5, [1, 2, 3, 4, 5]), (1024, [512] * 8, [8, 7, 6, 5, 4, 3, 2, 1]), (256, [500] * 7, [1, 2, 3, 4, 5, 6, 7])])
+def test_up_to_eight_adapters_are_captured(d_in, rows, ids):
+    c = Case(d_in, 2056, 256, rows, ids, seed=len(rows))
+    d = described(c)
+    assert d["merged"] == 0 and d["shrink"] == 1 and d["uploaded"] == 0, d
+    y = c.run()
+    c.check(y)
+    out = torch.zeros_like(y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(y=out)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y)
