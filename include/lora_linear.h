@@ -188,7 +188,7 @@ int lora_linear_forward_w4(lora_linear* h, const void* x, int T,
  * arguments, layouts and errors as lora_linear_forward, except that the base product may be summed in parts
  * of K chosen by the batch: the same call gives the same bits, but a row's last bit may differ in another batch.
  * A row without an adapter may share a tile of 128 rows with an adapter's and adds zero times its values, as in
- * lora_linear_forward (an infinity or a NaN in the adapter reaches it); rows of other adapters take nothing of it.
+ * lora_linear_forward (an infinity or a NaN in the adapter reaches it); rows of other tiles or adapters take nothing of it.
  * Stream capture as lora_linear_forward, with up to 8 adapters. Of the options, those of the launch's shape (tile widths, K parts,
  * clusters, unit orders) apply to the adapters' shrink alone; LORA_OPT_MAX_CTAS to both launches. Also LORA_ENOMEM where
  * the host has no memory for the plan.

@@ -1695,6 +1695,8 @@ int plan_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* s
         }
     } else {
         make_groups(plan.fused, cg, false, h->u_rows - kTileM, &groups);
+        for (Tile& t : groups)
+            if (t.adapter && t.u_row != t.row0) t.split_index = kApart;
     }
     const int nft = (int)groups.size();
 
@@ -1922,7 +1924,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
                   (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_2d(h, &q.tm_y, y, h->d_out, T, s8.wide ? 64 : 32, 32) != CUDA_SUCCESS)
         return LORA_ECUDA;
-    q.merged = merged;
+    q.mixed = merged || std::any_of(groups.begin(), groups.end(), [](const Tile& t) { return t.split_index == kApart; });
     std::copy(expands.begin(), expands.end(), q.expand);
     q.xs = f.xs;
     q.rows = T;

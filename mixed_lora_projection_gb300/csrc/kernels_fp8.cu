@@ -176,14 +176,16 @@ constexpr uint32_t kNothing = 0xffffffffu;
 // The scales of a block, as warp 3 lays them out for the epilogue, and its unit's place.
 struct ScaleSlot {
     float f[2][kTileM];                                // per half of the columns and row: xs ws, or kNothing
-    int4 unit;                                         // first row, rows, first column, blocks
+    int4 unit;                                         // first row, rows, first column (odd: kApart), blocks that its rows take
 };
 
 // CG: CTAs of the MMA's group; NT: columns of a TMEM buffer, half of them in each epilogue thread's registers. Registers
 // of the launch are dealt out anew: the loading warps' to the accumulators (LOW x 128 + HIGH x 256 <= 384 x the launch's).
-// MERGED: tiles hold several adapters. A form of its own: the same in all of them cost the pairs a tenth, and more.
-template <int CG, int NT, int LOW, int HIGH, bool MERGED>
+// MIXED: tiles hold several adapters (MERGED), or a pair's tiles differ in having one (APART). Forms of their own: the
+// first in all of them cost the pairs a tenth, and more, the second 0.8 %.
+template <int CG, int NT, int LOW, int HIGH, bool MIXED>
 __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_constant__ Fp8Params p) {
+    constexpr bool MERGED = MIXED && CG == 1, APART = MIXED && CG > 1;
     constexpr int EW = 8;                              // epilogue warps
     constexpr int kCols = NT / 2;                      // columns of an epilogue thread
     constexpr int kBufs = 512 / NT, kSlots = 2 * kBufs;   // TMEM buffers, places of scales
@@ -428,7 +430,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) slot.f[h][lane + 32 * i] = b0 + k < w.nk ? x[i][k] * c[h][k] : 1.f;
                         }
-                        if (lane == 0) slot.unit = make_int4(w.tile.row0, w.tile.nrows, w.n0, w.nb);
+                        const bool apart = APART && w.tile.split_index == kApart;
+                        if (lane == 0) slot.unit = make_int4(w.tile.row0, w.tile.nrows, w.n0 | (int)apart, apart ? w.nk : w.nb);
                         __syncwarp();
                         if (lane < kHalves) mbar_arrive(smem_addr(&tfull[buf * kHalves + lane]));
                         ++blk;
@@ -513,6 +516,17 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
                                 acc[8 * c + i] = fma2(pair(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f2, acc[8 * c + i]);
                         }
                     }
+                    if (++buf == kBufs) { buf = 0; phase ^= 1; }
+                    place = place + 1 == kSlots ? 0 : place + 1;
+                }
+            }
+            if (APART && (n0 & 1)) {                         // the partner's expand, unread
+                n0 &= ~1;
+#pragma unroll 1
+                for (int b = 0; b < p.expand_blocks && ok; ++b) {
+                    ok = wait_all(tfull0 + 8 * kHalves * buf, phase, abort_flag, p.status, limit);
+                    if (!ok) break;
+                    if (lane == 0) arrive_relaxed(tempty0 + 8 * kHalves * buf);
                     if (++buf == kBufs) { buf = 0; phase ^= 1; }
                     place = place + 1 == kSlots ? 0 : place + 1;
                 }
@@ -775,12 +789,12 @@ namespace {
 // 384 threads of 168 registers, dealt out anew: 72 x 128 + 216 x 256 = 168 x 384. A few bytes spilled in the loading warps
 // cost a tenth to a fifth of all (pairs with buffers of 256 columns, 9,728 rows of 5,120 -> 5,120: 198 us; with 64 and 216,
 // 40 bytes, 223).
-constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 72, 216, false>;
+constexpr auto kWide = dev::lora_fp8_kernel<2, 256, 72, 216, false>, kWideApart = dev::lora_fp8_kernel<2, 256, 72, 216, true>;
 constexpr auto kSingle = dev::lora_fp8_kernel<1, 256, 72, 216, false>, kSingleMerged = dev::lora_fp8_kernel<1, 256, 72, 216, true>;
 constexpr auto kNarrow = dev::lora_fp8_kernel<1, 128, 72, 216, false>, kNarrowMerged = dev::lora_fp8_kernel<1, 128, 72, 216, true>;
-inline auto kernel_of(int wide, int tile_n, int merged) {
-    if (wide) return kWide;
-    return tile_n == 256 ? (merged ? kSingleMerged : kSingle) : merged ? kNarrowMerged : kNarrow;
+inline auto kernel_of(int wide, int tile_n, int mixed) {
+    if (wide) return mixed ? kWideApart : kWide;
+    return tile_n == 256 ? (mixed ? kSingleMerged : kSingle) : mixed ? kNarrowMerged : kNarrow;
 }
 }  // namespace
 
@@ -822,7 +836,7 @@ cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
 cudaError_t fp8_prepare_device() {
     cudaError_t r = cudaFuncSetAttribute(dev::lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (r != cudaSuccess) return r;
-    for (const auto k : {kWide, kSingle, kNarrow, kSingleMerged, kNarrowMerged}) {
+    for (const auto k : {kWide, kWideApart, kSingle, kNarrow, kSingleMerged, kNarrowMerged}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
     }
@@ -880,7 +894,7 @@ cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream) {
     // stages: a lap is no shorter than the stages of the blocks between two uses of a TMEM buffer; an A stage's 128 rows lie
     // inside the rings; the parts' sums take the rings' place
     const size_t rings = (size_t)p.stages * (p.a_rows + tile_rows) * kFp8StageRow;
-    if ((p.wide && p.merged) || p.lora_stages < 1 || p.k_lora % p.lora_stages || p.most_expands < 0 || p.expand_blocks != p.k_lora / p.lora_stages ||
+    if (p.lora_stages < 1 || p.k_lora % p.lora_stages || p.most_expands < 0 || p.expand_blocks != p.k_lora / p.lora_stages ||
         p.stages < fp8_window(512 / p.tile_n, p.k_blocks / p.parts, p.most_expands * p.expand_blocks, p.lora_stages) ||
         fp8_smem_bytes(p.wide, p.tile_n, p.a_rows, p.stages) > (size_t)kSmemLimit ||
         (size_t)p.stages * tile_rows < (size_t)(kTileM - p.a_rows) || (p.parts > 1 && rings < (size_t)p.tile_n * kTileM * 4))
@@ -891,7 +905,7 @@ cudaError_t launch_fp8(const Fp8Params& p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     config(p, grid, stream, &cfg, attr);
-    return cudaLaunchKernelEx(&cfg, kernel_of(p.wide, p.tile_n, p.merged), p);
+    return cudaLaunchKernelEx(&cfg, kernel_of(p.wide, p.tile_n, p.mixed), p);
 }
 
 }  // namespace lora

@@ -14,6 +14,10 @@ constexpr int kFp8InlineAdapters = 8; // named in a call whose work list travels
 constexpr int kFp8Expands = 16;       // pairs of a row tile and an adapter, where tiles hold several
 constexpr int kFp8StageRow = 128;     // bytes of a stage's row: one group of e4m3, 64 bf16 of the expand
 
+// In place of a tile's split_index: a tile without an adapter that shares an SM pair, and so the expand, with an adapter's.
+// Its rows take nothing of the expand (its U is zeros, but zero times a NaN of the adapter's is none).
+constexpr int kApart = -1;
+
 // One expand of a tile that holds rows of several adapters.
 struct Fp8Expand {
     int adapter, slot;                // its U is the 128 rows from 128 slot on
@@ -25,9 +29,9 @@ struct Fp8Expand {
 struct Fp8Params {
     CUtensorMap inline_bmaps[kFp8InlineAdapters];   // B_a [d_out, rank] bf16 (inline work list)
     Tile inline_tiles[kInlineTiles];
-    // merged (single CTAs): a tile's u_row is its first expand, its adapter their number
+    // mixed: on single CTAs a tile's u_row is its first expand, its adapter their number; on pairs some tiles are kApart
     Fp8Expand expand[kFp8Expands];
-    int merged;
+    int mixed;
     int inline_wl;
     CUtensorMap tm_x;                 // X [T, d_in] e4m3, box 128 x a_rows, 128-byte swizzle
     CUtensorMap tm_w;                 // W [d_out, d_in] e4m3, box 128 x tile_n, on pairs 128 x 64

@@ -68,3 +68,24 @@ def test_up_to_eight_adapters_are_captured(d_in, rows, ids):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, y)
+
+
+# rows without an adapter in tiles of their own, which share an SM pair with an adapter's tile, before and behind it
+@pytest.mark.parametrize("rows,ids", [([128, 128], [0, 1]), ([128, 300, 84], [0, 1, 0]), ([256, 300], [0, 1]), ([384, 128, 640, 5], [0, 1, 0, 2]),
+                                      ([128, 128], [1, 0]), ([128, 128, 128, 100], [2, 0, 1, 0])])
+def test_an_adapter_with_a_nan_stays_off_tiles_without_one(rows, ids):
+    c = Case(1024, 12288, 64, rows, ids, seed=len(rows))
+    d = described(c)
+    assert (d["cluster"], d["tile_n"], d["merged"]) == (2, 256, 0), d
+    y = c.run()
+    c.check(y)
+    c.b[0][5, 3] = float("nan")
+    c.b[0][4097] = float("inf")
+    bad = c.run()
+    named = {t // 128 for i, a in enumerate(ids) if a == 1 for t in range(c.off[i], c.off[i + 1])}
+    i = ids.index(1)
+    assert torch.isnan(bad[c.off[i]:c.off[i + 1], 5]).all()
+    rest = [t for t in range(c.T) if t // 128 not in named]
+    assert len(rest) >= 84 and torch.equal(bad[rest], y[rest])
+    tile = [t for t in range(c.T) if t // 128 in named]
+    assert torch.equal(bad[tile][:, 6:4097], y[tile][:, 6:4097])
