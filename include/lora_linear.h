@@ -190,8 +190,8 @@ int lora_linear_forward_w4(lora_linear* h, const void* x, int T,
  * A row without an adapter may share a tile of 128 rows with an adapter's and adds zero times its values, as in
  * lora_linear_forward (an infinity or a NaN in the adapter reaches it); rows of other tiles or adapters take nothing of it.
  * Stream capture as lora_linear_forward, with up to 8 adapters. Of the options, those of the launch's shape (tile widths, K parts,
- * clusters, unit orders) apply to the adapters' shrink alone; LORA_OPT_MAX_CTAS to both launches. Also LORA_ENOMEM where
- * the host has no memory for the plan.
+ * clusters, unit orders) apply to the adapters' shrink alone; LORA_OPT_MAX_CTAS to both launches, one of which then ends
+ * before the next begins, and to the choice of the parts of K. Also LORA_ENOMEM where the host has no memory for the plan.
  * Source: no counterpart on the pages (their base is 4-bit); the scales' layout is the one that this library's
  * 8-bit norm writes.
  */
@@ -287,7 +287,8 @@ enum {
                                    summation for later calls; may allocate (LORA_ENOMEM) */
     LORA_OPT_MAX_CTAS = 15,     /* at most this many CTAs (one per SM) per launch, >= 2; 0 = every SM (default).
                                    Leaves the other SMs to calls on other streams; the launch shape is chosen
-                                   for the SMs it may use. Does not change any result */
+                                   for the SMs it may use. Does not change any result, but for an 8-bit
+                                   projection's last bit (its parts of K are chosen for those SMs too) */
     LORA_OPT_PDL = 16,          /* 1 = programmatic dependent launch for calls without adapter rows (bf16 base,
                                    one launch): the launch may start on SMs the previous kernel of the stream
                                    leaves, requests its first W tiles, and waits for that kernel before it

@@ -1766,8 +1766,11 @@ int fp8_grid(const lora_linear* h, const Fp8Call& c) {
     const int units = (int)c.groups.size() / (c.s8.wide ? 2 : 1) * c.s8.n_ntiles;
     return c.s8.wide ? std::min(units, usable_sms(h) / 2) * 2 : c.s8.parts > 1 ? units * c.s8.parts : std::min(units, usable_sms(h));
 }
-// The shrink's, of the K-part kernel.
-int shrink_grid(const Fp8Call& c, int rank) { return (int)c.plan.shrink.size() * ceil_div(rank, c.shrink_n) * c.parts; }
+// The shrink's, of the K-part kernel: a unit a cluster where K is in parts, else as many CTAs as there may be.
+int shrink_grid(const lora_linear* h, const Fp8Call& c) {
+    const int units = (int)c.plan.shrink.size() * ceil_div(h->rank, c.shrink_n);
+    return c.parts > 1 ? units * c.parts : std::min(units, usable_sms(h));
+}
 // The shrink by the bf16 kernel's units: what its launch's shape depends on, and its grid (0: none).
 int fill_shrink_units(lora_linear* h, const Fp8Call& c, GemmParams* p) {
     p->n_shrink = (int)c.sh.shrink_groups.size() / c.sh.cs;
@@ -1806,6 +1809,8 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return LORA_ECUDA;
     if (capture != cudaStreamCaptureStatusNone && !inline_wl) return LORA_EUNSUPPORTED;   // as lora_linear_forward
 
+    // Under LORA_OPT_MAX_CTAS one launch ends before the next begins: blocks that wait would hold SMs past the limit.
+    const bool chained = usable_sms(h) == h->num_sms;
     const int q_groups = ceil_div(h->d_in, kFp8Group);
     Fp8Params q;
     memset(&q, 0, sizeof(q));
@@ -1897,7 +1902,8 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
         r.parts = parts;
         r.stages = shrink_stages(shrink_n);
         r.debug_stall = h->debug_stall;
-        if (launch_shrink(r, stream) != cudaSuccess) return LORA_ECUDA;
+        r.chained = chained;
+        if (launch_shrink(r, shrink_grid(h, call), stream) != cudaSuccess) return LORA_ECUDA;
         ++h->launches;
         rec.has_shrink = true;
     } else if (n_used) {
@@ -1952,7 +1958,8 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     q.a_rows = s8.a_rows;
     q.stages = s8.stages;
     q.wide = s8.wide;
-    q.late_u = parts && inline_wl;                     // (a list that was copied is read after the wait)
+    q.chained = chained;
+    q.late_u = chained && parts && inline_wl;          // (a list that was copied is read after the wait)
     q.debug_stall = h->debug_stall;
     if (launch_fp8(q, fp8_grid(h, call), stream) != cudaSuccess) return LORA_ECUDA;
     ++h->launches;
@@ -2003,7 +2010,7 @@ extern "C" int lora_linear_describe_fp8(lora_linear* h, int T, const int32_t* se
             if (c.parts) {
                 v[5] = 1;
                 v[6] = c.parts;
-                v[7] = shrink_grid(c, h->rank);
+                v[7] = shrink_grid(h, c);
             } else if (!c.plan.shrink.empty()) {
                 GemmParams p;
                 memset(&p, 0, sizeof(p));

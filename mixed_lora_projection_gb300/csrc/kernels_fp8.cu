@@ -632,8 +632,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     }
 }
 
-// U[t, :] = bf16(s_a X[t, :] A_a^T) for one tile of 128 rows, n columns of the rank and one part of K a CTA, the parts of a
-// tile a cluster: the bf16 kernel's shrink units take a tile's whole K each, 272 K steps of it at d_in 17,408 (1,553 rows
+// U[t, :] = bf16(s_a X[t, :] A_a^T) for one tile of 128 rows, n columns of the rank and one part of K a unit, the parts of a
+// tile a cluster; a CTA takes one unit after another where there are more than CTAs, its K whole then. The bf16 kernel's shrink units take a tile's whole K each, 272 K steps of it at d_in 17,408 (1,553 rows
 // of rank 64 there 80 us; in 8 parts 12). Bound by the fill of shared memory, 61 bytes a cycle and SM.
 __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -644,8 +644,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     uint8_t* b_ring = a_ring + (size_t)stages * a_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(b_ring + (size_t)stages * b_bytes);
     uint64_t* empty = full + stages;
-    uint64_t* done = empty + stages;                   // every MMA has completed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* done = empty + stages;                   // a unit's MMAs have completed
+    uint64_t* taken = done + 1;                        // and its sums have been read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(taken + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int part = p.parts > 1 ? (int)cluster_ctarank() : 0;
@@ -655,6 +656,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
             mbar_init(smem_addr(&empty[s]), 1);
         }
         mbar_init(smem_addr(done), 1);
+        mbar_init(smem_addr(taken), 4);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -667,61 +669,85 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     griddep_wait();
     griddep_launch_dependents();
 
-    const int unit = (int)blockIdx.x / p.parts, c0 = unit % p.rank_tiles * p.n, cols = min(p.n, p.rank - c0);
-    const Tile tile = (p.inline_wl ? p.inline_tiles : p.tiles)[unit / p.rank_tiles];
+    const int n_units = p.n_tiles * p.rank_tiles, first = (int)blockIdx.x / p.parts, step = (int)gridDim.x / p.parts;
     const int k0 = part * p.k_steps / p.parts, nk = (part + 1) * p.k_steps / p.parts - k0;
+    Tile tile;                                         // of a unit, and its columns of the rank
+    int c0, cols;
+    auto place = [&](int unit) {
+        tile = (p.inline_wl ? p.inline_tiles : p.tiles)[unit / p.rank_tiles];
+        c0 = unit % p.rank_tiles * p.n;
+        cols = min(p.n, p.rank - c0);
+    };
+    place(first);
     bool ok = true;
     if (warp == 0 && !p.debug_stall) {
-        const CUtensorMap* am = &(p.inline_wl ? p.inline_amaps : p.tm_a)[tile.adapter - 1];
-        if (!p.inline_wl) tensormap_acquire(am);
-        int issued = 0;
-        for (int k = 0; k < nk; ++k) {
-            const int stage = k % stages;
-            if (!wait_all(smem_addr(&empty[stage]), ((k / stages) & 1) ^ 1, abort_flag, p.status, limit)) {
-                ok = false;
-                break;
+        int issued = 0, stage = 0;
+        uint32_t phase = 0;
+        for (int unit = first; unit < n_units && ok; unit += step) {
+            if (unit != first) place(unit);
+            const CUtensorMap* am = &(p.inline_wl ? p.inline_amaps : p.tm_a)[tile.adapter - 1];
+            if (!p.inline_wl) tensormap_acquire(am);
+            for (int k = 0; k < nk; ++k) {
+                if (!wait_all(smem_addr(&empty[stage]), phase ^ 1, abort_flag, p.status, limit)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = smem_addr(&full[stage]);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, a_bytes + b_bytes, 1u);
+                    tma_load_2d<1>(smem_addr(a_ring + (size_t)stage * a_bytes), &p.tm_x, bar, (k0 + k) * 64, tile.row0, 1u);
+                    tma_load_2d<1>(smem_addr(b_ring + (size_t)stage * b_bytes), am, bar, (k0 + k) * 64, c0, 1u);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == stages) { stage = 0; phase ^= 1; }
             }
-            const uint32_t bar = smem_addr(&full[stage]);
-            if (elect_one()) {
-                mbar_arrive_expect_tx(bar, a_bytes + b_bytes, 1u);
-                tma_load_2d<1>(smem_addr(a_ring + (size_t)stage * a_bytes), &p.tm_x, bar, (k0 + k) * 64, tile.row0, 1u);
-                tma_load_2d<1>(smem_addr(b_ring + (size_t)stage * b_bytes), am, bar, (k0 + k) * 64, c0, 1u);
-            }
-            __syncwarp();
-            ++issued;
         }
         if (!ok && lane == 0)                              // copies in flight (bounded, whatever the abort flag says)
             for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
                 wait_lane(smem_addr(&full[j % stages]), (uint32_t)((j / stages) & 1), abort_flag, p.status, limit, false);
     } else if (warp == 1) {
         const uint32_t idesc = instr_desc_bf16(kTileM, p.n);
-        for (int k = 0; k < nk; ++k) {
-            const int stage = k % stages;
-            if (!wait_all(smem_addr(&full[stage]), (k / stages) & 1, abort_flag, p.status, limit)) break;
-            tc_fence_after();
-            const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
-            const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
-            if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_bf16<1>(tmem_base, ad + (uint64_t)(2 * i), bd + (uint64_t)(2 * i), idesc, (k > 0 || i > 0) ? 1u : 0u, 1u);
-                mma_commit<1>(smem_addr(&empty[stage]), 1u);
+        int stage = 0, n = 0;                              // n: units before this one
+        uint32_t phase = 0;
+        for (int unit = first;; unit += step, ++n) {
+            if (n > 0) {                                   // the unit before has been read
+                ok = wait_all(smem_addr(taken), (n - 1) & 1, abort_flag, p.status, limit);
+                tc_fence_after();
             }
+            for (int k = 0; k < nk && ok; ++k) {
+                ok = wait_all(smem_addr(&full[stage]), phase, abort_flag, p.status, limit);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ad = smem_desc<64>(smem_addr(a_ring + (size_t)stage * a_bytes));
+                const uint64_t bd = smem_desc<64>(smem_addr(b_ring + (size_t)stage * b_bytes));
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_bf16<1>(tmem_base, ad + (uint64_t)(2 * i), bd + (uint64_t)(2 * i), idesc, (k > 0 || i > 0) ? 1u : 0u, 1u);
+                    mma_commit<1>(smem_addr(&empty[stage]), 1u);
+                }
+                __syncwarp();
+                if (++stage == stages) { stage = 0; phase ^= 1; }
+            }
+            // (also where a wait ran out: every MMA this warp issued completes before TMEM is released)
+            if (elect_one()) mma_commit<1>(smem_addr(done), 1u);
             __syncwarp();
+            if (!ok || unit + step >= n_units) break;
         }
-        // (also where a wait ran out: every MMA this warp issued completes before TMEM is released)
-        if (elect_one()) mma_commit<1>(smem_addr(done), 1u);
-        __syncwarp();
-        if (lane == 0) wait_lane(smem_addr(done), 0, abort_flag, p.status, limit, false);
+        if (lane == 0) wait_lane(smem_addr(done), n & 1, abort_flag, p.status, limit, false);
     }
     __syncwarp();
     float4* sums = reinterpret_cast<float4*>(base);
-    if (warp >= 4) {
+    for (int unit = first, n = 0; warp >= 4 && unit < n_units; unit += step, ++n) {
         // ------------------------------------------------------------ epilogue: row 32 q + lane
+        if (unit != first) place(unit);
         const int q = warp & 3, r_local = q * 32 + lane, row = tile.row0 + r_local;
-        ok = wait_all(smem_addr(done), 0, abort_flag, p.status, limit) && !*abort_flag;
+        ok = wait_all(smem_addr(done), n & 1, abort_flag, p.status, limit) && !*abort_flag;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
-        if (ok && q * 32 < tile.nrows) {
+        if (q * 32 < tile.nrows) {
             const bool mine = r_local < tile.nrows;
             const int32_t* seg_off = p.inline_wl ? p.inline_seg : p.seg_off;
             const int32_t* seg_id = p.inline_wl ? p.inline_seg + p.n_seg + 1 : p.seg_id;
@@ -748,8 +774,12 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
                 }
             }
         }
+        if (unit + step >= n_units) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(taken));
     }
-    if (p.parts > 1) {
+    if (p.parts > 1) {                                     // (one unit a cluster)
         __syncwarp();
         cluster_sync();
         if (warp >= 4 && ok) {
@@ -804,7 +834,7 @@ size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages) {
 }
 
 static size_t shrink_smem_bytes(int n, int stages) {
-    return 1024 + (size_t)stages * (kTileM + n) * kFp8StageRow + 8 * (2 * (size_t)stages + 1) + 16;
+    return 1024 + (size_t)stages * (kTileM + n) * kFp8StageRow + 8 * (2 * (size_t)stages + 2) + 16;
 }
 int shrink_stages(int n) {
     int s = 2;
@@ -812,15 +842,17 @@ int shrink_stages(int n) {
     return s;
 }
 
-cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
-    // the parts' sums take the rings' place
+cudaError_t launch_shrink(const ShrinkParams& p, int grid, cudaStream_t stream) {
+    // the parts' sums take the rings' place: one unit a cluster
+    const long long ctas = (long long)p.n_tiles * p.rank_tiles * p.parts;
+    if (grid < 1 || grid > ctas || (p.parts > 1 && grid != ctas)) return cudaErrorInvalidValue;
     if (p.n < 16 || p.n > 256 || p.n % 16 || p.rank < 8 || p.rank % 8 || p.rank_tiles != (p.rank + p.n - 1) / p.n || p.parts < 1 || p.parts > kFp8MaxParts ||
         p.parts > p.k_steps || p.n_tiles < 1 || p.stages < 2 || shrink_smem_bytes(p.n, p.stages) > (size_t)kSmemLimit ||
         (p.parts > 1 && (size_t)p.stages * (kTileM + p.n) * kFp8StageRow < (size_t)p.n * kTileM * 4))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3(p.n_tiles * p.rank_tiles * p.parts);
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kShrinkThreads);
     cfg.dynamicSmemBytes = shrink_smem_bytes(p.n, p.stages);
     cfg.stream = stream;
@@ -829,7 +861,7 @@ cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = p.chained ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, dev::lora_shrink_kernel, p);
 }
 
@@ -854,7 +886,7 @@ static void config(const Fp8Params& p, int grid, cudaStream_t stream, cudaLaunch
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg->attrs = attr;
-    cfg->numAttrs = 2;
+    cfg->numAttrs = p.chained ? 2 : 1;
 }
 
 // Clusters of `parts` CTAs of the single-CTA forms that the GPU holds at once.
@@ -867,7 +899,6 @@ int fp8_max_clusters(int tile_n, int parts) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     config(p, parts, nullptr, &cfg, attr);
-    cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kernel_of(0, tile_n, 0), &cfg) != cudaSuccess) {
         cudaGetLastError();

@@ -58,7 +58,8 @@ struct Fp8Params {
     int stages;
     int rows;                         // T
     int vec_scales;                   // both scales' rows are 16-byte aligned
-    int late_u;                       // launched beside the call's own shrink, which it waits for ahead of U alone
+    int chained;                      // may begin while the stream's kernel before it ends
+    int late_u;                       // (chained) beside the call's own shrink, which it waits for ahead of U alone
     int wide;                         // SM pairs, 256 x 256 blocks, persistent
     int debug_stall;
 };
@@ -82,9 +83,9 @@ struct ShrinkParams {
     int* status;
     unsigned long long wait_limit_ns;
     int n_tiles, n_seg, rank;
-    int n, rank_tiles;                // columns of a CTA, a multiple of 16; CTAs side by side
+    int n, rank_tiles;                // columns of a unit, a multiple of 16; units side by side
     int k_steps;                      // ceil(d_in / 64)
-    int parts, stages, debug_stall;
+    int parts, stages, chained, debug_stall;
 };
 
 // kernels_fp8.cu
@@ -92,7 +93,7 @@ struct ShrinkParams {
 // `expands` blocks of `lora_stages` follow one another: the ring is at least as long (the issuing warps' comment).
 int fp8_window(int bufs, int nk, int expands, int lora_stages);
 int shrink_stages(int n);
-cudaError_t launch_shrink(const ShrinkParams& p, cudaStream_t stream);
+cudaError_t launch_shrink(const ShrinkParams& p, int grid, cudaStream_t stream);
 size_t fp8_smem_bytes(int wide, int tile_n, int a_rows, int stages);
 int fp8_max_clusters(int tile_n, int parts);
 cudaError_t fp8_prepare_device();

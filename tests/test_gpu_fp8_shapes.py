@@ -89,3 +89,51 @@ def test_an_adapter_with_a_nan_stays_off_tiles_without_one(rows, ids):
     assert len(rest) >= 84 and torch.equal(bad[rest], y[rest])
     tile = [t for t in range(c.T) if t // 128 in named]
     assert torch.equal(bad[tile][:, 6:4097], y[tile][:, 6:4097])
+
+
+# LORA_OPT_MAX_CTAS: neither launch has more CTAs; the shrink's take several units then
+@pytest.mark.parametrize("d_in,d_out,rank,rows,ids", [
+    (5120, 12288, 256, [48], [1]),
+    (6144, 5120, 64, [1] * 8, [8, 7, 6, 5, 4, 3, 2, 1]),
+    (1024, 1288, 40, [60] * 7, [1, 2, 1, 2, 1, 2, 1]),
+    (1024, 2568, 256, [700, 5, 300], [1, 0, 2]),
+    (5120, 5120, 256, [1500], [1]),
+    (640, 264, 24, [4000], [1]),
+])
+@pytest.mark.parametrize("most", [2, 3, 9, 40, 151])
+def test_fewer_sms(d_in, d_out, rank, rows, ids, most):
+    from mixed_lora_projection_gb300 import _lib
+    c = Case(d_in, d_out, rank, rows, ids, seed=d_in + rank)
+    y = c.run()
+    before = described(c)
+    c.linear.set_option(_lib.OPT_MAX_CTAS, most)
+    d = described(c)
+    assert 1 <= d["grid"] <= most and 1 <= d["shrink_grid"] <= most, d
+    z = c.run()
+    c.check(z)
+    assert all(torch.equal(c.run(), z) for _ in range(3))
+    c.linear.set_option(_lib.OPT_MAX_CTAS, 0)
+    assert described(c) == before and torch.equal(c.run(), y)
+
+
+def test_more_units_of_the_shrink_than_sms():
+    # (pairs of a tile and an adapter, by columns of the rank; and many tiles of few rows)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    c = Case(640, 136, 256, [1, 1] * 100, [1, 2] * 100, seed=1)
+    c.check(c.run())
+    d = described(c)
+    assert d["grid"] <= sms and d["shrink_grid"] <= sms
+    # a wait that runs out while CTAs have further units before them
+    from mixed_lora_projection_gb300 import _lib
+    e = Case(640, 264, 16, [30] * 8, [1, 2, 3, 4, 5, 6, 7, 8], seed=2)
+    e.linear.set_option(_lib.OPT_MAX_CTAS, 3)
+    y = e.run()
+    e.check(y)
+    e.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 2000)
+    e.linear.set_option(_lib.OPT_DEBUG_STALL, 1)
+    e.run()
+    assert e.linear.status() == _lib.LORA_ETIMEOUT
+    e.linear.set_option(_lib.OPT_DEBUG_STALL, 0)
+    assert e.linear.status(reset=True) == _lib.LORA_ETIMEOUT
+    e.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 4000000)
+    assert torch.equal(e.run(), y) and e.linear.status() == 0
