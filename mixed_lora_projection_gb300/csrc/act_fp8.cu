@@ -58,19 +58,51 @@ __device__ __forceinline__ uint2 to_e4m3(const float* f, float inv) {
     return make_uint2(w[0], w[1]);
 }
 
-// g / (1 + e^-g) * u. Past e^-g's range the quotient is -0, its limit.
+__device__ __forceinline__ float exp2_of(float t) {      // 2^-22 of the value; 0 below 2^-126
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e;
+}
+// g / (1 + e^-g) u as (g / 4) (1 / (1/4 + e^-g / 4)) u: the reciprocal is no subnormal however large e^-g is (__fdividef is 0
+// from 2^126 on). e^-g itself is infinite from g = -88.7 on, where a large u still gives a y that is not 0: threads with a
+// gate below -80, which are rare, take h = e^(-|g| / 2) (FAR): g u / (1 + h^2) for g >= 0, g h u h / (1 + h^2) below, 0 only
+// where no bf16 y is left. (That for all of them: 4,001 rows of 17,408 to 8 bits 69 us by groups, 90 by rows.)
+template <bool FAR>
 __device__ __forceinline__ void silu_mul8(const uint4& gate, const uint4& up, float* y) {
-    float g[8], u[8];
-    unpack8(gate, g);
+    constexpr float kLog2e = 1.4426950408889634f;
+    float u[8];
+    unpack8(gate, y);
     unpack8(up, u);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = __fdividef(g[k], 1.f + __expf(-g[k])) * u[k];
+    for (int k = 0; k < 8; ++k) {
+        float r;
+        if (FAR) {
+            float h;
+            asm("ex2.approx.f32 %0, %1;" : "=f"(h) : "f"(fabsf(y[k]) * (-0.5f * kLog2e)));   // (subnormal from |g| = 174 on)
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.f)));
+            const float t = y[k] < 0.f ? h : 1.f;
+            y[k] = y[k] * t * r * u[k] * t;
+        } else {
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(exp2_of(y[k] * -kLog2e), 0.25f, 0.25f)));
+            y[k] = 0.25f * y[k] * r * u[k];
+        }
+    }
+}
+// Whether a thread's gates go below -80.
+template <int N>
+__device__ __forceinline__ bool far_gates(const uint4 (&a)[N]) {
+    uint32_t m = a[0].x;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (const uint32_t w : {a[i].x, a[i].y, a[i].z, a[i].w}) asm("min.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+    return fminf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)) < -80.f;
 }
 
 // One row's vector c (8 features) of the operator's values in fp32.
-template <bool GATE>
+template <bool GATE, bool FAR>
 __device__ __forceinline__ void values8(const uint4& a, const uint4& b, float* y) {
-    if (GATE) silu_mul8(a, b, y);
+    if (GATE) silu_mul8<FAR>(a, b, y);
     else unpack8(a, y);
 }
 
@@ -104,11 +136,13 @@ __global__ void __launch_bounds__(256, B) act_groups_kernel(const __grid_constan
             ++row;
         }
     }
+    const bool far = GATE && far_gates(a);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         if (rows[i] >= p.rows) break;
         float y[8];
-        values8<GATE>(a[i], b[i], y);
+        if (far) values8<GATE, true>(a[i], b[i], y);
+        else values8<GATE, false>(a[i], b[i], y);
         if (p.y && c[i] < nvec) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + rows[i] * p.y_stride)[c[i]] = pack8(y);
         if (!p.q8) continue;
         float m;
@@ -128,9 +162,10 @@ __global__ void __launch_bounds__(256, B) act_groups_kernel(const __grid_constan
 }
 
 // One scale a row: a block a row, which stays in registers between its maximum and its output (4,001 rows of 17,408 gated
-// 62 us, 5.6 TB/s; 48 rows 3.0).
+// 52 us, 6.7 TB/s; 48 rows 3.0). Registers for two blocks an SM: 17,408 features are 544 threads, at 64 registers one block
+// and 76 us; 12,288 are 768, at 48 one block and 78 us for 55 (5,668 rows).
 template <bool GATE, int V>
-__global__ void __launch_bounds__(1024) act_rows_kernel(const __grid_constant__ ActParams p) {
+__global__ void __maxnreg__(V == 1 ? 32 : V == 2 ? 40 : 56) act_rows_kernel(const __grid_constant__ ActParams p) {
     __shared__ float buf[32];
     dev::griddep_wait();
     dev::griddep_launch_dependents();
@@ -148,11 +183,15 @@ __global__ void __launch_bounds__(1024) act_rows_kernel(const __grid_constant__ 
         }
     }
     float y[V][8], m = 0.f;
+    if (GATE && far_gates(a)) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        values8<GATE>(a[i], b[i], y[i]);
-        m = max_nan(m, amax8(y[i]));
+        for (int i = 0; i < V; ++i) values8<GATE, true>(a[i], b[i], y[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) values8<GATE, false>(a[i], b[i], y[i]);
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max_nan(m, amax8(y[i]));
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((tid & 31) == 0) buf[tid >> 5] = m;
