@@ -65,8 +65,8 @@ enum {
  *   max_tokens   largest T a forward call will pass, in [1, LORA_MAX_TOKENS].
  *   max_segments largest n_seg a forward call will pass, in [1, LORA_MAX_SEGMENTS].
  *   device       CUDA device ordinal; it must be an sm_103 GPU.
- * The handle owns its workspace: the shrink output U (bf16 [max_tokens + 128, rank]),
- * a ring of work-list buffers (device and pinned host), a device status word and CUDA
+ * The handle owns its workspace: the shrink output U (bf16 [max_tokens + 128, rank]; where max_tokens is
+ * small and max_segments more than 1, up to 2,048 rows more for 8-bit calls of several adapters), a ring of work-list buffers (device and pinned host), a device status word and CUDA
  * events. The caller keeps the current device unchanged across the call.
  * Returns LORA_OK, LORA_EINVAL, LORA_ENODEV, LORA_ENOMEM or LORA_ECUDA.
  * Source: the shapes of "Two 27B models on a single RTX 5090", sections 2-3 (hidden

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <unordered_map>
 #include <vector>
 
@@ -67,7 +68,8 @@ struct lora_linear {
     int device = 0, d_in = 0, d_out = 0, rank = 0, max_tokens = 0, max_segments = 0;
     int num_sms = 0;
     void* u_ws = nullptr;       // bf16 [u_rows, rank]: shrink output, read by the fused pass
-    void* u_pairs = nullptr;    // bf16 [128 kFp8Expands, rank]: the 8-bit kernel's, by tile and adapter
+    void* u_pairs = nullptr;    // bf16 [u_pair_rows, rank]: the 8-bit kernel's, by tile and adapter; u_ws where that is as long
+    int u_pair_rows = 0;
     int u_rows = 0;
     int* status = nullptr;      // device status word
     int* flags = nullptr;       // per fused tile: U rows ready (1) in the running launch; then the
@@ -141,7 +143,8 @@ void free_handle(lora_linear* h) {
         for (cudaEvent_t e : r.ev) h->ev_pool.push_back(e);
     for (cudaEvent_t e : h->ev_pool) cudaEventDestroy(e);
     if (h->u_ws) cudaFree(h->u_ws);
-    if (h->u_pairs) cudaFree(h->u_pairs);
+    if (h->u_pairs && h->u_pairs != h->u_ws) cudaFree(h->u_pairs);
+    h->u_pairs = nullptr;
     if (h->partials) cudaFree(h->partials);
     if (h->split_ctr) cudaFree(h->split_ctr);
     if (h->w4_partials) cudaFree(h->w4_partials);
@@ -158,6 +161,30 @@ void free_handle(lora_linear* h) {
         if (h->ev_done[i]) cudaEventDestroy(h->ev_done[i]);
     }
     delete h;
+}
+
+// Clusters of the 8-bit kernel that the handle's device, the current one, holds at once: asked once a device (14 questions
+// took a sixth of lora_linear_create's time).
+void find_fp8_clusters(lora_linear* h) {
+    struct Known {
+        bool yes;
+        int clusters[2][kFp8MaxParts + 1];
+    };
+    static std::mutex lock;
+    static Known known[64];                                // (further devices: asked each time)
+    std::lock_guard<std::mutex> hold(lock);
+    Known* k = h->device < 64 ? &known[h->device] : nullptr;
+    if (!k || !k->yes) {
+        bool all = true;
+        for (int i = 0; i < 2; ++i)
+            for (int n = 2; n <= kFp8MaxParts; ++n) all &= (h->fp8_clusters[i][n] = fp8_max_clusters(128 * (i + 1), n)) > 0;
+        if (k && all) {
+            memcpy(k->clusters, h->fp8_clusters, sizeof(k->clusters));
+            k->yes = true;
+        }
+        return;
+    }
+    memcpy(h->fp8_clusters, k->clusters, sizeof(k->clusters));
 }
 
 cudaEvent_t take_event(lora_linear* h) {
@@ -867,10 +894,12 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
         return LORA_ECUDA;
     }
 
-    for (int i = 0; i < 2; ++i)
-        for (int n = 2; n <= kFp8MaxParts; ++n) h->fp8_clusters[i][n] = fp8_max_clusters(128 * (i + 1), n);
+    find_fp8_clusters(h);
 
     h->u_rows = ceil_div(max_tokens, kTileM) * kTileM + kTileM;
+    // (no batch of one segment, and none that the 8-bit kernel does not take, merges tiles)
+    if (max_segments > 1 && d_in % 16 == 0)
+        h->u_pair_rows = (int)std::min<long long>(kFp8Expands, (long long)ceil_div(max_tokens, kTileM) * std::min(max_segments, kFp8InlineAdapters)) * kTileM;
     h->max_fused = ceil_div(max_tokens, kTileM) + max_segments + 1;
     h->k_split = choose_k_split(h);
     h->slot_bytes = align_up(2 * (size_t)max_segments * sizeof(CUtensorMap), 128) +
@@ -881,10 +910,17 @@ int lora_linear_create(lora_linear** out, int d_in, int d_out, int rank, int max
                     align_up((size_t)max_segments * sizeof(CUtensorMap), 128) +
                     (size_t)(h->max_fused / 2 + 1) * sizeof(W4Group) + 256;
     if (cudaMalloc(&h->u_ws, (size_t)h->u_rows * rank * 2) != cudaSuccess ||
-        cudaMalloc(&h->u_pairs, (size_t)kFp8Expands * kTileM * rank * 2) != cudaSuccess ||
         cudaMalloc((void**)&h->status, sizeof(int)) != cudaSuccess ||
         cudaMalloc((void**)&h->flags, sizeof(int) * ((size_t)h->max_fused + 1)) != cudaSuccess ||
         cudaHostAlloc((void**)&h->status_host, sizeof(int), cudaHostAllocDefault) != cudaSuccess) {
+        cudaGetLastError();
+        free_handle(h);
+        return LORA_ENOMEM;
+    }
+    // (calls of a handle follow one another; the last 128 rows of u_ws stay zeros)
+    if (h->u_pair_rows <= h->u_rows - kTileM) {
+        h->u_pairs = h->u_ws;
+    } else if (cudaMalloc(&h->u_pairs, (size_t)h->u_pair_rows * rank * 2) != cudaSuccess) {
         cudaGetLastError();
         free_handle(h);
         return LORA_ENOMEM;
@@ -1611,7 +1647,7 @@ int validate_fp8(int d_in, int d_out, int rank, int max_tokens, int max_segments
 // rows of nine segments and two adapters, 5,120 -> 12,288, rank 256, 28 us for 74; two rows of two adapters, rank 16, 18 for
 // 45; and 223 rows of five segments, whose two tiles no SM pair may share, 26 for 40. The tiles are in `plan`; the pairs,
 // in the order of tiles, are the shrink's tiles. False where they do not fit.
-bool merge_tiles(int T, Plan* plan) {
+bool merge_tiles(int T, int most_pairs, Plan* plan) {
     const int nf = ceil_div(T, kTileM), n_used = (int)plan->used_adapters.size();
     if (n_used < 2 || n_used > kFp8InlineAdapters || nf > kFp8Expands || (int)plan->seg_id.size() > kInlineSegs) return false;
     std::vector<Tile> tiles, pairs;
@@ -1631,7 +1667,7 @@ bool merge_tiles(int T, Plan* plan) {
                     break;
                 }
     }
-    if ((int)pairs.size() > kFp8Expands || nf + (int)pairs.size() > kInlineTiles) return false;
+    if ((int)pairs.size() > most_pairs || nf + (int)pairs.size() > kInlineTiles) return false;
     plan->fused = tiles;
     plan->shrink = pairs;
     return true;
@@ -1669,7 +1705,7 @@ int plan_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* s
     s8 = fp8_shape(h, plan, false);
     if (h->allow_inline && n_used > 1) {
         Plan whole = plan;
-        if (merge_tiles(T, &whole)) {
+        if (merge_tiles(T, h->u_pair_rows / kTileM, &whole)) {
             const Fp8Shape s = fp8_shape(h, whole, true);
             merged = s.us < s8.us;
             if (merged) {
@@ -1753,7 +1789,7 @@ int plan_fp8(lora_linear* h, int T, const int32_t* seg_offsets, const int32_t* s
     if (expands.size() > kFp8Expands) return LORA_EINVAL;
     for (int i = 0; i < nst; ++i) {
         const Tile& t = sh.shrink_groups[i];
-        if (parts && (t.u_row < 0 || t.u_row + t.nrows > (merged ? kFp8Expands * kTileM : h->u_rows))) return LORA_EINVAL;
+        if (parts && (t.u_row < 0 || t.u_row + t.nrows > (merged ? h->u_pair_rows : h->u_rows))) return LORA_EINVAL;
         if (t.adapter < 1 || t.adapter > n_used || t.row0 < 0 || t.nrows < 0 || t.row0 + t.nrows > T) return LORA_EINVAL;
     }
 
@@ -1926,7 +1962,7 @@ int forward_fp8_impl(lora_linear* h, const Fp8Operands& f, const void* x, int T,
     if (timing) cudaEventRecord(rec.ev[1], stream);
     if (encode_u8_sw128(h, &q.tm_x, f.x8, h->d_in, T, (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_u8_sw128(h, &q.tm_w, f.w8, h->d_in, h->d_out, (uint32_t)(s8.wide ? 64 : s8.tile_n)) != CUDA_SUCCESS ||
-        encode_2d(h, &q.tm_u, merged ? h->u_pairs : h->u_ws, h->rank, merged ? kFp8Expands * kTileM : h->u_rows, 64,
+        encode_2d(h, &q.tm_u, merged ? h->u_pairs : h->u_ws, h->rank, merged ? h->u_pair_rows : h->u_rows, 64,
                   (uint32_t)s8.a_rows) != CUDA_SUCCESS ||
         encode_2d(h, &q.tm_y, y, h->d_out, T, s8.wide ? 64 : 32, 32) != CUDA_SUCCESS)
         return LORA_ECUDA;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from mixed_lora_projection_gb300 import LoraLinear
-from test_gpu_fp8 import Case
+from test_gpu_fp8 import BF16, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +137,36 @@ def test_more_units_of_the_shrink_than_sms():
     assert e.linear.status(reset=True) == _lib.LORA_ETIMEOUT
     e.linear.set_option(_lib.OPT_WAIT_LIMIT_US, 4000000)
     assert torch.equal(e.run(), y) and e.linear.status() == 0
+
+
+# the blocks of U of tiles that hold several adapters lie in the projection's own U where that is long enough
+@pytest.mark.parametrize("most,segs", [(48, 6), (128, 2), (300, 16), (2047, 8), (2048, 8), (16384, 2)])
+@pytest.mark.parametrize("d_in,d_out", [(640, 264), (6144, 5120)])
+def test_several_adapters_on_handles_of_any_size(most, segs, d_in, d_out):
+    rows = [max(1, min(most, 300) // segs)] * segs
+    ids = [1 + i % 8 for i in range(segs)]
+    c = Case(d_in, d_out, 64, rows, ids, seed=most)
+    c.linear.close()
+    c.linear = LoraLinear(d_in, d_out, 64, most, segs)
+    y = c.run()
+    # (tiles are merged where they would read much of the base several times)
+    assert described(c)["merged"] == 1 or d_out == 264 or (most, segs) not in ((48, 6), (2047, 8), (2048, 8))
+    c.check(y)
+    # bf16 and 8-bit calls of one handle in turn, and one adapter's tiles beside none's: the zeros stay zeros
+    w = torch.randn(d_out, d_in, device="cuda").to(BF16)
+    base, z = c.x[:c.T], None
+    for _ in range(3):
+        b = c.linear.forward(base, c.off, c.ids, w, c.a, c.b, c.s)
+        one = c.linear.forward_fp8(c.x8, c.xs, [0, c.T], [1], c.w8, c.ws, c.a, c.b, c.s, x=c.x)
+        assert torch.equal(c.run(), y)
+        if z is not None:
+            assert torch.equal(b, z[0]) and torch.equal(one, z[1])
+        z = b, one
+
+
+def test_one_segment_or_odd_widths_keep_no_blocks():
+    a = LoraLinear(640, 264, 64, 48, 1)
+    assert a.describe_fp8(48, [0, 48], [1])["merged"] == 0
+    b = LoraLinear(648, 264, 64, 48, 4)                      # (not for 8 bits)
+    x, w = torch.randn(48, 648, device="cuda").to(BF16), torch.randn(264, 648, device="cuda").to(BF16)
+    assert torch.isfinite(b.forward(x, [0, 48], [0], w, [], [], [])).all()
