@@ -164,6 +164,7 @@ __device__ __forceinline__ Work decode(const Fp8Params& p, const Tile* tiles, in
         w.ns = w.nk + mine * p.k_lora;
         return w;
     }
+    w.e0 = 0;
     const bool expand = w.tile.adapter && part == p.parts - 1;
     w.nb = w.nk + (expand ? p.expand_blocks : 0);
     w.ns = w.nk + (expand ? p.k_lora : 0);
