@@ -51,3 +51,17 @@ def test_eight_bits_take_the_same_values():
     q, s = silu_mul_fp8(x, group=128)
     assert abs(s.item() * 448 / ref.abs().max().item() - 1) <= 2.0 ** -14
     assert ((q.to(F64) * s.to(F64) - ref).abs() <= (2.0 ** -4 + 2.0 ** -14) * ref.abs() + 2.0 ** -10 * s.to(F64)).all()
+
+
+@pytest.mark.parametrize("rows", [5, 300, 700])
+def test_a_row_takes_nothing_of_gates_beside_it(rows):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(rows)
+    x = (torch.randn(rows, 2 * 17408, generator=gen, device="cuda") * 2).to(BF16)
+    y, (q, s) = silu_mul(x), silu_mul_fp8(x)
+    far = x.clone()
+    far[1::2, :17408:5] = -100.0
+    z, (r, t) = silu_mul(far), silu_mul_fp8(far)
+    assert torch.equal(y[::2], z[::2]) and torch.equal(q[::2].view(torch.uint8), r[::2].view(torch.uint8)) and torch.equal(s[::2], t[::2])
+    rest = torch.arange(17408, device="cuda") % 5 != 0
+    assert torch.equal(y[:, rest], z[:, rest])
