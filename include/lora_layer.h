@@ -92,7 +92,7 @@ int lora_linear_fp8_rows(const void* x, long long x_stride, int rows, int width,
  *   w, w_stride    device bf16 [rows, cols]: rows >= 0, cols a multiple of 8, both at most LORA_MAX_FEATURES.
  *   q8, q8_stride  device e4m3 [rows, cols]: q = e4m3(w r), r = 1 / s rounded to fp32 (nearest even, saturating).
  *   scales         device fp32 [ceil(rows / 128), ceil(cols / 128)], contiguous: s = max(max|w| / 448, 2^-100) over
- *                  every block of 128 x 128 (the last ones may be smaller).
+ *                  every block of 128 x 128 (the last ones may be smaller); / 448 is a product with 1 / 448 in fp32.
  * No output may overlap another buffer. A NaN or an infinity leaves nothing of its block.
  */
 int lora_linear_fp8_blocks(const void* w, long long w_stride, int rows, int cols, void* q8, long long q8_stride,

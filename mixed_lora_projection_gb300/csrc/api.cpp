@@ -1571,12 +1571,14 @@ struct Fp8Shape {
 
 // Three forms, each with one CTA (or pair) an SM: blocks of 128 x 128 and 128 x 256 on single CTAs, whose units a cluster
 // of up to eight CTAs may split by K where they would leave SMs idle, and of 256 x 256 on SM pairs. The one that would end
-// first: the units' waves times a block's time, per 128-wide K step (0.28 us at 128 columns, 0.46 at 256, 0.39 on pairs),
-// or the weight at 6.5 TB/s, and 1.2 us and up to 5 for the sums of joined parts, by their size. On 44 batches timed (1 to
-// 2,048 rows of four projections) that picks the fastest or one within 3 %: one row of 6,144 -> 5,120 in three parts of 128
-// columns 10.8 us against 11.5 (256 columns, six parts), 128 rows there 13.4 against 17.3 (four), 48 rows of 5,120 ->
-// 12,288 in 128 columns 17.0 against 17.8 (256, two parts), 348 rows in 256 columns 24.0 against 27.5 and, on pairs, 40.6;
-// 2,048 rows there on pairs 113 against 120 (256 columns).
+// first: the units' waves times a block's time, per 128-wide K step (0.28 us at 128 columns, 0.46 at 256, 0.39 on pairs: what
+// a wave of 40 blocks adds in few waves, 0.43 in many), or the weight at 6.5 TB/s, and 1.2 us and up to 5 for the sums of
+// joined parts, by their size. On 44 batches timed in every form (1 to 2,048 rows of four projections) that picks the fastest
+// or one within 1 %; so does any time of a pair's block from 0.36 to 0.41 (0.43: within 11 %):
+one row of 6,144 -> 5,120 in three parts of 128
+// columns 10.8 us against 11.5 (256 columns, six parts), 128 rows there 13.5 against 17.3 (four), 48 rows of 5,120 ->
+// 12,288 in 128 columns 17.0 against 17.9 (256, two parts), 348 rows in 256 columns 24.4 against 27.7 and, on pairs, 36.9;
+// 2,048 rows there on pairs 101 against 120 (256 columns).
 Fp8Shape fp8_shape(const lora_linear* h, const Plan& plan, bool merged) {
     const int nf = (int)plan.fused.size(), k_blocks = ceil_div(h->d_in, kFp8Group), sms = usable_sms(h);
     Fp8Shape s;

@@ -247,7 +247,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1) lora_fp8_kernel(const __grid_c
     const CUtensorMap* bmaps = p.inline_wl ? p.inline_bmaps : p.tm_b;
     // Behind this call's own shrink, which began when the kernel before it had completed, the base runs beside the shrink:
     // only the warp that loads U waits for it (rank 256, 48 rows of 5,120 -> 12,288 25 -> 19 us, 2,048 rows of 6,144 -> 5,120
-    // 93 -> 77, of 17,408 -> 5,120 220 -> 198).
+    // 93 -> 77, of 17,408 -> 5,120 220 -> 198). X, W and the scales are read without a wait of this grid's own: the kernel that
+    // wrote them had completed, its writes performed, before the shrink began, but the model promises their visibility to the
+    // grid that waits alone. It is so because they are read from L2, by TMA and past L1.
     if (!p.late_u) griddep_wait();
     griddep_launch_dependents();
 
