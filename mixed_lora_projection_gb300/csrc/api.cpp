@@ -1575,7 +1575,7 @@ struct Fp8Shape {
 // a wave of 40 blocks adds in few waves, 0.43 in many), or the weight at 6.5 TB/s, and 1.2 us and up to 5 for the sums of
 // joined parts, by their size. On 44 batches timed in every form (1 to 2,048 rows of four projections) that picks the fastest
 // or one within 1 %; so does any time of a pair's block from 0.36 to 0.41 (0.43: within 11 %):
-one row of 6,144 -> 5,120 in three parts of 128
+// one row of 6,144 -> 5,120 in three parts of 128
 // columns 10.8 us against 11.5 (256 columns, six parts), 128 rows there 13.5 against 17.3 (four), 48 rows of 5,120 ->
 // 12,288 in 128 columns 17.0 against 17.9 (256, two parts), 348 rows in 256 columns 24.4 against 27.7 and, on pairs, 36.9;
 // 2,048 rows there on pairs 101 against 120 (256 columns).
